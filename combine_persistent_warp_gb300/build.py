@@ -1,6 +1,6 @@
 """Build the CUDA library libcpw_moe.so in-tree (nvcc, sm_103a only).
 
-Three translation units are compiled in parallel and linked into one shared library
+The translation units are compiled in parallel and linked into one shared library
 that exports the C ABI of include/cpw_moe.h.  The CUDA runtime is linked statically;
 the driver's tensor-map encoder is fetched at run time, so no libcuda link is needed.
 """
@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcpw_moe.so")
-SOURCES = ["api.cu", "routing.cu", "ffn.cu", "ffn_bs.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "routing.cu", "ffn.cu", "ffn_bs.cu", "noalloc.cu", "norm.cu", "router.cu",
+           "rows.cu", "grouped_mm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                 "-I" + os.path.join(ROOT, "include")]

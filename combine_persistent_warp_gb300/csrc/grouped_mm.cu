@@ -1,0 +1,753 @@
+// grouped_mm.cu -- matrix products with one weight per expert over ragged groups of rows
+// (16-bit operands, fp32 accumulators in TMEM).  offsets[e] .. offsets[e+1] are expert e's rows:
+//
+//   forward   y[r][n]     = sum_k x[r][k] * W[e][n][k]
+//   rows      dx[r][k]    = sum_n dy[r][n] * W[e][n][k]
+//   weights   dW[e][n][k] = sum_{r of e} dy[r][n] * x[r][k]
+//
+// Bound by the tensor cores where experts have many rows, by reading the weights where they have
+// few.  The 256-wide side of a tile (the UMMA's M, split over a pair of CTAs) is always a
+// dimension of the weights: features of the forward product and of the rows' gradient, rows n of
+// the weights' gradient.  A ragged group then lies on the UMMA's N, which goes in steps of 32
+// rows: a group of m rows is cut into ceil(m/256) tiles of equal height, so groups of odd or
+// small sizes waste at most 31 rows a tile instead of up to half a 256-row tile.  In the weights'
+// gradient the group is the contracted dimension; the rows that a last 16-row step has past
+// its group's end are zeroed in shared memory, in both operands, before the UMMA reads them.
+//
+// Persistent pairs of CTAs (cta_group::2; each CTA holds 128 of the 256 M rows and half of the N
+// columns' operand), roles by warp: TMA producer, UMMA issuer (the even CTA's), tail warp, and
+// four epilogue warps that drain one TMEM accumulator while the other is filled.
+// Operand layouts, both 128-byte swizzled: "K-major" rows of 64 contracted elements, and
+// "MN-major" boxes of 64 contracted rows x 64 elements of M or N, so no operand is transposed
+// in memory.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <type_traits>
+
+#include "moe_internal.cuh"
+#include "op_common.cuh"
+#include "ptx.cuh"
+
+using namespace cpw;
+
+namespace {
+
+constexpr int TILE_F = 256;            // M of a pair's UMMA: features of a tile
+constexpr int TILE_R = 256;            // N at most: rows (or columns of dW) of a tile
+constexpr int KB = 64;                 // contracted elements of a pipeline stage
+constexpr int OPER_BYTES = 128 * KB * 2;       // one operand's half in a CTA: 16 KB
+constexpr int STAGE = 2 * OPER_BYTES;
+constexpr int RING = 6;
+constexpr int THREADS = 256;
+constexpr int MAX_E = 1024;
+constexpr uint64_t WAIT_NS = 2000000000ull;    // limit of every wait
+constexpr int SMEM = RING * STAGE + 1024;
+
+__device__ uint32_t g_op_error;        // sticky status of the grouped products (moe_ops_get_error)
+
+// ------------------------------------------------------------------ PTX of CTA pairs ------
+__device__ __forceinline__ uint32_t cta_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address in the pair's even CTA of the same shared-memory offset.
+__device__ __forceinline__ uint32_t leader_addr(const void *p)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(ptx::smem_u32(p)));
+    return a;
+}
+// Arrivals on a barrier of the even CTA.  The relaxed ones publish no memory (a release at
+// cluster scope waits for the thread's earlier accesses, which on the producer's path would cost
+// a memory round trip a stage): TMA orders the operands by its own byte counts, and the
+// accumulator's readers have waited for their TMEM loads.  The tail warp's zeros are released.
+__device__ __forceinline__ void arrive_relaxed(uint32_t addr)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void arrive_release(uint32_t addr)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void arrive_tx_relaxed(uint32_t addr, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(ptx::smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+// Wait for the phase of the given parity, `ns` at most; CLUSTER: what the other CTA released
+// before its arrival is visible after it.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint64_t ns = WAIT_NS)
+{
+    // the timer is read only once a wait has already been long
+    uint64_t limit = 0;
+    for (uint32_t i = 0;; ++i) {
+        if (CLUSTER ? try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity))
+            return true;
+        if ((i & 255u) == 255u) {
+            const uint64_t now = ptx::globaltimer();
+            if (limit == 0)
+                limit = now + ns;
+            else if (now > limit)
+                return false;
+        }
+    }
+}
+// Tiled loads into this CTA's shared memory, counted on a barrier of either CTA of the pair.
+__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%3, %4}], [%2];" ::"r"(ptx::smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+                 : "memory");
+}
+__device__ __forceinline__ void load_3d(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(ptx::smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+// One arrival on the barrier at this offset in both CTAs when the UMMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     ptx::smem_u32(bar)),
+                 "h"(static_cast<uint16_t>(3))
+                 : "memory");
+}
+
+// MN-major operand, 128-byte swizzle: boxes of 64 elements of M or N (8 KB apart: leading byte
+// offset), 8 contracted rows of 128 bytes each 1024 bytes (stride byte offset).
+__device__ __forceinline__ uint64_t mn_major_desc(uint32_t smem_addr)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>((KB * 128) >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+// ------------------------------------------------------------------ the kernel -----------
+struct Args {
+    int E, F, C;       // experts, features (M side), contracted length (0: ragged rows)
+    int R;             // rows of the ragged tensors; dW: columns (N side) of the weights' gradient
+    int M;             // rows of the ragged tensors
+    const int32_t *offsets;
+    void *out;
+    long long ldo;     // elements between rows of out
+    uint32_t idesc;    // without N
+    int f16;           // operands (and a 16-bit out) are fp16, else bf16
+    int out32;         // dW: fp32 out
+    int accumulate;    // dW: add to out
+};
+
+struct Shared {
+    uint64_t full[RING], empty[RING], tail[RING];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int32_t off[MAX_E + 1];     // clamped offsets
+    int32_t tile0[MAX_E + 1];   // first tile of each expert
+};
+
+enum Kind { FORWARD, ROWS, WEIGHTS };
+
+// Operand geometry of the three products.
+template <Kind KIND>
+struct Geo {
+    static constexpr bool A_MN = KIND != FORWARD;
+    static constexpr bool B_MN = KIND == WEIGHTS;
+};
+
+// A tile of the persistent list.
+struct Tile {
+    int e;         // expert
+    int f0;        // first feature
+    int r0, rows;  // FORWARD / ROWS: first row and valid rows;  WEIGHTS: first column, valid columns
+    int n;         // N of the UMMA (multiple of 32)
+    int blocks;    // pipeline stages
+    int k0, klen;  // contracted range (WEIGHTS: rows of the group)
+};
+
+template <Kind KIND>
+struct Tiles {
+    const Args &a;
+    const Shared &s;
+    int total, step, at, e;
+    __device__ Tiles(const Args &a_, const Shared &s_) : a(a_), s(s_), e(0)
+    {
+        total = s.tile0[a.E];
+        at = blockIdx.x >> 1;
+        step = gridDim.x >> 1;
+    }
+    __device__ bool next(Tile &t)
+    {
+        if (at >= total)
+            return false;
+        const int ft = (a.F + TILE_F - 1) / TILE_F;
+        if (KIND == WEIGHTS) {
+            const int ct = (a.R + TILE_R - 1) / TILE_R;
+            t.e = at / (ft * ct);
+            const int i = at - t.e * (ft * ct);
+            t.f0 = (i / ct) * TILE_F;
+            t.r0 = (i % ct) * TILE_R;
+            t.rows = min(TILE_R, a.R - t.r0);
+            t.k0 = s.off[t.e];
+            t.klen = s.off[t.e + 1] - t.k0;
+        } else {
+            while (s.tile0[e + 1] <= at)
+                ++e;
+            t.e = e;
+            const int m = s.off[e + 1] - s.off[e];
+            const int rt = (m + TILE_R - 1) / TILE_R;
+            const int i = at - s.tile0[e];
+            const int h = ((m + rt - 1) / rt + 31) & ~31;
+            t.f0 = (i / rt) * TILE_F;
+            t.r0 = s.off[e] + (i % rt) * h;
+            t.rows = min(h, s.off[e + 1] - t.r0);   // at least 1: h <= 256
+            t.k0 = 0;
+            t.klen = a.C;
+        }
+        t.n = max(32, (t.rows + 31) & ~31);
+        t.blocks = (t.klen + KB - 1) / KB;
+        at += step;
+        return true;
+    }
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int f16)
+{
+    if (f16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// 32 accumulator columns (rows r .. r + 31 of the tile) of this lane's feature: neighbouring
+// lanes swap halves of a pair of rows, so that a lane stores two features of one row and a warp
+// 64 contiguous bytes of each of two rows.
+__device__ __forceinline__ void store_rows(const Args &a, const Tile &t, const uint32_t (&v)[32], int r, int f, int lane)
+{
+    uint16_t *out = static_cast<uint16_t *>(a.out);
+    const int odd = lane & 1;
+    const int fe = f & ~1;
+#pragma unroll
+    for (int p = 0; p < 16; ++p) {
+        const uint32_t own = pack2(__uint_as_float(v[2 * p]), __uint_as_float(v[2 * p + 1]), a.f16);
+        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+        const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+        const int row = r + 2 * p + odd;
+        if (row < t.rows && fe < a.F)
+            *reinterpret_cast<uint32_t *>(out + static_cast<size_t>(t.r0 + row) * a.ldo + fe) = w;
+    }
+}
+
+// 32 columns of this lane's row n of dW[e].
+__device__ __forceinline__ void store_weights(const Args &a, const Tile &t, const uint32_t (&v)[32], int c, int n)
+{
+    if (n >= a.F)
+        return;
+    const size_t at = (static_cast<size_t>(t.e) * a.F + n) * a.R + t.r0 + c;
+    if (a.out32) {
+        float *out = static_cast<float *>(a.out) + at;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (c + 4 * q < t.rows) {
+                float4 o = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                       __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+                if (a.accumulate) {
+                    const float4 old = *reinterpret_cast<const float4 *>(out + 4 * q);
+                    o.x += old.x, o.y += old.y, o.z += old.z, o.w += old.w;
+                }
+                *reinterpret_cast<float4 *>(out + 4 * q) = o;
+            }
+        }
+    } else {
+        uint16_t *out = static_cast<uint16_t *>(a.out) + at;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (c + 8 * q < t.rows) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    f[i] = __uint_as_float(v[8 * q + i]);
+                if (a.accumulate) {
+                    const uint4 old = *reinterpret_cast<const uint4 *>(out + 8 * q);
+                    const uint32_t w[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (a.f16) {
+                            const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                            f[2 * i] += g.x, f[2 * i + 1] += g.y;
+                        } else {
+                            const float2 g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+                            f[2 * i] += g.x, f[2 * i + 1] += g.y;
+                        }
+                    }
+                }
+                *reinterpret_cast<uint4 *>(out + 8 * q) = make_uint4(pack2(f[0], f[1], a.f16), pack2(f[2], f[3], a.f16),
+                                                                     pack2(f[4], f[5], a.f16), pack2(f[6], f[7], a.f16));
+            }
+        }
+    }
+}
+
+template <Kind KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ CUtensorMap map_b16, const Args a)
+{
+    extern __shared__ uint8_t raw[];
+    __shared__ Shared s;
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cta_rank();
+
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tmap(&map_a);
+        ptx::prefetch_tmap(&map_b);
+        if (!Geo<KIND>::B_MN)
+            ptx::prefetch_tmap(&map_b16);
+    }
+    if (warp == 1 && lane == 0) {
+        for (int i = 0; i < RING; ++i) {
+            ptx::mbar_init(&s.full[i], 2);    // one arrival of each CTA
+            ptx::mbar_init(&s.empty[i], 1);
+            ptx::mbar_init(&s.tail[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&s.acc_full[i], 1);
+            ptx::mbar_init(&s.acc_empty[i], 8);   // four epilogue warps of each CTA
+        }
+        ptx::mbar_init(&s.drain, 1);
+        ptx::fence_mbar_init();
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(ptx::smem_u32(&s.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (warp == 3) {
+        // offsets clamped to a non-decreasing sequence inside [0, M], whatever they hold, and
+        // the number of tiles before each expert
+        const int ft = (a.F + TILE_F - 1) / TILE_F;
+        int high = 0, tiles = 0;
+        for (int e0 = 0; e0 <= a.E; e0 += 32) {
+            const int e = e0 + lane;
+            int v = e <= a.E ? min(max(a.offsets[e], 0), a.M) : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+                if (lane >= o)
+                    v = max(v, u);
+            }
+            v = max(v, high);
+            int prev = __shfl_up_sync(0xFFFFFFFFu, v, 1);
+            if (lane == 0)
+                prev = high;
+            // tiles of expert e - 1, which lies between prev and v
+            int n = 0;
+            if (e >= 1 && e <= a.E)
+                n = KIND == WEIGHTS ? ft * ((a.R + TILE_R - 1) / TILE_R) : ft * ((v - prev + TILE_R - 1) / TILE_R);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xFFFFFFFFu, n, o);
+                if (lane >= o)
+                    n += u;
+            }
+            n += tiles;
+            if (e <= a.E) {
+                s.off[e] = v;
+                s.tile0[e] = n;
+            }
+            high = __shfl_sync(0xFFFFFFFFu, v, 31);
+            tiles = __shfl_sync(0xFFFFFFFFu, n, 31);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    ptx::tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------------------------------------------------------- producer ----
+            Tiles<KIND> list(a, s);
+            Tile t;
+            int stage = 0;
+            uint32_t phase = 1;
+            while (ok && list.next(t)) {
+                const int half = t.n >> 1;
+                const int fa = t.f0 + static_cast<int>(rank) * 128;
+                const int rb = t.r0 + static_cast<int>(rank) * half;
+                const uint32_t bytes = OPER_BYTES + (Geo<KIND>::B_MN ? (half + 63) / 64 * (64 * 128) : half * 128);
+                for (int b = 0; b < t.blocks; ++b) {
+                    if (!wait_phase(&s.empty[stage], phase)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *pa = ring + stage * STAGE, *pb = pa + OPER_BYTES;
+                    const int k = t.k0 + b * KB;
+                    uint32_t bar = leader_addr(&s.full[stage]);
+                    const bool odd_tail = KIND == WEIGHTS && b == t.blocks - 1 && (t.klen & 15) != 0;
+                    if (odd_tail) {
+                        bar = ptx::smem_u32(&s.tail[stage]);
+                        ptx::mbar_arrive_expect_tx(&s.tail[stage], bytes);
+                    } else {
+                        arrive_tx_relaxed(bar, bytes);
+                    }
+                    if (KIND == FORWARD) {
+                        load_3d(pa, &map_a, bar, k, fa, t.e);
+                    } else if (KIND == ROWS) {
+                        load_3d(pa, &map_a, bar, fa, k, t.e);
+                        load_3d(pa + 64 * 128, &map_a, bar, fa + 64, k, t.e);
+                    } else {
+                        load_2d(pa, &map_a, bar, fa, k);
+                        load_2d(pa + 64 * 128, &map_a, bar, fa + 64, k);
+                    }
+                    if (Geo<KIND>::B_MN) {
+                        for (int c = 0; c < half; c += 64)
+                            load_2d(pb + c * 128, &map_b, bar, rb + c, k);
+                    } else {
+                        int r = 0;
+                        for (; r + 64 <= half; r += 64)
+                            load_2d(pb + r * 128, &map_b, bar, k, rb + r);
+                        for (; r < half; r += 16)
+                            load_2d(pb + r * 128, &map_b16, bar, k, rb + r);
+                    }
+                    if (++stage == RING) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ---------------------------------------------------------------- issuer ------
+            Tiles<KIND> list(a, s);
+            Tile t;
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 1;
+            while (ok && list.next(t)) {
+                if (t.blocks == 0)
+                    continue;   // an empty group's dW tile: the epilogue writes zeros
+                if (!wait_phase(&s.acc_empty[acc], acc_phase)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t d = tmem + acc * TILE_R;
+                const uint32_t idesc = a.idesc | (static_cast<uint32_t>(t.n >> 3) << 17);
+                for (int b = 0; b < t.blocks; ++b) {
+                    const bool odd_tail = KIND == WEIGHTS && b == t.blocks - 1 && (t.klen & 15) != 0;
+                    if (!(odd_tail ? wait_phase<true>(&s.full[stage], phase) : wait_phase(&s.full[stage], phase))) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t pa = ptx::smem_u32(ring + stage * STAGE), pb = pa + OPER_BYTES;
+                    const int left = t.klen - b * KB;
+                    const int steps = left >= KB ? KB / 16 : (left + 15) / 16;
+                    for (int i = 0; i < steps; ++i) {
+                        const uint64_t da = Geo<KIND>::A_MN ? mn_major_desc(pa + i * 16 * 128)
+                                                            : ptx::kmajor_swizzled_desc<128>(pa + i * 32);
+                        const uint64_t db = Geo<KIND>::B_MN ? mn_major_desc(pb + i * 16 * 128)
+                                                            : ptx::kmajor_swizzled_desc<128>(pb + i * 32);
+                        umma_pair(d, da, db, idesc, b > 0 || i > 0);
+                    }
+                    commit_pair(&s.empty[stage]);
+                    if (++stage == RING) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok)
+                    break;
+                commit_pair(&s.acc_full[acc]);
+                acc ^= 1;
+                if (acc == 0)
+                    acc_phase ^= 1;
+            }
+            if (!ok) {
+                // after a wait that ran out: let the issued UMMAs and the loads in flight land
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                 ptx::smem_u32(&s.drain))
+                             : "memory");
+                wait_phase(&s.drain, 0, WAIT_NS / 16);
+                for (int i = 0; i < RING; ++i)
+                    wait_phase(&s.full[i], i < stage ? phase ^ 1 : phase, WAIT_NS / 16);
+            }
+        }
+    } else if (warp == 2) {
+        if (KIND == WEIGHTS) {
+            // ---------------------------------------------------------------- tail --------
+            // rows past the group's end in the last 16-row step of a tile: zeroed in both operands
+            Tiles<KIND> list(a, s);
+            Tile t;
+            long long blocks = 0;      // stages used so far
+            uint32_t parity = 0;       // next parity of each stage's tail barrier
+            while (ok && list.next(t)) {
+                blocks += t.blocks;
+                if ((t.klen & 15) == 0)
+                    continue;
+                const int stage = static_cast<int>((blocks - 1) % RING);
+                if (!wait_phase(&s.tail[stage], (parity >> stage) & 1)) {
+                    ok = false;
+                    break;
+                }
+                parity ^= 1u << stage;
+                const int left = t.klen & (KB - 1), end = (left + 15) & ~15;
+                uint8_t *p = ring + stage * STAGE;
+                // (end - left) rows of 128 bytes in each of four boxes of 64 rows (two an operand)
+                const int words = (end - left) * 8;
+                for (int i = lane; i < 4 * words; i += 32) {
+                    const int box = i / words, j = i - box * words;
+                    *reinterpret_cast<uint4 *>(p + box * (64 * 128) + left * 128 + j * 16) = make_uint4(0, 0, 0, 0);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0)
+                    arrive_release(leader_addr(&s.full[stage]));
+            }
+        }
+    } else if (warp >= 4) {
+        // -------------------------------------------------------------------- epilogue ----
+        const int quarter = warp - 4;
+        if (KIND != WEIGHTS) {
+            // rows that belong to no expert: zero (before the first one only if offsets[0] > 0)
+            uint32_t *out = static_cast<uint32_t *>(a.out);
+            const int words = a.F / 2;
+            const int lo = s.off[0], hi = s.off[a.E];
+            for (int i = blockIdx.x; i < lo + a.M - hi; i += gridDim.x) {
+                const int row = i < lo ? i : hi + i - lo;
+                for (int w = threadIdx.x - 128; w < words; w += 128)
+                    out[(static_cast<size_t>(row) * a.ldo >> 1) + w] = 0;
+            }
+        }
+        Tiles<KIND> list(a, s);
+        Tile t;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        while (ok && list.next(t)) {
+            const int f = t.f0 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+            if (KIND == WEIGHTS && t.blocks == 0) {
+                if (!a.accumulate) {
+                    uint32_t z[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        z[i] = 0;
+                    for (int c = 0; c < t.rows; c += 32)
+                        store_weights(a, t, z, c, f);
+                }
+                continue;
+            }
+            if (!wait_phase(&s.acc_full[acc], acc_phase)) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t src = tmem + acc * TILE_R + (static_cast<uint32_t>(quarter * 32) << 16);
+            for (int c = 0; c < t.rows; c += 32) {
+                uint32_t v[32];
+                ptx::tmem_ld32(src + c, v);
+                ptx::tmem_ld_wait(v);
+                if (KIND == WEIGHTS)
+                    store_weights(a, t, v, c, f);
+                else
+                    store_rows(a, t, v, c, f, lane);
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                arrive_relaxed(leader_addr(&s.acc_empty[acc]));
+            acc ^= 1;
+            if (acc == 0)
+                acc_phase ^= 1;
+        }
+    }
+    if (!ok)
+        atomicExch(&g_op_error, static_cast<uint32_t>(MOE_ERR_TIMEOUT));
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// ------------------------------------------------------------------ host side ------------
+PFN_cuTensorMapEncodeTiled_v12000 encoder()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// [d1][d0] (or [d2][d1][d0], slices packed) 16-bit elements, rows `ld` elements apart, boxes of
+// 64 x b1, 128-byte swizzle.  Elements outside the tensor read as zero.
+bool encode(CUtensorMap *m, const void *base, bool f16, long long d0, long long d1, long long d2, long long ld, int b1)
+{
+    const auto fn = encoder();
+    if (!fn)
+        return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * 2 * static_cast<cuuint64_t>(d1)};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(b1), 1};
+    cuuint32_t one[3] = {1, 1, 1};
+    return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 > 0 ? 3 : 2,
+              const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Instruction descriptor of kind::f16 without N: fp32 D, 16-bit A and B, M = 256.
+uint32_t instr(bool f16, bool a_mn, bool b_mn)
+{
+    const uint32_t type = f16 ? 0u : 1u;
+    return (1u << 4) | (type << 7) | (type << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           (static_cast<uint32_t>(TILE_F >> 4) << 24);
+}
+
+template <Kind KIND>
+int launch_grouped(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mb16, const Args &a, int sms, cudaStream_t s)
+{
+    const auto kern = grouped_kernel<KIND>;
+    if (ensure_max_dynamic_smem(reinterpret_cast<const void *>(kern), SMEM) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    kern<<<sms / 2 * 2, THREADS, SMEM, s>>>(ma, mb, mb16, a);
+    return launched();
+}
+
+bool grouped_sizes_ok(int64_t M, int E, int N, int K, int dtype)
+{
+    return M >= 0 && M <= 0x7FFFFFFFll - 1024 && E >= 1 && E <= MAX_E && N >= 8 && N % 8 == 0 && K >= 8 && K % 8 == 0 &&
+           N <= (1 << 20) && K <= (1 << 20) && (dtype == MOE_BF16 || dtype == MOE_F16);
+}
+
+bool rows_ok(const void *p, int64_t ld, int width) { return p && op_aligned(p, 16) && ld >= width && ld % 8 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+int moe_grouped_mm(int64_t M, int E, int N, int K, const void *x, int64_t ldx, const void *w, const int32_t *offsets,
+                   void *out, int64_t ldo, int dtype, void *stream)
+{
+    if (!grouped_sizes_ok(M, E, N, K, dtype))
+        return MOE_ERR_INVALID_ARG;
+    if (M == 0)
+        return MOE_OK;
+    if (!rows_ok(x, ldx, K) || !rows_ok(out, ldo, N) || !w || !op_aligned(w, 16) || !offsets || !op_aligned(offsets, 4))
+        return MOE_ERR_INVALID_ARG;
+    OP_DEVICE(sms);
+    const bool f16 = dtype == MOE_F16;
+    CUtensorMap ma, mb, mb16;
+    if (!encode(&ma, w, f16, K, N, E, K, 128) || !encode(&mb, x, f16, K, M, 0, ldx, 64) || !encode(&mb16, x, f16, K, M, 0, ldx, 16))
+        return MOE_ERR_CUDA;
+    const Args a{E, N, K, 0, static_cast<int>(M), offsets, out, ldo, instr(f16, false, false), f16, 0, 0};
+    return launch_grouped<FORWARD>(ma, mb, mb16, a, sms, static_cast<cudaStream_t>(stream));
+}
+
+int moe_grouped_mm_dx(int64_t M, int E, int N, int K, const void *dy, int64_t lddy, const void *w, const int32_t *offsets,
+                      void *dx, int64_t lddx, int dtype, void *stream)
+{
+    if (!grouped_sizes_ok(M, E, N, K, dtype))
+        return MOE_ERR_INVALID_ARG;
+    if (M == 0)
+        return MOE_OK;
+    if (!rows_ok(dy, lddy, N) || !rows_ok(dx, lddx, K) || !w || !op_aligned(w, 16) || !offsets || !op_aligned(offsets, 4))
+        return MOE_ERR_INVALID_ARG;
+    OP_DEVICE(sms);
+    const bool f16 = dtype == MOE_F16;
+    CUtensorMap ma, mb, mb16;
+    if (!encode(&ma, w, f16, K, N, E, K, KB) || !encode(&mb, dy, f16, N, M, 0, lddy, 64) || !encode(&mb16, dy, f16, N, M, 0, lddy, 16))
+        return MOE_ERR_CUDA;
+    const Args a{E, K, N, 0, static_cast<int>(M), offsets, dx, lddx, instr(f16, true, false), f16, 0, 0};
+    return launch_grouped<ROWS>(ma, mb, mb16, a, sms, static_cast<cudaStream_t>(stream));
+}
+
+int moe_grouped_mm_dw(int64_t M, int E, int N, int K, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                      const int32_t *offsets, void *dw, int dtype, int dw_dtype, int accumulate, void *stream)
+{
+    if (!grouped_sizes_ok(M, E, N, K, dtype) || (dw_dtype != dtype && dw_dtype != MOE_F32) || accumulate < 0 || accumulate > 1)
+        return MOE_ERR_INVALID_ARG;
+    if (!dw || !op_aligned(dw, 16))
+        return MOE_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (M > 0 && (!rows_ok(dy, lddy, N) || !rows_ok(x, ldx, K) || !offsets || !op_aligned(offsets, 4)))
+        return MOE_ERR_INVALID_ARG;
+    OP_DEVICE(sms);
+    if (M == 0) {
+        if (!accumulate && cudaMemsetAsync(dw, 0, static_cast<size_t>(E) * N * K * dtype_bytes(dw_dtype), s) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    const bool f16 = dtype == MOE_F16;
+    CUtensorMap ma, mb;
+    if (!encode(&ma, dy, f16, N, M, 0, lddy, KB) || !encode(&mb, x, f16, K, M, 0, ldx, KB))
+        return MOE_ERR_CUDA;
+    const Args a{E, N, 0, K, static_cast<int>(M), offsets, dw, K, instr(f16, true, true), f16, dw_dtype == MOE_F32, accumulate};
+    return launch_grouped<WEIGHTS>(ma, mb, mb, a, sms, s);
+}
+
+int moe_ops_get_error(int *device_status, void *stream)
+{
+    if (!device_status)
+        return MOE_ERR_INVALID_ARG;
+    *device_status = MOE_OK;
+    OP_DEVICE(sms);
+    uint32_t v = 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cudaMemcpyFromSymbolAsync(&v, g_op_error, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    if (v) {
+        const uint32_t zero = 0;
+        if (cudaMemcpyToSymbolAsync(g_op_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+            cudaStreamSynchronize(s) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    }
+    *device_status = static_cast<int>(v);
+    return MOE_OK;
+}
+
+}  // extern "C"

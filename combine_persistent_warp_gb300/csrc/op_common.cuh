@@ -1,0 +1,134 @@
+// op_common.cuh -- what the translation units of the operators around the expert layer
+// (norm.cu, router.cu, rows.cu, grouped_mm.cu) share: element types, vector loads and stores,
+// block sums, argument checks.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/cpw_moe.h"
+
+namespace cpw {
+
+// ------------------------------------------------------------------ element types ------
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+// N consecutive elements moved by as few 16-byte accesses as they fill (an element each when
+// N == 1; the address of N > 1 elements is 16-byte aligned).
+template <typename T, int N>
+struct alignas(N == 1 ? sizeof(T) : 16) Pack {
+    T v[N];
+};
+
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> load_pack(const T *p)
+{
+    if constexpr (N == 1) {
+        Pack<T, 1> r;
+        r.v[0] = __ldg(p);
+        return r;
+    } else {
+        static_assert(sizeof(T) * N % 16 == 0, "whole 16-byte accesses");
+        union {
+            Pack<T, N> pack;
+            uint4 q[sizeof(T) * N / 16];
+        } u;
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) * N / 16); ++i)
+            u.q[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        return u.pack;
+    }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_pack(T *p, const Pack<T, N> &v)
+{
+    if constexpr (N == 1) {
+        *p = v.v[0];
+    } else {
+        union {
+            Pack<T, N> pack;
+            uint4 q[sizeof(T) * N / 16];
+        } u;
+        u.pack = v;
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) * N / 16); ++i)
+            reinterpret_cast<uint4 *>(p)[i] = u.q[i];
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// ------------------------------------------------------------------ host side ----------
+inline bool op_aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+inline size_t dtype_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
+inline bool dtype_ok(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16; }
+
+// Number of SMs of the current device; 0 if a CUDA call failed, -1 if it is not an sm_103 GPU.
+// The answer of a device is looked up once.
+inline int op_num_sms()
+{
+    constexpr int MAX_DEV = 64;
+    static int cache[MAX_DEV];   // written with the one value that every thread would write
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEV)
+        return 0;
+    const int c = __atomic_load_n(&cache[dev], __ATOMIC_RELAXED);
+    if (c)
+        return c;
+    int major = 0, minor = 0, sms = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    const int got = major == 10 && minor == 3 ? sms : -1;
+    __atomic_store_n(&cache[dev], got, __ATOMIC_RELAXED);
+    return got;
+}
+
+#define OP_DEVICE(sms)                                                       \
+    const int sms = cpw::op_num_sms();                                       \
+    do {                                                                     \
+        if (sms <= 0)                                                        \
+            return sms == 0 ? MOE_ERR_CUDA : MOE_ERR_UNSUPPORTED_DEVICE;     \
+    } while (0)
+
+// Calls f with a null pointer of the element type that `dtype` names.
+template <typename F>
+inline auto with_dtype(int dtype, F f)
+{
+    if (dtype == MOE_F32)
+        return f(static_cast<float *>(nullptr));
+    if (dtype == MOE_BF16)
+        return f(static_cast<__nv_bfloat16 *>(nullptr));
+    return f(static_cast<__half *>(nullptr));
+}
+
+inline int launched() { return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+}  // namespace cpw

@@ -1,0 +1,276 @@
+// rows.cu -- rows moved from token order into expert-major order and weighted back out of it,
+// with both directions' gradients.  rows[t][j] is the row of slot j of token t (-1: none).
+//
+//   gather    out[rows[t][j]] = x[t]
+//   combine   out[t] = sum_j w[t][j] * y[rows[t][j]]      (fp32, j ascending, rounded once)
+//   its gradients   dy[rows[t][j]] = w[t][j] * dout[t],   dw[t][j] = sum_h dout[t][h] * y[rows[t][j]][h]
+//
+// The gradient of gather is combine with w = 1.  All three are bound by HBM: a block takes a
+// token, so the token's row is read (or written) once however many slots it has, and every row
+// in expert order once.
+#include <type_traits>
+
+#include "op_common.cuh"
+
+using namespace cpw;
+
+namespace {
+
+constexpr int MAX_K = 32;
+constexpr int SLOTS = 8;   // slots of a token handled together
+
+struct RowArgs {
+    int T, k, H;
+    int M;                   // rows in expert order
+    const void *x;           // [T][H]: gather's input, combine's gradient
+    long long ldx;
+    const void *y;           // [M][H]
+    const int32_t *rows;     // [T][k]
+    const float *w;          // [T][k] or null (1)
+    const int32_t *total;    // rows that are named: rows from there on are zeroed
+    void *out;               // gather [M][H], combine [T][H]
+    void *dy;                // [M][H]
+    float *dw;               // [T][k]
+};
+
+__device__ __forceinline__ int row_of(const RowArgs &a, int t, int j)
+{
+    if (j >= a.k)
+        return -1;
+    const int r = a.rows[static_cast<size_t>(t) * a.k + j];
+    return r >= 0 && r < a.M ? r : -1;
+}
+
+// Blocks past the T of the tokens zero the rows that no slot names.
+template <typename T, int V>
+__device__ __forceinline__ void zero_rest(const RowArgs &a, void *out)
+{
+    const int packs = a.H / V;
+    int first = *a.total;
+    first = first < 0 ? 0 : first;
+    Pack<T, V> z;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        z.v[i] = from_f<T>(0.0f);
+    for (int r = first + blockIdx.x - a.T; r < a.M; r += gridDim.x - a.T)
+        for (int p = threadIdx.x; p < packs; p += blockDim.x)
+            store_pack<T, V>(static_cast<T *>(out) + static_cast<size_t>(r) * a.H + static_cast<size_t>(p) * V, z);
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) gather_kernel(const RowArgs a)
+{
+    if (static_cast<int>(blockIdx.x) >= a.T) {
+        zero_rest<T, V>(a, a.out);
+        return;
+    }
+    const int t = blockIdx.x, packs = a.H / V;
+    const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(t) * a.ldx;
+    T *out = static_cast<T *>(a.out);
+    for (int j0 = 0; j0 < a.k; j0 += SLOTS) {
+        int r[SLOTS];
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i)
+            r[i] = row_of(a, t, j0 + i);
+        for (int p = threadIdx.x; p < packs; p += blockDim.x) {
+            const Pack<T, V> v = load_pack<T, V>(x + static_cast<size_t>(p) * V);
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i)
+                if (r[i] >= 0)
+                    store_pack<T, V>(out + static_cast<size_t>(r[i]) * a.H + static_cast<size_t>(p) * V, v);
+        }
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) combine_rows_kernel(const RowArgs a)
+{
+    const int t = blockIdx.x, packs = a.H / V;
+    const T *y = static_cast<const T *>(a.y);
+    int r[SLOTS];
+    float w[SLOTS];
+    for (int p = threadIdx.x; p < packs; p += blockDim.x) {
+        float acc[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            acc[i] = 0.0f;
+        for (int j0 = 0; j0 < a.k; j0 += SLOTS) {
+            Pack<T, V> v[SLOTS];
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) {
+                r[i] = row_of(a, t, j0 + i);
+                w[i] = r[i] < 0 ? 0.0f : a.w ? a.w[static_cast<size_t>(t) * a.k + j0 + i] : 1.0f;
+                if (r[i] >= 0)
+                    v[i] = load_pack<T, V>(y + static_cast<size_t>(r[i]) * a.H + static_cast<size_t>(p) * V);
+            }
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i)
+                if (r[i] >= 0) {
+#pragma unroll
+                    for (int c = 0; c < V; ++c)
+                        acc[c] = fmaf(w[i], to_f<T>(v[i].v[c]), acc[c]);
+                }
+        }
+        Pack<T, V> o;
+#pragma unroll
+        for (int c = 0; c < V; ++c)
+            o.v[c] = from_f<T>(acc[c]);
+        store_pack<T, V>(static_cast<T *>(a.out) + static_cast<size_t>(t) * a.H + static_cast<size_t>(p) * V, o);
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) combine_rows_backward_kernel(const RowArgs a)
+{
+    if (static_cast<int>(blockIdx.x) >= a.T) {
+        zero_rest<T, V>(a, a.dy);
+        return;
+    }
+    __shared__ float red[32][SLOTS];
+    const int t = blockIdx.x, packs = a.H / V;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const T *d = static_cast<const T *>(a.x) + static_cast<size_t>(t) * a.ldx;
+    const T *y = static_cast<const T *>(a.y);
+    T *dy = static_cast<T *>(a.dy);
+    for (int j0 = 0; j0 < a.k; j0 += SLOTS) {
+        int r[SLOTS];
+        float w[SLOTS], dot[SLOTS];
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) {
+            r[i] = row_of(a, t, j0 + i);
+            w[i] = r[i] < 0 ? 0.0f : a.w ? a.w[static_cast<size_t>(t) * a.k + j0 + i] : 1.0f;
+            dot[i] = 0.0f;
+        }
+        for (int p = threadIdx.x; p < packs; p += blockDim.x) {
+            const Pack<T, V> q = load_pack<T, V>(d + static_cast<size_t>(p) * V);
+            Pack<T, V> v[SLOTS];
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i)
+                if (r[i] >= 0)
+                    v[i] = load_pack<T, V>(y + static_cast<size_t>(r[i]) * a.H + static_cast<size_t>(p) * V);
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i)
+                if (r[i] >= 0) {
+                    Pack<T, V> o;
+#pragma unroll
+                    for (int c = 0; c < V; ++c) {
+                        const float g = to_f<T>(q.v[c]);
+                        dot[i] = fmaf(g, to_f<T>(v[i].v[c]), dot[i]);
+                        o.v[c] = from_f<T>(w[i] * g);
+                    }
+                    store_pack<T, V>(dy + static_cast<size_t>(r[i]) * a.H + static_cast<size_t>(p) * V, o);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i)
+            dot[i] = warp_sum(dot[i]);
+        __syncthreads();
+        if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i)
+                red[warp][i] = dot[i];
+        }
+        __syncthreads();
+        if (a.dw && threadIdx.x < SLOTS && j0 + static_cast<int>(threadIdx.x) < a.k) {
+            float s = 0.0f;
+            for (int wi = 0; wi < warps; ++wi)
+                s += red[wi][threadIdx.x];
+            // a slot without a row: its dot stayed zero
+            a.dw[static_cast<size_t>(t) * a.k + j0 + threadIdx.x] = s;
+        }
+    }
+}
+
+int rows_threads(int packs)
+{
+    const int t = (packs + 31) / 32 * 32;
+    return t < 32 ? 32 : t > 512 ? 512 : t;
+}
+
+bool rows_sizes_ok(int T, int k, int H, long long M, int dtype)
+{
+    return T >= 0 && k >= 1 && k <= MAX_K && H >= 1 && M >= 0 && M <= 0x7FFFFFFFll && dtype_ok(dtype);
+}
+
+// 16-byte packs where every row starts on a 16-byte boundary, single elements otherwise.
+template <typename F>
+int by_rows(int dtype, int H, long long ldx, const void *p0, const void *p1, const void *p2, F f)
+{
+    const size_t b = dtype_bytes(dtype);
+    const bool packed = H * b % 16 == 0 && static_cast<size_t>(ldx) * b % 16 == 0 && op_aligned(p0, 16) &&
+                        op_aligned(p1, 16) && op_aligned(p2, 16);
+    with_dtype(dtype, [&](auto *t) {
+        using E = std::remove_pointer_t<decltype(t)>;
+        if (packed)
+            f(t, std::integral_constant<int, 16 / static_cast<int>(sizeof(E))>{});
+        else
+            f(t, std::integral_constant<int, 1>{});
+    });
+    return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_gather_rows(int T, int topk, int H, int E, int64_t M, const void *x, int64_t ldx, int dtype,
+                    const int32_t *rows, const int32_t *offsets, void *out, void *stream)
+{
+    if (!rows_sizes_ok(T, topk, H, M, dtype) || E < 1 || ldx < H)
+        return MOE_ERR_INVALID_ARG;
+    if (M == 0)
+        return MOE_OK;
+    const size_t b = dtype_bytes(dtype);
+    if (!out || !offsets || !op_aligned(out, b) || !op_aligned(offsets, 4) ||
+        (T > 0 && (!x || !rows || !op_aligned(x, b) || !op_aligned(rows, 4))))
+        return MOE_ERR_INVALID_ARG;
+    OP_DEVICE(sms);
+    const RowArgs a{T, topk, H, static_cast<int>(M), x, ldx, nullptr, rows, nullptr, offsets + E, out, nullptr, nullptr};
+    return by_rows(dtype, H, ldx, x, out, nullptr, [&](auto *t, auto v) {
+        using Ty = std::remove_pointer_t<decltype(t)>;
+        constexpr int V = decltype(v)::value;
+        gather_kernel<Ty, V><<<T + sms, rows_threads(H / V), 0, static_cast<cudaStream_t>(stream)>>>(a);
+    });
+}
+
+int moe_combine_rows(int T, int topk, int H, int64_t M, const void *y, int dtype, const int32_t *rows, const float *w,
+                     void *out, void *stream)
+{
+    if (!rows_sizes_ok(T, topk, H, M, dtype))
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0)
+        return MOE_OK;
+    const size_t b = dtype_bytes(dtype);
+    if (!out || !rows || (M > 0 && !y) || !op_aligned(out, b) || !op_aligned(y, b) || !op_aligned(rows, 4) || !op_aligned(w, 4))
+        return MOE_ERR_INVALID_ARG;
+    OP_DEVICE(sms);
+    const RowArgs a{T, topk, H, static_cast<int>(M), nullptr, H, y, rows, w, nullptr, out, nullptr, nullptr};
+    return by_rows(dtype, H, H, y, out, nullptr, [&](auto *t, auto v) {
+        using Ty = std::remove_pointer_t<decltype(t)>;
+        constexpr int V = decltype(v)::value;
+        combine_rows_kernel<Ty, V><<<T, rows_threads(H / V), 0, static_cast<cudaStream_t>(stream)>>>(a);
+    });
+}
+
+int moe_combine_rows_backward(int T, int topk, int H, int E, int64_t M, const void *dout, int64_t lddout, const void *y,
+                              int dtype, const int32_t *rows, const float *w, const int32_t *offsets, void *dy,
+                              float *dw, void *stream)
+{
+    if (!rows_sizes_ok(T, topk, H, M, dtype) || E < 1 || lddout < H)
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0 && M == 0)
+        return MOE_OK;
+    const size_t b = dtype_bytes(dtype);
+    if (!offsets || !op_aligned(offsets, 4) || (M > 0 && (!y || !dy)) || !op_aligned(y, b) || !op_aligned(dy, b) ||
+        (T > 0 && (!dout || !rows || !op_aligned(dout, b) || !op_aligned(rows, 4))) || !op_aligned(w, 4) || !op_aligned(dw, 4))
+        return MOE_ERR_INVALID_ARG;
+    OP_DEVICE(sms);
+    const RowArgs a{T, topk, H, static_cast<int>(M), dout, lddout, y, rows, w, offsets + E, nullptr, dy, dw};
+    return by_rows(dtype, H, lddout, dout, y, dy, [&](auto *t, auto v) {
+        using Ty = std::remove_pointer_t<decltype(t)>;
+        constexpr int V = decltype(v)::value;
+        combine_rows_backward_kernel<Ty, V><<<T + sms, rows_threads(H / V), 0, static_cast<cudaStream_t>(stream)>>>(a);
+    });
+}
+
+}  // extern "C"

@@ -32,6 +32,7 @@ OPT_COMBINE_MODE = 4
 COMBINE_KERNEL, COMBINE_IN_FFN, COMBINE_AUTO = 0, 1, 2   # values of OPT_COMBINE_MODE (default COMBINE_AUTO)
 SCALE_FP32, SCALE_POW2, SCALE_AUTO = 0, 1, 2   # values of OPT_SCALE_MODE (default SCALE_AUTO)
 WEIGHTS_FP8, WEIGHTS_MXFP4 = 0, 1              # values of MoeInfo.weight_format
+F32, BF16, F16 = 0, 1, 2                       # moe_dtype of the operators' tensors
 
 
 class MoeError(RuntimeError):
@@ -70,6 +71,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         raise ImportError(f"CUDA library {LIB_PATH} is not built (run __graft_entry__.build())")
     L = ctypes.CDLL(LIB_PATH)
     P, I, I64, U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64
+    F = ctypes.c_float
     H = ctypes.c_void_p
     sig = {
         "moe_create": [I, I, I, I, I, ctypes.POINTER(H)],
@@ -92,6 +94,21 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "moe_profile_enable": [H, I],
         "moe_profile_read": [H, P, ctypes.POINTER(I), ctypes.POINTER(I)],
         "moe_route_noalloc": [I, I, I, I, P, P, P, P, P, P, P],
+        "moe_layer_norm": [I, I, P, I64, I, P, P, I, F, P, P, P, P],
+        "moe_layer_norm_fp8": [I, I, P, I64, I, P, P, I, F, I, P, P, P],
+        "moe_layer_norm_backward_workspace": [I, I, ctypes.POINTER(U64)],
+        "moe_layer_norm_backward": [I, I, P, I64, P, I64, I, P, I, P, P, P, P, P, P, U64, P],
+        "moe_route_topk": [I, I, I, P, I64, I, P, I, P, P, P],
+        "moe_route_topk_backward": [I, I, I, P, P, P, P, I64, I, I, P, P],
+        "moe_expert_order_workspace": [I, I, I, ctypes.POINTER(U64)],
+        "moe_expert_order": [I, I, I, P, P, P, P, P, U64, P],
+        "moe_gather_rows": [I, I, I, I, I64, P, I64, I, P, P, P, P],
+        "moe_combine_rows": [I, I, I, I64, P, I, P, P, P, P],
+        "moe_combine_rows_backward": [I, I, I, I, I64, P, I64, P, I, P, P, P, P, P, P],
+        "moe_grouped_mm": [I64, I, I, I, P, I64, P, P, P, I64, I, P],
+        "moe_grouped_mm_dx": [I64, I, I, I, P, I64, P, P, P, I64, I, P],
+        "moe_grouped_mm_dw": [I64, I, I, I, P, I64, P, I64, P, P, I, I, I, P],
+        "moe_ops_get_error": [ctypes.POINTER(I), P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)

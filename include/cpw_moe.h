@@ -283,6 +283,110 @@ int moe_route_noalloc(int T, int E, int topk, int R, const int64_t *topk_idx, ui
                       uint32_t *recv, int32_t *block_offset, uint32_t *meta, int32_t *status,
                       void *stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Operators around the expert layer, for training a block and for feeding the layer above:
+ * layer norm, the router with its gradient, rows into and out of expert order, and products
+ * with one weight per expert over ragged groups of rows.  They need no handle; the caller owns
+ * every buffer, workspaces included (the *_workspace calls say how many bytes).  All are
+ * asynchronous on `stream`, which belongs to the current device, an sm_103 GPU
+ * (MOE_ERR_UNSUPPORTED_DEVICE otherwise), allocate nothing, and may be captured into a graph.
+ * The source pages have no counterpart of them.
+ *
+ * Pointers are device pointers aligned to their element type unless a call asks for more; a row
+ * stride (ld...) counts elements and is at least the row's length; other tensors are contiguous.
+ * Calls with T == 0 (or M == 0) do nothing but write the results that an empty batch has (zero
+ * gradients of weights, zero offsets). */
+
+/* Element types. */
+enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 };
+
+/* Layer norm of each of T rows: y = (x - mean) * rstd * weight + bias with the biased variance
+ * and rstd = 1 / sqrt(var + eps); statistics in fp32, y [T][H] of x's type.  weight and bias
+ * [H] are of w_dtype (x's type or MOE_F32), either may be NULL; mean and rstd [T] fp32 (NULL:
+ * not written) are what the backward call reads.  1 <= H <= 16384. */
+int moe_layer_norm(int T, int H, const void *x, int64_t ldx, int dtype, const void *weight, const void *bias,
+                   int w_dtype, float eps, void *y, float *mean, float *rstd, void *stream);
+
+/* Layer norm written as the FP8 rows and 1x128 scales that moe_forward reads: q [T][H] e4m3,
+ * sf [T][H/128] = max(amax, 1e-4) / 448 of each group of 128, or with pow2_scales = 1 the
+ * smallest power of two at or above it (what the block-scaled kernel needs).  H % 128 == 0;
+ * x, weight, bias and q 16-byte aligned, rows of x too. */
+int moe_layer_norm_fp8(int T, int H, const void *x, int64_t ldx, int dtype, const void *weight, const void *bias,
+                       int w_dtype, float eps, int pow2_scales, uint8_t *q, float *sf, void *stream);
+
+/* Gradients of moe_layer_norm: dx [T][H] of x's type, and the sums over the rows dweight and
+ * dbias [H] of w_dtype (either may be NULL).  weight may be NULL (all ones).  Sums in fp32, in a
+ * fixed order on one kind of GPU: equal inputs give equal bits.  The workspace is needed when
+ * dweight or dbias is asked for (16-byte aligned). */
+int moe_layer_norm_backward_workspace(int T, int H, uint64_t *bytes);
+int moe_layer_norm_backward(int T, int H, const void *dy, int64_t lddy, const void *x, int64_t ldx, int dtype,
+                            const void *weight, int w_dtype, const float *mean, const float *rstd, void *dx,
+                            void *dweight, void *dbias, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* The router: the topk largest logits of each token ([T][E], rows ld apart), in descending order,
+ * ties to the lowest expert, and their gate weights: the softmax over the chosen experts
+ * (renormalize = 1) or over all of them (0).  topk_idx and topk_w [T][topk] are moe_forward's.  A logit
+ * of -inf is never chosen: a token with fewer others gets idx -1 and weight 0 in the slots left
+ * over.  A NaN counts as the largest value and makes the token's weights NaN.  token_mask [T]
+ * (bytes; NULL: all ones) is 0 for a token that is not routed: idx -1 and weight 0 throughout,
+ * whatever its logits hold.  E <= 1024, topk <= 32, topk <= E. */
+int moe_route_topk(int T, int E, int topk, const void *logits, int64_t ld, int dtype, const uint8_t *token_mask,
+                   int renormalize, int64_t *topk_idx, float *topk_w, void *stream);
+
+/* Gradient of the logits ([T][E], of `dtype`) from that of the gate weights, dw [T][topk] fp32, with the
+ * indices and weights that the forward call gave.  The choice itself is constant.  logits is
+ * read only with renormalize = 0 (may be NULL with 1).  dw in a slot of index -1 is not read. */
+int moe_route_topk_backward(int T, int E, int topk, const float *dw, const int64_t *topk_idx, const float *topk_w,
+                            const void *logits, int64_t ld, int dtype, int renormalize, void *dlogits, void *stream);
+
+/* Expert-major order of the T*topk slots: by expert, then token, then slot.  offsets [E+1] (expert
+ * e has rows offsets[e] .. offsets[e+1]) and rows [T][topk], the row of each slot or -1 for a
+ * skipped one.  *status (device int32) is MOE_OK, or MOE_ERR_BAD_INDEX if an id is neither -1
+ * nor in [0, E); such a slot is skipped.  T*topk < 2^31, E <= 1024, topk <= 32. */
+int moe_expert_order_workspace(int T, int topk, int E, uint64_t *bytes);
+int moe_expert_order(int T, int topk, int E, const int64_t *topk_idx, int32_t *offsets, int32_t *rows,
+                     int32_t *status, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* out[rows[t][j]] = x[t] for every slot with a row in [0, M); the rows of out [M][H] from
+ * offsets[E] on are zeroed.  Its gradient is moe_combine_rows with w = NULL. */
+int moe_gather_rows(int T, int topk, int H, int E, int64_t M, const void *x, int64_t ldx, int dtype,
+                    const int32_t *rows, const int32_t *offsets, void *out, void *stream);
+
+/* out[t] = sum over j of w[t][j] * y[rows[t][j]], in fp32 with j ascending, rounded once to y's
+ * type; slots without a row in [0, M) are left out (their w and y are not read).  w = NULL: ones. */
+int moe_combine_rows(int T, int topk, int H, int64_t M, const void *y, int dtype, const int32_t *rows, const float *w,
+                     void *out, void *stream);
+
+/* Gradients of moe_combine_rows: dy[rows[t][j]] = w[t][j] * dout[t] (rows of dy [M][H] from offsets[E]
+ * on are zeroed) and dw[t][j] = <dout[t], y[rows[t][j]]> (0 in a slot without a row; NULL: not
+ * written).  No two slots may have the same row. */
+int moe_combine_rows_backward(int T, int topk, int H, int E, int64_t M, const void *dout, int64_t lddout, const void *y,
+                              int dtype, const int32_t *rows, const float *w, const int32_t *offsets, void *dy,
+                              float *dw, void *stream);
+
+/* Products with one weight per expert, w [E][N][K], over rows in expert order (16-bit types
+ * MOE_BF16 and MOE_F16, fp32 accumulation): for the rows r of expert e,
+ *   moe_grouped_mm     out[r][n] = sum_k x[r][k] w[e][n][k]         x [M][K], out [M][N]
+ *   moe_grouped_mm_dx  dx[r][k]  = sum_n dy[r][n] w[e][n][k]        dy [M][N], dx [M][K]
+ *   moe_grouped_mm_dw  dw[e][n][k] = sum_r dy[r][n] x[r][k]         dw [E][N][K] of dtype or MOE_F32,
+ *                      added to what dw holds if accumulate = 1; an expert without rows gets 0
+ * offsets [E+1] is read by the GPU and taken as the non-decreasing sequence max(0, min(M, offsets))
+ * that its running maximum gives, so no value of it leads out of the tensors; rows of out and dx
+ * that belong to no expert are zeroed.  N and K multiples of 8 up to 2^20, E <= 1024, tensors
+ * 16-byte aligned, row strides multiples of 8.  The tensor core adds products to a 32-bit sum
+ * by truncation, so an fp32 dw is a few 1e-6 off over a thousand rows. */
+int moe_grouped_mm(int64_t M, int E, int N, int K, const void *x, int64_t ldx, const void *w, const int32_t *offsets,
+                   void *out, int64_t ldo, int dtype, void *stream);
+int moe_grouped_mm_dx(int64_t M, int E, int N, int K, const void *dy, int64_t lddy, const void *w, const int32_t *offsets,
+                      void *dx, int64_t lddx, int dtype, void *stream);
+int moe_grouped_mm_dw(int64_t M, int E, int N, int K, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                      const int32_t *offsets, void *dw, int dtype, int dw_dtype, int accumulate, void *stream);
+
+/* Waits for `stream`, then returns and clears the sticky status of the operators' device-side
+ * waits on the current device: MOE_OK, or MOE_ERR_TIMEOUT if a wait of a grouped product ran
+ * past its limit (2 s; its outputs are then undefined).  Not inside a stream capture. */
+int moe_ops_get_error(int *device_status, void *stream);
+
 /* Release every device buffer of the handle (after syncing its last stream): the teardown
  * of the buffers the layer object of "DeepGEMM Mega MoE 对称内存（Symmetric Memory）深度分析"
  * §10.1 allocates. */
