@@ -9,14 +9,16 @@
 // few.  The 256-wide side of a tile (the UMMA's M, split over a pair of CTAs) is always a
 // dimension of the weights: features of the forward product and of the rows' gradient, rows n of
 // the weights' gradient.  A ragged group then lies on the UMMA's N, which goes in steps of 32
-// rows: a group of m rows is cut into ceil(m/256) tiles of equal height, so groups of odd or
-// small sizes waste at most 31 rows a tile instead of up to half a 256-row tile.  In the weights'
-// gradient the group is the contracted dimension; the rows that a last 16-row step has past
-// its group's end are zeroed in shared memory, in both operands, before the UMMA reads them.
+// rows: a group of m rows is cut into ceil(m/256) tiles whose heights differ by at most one
+// step, so a group of any size wastes at most 31 rows, not up to half a 256-row tile, and
+// pairs that walk the tile list side by side stay balanced.  In the weights'
+// gradient the group is the contracted dimension: each expert has tensor maps of its own that end
+// with its last row (a small kernel writes them from the offsets), so TMA fills what a last
+// 64-row stage has past the group's end with zeros, in both operands.
 //
 // Persistent pairs of CTAs (cta_group::2; each CTA holds 128 of the 256 M rows and half of the N
-// columns' operand), roles by warp: TMA producer, UMMA issuer (the even CTA's), tail warp, and
-// four epilogue warps that drain one TMEM accumulator while the other is filled.
+// columns' operand), roles by warp: TMA producer, UMMA issuer (the even CTA's), and four
+// epilogue warps that drain one TMEM accumulator while the other is filled.
 // Operand layouts, both 128-byte swizzled: "K-major" rows of 64 contracted elements, and
 // "MN-major" boxes of 64 contracted rows x 64 elements of M or N, so no operand is transposed
 // in memory.
@@ -42,7 +44,9 @@ constexpr int RING = 6;
 constexpr int THREADS = 256;
 constexpr int MAX_E = 1024;
 constexpr uint64_t WAIT_NS = 2000000000ull;    // limit of every wait
+constexpr int STAGE_OUT = 32 * 128;    // dW: an epilogue warp's 32 rows x 128 bytes on their way out
 constexpr int SMEM = RING * STAGE + 1024;
+constexpr int SMEM_WEIGHTS = SMEM + 4 * STAGE_OUT;
 
 __device__ uint32_t g_op_error;        // sticky status of the grouped products (moe_ops_get_error)
 
@@ -64,43 +68,26 @@ __device__ __forceinline__ uint32_t leader_addr(const void *p)
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(ptx::smem_u32(p)));
     return a;
 }
-// Arrivals on a barrier of the even CTA.  The relaxed ones publish no memory (a release at
-// cluster scope waits for the thread's earlier accesses, which on the producer's path would cost
-// a memory round trip a stage): TMA orders the operands by its own byte counts, and the
-// accumulator's readers have waited for their TMEM loads.  The tail warp's zeros are released.
+// Arrivals on a barrier of the even CTA.  They publish no memory, so they are relaxed (a release
+// at cluster scope waits for the thread's earlier accesses: 700 cycles a stage on the producer's
+// path): TMA orders the operands by its byte counts, and the accumulator's readers have waited
+// for their TMEM loads and fenced them.
 __device__ __forceinline__ void arrive_relaxed(uint32_t addr)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-__device__ __forceinline__ void arrive_release(uint32_t addr)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 __device__ __forceinline__ void arrive_tx_relaxed(uint32_t addr, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok)
-                 : "r"(ptx::smem_u32(bar)), "r"(parity)
-                 : "memory");
-    return ok != 0;
-}
-// Wait for the phase of the given parity, `ns` at most; CLUSTER: what the other CTA released
-// before its arrival is visible after it.
-template <bool CLUSTER = false>
+// Wait for the phase of the given parity, `ns` at most.
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint64_t ns = WAIT_NS)
 {
     // the timer is read only once a wait has already been long
     uint64_t limit = 0;
     for (uint32_t i = 0;; ++i) {
-        if (CLUSTER ? try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity))
+        if (ptx::mbar_try_wait(bar, parity))
             return true;
         if ((i & 255u) == 255u) {
             const uint64_t now = ptx::globaltimer();
@@ -132,6 +119,34 @@ __device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, ui
                  "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
                  "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
                  : "memory");
+}
+// The four 16-deep steps of a full stage; A_STEP and B_STEP: a step in descriptor units (16 bytes).
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void umma_pair_stage(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "add.s64 a1, %1, %5;\n\tadd.s64 a2, %1, %6;\n\tadd.s64 a3, %1, %7;\n\t"
+                 "add.s64 b1, %2, %8;\n\tadd.s64 b2, %2, %9;\n\tadd.s64 b3, %2, %10;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(A_STEP), "n"(2 * A_STEP), "n"(3 * A_STEP), "n"(B_STEP),
+                 "n"(2 * B_STEP), "n"(3 * B_STEP)
+                 : "memory");
+}
+// Makes a tensor map that a kernel wrote to global memory visible to this thread's TMA loads.
+__device__ __forceinline__ void acquire_map(const CUtensorMap *m)
+{
+    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
 }
 // One arrival on the barrier at this offset in both CTAs when the UMMAs issued so far are done.
 __device__ __forceinline__ void commit_pair(uint64_t *bar)
@@ -167,10 +182,11 @@ struct Args {
     int f16;           // operands (and a 16-bit out) are fp16, else bf16
     int out32;         // dW: fp32 out
     int accumulate;    // dW: add to out
+    const CUtensorMap *maps;   // dW: [E][2] maps of dy and x that end with the expert's rows
 };
 
 struct Shared {
-    uint64_t full[RING], empty[RING], tail[RING];
+    uint64_t full[RING], empty[RING];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
     uint32_t tmem;
@@ -185,6 +201,11 @@ template <Kind KIND>
 struct Geo {
     static constexpr bool A_MN = KIND != FORWARD;
     static constexpr bool B_MN = KIND == WEIGHTS;
+};
+
+// Maps of the K-major operand on the UMMA's N: boxes of 128, 64, 32 and 16 rows.
+struct MapsB {
+    CUtensorMap m[4];
 };
 
 // A tile of the persistent list.
@@ -227,12 +248,14 @@ struct Tiles {
                 ++e;
             t.e = e;
             const int m = s.off[e + 1] - s.off[e];
-            const int rt = (m + TILE_R - 1) / TILE_R;
-            const int i = at - s.tile0[e];
-            const int h = ((m + rt - 1) / rt + 31) & ~31;
-            t.f0 = (i / rt) * TILE_F;
-            t.r0 = s.off[e] + (i % rt) * h;
-            t.rows = min(h, s.off[e + 1] - t.r0);   // at least 1: h <= 256
+            // the group's units of 32 rows, dealt evenly to its tiles
+            const int rt = (m + TILE_R - 1) / TILE_R, units = (m + 31) >> 5;
+            const int i = at - s.tile0[e], r = i / ft;
+            const int first = r * (units / rt) + min(r, units % rt);
+            const int count = units / rt + (r < units % rt ? 1 : 0);
+            t.f0 = (i - r * ft) * TILE_F;
+            t.r0 = s.off[e] + 32 * first;
+            t.rows = min(32 * count, m - 32 * first);
             t.k0 = 0;
             t.klen = a.C;
         }
@@ -272,60 +295,89 @@ __device__ __forceinline__ void store_rows(const Args &a, const Tile &t, const u
     }
 }
 
-// 32 columns of this lane's row n of dW[e].
-__device__ __forceinline__ void store_weights(const Args &a, const Tile &t, const uint32_t (&v)[32], int c, int n)
+// A warp's 32 rows of dW[e] from the accumulator: 128 bytes of each row at a time through the
+// warp's shared-memory buffer (swizzled at 128 bytes: conflict-free) and a TMA store, which
+// writes whole lines and drops what lies outside [F][R]; in 32 bits the accumulating form is a
+// TMA reduction, so the old values are not read by the SM.  (Each lane storing 16 bytes of its
+// own row took 12,000 cycles a tile, more than the 8192 of a 1024-row group's products.)
+template <bool F32, bool ZERO>
+__device__ __forceinline__ void store_weights(const Args &a, const CUtensorMap *map, const Tile &t, uint32_t src, uint8_t *buf,
+                                              int n0, int lane)
+{
+    constexpr int COLS = F32 ? 32 : 64;   // columns of 128 bytes
+    for (int c = 0; c < t.rows; c += COLS) {
+        uint32_t w[32];
+        if (ZERO) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                w[i] = 0;
+        } else if (F32) {
+            ptx::tmem_ld32(src + c, w);
+            ptx::tmem_ld_wait(w);
+        } else {
+            uint32_t v[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ptx::tmem_ld32(src + c + 32 * h, v);
+                ptx::tmem_ld_wait(v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    w[16 * h + i] = pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), a.f16);
+            }
+        }
+        // the previous store has read the buffer
+        if (lane == 0)
+            ptx::bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4 *>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            if (F32 && a.accumulate)
+                asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                                 reinterpret_cast<uint64_t>(map)),
+                             "r"(ptx::smem_u32(buf)), "r"(t.r0 + c), "r"(n0), "r"(t.e)
+                             : "memory");
+            else
+                asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                                 reinterpret_cast<uint64_t>(map)),
+                             "r"(ptx::smem_u32(buf)), "r"(t.r0 + c), "r"(n0), "r"(t.e)
+                             : "memory");
+            ptx::bulk_commit();
+        }
+    }
+}
+
+// The accumulating form in 16 bits: 32 columns of this lane's row n, added in fp32 and rounded
+// once (a 16-bit TMA reduction would round the product first).
+__device__ __forceinline__ void add_weights16(const Args &a, const Tile &t, const uint32_t (&v)[32], int c, int n)
 {
     if (n >= a.F)
         return;
-    const size_t at = (static_cast<size_t>(t.e) * a.F + n) * a.R + t.r0 + c;
-    if (a.out32) {
-        float *out = static_cast<float *>(a.out) + at;
+    uint16_t *out = static_cast<uint16_t *>(a.out) + (static_cast<size_t>(t.e) * a.F + n) * a.R + t.r0 + c;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            if (c + 4 * q < t.rows) {
-                float4 o = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
-                                       __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
-                if (a.accumulate) {
-                    const float4 old = *reinterpret_cast<const float4 *>(out + 4 * q);
-                    o.x += old.x, o.y += old.y, o.z += old.z, o.w += old.w;
-                }
-                *reinterpret_cast<float4 *>(out + 4 * q) = o;
+    for (int q = 0; q < 4; ++q) {
+        if (c + 8 * q < t.rows) {
+            const uint4 old = *reinterpret_cast<const uint4 *>(out + 8 * q);
+            uint32_t w[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 g = a.f16 ? __half22float2(*reinterpret_cast<const __half2 *>(&w[i]))
+                                       : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+                w[i] = pack2(__uint_as_float(v[8 * q + 2 * i]) + g.x, __uint_as_float(v[8 * q + 2 * i + 1]) + g.y, a.f16);
             }
-        }
-    } else {
-        uint16_t *out = static_cast<uint16_t *>(a.out) + at;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (c + 8 * q < t.rows) {
-                float f[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    f[i] = __uint_as_float(v[8 * q + i]);
-                if (a.accumulate) {
-                    const uint4 old = *reinterpret_cast<const uint4 *>(out + 8 * q);
-                    const uint32_t w[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (a.f16) {
-                            const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-                            f[2 * i] += g.x, f[2 * i + 1] += g.y;
-                        } else {
-                            const float2 g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
-                            f[2 * i] += g.x, f[2 * i + 1] += g.y;
-                        }
-                    }
-                }
-                *reinterpret_cast<uint4 *>(out + 8 * q) = make_uint4(pack2(f[0], f[1], a.f16), pack2(f[2], f[3], a.f16),
-                                                                     pack2(f[4], f[5], a.f16), pack2(f[6], f[7], a.f16));
-            }
+            *reinterpret_cast<uint4 *>(out + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 }
 
 template <Kind KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                   const __grid_constant__ CUtensorMap map_b16, const Args a)
+    grouped_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ MapsB maps_b,
+                   const __grid_constant__ CUtensorMap map_out, const Args a)
 {
     extern __shared__ uint8_t raw[];
     __shared__ Shared s;
@@ -334,16 +386,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t rank = cta_rank();
 
     if (warp == 0 && lane == 0) {
-        ptx::prefetch_tmap(&map_a);
-        ptx::prefetch_tmap(&map_b);
-        if (!Geo<KIND>::B_MN)
-            ptx::prefetch_tmap(&map_b16);
+        if (KIND != WEIGHTS) {
+            ptx::prefetch_tmap(&map_a);
+            for (int i = 0; i < 4; ++i)
+                ptx::prefetch_tmap(&maps_b.m[i]);
+        }
     }
     if (warp == 1 && lane == 0) {
         for (int i = 0; i < RING; ++i) {
             ptx::mbar_init(&s.full[i], 2);    // one arrival of each CTA
             ptx::mbar_init(&s.empty[i], 1);
-            ptx::mbar_init(&s.tail[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&s.acc_full[i], 1);
@@ -357,6 +409,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    if (KIND == WEIGHTS)
+        ptx::grid_dependency_wait();   // the maps' kernel (launched ahead of its end)
     if (warp == 3) {
         // offsets clamped to a non-decreasing sequence inside [0, M], whatever they hold, and
         // the number of tiles before each expert
@@ -402,145 +456,142 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     bool ok = true;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------------------------------------------------------- producer ----
-            Tiles<KIND> list(a, s);
-            Tile t;
-            int stage = 0;
-            uint32_t phase = 1;
-            while (ok && list.next(t)) {
-                const int half = t.n >> 1;
-                const int fa = t.f0 + static_cast<int>(rank) * 128;
-                const int rb = t.r0 + static_cast<int>(rank) * half;
-                const uint32_t bytes = OPER_BYTES + (Geo<KIND>::B_MN ? (half + 63) / 64 * (64 * 128) : half * 128);
-                for (int b = 0; b < t.blocks; ++b) {
-                    if (!wait_phase(&s.empty[stage], phase)) {
-                        ok = false;
-                        break;
-                    }
+        // -------------------------------------------------------------------- producer ----
+        // (warp-uniform like the issuer: TMA instructions read uniform registers too)
+        const uint32_t full0 = __shfl_sync(0xFFFFFFFFu, leader_addr(&s.full[0]), 0);
+        const bool issue = elect_one();
+        Tiles<KIND> list(a, s);
+        Tile t;
+        int stage = 0;
+        uint32_t phase = 1;
+        while (ok && list.next(t)) {
+            const int half = t.n >> 1;
+            const int fa = t.f0 + static_cast<int>(rank) * 128;
+            const int rb = t.r0 + static_cast<int>(rank) * half;
+            const int blocks = __shfl_sync(0xFFFFFFFFu, t.blocks, 0);
+            // N side: boxes of 64 columns, or the largest box of rows that fits and the smallest
+            // one that covers the rest
+            int box0 = 0, box1 = 0;
+            if (!Geo<KIND>::B_MN) {
+                while (box0 < 3 && (128 >> box0) > half)
+                    ++box0;
+                const int rest = half - (128 >> box0);
+                box1 = 3;
+                while (rest > (128 >> box1))
+                    --box1;
+                if (rest <= 0)
+                    box1 = -1;
+            }
+            const int rows_b = Geo<KIND>::B_MN ? (half + 63) / 64 * 64 : (128 >> box0) + (box1 < 0 ? 0 : 128 >> box1);
+            const uint32_t bytes = OPER_BYTES + rows_b * 128;
+            const int e = t.e;
+            // WEIGHTS: the expert's maps (dy, x), written by the kernel before this one
+            const CUtensorMap *ea = KIND == WEIGHTS ? a.maps + 2 * e : &map_a, *eb = KIND == WEIGHTS ? ea + 1 : nullptr;
+            if (KIND == WEIGHTS && issue) {
+                acquire_map(ea);
+                acquire_map(eb);
+            }
+            int k = t.k0;
+            for (int b = 0; b < blocks; ++b, k += KB) {
+                ok = __all_sync(0xFFFFFFFFu, wait_phase(&s.empty[stage], phase));
+                if (!ok)
+                    break;
+                if (issue) {
                     uint8_t *pa = ring + stage * STAGE, *pb = pa + OPER_BYTES;
-                    const int k = t.k0 + b * KB;
-                    uint32_t bar = leader_addr(&s.full[stage]);
-                    const bool odd_tail = KIND == WEIGHTS && b == t.blocks - 1 && (t.klen & 15) != 0;
-                    if (odd_tail) {
-                        bar = ptx::smem_u32(&s.tail[stage]);
-                        ptx::mbar_arrive_expect_tx(&s.tail[stage], bytes);
-                    } else {
-                        arrive_tx_relaxed(bar, bytes);
-                    }
+                    const uint32_t bar = full0 + stage * 8;
+                    arrive_tx_relaxed(bar, bytes);
                     if (KIND == FORWARD) {
-                        load_3d(pa, &map_a, bar, k, fa, t.e);
+                        load_3d(pa, &map_a, bar, k, fa, e);
                     } else if (KIND == ROWS) {
-                        load_3d(pa, &map_a, bar, fa, k, t.e);
-                        load_3d(pa + 64 * 128, &map_a, bar, fa + 64, k, t.e);
+                        load_3d(pa, &map_a, bar, fa, k, e);
+                        load_3d(pa + 64 * 128, &map_a, bar, fa + 64, k, e);
                     } else {
-                        load_2d(pa, &map_a, bar, fa, k);
-                        load_2d(pa + 64 * 128, &map_a, bar, fa + 64, k);
+                        load_2d(pa, ea, bar, fa, k);
+                        load_2d(pa + 64 * 128, ea, bar, fa + 64, k);
                     }
                     if (Geo<KIND>::B_MN) {
-                        for (int c = 0; c < half; c += 64)
-                            load_2d(pb + c * 128, &map_b, bar, rb + c, k);
+                        load_2d(pb, eb, bar, rb, k);
+                        if (half > 64)
+                            load_2d(pb + 64 * 128, eb, bar, rb + 64, k);
                     } else {
-                        int r = 0;
-                        for (; r + 64 <= half; r += 64)
-                            load_2d(pb + r * 128, &map_b, bar, k, rb + r);
-                        for (; r < half; r += 16)
-                            load_2d(pb + r * 128, &map_b16, bar, k, rb + r);
+                        load_2d(pb, &maps_b.m[box0], bar, k, rb);
+                        if (box1 >= 0)
+                            load_2d(pb + (128 >> box0) * 128, &maps_b.m[box1], bar, k, rb + (128 >> box0));
                     }
-                    if (++stage == RING) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                if (++stage == RING) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             // ---------------------------------------------------------------- issuer ------
+            // The whole warp runs the loops, one lane issues: with warp-uniform control flow the
+            // descriptors stay in uniform registers, which the tcgen05 instructions read (issued
+            // from a single lane's branch, the four steps of a stage took 475 cycles of issue, now
+            // fewer than the tensor cores' 512).
+            constexpr int A_STEP = Geo<KIND>::A_MN ? 16 * 128 / 16 : 2, B_STEP = Geo<KIND>::B_MN ? 16 * 128 / 16 : 2;
+            const uint32_t base = ptx::smem_u32(ring);
+            const uint64_t desc_a = Geo<KIND>::A_MN ? mn_major_desc(base) : ptx::kmajor_swizzled_desc<128>(base);
+            const uint64_t desc_b = Geo<KIND>::B_MN ? mn_major_desc(base + OPER_BYTES) : ptx::kmajor_swizzled_desc<128>(base + OPER_BYTES);
+            const bool issue = elect_one();
             Tiles<KIND> list(a, s);
             Tile t;
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 1;
             while (ok && list.next(t)) {
-                if (t.blocks == 0)
+                const int blocks = __shfl_sync(0xFFFFFFFFu, t.blocks, 0);
+                if (blocks == 0)
                     continue;   // an empty group's dW tile: the epilogue writes zeros
-                if (!wait_phase(&s.acc_empty[acc], acc_phase)) {
-                    ok = false;
+                ok = __all_sync(0xFFFFFFFFu, wait_phase(&s.acc_empty[acc], acc_phase));
+                if (!ok)
                     break;
-                }
                 ptx::tc_fence_after();
-                const uint32_t d = tmem + acc * TILE_R;
-                const uint32_t idesc = a.idesc | (static_cast<uint32_t>(t.n >> 3) << 17);
-                for (int b = 0; b < t.blocks; ++b) {
-                    const bool odd_tail = KIND == WEIGHTS && b == t.blocks - 1 && (t.klen & 15) != 0;
-                    if (!(odd_tail ? wait_phase<true>(&s.full[stage], phase) : wait_phase(&s.full[stage], phase))) {
-                        ok = false;
+                const uint32_t d = __shfl_sync(0xFFFFFFFFu, tmem + acc * TILE_R, 0);
+                const uint32_t idesc = __shfl_sync(0xFFFFFFFFu, a.idesc | (static_cast<uint32_t>(t.n >> 3) << 17), 0);
+                // steps of the last stage (every other one has four)
+                const int last = __shfl_sync(0xFFFFFFFFu, (t.klen - (blocks - 1) * KB + 15) / 16, 0);
+                for (int b = 0; b < blocks; ++b) {
+                    const bool end = b == blocks - 1;
+                    ok = __all_sync(0xFFFFFFFFu, wait_phase(&s.full[stage], phase));
+                    if (!ok)
                         break;
-                    }
                     ptx::tc_fence_after();
-                    const uint32_t pa = ptx::smem_u32(ring + stage * STAGE), pb = pa + OPER_BYTES;
-                    const int left = t.klen - b * KB;
-                    const int steps = left >= KB ? KB / 16 : (left + 15) / 16;
-                    for (int i = 0; i < steps; ++i) {
-                        const uint64_t da = Geo<KIND>::A_MN ? mn_major_desc(pa + i * 16 * 128)
-                                                            : ptx::kmajor_swizzled_desc<128>(pa + i * 32);
-                        const uint64_t db = Geo<KIND>::B_MN ? mn_major_desc(pb + i * 16 * 128)
-                                                            : ptx::kmajor_swizzled_desc<128>(pb + i * 32);
-                        umma_pair(d, da, db, idesc, b > 0 || i > 0);
+                    const uint64_t da = desc_a + static_cast<uint32_t>(stage * (STAGE / 16));
+                    const uint64_t db = desc_b + static_cast<uint32_t>(stage * (STAGE / 16));
+                    if (issue) {
+                        if (!end || last == KB / 16) {
+                            umma_pair_stage<A_STEP, B_STEP>(d, da, db, idesc, b > 0);
+                        } else {
+                            for (int i = 0; i < last; ++i)
+                                umma_pair(d, da + i * A_STEP, db + i * B_STEP, idesc, b > 0 || i > 0);
+                        }
+                        commit_pair(&s.empty[stage]);
+                        if (end)
+                            commit_pair(&s.acc_full[acc]);
                     }
-                    commit_pair(&s.empty[stage]);
+                    __syncwarp();
                     if (++stage == RING) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
-                if (!ok)
-                    break;
-                commit_pair(&s.acc_full[acc]);
                 acc ^= 1;
                 if (acc == 0)
                     acc_phase ^= 1;
             }
             if (!ok) {
                 // after a wait that ran out: let the issued UMMAs and the loads in flight land
-                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                                 ptx::smem_u32(&s.drain))
-                             : "memory");
+                if (issue)
+                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                     ptx::smem_u32(&s.drain))
+                                 : "memory");
                 wait_phase(&s.drain, 0, WAIT_NS / 16);
                 for (int i = 0; i < RING; ++i)
                     wait_phase(&s.full[i], i < stage ? phase ^ 1 : phase, WAIT_NS / 16);
-            }
-        }
-    } else if (warp == 2) {
-        if (KIND == WEIGHTS) {
-            // ---------------------------------------------------------------- tail --------
-            // rows past the group's end in the last 16-row step of a tile: zeroed in both operands
-            Tiles<KIND> list(a, s);
-            Tile t;
-            long long blocks = 0;      // stages used so far
-            uint32_t parity = 0;       // next parity of each stage's tail barrier
-            while (ok && list.next(t)) {
-                blocks += t.blocks;
-                if ((t.klen & 15) == 0)
-                    continue;
-                const int stage = static_cast<int>((blocks - 1) % RING);
-                if (!wait_phase(&s.tail[stage], (parity >> stage) & 1)) {
-                    ok = false;
-                    break;
-                }
-                parity ^= 1u << stage;
-                const int left = t.klen & (KB - 1), end = (left + 15) & ~15;
-                uint8_t *p = ring + stage * STAGE;
-                // (end - left) rows of 128 bytes in each of four boxes of 64 rows (two an operand)
-                const int words = (end - left) * 8;
-                for (int i = lane; i < 4 * words; i += 32) {
-                    const int box = i / words, j = i - box * words;
-                    *reinterpret_cast<uint4 *>(p + box * (64 * 128) + left * 128 + j * 16) = make_uint4(0, 0, 0, 0);
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0)
-                    arrive_release(leader_addr(&s.full[stage]));
             }
         }
     } else if (warp >= 4) {
@@ -561,33 +612,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         Tile t;
         int acc = 0;
         uint32_t acc_phase = 0;
+        uint8_t *buf = ring + RING * STAGE + quarter * STAGE_OUT;   // WEIGHTS
         while (ok && list.next(t)) {
-            const int f = t.f0 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+            const int f0 = t.f0 + static_cast<int>(rank) * 128 + quarter * 32;
             if (KIND == WEIGHTS && t.blocks == 0) {
-                if (!a.accumulate) {
-                    uint32_t z[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        z[i] = 0;
-                    for (int c = 0; c < t.rows; c += 32)
-                        store_weights(a, t, z, c, f);
+                if (!a.accumulate && f0 < a.F) {
+                    if (a.out32)
+                        store_weights<true, true>(a, &map_out, t, 0, buf, f0, lane);
+                    else
+                        store_weights<false, true>(a, &map_out, t, 0, buf, f0, lane);
                 }
                 continue;
             }
-            if (!wait_phase(&s.acc_full[acc], acc_phase)) {
-                ok = false;
+            ok = __all_sync(0xFFFFFFFFu, wait_phase(&s.acc_full[acc], acc_phase));
+            if (!ok)
                 break;
-            }
             ptx::tc_fence_after();
             const uint32_t src = tmem + acc * TILE_R + (static_cast<uint32_t>(quarter * 32) << 16);
-            for (int c = 0; c < t.rows; c += 32) {
-                uint32_t v[32];
-                ptx::tmem_ld32(src + c, v);
-                ptx::tmem_ld_wait(v);
-                if (KIND == WEIGHTS)
-                    store_weights(a, t, v, c, f);
-                else
-                    store_rows(a, t, v, c, f, lane);
+            if (KIND == WEIGHTS && (a.out32 || !a.accumulate)) {
+                if (f0 < a.F) {
+                    if (a.out32)
+                        store_weights<true, false>(a, &map_out, t, src, buf, f0, lane);
+                    else
+                        store_weights<false, false>(a, &map_out, t, src, buf, f0, lane);
+                }
+            } else {
+                for (int c = 0; c < t.rows; c += 32) {
+                    uint32_t v[32];
+                    ptx::tmem_ld32(src + c, v);
+                    ptx::tmem_ld_wait(v);
+                    if (KIND == WEIGHTS)
+                        add_weights16(a, t, v, c, f0 + lane);
+                    else
+                        store_rows(a, t, v, c, f0 + lane, lane);
+                }
             }
             ptx::tc_fence_before();
             __syncwarp();
@@ -597,6 +655,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (acc == 0)
                 acc_phase ^= 1;
         }
+        if (KIND == WEIGHTS && lane == 0)
+            ptx::bulk_wait<0>();   // the stores read this CTA's shared memory
     }
     if (!ok)
         atomicExch(&g_op_error, static_cast<uint32_t>(MOE_ERR_TIMEOUT));
@@ -606,6 +666,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     cluster_sync_all();
     if (warp == 2)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Tensor maps of each expert's rows of dy and x: copies of the whole tensors' maps whose row
+// count is the (clamped) end of the expert's group, so that loads past it read zeros.  A warp an
+// expert.
+constexpr int MAP_WARPS = 4;
+__global__ void __launch_bounds__(MAP_WARPS * 32)
+    group_maps_kernel(const __grid_constant__ CUtensorMap dy, const __grid_constant__ CUtensorMap x, const int32_t *offsets, int E,
+                      int M, CUtensorMap *maps)
+{
+    ptx::launch_dependents();
+    const int e = blockIdx.x * MAP_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (e >= E)
+        return;
+    int end = 0;
+    for (int i = lane; i <= e + 1; i += 32)
+        end = max(end, offsets[i]);
+    end = min(max(__reduce_max_sync(0xFFFFFFFFu, end), 1), M);   // no stage of an empty group is loaded
+    uint32_t *dst = reinterpret_cast<uint32_t *>(maps + 2 * e);
+    dst[lane] = reinterpret_cast<const uint32_t *>(&dy)[lane];
+    dst[32 + lane] = reinterpret_cast<const uint32_t *>(&x)[lane];
+    __syncwarp();
+    if (lane < 2) {
+        asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(
+                         reinterpret_cast<uint64_t>(maps + 2 * e + lane)),
+                     "r"(end)
+                     : "memory");
+        asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
+    }
 }
 
 // ------------------------------------------------------------------ host side ------------
@@ -622,21 +711,34 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
     return fn;
 }
 
-// [d1][d0] (or [d2][d1][d0], slices packed) 16-bit elements, rows `ld` elements apart, boxes of
-// 64 x b1, 128-byte swizzle.  Elements outside the tensor read as zero.
-bool encode(CUtensorMap *m, const void *base, bool f16, long long d0, long long d1, long long d2, long long ld, int b1)
+// [d1][d0] (or [d2][d1][d0], slices packed) elements, rows `ld` elements apart, boxes of 128
+// bytes x b1 rows, 128-byte swizzle.  Elements outside the tensor read as zero.
+bool encode(CUtensorMap *m, const void *base, int dtype, long long d0, long long d1, long long d2, long long ld, int b1)
 {
+    const cuuint64_t size = dtype_bytes(dtype);
     const auto fn = encoder();
     if (!fn)
         return false;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * 2 * static_cast<cuuint64_t>(d1)};
-    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(b1), 1};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * size, static_cast<cuuint64_t>(ld) * size * static_cast<cuuint64_t>(d1)};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(b1), 1};
     cuuint32_t one[3] = {1, 1, 1};
-    return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 > 0 ? 3 : 2,
+    return fn(m,
+              dtype == MOE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+              : dtype == MOE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              d2 > 0 ? 3 : 2,
               const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_rows(MapsB &maps, const void *base, int dtype, long long width, long long rows, long long ld)
+{
+    for (int i = 0; i < 4; ++i)
+        if (!encode(&maps.m[i], base, dtype, width, rows, 0, ld, 128 >> i))
+            return false;
+    return true;
 }
 
 // Instruction descriptor of kind::f16 without N: fp32 D, 16-bit A and B, M = 256.
@@ -648,12 +750,15 @@ uint32_t instr(bool f16, bool a_mn, bool b_mn)
 }
 
 template <Kind KIND>
-int launch_grouped(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mb16, const Args &a, int sms, cudaStream_t s)
+int launch_grouped(const CUtensorMap &ma, const MapsB &mb, const CUtensorMap &mo, const Args &a, int sms, cudaStream_t s)
 {
     const auto kern = grouped_kernel<KIND>;
-    if (ensure_max_dynamic_smem(reinterpret_cast<const void *>(kern), SMEM) != cudaSuccess)
+    constexpr int smem = KIND == WEIGHTS ? SMEM_WEIGHTS : SMEM;
+    if (ensure_max_dynamic_smem(reinterpret_cast<const void *>(kern), smem) != cudaSuccess)
         return MOE_ERR_CUDA;
-    kern<<<sms / 2 * 2, THREADS, SMEM, s>>>(ma, mb, mb16, a);
+    if (KIND == WEIGHTS)
+        return launch_programmatic(kern, sms / 2 * 2, THREADS, smem, s, ma, mb, mo, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    kern<<<sms / 2 * 2, THREADS, smem, s>>>(ma, mb, mo, a);
     return launched();
 }
 
@@ -680,11 +785,12 @@ int moe_grouped_mm(int64_t M, int E, int N, int K, const void *x, int64_t ldx, c
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
     const bool f16 = dtype == MOE_F16;
-    CUtensorMap ma, mb, mb16;
-    if (!encode(&ma, w, f16, K, N, E, K, 128) || !encode(&mb, x, f16, K, M, 0, ldx, 64) || !encode(&mb16, x, f16, K, M, 0, ldx, 16))
+    CUtensorMap ma;
+    MapsB mb;
+    if (!encode(&ma, w, dtype, K, N, E, K, 128) || !encode_rows(mb, x, dtype, K, M, ldx))
         return MOE_ERR_CUDA;
-    const Args a{E, N, K, 0, static_cast<int>(M), offsets, out, ldo, instr(f16, false, false), f16, 0, 0};
-    return launch_grouped<FORWARD>(ma, mb, mb16, a, sms, static_cast<cudaStream_t>(stream));
+    const Args a{E, N, K, 0, static_cast<int>(M), offsets, out, ldo, instr(f16, false, false), f16, 0, 0, nullptr};
+    return launch_grouped<FORWARD>(ma, mb, ma, a, sms, static_cast<cudaStream_t>(stream));
 }
 
 int moe_grouped_mm_dx(int64_t M, int E, int N, int K, const void *dy, int64_t lddy, const void *w, const int32_t *offsets,
@@ -698,22 +804,33 @@ int moe_grouped_mm_dx(int64_t M, int E, int N, int K, const void *dy, int64_t ld
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
     const bool f16 = dtype == MOE_F16;
-    CUtensorMap ma, mb, mb16;
-    if (!encode(&ma, w, f16, K, N, E, K, KB) || !encode(&mb, dy, f16, N, M, 0, lddy, 64) || !encode(&mb16, dy, f16, N, M, 0, lddy, 16))
+    CUtensorMap ma;
+    MapsB mb;
+    if (!encode(&ma, w, dtype, K, N, E, K, KB) || !encode_rows(mb, dy, dtype, N, M, lddy))
         return MOE_ERR_CUDA;
-    const Args a{E, K, N, 0, static_cast<int>(M), offsets, dx, lddx, instr(f16, true, false), f16, 0, 0};
-    return launch_grouped<ROWS>(ma, mb, mb16, a, sms, static_cast<cudaStream_t>(stream));
+    const Args a{E, K, N, 0, static_cast<int>(M), offsets, dx, lddx, instr(f16, true, false), f16, 0, 0, nullptr};
+    return launch_grouped<ROWS>(ma, mb, ma, a, sms, static_cast<cudaStream_t>(stream));
+}
+
+int moe_grouped_mm_dw_workspace(int E, uint64_t *bytes)
+{
+    if (E < 1 || E > MAX_E || !bytes)
+        return MOE_ERR_INVALID_ARG;
+    *bytes = 2ull * E * sizeof(CUtensorMap);
+    return MOE_OK;
 }
 
 int moe_grouped_mm_dw(int64_t M, int E, int N, int K, const void *dy, int64_t lddy, const void *x, int64_t ldx,
-                      const int32_t *offsets, void *dw, int dtype, int dw_dtype, int accumulate, void *stream)
+                      const int32_t *offsets, void *dw, int dtype, int dw_dtype, int accumulate, void *workspace,
+                      uint64_t workspace_bytes, void *stream)
 {
     if (!grouped_sizes_ok(M, E, N, K, dtype) || (dw_dtype != dtype && dw_dtype != MOE_F32) || accumulate < 0 || accumulate > 1)
         return MOE_ERR_INVALID_ARG;
     if (!dw || !op_aligned(dw, 16))
         return MOE_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (M > 0 && (!rows_ok(dy, lddy, N) || !rows_ok(x, ldx, K) || !offsets || !op_aligned(offsets, 4)))
+    if (M > 0 && (!rows_ok(dy, lddy, N) || !rows_ok(x, ldx, K) || !offsets || !op_aligned(offsets, 4) ||
+                  !workspace || !op_aligned(workspace, 128) || workspace_bytes < 2ull * E * sizeof(CUtensorMap)))
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
     if (M == 0) {
@@ -722,11 +839,16 @@ int moe_grouped_mm_dw(int64_t M, int E, int N, int K, const void *dy, int64_t ld
         return MOE_OK;
     }
     const bool f16 = dtype == MOE_F16;
-    CUtensorMap ma, mb;
-    if (!encode(&ma, dy, f16, N, M, 0, lddy, KB) || !encode(&mb, x, f16, K, M, 0, ldx, KB))
+    CUtensorMap mdy, mx, mo;
+    if (!encode(&mdy, dy, dtype, N, M, 0, lddy, KB) || !encode(&mx, x, dtype, K, M, 0, ldx, KB) ||
+        !encode(&mo, dw, dw_dtype, K, N, E, K, 32))
         return MOE_ERR_CUDA;
-    const Args a{E, N, 0, K, static_cast<int>(M), offsets, dw, K, instr(f16, true, true), f16, dw_dtype == MOE_F32, accumulate};
-    return launch_grouped<WEIGHTS>(ma, mb, mb, a, sms, s);
+    CUtensorMap *maps = static_cast<CUtensorMap *>(workspace);
+    group_maps_kernel<<<(E + MAP_WARPS - 1) / MAP_WARPS, MAP_WARPS * 32, 0, s>>>(mdy, mx, offsets, E, static_cast<int>(M), maps);
+    if (launched() != MOE_OK)
+        return MOE_ERR_CUDA;
+    const Args a{E, N, 0, K, static_cast<int>(M), offsets, dw, K, instr(f16, true, true), f16, dw_dtype == MOE_F32, accumulate, maps};
+    return launch_grouped<WEIGHTS>(mdy, MapsB{}, mo, a, sms, s);
 }
 
 int moe_ops_get_error(int *device_status, void *stream)

@@ -107,7 +107,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "moe_combine_rows_backward": [I, I, I, I, I64, P, I64, P, I, P, P, P, P, P, P],
         "moe_grouped_mm": [I64, I, I, I, P, I64, P, P, P, I64, I, P],
         "moe_grouped_mm_dx": [I64, I, I, I, P, I64, P, P, P, I64, I, P],
-        "moe_grouped_mm_dw": [I64, I, I, I, P, I64, P, I64, P, P, I, I, I, P],
+        "moe_grouped_mm_dw_workspace": [I, ctypes.POINTER(U64)],
+        "moe_grouped_mm_dw": [I64, I, I, I, P, I64, P, I64, P, P, I, I, I, P, U64, P],
         "moe_ops_get_error": [ctypes.POINTER(I), P],
     }
     for name, args in sig.items():

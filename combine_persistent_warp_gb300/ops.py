@@ -365,9 +365,13 @@ def grouped_mm_dw(dy, x, offsets, *, out=None, accumulate: bool = False, dtype=N
         _flat(out, "out", (E, N, K), dtype or out.dtype, x)
     if out.dtype not in (x.dtype, torch.float32):
         raise TypeError(f"out: dtype {out.dtype} is neither {x.dtype} nor float32")
-    _check(native.load().moe_grouped_mm_dw(M, E, N, K, dy.data_ptr(), lddy, x.data_ptr(), ldx, offsets.data_ptr(),
-                                           out.data_ptr(), dt, _DTYPE[out.dtype], int(accumulate),
-                                           _stream(stream, dy, x, offsets)), "moe_grouped_mm_dw")
+    L = native.load()
+    need = ctypes.c_uint64()
+    _check(L.moe_grouped_mm_dw_workspace(E, ctypes.byref(need)), "moe_grouped_mm_dw_workspace")
+    ws = _empty((need.value,), torch.uint8, x.device, stream)
+    _check(L.moe_grouped_mm_dw(M, E, N, K, dy.data_ptr(), lddy, x.data_ptr(), ldx, offsets.data_ptr(), out.data_ptr(), dt,
+                               _DTYPE[out.dtype], int(accumulate), ws.data_ptr(), need.value,
+                               _stream(stream, dy, x, offsets)), "moe_grouped_mm_dw")
     return out
 
 

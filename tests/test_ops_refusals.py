@@ -105,13 +105,18 @@ def test_grouped_refuse(lib, bad):
     assert lib.moe_grouped_mm(*args) == INVALID
     assert lib.moe_grouped_mm_dx(*args) == INVALID
     assert lib.moe_grouped_mm_dw(a["M"], a["E"], a["N"], a["K"], a["x"], a["ld"], a["w"], 64, a["offsets"], a["out"], a["dtype"],
-                                 a["dtype"], 0, None) == INVALID
+                                 a["dtype"], 0, P, 1 << 20, None) == INVALID
 
 
 def test_grouped_dw_refuses_types(lib):
     def dw(dtype, out, acc):
-        return lib.moe_grouped_mm_dw(16, 4, 64, 64, P, 64, P, 64, P, P, dtype, out, acc, None)
+        return lib.moe_grouped_mm_dw(16, 4, 64, 64, P, 64, P, 64, P, P, dtype, out, acc, ws, ws_bytes, None)
+    ws, ws_bytes = P, 4 * 256
     assert dw(BF16, F16, 0) == INVALID and dw(F16, BF16, 0) == INVALID and dw(BF16, BF16, 2) == INVALID
+    for ws, ws_bytes in ((None, 4 * 256), (P + 64, 4 * 256), (P, 4 * 256 - 1)):
+        assert dw(BF16, BF16, 0) == INVALID
+    assert lib.moe_grouped_mm_dw_workspace(0, ctypes.byref(ctypes.c_uint64())) == INVALID
+    assert lib.moe_grouped_mm_dw_workspace(8, None) == INVALID
 
 
 def test_python_entry_points_check_shapes_and_types():
