@@ -242,6 +242,8 @@ __global__ void __launch_bounds__(ORDER_THREADS) order_count_kernel(const OrderA
     extern __shared__ int32_t cnt[];   // [E]
     for (int e = threadIdx.x; e < a.E; e += ORDER_THREADS)
         cnt[e] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *a.status = MOE_OK;   // before the placing kernel, whose blocks record bad ids
     __syncthreads();
     const int lo = blockIdx.x * a.chunk, hi = min(a.n, lo + a.chunk);
     bool bad = false;
@@ -334,8 +336,13 @@ __global__ void __launch_bounds__(ORDER_THREADS) order_place_kernel(const OrderA
         if (i < whi)
             a.rows[i] = ex >= 0 ? at : -1;
     }
-    if (bad)
+    if (gridDim.x == 1) {
+        bad = __syncthreads_or(bad);
+        if (threadIdx.x == 0)
+            *a.status = bad ? MOE_ERR_BAD_INDEX : MOE_OK;
+    } else if (bad) {
         atomicExch(a.status, static_cast<int32_t>(MOE_ERR_BAD_INDEX));
+    }
 }
 
 // Blocks and slots a block: one block for up to ORDER_CHUNK slots (one launch), then as many as
@@ -453,8 +460,6 @@ int moe_expert_order(int T, int topk, int E, const int64_t *topk_idx, int32_t *o
     int blocks, chunk;
     order_shape(n, blocks, chunk);
     const OrderArgs a{static_cast<int>(n), E, chunk, topk_idx, offsets, rows, status, static_cast<int32_t *>(workspace)};
-    if (cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess)
-        return MOE_ERR_CUDA;
     if (blocks > 1) {
         order_count_kernel<<<blocks, ORDER_THREADS, E * sizeof(int32_t), s>>>(a);
         if (launched() != MOE_OK)
