@@ -15,6 +15,7 @@
 
 #include "op_common.cuh"
 #include "moe_internal.cuh"
+#include "ptx.cuh"
 
 using namespace cpw;
 
@@ -48,7 +49,76 @@ struct RouteArgs {
     float *w;
 };
 
-// IPL logits a lane: lane l holds experts l, l + 32, ...
+// The k largest of a token's logits, IPL a lane (lane l holds experts l, l + 32, ...): one warp
+// maximum and one warp minimum a slot.
+template <int IPL>
+__device__ __forceinline__ int choose(const RouteArgs &a, const float (&f)[IPL], int lane, int &my_idx, float &mine, float &top)
+{
+    uint32_t key[IPL];
+#pragma unroll
+    for (int i = 0; i < IPL; ++i)
+        key[i] = order_key(f[i]);
+    for (int j = 0; j < a.k; ++j) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < IPL; ++i)
+            best = max(best, key[i]);
+        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
+        if (m == 0)
+            return j;   // only logits of -inf are left
+        int at = INT_MAX;
+#pragma unroll
+        for (int i = IPL - 1; i >= 0; --i)
+            at = key[i] == m ? i * 32 + lane : at;
+        const int e = __reduce_min_sync(0xFFFFFFFFu, at);
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+            key[i] = i * 32 + lane == e ? 0u : key[i];
+        if (lane == j)
+            my_idx = e;
+        if (j == 0)
+            top = key_value(m);
+        mine = lane == j ? key_value(m) : mine;
+    }
+    return a.k;
+}
+
+// 16-bit logits: the key (its upper half) and the expert (ties to the lowest) fit one word, so
+// one warp maximum a slot finds both.
+template <int IPL>
+__device__ __forceinline__ int choose16(const RouteArgs &a, const float (&f)[IPL], int lane, int &my_idx, float &mine, float &top)
+{
+    uint32_t key[IPL];
+#pragma unroll
+    for (int i = 0; i < IPL; ++i) {
+        // the fp32 image of a 16-bit float keeps its order in 16 + 3 bits: sign, 8 bits of
+        // exponent and 10 of fraction; the expert takes 10 bits and 3 are left over
+        const uint32_t k = order_key(f[i]);
+        key[i] = k == 0u ? 0u : (k & 0xFFFFE000u) | static_cast<uint32_t>(1023 - (i * 32 + lane));
+    }
+    for (int j = 0; j < a.k; ++j) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < IPL; ++i)
+            best = max(best, key[i]);
+        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
+        if (m == 0)
+            return j;
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+            key[i] = key[i] == m ? 0u : key[i];
+        // the low bits of a positive value's key are zeros, of a negative one's are ones
+        const uint32_t up = m & 0xFFFFE000u;
+        const float v = up == 0xFFFFE000u ? __uint_as_float(0x7FC00000u) : key_value((up & 0x80000000u) ? up : up | 0x1FFFu);
+        if (lane == j)
+            my_idx = 1023 - static_cast<int>(m & 0x1FFFu);
+        if (j == 0)
+            top = v;
+        mine = lane == j ? v : mine;
+    }
+    return a.k;
+}
+
 template <typename T, int IPL>
 __global__ void __launch_bounds__(WARPS * 32) route_kernel(const RouteArgs a)
 {
@@ -60,45 +130,18 @@ __global__ void __launch_bounds__(WARPS * 32) route_kernel(const RouteArgs a)
     float my_w = 0.0f;
     if (!a.mask || a.mask[t]) {
         const T *l = static_cast<const T *>(a.logits) + static_cast<size_t>(t) * a.ld;
-        uint32_t key[IPL];
         float f[IPL];
 #pragma unroll
         for (int i = 0; i < IPL; ++i) {
             const int e = i * 32 + lane;
             f[i] = e < a.E ? to_f<T>(l[e]) : -INFINITY;
-            key[i] = order_key(f[i]);
         }
         float top = 0.0f, mine = 0.0f;
-        int found = 0;
-        for (int j = 0; j < a.k; ++j) {
-            uint32_t best = 0;
-            int at = 0;
-#pragma unroll
-            for (int i = 0; i < IPL; ++i) {
-                if (key[i] > best) {
-                    best = key[i];
-                    at = i;
-                }
-            }
-            const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
-            if (m == 0)
-                break;   // only logits of -inf are left
-            const int e = __reduce_min_sync(0xFFFFFFFFu, best == m ? at * 32 + lane : INT_MAX);
-            const float v = key_value(m);
-            if (j == 0)
-                top = v;
-            if (lane == j) {
-                my_idx = e;
-                mine = v;
-            }
-            if ((e & 31) == lane) {
-#pragma unroll
-                for (int i = 0; i < IPL; ++i)
-                    if (i == e >> 5)
-                        key[i] = 0;
-            }
-            found = j + 1;
-        }
+        int found;
+        if constexpr (sizeof(T) == 2)
+            found = choose16<IPL>(a, f, lane, my_idx, mine, top);
+        else
+            found = choose<IPL>(a, f, lane, my_idx, mine, top);
         const float p = lane < found ? expf(mine - top) : 0.0f;
         float sum = p;
         if (!a.renorm) {
@@ -212,12 +255,14 @@ __global__ void __launch_bounds__(WARPS * 32) route_backward_kernel(const RouteB
 
 // ------------------------------------------------------------------ expert-major order ----
 // A stable counting sort of the n = T*k slots by expert.  Each block has a run of `chunk`
-// slots, each of its warps a run of chunk / 32; counts per (warp, expert) in shared memory give
-// every slot its row without atomics on shared results, so equal inputs give equal rows.
-constexpr int ORDER_THREADS = 1024;
+// slots, each of its warps an equal part of it; counts per (warp, expert) in shared memory give
+// every slot its row without atomics on shared results, so equal inputs give equal rows.  More
+// than one block: a first kernel counts each block's slots, and every block of the second sums
+// the counts of all blocks for itself.
+constexpr int ORDER_THREADS = 512;
 constexpr int ORDER_WARPS = ORDER_THREADS / 32;
-constexpr int ORDER_MAX_BLOCKS = 256;
-constexpr int ORDER_CHUNK = 4096;
+constexpr int ORDER_CHUNK = 2048;
+constexpr int ORDER_SLOTS = ORDER_CHUNK / ORDER_THREADS;   // slots of a lane in a run of ORDER_CHUNK
 
 struct OrderArgs {
     int n, E, chunk;
@@ -240,6 +285,7 @@ __device__ __forceinline__ int slot_expert(const OrderArgs &a, int i, bool &bad)
 __global__ void __launch_bounds__(ORDER_THREADS) order_count_kernel(const OrderArgs a)
 {
     extern __shared__ int32_t cnt[];   // [E]
+    ptx::launch_dependents();
     for (int e = threadIdx.x; e < a.E; e += ORDER_THREADS)
         cnt[e] = 0;
     if (blockIdx.x == 0 && threadIdx.x == 0)
@@ -247,6 +293,7 @@ __global__ void __launch_bounds__(ORDER_THREADS) order_count_kernel(const OrderA
     __syncthreads();
     const int lo = blockIdx.x * a.chunk, hi = min(a.n, lo + a.chunk);
     bool bad = false;
+#pragma unroll 4
     for (int i = lo + threadIdx.x; i < hi; i += ORDER_THREADS) {
         const int e = slot_expert(a, i, bad);
         if (e >= 0)
@@ -257,84 +304,126 @@ __global__ void __launch_bounds__(ORDER_THREADS) order_count_kernel(const OrderA
         a.hist[static_cast<size_t>(blockIdx.x) * a.E + e] = cnt[e];
 }
 
+// Rows of the slots i0 .. i0 + 31 of a warp whose counters (the next row of each expert within the
+// block's run) are `mine`.
+__device__ __forceinline__ void place_slots(const OrderArgs &a, int i, int hi, int ex, const int32_t *start, int32_t *mine, int lane)
+{
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, ex);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    int at = -1;
+    if (ex >= 0)
+        at = start[ex] + mine[ex] + rank;
+    __syncwarp();
+    if (ex >= 0 && rank == 0)
+        mine[ex] += __popc(same);
+    __syncwarp();
+    if (i < hi)
+        a.rows[i] = at;
+}
+
 __global__ void __launch_bounds__(ORDER_THREADS) order_place_kernel(const OrderArgs a)
 {
     extern __shared__ int32_t smem[];
     int32_t *cnt = smem;                        // [ORDER_WARPS][E]
-    int32_t *start = smem + ORDER_WARPS * a.E;  // [E]
+    int32_t *start = smem + ORDER_WARPS * a.E;  // [E]: rows of the blocks before this one, then first rows
+    int32_t *all = start + a.E;                 // [E]: rows of all blocks
     __shared__ int32_t wsum[ORDER_WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < ORDER_WARPS * a.E; i += ORDER_THREADS)
-        cnt[i] = 0;
-    __syncthreads();
-    // this warp's run: counts per expert
+    for (int i = threadIdx.x; i < (ORDER_WARPS + 2) * a.E; i += ORDER_THREADS)
+        smem[i] = 0;
+    // this warp's run; a run of the usual length is held in registers
     const int lo = min(a.n, blockIdx.x * a.chunk), hi = min(a.n, lo + a.chunk);
-    const int per = (a.chunk / ORDER_WARPS);
+    const int per = a.chunk / ORDER_WARPS;
     const int wlo = min(hi, lo + warp * per), whi = min(hi, wlo + per);
-    int32_t *mine = cnt + warp * a.E;
+    const bool held = a.chunk == ORDER_CHUNK;
+    int ex[ORDER_SLOTS];
     bool bad = false;
-    for (int i = wlo + lane; i < whi; i += 32) {
-        const int e = slot_expert(a, i, bad);
-        if (e >= 0)
-            atomicAdd(&mine[e], 1);
+    if (held) {
+#pragma unroll
+        for (int s = 0; s < ORDER_SLOTS; ++s) {
+            const int i = wlo + s * 32 + lane;
+            ex[s] = i < whi ? slot_expert(a, i, bad) : -2;
+        }
     }
     __syncthreads();
-    // per expert: rows of all blocks, rows of the blocks before this one, and the warps' starts
-    int total = 0, before = 0;
-    const int e = threadIdx.x;
-    if (e < a.E) {
-        int run = 0;
-        for (int w = 0; w < ORDER_WARPS; ++w) {
-            const int c = cnt[w * a.E + e];
-            cnt[w * a.E + e] = run;
-            run += c;
+    int32_t *mine = cnt + warp * a.E;
+    if (held) {
+#pragma unroll
+        for (int s = 0; s < ORDER_SLOTS; ++s)
+            if (ex[s] >= 0)
+                atomicAdd(&mine[ex[s]], 1);
+    } else {
+        for (int i = wlo + lane; i < whi; i += 32) {
+            const int e = slot_expert(a, i, bad);
+            if (e >= 0)
+                atomicAdd(&mine[e], 1);
         }
-        total = run;
-        if (gridDim.x > 1) {
-            total = 0;
+    }
+    if (gridDim.x > 1) {
+        ptx::grid_dependency_wait();   // the counting kernel
+        // counts of all blocks and of those before this one: groups of E (rounded up to a warp)
+        // threads take every groups-th block
+        const int wide = min(ORDER_THREADS, (a.E + 31) / 32 * 32), groups = ORDER_THREADS / wide;
+        const int g = threadIdx.x / wide;
+        for (int e = threadIdx.x % wide; e < a.E && g < groups; e += wide) {
+            int total = 0, before = 0;
 #pragma unroll 8
-            for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
+            for (int b = g; b < static_cast<int>(gridDim.x); b += groups) {
                 const int c = a.hist[static_cast<size_t>(b) * a.E + e];
                 total += c;
                 before += b < static_cast<int>(blockIdx.x) ? c : 0;
             }
+            atomicAdd(&all[e], total);      // sums of integers: any order gives the same
+            atomicAdd(&start[e], before);
         }
     }
-    // exclusive sum over the experts
-    int incl = total;
+    __syncthreads();
+    // per expert: the warps' starts, then an exclusive sum of the rows over the experts
+    int carry = 0;
+    for (int e0 = 0; e0 < a.E; e0 += ORDER_THREADS) {
+        const int e = e0 + threadIdx.x;
+        int total = 0;
+        if (e < a.E) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        incl += lane >= o ? v : 0;
-    }
-    if (lane == 31)
-        wsum[warp] = incl;
-    __syncthreads();
-    int base = lane < warp ? wsum[lane] : 0;
-    base = __reduce_add_sync(0xFFFFFFFFu, base);
-    if (e < a.E) {
-        start[e] = base + incl - total + before;
-        if (blockIdx.x == 0) {
-            a.offsets[e] = base + incl - total;
-            if (e == a.E - 1)
-                a.offsets[a.E] = base + incl;
+            for (int w = 0; w < ORDER_WARPS; ++w) {
+                const int c = cnt[w * a.E + e];
+                cnt[w * a.E + e] = total;
+                total += c;
+            }
+            if (gridDim.x > 1)
+                total = all[e];
+        }
+        int incl = total;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            incl += lane >= o ? v : 0;
+        }
+        __syncthreads();
+        if (lane == 31)
+            wsum[warp] = incl;
+        __syncthreads();
+        const int base = carry + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wsum[lane] : 0);
+        carry += __reduce_add_sync(0xFFFFFFFFu, lane < ORDER_WARPS ? wsum[lane] : 0);
+        if (e < a.E) {
+            start[e] += base + incl - total;
+            if (blockIdx.x == 0) {
+                a.offsets[e] = base + incl - total;
+                if (e == a.E - 1)
+                    a.offsets[a.E] = base + incl;
+            }
         }
     }
     __syncthreads();
-    for (int i0 = wlo; i0 < whi; i0 += 32) {
-        const int i = i0 + lane;
-        const int ex = i < whi ? slot_expert(a, i, bad) : -2;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, ex);
-        const int rank = __popc(same & ((1u << lane) - 1u));
-        int at = 0;
-        if (ex >= 0)
-            at = start[ex] + mine[ex] + rank;
-        __syncwarp();
-        if (ex >= 0 && rank == 0)
-            mine[ex] += __popc(same);
-        __syncwarp();
-        if (i < whi)
-            a.rows[i] = ex >= 0 ? at : -1;
+    if (held) {
+#pragma unroll
+        for (int s = 0; s < ORDER_SLOTS; ++s)
+            place_slots(a, wlo + s * 32 + lane, whi, ex[s], start, mine, lane);
+    } else {
+        for (int i0 = wlo; i0 < whi; i0 += 32) {
+            const int i = i0 + lane;
+            place_slots(a, i, whi, i < whi ? slot_expert(a, i, bad) : -2, start, mine, lane);
+        }
     }
     if (gridDim.x == 1) {
         bad = __syncthreads_or(bad);
@@ -345,13 +434,17 @@ __global__ void __launch_bounds__(ORDER_THREADS) order_place_kernel(const OrderA
     }
 }
 
-// Blocks and slots a block: one block for up to ORDER_CHUNK slots (one launch), then as many as
-// there are runs of ORDER_CHUNK, and longer runs once ORDER_MAX_BLOCKS would be passed.
-void order_shape(long long n, int &blocks, int &chunk)
+// Blocks and slots a block: one block (one launch) for up to 4 * ORDER_CHUNK slots; then a block
+// for each run of ORDER_CHUNK, and longer runs where the blocks' counts, which every block
+// reads, would pass 32768 words.
+void order_shape(long long n, int E, int &blocks, int &chunk)
 {
+    const long long most = 32768 / E < 32 ? 32 : 32768 / E > 256 ? 256 : 32768 / E;
     long long c = ORDER_CHUNK;
-    if (n > c * ORDER_MAX_BLOCKS)
-        c = (n + ORDER_MAX_BLOCKS - 1) / ORDER_MAX_BLOCKS;
+    if (n <= 4 * ORDER_CHUNK)
+        c = n > ORDER_CHUNK ? 4 * ORDER_CHUNK : ORDER_CHUNK;
+    else if (n > c * most)
+        c = (n + most - 1) / most;
     c = (c + ORDER_THREADS - 1) / ORDER_THREADS * ORDER_THREADS;
     chunk = static_cast<int>(c);
     blocks = static_cast<int>(n <= 0 ? 1 : (n + c - 1) / c);
@@ -439,7 +532,7 @@ int moe_expert_order_workspace(int T, int topk, int E, uint64_t *bytes)
     if (T < 0 || topk < 1 || topk > 32 || E < 1 || E > 1024 || n > INT_MAX || !bytes)
         return MOE_ERR_INVALID_ARG;
     int blocks, chunk;
-    order_shape(n, blocks, chunk);
+    order_shape(n, E, blocks, chunk);
     *bytes = blocks > 1 ? static_cast<uint64_t>(blocks) * E * sizeof(int32_t) : 0;
     return MOE_OK;
 }
@@ -458,17 +551,19 @@ int moe_expert_order(int T, int topk, int E, const int64_t *topk_idx, int32_t *o
     OP_DEVICE(sms);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int blocks, chunk;
-    order_shape(n, blocks, chunk);
+    order_shape(n, E, blocks, chunk);
     const OrderArgs a{static_cast<int>(n), E, chunk, topk_idx, offsets, rows, status, static_cast<int32_t *>(workspace)};
     if (blocks > 1) {
         order_count_kernel<<<blocks, ORDER_THREADS, E * sizeof(int32_t), s>>>(a);
         if (launched() != MOE_OK)
             return MOE_ERR_CUDA;
     }
-    const int smem = (ORDER_WARPS + 1) * E * static_cast<int>(sizeof(int32_t));
+    const int smem = (ORDER_WARPS + 2) * E * static_cast<int>(sizeof(int32_t));
     if (smem > 48 * 1024 &&
         ensure_max_dynamic_smem(reinterpret_cast<const void *>(&order_place_kernel), smem) != cudaSuccess)
         return MOE_ERR_CUDA;
+    if (blocks > 1)
+        return launch_programmatic(order_place_kernel, blocks, ORDER_THREADS, smem, s, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     order_place_kernel<<<blocks, ORDER_THREADS, smem, s>>>(a);
     return launched();
 }
