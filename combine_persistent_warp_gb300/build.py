@@ -1,8 +1,9 @@
-"""Build the CUDA library libcpw_moe.so in-tree (nvcc, sm_103a only).
+"""Build the CUDA library libcpw_moe.so in-tree (nvcc, sm_103a only) and the Python module _ops.so.
 
 The translation units are compiled in parallel and linked into one shared library
 that exports the C ABI of include/cpw_moe.h.  The CUDA runtime is linked statically;
 the driver's tensor-map encoder is fetched at run time, so no libcuda link is needed.
+_ops.so (g++, PyTorch's headers) marshals the operators' arguments over that ABI.
 """
 import concurrent.futures as cf
 import glob
@@ -15,6 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcpw_moe.so")
+OPS = os.path.join(PKG, "_ops.so")
 SOURCES = ["api.cu", "routing.cu", "ffn.cu", "ffn_bs.cu", "noalloc.cu", "norm.cu", "router.cu",
            "rows.cu", "grouped_mm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -29,14 +31,45 @@ def _nvcc():
 
 def _deps():
     return (glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
-            [os.path.join(ROOT, "include", "cpw_moe.h"), __file__])
+            [os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "cpw_moe.h"), __file__])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(OPS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(OPS))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _compile_binding() -> str:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) if os.path.isabs(_nvcc()) else "/usr/local/cuda"
+    inc = [f"-I{p}" for p in cpp_extension.include_paths()]
+    inc += ["-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include")]
+    obj = os.path.join(BUILD, "bind.o")
+    abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", abi, *inc, "-c", os.path.join(CSRC, "bind.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on bind.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    from torch.utils import cpp_extension
+
+    tmp = OPS + f".tmp{os.getpid()}"
+    libs = [f"-L{p}" for p in cpp_extension.library_paths()]
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libcpw_moe.so", *libs, "-ltorch_python", "-ltorch_cpu",
+           "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, OPS)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -54,7 +87,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(compile_one, SOURCES))
     if verbose_ptxas:
         for _, log in results:
@@ -65,6 +99,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding.result())
     return LIB
 
 
