@@ -465,7 +465,13 @@ PyObject *grouped(Args a)
         o = matrix(tensor(a[3], "out"), "out", f, m.rows, width);
     }
     const auto call = TO_N ? moe_grouped_mm : moe_grouped_mm_dx;
-    check(call(m.rows, count(w.E, "w"), count(w.N, "w"), count(w.K, "w"), m.p, m.ld, w.p, g.p, o.p, o.ld, f.dtype, current_stream(f.dev)),
+    uint64_t need = 0;
+    check(moe_grouped_mm_workspace(m.rows, count(w.E, "w"), count(w.N, "w"), count(w.K, "w"), &need), "moe_grouped_mm_workspace");
+    at::Tensor ws;
+    if (need)
+        ws = make({static_cast<int64_t>(need)}, at::kByte, f.dev);
+    check(call(m.rows, g.E, static_cast<int>(w.N), static_cast<int>(w.K), m.p, m.ld, w.p, g.p, o.p, o.ld, f.dtype,
+               need ? ws.data_ptr() : nullptr, need, current_stream(f.dev)),
           TO_N ? "moe_grouped_mm" : "moe_grouped_mm_dx");
     if (none(a[3]))
         return THPVariable_Wrap(fresh);
@@ -498,7 +504,7 @@ PyObject *grouped_dw(Args a)
         po = flat(out, "out", {g.E, N, K}, type, f.dev);
     }
     uint64_t need = 0;
-    check(moe_grouped_mm_dw_workspace(g.E, &need), "moe_grouped_mm_dw_workspace");
+    check(moe_grouped_mm_dw_workspace(m.rows, g.E, count(N, "dy"), count(K, "x"), &need), "moe_grouped_mm_dw_workspace");
     at::Tensor ws = make({static_cast<int64_t>(need)}, at::kByte, f.dev);
     check(moe_grouped_mm_dw(m.rows, g.E, count(N, "dy"), count(K, "x"), d.p, d.ld, m.p, m.ld, g.p, po, f.dtype, code_of(type), accumulate,
                             ws.data_ptr(), need, current_stream(f.dev)),

@@ -16,6 +16,9 @@
 // with its last row (a small kernel writes them from the offsets), so TMA fills what a last
 // 64-row stage has past the group's end with zeros, in both operands.
 //
+// Few tiles with a long contraction (small batches, few experts) are split along it: each part
+// writes fp32 sums of its own, which a second kernel adds in a fixed order.
+//
 // Persistent pairs of CTAs (cta_group::2; each CTA holds 128 of the 256 M rows and half of the N
 // columns' operand), roles by warp: TMA producer, UMMA issuer (the even CTA's), and four
 // epilogue warps that drain one TMEM accumulator while the other is filled.
@@ -183,6 +186,8 @@ struct Args {
     int out32;         // dW: fp32 out
     int accumulate;    // dW: add to out
     const CUtensorMap *maps;   // dW: [E][2] maps of dy and x that end with the expert's rows
+    int splits;        // parts of the contraction
+    float *part;       // splits > 1: fp32 sums of each part, [splits][M][F] (dW: through map_out)
 };
 
 struct Shared {
@@ -216,6 +221,7 @@ struct Tile {
     int n;         // N of the UMMA (multiple of 32)
     int blocks;    // pipeline stages
     int k0, klen;  // contracted range (WEIGHTS: rows of the group)
+    int part;      // of the contraction
 };
 
 template <Kind KIND>
@@ -225,7 +231,7 @@ struct Tiles {
     int total, step, at, e;
     __device__ Tiles(const Args &a_, const Shared &s_) : a(a_), s(s_), e(0)
     {
-        total = s.tile0[a.E];
+        total = s.tile0[a.E] * a.splits;   // parts of a tile side by side
         at = blockIdx.x >> 1;
         step = gridDim.x >> 1;
     }
@@ -234,26 +240,28 @@ struct Tiles {
         if (at >= total)
             return false;
         const int ft = (a.F + TILE_F - 1) / TILE_F;
+        const int tile = at / a.splits;
+        t.part = at - tile * a.splits;
         if (KIND == WEIGHTS) {
             const int ct = (a.R + TILE_R - 1) / TILE_R;
-            t.e = at / (ft * ct);
-            const int i = at - t.e * (ft * ct);
+            t.e = tile / (ft * ct);
+            const int i = tile - t.e * (ft * ct);
             t.f0 = (i / ct) * TILE_F;
             t.r0 = (i % ct) * TILE_R;
             t.rows = min(TILE_R, a.R - t.r0);
             t.k0 = s.off[t.e];
             t.klen = s.off[t.e + 1] - t.k0;
         } else {
-            while (s.tile0[e + 1] <= at)
+            while (s.tile0[e + 1] <= tile)
                 ++e;
             t.e = e;
             const int m = s.off[e + 1] - s.off[e];
             // the group's units of 32 rows, dealt evenly to its tiles
             const int rt = (m + TILE_R - 1) / TILE_R, units = (m + 31) >> 5;
-            const int i = at - s.tile0[e], r = i / ft;
+            const int i = tile - s.tile0[e], r = i % rt;   // rows fastest: the pairs side by side share W
             const int first = r * (units / rt) + min(r, units % rt);
             const int count = units / rt + (r < units % rt ? 1 : 0);
-            t.f0 = (i - r * ft) * TILE_F;
+            t.f0 = (i / rt) * TILE_F;
             t.r0 = s.off[e] + 32 * first;
             t.rows = min(32 * count, m - 32 * first);
             t.k0 = 0;
@@ -261,6 +269,12 @@ struct Tiles {
         }
         t.n = max(32, (t.rows + 31) & ~31);
         t.blocks = (t.klen + KB - 1) / KB;
+        if (a.splits > 1) {
+            const int per = (t.blocks + a.splits - 1) / a.splits, before = min(t.blocks, t.part * per);
+            t.blocks = min(per, t.blocks - before);
+            t.k0 += before * KB;
+            t.klen = max(0, min(t.klen - before * KB, per * KB));
+        }
         at += step;
         return true;
     }
@@ -293,6 +307,18 @@ __device__ __forceinline__ void store_rows(const Args &a, const Tile &t, const u
         if (row < t.rows && fe < a.F)
             *reinterpret_cast<uint32_t *>(out + static_cast<size_t>(t.r0 + row) * a.ldo + fe) = w;
     }
+}
+
+// 32 accumulator columns of this lane's feature as fp32 sums of a part.
+__device__ __forceinline__ void store_part(const Args &a, const Tile &t, const uint32_t (&v)[32], int r, int f)
+{
+    if (f >= a.F)
+        return;
+    float *out = a.part + (static_cast<size_t>(t.part) * a.M + t.r0 + r) * a.F + f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (r + i < t.rows)
+            out[static_cast<size_t>(i) * a.F] = __uint_as_float(v[i]);
 }
 
 // A warp's 32 rows of dW[e] from the accumulator: 128 bytes of each row at a time through the
@@ -339,12 +365,12 @@ __device__ __forceinline__ void store_weights(const Args &a, const CUtensorMap *
             if (F32 && a.accumulate)
                 asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                                  reinterpret_cast<uint64_t>(map)),
-                             "r"(ptx::smem_u32(buf)), "r"(t.r0 + c), "r"(n0), "r"(t.e)
+                             "r"(ptx::smem_u32(buf)), "r"(t.r0 + c), "r"(n0), "r"(t.part * a.E + t.e)
                              : "memory");
             else
                 asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                                  reinterpret_cast<uint64_t>(map)),
-                             "r"(ptx::smem_u32(buf)), "r"(t.r0 + c), "r"(n0), "r"(t.e)
+                             "r"(ptx::smem_u32(buf)), "r"(t.r0 + c), "r"(n0), "r"(t.part * a.E + t.e)
                              : "memory");
             ptx::bulk_commit();
         }
@@ -409,8 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    if (KIND == WEIGHTS)
-        ptx::grid_dependency_wait();   // the maps' kernel (launched ahead of its end)
+    ptx::grid_dependency_wait();   // launched ahead of the end of the kernel before
     if (warp == 3) {
         // offsets clamped to a non-decreasing sequence inside [0, M], whatever they hold, and
         // the number of tiles before each expert
@@ -597,7 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     } else if (warp >= 4) {
         // -------------------------------------------------------------------- epilogue ----
         const int quarter = warp - 4;
-        if (KIND != WEIGHTS) {
+        if (KIND != WEIGHTS && a.splits == 1) {
             // rows that belong to no expert: zero (before the first one only if offsets[0] > 0)
             uint32_t *out = static_cast<uint32_t *>(a.out);
             const int words = a.F / 2;
@@ -643,6 +668,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     ptx::tmem_ld_wait(v);
                     if (KIND == WEIGHTS)
                         add_weights16(a, t, v, c, f0 + lane);
+                    else if (a.splits > 1)
+                        store_part(a, t, v, c, f0 + lane);
                     else
                         store_rows(a, t, v, c, f0 + lane, lane);
                 }
@@ -666,6 +693,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     cluster_sync_all();
     if (warp == 2)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// out[r][c] = sum over the parts, in order (+ out if ADD); rows outside [offsets[0], offsets[E]) zero.
+struct SumArgs {
+    const float *part;
+    int splits;
+    long long rows, plane;     // plane: rows * width, elements of a part
+    int width;
+    void *out;
+    long long ldo;
+    const int32_t *offsets;    // null: every row
+    int E, add;
+};
+template <typename T>
+__global__ void __launch_bounds__(256) sum_parts_kernel(const SumArgs a)
+{
+    ptx::grid_dependency_wait();
+    long long lo = 0, hi = a.rows;
+    if (a.offsets) {
+        // as the products' kernel clamps them: the running maximum, inside [0, rows]
+        int top = 0;
+        for (int i = threadIdx.x & 31; i <= a.E; i += 32)
+            top = max(top, a.offsets[i]);
+        hi = min(static_cast<long long>(__reduce_max_sync(0xFFFFFFFFu, top)), a.rows);
+        lo = min(static_cast<long long>(max(a.offsets[0], 0)), a.rows);
+    }
+    const int packs = a.width / 4;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < a.rows * packs; i += gridDim.x * 256ll) {
+        const long long row = i / packs;
+        const int c = static_cast<int>(i - row * packs) * 4;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (row >= lo && row < hi) {
+            const float *p = a.part + row * a.width + c;
+#pragma unroll 4
+            for (int s = 0; s < a.splits; ++s) {
+                const float4 q = __ldcs(reinterpret_cast<const float4 *>(p + s * a.plane));
+                v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+            }
+        }
+        T *o = static_cast<T *>(a.out) + row * a.ldo + c;
+        if (a.add) {
+            v.x += to_f<T>(o[0]), v.y += to_f<T>(o[1]), v.z += to_f<T>(o[2]), v.w += to_f<T>(o[3]);
+        }
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4 *>(o) = v;
+        } else {
+            alignas(8) T h[4] = {from_f<T>(v.x), from_f<T>(v.y), from_f<T>(v.z), from_f<T>(v.w)};
+            *reinterpret_cast<uint2 *>(o) = *reinterpret_cast<const uint2 *>(h);
+        }
+    }
 }
 
 // Tensor maps of each expert's rows of dy and x: copies of the whole tensors' maps whose row
@@ -756,10 +833,7 @@ int launch_grouped(const CUtensorMap &ma, const MapsB &mb, const CUtensorMap &mo
     constexpr int smem = KIND == WEIGHTS ? SMEM_WEIGHTS : SMEM;
     if (ensure_max_dynamic_smem(reinterpret_cast<const void *>(kern), smem) != cudaSuccess)
         return MOE_ERR_CUDA;
-    if (KIND == WEIGHTS)
-        return launch_programmatic(kern, sms / 2 * 2, THREADS, smem, s, ma, mb, mo, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-    kern<<<sms / 2 * 2, THREADS, smem, s>>>(ma, mb, mo, a);
-    return launched();
+    return launch_programmatic(kern, sms / 2 * 2, THREADS, smem, s, ma, mb, mo, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 bool grouped_sizes_ok(int64_t M, int E, int N, int K, int dtype)
@@ -768,14 +842,79 @@ bool grouped_sizes_ok(int64_t M, int E, int N, int K, int dtype)
            N <= (1 << 20) && K <= (1 << 20) && (dtype == MOE_BF16 || dtype == MOE_F16);
 }
 
+// Parts of the contraction: 1 unless the tiles (of groups of equal size) fill at most half of the
+// pairs and each part keeps at least four stages.
+int split_count(long long tiles, long long blocks, int sms)
+{
+    const long long pairs = sms / 2;
+    if (tiles * 2 > pairs || blocks < 8)
+        return 1;
+    long long n = pairs / tiles;
+    n = n < blocks / 4 ? n : blocks / 4;
+    const long long per = (blocks + n - 1) / n;
+    return static_cast<int>((blocks + per - 1) / per);
+}
+long long div_up(long long a, long long b) { return (a + b - 1) / b; }
+int row_splits(int64_t M, int E, int F, int C, int sms)
+{
+    const long long groups = M < E ? M : E, by_rows = div_up(M, TILE_R);
+    return split_count(div_up(F, TILE_F) * (groups > by_rows ? groups : by_rows), div_up(C, KB), sms);
+}
+int weight_splits(int64_t M, int E, int N, int K, int sms)
+{
+    return split_count(E * div_up(N, TILE_F) * div_up(K, TILE_R), div_up(div_up(M, E), KB), sms);
+}
+
+template <typename T>
+int sum_parts(const SumArgs &a, int sms, cudaStream_t s)
+{
+    const long long work = a.rows * (a.width / 4), blocks = div_up(work, 256);
+    return launch_programmatic(sum_parts_kernel<T>, static_cast<int>(blocks < 8ll * sms ? blocks : 8ll * sms), 256, 0, s, a) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+// Forward product and rows' gradient: F features of out, contraction of length C.
+template <Kind KIND>
+int run_rows(int64_t M, int E, int F, int C, const CUtensorMap &ma, const MapsB &mb, const int32_t *offsets, void *out, int64_t ldo,
+             int dtype, void *workspace, uint64_t workspace_bytes, int sms, cudaStream_t s)
+{
+    const int splits = row_splits(M, E, F, C, sms);
+    const uint64_t need = splits > 1 ? static_cast<uint64_t>(splits) * M * F * sizeof(float) : 0;
+    if (need && (!workspace || !op_aligned(workspace, 128) || workspace_bytes < need))
+        return MOE_ERR_INVALID_ARG;
+    const Args a{E, F, C, 0, static_cast<int>(M), offsets, out, ldo, instr(dtype == MOE_F16, KIND == ROWS, false), dtype == MOE_F16, 0, 0,
+                 nullptr, splits, static_cast<float *>(workspace)};
+    const int rc = launch_grouped<KIND>(ma, mb, ma, a, sms, s);
+    if (rc != MOE_OK || splits == 1)
+        return rc;
+    const SumArgs q{a.part, splits, M, M * F, F, out, ldo, offsets, E, 0};
+    return dtype == MOE_F16 ? sum_parts<__half>(q, sms, s) : sum_parts<__nv_bfloat16>(q, sms, s);
+}
+
 bool rows_ok(const void *p, int64_t ld, int width) { return p && op_aligned(p, 16) && ld >= width && ld % 8 == 0; }
 
 }  // namespace
 
 extern "C" {
 
+int moe_grouped_mm_workspace(int64_t M, int E, int N, int K, uint64_t *bytes)
+{
+    if (!grouped_sizes_ok(M, E, N, K, MOE_BF16) || !bytes)
+        return MOE_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (M == 0)
+        return MOE_OK;
+    OP_DEVICE(sms);
+    // the larger of the forward product's need and the rows' gradient's
+    const int fwd = row_splits(M, E, N, K, sms), dx = row_splits(M, E, K, N, sms);
+    const uint64_t a = fwd > 1 ? static_cast<uint64_t>(fwd) * M * N : 0, b = dx > 1 ? static_cast<uint64_t>(dx) * M * K : 0;
+    *bytes = (a > b ? a : b) * sizeof(float);
+    return MOE_OK;
+}
+
 int moe_grouped_mm(int64_t M, int E, int N, int K, const void *x, int64_t ldx, const void *w, const int32_t *offsets,
-                   void *out, int64_t ldo, int dtype, void *stream)
+                   void *out, int64_t ldo, int dtype, void *workspace, uint64_t workspace_bytes, void *stream)
 {
     if (!grouped_sizes_ok(M, E, N, K, dtype))
         return MOE_ERR_INVALID_ARG;
@@ -784,17 +923,15 @@ int moe_grouped_mm(int64_t M, int E, int N, int K, const void *x, int64_t ldx, c
     if (!rows_ok(x, ldx, K) || !rows_ok(out, ldo, N) || !w || !op_aligned(w, 16) || !offsets || !op_aligned(offsets, 4))
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
-    const bool f16 = dtype == MOE_F16;
     CUtensorMap ma;
     MapsB mb;
     if (!encode(&ma, w, dtype, K, N, E, K, 128) || !encode_rows(mb, x, dtype, K, M, ldx))
         return MOE_ERR_CUDA;
-    const Args a{E, N, K, 0, static_cast<int>(M), offsets, out, ldo, instr(f16, false, false), f16, 0, 0, nullptr};
-    return launch_grouped<FORWARD>(ma, mb, ma, a, sms, static_cast<cudaStream_t>(stream));
+    return run_rows<FORWARD>(M, E, N, K, ma, mb, offsets, out, ldo, dtype, workspace, workspace_bytes, sms, static_cast<cudaStream_t>(stream));
 }
 
 int moe_grouped_mm_dx(int64_t M, int E, int N, int K, const void *dy, int64_t lddy, const void *w, const int32_t *offsets,
-                      void *dx, int64_t lddx, int dtype, void *stream)
+                      void *dx, int64_t lddx, int dtype, void *workspace, uint64_t workspace_bytes, void *stream)
 {
     if (!grouped_sizes_ok(M, E, N, K, dtype))
         return MOE_ERR_INVALID_ARG;
@@ -803,20 +940,20 @@ int moe_grouped_mm_dx(int64_t M, int E, int N, int K, const void *dy, int64_t ld
     if (!rows_ok(dy, lddy, N) || !rows_ok(dx, lddx, K) || !w || !op_aligned(w, 16) || !offsets || !op_aligned(offsets, 4))
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
-    const bool f16 = dtype == MOE_F16;
     CUtensorMap ma;
     MapsB mb;
     if (!encode(&ma, w, dtype, K, N, E, K, KB) || !encode_rows(mb, dy, dtype, N, M, lddy))
         return MOE_ERR_CUDA;
-    const Args a{E, K, N, 0, static_cast<int>(M), offsets, dx, lddx, instr(f16, true, false), f16, 0, 0, nullptr};
-    return launch_grouped<ROWS>(ma, mb, ma, a, sms, static_cast<cudaStream_t>(stream));
+    return run_rows<ROWS>(M, E, K, N, ma, mb, offsets, dx, lddx, dtype, workspace, workspace_bytes, sms, static_cast<cudaStream_t>(stream));
 }
 
-int moe_grouped_mm_dw_workspace(int E, uint64_t *bytes)
+int moe_grouped_mm_dw_workspace(int64_t M, int E, int N, int K, uint64_t *bytes)
 {
-    if (E < 1 || E > MAX_E || !bytes)
+    if (!grouped_sizes_ok(M, E, N, K, MOE_BF16) || !bytes)
         return MOE_ERR_INVALID_ARG;
-    *bytes = 2ull * E * sizeof(CUtensorMap);
+    OP_DEVICE(sms);
+    const int splits = weight_splits(M, E, N, K, sms);
+    *bytes = 2ull * E * sizeof(CUtensorMap) + (splits > 1 ? static_cast<uint64_t>(splits) * E * N * K * sizeof(float) : 0);
     return MOE_OK;
 }
 
@@ -830,25 +967,36 @@ int moe_grouped_mm_dw(int64_t M, int E, int N, int K, const void *dy, int64_t ld
         return MOE_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (M > 0 && (!rows_ok(dy, lddy, N) || !rows_ok(x, ldx, K) || !offsets || !op_aligned(offsets, 4) ||
-                  !workspace || !op_aligned(workspace, 128) || workspace_bytes < 2ull * E * sizeof(CUtensorMap)))
+                  !workspace || !op_aligned(workspace, 128)))
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
+    uint64_t need = 0;
+    if (M > 0 && (moe_grouped_mm_dw_workspace(M, E, N, K, &need) != MOE_OK || workspace_bytes < need))
+        return MOE_ERR_INVALID_ARG;
     if (M == 0) {
         if (!accumulate && cudaMemsetAsync(dw, 0, static_cast<size_t>(E) * N * K * dtype_bytes(dw_dtype), s) != cudaSuccess)
             return MOE_ERR_CUDA;
         return MOE_OK;
     }
-    const bool f16 = dtype == MOE_F16;
+    const int splits = weight_splits(M, E, N, K, sms);
+    CUtensorMap *maps = static_cast<CUtensorMap *>(workspace);
+    float *part = reinterpret_cast<float *>(maps + 2 * E);
     CUtensorMap mdy, mx, mo;
     if (!encode(&mdy, dy, dtype, N, M, 0, lddy, KB) || !encode(&mx, x, dtype, K, M, 0, ldx, KB) ||
-        !encode(&mo, dw, dw_dtype, K, N, E, K, 32))
+        !(splits > 1 ? encode(&mo, part, MOE_F32, K, N, static_cast<long long>(splits) * E, K, 32)
+                     : encode(&mo, dw, dw_dtype, K, N, E, K, 32)))
         return MOE_ERR_CUDA;
-    CUtensorMap *maps = static_cast<CUtensorMap *>(workspace);
     group_maps_kernel<<<(E + MAP_WARPS - 1) / MAP_WARPS, MAP_WARPS * 32, 0, s>>>(mdy, mx, offsets, E, static_cast<int>(M), maps);
     if (launched() != MOE_OK)
         return MOE_ERR_CUDA;
-    const Args a{E, N, 0, K, static_cast<int>(M), offsets, dw, K, instr(f16, true, true), f16, dw_dtype == MOE_F32, accumulate, maps};
-    return launch_grouped<WEIGHTS>(mdy, MapsB{}, mo, a, sms, s);
+    const Args a{E, N, 0, K, static_cast<int>(M), offsets, dw, K, instr(dtype == MOE_F16, true, true), dtype == MOE_F16,
+                 splits > 1 || dw_dtype == MOE_F32, splits > 1 ? 0 : accumulate, maps, splits, part};
+    const int rc = launch_grouped<WEIGHTS>(mdy, MapsB{}, mo, a, sms, s);
+    if (rc != MOE_OK || splits == 1)
+        return rc;
+    const long long rows = static_cast<long long>(E) * N;
+    const SumArgs q{part, splits, rows, rows * K, K, dw, K, nullptr, E, accumulate};
+    return dw_dtype == MOE_F32 ? sum_parts<float>(q, sms, s) : dtype == MOE_F16 ? sum_parts<__half>(q, sms, s) : sum_parts<__nv_bfloat16>(q, sms, s);
 }
 
 int moe_ops_get_error(int *device_status, void *stream)

@@ -105,9 +105,10 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "moe_gather_rows": [I, I, I, I, I64, P, I64, I, P, P, P, P],
         "moe_combine_rows": [I, I, I, I64, P, I, P, P, P, P],
         "moe_combine_rows_backward": [I, I, I, I, I64, P, I64, P, I, P, P, P, P, P, P],
-        "moe_grouped_mm": [I64, I, I, I, P, I64, P, P, P, I64, I, P],
-        "moe_grouped_mm_dx": [I64, I, I, I, P, I64, P, P, P, I64, I, P],
-        "moe_grouped_mm_dw_workspace": [I, ctypes.POINTER(U64)],
+        "moe_grouped_mm_workspace": [I64, I, I, I, ctypes.POINTER(U64)],
+        "moe_grouped_mm": [I64, I, I, I, P, I64, P, P, P, I64, I, P, U64, P],
+        "moe_grouped_mm_dx": [I64, I, I, I, P, I64, P, P, P, I64, I, P, U64, P],
+        "moe_grouped_mm_dw_workspace": [I64, I, I, I, ctypes.POINTER(U64)],
         "moe_grouped_mm_dw": [I64, I, I, I, P, I64, P, I64, P, P, I, I, I, P, U64, P],
         "moe_ops_get_error": [ctypes.POINTER(I), P],
     }

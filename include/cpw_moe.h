@@ -373,14 +373,17 @@ int moe_combine_rows_backward(int T, int topk, int H, int E, int64_t M, const vo
  * offsets [E+1] is read by the GPU and taken as the non-decreasing sequence max(0, min(M, offsets))
  * that its running maximum gives, so no value of it leads out of the tensors; rows of out and dx
  * that belong to no expert are zeroed.  N and K multiples of 8 up to 2^20, E <= 1024, tensors
- * 16-byte aligned, row strides multiples of 8; the workspace of moe_grouped_mm_dw 128-byte
- * aligned.  The tensor core adds products to a 32-bit sum
+ * 16-byte aligned, row strides multiples of 8; workspaces 128-byte aligned.  moe_grouped_mm and
+ * moe_grouped_mm_dx need theirs (one size serves both) where a small batch is split along the
+ * contraction; 0 bytes otherwise.  Results do not depend on anything but the arguments: equal
+ * inputs give equal bits.  The tensor core adds products to a 32-bit sum
  * by truncation, so an fp32 dw is a few 1e-6 off over a thousand rows. */
+int moe_grouped_mm_workspace(int64_t M, int E, int N, int K, uint64_t *bytes);
 int moe_grouped_mm(int64_t M, int E, int N, int K, const void *x, int64_t ldx, const void *w, const int32_t *offsets,
-                   void *out, int64_t ldo, int dtype, void *stream);
+                   void *out, int64_t ldo, int dtype, void *workspace, uint64_t workspace_bytes, void *stream);
 int moe_grouped_mm_dx(int64_t M, int E, int N, int K, const void *dy, int64_t lddy, const void *w, const int32_t *offsets,
-                      void *dx, int64_t lddx, int dtype, void *stream);
-int moe_grouped_mm_dw_workspace(int E, uint64_t *bytes);
+                      void *dx, int64_t lddx, int dtype, void *workspace, uint64_t workspace_bytes, void *stream);
+int moe_grouped_mm_dw_workspace(int64_t M, int E, int N, int K, uint64_t *bytes);
 int moe_grouped_mm_dw(int64_t M, int E, int N, int K, const void *dy, int64_t lddy, const void *x, int64_t ldx,
                       const int32_t *offsets, void *dw, int dtype, int dw_dtype, int accumulate, void *workspace,
                       uint64_t workspace_bytes, void *stream);

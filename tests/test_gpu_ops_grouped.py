@@ -57,6 +57,39 @@ def test_products(sizes, N, K, dtype):
     _check(*_case(sizes, N, K, dtype))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("sizes,N,K", [
+    ([1], 256, 4096), ([3, 0, 40], 136, 2056), ([200], 520, 1544), ([5] * 9, 64, 7168), ([3000], 264, 136), ([900, 0, 4001], 72, 200),
+    ([2000, 33], 2056, 64)])
+def test_products_split_along_the_contraction(sizes, N, K, dtype):
+    """Few tiles and a long contraction, with rows of no expert: sums of parts."""
+    x, w, dy, off = _case(sizes, N, K, dtype, extra=3)
+    _check(x, w, dy, off)
+    _check(x, w, dy, off, torch.float32)
+    acc = torch.randn(len(sizes), N, K, device="cuda").to(dtype)
+    got = ops.grouped_mm_dw(dy, x, off, out=acc.clone(), accumulate=True)
+    assert torch.equal(got, (acc.float() + ops.grouped_mm_dw(dy, x, off, dtype=torch.float32)).to(dtype))
+    out = torch.full((x.shape[0], N + 24), 5.0, device="cuda", dtype=dtype)
+    assert torch.equal(ops.grouped_mm(x, w, off, out=out[:, 8:8 + N]), ops.grouped_mm(x, w, off)) and (out[:, :8] == 5).all()
+
+
+def test_missing_workspace_is_refused():
+    import ctypes
+    from combine_persistent_warp_gb300 import native
+    lib, n = native.load(), ctypes.c_uint64()
+    assert lib.moe_grouped_mm_workspace(16, 1, 256, 4096, ctypes.byref(n)) == 0 and n.value > 0
+    x, w, dy, off = _case([16], 256, 4096, torch.bfloat16)
+    out = torch.empty(16, 256, device="cuda", dtype=torch.bfloat16)
+    ws = torch.empty(n.value, device="cuda", dtype=torch.uint8)
+    args = (16, 1, 256, 4096, x.data_ptr(), 4096, w.data_ptr(), off.data_ptr(), out.data_ptr(), 256, native.BF16)
+    for p, size in ((None, n.value), (ws.data_ptr(), n.value - 1), (ws.data_ptr() + 64, n.value)):
+        assert lib.moe_grouped_mm(*args, p, size, None) == 1
+    assert lib.moe_grouped_mm_dw_workspace(16, 1, 256, 4096, ctypes.byref(n)) == 0 and n.value >= 256
+    dw = torch.empty(1, 256, 4096, device="cuda", dtype=torch.bfloat16)
+    assert lib.moe_grouped_mm_dw(16, 1, 256, 4096, dy.data_ptr(), 256, x.data_ptr(), 4096, off.data_ptr(), dw.data_ptr(), native.BF16,
+                                 native.BF16, 0, ws.data_ptr(), n.value - 1, None) == 1
+
+
 def test_ragged_groups_of_every_remainder():
     sizes = list(range(0, 70)) + [127, 129, 191, 193, 255, 257, 272, 289, 320]
     _check(*_case(sizes, 64, 72, torch.bfloat16))

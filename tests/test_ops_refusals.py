@@ -36,8 +36,10 @@ def test_empty_batches_need_no_gpu(lib):
     assert lib.moe_route_topk_backward(0, 8, 2, None, None, None, None, 8, F32, 1, None, None) == 0
     assert lib.moe_gather_rows(0, 2, 64, 4, 0, None, 64, BF16, None, None, None, None) == 0
     assert lib.moe_combine_rows(0, 2, 64, 0, None, BF16, None, None, None, None) == 0
-    assert lib.moe_grouped_mm(0, 4, 64, 64, None, 64, None, None, None, 64, BF16, None) == 0
-    assert lib.moe_grouped_mm_dx(0, 4, 64, 64, None, 64, None, None, None, 64, BF16, None) == 0
+    assert lib.moe_grouped_mm(0, 4, 64, 64, None, 64, None, None, None, 64, BF16, None, 0, None) == 0
+    assert lib.moe_grouped_mm_dx(0, 4, 64, 64, None, 64, None, None, None, 64, BF16, None, 0, None) == 0
+    n = ctypes.c_uint64(1)
+    assert lib.moe_grouped_mm_workspace(0, 4, 64, 64, ctypes.byref(n)) == 0 and n.value == 0
 
 
 @pytest.mark.parametrize("bad", [
@@ -101,7 +103,7 @@ def test_rows_refuse(lib, bad):
                                  dict(out=None), dict(out=P + 8)])
 def test_grouped_refuse(lib, bad):
     a = dict(M=16, E=4, N=64, K=64, x=P, ld=64, w=P, offsets=P, out=P, dtype=BF16) | bad
-    args = (a["M"], a["E"], a["N"], a["K"], a["x"], a["ld"], a["w"], a["offsets"], a["out"], 64, a["dtype"], None)
+    args = (a["M"], a["E"], a["N"], a["K"], a["x"], a["ld"], a["w"], a["offsets"], a["out"], 64, a["dtype"], None, 0, None)
     assert lib.moe_grouped_mm(*args) == INVALID
     assert lib.moe_grouped_mm_dx(*args) == INVALID
     assert lib.moe_grouped_mm_dw(a["M"], a["E"], a["N"], a["K"], a["x"], a["ld"], a["w"], 64, a["offsets"], a["out"], a["dtype"],
@@ -113,10 +115,12 @@ def test_grouped_dw_refuses_types(lib):
         return lib.moe_grouped_mm_dw(16, 4, 64, 64, P, 64, P, 64, P, P, dtype, out, acc, ws, ws_bytes, None)
     ws, ws_bytes = P, 4 * 256
     assert dw(BF16, F16, 0) == INVALID and dw(F16, BF16, 0) == INVALID and dw(BF16, BF16, 2) == INVALID
-    for ws, ws_bytes in ((None, 4 * 256), (P + 64, 4 * 256), (P, 4 * 256 - 1)):
+    for ws, ws_bytes in ((None, 4 * 256), (P + 64, 4 * 256)):
         assert dw(BF16, BF16, 0) == INVALID
-    assert lib.moe_grouped_mm_dw_workspace(0, ctypes.byref(ctypes.c_uint64())) == INVALID
-    assert lib.moe_grouped_mm_dw_workspace(8, None) == INVALID
+    for call in (lib.moe_grouped_mm_workspace, lib.moe_grouped_mm_dw_workspace):
+        assert call(16, 0, 64, 64, ctypes.byref(ctypes.c_uint64())) == INVALID
+        assert call(16, 8, 60, 64, ctypes.byref(ctypes.c_uint64())) == INVALID
+        assert call(16, 8, 64, 64, None) == INVALID
 
 
 def test_python_entry_points_check_shapes_and_types():
