@@ -50,22 +50,24 @@ struct RouteArgs {
 };
 
 // The k largest of a token's logits, IPL a lane (lane l holds experts l, l + 32, ...): one warp
-// maximum and one warp minimum a slot.
+// maximum and one warp minimum a slot.  Returns how many there are; lane j gets slot j's expert and
+// logit, every lane the largest logit.
 template <int IPL>
-__device__ __forceinline__ int choose(const RouteArgs &a, const float (&f)[IPL], int lane, int &my_idx, float &mine, float &top)
+__device__ __forceinline__ int choose(int k, const float (&f)[IPL], int lane, int &my_idx, float &mine, float &top)
 {
-    uint32_t key[IPL];
+    uint32_t key[IPL], kept = 0u, first = 0u;
 #pragma unroll
     for (int i = 0; i < IPL; ++i)
         key[i] = order_key(f[i]);
-    for (int j = 0; j < a.k; ++j) {
+    int j = 0;
+    for (; j < k; ++j) {
         uint32_t best = key[0];
 #pragma unroll
         for (int i = 1; i < IPL; ++i)
             best = max(best, key[i]);
         const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
         if (m == 0)
-            return j;   // only logits of -inf are left
+            break;   // only logits of -inf are left
         int at = INT_MAX;
 #pragma unroll
         for (int i = IPL - 1; i >= 0; --i)
@@ -74,49 +76,54 @@ __device__ __forceinline__ int choose(const RouteArgs &a, const float (&f)[IPL],
 #pragma unroll
         for (int i = 0; i < IPL; ++i)
             key[i] = i * 32 + lane == e ? 0u : key[i];
-        if (lane == j)
-            my_idx = e;
-        if (j == 0)
-            top = key_value(m);
-        mine = lane == j ? key_value(m) : mine;
+        my_idx = lane == j ? e : my_idx;
+        kept = lane == j ? m : kept;
+        first = j == 0 ? m : first;
     }
-    return a.k;
+    mine = key_value(kept);
+    top = key_value(first);
+    return j;
 }
 
-// 16-bit logits: the key (its upper half) and the expert (ties to the lowest) fit one word, so
-// one warp maximum a slot finds both.
-template <int IPL>
-__device__ __forceinline__ int choose16(const RouteArgs &a, const float (&f)[IPL], int lane, int &my_idx, float &mine, float &top)
+// 16-bit logits: the key (its upper 19 bits: the fp32 image of a 16-bit float has a sign, 8 bits
+// of exponent and at most 10 of fraction) and the expert (10 bits, ties to the lowest) fit one
+// word, so one warp maximum a slot finds both.
+constexpr uint32_t KEY16 = 0xFFFFE000u;
+__device__ __forceinline__ float key16_value(uint32_t word)
 {
-    uint32_t key[IPL];
+    // the low bits of a positive value's key are zeros, of a negative one's are ones
+    const uint32_t up = word & KEY16;
+    return up == KEY16 ? __uint_as_float(0x7FC00000u) : key_value((up & 0x80000000u) ? up : up | ~KEY16);
+}
+template <int IPL>
+__device__ __forceinline__ int choose16(int k, const float (&f)[IPL], int lane, int &my_idx, float &mine, float &top)
+{
+    uint32_t key[IPL], kept = 0u, first = 0u;
 #pragma unroll
     for (int i = 0; i < IPL; ++i) {
-        // the fp32 image of a 16-bit float keeps its order in 16 + 3 bits: sign, 8 bits of
-        // exponent and 10 of fraction; the expert takes 10 bits and 3 are left over
-        const uint32_t k = order_key(f[i]);
-        key[i] = k == 0u ? 0u : (k & 0xFFFFE000u) | static_cast<uint32_t>(1023 - (i * 32 + lane));
+        const uint32_t v = order_key(f[i]);
+        key[i] = v == 0u ? 0u : (v & KEY16) | static_cast<uint32_t>(1023 - (i * 32 + lane));
     }
-    for (int j = 0; j < a.k; ++j) {
+    int j = 0;
+    for (; j < k; ++j) {
         uint32_t best = key[0];
 #pragma unroll
         for (int i = 1; i < IPL; ++i)
             best = max(best, key[i]);
         const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
         if (m == 0)
-            return j;
+            break;
 #pragma unroll
         for (int i = 0; i < IPL; ++i)
             key[i] = key[i] == m ? 0u : key[i];
-        // the low bits of a positive value's key are zeros, of a negative one's are ones
-        const uint32_t up = m & 0xFFFFE000u;
-        const float v = up == 0xFFFFE000u ? __uint_as_float(0x7FC00000u) : key_value((up & 0x80000000u) ? up : up | 0x1FFFu);
-        if (lane == j)
-            my_idx = 1023 - static_cast<int>(m & 0x1FFFu);
-        if (j == 0)
-            top = v;
-        mine = lane == j ? v : mine;
+        kept = lane == j ? m : kept;
+        first = j == 0 ? m : first;
     }
-    return a.k;
+    if (lane < j)
+        my_idx = 1023 - static_cast<int>(kept & ~KEY16);
+    mine = key16_value(kept);
+    top = key16_value(first);
+    return j;
 }
 
 template <typename T, int IPL>
@@ -139,9 +146,9 @@ __global__ void __launch_bounds__(WARPS * 32) route_kernel(const RouteArgs a)
         float top = 0.0f, mine = 0.0f;
         int found;
         if constexpr (sizeof(T) == 2)
-            found = choose16<IPL>(a, f, lane, my_idx, mine, top);
+            found = choose16<IPL>(a.k, f, lane, my_idx, mine, top);
         else
-            found = choose<IPL>(a, f, lane, my_idx, mine, top);
+            found = choose<IPL>(a.k, f, lane, my_idx, mine, top);
         const float p = lane < found ? expf(mine - top) : 0.0f;
         float sum = p;
         if (!a.renorm) {
@@ -201,12 +208,9 @@ __global__ void __launch_bounds__(WARPS * 32) route_backward_kernel(const RouteB
         for (int j = 0; j < a.k; ++j) {
             const int ej = __shfl_sync(0xFFFFFFFFu, e, j);
             const float v = __shfl_sync(0xFFFFFFFFu, mine, j);
-            if (ej >= 0 && (ej & 31) == lane) {
 #pragma unroll
-                for (int i = 0; i < IPL; ++i)
-                    if (i == ej >> 5)
-                        d[i] += v;
-            }
+            for (int i = 0; i < IPL; ++i)
+                d[i] += ej == i * 32 + lane ? v : 0.0f;
         }
     } else {
         const T *l = static_cast<const T *>(a.logits) + static_cast<size_t>(t) * a.ld;
@@ -233,12 +237,9 @@ __global__ void __launch_bounds__(WARPS * 32) route_backward_kernel(const RouteB
         for (int j = 0; j < a.k; ++j) {
             const int ej = __shfl_sync(0xFFFFFFFFu, e, j);
             const float v = __shfl_sync(0xFFFFFFFFu, dw, j);
-            if (ej >= 0 && (ej & 31) == lane) {
 #pragma unroll
-                for (int i = 0; i < IPL; ++i)
-                    if (i == ej >> 5)
-                        d[i] += v;
-            }
+            for (int i = 0; i < IPL; ++i)
+                d[i] += ej == i * 32 + lane ? v : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < IPL; ++i)
