@@ -52,59 +52,115 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// V elements as V / 2 pairs (V = 1: one pair whose second value is not used).
-template <int V>
-constexpr int PAIRS = V == 1 ? 1 : V / 2;
+// ------------------------------------------------------------------ a thread's part of a row ----
+// VPT packs of V elements (V = 8: 16-byte accesses; V = 1: any alignment), pack j at position
+// t + j * step of the row for thread t of the `step` threads that share it; held as pairs.
+template <int V, int VPT>
+constexpr int PAIRS = V * VPT / 2;
 
-template <typename T, int V>
-__device__ __forceinline__ void unpack(float2 (&f)[PAIRS<V>], const Pack<T, V> &q)
+template <typename T>
+__device__ __forceinline__ float2 pair_of(const T *q)
 {
-    if constexpr (V == 1) {
-        f[0] = make_float2(to_f<T>(q.v[0]), 0.0f);
-    } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-        const uint32_t *u = reinterpret_cast<const uint32_t *>(&q);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i)
-            f[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        const uint32_t u = *reinterpret_cast<const uint32_t *>(q);
+        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
     } else {
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i)
-            f[i] = make_float2(to_f<T>(q.v[2 * i]), to_f<T>(q.v[2 * i + 1]));
+        return make_float2(to_f<T>(q[0]), to_f<T>(q[1]));
     }
 }
 
-template <typename T, int V>
-__device__ __forceinline__ Pack<T, V> pack(const float2 (&f)[PAIRS<V>])
+template <typename T, int V, int VPT>
+__device__ __forceinline__ void unpack(float2 (&f)[PAIRS<V, VPT>], const Pack<T, V> (&q)[VPT])
 {
-    Pack<T, V> q;
-    if constexpr (V == 1) {
-        q.v[0] = from_f<T>(f[0].x);
-    } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i)
-            *reinterpret_cast<__nv_bfloat162 *>(&q.v[2 * i]) = __float22bfloat162_rn(f[i]);
-    } else {
+    for (int i = 0; i < PAIRS<V, VPT>; ++i) {
+        if constexpr (V == 1)
+            f[i] = make_float2(to_f<T>(q[2 * i].v[0]), to_f<T>(q[2 * i + 1].v[0]));
+        else
+            f[i] = pair_of<T>(&q[2 * i / V].v[2 * i % V]);
+    }
+}
+
+// Packs past the row's end are zeros.
+template <typename T, int V, int VPT>
+__device__ __forceinline__ void fetch(Pack<T, V> (&q)[VPT], const T *row, int t, int step, int packs)
+{
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            q.v[2 * i] = from_f<T>(f[i].x);
-            q.v[2 * i + 1] = from_f<T>(f[i].y);
+    for (int j = 0; j < VPT; ++j) {
+        const int p = t + j * step;
+        if (p < packs) {
+            q[j] = load_pack<T, V>(row + static_cast<size_t>(p) * V);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                q[j].v[i] = from_f<T>(0.0f);
         }
     }
-    return q;
 }
 
-// A weight's or bias's V values (`none` where there is no such vector).
-template <typename T, int V>
-__device__ __forceinline__ void load_affine(float2 (&f)[PAIRS<V>], const void *p, int w32, size_t at, float none)
+template <typename T, int V, int VPT>
+__device__ __forceinline__ void put(T *row, const float2 (&f)[PAIRS<V, VPT>], int t, int step, int packs)
+{
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int p = t + j * step;
+        if (p < packs) {
+            Pack<T, V> q;
+            if constexpr (V == 1) {
+                q.v[0] = from_f<T>((j & 1) ? f[j / 2].y : f[j / 2].x);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    const float2 u = f[j * (V / 2) + i];
+                    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+                        *reinterpret_cast<__nv_bfloat162 *>(&q.v[2 * i]) = __float22bfloat162_rn(u);
+                    } else {
+                        q.v[2 * i] = from_f<T>(u.x);
+                        q.v[2 * i + 1] = from_f<T>(u.y);
+                    }
+                }
+            }
+            store_pack<T, V>(row + static_cast<size_t>(p) * V, q);
+        }
+    }
+}
+
+// Zeroes the pairs (or halves of pairs) past the row's end.
+template <int V, int VPT>
+__device__ __forceinline__ void clip(float2 (&f)[PAIRS<V, VPT>], int t, int step, int packs)
+{
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const bool in = t + j * step < packs;
+        if constexpr (V == 1) {
+            if (j & 1)
+                f[j / 2].y = in ? f[j / 2].y : 0.0f;
+            else
+                f[j / 2].x = in ? f[j / 2].x : 0.0f;
+        } else if (!in) {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i)
+                f[j * (V / 2) + i] = both(0.0f);
+        }
+    }
+}
+
+// A weight's or bias's columns (`none` where there is no such vector).
+template <typename T, int V, int VPT>
+__device__ __forceinline__ void load_columns(float2 (&f)[PAIRS<V, VPT>], const void *p, int w32, float none, int t, int step, int packs)
 {
     if (!p) {
 #pragma unroll
-        for (int i = 0; i < PAIRS<V>; ++i)
+        for (int i = 0; i < PAIRS<V, VPT>; ++i)
             f[i] = both(none);
     } else if (w32) {
-        unpack<float, V>(f, load_pack<float, V>(static_cast<const float *>(p) + at));
+        Pack<float, V> q[VPT];
+        fetch<float, V, VPT>(q, static_cast<const float *>(p), t, step, packs);
+        unpack<float, V, VPT>(f, q);
     } else {
-        unpack<T, V>(f, load_pack<T, V>(static_cast<const T *>(p) + at));
+        Pack<T, V> q[VPT];
+        fetch<T, V, VPT>(q, static_cast<const T *>(p), t, step, packs);
+        unpack<T, V, VPT>(f, q);
     }
 }
 
@@ -155,6 +211,19 @@ __device__ __forceinline__ void clear_sums(float *red)
             red[i] = 0.0f;
 }
 
+// The same over the threads that share a row: a warp or the block.
+template <bool WARP, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float *red, int slot)
+{
+    if constexpr (WARP) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = warp_sum(v[i]);
+    } else {
+        block_sum(v, red, slot);
+    }
+}
+
 struct NormArgs {
     int T, H;
     const void *x;
@@ -194,11 +263,10 @@ __device__ __forceinline__ void copies_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-constexpr int AHEAD = 4;   // ring stages
 
 // Row r's packs of this thread into ring stage g (nothing past the last row).
 template <typename T, int V, int VPT>
-__device__ __forceinline__ void fetch_row(Pack<T, V> *ring, int g, const void *base, long long ld, int r, int T_, int packs)
+__device__ __forceinline__ void fetch_ahead(Pack<T, V> *ring, int g, const void *base, long long ld, int r, int T_, int packs)
 {
     if (r < T_) {
         const T *x = static_cast<const T *>(base) + static_cast<size_t>(r) * ld;
@@ -210,61 +278,65 @@ __device__ __forceinline__ void fetch_row(Pack<T, V> *ring, int g, const void *b
         }
     }
 }
+// (slots past the row's end were never copied to: clip() the pairs)
+template <typename T, int V, int VPT>
+__device__ __forceinline__ void from_ring(float2 (&f)[PAIRS<V, VPT>], const Pack<T, V> *ring, int g)
+{
+    Pack<T, V> q[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+        q[j] = ring[(g * VPT + j) * blockDim.x + threadIdx.x];
+    unpack<T, V, VPT>(f, q);
+}
 
 // ------------------------------------------------------------------ forward -------------
-// The row held in f (zeros in packs past its end), its statistics and outputs; w and b: the
-// thread's columns of weight and bias.  FP8: e4m3 codes and 1x128 scales instead of y (V = 8: 16
-// lanes hold one group of 128).  `after_read` runs once every thread has its row in registers.
-template <typename T, int V, int VPT, bool FP8, typename F>
-__device__ __forceinline__ void norm_row(const NormArgs &a, int row, float2 (&f)[VPT][PAIRS<V>], const float2 (&w)[VPT][PAIRS<V>],
-                                         const float2 (&b)[VPT][PAIRS<V>], float *red, F after_read)
+// The row held in f (zeros past its end), its statistics and outputs; w and b: the thread's
+// columns of weight and bias.  FP8: e4m3 codes and 1x128 scales instead of y (V = 8: 16 lanes
+// hold one group of 128).  `after_read` runs once every thread has its row in registers.
+template <typename T, int V, int VPT, bool FP8, bool WARP, typename F>
+__device__ __forceinline__ void norm_row(const NormArgs &a, int row, float2 (&f)[PAIRS<V, VPT>], const float2 (&w)[PAIRS<V, VPT>],
+                                         const float2 (&b)[PAIRS<V, VPT>], float *red, F after_read)
 {
-    constexpr int P = PAIRS<V>;
-    const int packs = a.H / V;
+    constexpr int P = PAIRS<V, VPT>;
+    const int packs = a.H / V, t = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
     const float inv = 1.0f / static_cast<float>(a.H);
     float2 acc = both(0.0f);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-            acc = add2(acc, f[j][i]);
+    for (int i = 0; i < P; ++i)
+        acc = add2(acc, f[i]);
     float s[1] = {acc.x + acc.y};
-    block_sum(s, red, 0);
+    row_sum<WARP>(s, red, 0);
     after_read();
     const float mean = s[0] * inv;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        f[i] = add2(f[i], both(-mean));
+    clip<V, VPT>(f, t, step, packs);
     acc = both(0.0f);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        if (static_cast<int>(threadIdx.x + j * blockDim.x) < packs) {
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                f[j][i] = add2(f[j][i], make_float2(-mean, V == 1 ? 0.0f : -mean));
-                acc = fma2(f[j][i], f[j][i], acc);
-            }
-        }
-    }
+    for (int i = 0; i < P; ++i)
+        acc = fma2(f[i], f[i], acc);
     s[0] = acc.x + acc.y;
-    block_sum(s, red, 1);
+    row_sum<WARP>(s, red, 1);
     const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
-    if (threadIdx.x == 0) {
+    if (t == 0) {
         if (a.mean)
             a.mean[row] = mean;
         if (a.rstd)
             a.rstd[row] = rstd;
     }
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int p = threadIdx.x + j * blockDim.x;
-        const bool in = p < packs;
-        float2 y[P];
+    for (int i = 0; i < P; ++i)
+        f[i] = fma2(mul2(f[i], both(rstd)), w[i], b[i]);
+    if constexpr (FP8) {
+        // packs of a group of 128 lie in one half-warp; whole groups are in or out
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-            y[i] = fma2(mul2(f[j][i], both(rstd)), w[j][i], b[j][i]);
-        if constexpr (FP8) {
-            // packs of a group of 128 lie in one half-warp; whole groups are in or out
+        for (int j = 0; j < VPT; ++j) {
+            const float2 *y = f + j * (V / 2);
+            const int p = t + j * step;
             float m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < P; ++i)
+            for (int i = 0; i < V / 2; ++i)
                 m = fmaxf(m, fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1)
@@ -274,97 +346,96 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, int row, float2 (&f)
                 const uint32_t u = __float_as_uint(sf);
                 sf = __uint_as_float((u + 0x7FFFFFu) & 0xFF800000u);
             }
-            if (in) {
+            // one reciprocal a group, not a quotient an element: the product is within one
+            // fp32 rounding of the quotient, which e4m3's three bits of fraction hide
+            const float2 r = both(1.0f / sf);
+            if (p < packs) {
                 uint32_t code[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    code[h] = ptx::cvt_e4m3x2(y[2 * h].x / sf, y[2 * h].y / sf) |
-                              (ptx::cvt_e4m3x2(y[2 * h + 1].x / sf, y[2 * h + 1].y / sf) << 16);
-                *reinterpret_cast<uint2 *>(a.q + static_cast<size_t>(row) * a.H + static_cast<size_t>(p) * V) =
-                    make_uint2(code[0], code[1]);
+                for (int h = 0; h < 2; ++h) {
+                    const float2 lo = mul2(y[2 * h], r), hi = mul2(y[2 * h + 1], r);
+                    code[h] = ptx::cvt_e4m3x2(lo.x, lo.y) | (ptx::cvt_e4m3x2(hi.x, hi.y) << 16);
+                }
+                *reinterpret_cast<uint2 *>(a.q + static_cast<size_t>(row) * a.H + static_cast<size_t>(p) * V) = make_uint2(code[0], code[1]);
                 if ((p & 15) == 0)
                     a.sf[static_cast<size_t>(row) * (a.H / 128) + (p >> 4)] = sf;
             }
-        } else if (in) {
-            store_pack<T, V>(static_cast<T *>(a.y) + static_cast<size_t>(row) * a.H + static_cast<size_t>(p) * V, pack<T, V>(y));
         }
+    } else {
+        put<T, V, VPT>(static_cast<T *>(a.y) + static_cast<size_t>(row) * a.H, f, t, step, packs);
     }
 }
 
-template <typename T, int V, int VPT>
-__device__ __forceinline__ void load_columns(float2 (&w)[VPT][PAIRS<V>], const void *p, int w32, int packs, float none)
+// One row a block; or (WARP, rows of at most 1024 elements) one row a warp at a time, the next
+// one on its way.  The weight and bias are loaded beside the first row, ahead of its sums.
+constexpr int ROW_WARPS = 4;
+template <typename T, int V, int VPT, bool FP8, bool WARP>
+__global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : V * VPT == 32 ? 512 : 1024) norm_kernel(const NormArgs a)
 {
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int at = threadIdx.x + j * blockDim.x;
-        load_affine<T, V>(w[j], at < packs ? p : nullptr, w32, static_cast<size_t>(at) * V, none);
-    }
-}
-
-// One block a row.  The weight and bias are loaded beside the row, ahead of its sums.
-template <typename T, int V, int VPT, bool FP8>
-__global__ void __launch_bounds__(V * VPT == 32 || V * VPT == 8 && V == 1 ? 512 : 1024) norm_kernel(const NormArgs a)
-{
-    __shared__ __align__(16) float red[64];
-    const int packs = a.H / V;
-    const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(blockIdx.x) * a.ldx;
-    clear_sums<1>(red);
-    float2 f[VPT][PAIRS<V>], w[VPT][PAIRS<V>], b[VPT][PAIRS<V>];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int p = threadIdx.x + j * blockDim.x;
-        if (p < packs) {
-            unpack<T, V>(f[j], load_pack<T, V>(x + static_cast<size_t>(p) * V));
-        } else {
-#pragma unroll
-            for (int i = 0; i < PAIRS<V>; ++i)
-                f[j][i] = both(0.0f);
+    constexpr int P = PAIRS<V, VPT>;
+    __shared__ __align__(16) float red[WARP ? 4 : 64];
+    const int packs = a.H / V, t = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
+    if constexpr (!WARP)
+        clear_sums<1>(red);
+    const T *x = static_cast<const T *>(a.x);
+    int row = WARP ? blockIdx.x * ROW_WARPS + (threadIdx.x >> 5) : blockIdx.x;
+    if (row >= a.T)
+        return;
+    Pack<T, V> q[VPT];
+    fetch<T, V, VPT>(q, x + static_cast<size_t>(row) * a.ldx, t, step, packs);
+    float2 f[P], w[P], b[P];
+    load_columns<T, V, VPT>(w, a.weight, a.w32, 1.0f, t, step, packs);
+    load_columns<T, V, VPT>(b, a.bias, a.w32, 0.0f, t, step, packs);
+    if constexpr (WARP) {
+        for (;;) {
+            unpack<T, V, VPT>(f, q);
+            const int next = row + gridDim.x * ROW_WARPS;
+            if (next < a.T)
+                fetch<T, V, VPT>(q, x + static_cast<size_t>(next) * a.ldx, t, step, packs);
+            norm_row<T, V, VPT, FP8, true>(a, row, f, w, b, red, [] {});
+            if (next >= a.T)
+                return;
+            row = next;
         }
+    } else {
+        unpack<T, V, VPT>(f, q);
+        norm_row<T, V, VPT, FP8, false>(a, row, f, w, b, red, [] {});
     }
-    load_columns<T, V, VPT>(w, a.weight, a.w32, packs, 1.0f);
-    load_columns<T, V, VPT>(b, a.bias, a.w32, packs, 0.0f);
-    norm_row<T, V, VPT, FP8>(a, blockIdx.x, f, w, b, red, [] {});
 }
 
 // Persistent blocks: rows copied AHEAD rows before their use, weight and bias kept in registers.
-template <typename T, int V, int VPT, bool FP8>
+template <typename T, int V, int VPT, bool FP8, int AHEAD>
 __global__ void __launch_bounds__(512) norm_ring_kernel(const NormArgs a)
 {
+    constexpr int P = PAIRS<V, VPT>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[64];
     Pack<T, V> *ring = reinterpret_cast<Pack<T, V> *>(smem);
     const int packs = a.H / V;
 #pragma unroll
     for (int g = 0; g < AHEAD; ++g) {
-        fetch_row<T, V, VPT>(ring, g, a.x, a.ldx, blockIdx.x + g * gridDim.x, a.T, packs);
+        fetch_ahead<T, V, VPT>(ring, g, a.x, a.ldx, blockIdx.x + g * gridDim.x, a.T, packs);
         copies_commit();
     }
     clear_sums<1>(red);
-    float2 w[VPT][PAIRS<V>], b[VPT][PAIRS<V>];
-    load_columns<T, V, VPT>(w, a.weight, a.w32, packs, 1.0f);
-    load_columns<T, V, VPT>(b, a.bias, a.w32, packs, 0.0f);
+    float2 w[P], b[P];
+    load_columns<T, V, VPT>(w, a.weight, a.w32, 1.0f, threadIdx.x, blockDim.x, packs);
+    load_columns<T, V, VPT>(b, a.bias, a.w32, 0.0f, threadIdx.x, blockDim.x, packs);
     int g = 0;
     for (int row = blockIdx.x; row < a.T; row += gridDim.x) {
         copies_wait<AHEAD - 1>();
-        float2 f[VPT][PAIRS<V>];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            if (static_cast<int>(threadIdx.x + j * blockDim.x) < packs) {
-                unpack<T, V>(f[j], ring[(g * VPT + j) * blockDim.x + threadIdx.x]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < PAIRS<V>; ++i)
-                    f[j][i] = both(0.0f);
-            }
-        }
-        norm_row<T, V, VPT, FP8>(a, row, f, w, b, red, [&] {
-            fetch_row<T, V, VPT>(ring, g, a.x, a.ldx, row + AHEAD * gridDim.x, a.T, packs);
+        float2 f[P];
+        from_ring<T, V, VPT>(f, ring, g);
+        clip<V, VPT>(f, threadIdx.x, blockDim.x, packs);
+        norm_row<T, V, VPT, FP8, false>(a, row, f, w, b, red, [&] {
+            fetch_ahead<T, V, VPT>(ring, g, a.x, a.ldx, row + AHEAD * gridDim.x, a.T, packs);
             copies_commit();
         });
         g = g == AHEAD - 1 ? 0 : g + 1;
     }
 }
 
+// ------------------------------------------------------------------ backward ------------
 struct NormBwdArgs {
     int T, H;
     const void *dy, *x;
@@ -376,113 +447,168 @@ struct NormBwdArgs {
     float *part;   // [2][blocks][H] sums of dy*xh and of dy over each block's rows
 };
 
-// Block b takes rows b, b + blocks, ...: a thread keeps its columns' two sums in registers over
-// all of them, so dy and x are read once.  RING: rows of x and dy copied AHEAD rows before use.
-template <typename T, int V, int VPT, bool RING>
-__global__ void __launch_bounds__(V == 1 && VPT == 16 ? 1024 : 512) norm_backward_kernel(const NormBwdArgs a)
+// xh and a = dy*g of one row, its two sums, and the columns' sums so far.
+template <int P>
+__device__ __forceinline__ void backward_sums(float2 (&xh)[P], const float2 (&d)[P], const float2 (&w)[P], float2 (&dg)[P], float2 (&db)[P],
+                                              float mean, float rstd, float (&s)[2])
 {
-    constexpr int P = PAIRS<V>;
+    float2 s0 = both(0.0f), s1 = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        xh[i] = mul2(add2(xh[i], both(-mean)), both(rstd));
+        dg[i] = fma2(d[i], xh[i], dg[i]);
+        db[i] = add2(db[i], d[i]);
+        const float2 g = mul2(d[i], w[i]);
+        s0 = add2(s0, g);
+        s1 = fma2(g, xh[i], s1);
+    }
+    s[0] = s0.x + s0.y;
+    s[1] = s1.x + s1.y;
+}
+template <int P>
+__device__ __forceinline__ void backward_out(float2 (&o)[P], const float2 (&xh)[P], const float2 (&d)[P], const float2 (&w)[P], float inv,
+                                             float rstd, const float (&s)[2])
+{
+    const float2 ma = both(-s[0] * inv), mb = both(-s[1] * inv);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        o[i] = mul2(fma2(xh[i], mb, fma2(d[i], w[i], ma)), both(rstd));
+}
+
+// Rows b, b + blocks, ... of block b: a thread keeps its columns' two sums in registers over all
+// of them, so dy and x are read once from HBM.  AHEAD > 0: rows of x and dy copied that many rows
+// before use, and read from shared memory twice (for the sums, then for dx) instead of held in
+// registers between.
+template <typename T, int V, int VPT, int AHEAD>
+__global__ void __launch_bounds__(V * VPT <= 16 && V == 1 ? 1024 : 512) norm_backward_kernel(const NormBwdArgs a)
+{
+    constexpr int P = PAIRS<V, VPT>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[128];
-    const int packs = a.H / V;
+    const int packs = a.H / V, t = threadIdx.x, step = blockDim.x;
     const float inv = 1.0f / static_cast<float>(a.H);
     Pack<T, V> *ring_x = reinterpret_cast<Pack<T, V> *>(smem), *ring_d = ring_x + AHEAD * VPT * blockDim.x;
-    if constexpr (RING) {
+    if constexpr (AHEAD > 0) {
 #pragma unroll
         for (int g = 0; g < AHEAD; ++g) {
-            fetch_row<T, V, VPT>(ring_x, g, a.x, a.ldx, blockIdx.x + g * gridDim.x, a.T, packs);
-            fetch_row<T, V, VPT>(ring_d, g, a.dy, a.lddy, blockIdx.x + g * gridDim.x, a.T, packs);
+            fetch_ahead<T, V, VPT>(ring_x, g, a.x, a.ldx, blockIdx.x + g * gridDim.x, a.T, packs);
+            fetch_ahead<T, V, VPT>(ring_d, g, a.dy, a.lddy, blockIdx.x + g * gridDim.x, a.T, packs);
             copies_commit();
         }
     }
     clear_sums<2>(red);
-    float2 w[VPT][P], dg[VPT][P], db[VPT][P];
-    load_columns<T, V, VPT>(w, a.weight, a.w32, packs, 1.0f);
+    float2 w[P], dg[P], db[P];
+    load_columns<T, V, VPT>(w, a.weight, a.w32, 1.0f, t, step, packs);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-            dg[j][i] = db[j][i] = both(0.0f);
+    for (int i = 0; i < P; ++i)
+        dg[i] = db[i] = both(0.0f);
     int slot = 0, stage = 0;
-    float mean = 0.0f, rstd = 0.0f;
-    if (static_cast<int>(blockIdx.x) < a.T) {
-        mean = a.mean[blockIdx.x];
-        rstd = a.rstd[blockIdx.x];
-    }
+    float mean = a.mean[blockIdx.x], rstd = a.rstd[blockIdx.x];   // (no more blocks than rows)
     for (int row = blockIdx.x; row < a.T; row += gridDim.x, slot ^= 1) {
         const int next = row + gridDim.x;
         const float mean1 = next < a.T ? a.mean[next] : 0.0f, rstd1 = next < a.T ? a.rstd[next] : 0.0f;
-        if constexpr (RING)
+        float2 xh[P], d[P];
+        if constexpr (AHEAD > 0) {
             copies_wait<AHEAD - 1>();
-        float2 xh[VPT][P], g[VPT][P];
-        float2 s0 = both(0.0f), s1 = both(0.0f);
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int p = threadIdx.x + j * blockDim.x;
-            if (p < packs) {
-                float2 d[P];
-                if constexpr (RING) {
-                    unpack<T, V>(xh[j], ring_x[(stage * VPT + j) * blockDim.x + threadIdx.x]);
-                    unpack<T, V>(d, ring_d[(stage * VPT + j) * blockDim.x + threadIdx.x]);
-                } else {
-                    unpack<T, V>(xh[j], load_pack<T, V>(static_cast<const T *>(a.x) + static_cast<size_t>(row) * a.ldx + static_cast<size_t>(p) * V));
-                    unpack<T, V>(d, load_pack<T, V>(static_cast<const T *>(a.dy) + static_cast<size_t>(row) * a.lddy + static_cast<size_t>(p) * V));
-                }
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    xh[j][i] = mul2(add2(xh[j][i], both(-mean)), both(rstd));
-                    dg[j][i] = fma2(d[i], xh[j][i], dg[j][i]);
-                    db[j][i] = add2(db[j][i], d[i]);
-                    g[j][i] = mul2(d[i], w[j][i]);
-                    s0 = add2(s0, g[j][i]);
-                    s1 = fma2(g[j][i], xh[j][i], s1);
-                }
-            }
+            from_ring<T, V, VPT>(xh, ring_x, stage);
+            from_ring<T, V, VPT>(d, ring_d, stage);
+        } else {
+            Pack<T, V> q[VPT];
+            fetch<T, V, VPT>(q, static_cast<const T *>(a.x) + static_cast<size_t>(row) * a.ldx, t, step, packs);
+            unpack<T, V, VPT>(xh, q);
+            fetch<T, V, VPT>(q, static_cast<const T *>(a.dy) + static_cast<size_t>(row) * a.lddy, t, step, packs);
+            unpack<T, V, VPT>(d, q);
         }
-        // (V = 1: the second values of d are zeros, and so are all products with them)
-        float s[2] = {s0.x + s0.y, s1.x + s1.y};
+        if constexpr (AHEAD > 0) {   // what lies past the row's end is not there: no products with it
+            clip<V, VPT>(xh, t, step, packs);
+            clip<V, VPT>(d, t, step, packs);
+        }
+        float s[2];
+        backward_sums<P>(xh, d, w, dg, db, mean, rstd, s);
         block_sum(s, red, slot);
-        if constexpr (RING) {   // every value read above has been used in the sums
-            fetch_row<T, V, VPT>(ring_x, stage, a.x, a.ldx, row + AHEAD * gridDim.x, a.T, packs);
-            fetch_row<T, V, VPT>(ring_d, stage, a.dy, a.lddy, row + AHEAD * gridDim.x, a.T, packs);
+        float2 o[P];
+        if constexpr (AHEAD > 0) {
+            from_ring<T, V, VPT>(xh, ring_x, stage);
+            from_ring<T, V, VPT>(d, ring_d, stage);
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                xh[i] = mul2(add2(xh[i], both(-mean)), both(rstd));
+        }
+        backward_out<P>(o, xh, d, w, inv, rstd, s);
+        put<T, V, VPT>(static_cast<T *>(a.dx) + static_cast<size_t>(row) * a.H, o, t, step, packs);
+        if constexpr (AHEAD > 0) {   // (every value read above has been used by now)
+            fetch_ahead<T, V, VPT>(ring_x, stage, a.x, a.ldx, row + AHEAD * gridDim.x, a.T, packs);
+            fetch_ahead<T, V, VPT>(ring_d, stage, a.dy, a.lddy, row + AHEAD * gridDim.x, a.T, packs);
             copies_commit();
             stage = stage == AHEAD - 1 ? 0 : stage + 1;
-        }
-        const float2 ma = both(-s[0] * inv), mb = both(-s[1] * inv);
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int p = threadIdx.x + j * blockDim.x;
-            if (p < packs) {
-                float2 o[P];
-#pragma unroll
-                for (int i = 0; i < P; ++i)
-                    o[i] = mul2(fma2(xh[j][i], mb, add2(g[j][i], ma)), both(rstd));
-                store_pack<T, V>(static_cast<T *>(a.dx) + static_cast<size_t>(row) * a.H + static_cast<size_t>(p) * V, pack<T, V>(o));
-            }
         }
         mean = mean1;
         rstd = rstd1;
     }
-    if (!a.part)
-        return;
-    float *pg = a.part + static_cast<size_t>(blockIdx.x) * a.H;
-    float *pb = pg + static_cast<size_t>(gridDim.x) * a.H;
+    if (a.part) {
+        put<float, V, VPT>(a.part + static_cast<size_t>(blockIdx.x) * a.H, dg, t, step, packs);
+        put<float, V, VPT>(a.part + (static_cast<size_t>(gridDim.x) + blockIdx.x) * a.H, db, t, step, packs);
+    }
+    ptx::launch_dependents();
+}
+
+// Rows of at most 1024 elements: one row a warp at a time, the next one on its way; the block's
+// warps add their columns' sums at the end, in order.
+template <typename T, int V, int VPT>
+__global__ void __launch_bounds__(ROW_WARPS * 32) norm_backward_warp_kernel(const NormBwdArgs a)
+{
+    constexpr int P = PAIRS<V, VPT>;
+    __shared__ float sums[2][ROW_WARPS][32 * V * VPT];
+    const int packs = a.H / V, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float inv = 1.0f / static_cast<float>(a.H);
+    const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
+    float2 w[P], dg[P], db[P];
+    load_columns<T, V, VPT>(w, a.weight, a.w32, 1.0f, lane, 32, packs);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int p = threadIdx.x + j * blockDim.x;
-        if (p < packs) {
-            if constexpr (V == 1) {
-                pg[p] = dg[j][0].x;
-                pb[p] = db[j][0].x;
-            } else {
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    *reinterpret_cast<float2 *>(pg + static_cast<size_t>(p) * V + 2 * i) = dg[j][i];
-                    *reinterpret_cast<float2 *>(pb + static_cast<size_t>(p) * V + 2 * i) = db[j][i];
-                }
+    for (int i = 0; i < P; ++i)
+        dg[i] = db[i] = both(0.0f);
+    int row = blockIdx.x * ROW_WARPS + warp;
+    if (row < a.T) {
+        Pack<T, V> qx[VPT], qd[VPT];
+        fetch<T, V, VPT>(qx, x + static_cast<size_t>(row) * a.ldx, lane, 32, packs);
+        fetch<T, V, VPT>(qd, dy + static_cast<size_t>(row) * a.lddy, lane, 32, packs);
+        float mean = a.mean[row], rstd = a.rstd[row];
+        for (;;) {
+            float2 xh[P], d[P], o[P];
+            unpack<T, V, VPT>(xh, qx);
+            unpack<T, V, VPT>(d, qd);
+            const int next = row + gridDim.x * ROW_WARPS;
+            const float m = mean, r = rstd;
+            if (next < a.T) {
+                fetch<T, V, VPT>(qx, x + static_cast<size_t>(next) * a.ldx, lane, 32, packs);
+                fetch<T, V, VPT>(qd, dy + static_cast<size_t>(next) * a.lddy, lane, 32, packs);
+                mean = a.mean[next];
+                rstd = a.rstd[next];
             }
+            float s[2];
+            backward_sums<P>(xh, d, w, dg, db, m, r, s);
+            row_sum<true>(s, nullptr, 0);
+            backward_out<P>(o, xh, d, w, inv, r, s);
+            put<T, V, VPT>(static_cast<T *>(a.dx) + static_cast<size_t>(row) * a.H, o, lane, 32, packs);
+            if (next >= a.T)
+                break;
+            row = next;
         }
     }
+    if (a.part) {
+        put<float, V, VPT>(sums[0][warp], dg, lane, 32, 32 * VPT);
+        put<float, V, VPT>(sums[1][warp], db, lane, 32, 32 * VPT);
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * a.H; i += ROW_WARPS * 32) {
+            const int which = i >= a.H, c = i - which * a.H;
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < ROW_WARPS; ++k)
+                v += sums[which][k][c];
+            a.part[(static_cast<size_t>(which) * gridDim.x + blockIdx.x) * a.H + c] = v;
+        }
+    }
+    ptx::launch_dependents();
 }
 
 // Column sums of the partial sums, in a fixed order: a block of 32 columns x 32 row lanes.
@@ -490,6 +616,7 @@ template <typename TW>
 __global__ void norm_reduce_kernel(const float *part, int blocks, int H, TW *dweight, TW *dbias)
 {
     __shared__ float tile[32][33];
+    ptx::grid_dependency_wait();
     const float *src = part + static_cast<size_t>(blockIdx.y) * blocks * H;
     TW *dst = blockIdx.y == 0 ? dweight : dbias;
     if (!dst)
@@ -507,6 +634,22 @@ __global__ void norm_reduce_kernel(const float *part, int blocks, int H, TW *dwe
     const int out = blockIdx.x * 32 + threadIdx.y;
     if (threadIdx.x == 0 && out < H)
         dst[out] = from_f<TW>(s);
+}
+
+// Started while the last rows are still worked on; it waits for them before it reads.
+template <typename TW>
+cudaError_t launch_reduce(const float *part, int blocks, int H, TW *dweight, TW *dbias, cudaStream_t s)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((H + 31) / 32, 2);
+    cfg.blockDim = dim3(32, 32);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_reduce_kernel<TW>, part, blocks, H, dweight, dbias);
 }
 
 int round32(int v) { return (v + 31) / 32 * 32; }
@@ -530,20 +673,6 @@ bool norm_args_ok(int T, int H, int dtype, int w_dtype, const void *weight, cons
     return op_aligned(weight, wb) && op_aligned(bias, wb);
 }
 
-// Persistent blocks an SM: about 512 threads, each with rows on their way.
-int ring_blocks_per_sm(int threads)
-{
-    const int n = 512 / threads;
-    return n < 1 ? 1 : n > 8 ? 8 : n;
-}
-
-// Shared memory of a block's ring, and whether its blocks fit an SM.
-size_t ring_bytes(int threads, int vpt, size_t pack_bytes, int tensors)
-{
-    return static_cast<size_t>(AHEAD) * vpt * threads * pack_bytes * tensors;
-}
-bool ring_fits(size_t bytes, int per_sm) { return bytes * per_sm <= 200 * 1024; }
-
 template <typename K>
 bool allow_smem(K kern, size_t bytes)
 {
@@ -551,67 +680,142 @@ bool allow_smem(K kern, size_t bytes)
            ensure_max_dynamic_smem(reinterpret_cast<const void *>(kern), static_cast<int>(bytes)) == cudaSuccess;
 }
 
-template <typename T, int V, int VPT, bool FP8>
+// Persistent blocks an SM of `threads` threads, AHEAD stages and `tensors` tensors in the ring:
+// about 512 threads, within the SM's shared memory.
+template <typename T, int V, int VPT>
+int ring_blocks(int threads, int ahead, int tensors, size_t &smem)
+{
+    smem = static_cast<size_t>(ahead) * VPT * threads * sizeof(Pack<T, V>) * tensors;
+    const size_t fit = smem ? 200 * 1024 / smem : 0;
+    const size_t want = threads >= 512 ? 1 : 512 / threads;
+    return static_cast<int>(fit < want ? fit : want);
+}
+
+template <typename T, bool FP8, int AHEAD>
 bool try_norm_ring(const NormArgs &a, int num_sms, cudaStream_t s)
 {
-    const int threads = round32((a.H / V + VPT - 1) / VPT);
-    if (threads > 512)
-        return false;
-    const int per_sm = ring_blocks_per_sm(threads);
-    const size_t smem = ring_bytes(threads, VPT, sizeof(Pack<T, V>), 1);
+    const int threads = round32((a.H / 8 + 3) / 4);
+    size_t smem;
+    const int per_sm = ring_blocks<T, 8, 4>(threads, AHEAD, 1, smem);
     // long batches only: every block has rows to copy ahead of
-    if (a.T < AHEAD * per_sm * num_sms || !ring_fits(smem, per_sm))
+    if (per_sm < 1 || a.T < AHEAD * per_sm * num_sms)
         return false;
-    const auto kern = norm_ring_kernel<T, V, VPT, FP8>;
+    const auto kern = norm_ring_kernel<T, 8, 4, FP8, AHEAD>;
     if (!allow_smem(kern, smem))
         return false;
     kern<<<per_sm * num_sms, threads, smem, s>>>(a);
     return true;
 }
 
+// Blocks of one-row-a-warp kernels: a warp for each row up to `per_sm` blocks an SM.
+int warp_blocks(int T, int per_sm, int num_sms)
+{
+    const int need = (T + ROW_WARPS - 1) / ROW_WARPS, most = per_sm * num_sms;
+    return need < most ? need : most;
+}
+
+template <typename T, int V, int VPT, bool FP8>
+void launch_norm_warps(const NormArgs &a, int num_sms, cudaStream_t s)
+{
+    norm_kernel<T, V, VPT, FP8, true><<<warp_blocks(a.T, 8, num_sms), ROW_WARPS * 32, 0, s>>>(a);
+}
+
 template <typename T, bool FP8>
 void launch_norm(const NormArgs &a, bool packed, int num_sms, cudaStream_t s)
 {
+    const bool few = a.T <= 4 * num_sms;   // few rows: as many threads a row as it has packs (latency)
     if (packed) {
         const int packs = a.H / 8;
-        if (try_norm_ring<T, 8, 4, FP8>(a, num_sms, s))
-            return;
-        // few rows: as many threads as a row has packs (latency); else four packs a thread
-        if (a.T <= 4 * num_sms && packs <= 1024)
-            norm_kernel<T, 8, 1, FP8><<<a.T, round32(packs), 0, s>>>(a);
-        else
-            norm_kernel<T, 8, 4, FP8><<<a.T, round32((packs + 3) / 4), 0, s>>>(a);
+        if (packs <= 32)
+            launch_norm_warps<T, 8, 1, FP8>(a, num_sms, s);
+        else if (packs <= 128 && !few)
+            launch_norm_warps<T, 8, 4, FP8>(a, num_sms, s);
+        else if (few && packs <= 1024)
+            norm_kernel<T, 8, 1, FP8, false><<<a.T, round32(packs), 0, s>>>(a);
+        else if (!try_norm_ring<T, FP8, 4>(a, num_sms, s))
+            norm_kernel<T, 8, 4, FP8, false><<<a.T, round32((packs + 3) / 4), 0, s>>>(a);
     } else if constexpr (!FP8) {
-        if constexpr (sizeof(T) == 4)
-            if (try_norm_ring<T, 1, 8, false>(a, num_sms, s))
-                return;
-        if (a.H <= 4096)
-            norm_kernel<T, 1, 8, false><<<a.T, round32((a.H + 7) / 8), 0, s>>>(a);
+        if (a.H <= 256)
+            launch_norm_warps<T, 1, 8, false>(a, num_sms, s);
+        else if (a.H <= 1024 && !few)
+            launch_norm_warps<T, 1, 32, false>(a, num_sms, s);
+        else if (a.H <= 4096)
+            norm_kernel<T, 1, 8, false, false><<<a.T, round32((a.H + 7) / 8), 0, s>>>(a);
         else
-            norm_kernel<T, 1, 16, false><<<a.T, round32((a.H + 15) / 16), 0, s>>>(a);
+            norm_kernel<T, 1, 16, false, false><<<a.T, round32((a.H + 15) / 16), 0, s>>>(a);
     }
 }
 
-// Blocks of the backward kernel: each keeps one row of partial sums.
-int backward_blocks(int T, int H, int num_sms)
+// The backward pass: kernel, blocks (each keeps a row of partial sums) and how they are found.
+enum Plan { WARPS_1, WARPS_4, RING, DIRECT };
+template <typename T>
+Plan backward_plan(int T_, int H, bool packed, int num_sms, int &blocks)
 {
-    const int most = ring_blocks_per_sm(H >= 8192 ? 512 : H >= 1024 ? 256 : 128) * num_sms;
-    return T < most ? T : most;
-}
-
-template <typename T, int V, int VPT>
-void launch_backward(const NormBwdArgs &a, int blocks, cudaStream_t s)
-{
-    const int threads = round32((a.H / V + VPT - 1) / VPT);
-    if constexpr (sizeof(Pack<T, V>) >= 4) {
-        const size_t smem = ring_bytes(threads, VPT, sizeof(Pack<T, V>), 2);
-        const auto kern = norm_backward_kernel<T, V, VPT, true>;
-        if (a.T >= AHEAD * blocks && smem <= 100 * 1024 && allow_smem(kern, smem)) {
-            kern<<<blocks, threads, smem, s>>>(a);
-            return;
+    if (H <= 256 || (H <= 1024 && T_ > 2 * num_sms)) {
+        blocks = warp_blocks(T_, 3, num_sms);
+        return H <= 256 ? WARPS_1 : WARPS_4;
+    }
+    if (packed) {
+        size_t smem;
+        const int per_sm = H <= 8192 ? ring_blocks<T, 8, 2>(round32((H / 8 + 1) / 2), H <= 4096 ? 4 : 3, 2, smem)
+                                     : ring_blocks<T, 8, 4>(round32((H / 8 + 3) / 4), 2, 2, smem);
+        if (per_sm >= 1 && T_ >= 4 * per_sm * num_sms) {
+            blocks = per_sm * num_sms;
+            return RING;
         }
     }
-    norm_backward_kernel<T, V, VPT, false><<<blocks, threads, 0, s>>>(a);
+    blocks = H >= 4096 ? num_sms : 2 * num_sms;
+    blocks = T_ < blocks ? T_ : blocks;
+    return DIRECT;
+}
+// (the workspace covers either alignment)
+template <typename T>
+int most_backward_blocks(int T_, int H, int num_sms)
+{
+    int p, u;
+    backward_plan<T>(T_, H, true, num_sms, p);
+    backward_plan<T>(T_, H, false, num_sms, u);
+    return p > u ? p : u;
+}
+
+template <typename T, int VPT, int AHEAD>
+bool launch_backward_ring(const NormBwdArgs &a, int blocks, cudaStream_t s)
+{
+    const int threads = round32((a.H / 8 + VPT - 1) / VPT);
+    size_t smem;
+    ring_blocks<T, 8, VPT>(threads, AHEAD, 2, smem);
+    const auto kern = norm_backward_kernel<T, 8, VPT, AHEAD>;
+    if (!allow_smem(kern, smem))
+        return false;
+    kern<<<blocks, threads, smem, s>>>(a);
+    return true;
+}
+
+template <typename T>
+bool launch_backward(const NormBwdArgs &a, bool packed, Plan plan, int blocks, cudaStream_t s)
+{
+    const int packs = a.H / 8;
+    if (plan == RING)
+        return a.H <= 4096   ? launch_backward_ring<T, 2, 4>(a, blocks, s)
+               : a.H <= 8192 ? launch_backward_ring<T, 2, 3>(a, blocks, s)
+                             : launch_backward_ring<T, 4, 2>(a, blocks, s);
+    if (plan == WARPS_1 && packed)
+        norm_backward_warp_kernel<T, 8, 1><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
+    else if (plan == WARPS_1)
+        norm_backward_warp_kernel<T, 1, 8><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
+    else if (plan == WARPS_4 && packed)
+        norm_backward_warp_kernel<T, 8, 4><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
+    else if (plan == WARPS_4)
+        norm_backward_warp_kernel<T, 1, 32><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
+    else if (packed && a.H <= 8192)
+        norm_backward_kernel<T, 8, 2, 0><<<blocks, round32((packs + 1) / 2), 0, s>>>(a);
+    else if (packed)
+        norm_backward_kernel<T, 8, 4, 0><<<blocks, round32((packs + 3) / 4), 0, s>>>(a);
+    else if (a.H <= 4096)
+        norm_backward_kernel<T, 1, 8, 0><<<blocks, round32((a.H + 7) / 8), 0, s>>>(a);
+    else
+        norm_backward_kernel<T, 1, 16, 0><<<blocks, round32((a.H + 15) / 16), 0, s>>>(a);
+    return true;
 }
 
 }  // namespace
@@ -661,7 +865,9 @@ int moe_layer_norm_backward_workspace(int T, int H, uint64_t *bytes)
     if (T < 0 || H < 1 || H > MAX_H || !bytes)
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
-    *bytes = 2ull * backward_blocks(T, H, sms) * static_cast<uint64_t>(H) * sizeof(float);
+    // enough for every element type
+    const int a = most_backward_blocks<float>(T, H, sms), b = most_backward_blocks<__nv_bfloat16>(T, H, sms);
+    *bytes = 2ull * (a > b ? a : b) * static_cast<uint64_t>(H) * sizeof(float);
     return MOE_OK;
 }
 
@@ -680,39 +886,32 @@ int moe_layer_norm_backward(int T, int H, const void *dy, int64_t lddy, const vo
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int blocks = backward_blocks(T, H, sms);
     const bool sums = dweight || dbias;
+    uint64_t need = 0;
     if (sums && T > 0 &&
-        (!workspace || !op_aligned(workspace, 16) || workspace_bytes < 2ull * blocks * static_cast<uint64_t>(H) * sizeof(float)))
+        (!workspace || !op_aligned(workspace, 16) || moe_layer_norm_backward_workspace(T, H, &need) != MOE_OK || workspace_bytes < need))
         return MOE_ERR_INVALID_ARG;
+    int blocks = 0;
     if (T > 0) {
         const NormBwdArgs a{T, H, dy, x, lddy, ldx, weight, w_dtype == MOE_F32 && dtype != MOE_F32, mean, rstd, dx,
                             sums ? static_cast<float *>(workspace) : nullptr};
         const bool packed = packed_rows(H, dtype, x, ldx) && packed_rows(H, dtype, dy, lddy) && op_aligned(dx, 16) &&
                             packed_affine(weight);
-        with_dtype(dtype, [&](auto *t) {
+        const bool ok = with_dtype(dtype, [&](auto *t) {
             using E = std::remove_pointer_t<decltype(t)>;
-            if (packed && H <= 8192)
-                launch_backward<E, 8, 2>(a, blocks, s);
-            else if (packed)
-                launch_backward<E, 8, 4>(a, blocks, s);
-            else if (H <= 4096)
-                launch_backward<E, 1, 8>(a, blocks, s);
-            else
-                launch_backward<E, 1, 16>(a, blocks, s);
+            const Plan plan = backward_plan<E>(T, H, packed, sms, blocks);
+            return launch_backward<E>(a, packed, plan, blocks, s);
         });
-        const int rc = launched();
-        if (rc != MOE_OK)
-            return rc;
+        if (!ok || launched() != MOE_OK)
+            return MOE_ERR_CUDA;
     }
     if (sums) {
         // T == 0: no partial rows, the sums are zero
-        with_dtype(w_dtype, [&](auto *t) {
+        const cudaError_t e = with_dtype(w_dtype, [&](auto *t) {
             using E = std::remove_pointer_t<decltype(t)>;
-            norm_reduce_kernel<E><<<dim3((H + 31) / 32, 2), dim3(32, 32), 0, s>>>(
-                static_cast<const float *>(workspace), blocks, H, static_cast<E *>(dweight), static_cast<E *>(dbias));
+            return launch_reduce<E>(static_cast<const float *>(workspace), blocks, H, static_cast<E *>(dweight), static_cast<E *>(dbias), s);
         });
-        return launched();
+        return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     }
     return MOE_OK;
 }
