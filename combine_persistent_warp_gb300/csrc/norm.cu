@@ -246,16 +246,11 @@ __device__ __forceinline__ void copy_ahead(Pack<T, V> *slot, const T *src)
 {
     constexpr int BYTES = static_cast<int>(sizeof(Pack<T, V>));
     const uint32_t dst = ptx::smem_u32(slot);
-    if constexpr (BYTES >= 16) {
+    static_assert(BYTES % 16 == 0, "copies of 16 bytes");
 #pragma unroll
-        for (int i = 0; i < BYTES / 16; ++i)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * i),
-                         "l"(reinterpret_cast<uint64_t>(src) + 16 * i)
-                         : "memory");
-    } else {
-        static_assert(BYTES == 4, "copies of 4 or 16 bytes");
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
-    }
+    for (int i = 0; i < BYTES / 16; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * i), "l"(reinterpret_cast<uint64_t>(src) + 16 * i)
+                     : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -287,6 +282,62 @@ __device__ __forceinline__ void from_ring(float2 (&f)[PAIRS<V, VPT>], const Pack
     for (int j = 0; j < VPT; ++j)
         q[j] = ring[(g * VPT + j) * blockDim.x + threadIdx.x];
     unpack<T, V, VPT>(f, q);
+}
+
+// ------------------------------------------------------------------ unaligned rows ahead ----
+// Rows of any alignment, copied by the whole block in the 16-byte vectors that cover them: the
+// row lies in its stage at the byte phase that it has in memory, so both sides are aligned, and
+// a thread then reads single elements.  The vectors may hold neighbouring bytes of the matrix,
+// but none outside [begin, end): the last ones are cut short (cp.async fills with zeros), and
+// the elements of one that starts before the matrix are moved one by one.
+struct ByteRows {
+    const char *begin, *end;   // of the matrix
+    long long pitch;           // bytes
+    int bytes;                 // of a row
+};
+template <typename T>
+ByteRows byte_rows(const void *p, long long ld, int T_, int H)
+{
+    const char *b = static_cast<const char *>(p);
+    const long long pitch = ld * static_cast<long long>(sizeof(T));
+    return {b, b + pitch * (T_ - 1) + static_cast<long long>(H) * sizeof(T), pitch, static_cast<int>(H * sizeof(T))};
+}
+__host__ __device__ __forceinline__ int stage_bytes(int row_bytes) { return (row_bytes + 15 + 15) / 16 * 16; }
+template <typename T>
+__device__ __forceinline__ void fetch_bytes(uint8_t *stage, const ByteRows &m, int row)
+{
+    const char *a = m.begin + m.pitch * row;
+    const int phase = static_cast<int>(reinterpret_cast<uint64_t>(a) & 15);
+    const char *a0 = a - phase;
+    const int vectors = (phase + m.bytes + 15) >> 4;
+    for (int v = threadIdx.x; v < vectors; v += blockDim.x) {
+        const char *src = a0 + 16 * static_cast<long long>(v);
+        if (src < m.begin) {
+            const int stop = min(16, phase + m.bytes);
+            for (int i = phase; i < stop; i += static_cast<int>(sizeof(T)))
+                *reinterpret_cast<T *>(stage + i) = *reinterpret_cast<const T *>(a0 + i);
+        } else {
+            const long long left = m.end - src;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(stage + 16 * v)),
+                         "l"(reinterpret_cast<uint64_t>(src)), "r"(static_cast<int>(left < 16 ? left : 16))
+                         : "memory");
+        }
+    }
+}
+// Elements t, t + step, ... of a row in its stage (zeros past its end).
+template <typename T, int VPT>
+__device__ __forceinline__ void from_bytes(float2 (&f)[PAIRS<1, VPT>], const uint8_t *stage, const ByteRows &m, int row, int H)
+{
+    const T *e = reinterpret_cast<const T *>(stage + (reinterpret_cast<uint64_t>(m.begin + m.pitch * row) & 15));
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int c = threadIdx.x + j * blockDim.x;
+        const float v = c < H ? to_f<T>(e[c]) : 0.0f;
+        if (j & 1)
+            f[j / 2].y = v;
+        else
+            f[j / 2].x = v;
+    }
 }
 
 // ------------------------------------------------------------------ forward -------------
@@ -346,9 +397,9 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, int row, float2 (&f)
                 const uint32_t u = __float_as_uint(sf);
                 sf = __uint_as_float((u + 0x7FFFFFu) & 0xFF800000u);
             }
-            // one reciprocal a group, not a quotient an element: the product is within one
-            // fp32 rounding of the quotient, which e4m3's three bits of fraction hide
-            const float2 r = both(1.0f / sf);
+            // one reciprocal a group, not a quotient an element: the product is within a few
+            // fp32 roundings of the quotient, which e4m3's three bits of fraction hide
+            const float2 r = both(__fdividef(1.0f, sf));
             if (p < packs) {
                 uint32_t code[2];
 #pragma unroll
@@ -429,6 +480,41 @@ __global__ void __launch_bounds__(512) norm_ring_kernel(const NormArgs a)
         clip<V, VPT>(f, threadIdx.x, blockDim.x, packs);
         norm_row<T, V, VPT, FP8, false>(a, row, f, w, b, red, [&] {
             fetch_ahead<T, V, VPT>(ring, g, a.x, a.ldx, row + AHEAD * gridDim.x, a.T, packs);
+            copies_commit();
+        });
+        g = g == AHEAD - 1 ? 0 : g + 1;
+    }
+}
+
+// Persistent blocks over rows of any alignment (more than 1024 elements).
+template <typename T, int VPT, int AHEAD>
+__global__ void __launch_bounds__(1024) norm_bytes_kernel(const NormArgs a, const ByteRows m)
+{
+    constexpr int P = PAIRS<1, VPT>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float red[64];
+    const int size = stage_bytes(m.bytes);
+#pragma unroll
+    for (int g = 0; g < AHEAD; ++g) {
+        const int row = blockIdx.x + g * gridDim.x;
+        if (row < a.T)
+            fetch_bytes<T>(smem + g * size, m, row);
+        copies_commit();
+    }
+    clear_sums<1>(red);
+    float2 w[P], b[P];
+    load_columns<T, 1, VPT>(w, a.weight, a.w32, 1.0f, threadIdx.x, blockDim.x, a.H);
+    load_columns<T, 1, VPT>(b, a.bias, a.w32, 0.0f, threadIdx.x, blockDim.x, a.H);
+    int g = 0;
+    for (int row = blockIdx.x; row < a.T; row += gridDim.x) {
+        copies_wait<AHEAD - 1>();
+        __syncthreads();   // the other threads' copies
+        float2 f[P];
+        from_bytes<T, VPT>(f, smem + g * size, m, row, a.H);
+        norm_row<T, 1, VPT, false, false>(a, row, f, w, b, red, [&] {
+            const int next = row + AHEAD * gridDim.x;
+            if (next < a.T)
+                fetch_bytes<T>(smem + g * size, m, next);
             copies_commit();
         });
         g = g == AHEAD - 1 ? 0 : g + 1;
@@ -548,6 +634,59 @@ __global__ void __launch_bounds__(V * VPT <= 16 && V == 1 ? 1024 : 512) norm_bac
     if (a.part) {
         put<float, V, VPT>(a.part + static_cast<size_t>(blockIdx.x) * a.H, dg, t, step, packs);
         put<float, V, VPT>(a.part + (static_cast<size_t>(gridDim.x) + blockIdx.x) * a.H, db, t, step, packs);
+    }
+    ptx::launch_dependents();
+}
+
+// Rows of any alignment (more than 1024 elements).
+template <typename T, int VPT, int AHEAD>
+__global__ void __launch_bounds__(1024) norm_backward_bytes_kernel(const NormBwdArgs a, const ByteRows mx, const ByteRows md)
+{
+    constexpr int P = PAIRS<1, VPT>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float red[128];
+    const int t = threadIdx.x, step = blockDim.x, size = stage_bytes(mx.bytes);
+    const float inv = 1.0f / static_cast<float>(a.H);
+    uint8_t *ring_d = smem + AHEAD * size;
+#pragma unroll
+    for (int g = 0; g < AHEAD; ++g) {
+        const int row = blockIdx.x + g * gridDim.x;
+        if (row < a.T) {
+            fetch_bytes<T>(smem + g * size, mx, row);
+            fetch_bytes<T>(ring_d + g * size, md, row);
+        }
+        copies_commit();
+    }
+    clear_sums<2>(red);
+    float2 w[P], dg[P], db[P];
+    load_columns<T, 1, VPT>(w, a.weight, a.w32, 1.0f, t, step, a.H);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        dg[i] = db[i] = both(0.0f);
+    int slot = 0, g = 0;
+    for (int row = blockIdx.x; row < a.T; row += gridDim.x, slot ^= 1) {
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        copies_wait<AHEAD - 1>();
+        __syncthreads();   // the other threads' copies
+        float2 xh[P], d[P], o[P];
+        from_bytes<T, VPT>(xh, smem + g * size, mx, row, a.H);
+        from_bytes<T, VPT>(d, ring_d + g * size, md, row, a.H);
+        float s[2];
+        backward_sums<P>(xh, d, w, dg, db, mean, rstd, s);
+        block_sum(s, red, slot);
+        const int next = row + AHEAD * gridDim.x;   // every thread has read the stage
+        if (next < a.T) {
+            fetch_bytes<T>(smem + g * size, mx, next);
+            fetch_bytes<T>(ring_d + g * size, md, next);
+        }
+        copies_commit();
+        g = g == AHEAD - 1 ? 0 : g + 1;
+        backward_out<P>(o, xh, d, w, inv, rstd, s);
+        put<T, 1, VPT>(static_cast<T *>(a.dx) + static_cast<size_t>(row) * a.H, o, t, step, a.H);
+    }
+    if (a.part) {
+        put<float, 1, VPT>(a.part + static_cast<size_t>(blockIdx.x) * a.H, dg, t, step, a.H);
+        put<float, 1, VPT>(a.part + (static_cast<size_t>(gridDim.x) + blockIdx.x) * a.H, db, t, step, a.H);
     }
     ptx::launch_dependents();
 }
@@ -714,6 +853,45 @@ int warp_blocks(int T, int per_sm, int num_sms)
     return need < most ? need : most;
 }
 
+// Blocks an SM (about 1024 threads), stages and shared memory of the kernels for rows of any
+// alignment, `tensors` rows a stage.
+struct BytesPlan {
+    int threads, per_sm, ahead;
+    size_t smem;
+};
+BytesPlan bytes_plan(int H, size_t elem, int tensors)
+{
+    BytesPlan p{};
+    p.threads = H <= 8192 ? round32((H + 7) / 8) : 1024;
+    const size_t stage = static_cast<size_t>(stage_bytes(static_cast<int>(H * elem))) * tensors;
+    p.ahead = 3 * stage <= 200 * 1024 ? 3 : 1;
+    p.smem = p.ahead * stage;
+    const size_t fit = 200 * 1024 / p.smem, want = 1024 / p.threads;
+    p.per_sm = static_cast<int>(fit < want ? fit : want);
+    return p;
+}
+
+template <typename T, int VPT, int AHEAD>
+bool launch_norm_bytes(const NormArgs &a, const BytesPlan &p, int num_sms, cudaStream_t s)
+{
+    const auto kern = norm_bytes_kernel<T, VPT, AHEAD>;
+    if (!allow_smem(kern, p.smem))
+        return false;
+    const int most = p.per_sm * num_sms;
+    kern<<<a.T < most ? a.T : most, p.threads, p.smem, s>>>(a, byte_rows<T>(a.x, a.ldx, a.T, a.H));
+    return true;
+}
+
+template <typename T, int VPT, int AHEAD>
+bool launch_backward_bytes(const NormBwdArgs &a, const BytesPlan &p, int blocks, cudaStream_t s)
+{
+    const auto kern = norm_backward_bytes_kernel<T, VPT, AHEAD>;
+    if (!allow_smem(kern, p.smem))
+        return false;
+    kern<<<blocks, p.threads, p.smem, s>>>(a, byte_rows<T>(a.x, a.ldx, a.T, a.H), byte_rows<T>(a.dy, a.lddy, a.T, a.H));
+    return true;
+}
+
 template <typename T, int V, int VPT, bool FP8>
 void launch_norm_warps(const NormArgs &a, int num_sms, cudaStream_t s)
 {
@@ -721,7 +899,7 @@ void launch_norm_warps(const NormArgs &a, int num_sms, cudaStream_t s)
 }
 
 template <typename T, bool FP8>
-void launch_norm(const NormArgs &a, bool packed, int num_sms, cudaStream_t s)
+bool launch_norm(const NormArgs &a, bool packed, int num_sms, cudaStream_t s)
 {
     const bool few = a.T <= 4 * num_sms;   // few rows: as many threads a row as it has packs (latency)
     if (packed) {
@@ -737,21 +915,24 @@ void launch_norm(const NormArgs &a, bool packed, int num_sms, cudaStream_t s)
     } else if constexpr (!FP8) {
         if (a.H <= 256)
             launch_norm_warps<T, 1, 8, false>(a, num_sms, s);
-        else if (a.H <= 1024 && !few)
+        else if (a.H <= 1024)
             launch_norm_warps<T, 1, 32, false>(a, num_sms, s);
-        else if (a.H <= 4096)
-            norm_kernel<T, 1, 8, false, false><<<a.T, round32((a.H + 7) / 8), 0, s>>>(a);
-        else
-            norm_kernel<T, 1, 16, false, false><<<a.T, round32((a.H + 15) / 16), 0, s>>>(a);
+        else {
+            const BytesPlan p = bytes_plan(a.H, sizeof(T), 1);
+            return a.H > 8192    ? (p.ahead == 3 ? launch_norm_bytes<T, 16, 3>(a, p, num_sms, s) : launch_norm_bytes<T, 16, 1>(a, p, num_sms, s))
+                   : p.ahead == 3 ? launch_norm_bytes<T, 8, 3>(a, p, num_sms, s)
+                                  : launch_norm_bytes<T, 8, 1>(a, p, num_sms, s);
+        }
     }
+    return true;
 }
 
 // The backward pass: kernel, blocks (each keeps a row of partial sums) and how they are found.
-enum Plan { WARPS_1, WARPS_4, RING, DIRECT };
+enum Plan { WARPS_1, WARPS_4, RING, DIRECT, BYTES };
 template <typename T>
 Plan backward_plan(int T_, int H, bool packed, int num_sms, int &blocks)
 {
-    if (H <= 256 || (H <= 1024 && T_ > 2 * num_sms)) {
+    if (H <= 256 || (H <= 1024 && (!packed || T_ > 2 * num_sms))) {
         blocks = warp_blocks(T_, 3, num_sms);
         return H <= 256 ? WARPS_1 : WARPS_4;
     }
@@ -764,9 +945,9 @@ Plan backward_plan(int T_, int H, bool packed, int num_sms, int &blocks)
             return RING;
         }
     }
-    blocks = H >= 4096 ? num_sms : 2 * num_sms;
+    blocks = packed ? (H >= 4096 ? 1 : 2) * num_sms : bytes_plan(H, sizeof(T), 2).per_sm * num_sms;
     blocks = T_ < blocks ? T_ : blocks;
-    return DIRECT;
+    return packed ? DIRECT : BYTES;
 }
 // (the workspace covers either alignment)
 template <typename T>
@@ -807,14 +988,15 @@ bool launch_backward(const NormBwdArgs &a, bool packed, Plan plan, int blocks, c
         norm_backward_warp_kernel<T, 8, 4><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
     else if (plan == WARPS_4)
         norm_backward_warp_kernel<T, 1, 32><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
-    else if (packed && a.H <= 8192)
+    else if (plan == BYTES) {
+        const BytesPlan p = bytes_plan(a.H, sizeof(T), 2);
+        return a.H > 8192     ? (p.ahead == 3 ? launch_backward_bytes<T, 16, 3>(a, p, blocks, s) : launch_backward_bytes<T, 16, 1>(a, p, blocks, s))
+               : p.ahead == 3 ? launch_backward_bytes<T, 8, 3>(a, p, blocks, s)
+                              : launch_backward_bytes<T, 8, 1>(a, p, blocks, s);
+    } else if (a.H <= 8192)
         norm_backward_kernel<T, 8, 2, 0><<<blocks, round32((packs + 1) / 2), 0, s>>>(a);
-    else if (packed)
-        norm_backward_kernel<T, 8, 4, 0><<<blocks, round32((packs + 3) / 4), 0, s>>>(a);
-    else if (a.H <= 4096)
-        norm_backward_kernel<T, 1, 8, 0><<<blocks, round32((a.H + 7) / 8), 0, s>>>(a);
     else
-        norm_backward_kernel<T, 1, 16, 0><<<blocks, round32((a.H + 15) / 16), 0, s>>>(a);
+        norm_backward_kernel<T, 8, 4, 0><<<blocks, round32((packs + 3) / 4), 0, s>>>(a);
     return true;
 }
 
@@ -835,10 +1017,10 @@ int moe_layer_norm(int T, int H, const void *x, int64_t ldx, int dtype, const vo
     OP_DEVICE(sms);
     const NormArgs a{T, H, x, ldx, weight, bias, w_dtype == MOE_F32 && dtype != MOE_F32, eps, y, mean, rstd, nullptr, nullptr, 0};
     const bool packed = packed_rows(H, dtype, x, ldx) && op_aligned(y, 16) && packed_affine(weight) && packed_affine(bias);
-    with_dtype(dtype, [&](auto *t) {
-        launch_norm<std::remove_pointer_t<decltype(t)>, false>(a, packed, sms, static_cast<cudaStream_t>(stream));
+    const bool ok = with_dtype(dtype, [&](auto *t) {
+        return launch_norm<std::remove_pointer_t<decltype(t)>, false>(a, packed, sms, static_cast<cudaStream_t>(stream));
     });
-    return launched();
+    return ok ? launched() : MOE_ERR_CUDA;
 }
 
 int moe_layer_norm_fp8(int T, int H, const void *x, int64_t ldx, int dtype, const void *weight, const void *bias,
@@ -854,10 +1036,10 @@ int moe_layer_norm_fp8(int T, int H, const void *x, int64_t ldx, int dtype, cons
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
     const NormArgs a{T, H, x, ldx, weight, bias, w_dtype == MOE_F32 && dtype != MOE_F32, eps, nullptr, nullptr, nullptr, q, sf, pow2_scales};
-    with_dtype(dtype, [&](auto *t) {
-        launch_norm<std::remove_pointer_t<decltype(t)>, true>(a, true, sms, static_cast<cudaStream_t>(stream));
+    const bool ok = with_dtype(dtype, [&](auto *t) {
+        return launch_norm<std::remove_pointer_t<decltype(t)>, true>(a, true, sms, static_cast<cudaStream_t>(stream));
     });
-    return launched();
+    return ok ? launched() : MOE_ERR_CUDA;
 }
 
 int moe_layer_norm_backward_workspace(int T, int H, uint64_t *bytes)

@@ -78,6 +78,18 @@ def test_strided_and_unaligned_rows(H, off, pitch):
     _check_backward(x, g[:H].clone(), big.flip(0)[:, off:off + H])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("T,H,off,pitch", [(1, 2049, 1, 2050), (3, 2049, 1, 2051), (700, 1500, 3, 1503), (5, 1025, 5, 1030), (2, 9001, 7, 9009),
+                                           (4, 1030, 0, 1030), (3, 3000, 2, 3003)])
+def test_long_unaligned_rows(T, H, off, pitch, dtype):
+    """Rows that start before, on and after 16-byte boundaries, at both ends of the allocation."""
+    flat = torch.randn(T * pitch + off, device="cuda").to(dtype)[off:].clone() if off == 0 else torch.randn(T * pitch + off, device="cuda").to(dtype)[off:]
+    x = flat.as_strided((T, H), (pitch, 1))
+    _, g, b, dy = _inputs(T, H, dtype, dtype)
+    _check_forward(x, g, b, ops.layer_norm(x, g, b))
+    _check_backward(x, g, dy)
+
+
 def test_large_mean_keeps_the_variance():
     x, g, b, _ = _inputs(16, 4096, torch.float32, torch.float32, mean=1000.0)
     y, _, _ = ops.layer_norm(x, g, b)
