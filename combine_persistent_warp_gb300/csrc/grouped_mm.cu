@@ -48,8 +48,9 @@ constexpr int THREADS = 256;
 constexpr int MAX_E = 1024;
 constexpr uint64_t WAIT_NS = 2000000000ull;    // limit of every wait
 constexpr int STAGE_OUT = 32 * 128;    // dW: an epilogue warp's 32 rows x 128 bytes on their way out
-constexpr int SMEM = RING * STAGE + 1024;
-constexpr int SMEM_WEIGHTS = SMEM + 4 * STAGE_OUT;
+constexpr int ROWS_OUT = 2 * 32 * (256 + 64);   // rows of the other products on their way out
+constexpr int SMEM = RING * STAGE + 1024 + ROWS_OUT;
+constexpr int SMEM_WEIGHTS = RING * STAGE + 1024 + 4 * STAGE_OUT;
 
 __device__ uint32_t g_op_error;        // sticky status of the grouped products (moe_ops_get_error)
 
@@ -290,23 +291,46 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, int f16)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// 32 accumulator columns (rows r .. r + 31 of the tile) of this lane's feature: neighbouring
-// lanes swap halves of a pair of rows, so that a lane stores two features of one row and a warp
-// 64 contiguous bytes of each of two rows.
-__device__ __forceinline__ void store_rows(const Args &a, const Tile &t, const uint32_t (&v)[32], int r, int f, int lane)
+// 32 accumulator columns (rows r .. r + 31 of the tile), 128 features f0 .. f0 + 127 of a CTA, one
+// feature a lane of the four epilogue warps, into rows of out.  Neighbouring lanes swap halves of
+// a pair of rows, so that a lane holds two features of one row; the warps put their 64 bytes of
+// every row into shared memory (rows ROW_PITCH apart: conflict-free) and, behind one barrier a
+// chunk (two buffers in turn), store whole 256-byte rows with 16-byte accesses.  (Each warp
+// storing its own 64 bytes took 13,600 cycles a tile of 256 rows: 29095 x 2336 x 64 107 us.)
+constexpr int ROW_PITCH = 256 + 64;
+constexpr int ROW_BUFFER = 32 * ROW_PITCH;
+__device__ __forceinline__ void store_rows(const Args &a, const Tile &t, const uint32_t (&v)[32], int r, int f0, int quarter, int lane,
+                                           uint8_t *buf)
 {
-    uint16_t *out = static_cast<uint16_t *>(a.out);
     const int odd = lane & 1;
-    const int fe = f & ~1;
 #pragma unroll
     for (int p = 0; p < 16; ++p) {
         const uint32_t own = pack2(__uint_as_float(v[2 * p]), __uint_as_float(v[2 * p + 1]), a.f16);
         const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
         const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
-        const int row = r + 2 * p + odd;
-        if (row < t.rows && fe < a.F)
-            *reinterpret_cast<uint32_t *>(out + static_cast<size_t>(t.r0 + row) * a.ldo + fe) = w;
+        *reinterpret_cast<uint32_t *>(buf + (2 * p + odd) * ROW_PITCH + quarter * 64 + (lane >> 1) * 4) = w;
     }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    uint16_t *out = static_cast<uint16_t *>(a.out);
+    const int part = lane & 15, f = f0 + 8 * part;   // 16 lanes a row
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int q = i * 8 + quarter * 2 + (lane >> 4);
+        if (r + q < t.rows && f < a.F)
+            *reinterpret_cast<uint4 *>(out + static_cast<size_t>(t.r0 + r + q) * a.ldo + f) =
+                *reinterpret_cast<const uint4 *>(buf + q * ROW_PITCH + part * 16);
+    }
+}
+
+// Whether all four epilogue warps have `ok`: they go on, or stop, together.
+__device__ __forceinline__ bool epilogue_all(bool ok)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(static_cast<uint32_t>(ok))
+                 : "memory");
+    return r != 0;
 }
 
 // 32 accumulator columns of this lane's feature as fp32 sums of a part.
@@ -638,6 +662,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         uint8_t *buf = ring + RING * STAGE + quarter * STAGE_OUT;   // WEIGHTS
+        int flip = 0;
         while (ok && list.next(t)) {
             const int f0 = t.f0 + static_cast<int>(rank) * 128 + quarter * 32;
             if (KIND == WEIGHTS && t.blocks == 0) {
@@ -650,6 +675,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 continue;
             }
             ok = __all_sync(0xFFFFFFFFu, wait_phase(&s.acc_full[acc], acc_phase));
+            if (KIND != WEIGHTS)
+                ok = epilogue_all(ok);   // store_rows' barriers need all four warps
             if (!ok)
                 break;
             ptx::tc_fence_after();
@@ -670,8 +697,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         add_weights16(a, t, v, c, f0 + lane);
                     else if (a.splits > 1)
                         store_part(a, t, v, c, f0 + lane);
-                    else
-                        store_rows(a, t, v, c, f0 + lane, lane);
+                    else {
+                        store_rows(a, t, v, c, f0 - quarter * 32, quarter, lane, ring + RING * STAGE + flip);
+                        flip ^= ROW_BUFFER;   // (goes on over the tiles: a warp may be one chunk ahead)
+                    }
                 }
             }
             ptx::tc_fence_before();
