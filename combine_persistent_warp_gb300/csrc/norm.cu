@@ -915,6 +915,8 @@ bool launch_norm(const NormArgs &a, bool packed, int num_sms, cudaStream_t s)
     } else if constexpr (!FP8) {
         if (a.H <= 256)
             launch_norm_warps<T, 1, 8, false>(a, num_sms, s);
+        else if (a.H <= 576)
+            launch_norm_warps<T, 1, 18, false>(a, num_sms, s);
         else if (a.H <= 1024)
             launch_norm_warps<T, 1, 32, false>(a, num_sms, s);
         else {
@@ -986,6 +988,8 @@ bool launch_backward(const NormBwdArgs &a, bool packed, Plan plan, int blocks, c
         norm_backward_warp_kernel<T, 1, 8><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
     else if (plan == WARPS_4 && packed)
         norm_backward_warp_kernel<T, 8, 4><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
+    else if (plan == WARPS_4 && a.H <= 576)
+        norm_backward_warp_kernel<T, 1, 18><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
     else if (plan == WARPS_4)
         norm_backward_warp_kernel<T, 1, 32><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
     else if (plan == BYTES) {

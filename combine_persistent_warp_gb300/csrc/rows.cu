@@ -19,6 +19,7 @@ namespace {
 constexpr int MAX_K = 32;
 constexpr int SLOTS = 8;   // slots of a token handled together
 constexpr int COMBINE_BLOCK = 128;
+constexpr int NARROW = 96;   // packs of a row up to which a block of 128 threads takes several tokens
 constexpr int BWD_BLOCK = 128;   // 8192 x 8 x 7168 bf16: 493 us for both passes (64: 497, 256: 507, 448: 550)
 
 struct RowArgs {
@@ -140,6 +141,146 @@ __global__ void __launch_bounds__(COMBINE_BLOCK) combine_rows_kernel(const RowAr
     }
 }
 
+// One pack of a token's gradient: its part of the slots' sums, and the rows' gradients.
+template <typename T, int V>
+__device__ __forceinline__ void backward_pack(const RowArgs &a, const T *d, const T *y, T *dy, int p, const int (&r)[SLOTS],
+                                              const float (&w)[SLOTS], float (&dot)[SLOTS])
+{
+                const Pack<T, V> q = load_pack<T, V>(d + static_cast<size_t>(p) * V);
+                Pack<T, V> v[SLOTS];
+#pragma unroll
+                for (int i = 0; i < SLOTS; ++i)
+                    if (r[i] >= 0)
+                        v[i] = load_pack<T, V>(y + static_cast<size_t>(r[i]) * a.H + static_cast<size_t>(p) * V);
+#pragma unroll
+                for (int i = 0; i < SLOTS; ++i)
+                    if (r[i] >= 0) {
+                        Pack<T, V> o;
+#pragma unroll
+                        for (int c = 0; c < V; ++c) {
+                            const float g = to_f<T>(q.v[c]);
+                            dot[i] = fmaf(g, to_f<T>(v[i].v[c]), dot[i]);
+                            o.v[c] = from_f<T>(w[i] * g);
+                        }
+                        store_pack<T, V>(dy + static_cast<size_t>(r[i]) * a.H + static_cast<size_t>(p) * V, o);
+                    }
+}
+
+// Short rows (at most NARROW packs): a thread a (token, pack), so that a warp is not left with
+// lanes past the row's end.
+__device__ __forceinline__ void slot_of(const RowArgs &a, int t, int j, int &r, float &w)
+{
+    r = -1;
+    w = 0.0f;
+    if (j < a.k) {
+        const size_t at = static_cast<size_t>(t) * a.k + j;
+        const int v = a.rows[at];
+        if (v >= 0 && v < a.M) {
+            r = v;
+            w = a.w ? a.w[at] : 1.0f;
+        }
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(COMBINE_BLOCK) gather_narrow_kernel(const RowArgs a, int blocks)
+{
+    if (static_cast<int>(blockIdx.x) >= blocks) {
+        zero_rest<T, V>(a, a.out, blockIdx.x - blocks, gridDim.x - blocks);
+        return;
+    }
+    const int packs = a.H / V;
+    const long long i = static_cast<long long>(blockIdx.x) * COMBINE_BLOCK + threadIdx.x;
+    const int t = static_cast<int>(i / packs), p = static_cast<int>(i - static_cast<long long>(t) * packs);
+    if (t >= a.T)
+        return;
+    const Pack<T, V> v = load_pack<T, V>(static_cast<const T *>(a.x) + static_cast<size_t>(t) * a.ldx + static_cast<size_t>(p) * V);
+    for (int j0 = 0; j0 < a.k; j0 += SLOTS) {
+        int r[SLOTS];
+        float w[SLOTS];
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+            slot_of(a, t, j0 + s, r[s], w[s]);
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+            if (r[s] >= 0)
+                store_pack<T, V>(static_cast<T *>(a.out) + static_cast<size_t>(r[s]) * a.H + static_cast<size_t>(p) * V, v);
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(COMBINE_BLOCK) combine_narrow_kernel(const RowArgs a)
+{
+    const int packs = a.H / V;
+    const long long i = static_cast<long long>(blockIdx.x) * COMBINE_BLOCK + threadIdx.x;
+    const int t = static_cast<int>(i / packs), p = static_cast<int>(i - static_cast<long long>(t) * packs);
+    if (t >= a.T)
+        return;
+    const T *y = static_cast<const T *>(a.y) + static_cast<size_t>(p) * V;
+    float acc[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c)
+        acc[c] = 0.0f;
+    for (int j0 = 0; j0 < a.k; j0 += SLOTS) {
+        int r[SLOTS];
+        float w[SLOTS];
+        Pack<T, V> v[SLOTS];
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+            slot_of(a, t, j0 + s, r[s], w[s]);
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+            if (r[s] >= 0)
+                v[s] = load_pack<T, V>(y + static_cast<size_t>(r[s]) * a.H);
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+            if (r[s] >= 0) {
+#pragma unroll
+                for (int c = 0; c < V; ++c)
+                    acc[c] = fmaf(w[s], to_f<T>(v[s].v[c]), acc[c]);
+            }
+    }
+    Pack<T, V> o;
+#pragma unroll
+    for (int c = 0; c < V; ++c)
+        o.v[c] = from_f<T>(acc[c]);
+    store_pack<T, V>(static_cast<T *>(a.out) + static_cast<size_t>(t) * a.H + static_cast<size_t>(p) * V, o);
+}
+
+// A warp a token: its sums over the columns need no other warp.
+template <typename T, int V>
+__global__ void __launch_bounds__(COMBINE_BLOCK) combine_narrow_backward_kernel(const RowArgs a, int blocks)
+{
+    if (static_cast<int>(blockIdx.x) >= blocks) {
+        zero_rest<T, V>(a, a.dy, blockIdx.x - blocks, gridDim.x - blocks);
+        return;
+    }
+    const int t = blockIdx.x * (COMBINE_BLOCK / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31, packs = a.H / V;
+    if (t >= a.T)
+        return;
+    const T *d = static_cast<const T *>(a.x) + static_cast<size_t>(t) * a.ldx;
+    const T *y = static_cast<const T *>(a.y);
+    T *dy = static_cast<T *>(a.dy);
+    for (int j0 = 0; j0 < a.k; j0 += SLOTS) {
+        int r[SLOTS];
+        float w[SLOTS], dot[SLOTS];
+        load_slots(a, t, j0, r, w);
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+            dot[s] = 0.0f;
+        for (int p = lane; p < packs; p += 32)
+            backward_pack<T, V>(a, d, y, dy, p, r, w, dot);
+        float mine = 0.0f;
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+            const float v = warp_sum(dot[s]);
+            mine = lane == s ? v : mine;
+        }
+        if (a.dw && lane < SLOTS && j0 + lane < a.k)
+            a.dw[static_cast<size_t>(t) * a.k + j0 + lane] = mine;
+    }
+}
+
 // A block takes a whole token, for the sums over its columns.
 template <typename T, int V>
 __global__ void __launch_bounds__(512) combine_rows_backward_kernel(const RowArgs a)
@@ -161,26 +302,8 @@ __global__ void __launch_bounds__(512) combine_rows_backward_kernel(const RowArg
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i)
             dot[i] = 0.0f;
-        for (int p = threadIdx.x; p < packs; p += blockDim.x) {
-            const Pack<T, V> q = load_pack<T, V>(d + static_cast<size_t>(p) * V);
-            Pack<T, V> v[SLOTS];
-#pragma unroll
-            for (int i = 0; i < SLOTS; ++i)
-                if (r[i] >= 0)
-                    v[i] = load_pack<T, V>(y + static_cast<size_t>(r[i]) * a.H + static_cast<size_t>(p) * V);
-#pragma unroll
-            for (int i = 0; i < SLOTS; ++i)
-                if (r[i] >= 0) {
-                    Pack<T, V> o;
-#pragma unroll
-                    for (int c = 0; c < V; ++c) {
-                        const float g = to_f<T>(q.v[c]);
-                        dot[i] = fmaf(g, to_f<T>(v[i].v[c]), dot[i]);
-                        o.v[c] = from_f<T>(w[i] * g);
-                    }
-                    store_pack<T, V>(dy + static_cast<size_t>(r[i]) * a.H + static_cast<size_t>(p) * V, o);
-                }
-        }
+        for (int p = threadIdx.x; p < packs; p += blockDim.x)
+            backward_pack<T, V>(a, d, y, dy, p, r, w, dot);
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i)
             dot[i] = warp_sum(dot[i]);
@@ -256,6 +379,11 @@ int moe_gather_rows(int T, int topk, int H, int E, int64_t M, const void *x, int
     return by_rows(dtype, H, ldx, x, out, nullptr, [&](auto *t, auto v) {
         using Ty = std::remove_pointer_t<decltype(t)>;
         constexpr int V = decltype(v)::value;
+        if (H / V <= NARROW) {
+            const int blocks = static_cast<int>((static_cast<long long>(T) * (H / V) + COMBINE_BLOCK - 1) / COMBINE_BLOCK);
+            gather_narrow_kernel<Ty, V><<<blocks + sms, COMBINE_BLOCK, 0, static_cast<cudaStream_t>(stream)>>>(a, blocks);
+            return;
+        }
         gather_kernel<Ty, V><<<T + sms, rows_threads(H / V), 0, static_cast<cudaStream_t>(stream)>>>(a);
     });
 }
@@ -275,6 +403,11 @@ int moe_combine_rows(int T, int topk, int H, int64_t M, const void *y, int dtype
     return by_rows(dtype, H, H, y, out, nullptr, [&](auto *t, auto v) {
         using Ty = std::remove_pointer_t<decltype(t)>;
         constexpr int V = decltype(v)::value;
+        if (H / V <= NARROW) {
+            const int blocks = static_cast<int>((static_cast<long long>(T) * (H / V) + COMBINE_BLOCK - 1) / COMBINE_BLOCK);
+            combine_narrow_kernel<Ty, V><<<blocks, COMBINE_BLOCK, 0, static_cast<cudaStream_t>(stream)>>>(a);
+            return;
+        }
         const int gy = T < 32768 ? T : 32768;
         combine_rows_kernel<Ty, V><<<dim3((H / V + COMBINE_BLOCK - 1) / COMBINE_BLOCK, gy, (T + gy - 1) / gy), COMBINE_BLOCK, 0,
                                      static_cast<cudaStream_t>(stream)>>>(a);
@@ -298,6 +431,11 @@ int moe_combine_rows_backward(int T, int topk, int H, int E, int64_t M, const vo
     return by_rows(dtype, H, lddout, dout, y, dy, [&](auto *t, auto v) {
         using Ty = std::remove_pointer_t<decltype(t)>;
         constexpr int V = decltype(v)::value;
+        if (H / V <= NARROW) {
+            const int blocks = (T + COMBINE_BLOCK / 32 - 1) / (COMBINE_BLOCK / 32);
+            combine_narrow_backward_kernel<Ty, V><<<blocks + sms, COMBINE_BLOCK, 0, static_cast<cudaStream_t>(stream)>>>(a, blocks);
+            return;
+        }
         combine_rows_backward_kernel<Ty, V><<<T + sms, backward_threads(H / V, T, sms), 0, static_cast<cudaStream_t>(stream)>>>(a);
     });
 }
