@@ -31,10 +31,10 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return
 template <>
 __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 
-// N consecutive elements moved by as few 16-byte accesses as they fill (an element each when
-// N == 1; the address of N > 1 elements is 16-byte aligned).
+// N consecutive elements moved by as few accesses of at most 16 bytes as they fill; the address
+// is aligned to the access.
 template <typename T, int N>
-struct alignas(N == 1 ? sizeof(T) : 16) Pack {
+struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
     T v[N];
 };
 
@@ -45,8 +45,11 @@ __device__ __forceinline__ Pack<T, N> load_pack(const T *p)
         Pack<T, 1> r;
         r.v[0] = __ldg(p);
         return r;
+    } else if constexpr (sizeof(T) * N == 4) {
+        const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(p));
+        return *reinterpret_cast<const Pack<T, N> *>(&u);
     } else {
-        static_assert(sizeof(T) * N % 16 == 0, "whole 16-byte accesses");
+        static_assert(sizeof(T) * N % 16 == 0, "whole accesses");
         union {
             Pack<T, N> pack;
             uint4 q[sizeof(T) * N / 16];
@@ -63,6 +66,8 @@ __device__ __forceinline__ void store_pack(T *p, const Pack<T, N> &v)
 {
     if constexpr (N == 1) {
         *p = v.v[0];
+    } else if constexpr (sizeof(T) * N == 4) {
+        *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<const uint32_t *>(&v);
     } else {
         union {
             Pack<T, N> pack;

@@ -37,26 +37,37 @@ struct RowArgs {
 };
 
 // Rows and weights of a token's slots j0 .. j0 + SLOTS - 1 (-1 and 0 where there is none): one
-// load a lane, then shuffles, so that a warp has all of them after one memory latency.
-__device__ __forceinline__ void load_slots(const RowArgs &a, int t, int j0, int (&r)[SLOTS], float (&w)[SLOTS])
+// load a lane (fetch_slot), then shuffles (spread_slots), so that a warp has all of them after
+// one memory latency, and can ask for the next token's ahead of time.
+struct Slot {
+    int row;
+    float w;
+};
+__device__ __forceinline__ Slot fetch_slot(const RowArgs &a, int t, int j0)
 {
     const int lane = threadIdx.x & 31, j = j0 + lane;
-    int mine = -1;
-    float weight = 0.0f;
-    if (lane < SLOTS && j < a.k) {
+    Slot s{-1, 0.0f};
+    if (lane < SLOTS && j < a.k && t < a.T) {
         const size_t at = static_cast<size_t>(t) * a.k + j;
-        const int v = a.rows[at];
-        const float g = a.w ? a.w[at] : 1.0f;
-        if (v >= 0 && v < a.M) {
-            mine = v;
-            weight = g;
-        }
+        s.row = a.rows[at];
+        s.w = a.w ? a.w[at] : 1.0f;
     }
+    return s;
+}
+__device__ __forceinline__ void spread_slots(const RowArgs &a, const Slot &s, int (&r)[SLOTS], float (&w)[SLOTS])
+{
+    const bool in = s.row >= 0 && s.row < a.M;
+    const int row = in ? s.row : -1;
+    const float weight = in ? s.w : 0.0f;
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
-        r[i] = __shfl_sync(0xFFFFFFFFu, mine, i);
+        r[i] = __shfl_sync(0xFFFFFFFFu, row, i);
         w[i] = __shfl_sync(0xFFFFFFFFu, weight, i);
     }
+}
+__device__ __forceinline__ void load_slots(const RowArgs &a, int t, int j0, int (&r)[SLOTS], float (&w)[SLOTS])
+{
+    spread_slots(a, fetch_slot(a, t, j0), r, w);
 }
 
 // Zeroes the rows that no slot names; block b of `blocks`.
@@ -75,6 +86,10 @@ __device__ __forceinline__ void zero_rest(const RowArgs &a, void *out, int b, in
             store_pack<T, V>(static_cast<T *>(out) + static_cast<size_t>(r) * a.H + static_cast<size_t>(p) * V, z);
 }
 
+// Packs of a thread: a block covers a like number of bytes of a row whatever its packs' size.
+template <typename T, int V>
+constexpr int PACKS = sizeof(T) * V >= 16 ? 1 : V == 2 ? 2 : 4;
+
 template <typename T, int V>
 __global__ void __launch_bounds__(1024) gather_kernel(const RowArgs a)
 {
@@ -89,55 +104,75 @@ __global__ void __launch_bounds__(1024) gather_kernel(const RowArgs a)
         int r[SLOTS];
         float w[SLOTS];
         load_slots(a, t, j0, r, w);
-        for (int p = threadIdx.x; p < packs; p += blockDim.x) {
-            const Pack<T, V> v = load_pack<T, V>(x + static_cast<size_t>(p) * V);
+        constexpr int N = PACKS<T, V>;
+        for (int p = threadIdx.x; p < packs; p += N * blockDim.x) {
+            Pack<T, V> v[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                if (p + n * static_cast<int>(blockDim.x) < packs)
+                    v[n] = load_pack<T, V>(x + static_cast<size_t>(p + n * blockDim.x) * V);
 #pragma unroll
             for (int i = 0; i < SLOTS; ++i)
-                if (r[i] >= 0)
-                    store_pack<T, V>(out + static_cast<size_t>(r[i]) * a.H + static_cast<size_t>(p) * V, v);
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+                    if (r[i] >= 0 && p + n * static_cast<int>(blockDim.x) < packs)
+                        store_pack<T, V>(out + static_cast<size_t>(r[i]) * a.H + static_cast<size_t>(p + n * blockDim.x) * V, v[n]);
         }
     }
 }
 
-// A block takes a run of a token's columns, one pack a thread: the loads of all its slots are in
-// flight together and many small blocks share an SM.
+// A block takes a run of columns of `tokens` tokens, one after the other: the loads of all slots
+// of a token are in flight together, those of the next token's slots beside them, and many
+// small blocks share an SM.
 template <typename T, int V>
-__global__ void __launch_bounds__(COMBINE_BLOCK) combine_rows_kernel(const RowArgs a)
+__global__ void __launch_bounds__(COMBINE_BLOCK) combine_rows_kernel(const RowArgs a, int tokens)
 {
-    const int t = blockIdx.y + blockIdx.z * gridDim.y, packs = a.H / V;
-    if (t >= a.T)
+    constexpr int N = PACKS<T, V>;
+    const int packs = a.H / V, p0 = blockIdx.x * (COMBINE_BLOCK * N) + threadIdx.x;
+    const T *y = static_cast<const T *>(a.y);
+    int t = (blockIdx.y + blockIdx.z * gridDim.y) * tokens;
+    const int end = min(a.T, t + tokens);
+    if (t >= end)
         return;
-    const int p = blockIdx.x * COMBINE_BLOCK + threadIdx.x;
-    const T *y = static_cast<const T *>(a.y) + static_cast<size_t>(p) * V;
-    float acc[V];
+    Slot ahead = fetch_slot(a, t, 0);
+    for (; t < end; ++t) {
+        float acc[N][V];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        acc[i] = 0.0f;
-    for (int j0 = 0; j0 < a.k; j0 += SLOTS) {
-        int r[SLOTS];
-        float w[SLOTS];
-        load_slots(a, t, j0, r, w);
-        if (p < packs) {
-            Pack<T, V> v[SLOTS];
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-            for (int i = 0; i < SLOTS; ++i)
-                if (r[i] >= 0)
-                    v[i] = load_pack<T, V>(y + static_cast<size_t>(r[i]) * a.H);
+            for (int i = 0; i < V; ++i)
+                acc[n][i] = 0.0f;
+        for (int j0 = 0; j0 < a.k; j0 += SLOTS) {
+            int r[SLOTS];
+            float w[SLOTS];
+            spread_slots(a, ahead, r, w);
+            Pack<T, V> v[N][SLOTS];
 #pragma unroll
-            for (int i = 0; i < SLOTS; ++i)
-                if (r[i] >= 0) {
+            for (int n = 0; n < N; ++n)
 #pragma unroll
-                    for (int c = 0; c < V; ++c)
-                        acc[c] = fmaf(w[i], to_f<T>(v[i].v[c]), acc[c]);
-                }
+                for (int i = 0; i < SLOTS; ++i)
+                    if (r[i] >= 0 && p0 + n * COMBINE_BLOCK < packs)
+                        v[n][i] = load_pack<T, V>(y + static_cast<size_t>(r[i]) * a.H + static_cast<size_t>(p0 + n * COMBINE_BLOCK) * V);
+            ahead = j0 + SLOTS < a.k ? fetch_slot(a, t, j0 + SLOTS) : fetch_slot(a, t + 1, 0);
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int i = 0; i < SLOTS; ++i)
+                    if (r[i] >= 0 && p0 + n * COMBINE_BLOCK < packs) {
+#pragma unroll
+                        for (int c = 0; c < V; ++c)
+                            acc[n][c] = fmaf(w[i], to_f<T>(v[n][i].v[c]), acc[n][c]);
+                    }
         }
-    }
-    if (p < packs) {
-        Pack<T, V> o;
 #pragma unroll
-        for (int c = 0; c < V; ++c)
-            o.v[c] = from_f<T>(acc[c]);
-        store_pack<T, V>(static_cast<T *>(a.out) + static_cast<size_t>(t) * a.H + static_cast<size_t>(p) * V, o);
+        for (int n = 0; n < N; ++n)
+            if (p0 + n * COMBINE_BLOCK < packs) {
+                Pack<T, V> o;
+#pragma unroll
+                for (int c = 0; c < V; ++c)
+                    o.v[c] = from_f<T>(acc[n][c]);
+                store_pack<T, V>(static_cast<T *>(a.out) + static_cast<size_t>(t) * a.H + static_cast<size_t>(p0 + n * COMBINE_BLOCK) * V, o);
+            }
     }
 }
 
@@ -342,19 +377,27 @@ bool rows_sizes_ok(int T, int k, int H, long long M, int dtype)
     return T >= 0 && k >= 1 && k <= MAX_K && H >= 1 && M >= 0 && M <= 0x7FFFFFFFll && dtype_ok(dtype);
 }
 
-// 16-byte packs where every row starts on a 16-byte boundary, single elements otherwise.
+// 16-byte packs where every row starts on a 16-byte boundary, pairs of 16-bit elements where it
+// does on a 4-byte one, single elements otherwise.
 template <typename F>
 int by_rows(int dtype, int H, long long ldx, const void *p0, const void *p1, const void *p2, F f)
 {
     const size_t b = dtype_bytes(dtype);
-    const bool packed = H * b % 16 == 0 && static_cast<size_t>(ldx) * b % 16 == 0 && op_aligned(p0, 16) &&
-                        op_aligned(p1, 16) && op_aligned(p2, 16);
+    const auto all = [&](size_t n) {
+        return H * b % n == 0 && static_cast<size_t>(ldx) * b % n == 0 && op_aligned(p0, n) && op_aligned(p1, n) && op_aligned(p2, n);
+    };
     with_dtype(dtype, [&](auto *t) {
         using E = std::remove_pointer_t<decltype(t)>;
-        if (packed)
+        if (all(16)) {
             f(t, std::integral_constant<int, 16 / static_cast<int>(sizeof(E))>{});
-        else
-            f(t, std::integral_constant<int, 1>{});
+            return;
+        }
+        if constexpr (sizeof(E) == 2)
+            if (all(4)) {
+                f(t, std::integral_constant<int, 2>{});
+                return;
+            }
+        f(t, std::integral_constant<int, 1>{});
     });
     return launched();
 }
@@ -408,9 +451,13 @@ int moe_combine_rows(int T, int topk, int H, int64_t M, const void *y, int dtype
             combine_narrow_kernel<Ty, V><<<blocks, COMBINE_BLOCK, 0, static_cast<cudaStream_t>(stream)>>>(a);
             return;
         }
-        const int gy = T < 32768 ? T : 32768;
-        combine_rows_kernel<Ty, V><<<dim3((H / V + COMBINE_BLOCK - 1) / COMBINE_BLOCK, gy, (T + gy - 1) / gy), COMBINE_BLOCK, 0,
-                                     static_cast<cudaStream_t>(stream)>>>(a);
+        constexpr int RUN = COMBINE_BLOCK * PACKS<Ty, V>;
+        const int runs = (H / V + RUN - 1) / RUN;
+        // tokens a block: as many as leave about eight blocks an SM, up to eight
+        const long long each = static_cast<long long>(T) * runs / (8 * sms);
+        const int tokens = each < 1 ? 1 : each > 8 ? 8 : static_cast<int>(each);
+        const int groups = (T + tokens - 1) / tokens, gy = groups < 32768 ? groups : 32768;
+        combine_rows_kernel<Ty, V><<<dim3(runs, gy, (groups + gy - 1) / gy), COMBINE_BLOCK, 0, static_cast<cudaStream_t>(stream)>>>(a, tokens);
     });
 }
 
