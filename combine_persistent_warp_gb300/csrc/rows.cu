@@ -5,6 +5,10 @@
 //   combine   out[t] = sum_j w[t][j] * y[rows[t][j]]      (fp32, j ascending, rounded once)
 //   its gradients   dy[rows[t][j]] = w[t][j] * dout[t],   dw[t][j] = sum_h dout[t][h] * y[rows[t][j]][h]
 //
+// Measured on a GB300, bf16: gather of 16384 x 8 x 4096 189 us (floor 181), combine of 8192 x 8 x
+// 7168 180 us and its gradients 282 us with 5% of the slots skipped (both 462 us, floor 444), combine
+// of 128 x 8 x 7168 4.4 us.
+//
 // The gradient of gather is combine with w = 1.  All three are bound by HBM: a thread handles a
 // piece of a token for all of its slots, so the token's row is read (or written) once however
 // many slots it has, and every row in expert order once.
