@@ -874,7 +874,7 @@ int launch_grouped(const CUtensorMap &ma, const MapsB &mb, const CUtensorMap &mo
 
 bool grouped_sizes_ok(int64_t M, int E, int N, int K, int dtype)
 {
-    return M >= 0 && M <= 0x7FFFFFFFll - 1024 && E >= 1 && E <= MAX_E && N >= 8 && N % 8 == 0 && K >= 8 && K % 8 == 0 &&
+    return M >= 0 && M <= MAX_ROWS && E >= 1 && E <= MAX_E && N >= 8 && N % 8 == 0 && K >= 8 && K % 8 == 0 &&
            N <= (1 << 20) && K <= (1 << 20) && (dtype == MOE_BF16 || dtype == MOE_F16);
 }
 

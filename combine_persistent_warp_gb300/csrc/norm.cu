@@ -808,7 +808,7 @@ bool packed_affine(const void *p) { return p == nullptr || op_aligned(p, 16); }
 
 bool norm_args_ok(int T, int H, int dtype, int w_dtype, const void *weight, const void *bias)
 {
-    if (T < 0 || H < 1 || H > MAX_H || !dtype_ok(dtype))
+    if (T < 0 || T > MAX_ROWS || H < 1 || H > MAX_H || !dtype_ok(dtype))
         return false;
     if ((weight || bias) && w_dtype != dtype && w_dtype != MOE_F32)
         return false;
@@ -1052,7 +1052,7 @@ int moe_layer_norm_fp8(int T, int H, const void *x, int64_t ldx, int dtype, cons
 
 int moe_layer_norm_backward_workspace(int T, int H, uint64_t *bytes)
 {
-    if (T < 0 || H < 1 || H > MAX_H || !bytes)
+    if (T < 0 || T > MAX_ROWS || H < 1 || H > MAX_H || !bytes)
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
     // enough for every element type

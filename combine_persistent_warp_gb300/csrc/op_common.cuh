@@ -92,6 +92,8 @@ __device__ __forceinline__ float warp_sum(float v)
 inline bool op_aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 inline size_t dtype_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
+// Most tokens, slots or rows of a call: row indices plus a grid's strides stay in 31 bits.
+constexpr long long MAX_ROWS = 1ll << 30;
 inline bool dtype_ok(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16; }
 
 // Number of SMs of the current device; 0 if a CUDA call failed, -1 if it is not an sm_103 GPU.

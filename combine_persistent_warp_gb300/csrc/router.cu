@@ -489,7 +489,7 @@ struct RouteBwdLaunch {
 
 bool route_sizes_ok(int T, int E, int topk, int dtype)
 {
-    return T >= 0 && E >= 1 && E <= 1024 && topk >= 1 && topk <= 32 && topk <= E && dtype_ok(dtype);
+    return T >= 0 && T <= MAX_ROWS && E >= 1 && E <= 1024 && topk >= 1 && topk <= 32 && topk <= E && dtype_ok(dtype);
 }
 
 }  // namespace
@@ -532,7 +532,7 @@ int moe_route_topk_backward(int T, int E, int topk, const float *dw, const int64
 int moe_expert_order_workspace(int T, int topk, int E, uint64_t *bytes)
 {
     const long long n = static_cast<long long>(T) * topk;
-    if (T < 0 || topk < 1 || topk > 32 || E < 1 || E > 1024 || n > INT_MAX || !bytes)
+    if (T < 0 || topk < 1 || topk > 32 || E < 1 || E > 1024 || n > MAX_ROWS || !bytes)
         return MOE_ERR_INVALID_ARG;
     int blocks, chunk;
     order_shape(n, E, blocks, chunk);

@@ -378,7 +378,7 @@ int backward_threads(int packs, int T, int sms)
 
 bool rows_sizes_ok(int T, int k, int H, long long M, int dtype)
 {
-    return T >= 0 && k >= 1 && k <= MAX_K && H >= 1 && M >= 0 && M <= 0x7FFFFFFFll && dtype_ok(dtype);
+    return T >= 0 && T <= MAX_ROWS && k >= 1 && k <= MAX_K && H >= 1 && M >= 0 && M <= MAX_ROWS && dtype_ok(dtype);
 }
 
 // 16-byte packs where every row starts on a 16-byte boundary, pairs of 16-bit elements where it

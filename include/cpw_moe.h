@@ -294,6 +294,7 @@ int moe_route_noalloc(int T, int E, int topk, int R, const int64_t *topk_idx, ui
  *
  * Pointers are device pointers aligned to their element type unless a call asks for more; a row
  * stride (ld...) counts elements and is at least the row's length; other tensors are contiguous.
+ * T, M and T*topk are at most 2^30.
  * Calls with T == 0 (or M == 0) do nothing but write the results that an empty batch has (zero
  * gradients of weights, zero offsets). */
 
@@ -342,7 +343,7 @@ int moe_route_topk_backward(int T, int E, int topk, const float *dw, const int64
 /* Expert-major order of the T*topk slots: by expert, then token, then slot.  offsets [E+1] (expert
  * e has rows offsets[e] .. offsets[e+1]) and rows [T][topk], the row of each slot or -1 for a
  * skipped one.  *status (device int32) is MOE_OK, or MOE_ERR_BAD_INDEX if an id is neither -1
- * nor in [0, E); such a slot is skipped.  T*topk < 2^31, E <= 1024, topk <= 32. */
+ * nor in [0, E); such a slot is skipped.  E <= 1024, topk <= 32. */
 int moe_expert_order_workspace(int T, int topk, int E, uint64_t *bytes);
 int moe_expert_order(int T, int topk, int E, const int64_t *topk_idx, int32_t *offsets, int32_t *rows,
                      int32_t *status, void *workspace, uint64_t workspace_bytes, void *stream);

@@ -123,6 +123,17 @@ def test_grouped_dw_refuses_types(lib):
         assert call(16, 8, 64, 64, None) == INVALID
 
 
+def test_more_rows_than_31_bits_hold_are_refused(lib):
+    n, big = ctypes.c_uint64(), (1 << 30) + 1
+    assert _layer_norm(lib, T=big) == INVALID
+    assert lib.moe_layer_norm_backward_workspace(big, 256, ctypes.byref(n)) == INVALID
+    assert lib.moe_route_topk(big, 8, 2, P, 8, F32, None, 1, P, P, None) == INVALID
+    assert lib.moe_expert_order_workspace(1 << 28, 5, 8, ctypes.byref(n)) == INVALID
+    assert lib.moe_gather_rows(4, 2, 64, 3, big, P, 64, BF16, P, P, P, None) == INVALID
+    assert lib.moe_combine_rows(big, 2, 64, 8, P, BF16, P, P, P, None) == INVALID
+    assert lib.moe_grouped_mm_workspace(big, 4, 64, 64, ctypes.byref(n)) == INVALID
+
+
 def test_python_entry_points_check_shapes_and_types():
     x = torch.zeros(4, 256, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
