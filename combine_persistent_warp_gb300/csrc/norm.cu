@@ -819,7 +819,8 @@ bool norm_args_ok(int T, int H, int dtype, int w_dtype, const void *weight, cons
 template <typename K>
 bool allow_smem(K kern, size_t bytes)
 {
-    return bytes <= 48 * 1024 ||
+    // (without the attribute a block's static and dynamic shared memory together stay within 48 KB)
+    return bytes <= 40 * 1024 ||
            ensure_max_dynamic_smem(reinterpret_cast<const void *>(kern), static_cast<int>(bytes)) == cudaSuccess;
 }
 

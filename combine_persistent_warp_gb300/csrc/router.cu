@@ -562,7 +562,7 @@ int moe_expert_order(int T, int topk, int E, const int64_t *topk_idx, int32_t *o
             return MOE_ERR_CUDA;
     }
     const int smem = (ORDER_WARPS + 2) * E * static_cast<int>(sizeof(int32_t));
-    if (smem > 48 * 1024 &&
+    if (smem > 40 * 1024 &&   // (static shared memory counts towards the 48 KB that need no attribute)
         ensure_max_dynamic_smem(reinterpret_cast<const void *>(&order_place_kernel), smem) != cudaSuccess)
         return MOE_ERR_CUDA;
     if (blocks > 1)

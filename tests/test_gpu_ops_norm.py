@@ -90,6 +90,17 @@ def test_long_unaligned_rows(T, H, off, pitch, dtype):
     _check_backward(x, g, dy)
 
 
+@pytest.mark.parametrize("T,H", [(3042, 5888), (1300, 6016), (2500, 2952), (2500, 3064), (1300, 12288), (700, 4104)])
+def test_every_block_size_of_the_persistent_kernels_launches(T, H):
+    """Hidden sizes whose rings of rows take 48 KB of shared memory, a little less and more."""
+    x, g, b, dy = _inputs(T, H, torch.bfloat16, torch.bfloat16)
+    _check_forward(x, g, b, ops.layer_norm(x, g, b))
+    _check_backward(x, g, dy)
+    if H % 128 == 0:
+        q, sf = ops.layer_norm_fp8(x, g, b)
+        assert sf.isfinite().all() and (q.view(torch.float8_e4m3fn).float().abs().amax(1) <= 448).all()
+
+
 def test_large_mean_keeps_the_variance():
     x, g, b, _ = _inputs(16, 4096, torch.float32, torch.float32, mean=1000.0)
     y, _, _ = ops.layer_norm(x, g, b)

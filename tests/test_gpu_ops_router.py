@@ -175,7 +175,8 @@ def _plain_order(idx, E):
 
 
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 32), (3, 2, 1000), (128, 8, 32), (512, 8, 128), (513, 8, 128), (4096, 8, 32),
-                                   (4097, 7, 1024), (16384, 8, 128), (20001, 5, 257), (150000, 8, 64), (300000, 4, 1024)])
+                                   (4097, 7, 1024), (16384, 8, 128), (20001, 5, 257), (150000, 8, 64), (300000, 4, 1024),
+                                   (700, 8, 680), (5000, 8, 681), (5000, 8, 682), (5000, 8, 683), (700, 8, 682)])
 @pytest.mark.parametrize("kind", ["uniform", "skewed", "one"])
 def test_order(T, k, E, kind):
     g = torch.Generator(device="cuda").manual_seed(T + k)
