@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(512) norm_ring_kernel(const NormArgs a)
 
 // Persistent blocks over rows of any alignment (more than 1024 elements).
 template <typename T, int VPT, int AHEAD>
-__global__ void __launch_bounds__(1024) norm_bytes_kernel(const NormArgs a, const ByteRows m)
+__global__ void __launch_bounds__(512) norm_bytes_kernel(const NormArgs a, const ByteRows m)
 {
     constexpr int P = PAIRS<1, VPT>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(V * VPT <= 16 && V == 1 ? 1024 : 512) norm_bac
 
 // Rows of any alignment (more than 1024 elements).
 template <typename T, int VPT, int AHEAD>
-__global__ void __launch_bounds__(1024) norm_backward_bytes_kernel(const NormBwdArgs a, const ByteRows mx, const ByteRows md)
+__global__ void __launch_bounds__(512) norm_backward_bytes_kernel(const NormBwdArgs a, const ByteRows mx, const ByteRows md)
 {
     constexpr int P = PAIRS<1, VPT>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -858,7 +858,7 @@ int warp_blocks(int T, int per_sm, int num_sms)
     return need < most ? need : most;
 }
 
-// Blocks an SM (about 1024 threads), stages and shared memory of the kernels for rows of any
+// Blocks an SM (about 512 threads), stages and shared memory of the kernels for rows of any
 // alignment, `tensors` rows a stage.
 struct BytesPlan {
     int threads, per_sm, ahead;
@@ -867,11 +867,11 @@ struct BytesPlan {
 BytesPlan bytes_plan(int H, size_t elem, int tensors)
 {
     BytesPlan p{};
-    p.threads = H <= 8192 ? round32((H + 7) / 8) : 1024;
+    p.threads = round32(H <= 8192 ? (H + 15) / 16 : (H + 31) / 32);
     const size_t stage = static_cast<size_t>(stage_bytes(static_cast<int>(H * elem))) * tensors;
     p.ahead = 3 * stage <= 200 * 1024 ? 3 : 1;
     p.smem = p.ahead * stage;
-    const size_t fit = 200 * 1024 / p.smem, want = 1024 / p.threads;
+    const size_t fit = 200 * 1024 / p.smem, want = 512 / p.threads;
     p.per_sm = static_cast<int>(fit < want ? fit : want);
     return p;
 }
@@ -926,9 +926,9 @@ bool launch_norm(const NormArgs &a, bool packed, int num_sms, cudaStream_t s)
             launch_norm_warps<T, 1, 32, false>(a, num_sms, s);
         else {
             const BytesPlan p = bytes_plan(a.H, sizeof(T), 1);
-            return a.H > 8192    ? (p.ahead == 3 ? launch_norm_bytes<T, 16, 3>(a, p, num_sms, s) : launch_norm_bytes<T, 16, 1>(a, p, num_sms, s))
-                   : p.ahead == 3 ? launch_norm_bytes<T, 8, 3>(a, p, num_sms, s)
-                                  : launch_norm_bytes<T, 8, 1>(a, p, num_sms, s);
+            return a.H > 8192    ? (p.ahead == 3 ? launch_norm_bytes<T, 32, 3>(a, p, num_sms, s) : launch_norm_bytes<T, 32, 1>(a, p, num_sms, s))
+                   : p.ahead == 3 ? launch_norm_bytes<T, 16, 3>(a, p, num_sms, s)
+                                  : launch_norm_bytes<T, 16, 1>(a, p, num_sms, s);
         }
     }
     return true;
@@ -999,9 +999,9 @@ bool launch_backward(const NormBwdArgs &a, bool packed, Plan plan, int blocks, c
         norm_backward_warp_kernel<T, 1, 32><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
     else if (plan == BYTES) {
         const BytesPlan p = bytes_plan(a.H, sizeof(T), 2);
-        return a.H > 8192     ? (p.ahead == 3 ? launch_backward_bytes<T, 16, 3>(a, p, blocks, s) : launch_backward_bytes<T, 16, 1>(a, p, blocks, s))
-               : p.ahead == 3 ? launch_backward_bytes<T, 8, 3>(a, p, blocks, s)
-                              : launch_backward_bytes<T, 8, 1>(a, p, blocks, s);
+        return a.H > 8192     ? (p.ahead == 3 ? launch_backward_bytes<T, 32, 3>(a, p, blocks, s) : launch_backward_bytes<T, 32, 1>(a, p, blocks, s))
+               : p.ahead == 3 ? launch_backward_bytes<T, 16, 3>(a, p, blocks, s)
+                              : launch_backward_bytes<T, 16, 1>(a, p, blocks, s);
     } else if (a.H <= 8192)
         norm_backward_kernel<T, 8, 2, 0><<<blocks, round32((packs + 1) / 2), 0, s>>>(a);
     else
