@@ -64,7 +64,7 @@ def _link_binding(obj: str) -> None:
 
     tmp = OPS + f".tmp{os.getpid()}"
     libs = [f"-L{p}" for p in cpp_extension.library_paths()]
-    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libcpw_moe.so", *libs, "-ltorch_python", "-ltorch_cpu",
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libcpw_moe.so", *libs, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda",
            "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

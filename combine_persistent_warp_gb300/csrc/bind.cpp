@@ -7,6 +7,8 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -144,8 +146,21 @@ void *flat_or_null(PyObject *o, const char *name, at::IntArrayRef shape, at::Sca
 
 at::Tensor make(at::IntArrayRef shape, at::ScalarType dtype, int dev)
 {
-    return at::empty(shape, at::TensorOptions().dtype(dtype).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
+    // (at::empty without the dispatcher's 0.3 us)
+    return at::detail::empty_cuda(shape, at::TensorOptions().dtype(dtype).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
 }
+
+// A workspace for a call: memory of the current stream, back in the allocator's hands (and so in
+// that stream's order) when the call has been enqueued.
+struct Workspace {
+    c10::DataPtr p;
+    explicit Workspace(uint64_t bytes)
+    {
+        if (bytes)
+            p = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
+    }
+    void *get() const { return p.get(); }
+};
 
 void *current_stream(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
 
@@ -283,11 +298,12 @@ PyObject *layer_norm_backward(Args a)
     const int T = count(m.rows, "x"), H = count(m.width, "x");
     uint64_t need = 0;
     check(moe_layer_norm_backward_workspace(T, H, &need), "moe_layer_norm_backward_workspace");
-    at::Tensor ws = make({static_cast<int64_t>(need)}, at::kByte, f.dev), dx = make({m.rows, m.width}, f.type, f.dev);
+    const Workspace ws(need);
+    at::Tensor dx = make({m.rows, m.width}, f.type, f.dev);
     at::Tensor dweight = make({m.width}, w.type, f.dev), dbias = make({m.width}, w.type, f.dev);
     check(moe_layer_norm_backward(T, H, d.p, d.ld, m.p, m.ld, f.dtype, w.weight, w.dtype, static_cast<const float *>(mean),
                                   static_cast<const float *>(rstd), dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(),
-                                  ws.data_ptr(), need, current_stream(f.dev)),
+                                  ws.get(), need, current_stream(f.dev)),
           "moe_layer_norm_backward");
     return tuple_of({dx, dweight, dbias});
 }
@@ -348,12 +364,10 @@ PyObject *expert_order(Args a)
     const int E = small(a[1], "E");
     uint64_t need = 0;
     check(moe_expert_order_workspace(count(T, "idx"), count(k, "idx"), E, &need), "moe_expert_order_workspace");
-    at::Tensor ws;
-    if (need)
-        ws = make({static_cast<int64_t>(need)}, at::kByte, dev);
+    const Workspace ws(need);
     at::Tensor offsets = make({E + 1}, at::kInt, dev), rows = make({T, k}, at::kInt, dev), status = make({1}, at::kInt, dev);
     check(moe_expert_order(count(T, "idx"), count(k, "idx"), E, static_cast<const int64_t *>(pi), offsets.data_ptr<int32_t>(),
-                           rows.data_ptr<int32_t>(), status.data_ptr<int32_t>(), need ? ws.data_ptr() : nullptr, need,
+                           rows.data_ptr<int32_t>(), status.data_ptr<int32_t>(), ws.get(), need,
                            current_stream(dev)),
           "moe_expert_order");
     return tuple_of({offsets, rows, status});
@@ -467,11 +481,9 @@ PyObject *grouped(Args a)
     const auto call = TO_N ? moe_grouped_mm : moe_grouped_mm_dx;
     uint64_t need = 0;
     check(moe_grouped_mm_workspace(m.rows, count(w.E, "w"), count(w.N, "w"), count(w.K, "w"), &need), "moe_grouped_mm_workspace");
-    at::Tensor ws;
-    if (need)
-        ws = make({static_cast<int64_t>(need)}, at::kByte, f.dev);
+    const Workspace ws(need);
     check(call(m.rows, g.E, static_cast<int>(w.N), static_cast<int>(w.K), m.p, m.ld, w.p, g.p, o.p, o.ld, f.dtype,
-               need ? ws.data_ptr() : nullptr, need, current_stream(f.dev)),
+               ws.get(), need, current_stream(f.dev)),
           TO_N ? "moe_grouped_mm" : "moe_grouped_mm_dx");
     if (none(a[3]))
         return THPVariable_Wrap(fresh);
@@ -505,9 +517,9 @@ PyObject *grouped_dw(Args a)
     }
     uint64_t need = 0;
     check(moe_grouped_mm_dw_workspace(m.rows, g.E, count(N, "dy"), count(K, "x"), &need), "moe_grouped_mm_dw_workspace");
-    at::Tensor ws = make({static_cast<int64_t>(need)}, at::kByte, f.dev);
+    const Workspace ws(need);
     check(moe_grouped_mm_dw(m.rows, g.E, count(N, "dy"), count(K, "x"), d.p, d.ld, m.p, m.ld, g.p, po, f.dtype, code_of(type), accumulate,
-                            ws.data_ptr(), need, current_stream(f.dev)),
+                            ws.get(), need, current_stream(f.dev)),
           "moe_grouped_mm_dw");
     if (none(a[3]))
         return THPVariable_Wrap(fresh);

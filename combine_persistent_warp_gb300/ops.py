@@ -37,8 +37,7 @@ class ExpertOrder(NamedTuple):
 
 
 def _call(stream, fn, *args):
-    if stream is None:
-        return fn(*args)
+    """fn on another stream than the current one."""
     for t in args:
         if isinstance(t, torch.Tensor) and t.is_cuda:
             t.record_stream(stream)
@@ -50,11 +49,15 @@ def _call(stream, fn, *args):
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, *, stream=None):
     """y = (x - mean) * rstd * weight + bias over the last dimension of x [T, H] (rows may be
     strided).  Returns (y, mean, rstd): y of x's type, mean and rstd fp32 [T]."""
+    if stream is None:
+        return _ops.layer_norm(x, weight, bias, eps)
     return _call(stream, _ops.layer_norm, x, weight, bias, eps)
 
 
 def layer_norm_fp8(x, weight=None, bias=None, eps: float = 1e-5, *, pow2_scales: bool = False, stream=None):
     """Layer norm as FusedMoE.forward's activations: (e4m3 bytes uint8 [T, H], fp32 scales [T, H/128])."""
+    if stream is None:
+        return _ops.layer_norm_fp8(x, weight, bias, eps, pow2_scales)
     return _call(stream, _ops.layer_norm_fp8, x, weight, bias, eps, pow2_scales)
 
 
@@ -63,6 +66,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, param_dtype=None, stream=N
     (without a weight: ``param_dtype``, float32 or by default x's type)."""
     if param_dtype is not None and param_dtype != torch.float32 and param_dtype != x.dtype:
         raise TypeError(f"param_dtype: {param_dtype} is neither {x.dtype} nor float32")
+    if stream is None:
+        return _ops.layer_norm_backward(dy, x, weight, mean, rstd, param_dtype == torch.float32)
     return _call(stream, _ops.layer_norm_backward, dy, x, weight, mean, rstd, param_dtype == torch.float32)
 
 
@@ -71,33 +76,43 @@ def route_topk(logits, topk: int, *, token_mask=None, renormalize: bool = True, 
     """Top-k experts of each token and their gate weights, FusedMoE.forward's (topk_idx int64, topk_w
     fp32) [T, topk].  Ties go to the lowest expert; -inf logits and tokens whose ``token_mask`` (bool [T])
     is False choose nothing: idx -1, weight 0."""
+    if stream is None:
+        return _ops.route_topk(logits, topk, token_mask, renormalize)
     return _call(stream, _ops.route_topk, logits, topk, token_mask, renormalize)
 
 
 def route_topk_backward(dw, idx, w, logits, *, renormalize: bool = True, stream=None):
     """Gradient of the logits (their type) from dw, that of the gate weights (fp32 [T, topk])."""
+    if stream is None:
+        return _ops.route_topk_backward(dw, idx, w, logits, renormalize)
     return _call(stream, _ops.route_topk_backward, dw, idx, w, logits, renormalize)
 
 
 def expert_order(idx, E: int, *, stream=None) -> ExpertOrder:
     """Expert-major order of the slots idx [T, topk] names (-1: skipped): by expert, token, slot."""
-    return ExpertOrder(*_call(stream, _ops.expert_order, idx, E))
+    return ExpertOrder(*(_ops.expert_order(idx, E) if stream is None else _call(stream, _ops.expert_order, idx, E)))
 
 
 # -------------------------------------------------------------------------------- rows ----
 def gather_rows(x, rows, offsets, *, stream=None):
     """Rows of x [T, H] in expert order: out [T*topk, H] with out[rows[t, j]] = x[t], and zeros in the
     rows that no slot has.  Its gradient is ``combine_rows(dout, rows)``."""
+    if stream is None:
+        return _ops.gather_rows(x, rows, offsets)
     return _call(stream, _ops.gather_rows, x, rows, offsets)
 
 
 def combine_rows(y, rows, w=None, *, stream=None):
     """out[t] = sum_j w[t, j] * y[rows[t, j]] (w fp32 [T, topk], None: ones) in fp32, rounded once."""
+    if stream is None:
+        return _ops.combine_rows(y, rows, w)
     return _call(stream, _ops.combine_rows, y, rows, w)
 
 
 def combine_rows_backward(dout, y, rows, w, offsets, *, stream=None):
     """Gradients (dy, dw) of combine_rows: dy like y, dw fp32 [T, topk]."""
+    if stream is None:
+        return _ops.combine_rows_backward(dout, y, rows, w, offsets)
     return _call(stream, _ops.combine_rows_backward, dout, y, rows, w, offsets)
 
 
@@ -105,11 +120,15 @@ def combine_rows_backward(dout, y, rows, w, offsets, *, stream=None):
 def grouped_mm(x, w, offsets, *, out=None, stream=None):
     """out[r] = w[e] @ x[r] for the rows r of each expert e: x [M, K], w [E, N, K], out [M, N]
     (bfloat16 or float16; rows of x and out may be strided).  Rows past offsets[E] give zeros."""
+    if stream is None:
+        return _ops.grouped_mm(x, w, offsets, out)
     return _call(stream, _ops.grouped_mm, x, w, offsets, out)
 
 
 def grouped_mm_dx(dy, w, offsets, *, out=None, stream=None):
     """Gradient of grouped_mm's x: out[r] = dy[r] @ w[e], dy [M, N], w [E, N, K], out [M, K]."""
+    if stream is None:
+        return _ops.grouped_mm_dx(dy, w, offsets, out)
     return _call(stream, _ops.grouped_mm_dx, dy, w, offsets, out)
 
 
@@ -121,10 +140,14 @@ def grouped_mm_dw(dy, x, offsets, *, out=None, accumulate: bool = False, dtype=N
         raise TypeError(f"out: dtype {want} is neither {x.dtype} nor float32")
     if out is not None and out.dtype != want:
         raise TypeError(f"out: dtype {out.dtype} != {want}")
+    if stream is None:
+        return _ops.grouped_mm_dw(dy, x, offsets, out, accumulate, want == torch.float32)
     return _call(stream, _ops.grouped_mm_dw, dy, x, offsets, out, accumulate, want == torch.float32)
 
 
 def get_error(stream=None) -> int:
     """Waits for ``stream`` (default: the current stream), then returns (and clears) the sticky status
     of the grouped products' bounded waits: 0 or MOE_ERR_TIMEOUT."""
+    if stream is None:
+        return _ops.get_error()
     return _call(stream, _ops.get_error)
