@@ -7,7 +7,7 @@ sum of magnitudes (a thread's run, then a tree); a row's gradient is one product
 import pytest
 import torch
 
-from combine_persistent_warp_gb300 import ops
+from combine_persistent_warp_gb300 import native, ops
 
 pytestmark = pytest.mark.gpu
 E24 = 2.0 ** -24
@@ -123,6 +123,56 @@ def test_strided_inputs_and_another_stream():
     got = ops.combine_rows(y, o.rows, w, stream=s)
     s.synchronize()
     assert torch.equal(got, ops.combine_rows(y, o.rows, w))
+
+
+CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _inside(t, at, fill):
+    """A copy of t, `at` elements into a buffer that holds `fill` before and after it."""
+    b = torch.full((at + t.numel() + 16,), fill, dtype=t.dtype, device="cuda")
+    v = b[at:at + t.numel()].view(t.shape)
+    v.copy_(t)
+    return v, b
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("T,k,H", [(1, 1, 1), (1, 2, 9), (2, 1, 64), (3, 4, 31), (5, 3, 97), (4, 9, 513), (40, 4, 333), (7, 8, 775),
+                                   (3, 2, 3001), (2500, 5, 775), (2500, 2, 1543)])
+@pytest.mark.parametrize("at", [(1, 1, 1, 1), (0, 3, 0, 2), (5, 0, 6, 0)])
+def test_rows_of_any_alignment(T, k, H, dtype, at):
+    # every matrix between values that no result may hold, and every result between values that stay
+    o, x, y, w, dout = _case(T, k, H, 4, dtype, seed=H)
+    M = T * k
+    named = o.rows >= 0
+    y[int(o.offsets[-1]):] = float("nan")
+    x = torch.cat([x, torch.full((T, 3), float("nan"), dtype=dtype, device="cuda")], 1)   # a stride of H + 3
+    x = _inside(x, at[0], float("nan"))[0]
+    d = _inside(torch.cat([dout, torch.full_like(x[:, :2], float("nan"))], 1), at[0], float("nan"))[0]
+    y = _inside(y, at[1], float("nan"))[0]
+    results = [_inside(torch.zeros(r, H, dtype=dtype, device="cuda"), at[i], 7.0) for r, i in ((M, 2), (T, 3), (M, 3))]
+    (rows, rows_b), (out, out_b), (dy, dy_b) = results
+    dw = torch.empty(T, k, device="cuda")
+    lib, s, c = native.load(), torch.cuda.current_stream().cuda_stream, CODE[dtype]
+    q = lambda t: t.data_ptr()
+    assert lib.moe_gather_rows(T, k, H, 4, M, q(x), H + 3, c, q(o.rows), q(o.offsets), q(rows), s) == 0
+    assert lib.moe_combine_rows(T, k, H, M, q(y), c, q(o.rows), q(w), q(out), s) == 0
+    assert lib.moe_combine_rows_backward(T, k, H, 4, M, q(d), H + 2, q(y), c, q(o.rows), q(w), q(o.offsets), q(dy), q(dw), s) == 0
+    torch.cuda.synchronize()
+    for (v, b), i in zip(results, (2, 3, 3)):
+        assert (b[:at[i]] == 7).all() and (b[at[i] + v.numel():] == 7).all()
+    ref = torch.zeros_like(rows)
+    ref[o.rows[named].long()] = x[:, :H][named.nonzero()[:, 0]]
+    assert torch.equal(rows, ref)
+    yr = torch.where(named[:, :, None], y[o.rows.clamp_min(0).long()].double(), 0.0)
+    wr = torch.where(named, w.double(), 0.0)
+    terms = wr[:, :, None] * yr
+    assert ((out.double() - terms.sum(1)).abs() <= (k + 1) * E24 * terms.abs().sum(1) + U[dtype] * terms.sum(1).abs() + TINY[dtype]).all()
+    d = dout.double()[:, None, :]
+    rdy = torch.zeros(M, H, dtype=torch.double, device="cuda")
+    rdy[o.rows[named].long()] = (wr[:, :, None] * d)[named]
+    assert ((dy.double() - rdy).abs() <= (U[dtype] + E24) * rdy.abs() + TINY[dtype]).all()
+    assert ((dw.double() - (yr * d).sum(2)).abs() <= (H / 32 + 16) * E24 * (yr * d).abs().sum(2)).all()
 
 
 def test_offsets_past_32_bits():

@@ -148,3 +148,10 @@ def test_python_entry_points_check_shapes_and_types():
         ops.grouped_mm(x.float(), x.float()[None], torch.zeros(2, dtype=torch.int32))
     with pytest.raises(TypeError):
         ops.combine_rows(x.long(), torch.zeros(4, 2, dtype=torch.int32))
+
+
+def test_rows_longer_than_31_bits_hold_are_refused(lib):
+    big = (1 << 30) + 1
+    assert lib.moe_gather_rows(4, 2, big, 3, 8, P, big, BF16, P, P, P, None) == INVALID
+    assert lib.moe_combine_rows(4, 2, big, 8, P, BF16, P, P, P, None) == INVALID
+    assert lib.moe_combine_rows_backward(4, 2, big, 3, 8, P, big, P, BF16, P, P, P, P, P, None) == INVALID
