@@ -8,9 +8,10 @@
 // statistics run (the centred second pass keeps the variance free of cancellation), and every
 // statistic and sum is held in fp32.
 //
-// Measured on a GB300, bf16: 16384 x 4096 forward 45 us, backward 71 us (HBM floors 40 and 60 us
+// Measured on a GB300, bf16: 16384 x 4096 forward 45 us, backward 72 us (HBM floors 40 and 60 us
 // at the measured copy bandwidth), FP8 form 54 us (floor 30: its group maxima and conversions
-// are bound by issue); 128 x 7168 FP8 form 2.9 us in a graph; 4099 x 1001 fp32 9 and 13 us.
+// are bound by issue); 128 x 7168 FP8 form 2.9 us in a graph; 4099 x 1001 fp32 9 and 13 us; 8939 x 2895
+// fp16, rows off 16-byte boundaries, 29 and 45 (2896: 20 and 39; floors 16 and 23).
 //
 // Long batches run in persistent blocks that keep the next rows on their way: every thread
 // copies the packs of the rows ahead that it will itself use into its own slots of shared memory
@@ -85,6 +86,15 @@ __device__ __forceinline__ void unpack(float2 (&f)[PAIRS<V, VPT>], const Pack<T,
     }
 }
 
+// LEAD: rows that start `lead` elements past a 16-byte boundary.  Pack p holds elements p * V - lead ...
+// of the row, so that packs are aligned; the first and the last may hold bytes of the neighbouring rows
+// (clip() drops them, put() leaves them alone).
+template <int V, bool LEAD>
+__device__ __forceinline__ int packs_of(int H, int lead)
+{
+    return LEAD ? (lead + H + V - 1) / V : H / V;
+}
+
 // Packs past the row's end are zeros.
 template <typename T, int V, int VPT>
 __device__ __forceinline__ void fetch(Pack<T, V> (&q)[VPT], const T *row, int t, int step, int packs)
@@ -102,12 +112,12 @@ __device__ __forceinline__ void fetch(Pack<T, V> (&q)[VPT], const T *row, int t,
     }
 }
 
-template <typename T, int V, int VPT>
-__device__ __forceinline__ void put(T *row, const float2 (&f)[PAIRS<V, VPT>], int t, int step, int packs)
+template <typename T, int V, int VPT, bool LEAD = false>
+__device__ __forceinline__ void put(T *row, const float2 (&f)[PAIRS<V, VPT>], int t, int step, int packs, int lead = 0, int H = 0)
 {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int p = t + j * step;
+        const int p = t + j * step, e = p * V - lead;
         if (p < packs) {
             Pack<T, V> q;
             if constexpr (V == 1) {
@@ -124,14 +134,33 @@ __device__ __forceinline__ void put(T *row, const float2 (&f)[PAIRS<V, VPT>], in
                     }
                 }
             }
-            store_pack<T, V>(row + static_cast<size_t>(p) * V, q);
+            if (!LEAD || (e >= 0 && e + V <= H)) {
+                store_pack<T, V>(row + e, q);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (e + i >= 0 && e + i < H)
+                        row[e + i] = q.v[i];
+            }
         }
     }
 }
-
-// Zeroes the pairs (or halves of pairs) past the row's end.
+// One of the thread's packs lies partly outside the row.
 template <int V, int VPT>
-__device__ __forceinline__ void clip(float2 (&f)[PAIRS<V, VPT>], int t, int step, int packs)
+__device__ __forceinline__ bool cut_packs(int t, int step, int lead, int H)
+{
+    bool cut = false;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int e = (t + j * step) * V - lead;
+        cut = cut || (e < 0 && e + V > 0) || (e < H && e + V > H);
+    }
+    return cut;
+}
+// Zeroes the pairs (or halves of pairs) past the row's end and, in threads with cut packs, outside the row:
+// those are in two warps of a row, and the others step over it.
+template <int V, int VPT>
+__device__ __forceinline__ void clip(float2 (&f)[PAIRS<V, VPT>], int t, int step, int packs, bool cut = false, int lead = 0, int H = 0)
 {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -147,24 +176,60 @@ __device__ __forceinline__ void clip(float2 (&f)[PAIRS<V, VPT>], int t, int step
                 f[j * (V / 2) + i] = both(0.0f);
         }
     }
+    if (V > 1 && cut) {
+#pragma unroll
+        for (int i = 0; i < PAIRS<V, VPT>; ++i) {
+            const int c = (t + 2 * i / V * step) * V - lead + 2 * i % V;
+            f[i] = make_float2(c >= 0 && c < H ? f[i].x : 0.0f, c + 1 >= 0 && c + 1 < H ? f[i].y : 0.0f);
+        }
+    }
 }
 
 // A weight's or bias's columns (`none` where there is no such vector).
-template <typename T, int V, int VPT>
-__device__ __forceinline__ void load_columns(float2 (&f)[PAIRS<V, VPT>], const void *p, int w32, float none, int t, int step, int packs)
+template <typename W, int V, int VPT, bool LEAD>
+__device__ __forceinline__ void fetch_columns(float2 (&f)[PAIRS<V, VPT>], const W *p, int t, int step, int packs, int lead, int H)
+{
+    Pack<W, V> q[VPT];
+    if constexpr (LEAD) {
+        // of any alignment: 16 bytes are shifted out of two aligned vectors, all of them asked for before
+        // the first is waited for; where those would leave the vector, element by element
+        constexpr int N = VEC<W>, M = V / N;
+        Halves h[VPT * M];
+#pragma unroll
+        for (int j = 0; j < VPT * M; ++j) {
+            const int c = (t + j / M * step) * V - lead + j % M * N;
+            h[j] = load_halves(p + c, c >= N - 1 && c + 2 * N <= H);
+        }
+#pragma unroll
+        for (int j = 0; j < VPT * M; ++j) {
+            const int c = (t + j / M * step) * V - lead + j % M * N;
+            Pack<W, N> u = shifted(h[j], p + c);
+            if (!(c >= N - 1 && c + 2 * N <= H) && c + N > 0 && c < H) {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    u.v[i] = c + i >= 0 && c + i < H ? __ldg(p + c + i) : from_f<W>(0.0f);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                q[j / M].v[j % M * N + i] = u.v[i];
+        }
+    } else {
+        fetch<W, V, VPT>(q, p, t, step, packs);
+    }
+    unpack<W, V, VPT>(f, q);
+}
+template <typename T, int V, int VPT, bool LEAD = false>
+__device__ __forceinline__ void load_columns(float2 (&f)[PAIRS<V, VPT>], const void *p, int w32, float none, int t, int step, int packs,
+                                             int lead = 0, int H = 0)
 {
     if (!p) {
 #pragma unroll
         for (int i = 0; i < PAIRS<V, VPT>; ++i)
             f[i] = both(none);
     } else if (w32) {
-        Pack<float, V> q[VPT];
-        fetch<float, V, VPT>(q, static_cast<const float *>(p), t, step, packs);
-        unpack<float, V, VPT>(f, q);
+        fetch_columns<float, V, VPT, LEAD>(f, static_cast<const float *>(p), t, step, packs, lead, H);
     } else {
-        Pack<T, V> q[VPT];
-        fetch<T, V, VPT>(q, static_cast<const T *>(p), t, step, packs);
-        unpack<T, V, VPT>(f, q);
+        fetch_columns<T, V, VPT, LEAD>(f, static_cast<const T *>(p), t, step, packs, lead, H);
     }
 }
 
@@ -245,16 +310,23 @@ struct NormArgs {
 // ------------------------------------------------------------------ copies ahead --------
 // A thread's slots: pack j of ring stage g at slot (g * VPT + j) * blockDim + thread, so a
 // warp's accesses are contiguous.
-template <typename T, int V>
-__device__ __forceinline__ void copy_ahead(Pack<T, V> *slot, const T *src)
+// CUT: only the first `bytes` of the pack (which may be none) are there; zeros in place of the others.
+template <typename T, int V, bool CUT>
+__device__ __forceinline__ void copy_ahead(Pack<T, V> *slot, const T *src, int bytes)
 {
     constexpr int BYTES = static_cast<int>(sizeof(Pack<T, V>));
     const uint32_t dst = ptx::smem_u32(slot);
     static_assert(BYTES % 16 == 0, "copies of 16 bytes");
 #pragma unroll
-    for (int i = 0; i < BYTES / 16; ++i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * i), "l"(reinterpret_cast<uint64_t>(src) + 16 * i)
-                     : "memory");
+    for (int i = 0; i < BYTES / 16; ++i) {
+        const uint64_t from = reinterpret_cast<uint64_t>(src) + 16 * i;
+        if constexpr (CUT) {
+            const int n = max(0, min(16, bytes - 16 * i));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * i), "l"(n ? from : from - 16 * i), "r"(n) : "memory");
+        } else {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * i), "l"(from) : "memory");
+        }
+    }
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -264,16 +336,17 @@ __device__ __forceinline__ void copies_wait()
 }
 
 // Row r's packs of this thread into ring stage g (nothing past the last row).
-template <typename T, int V, int VPT>
-__device__ __forceinline__ void fetch_ahead(Pack<T, V> *ring, int g, const void *base, long long ld, int r, int T_, int packs)
+template <typename T, int V, int VPT, bool LEAD>
+__device__ __forceinline__ void fetch_ahead(Pack<T, V> *ring, int g, const void *base, long long ld, int r, int T_, int H, int packs, int lead)
 {
     if (r < T_) {
+        const int left = r == T_ - 1 ? H : H + V;   // elements that may be read
         const T *x = static_cast<const T *>(base) + static_cast<size_t>(r) * ld;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int p = threadIdx.x + j * blockDim.x;
+            const int p = threadIdx.x + j * blockDim.x, e = p * V - lead;
             if (p < packs)
-                copy_ahead<T, V>(ring + (g * VPT + j) * blockDim.x + threadIdx.x, x + static_cast<size_t>(p) * V);
+                copy_ahead<T, V, LEAD>(ring + (g * VPT + j) * blockDim.x + threadIdx.x, x + e, (left - e) * static_cast<int>(sizeof(T)));
         }
     }
 }
@@ -348,12 +421,12 @@ __device__ __forceinline__ void from_bytes(float2 (&f)[PAIRS<1, VPT>], const uin
 // The row held in f (zeros past its end), its statistics and outputs; w and b: the thread's
 // columns of weight and bias.  FP8: e4m3 codes and 1x128 scales instead of y (V = 8: 16 lanes
 // hold one group of 128).  `after_read` runs once every thread has its row in registers.
-template <typename T, int V, int VPT, bool FP8, bool WARP, typename F>
-__device__ __forceinline__ void norm_row(const NormArgs &a, int row, float2 (&f)[PAIRS<V, VPT>], const float2 (&w)[PAIRS<V, VPT>],
+template <typename T, int V, int VPT, bool FP8, bool WARP, bool LEAD, typename F>
+__device__ __forceinline__ void norm_row(const NormArgs &a, int row, int lead, bool cut, float2 (&f)[PAIRS<V, VPT>], const float2 (&w)[PAIRS<V, VPT>],
                                          const float2 (&b)[PAIRS<V, VPT>], float *red, F after_read)
 {
     constexpr int P = PAIRS<V, VPT>;
-    const int packs = a.H / V, t = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
+    const int packs = packs_of<V, LEAD>(a.H, lead), t = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
     const float inv = 1.0f / static_cast<float>(a.H);
     float2 acc = both(0.0f);
 #pragma unroll
@@ -366,7 +439,7 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, int row, float2 (&f)
 #pragma unroll
     for (int i = 0; i < P; ++i)
         f[i] = add2(f[i], both(-mean));
-    clip<V, VPT>(f, t, step, packs);
+    clip<V, VPT>(f, t, step, packs, LEAD && cut, lead, a.H);
     acc = both(0.0f);
 #pragma unroll
     for (int i = 0; i < P; ++i)
@@ -417,7 +490,7 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, int row, float2 (&f)
             }
         }
     } else {
-        put<T, V, VPT>(static_cast<T *>(a.y) + static_cast<size_t>(row) * a.H, f, t, step, packs);
+        put<T, V, VPT, LEAD>(static_cast<T *>(a.y) + static_cast<size_t>(row) * a.H, f, t, step, packs, lead, a.H);
     }
 }
 
@@ -447,43 +520,45 @@ __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : V * VPT == 32 ? 512 : 
             const int next = row + gridDim.x * ROW_WARPS;
             if (next < a.T)
                 fetch<T, V, VPT>(q, x + static_cast<size_t>(next) * a.ldx, t, step, packs);
-            norm_row<T, V, VPT, FP8, true>(a, row, f, w, b, red, [] {});
+            norm_row<T, V, VPT, FP8, true, false>(a, row, 0, false, f, w, b, red, [] {});
             if (next >= a.T)
                 return;
             row = next;
         }
     } else {
         unpack<T, V, VPT>(f, q);
-        norm_row<T, V, VPT, FP8, false>(a, row, f, w, b, red, [] {});
+        norm_row<T, V, VPT, FP8, false, false>(a, row, 0, false, f, w, b, red, [] {});
     }
 }
 
 // Persistent blocks: rows copied AHEAD rows before their use, weight and bias kept in registers.
-template <typename T, int V, int VPT, bool FP8, int AHEAD>
+template <typename T, int V, int VPT, bool FP8, int AHEAD, bool LEAD>
 __global__ void __launch_bounds__(512) norm_ring_kernel(const NormArgs a)
 {
     constexpr int P = PAIRS<V, VPT>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[64];
     Pack<T, V> *ring = reinterpret_cast<Pack<T, V> *>(smem);
-    const int packs = a.H / V;
+    const int lead = LEAD ? lead_of(static_cast<const T *>(a.x) + static_cast<size_t>(blockIdx.x) * a.ldx) : 0;
+    const int packs = packs_of<V, LEAD>(a.H, lead);
+    const bool cut = LEAD && cut_packs<V, VPT>(threadIdx.x, blockDim.x, lead, a.H);
 #pragma unroll
     for (int g = 0; g < AHEAD; ++g) {
-        fetch_ahead<T, V, VPT>(ring, g, a.x, a.ldx, blockIdx.x + g * gridDim.x, a.T, packs);
+        fetch_ahead<T, V, VPT, LEAD>(ring, g, a.x, a.ldx, blockIdx.x + g * gridDim.x, a.T, a.H, packs, lead);
         copies_commit();
     }
     clear_sums<1>(red);
     float2 w[P], b[P];
-    load_columns<T, V, VPT>(w, a.weight, a.w32, 1.0f, threadIdx.x, blockDim.x, packs);
-    load_columns<T, V, VPT>(b, a.bias, a.w32, 0.0f, threadIdx.x, blockDim.x, packs);
+    load_columns<T, V, VPT, LEAD>(w, a.weight, a.w32, 1.0f, threadIdx.x, blockDim.x, packs, lead, a.H);
+    load_columns<T, V, VPT, LEAD>(b, a.bias, a.w32, 0.0f, threadIdx.x, blockDim.x, packs, lead, a.H);
     int g = 0;
     for (int row = blockIdx.x; row < a.T; row += gridDim.x) {
         copies_wait<AHEAD - 1>();
         float2 f[P];
         from_ring<T, V, VPT>(f, ring, g);
-        clip<V, VPT>(f, threadIdx.x, blockDim.x, packs);
-        norm_row<T, V, VPT, FP8, false>(a, row, f, w, b, red, [&] {
-            fetch_ahead<T, V, VPT>(ring, g, a.x, a.ldx, row + AHEAD * gridDim.x, a.T, packs);
+        clip<V, VPT>(f, threadIdx.x, blockDim.x, packs, LEAD && cut, lead, a.H);
+        norm_row<T, V, VPT, FP8, false, LEAD>(a, row, lead, cut, f, w, b, red, [&] {
+            fetch_ahead<T, V, VPT, LEAD>(ring, g, a.x, a.ldx, row + AHEAD * gridDim.x, a.T, a.H, packs, lead);
             copies_commit();
         });
         g = g == AHEAD - 1 ? 0 : g + 1;
@@ -515,7 +590,7 @@ __global__ void __launch_bounds__(512) norm_bytes_kernel(const NormArgs a, const
         __syncthreads();   // the other threads' copies
         float2 f[P];
         from_bytes<T, VPT>(f, smem + g * size, m, row, a.H);
-        norm_row<T, 1, VPT, false, false>(a, row, f, w, b, red, [&] {
+        norm_row<T, 1, VPT, false, false, false>(a, row, 0, false, f, w, b, red, [&] {
             const int next = row + AHEAD * gridDim.x;
             if (next < a.T)
                 fetch_bytes<T>(smem + g * size, m, next);
@@ -534,7 +609,8 @@ struct NormBwdArgs {
     int w32;
     const float *mean, *rstd;
     void *dx;
-    float *part;   // [2][blocks][H] sums of dy*xh and of dy over each block's rows
+    float *part;   // [2][blocks][pitch] sums of dy*xh and of dy over each block's rows (LEAD: from their lead on)
+    int pitch;
 };
 
 // xh and a = dy*g of one row, its two sums, and the columns' sums so far.
@@ -569,26 +645,29 @@ __device__ __forceinline__ void backward_out(float2 (&o)[P], const float2 (&xh)[
 // of them, so dy and x are read once from HBM.  AHEAD > 0: rows of x and dy copied that many rows
 // before use, and read from shared memory twice (for the sums, then for dx) instead of held in
 // registers between.
-template <typename T, int V, int VPT, int AHEAD>
-__global__ void __launch_bounds__(V * VPT <= 16 && V == 1 ? 1024 : 512) norm_backward_kernel(const NormBwdArgs a)
+template <typename T, int V, int VPT, int AHEAD, bool LEAD>
+__global__ void __launch_bounds__(512) norm_backward_kernel(const NormBwdArgs a)
 {
     constexpr int P = PAIRS<V, VPT>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[128];
-    const int packs = a.H / V, t = threadIdx.x, step = blockDim.x;
+    const int t = threadIdx.x, step = blockDim.x;
+    const int lead = LEAD ? lead_of(static_cast<const T *>(a.x) + static_cast<size_t>(blockIdx.x) * a.ldx) : 0;
+    const int packs = packs_of<V, LEAD>(a.H, lead);
+    const bool cut = LEAD && cut_packs<V, VPT>(t, step, lead, a.H);
     const float inv = 1.0f / static_cast<float>(a.H);
     Pack<T, V> *ring_x = reinterpret_cast<Pack<T, V> *>(smem), *ring_d = ring_x + AHEAD * VPT * blockDim.x;
     if constexpr (AHEAD > 0) {
 #pragma unroll
         for (int g = 0; g < AHEAD; ++g) {
-            fetch_ahead<T, V, VPT>(ring_x, g, a.x, a.ldx, blockIdx.x + g * gridDim.x, a.T, packs);
-            fetch_ahead<T, V, VPT>(ring_d, g, a.dy, a.lddy, blockIdx.x + g * gridDim.x, a.T, packs);
+            fetch_ahead<T, V, VPT, LEAD>(ring_x, g, a.x, a.ldx, blockIdx.x + g * gridDim.x, a.T, a.H, packs, lead);
+            fetch_ahead<T, V, VPT, LEAD>(ring_d, g, a.dy, a.lddy, blockIdx.x + g * gridDim.x, a.T, a.H, packs, lead);
             copies_commit();
         }
     }
     clear_sums<2>(red);
     float2 w[P], dg[P], db[P];
-    load_columns<T, V, VPT>(w, a.weight, a.w32, 1.0f, t, step, packs);
+    load_columns<T, V, VPT, LEAD>(w, a.weight, a.w32, 1.0f, t, step, packs, lead, a.H);
 #pragma unroll
     for (int i = 0; i < P; ++i)
         dg[i] = db[i] = both(0.0f);
@@ -609,9 +688,9 @@ __global__ void __launch_bounds__(V * VPT <= 16 && V == 1 ? 1024 : 512) norm_bac
             fetch<T, V, VPT>(q, static_cast<const T *>(a.dy) + static_cast<size_t>(row) * a.lddy, t, step, packs);
             unpack<T, V, VPT>(d, q);
         }
-        if constexpr (AHEAD > 0) {   // what lies past the row's end is not there: no products with it
-            clip<V, VPT>(xh, t, step, packs);
-            clip<V, VPT>(d, t, step, packs);
+        if constexpr (AHEAD > 0) {   // what lies outside the row is not there: no products with it
+            clip<V, VPT>(xh, t, step, packs, LEAD && cut, lead, a.H);
+            clip<V, VPT>(d, t, step, packs, LEAD && cut, lead, a.H);
         }
         float s[2];
         backward_sums<P>(xh, d, w, dg, db, mean, rstd, s);
@@ -625,10 +704,10 @@ __global__ void __launch_bounds__(V * VPT <= 16 && V == 1 ? 1024 : 512) norm_bac
                 xh[i] = mul2(add2(xh[i], both(-mean)), both(rstd));
         }
         backward_out<P>(o, xh, d, w, inv, rstd, s);
-        put<T, V, VPT>(static_cast<T *>(a.dx) + static_cast<size_t>(row) * a.H, o, t, step, packs);
+        put<T, V, VPT, LEAD>(static_cast<T *>(a.dx) + static_cast<size_t>(row) * a.H, o, t, step, packs, lead, a.H);
         if constexpr (AHEAD > 0) {   // (every value read above has been used by now)
-            fetch_ahead<T, V, VPT>(ring_x, stage, a.x, a.ldx, row + AHEAD * gridDim.x, a.T, packs);
-            fetch_ahead<T, V, VPT>(ring_d, stage, a.dy, a.lddy, row + AHEAD * gridDim.x, a.T, packs);
+            fetch_ahead<T, V, VPT, LEAD>(ring_x, stage, a.x, a.ldx, row + AHEAD * gridDim.x, a.T, a.H, packs, lead);
+            fetch_ahead<T, V, VPT, LEAD>(ring_d, stage, a.dy, a.lddy, row + AHEAD * gridDim.x, a.T, a.H, packs, lead);
             copies_commit();
             stage = stage == AHEAD - 1 ? 0 : stage + 1;
         }
@@ -636,8 +715,9 @@ __global__ void __launch_bounds__(V * VPT <= 16 && V == 1 ? 1024 : 512) norm_bac
         rstd = rstd1;
     }
     if (a.part) {
-        put<float, V, VPT>(a.part + static_cast<size_t>(blockIdx.x) * a.H, dg, t, step, packs);
-        put<float, V, VPT>(a.part + (static_cast<size_t>(gridDim.x) + blockIdx.x) * a.H, db, t, step, packs);
+        float *p = a.part + static_cast<size_t>(blockIdx.x) * a.pitch;
+        put<float, V, VPT>(p, dg, t, step, packs);
+        put<float, V, VPT>(p + static_cast<size_t>(gridDim.x) * a.pitch, db, t, step, packs);
     }
     ptx::launch_dependents();
 }
@@ -689,8 +769,9 @@ __global__ void __launch_bounds__(512) norm_backward_bytes_kernel(const NormBwdA
         put<T, 1, VPT>(static_cast<T *>(a.dx) + static_cast<size_t>(row) * a.H, o, t, step, a.H);
     }
     if (a.part) {
-        put<float, 1, VPT>(a.part + static_cast<size_t>(blockIdx.x) * a.H, dg, t, step, a.H);
-        put<float, 1, VPT>(a.part + (static_cast<size_t>(gridDim.x) + blockIdx.x) * a.H, db, t, step, a.H);
+        float *p = a.part + static_cast<size_t>(blockIdx.x) * a.pitch;
+        put<float, 1, VPT>(p, dg, t, step, a.H);
+        put<float, 1, VPT>(p + static_cast<size_t>(gridDim.x) * a.pitch, db, t, step, a.H);
     }
     ptx::launch_dependents();
 }
@@ -748,19 +829,24 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) norm_backward_warp_kernel(cons
 #pragma unroll
             for (int k = 0; k < ROW_WARPS; ++k)
                 v += sums[which][k][c];
-            a.part[(static_cast<size_t>(which) * gridDim.x + blockIdx.x) * a.H + c] = v;
+            a.part[(static_cast<size_t>(which) * gridDim.x + blockIdx.x) * a.pitch + c] = v;
         }
     }
     ptx::launch_dependents();
 }
 
-// Column sums of the partial sums, in a fixed order: a block of 32 columns x 32 row lanes.
+// Column sums of the partial sums, in a fixed order: a block of 32 columns x 32 row lanes.  Row b of them
+// starts at b * step elements past a boundary of `boundary`.
+struct PartRows {
+    const float *part;
+    int blocks, pitch, step, boundary;
+};
 template <typename TW>
-__global__ void norm_reduce_kernel(const float *part, int blocks, int H, TW *dweight, TW *dbias)
+__global__ void norm_reduce_kernel(const PartRows p, int H, TW *dweight, TW *dbias)
 {
     __shared__ float tile[32][33];
     ptx::grid_dependency_wait();
-    const float *src = part + static_cast<size_t>(blockIdx.y) * blocks * H;
+    const float *src = p.part + static_cast<size_t>(blockIdx.y) * p.blocks * p.pitch;
     TW *dst = blockIdx.y == 0 ? dweight : dbias;
     if (!dst)
         return;
@@ -768,8 +854,8 @@ __global__ void norm_reduce_kernel(const float *part, int blocks, int H, TW *dwe
     float s = 0.0f;
     if (col < H) {
 #pragma unroll 4
-        for (int b = threadIdx.y; b < blocks; b += 32)
-            s += src[static_cast<size_t>(b) * H + col];
+        for (int b = threadIdx.y; b < p.blocks; b += 32)
+            s += src[static_cast<size_t>(b) * p.pitch + col + ((b * p.step) & (p.boundary - 1))];
     }
     tile[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
@@ -781,7 +867,7 @@ __global__ void norm_reduce_kernel(const float *part, int blocks, int H, TW *dwe
 
 // Started while the last rows are still worked on; it waits for them before it reads.
 template <typename TW>
-cudaError_t launch_reduce(const float *part, int blocks, int H, TW *dweight, TW *dbias, cudaStream_t s)
+cudaError_t launch_reduce(const PartRows &p, int H, TW *dweight, TW *dbias, cudaStream_t s)
 {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -792,19 +878,44 @@ cudaError_t launch_reduce(const float *part, int blocks, int H, TW *dweight, TW 
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_reduce_kernel<TW>, part, blocks, H, dweight, dbias);
+    return cudaLaunchKernelEx(&cfg, norm_reduce_kernel<TW>, p, H, dweight, dbias);
 }
 
 int round32(int v) { return (v + 31) / 32 * 32; }
 
-// Rows whose H elements and addresses allow 16-byte accesses move as packs of 8 elements, others
-// an element at a time (neighbouring lanes on neighbouring elements).
-bool packed_rows(int H, int dtype, const void *p, long long ld)
+// How rows move.  PACKED: every row starts on a 16-byte boundary and has whole packs of 8 elements.
+// PHASED: packs too, where rows start off the boundaries (or end inside a pack) but the same row of
+// every tensor at the same place past one: rows a multiple of 8 apart then have one lead, so with such
+// a stride a block's columns stay and only its packs' ends differ.  ANY: element by element
+// (neighbouring lanes on neighbouring elements).
+enum Rows { PACKED, PHASED, ANY };
+Rows rows_of(int H, int dtype, const void *p, long long ld)
 {
     const size_t b = dtype_bytes(dtype);
-    return H % 8 == 0 && op_aligned(p, 16) && static_cast<size_t>(ld) * b % 16 == 0;
+    if (!op_aligned(p, 16) || static_cast<size_t>(ld - H) * b % 16 != 0 || H < 8)
+        return ANY;
+    return H % 8 == 0 ? PACKED : PHASED;
 }
-bool packed_affine(const void *p) { return p == nullptr || op_aligned(p, 16); }
+Rows worst(Rows a, Rows b) { return a > b ? a : b; }
+// weight or bias
+Rows affine_of(const void *p) { return p == nullptr || op_aligned(p, 16) ? PACKED : PHASED; }
+// Packs of a row, at most.
+template <typename T>
+int most_packs(int H, Rows rows)
+{
+    return rows == PACKED ? H / 8 : (H + 16 / static_cast<int>(sizeof(T)) - 1 + 7) / 8;
+}
+// Rows in packs with a lead, in the persistent kernels (forward and backward in us, element by element in
+// brackets): 16384 x 5001 bf16 74 and 133 (155 and 218), 5000 x 2001 12.8 and 20 (14.8 and 24), fp32 16384 x
+// 3001 backward 117 (142).  Not where they are no faster: rows of a warp, 16384 x 1001 bf16 21 and 33 (21
+// and 31); single rows of a block, whose columns' shifts come once a row, 3000 x 1501 bf16 12 and 16 (9.1
+// and 16); 2000 x 8191 bf16, whose packs take four a thread, 27 and 54 (28 and 41); and fp32's
+// forward, 8192 x 7001 114 (106).
+template <typename T>
+bool phased(int H, Rows rows)
+{
+    return rows == PHASED && H > 1024 && most_packs<T>(H, rows) <= 1024;
+}
 
 bool norm_args_ok(int T, int H, int dtype, int w_dtype, const void *weight, const void *bias)
 {
@@ -835,19 +946,22 @@ int ring_blocks(int threads, int ahead, int tensors, size_t &smem)
     return static_cast<int>(fit < want ? fit : want);
 }
 
-template <typename T, bool FP8, int AHEAD>
-bool try_norm_ring(const NormArgs &a, int num_sms, cudaStream_t s)
+// Leads repeat after at most 8 rows: with a stride of whole eights a block's rows have one lead.
+int ring_grid(int per_sm, int num_sms) { return per_sm * num_sms / 8 * 8; }
+
+template <typename T, bool FP8, int AHEAD, bool LEAD>
+bool try_norm_ring(const NormArgs &a, int packs, int num_sms, cudaStream_t s)
 {
-    const int threads = round32((a.H / 8 + 3) / 4);
+    const int threads = round32((packs + 3) / 4);
     size_t smem;
     const int per_sm = ring_blocks<T, 8, 4>(threads, AHEAD, 1, smem);
     // long batches only: every block has rows to copy ahead of
     if (per_sm < 1 || a.T < AHEAD * per_sm * num_sms)
         return false;
-    const auto kern = norm_ring_kernel<T, 8, 4, FP8, AHEAD>;
+    const auto kern = norm_ring_kernel<T, 8, 4, FP8, AHEAD, LEAD>;
     if (!allow_smem(kern, smem))
         return false;
-    kern<<<per_sm * num_sms, threads, smem, s>>>(a);
+    kern<<<ring_grid(per_sm, num_sms), threads, smem, s>>>(a);
     return true;
 }
 
@@ -904,34 +1018,43 @@ void launch_norm_warps(const NormArgs &a, int num_sms, cudaStream_t s)
 }
 
 template <typename T, bool FP8>
-bool launch_norm(const NormArgs &a, bool packed, int num_sms, cudaStream_t s)
+void launch_norm_packs(const NormArgs &a, int num_sms, cudaStream_t s)
 {
     // few rows: as many threads a row as it has packs, for latency (128 x 7168 bf16 2.6 us, four packs a
     // thread 2.8; 600 x 4096 4.5 and 3.4)
     const bool few = a.T <= 2 * num_sms;
-    if (packed) {
-        const int packs = a.H / 8;
-        if (packs <= 32)
-            launch_norm_warps<T, 8, 1, FP8>(a, num_sms, s);
-        else if (packs <= 128 && !few)
-            launch_norm_warps<T, 8, 4, FP8>(a, num_sms, s);
-        else if (few && packs <= 1024)
-            norm_kernel<T, 8, 1, FP8, false><<<a.T, round32(packs), 0, s>>>(a);
-        else if (!try_norm_ring<T, FP8, 4>(a, num_sms, s))
-            norm_kernel<T, 8, 4, FP8, false><<<a.T, round32((packs + 3) / 4), 0, s>>>(a);
-    } else if constexpr (!FP8) {
-        if (a.H <= 256)
-            launch_norm_warps<T, 1, 8, false>(a, num_sms, s);
-        else if (a.H <= 576)
-            launch_norm_warps<T, 1, 18, false>(a, num_sms, s);
-        else if (a.H <= 1024)
-            launch_norm_warps<T, 1, 32, false>(a, num_sms, s);
-        else {
-            const BytesPlan p = bytes_plan(a.H, sizeof(T), 1);
-            return a.H > 8192    ? (p.ahead == 3 ? launch_norm_bytes<T, 32, 3>(a, p, num_sms, s) : launch_norm_bytes<T, 32, 1>(a, p, num_sms, s))
-                   : p.ahead == 3 ? launch_norm_bytes<T, 16, 3>(a, p, num_sms, s)
-                                  : launch_norm_bytes<T, 16, 1>(a, p, num_sms, s);
-        }
+    const int packs = a.H / 8;
+    if (packs <= 32)
+        launch_norm_warps<T, 8, 1, FP8>(a, num_sms, s);
+    else if (packs <= 128 && !few)
+        launch_norm_warps<T, 8, 4, FP8>(a, num_sms, s);
+    else if (few && packs <= 1024)
+        norm_kernel<T, 8, 1, FP8, false><<<a.T, round32(packs), 0, s>>>(a);
+    else if (!try_norm_ring<T, FP8, 4, false>(a, packs, num_sms, s))
+        norm_kernel<T, 8, 4, FP8, false><<<a.T, round32((packs + 3) / 4), 0, s>>>(a);
+}
+
+template <typename T>
+bool launch_norm(const NormArgs &a, Rows rows, int num_sms, cudaStream_t s)
+{
+    if (rows == PACKED) {
+        launch_norm_packs<T, false>(a, num_sms, s);
+        return true;
+    }
+    if constexpr (sizeof(T) == 2)   // (see phased)
+        if (phased<T>(a.H, rows) && try_norm_ring<T, false, 4, true>(a, most_packs<T>(a.H, rows), num_sms, s))
+            return true;
+    if (a.H <= 256)
+        launch_norm_warps<T, 1, 8, false>(a, num_sms, s);
+    else if (a.H <= 576)
+        launch_norm_warps<T, 1, 18, false>(a, num_sms, s);
+    else if (a.H <= 1024)
+        launch_norm_warps<T, 1, 32, false>(a, num_sms, s);
+    else {
+        const BytesPlan p = bytes_plan(a.H, sizeof(T), 1);
+        return a.H > 8192    ? (p.ahead == 3 ? launch_norm_bytes<T, 32, 3>(a, p, num_sms, s) : launch_norm_bytes<T, 32, 1>(a, p, num_sms, s))
+               : p.ahead == 3 ? launch_norm_bytes<T, 16, 3>(a, p, num_sms, s)
+                              : launch_norm_bytes<T, 16, 1>(a, p, num_sms, s);
     }
     return true;
 }
@@ -939,42 +1062,49 @@ bool launch_norm(const NormArgs &a, bool packed, int num_sms, cudaStream_t s)
 // The backward pass: kernel, blocks (each keeps a row of partial sums) and how they are found.
 enum Plan { WARPS_1, WARPS_4, RING, DIRECT, BYTES };
 template <typename T>
-Plan backward_plan(int T_, int H, bool packed, int num_sms, int &blocks)
+Plan backward_plan(int T_, int H, Rows rows, int num_sms, int &blocks)
 {
-    if (H <= 256 || (H <= 1024 && (!packed || T_ > 2 * num_sms))) {
+    if (H <= 256 || (H <= 1024 && (rows != PACKED || T_ > 2 * num_sms))) {
         blocks = warp_blocks(T_, 3, num_sms);
         return H <= 256 ? WARPS_1 : WARPS_4;
     }
-    if (packed) {
+    if (rows == PACKED || phased<T>(H, rows)) {
         size_t smem;
-        const int per_sm = H <= 8192 ? ring_blocks<T, 8, 2>(round32((H / 8 + 1) / 2), H <= 4096 ? 4 : 3, 2, smem)
-                                     : ring_blocks<T, 8, 4>(round32((H / 8 + 3) / 4), 2, 2, smem);
+        const int packs = most_packs<T>(H, rows);
+        const int per_sm = packs <= 1024 ? ring_blocks<T, 8, 2>(round32((packs + 1) / 2), packs <= 512 ? 4 : 3, 2, smem)
+                                         : ring_blocks<T, 8, 4>(round32((packs + 3) / 4), 2, 2, smem);
         if (per_sm >= 1 && T_ >= 4 * per_sm * num_sms) {
-            blocks = per_sm * num_sms;
+            blocks = ring_grid(per_sm, num_sms);
             return RING;
         }
     }
-    blocks = packed ? (H >= 4096 ? 1 : 2) * num_sms : bytes_plan(H, sizeof(T), 2).per_sm * num_sms;
+    blocks = rows == PACKED ? (H >= 4096 ? 1 : 2) * num_sms : bytes_plan(H, sizeof(T), 2).per_sm * num_sms;
     blocks = T_ < blocks ? T_ : blocks;
-    return packed ? DIRECT : BYTES;
+    return rows == PACKED ? DIRECT : BYTES;
 }
-// (the workspace covers either alignment)
+// (the workspace covers every alignment)
 template <typename T>
 int most_backward_blocks(int T_, int H, int num_sms)
 {
-    int p, u;
-    backward_plan<T>(T_, H, true, num_sms, p);
-    backward_plan<T>(T_, H, false, num_sms, u);
-    return p > u ? p : u;
+    int most = 0;
+    for (const Rows rows : {PACKED, PHASED, ANY}) {
+        int b;
+        backward_plan<T>(T_, H, rows, num_sms, b);
+        most = b > most ? b : most;
+    }
+    return most;
 }
 
-template <typename T, int VPT, int AHEAD>
-bool launch_backward_ring(const NormBwdArgs &a, int blocks, cudaStream_t s)
+// Floats of a row of partial sums: whole packs after any lead.
+int part_pitch(int H) { return (H + 7 + 7) / 8 * 8; }
+
+template <typename T, int VPT, int AHEAD, bool LEAD>
+bool launch_backward_ring(const NormBwdArgs &a, int packs, int blocks, cudaStream_t s)
 {
-    const int threads = round32((a.H / 8 + VPT - 1) / VPT);
+    const int threads = round32((packs + VPT - 1) / VPT);
     size_t smem;
     ring_blocks<T, 8, VPT>(threads, AHEAD, 2, smem);
-    const auto kern = norm_backward_kernel<T, 8, VPT, AHEAD>;
+    const auto kern = norm_backward_kernel<T, 8, VPT, AHEAD, LEAD>;
     if (!allow_smem(kern, smem))
         return false;
     kern<<<blocks, threads, smem, s>>>(a);
@@ -982,32 +1112,40 @@ bool launch_backward_ring(const NormBwdArgs &a, int blocks, cudaStream_t s)
 }
 
 template <typename T>
-bool launch_backward(const NormBwdArgs &a, bool packed, Plan plan, int blocks, cudaStream_t s)
+bool launch_backward(const NormBwdArgs &a, Rows rows, int num_sms, PartRows &part, cudaStream_t s)
 {
-    const int packs = a.H / 8;
+    int blocks;
+    const Plan plan = backward_plan<T>(a.T, a.H, rows, num_sms, blocks);
+    const bool packed = rows == PACKED;
+    const int packs = most_packs<T>(a.H, rows);
+    constexpr int boundary = VEC<T>;
+    part = {a.part, blocks, a.pitch, plan == RING && !packed ? a.H % boundary : 0, boundary};
+    if (plan == RING && !packed)
+        return packs <= 512 ? launch_backward_ring<T, 2, 4, true>(a, packs, blocks, s) : launch_backward_ring<T, 2, 3, true>(a, packs, blocks, s);
     if (plan == RING)
-        return a.H <= 4096   ? launch_backward_ring<T, 2, 4>(a, blocks, s)
-               : a.H <= 8192 ? launch_backward_ring<T, 2, 3>(a, blocks, s)
-                             : launch_backward_ring<T, 4, 2>(a, blocks, s);
+        return packs <= 512    ? launch_backward_ring<T, 2, 4, false>(a, packs, blocks, s)
+               : packs <= 1024 ? launch_backward_ring<T, 2, 3, false>(a, packs, blocks, s)
+                               : launch_backward_ring<T, 4, 2, false>(a, packs, blocks, s);
     if (plan == WARPS_1 && packed)
         norm_backward_warp_kernel<T, 8, 1><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
-    else if (plan == WARPS_1)
-        norm_backward_warp_kernel<T, 1, 8><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
     else if (plan == WARPS_4 && packed)
         norm_backward_warp_kernel<T, 8, 4><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
+    else if (plan == DIRECT && packs <= 1024)
+        norm_backward_kernel<T, 8, 2, 0, false><<<blocks, round32((packs + 1) / 2), 0, s>>>(a);
+    else if (plan == DIRECT)
+        norm_backward_kernel<T, 8, 4, 0, false><<<blocks, round32((packs + 3) / 4), 0, s>>>(a);
+    else if (plan == WARPS_1)
+        norm_backward_warp_kernel<T, 1, 8><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
     else if (plan == WARPS_4 && a.H <= 576)
         norm_backward_warp_kernel<T, 1, 18><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
     else if (plan == WARPS_4)
         norm_backward_warp_kernel<T, 1, 32><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
-    else if (plan == BYTES) {
+    else {
         const BytesPlan p = bytes_plan(a.H, sizeof(T), 2);
         return a.H > 8192     ? (p.ahead == 3 ? launch_backward_bytes<T, 32, 3>(a, p, blocks, s) : launch_backward_bytes<T, 32, 1>(a, p, blocks, s))
                : p.ahead == 3 ? launch_backward_bytes<T, 16, 3>(a, p, blocks, s)
                               : launch_backward_bytes<T, 16, 1>(a, p, blocks, s);
-    } else if (a.H <= 8192)
-        norm_backward_kernel<T, 8, 2, 0><<<blocks, round32((packs + 1) / 2), 0, s>>>(a);
-    else
-        norm_backward_kernel<T, 8, 4, 0><<<blocks, round32((packs + 3) / 4), 0, s>>>(a);
+    }
     return true;
 }
 
@@ -1027,9 +1165,9 @@ int moe_layer_norm(int T, int H, const void *x, int64_t ldx, int dtype, const vo
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
     const NormArgs a{T, H, x, ldx, weight, bias, w_dtype == MOE_F32 && dtype != MOE_F32, eps, y, mean, rstd, nullptr, nullptr, 0};
-    const bool packed = packed_rows(H, dtype, x, ldx) && op_aligned(y, 16) && packed_affine(weight) && packed_affine(bias);
+    const Rows rows = worst(worst(rows_of(H, dtype, x, ldx), rows_of(H, dtype, y, H)), worst(affine_of(weight), affine_of(bias)));
     const bool ok = with_dtype(dtype, [&](auto *t) {
-        return launch_norm<std::remove_pointer_t<decltype(t)>, false>(a, packed, sms, static_cast<cudaStream_t>(stream));
+        return launch_norm<std::remove_pointer_t<decltype(t)>>(a, rows, sms, static_cast<cudaStream_t>(stream));
     });
     return ok ? launched() : MOE_ERR_CUDA;
 }
@@ -1042,15 +1180,15 @@ int moe_layer_norm_fp8(int T, int H, const void *x, int64_t ldx, int dtype, cons
         return MOE_ERR_INVALID_ARG;
     if (T == 0)
         return MOE_OK;
-    if (!x || !q || !sf || !packed_rows(H, dtype, x, ldx) || !op_aligned(q, 16) || !op_aligned(sf, 4) ||
-        !packed_affine(weight) || !packed_affine(bias))
+    if (!x || !q || !sf || rows_of(H, dtype, x, ldx) != PACKED || !op_aligned(q, 16) || !op_aligned(sf, 4) ||
+        affine_of(weight) != PACKED || affine_of(bias) != PACKED)
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
     const NormArgs a{T, H, x, ldx, weight, bias, w_dtype == MOE_F32 && dtype != MOE_F32, eps, nullptr, nullptr, nullptr, q, sf, pow2_scales};
-    const bool ok = with_dtype(dtype, [&](auto *t) {
-        return launch_norm<std::remove_pointer_t<decltype(t)>, true>(a, true, sms, static_cast<cudaStream_t>(stream));
+    with_dtype(dtype, [&](auto *t) {
+        launch_norm_packs<std::remove_pointer_t<decltype(t)>, true>(a, sms, static_cast<cudaStream_t>(stream));
     });
-    return ok ? launched() : MOE_ERR_CUDA;
+    return launched();
 }
 
 int moe_layer_norm_backward_workspace(int T, int H, uint64_t *bytes)
@@ -1060,7 +1198,7 @@ int moe_layer_norm_backward_workspace(int T, int H, uint64_t *bytes)
     OP_DEVICE(sms);
     // enough for every element type
     const int a = most_backward_blocks<float>(T, H, sms), b = most_backward_blocks<__nv_bfloat16>(T, H, sms);
-    *bytes = 2ull * (a > b ? a : b) * static_cast<uint64_t>(H) * sizeof(float);
+    *bytes = 2ull * (a > b ? a : b) * static_cast<uint64_t>(part_pitch(H)) * sizeof(float);
     return MOE_OK;
 }
 
@@ -1084,16 +1222,14 @@ int moe_layer_norm_backward(int T, int H, const void *dy, int64_t lddy, const vo
     if (sums && T > 0 &&
         (!workspace || !op_aligned(workspace, 16) || moe_layer_norm_backward_workspace(T, H, &need) != MOE_OK || workspace_bytes < need))
         return MOE_ERR_INVALID_ARG;
-    int blocks = 0;
+    PartRows part{};
     if (T > 0) {
         const NormBwdArgs a{T, H, dy, x, lddy, ldx, weight, w_dtype == MOE_F32 && dtype != MOE_F32, mean, rstd, dx,
-                            sums ? static_cast<float *>(workspace) : nullptr};
-        const bool packed = packed_rows(H, dtype, x, ldx) && packed_rows(H, dtype, dy, lddy) && op_aligned(dx, 16) &&
-                            packed_affine(weight);
+                            sums ? static_cast<float *>(workspace) : nullptr, part_pitch(H)};
+        const Rows rows = worst(worst(rows_of(H, dtype, x, ldx), rows_of(H, dtype, dy, lddy)),
+                                worst(rows_of(H, dtype, dx, H), affine_of(weight)));
         const bool ok = with_dtype(dtype, [&](auto *t) {
-            using E = std::remove_pointer_t<decltype(t)>;
-            const Plan plan = backward_plan<E>(T, H, packed, sms, blocks);
-            return launch_backward<E>(a, packed, plan, blocks, s);
+            return launch_backward<std::remove_pointer_t<decltype(t)>>(a, rows, sms, part, s);
         });
         if (!ok || launched() != MOE_OK)
             return MOE_ERR_CUDA;
@@ -1102,7 +1238,7 @@ int moe_layer_norm_backward(int T, int H, const void *dy, int64_t lddy, const vo
         // T == 0: no partial rows, the sums are zero
         const cudaError_t e = with_dtype(w_dtype, [&](auto *t) {
             using E = std::remove_pointer_t<decltype(t)>;
-            return launch_reduce<E>(static_cast<const float *>(workspace), blocks, H, static_cast<E *>(dweight), static_cast<E *>(dbias), s);
+            return launch_reduce<E>(part, H, static_cast<E *>(dweight), static_cast<E *>(dbias), s);
         });
         return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     }

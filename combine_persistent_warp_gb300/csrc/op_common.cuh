@@ -80,6 +80,66 @@ __device__ __forceinline__ void store_pack(T *p, const Pack<T, N> &v)
     }
 }
 
+// ------------------------------------------------------------------ rows of any alignment ----
+template <typename T>
+constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+
+// Elements that a row starts past a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ int lead_of(const T *row)
+{
+    return static_cast<int>(reinterpret_cast<uint64_t>(row) & 15) / static_cast<int>(sizeof(T));
+}
+// The aligned vector that holds p (zeros where `is` is false).  Written out, so that the loads of
+// all slots are issued without a branch between them.
+template <typename T>
+__device__ __forceinline__ uint4 load_aligned(const T *p, bool is, int ahead = 0)
+{
+    uint4 q;
+    asm volatile("{\n\t"
+                 ".reg .pred p;\n\t"
+                 "setp.ne.s32 p, %5, 0;\n\t"
+                 "mov.b32 %0, 0;\n\t"
+                 "mov.b32 %1, 0;\n\t"
+                 "mov.b32 %2, 0;\n\t"
+                 "mov.b32 %3, 0;\n\t"
+                 "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+                 "}"
+                 : "=&r"(q.x), "=&r"(q.y), "=&r"(q.z), "=&r"(q.w)
+                 : "l"((reinterpret_cast<uint64_t>(p) & ~15ull) + 16 * ahead), "r"(static_cast<int>(is)));
+    return q;
+}
+// 16 bytes at any element: the two aligned vectors that cover them, shifted.
+struct Halves {
+    uint4 lo, hi;
+};
+template <typename T>
+__device__ __forceinline__ Halves load_halves(const T *p, bool is = true)
+{
+    return {load_aligned(p, is), load_aligned(p, is, 1)};
+}
+// The 16 bytes from p on.
+template <typename T>
+__device__ __forceinline__ Pack<T, VEC<T>> shifted(const Halves &h, const T *p)
+{
+    const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uint64_t>(p));
+    const uint32_t u[8] = {h.lo.x, h.lo.y, h.lo.z, h.lo.w, h.hi.x, h.hi.y, h.hi.z, h.hi.w};
+    uint32_t v[6], x[5];
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+        v[i] = s & 8 ? u[i + 2] : u[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+        x[i] = s & 4 ? v[i + 1] : v[i];
+    union {
+        Pack<T, VEC<T>> pack;
+        uint32_t word[4];
+    } o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o.word[i] = sizeof(T) == 4 ? x[i] : __funnelshift_r(x[i], x[i + 1], 8 * (s & 2));
+    return o.pack;
+}
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll

@@ -134,28 +134,6 @@ struct PackBackward {
     __device__ __forceinline__ void zero(const RowArgs &a, int b, int blocks) const { zero_rest<T, V>(a, a.dy, b, blocks); }
 };
 
-template <typename T>
-constexpr int VEC = 16 / static_cast<int>(sizeof(T));
-
-// The aligned vector that holds p (zeros where `is` is false).  Written out, so that the loads of
-// all slots are issued without a branch between them.
-template <typename T>
-__device__ __forceinline__ uint4 load_aligned(const T *p, bool is, int ahead = 0)
-{
-    uint4 q;
-    asm volatile("{\n\t"
-                 ".reg .pred p;\n\t"
-                 "setp.ne.s32 p, %5, 0;\n\t"
-                 "mov.b32 %0, 0;\n\t"
-                 "mov.b32 %1, 0;\n\t"
-                 "mov.b32 %2, 0;\n\t"
-                 "mov.b32 %3, 0;\n\t"
-                 "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t"
-                 "}"
-                 : "=&r"(q.x), "=&r"(q.y), "=&r"(q.z), "=&r"(q.w)
-                 : "l"((reinterpret_cast<uint64_t>(p) & ~15ull) + 16 * ahead), "r"(static_cast<int>(is)));
-    return q;
-}
 
 // Vectors (or elements) of all tokens in a line; a thread takes `run` of them, a block's width apart.
 struct Line {
@@ -237,16 +215,11 @@ __global__ void __launch_bounds__(BLOCK) combine_kernel(const RowArgs a, int vec
 
 // ------------------------------------------------------------------ rows of any alignment ----
 // Where rows do not all start on 16-byte boundaries, a row is written in the aligned 16-byte
-// vectors of its own place: vector g starts at element g * V - lead(row).  Its bytes come from the
+// vectors of its own place: vector g starts at element g * V - lead_of(row).  Its bytes come from the
 // two aligned vectors of the source that cover them, shifted (the lanes' second vectors are their
 // neighbours' first, so they come from L1).  Those may hold bytes of the neighbouring rows, which
 // are not used, but none outside the matrix: a vector whose sources might leave it is moved by
 // elements.  Nothing outside a row is written.
-template <typename T>
-__device__ __forceinline__ int lead(const T *row)
-{
-    return static_cast<int>(reinterpret_cast<uint64_t>(row) & 15) / static_cast<int>(sizeof(T));
-}
 // vectors that a row of H elements may touch
 template <typename T>
 int vectors_of(int H)
@@ -268,36 +241,6 @@ int rim_of(int H)
     return (2 * VEC<T> + H - 1) / H;
 }
 
-struct Halves {
-    uint4 lo, hi;
-};
-template <typename T>
-__device__ __forceinline__ Halves load_halves(const T *p, bool is = true)
-{
-    return {load_aligned(p, is), load_aligned(p, is, 1)};
-}
-// The 16 bytes from p on.
-template <typename T>
-__device__ __forceinline__ Pack<T, VEC<T>> shifted(const Halves &h, const T *p)
-{
-    const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uint64_t>(p));
-    const uint32_t u[8] = {h.lo.x, h.lo.y, h.lo.z, h.lo.w, h.hi.x, h.hi.y, h.hi.z, h.hi.w};
-    uint32_t v[6], x[5];
-#pragma unroll
-    for (int i = 0; i < 6; ++i)
-        v[i] = s & 8 ? u[i + 2] : u[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i)
-        x[i] = s & 4 ? v[i + 1] : v[i];
-    union {
-        Pack<T, VEC<T>> pack;
-        uint32_t word[4];
-    } o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        o.word[i] = sizeof(T) == 4 ? x[i] : __funnelshift_r(x[i], x[i + 1], 8 * (s & 2));
-    return o.pack;
-}
 // Elements e .. e + V - 1 of a row one by one, zeros outside it.
 template <typename T>
 __device__ __forceinline__ Pack<T, VEC<T>> load_elements(const T *row, int e, int H)
@@ -335,7 +278,7 @@ __device__ __forceinline__ void zero_rest_shifted(const RowArgs &a, void *out, i
     for (int r = first + b; r < a.M; r += blocks) {
         T *o = static_cast<T *>(out) + static_cast<size_t>(r) * a.H;
         for (int g = threadIdx.x; g < vectors; g += blockDim.x)
-            store_vector<T>(o, g * V - lead(o), a.H, z);
+            store_vector<T>(o, g * V - lead_of(o), a.H, z);
     }
 }
 
@@ -362,7 +305,7 @@ __global__ void __launch_bounds__(BLOCK) gather_shifted_kernel(const RowArgs a, 
         for (int i = 0; i < FEW_SLOTS; ++i)
             if (r[i] >= 0) {
                 T *o = static_cast<T *>(a.out) + static_cast<size_t>(r[i]) * a.H;
-                const int e = l.g * V - lead(o);
+                const int e = l.g * V - lead_of(o);
                 store_vector<T>(o, e, a.H, in ? shifted(load_halves(x + e), x + e) : load_elements(x, e, a.H));
             }
     }
@@ -376,7 +319,7 @@ __global__ void __launch_bounds__(BLOCK) combine_shifted_kernel(const RowArgs a,
     Line l = line_start(vectors, run);
     for (int n = 0; n < run && l.t < a.T; ++n, line_step(l, vectors)) {
         T *out = static_cast<T *>(a.out) + static_cast<size_t>(l.t) * a.H;
-        const int e = l.g * V - lead(out);
+        const int e = l.g * V - lead_of(out);
         int r[FEW_SLOTS];
         float w[FEW_SLOTS];
         float acc[V];
@@ -440,7 +383,7 @@ struct ShiftedBackward {
         int e[FEW_SLOTS];
 #pragma unroll
         for (int i = 0; i < FEW_SLOTS; ++i) {
-            e[i] = g * V - lead(dy + static_cast<long long>(r[i]) * a.H);
+            e[i] = g * V - lead_of(dy + static_cast<long long>(r[i]) * a.H);
             in = in && (r[i] < 0 || amid(r[i], a.M, a.rim));
         }
         if (in || inside<T>(g, a.H)) {

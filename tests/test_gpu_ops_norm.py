@@ -101,6 +101,29 @@ def test_every_block_size_of_the_persistent_kernels_launches(T, H):
         assert sf.isfinite().all() and (q.view(torch.float8_e4m3fn).float().abs().amax(1) <= 448).all()
 
 
+@pytest.mark.parametrize("dtype,wdtype", [(torch.bfloat16, torch.bfloat16), (torch.float16, torch.float32), (torch.float32, torch.float32)])
+@pytest.mark.parametrize("T,H,pitch,woff", [(5003, 1025, 1025, 0), (4901, 1031, 1039, 1), (2500, 2895, 2903, 3), (1300, 4091, 4091, 0),
+                                            (1300, 8185, 8185, 5), (1250, 5004, 5012, 2), (3100, 2048, 2048, 1), (2500, 2003, 2006, 0)])
+def test_long_batches_of_rows_off_the_boundaries(T, H, pitch, woff, dtype, wdtype):
+    """Rows that lie alike in every tensor, and (the last) that do not; what lies between the rows and
+    after the last one is NaN, and one row in the middle is: no other row may show it."""
+    flat = torch.full((T * pitch,), float("nan"), device="cuda", dtype=dtype)
+    x = flat.as_strided((T, H), (pitch, 1))
+    v, g, b, dy = _inputs(T, H, dtype, wdtype)
+    x.copy_(v)
+    off = lambda t: torch.cat([t[:woff], t])[woff:]        # a vector that starts `woff` elements into its allocation
+    g, b = off(g), off(b)
+    _check_forward(x, g, b, ops.layer_norm(x, g, b))
+    _check_backward(x, g, dy)
+    clean = ops.layer_norm(x, g, b)
+    dx = ops.layer_norm_backward(dy, x, g, clean[1], clean[2])[0]
+    x[T // 2] = float("nan")
+    y, mean, rstd = ops.layer_norm(x, g, b)
+    rest = torch.arange(T, device="cuda") != T // 2
+    assert y[T // 2].isnan().all() and torch.equal(y[rest], clean[0][rest]) and torch.equal(rstd[rest], clean[2][rest])
+    assert torch.equal(ops.layer_norm_backward(dy, x, g, mean, rstd)[0][rest], dx[rest])
+
+
 def test_large_mean_keeps_the_variance():
     x, g, b, _ = _inputs(16, 4096, torch.float32, torch.float32, mean=1000.0)
     y, _, _ = ops.layer_norm(x, g, b)
