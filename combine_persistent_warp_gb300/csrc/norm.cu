@@ -417,6 +417,47 @@ __device__ __forceinline__ void from_bytes(float2 (&f)[PAIRS<1, VPT>], const uin
     }
 }
 
+// ------------------------------------------------------------------ FP8 scales ----------
+__device__ __forceinline__ float fp8_scale(float m, int pow2)
+{
+    const float sf = fmaxf(m, 1e-4f) / 448.0f;
+    if (!pow2)
+        return sf;
+    // the smallest power of two >= sf (sf is a normal number)
+    return __uint_as_float((__float_as_uint(sf) + 0x7FFFFFu) & 0xFF800000u);
+}
+// Scales of the groups that the half-warp's packs j make up, from the lanes' maxima m[j]: stored, and one
+// reciprocal r[j] a group, not a quotient an element: the product is within a few fp32 roundings of
+// the quotient, which e4m3's three bits of fraction hide.  Of four groups every lane reduces one (lane
+// bits 3 and 2 name it): 9 shuffles and one division, where four apart take 16 and 4 (16384 x 4096 bf16 54
+// us so).
+template <int VPT>
+__device__ __forceinline__ void fp8_scales(const float (&m)[VPT], float (&r)[VPT], float *sf, int t, int step, int packs, int pow2)
+{
+    constexpr uint32_t ALL = 0xFFFFFFFFu;
+    const int lane = threadIdx.x & 31;
+    float k;
+    if constexpr (VPT == 4) {
+        const bool b8 = lane & 8, b4 = lane & 4;
+        const float k0 = fmaxf(b8 ? m[2] : m[0], __shfl_xor_sync(ALL, b8 ? m[0] : m[2], 8));
+        const float k1 = fmaxf(b8 ? m[3] : m[1], __shfl_xor_sync(ALL, b8 ? m[1] : m[3], 8));
+        k = fmaxf(b4 ? k1 : k0, __shfl_xor_sync(ALL, b4 ? k0 : k1, 4));
+    } else {
+        static_assert(VPT == 1, "one group a half-warp, or four");
+        k = fmaxf(m[0], __shfl_xor_sync(ALL, m[0], 8));
+        k = fmaxf(k, __shfl_xor_sync(ALL, k, 4));
+    }
+    k = fmaxf(k, __shfl_xor_sync(ALL, k, 2));
+    k = fmaxf(k, __shfl_xor_sync(ALL, k, 1));
+    const float scale = fp8_scale(k, pow2), inverse = __fdividef(1.0f, scale);
+    const int p = t + (VPT == 4 ? (lane >> 2 & 3) * step : 0);
+    if ((lane & (VPT == 4 ? 3 : 15)) == 0 && p < packs)
+        sf[p >> 4] = scale;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+        r[j] = VPT == 4 ? __shfl_sync(ALL, inverse, (lane & 16) | j << 2) : inverse;
+}
+
 // ------------------------------------------------------------------ forward -------------
 // The row held in f (zeros past its end), its statistics and outputs; w and b: the thread's
 // columns of weight and bias.  FP8: e4m3 codes and 1x128 scales instead of y (V = 8: 16 lanes
@@ -458,35 +499,30 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, int row, int lead, b
         f[i] = fma2(mul2(f[i], both(rstd)), w[i], b[i]);
     if constexpr (FP8) {
         // packs of a group of 128 lie in one half-warp; whole groups are in or out
+        float m[VPT], r[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            m[j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 y = f[j * (V / 2) + i];
+                m[j] = fmaxf(m[j], fmaxf(fabsf(y.x), fabsf(y.y)));
+            }
+        }
+        float *sf = a.sf + static_cast<size_t>(row) * (a.H / 128);
+        fp8_scales(m, r, sf, t, step, packs, a.pow2);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const float2 *y = f + j * (V / 2);
             const int p = t + j * step;
-            float m = 0.0f;
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i)
-                m = fmaxf(m, fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1)
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            float sf = fmaxf(m, 1e-4f) / 448.0f;
-            if (a.pow2) {   // the smallest power of two >= sf (sf is a normal number)
-                const uint32_t u = __float_as_uint(sf);
-                sf = __uint_as_float((u + 0x7FFFFFu) & 0xFF800000u);
-            }
-            // one reciprocal a group, not a quotient an element: the product is within a few
-            // fp32 roundings of the quotient, which e4m3's three bits of fraction hide
-            const float2 r = both(__fdividef(1.0f, sf));
             if (p < packs) {
                 uint32_t code[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float2 lo = mul2(y[2 * h], r), hi = mul2(y[2 * h + 1], r);
+                    const float2 lo = mul2(y[2 * h], both(r[j])), hi = mul2(y[2 * h + 1], both(r[j]));
                     code[h] = ptx::cvt_e4m3x2(lo.x, lo.y) | (ptx::cvt_e4m3x2(hi.x, hi.y) << 16);
                 }
                 *reinterpret_cast<uint2 *>(a.q + static_cast<size_t>(row) * a.H + static_cast<size_t>(p) * V) = make_uint2(code[0], code[1]);
-                if ((p & 15) == 0)
-                    a.sf[static_cast<size_t>(row) * (a.H / 128) + (p >> 4)] = sf;
             }
         }
     } else {
