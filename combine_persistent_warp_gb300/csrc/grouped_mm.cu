@@ -20,8 +20,11 @@
 // writes fp32 sums of its own, which a second kernel adds in a fixed order.
 //
 // Persistent pairs of CTAs (cta_group::2; each CTA holds 128 of the 256 M rows and half of the N
-// columns' operand), roles by warp: TMA producer, UMMA issuer (the even CTA's), and four
-// epilogue warps that drain one TMEM accumulator while the other is filled.
+// columns' operand), roles by warp: TMA producer, UMMA issuer (the even CTA's), and the
+// epilogue's four warps to each of two TMEM accumulators, drained while the other is filled (the
+// weights' gradient, whose shared memory has room for four warps' stores only, has four for both).
+// With a short contraction the epilogue bounds: rows' gradient of 42000 x 3320 over 256 in 9 groups 86
+// us, 100 with four warps; without one 1% is lost (94 groups of 27 rows, 136 x 88: 9.0 us and 8.9).
 // Measured on a GB300, bf16 operands N(0,1) x N(0,0.02): 32 experts of about 1024 rows, N 4096,
 // K 7168: forward 1.22-1.25 ms back to back under the power cap (1.55 PFLOP/s; the library's batched
 // product on equal groups of 1024 rows 1.14 ms), 1.9 PFLOP/s in short bursts, the tensor pipe 86 to
@@ -51,11 +54,12 @@ constexpr int KB = 64;                 // contracted elements of a pipeline stag
 constexpr int OPER_BYTES = 128 * KB * 2;       // one operand's half in a CTA: 16 KB
 constexpr int STAGE = 2 * OPER_BYTES;
 constexpr int RING = 6;
-constexpr int THREADS = 256;
+template <bool DW>
+constexpr int THREADS = DW ? 256 : 384;   // four warps, and four of the epilogue; eight for rows (two tiles at a time)
 constexpr int MAX_E = 1024;
 constexpr uint64_t WAIT_NS = 2000000000ull;    // limit of every wait
 constexpr int STAGE_OUT = 32 * 128;    // dW: an epilogue warp's 32 rows x 128 bytes on their way out
-constexpr int ROWS_OUT = 2 * 32 * (256 + 64);   // rows of the other products on their way out
+constexpr int ROWS_OUT = 2 * 32 * (256 + 64);   // the other products: 32 rows of two tiles on their way out
 constexpr int SMEM = RING * STAGE + 1024 + ROWS_OUT;
 constexpr int SMEM_WEIGHTS = RING * STAGE + 1024 + 4 * STAGE_OUT;
 
@@ -300,16 +304,17 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, int f16)
 
 // 32 accumulator columns (rows r .. r + 31 of the tile), 128 features f0 .. f0 + 127 of a CTA, one
 // feature a lane of the four epilogue warps, into rows of out.  Neighbouring lanes swap halves of
-// a pair of rows, so that a lane holds two features of one row; the warps put their 64 bytes of
-// every row into shared memory (rows ROW_PITCH apart: conflict-free) and, behind one barrier a
-// chunk (two buffers in turn), store whole 256-byte rows with 16-byte accesses.  (Each warp
+// a pair of rows, so that a lane holds two features of one row; the four warps put their 64 bytes
+// of every row into shared memory (rows ROW_PITCH apart: conflict-free) and, behind a barrier, store
+// whole 256-byte rows with 16-byte accesses.  (Each warp
 // storing its own 64 bytes took 13,600 cycles a tile of 256 rows: 29095 x 2336 x 64 107 us.)
 constexpr int ROW_PITCH = 256 + 64;
 constexpr int ROW_BUFFER = 32 * ROW_PITCH;
 __device__ __forceinline__ void store_rows(const Args &a, const Tile &t, const uint32_t (&v)[32], int r, int f0, int quarter, int lane,
-                                           uint8_t *buf)
+                                           uint8_t *buf, int barrier)
 {
     const int odd = lane & 1;
+    asm volatile("bar.sync %0, 128;" ::"r"(barrier) : "memory");   // the chunk before has been read
 #pragma unroll
     for (int p = 0; p < 16; ++p) {
         const uint32_t own = pack2(__uint_as_float(v[2 * p]), __uint_as_float(v[2 * p + 1]), a.f16);
@@ -317,7 +322,7 @@ __device__ __forceinline__ void store_rows(const Args &a, const Tile &t, const u
         const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
         *reinterpret_cast<uint32_t *>(buf + (2 * p + odd) * ROW_PITCH + quarter * 64 + (lane >> 1) * 4) = w;
     }
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+    asm volatile("bar.sync %0, 128;" ::"r"(barrier) : "memory");
     uint16_t *out = static_cast<uint16_t *>(a.out);
     const int part = lane & 15, f = f0 + 8 * part;   // 16 lanes a row
 #pragma unroll
@@ -330,12 +335,12 @@ __device__ __forceinline__ void store_rows(const Args &a, const Tile &t, const u
 }
 
 // Whether all four epilogue warps have `ok`: they go on, or stop, together.
-__device__ __forceinline__ bool epilogue_all(bool ok)
+__device__ __forceinline__ bool epilogue_all(bool ok, int barrier)
 {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r)
-                 : "r"(static_cast<uint32_t>(ok))
+                 : "r"(static_cast<uint32_t>(ok)), "r"(barrier)
                  : "memory");
     return r != 0;
 }
@@ -357,18 +362,28 @@ __device__ __forceinline__ void store_part(const Args &a, const Tile &t, const u
 // writes whole lines and drops what lies outside [F][R]; in 32 bits the accumulating form is a
 // TMA reduction, so the old values are not read by the SM.  (Each lane storing 16 bytes of its
 // own row took 12,000 cycles a tile, more than the 8192 of a 1024-row group's products.)
-template <bool F32, bool ZERO>
+__device__ __forceinline__ void send_weights(const Args &a, const CUtensorMap *map, const Tile &t, const uint8_t *buf, int c, int n0, bool add)
+{
+    if (add)
+        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"(ptx::smem_u32(buf)), "r"(t.r0 + c), "r"(n0), "r"(t.part * a.E + t.e)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"(ptx::smem_u32(buf)), "r"(t.r0 + c), "r"(n0), "r"(t.part * a.E + t.e)
+                     : "memory");
+    ptx::bulk_commit();
+}
+template <bool F32>
 __device__ __forceinline__ void store_weights(const Args &a, const CUtensorMap *map, const Tile &t, uint32_t src, uint8_t *buf,
                                               int n0, int lane)
 {
     constexpr int COLS = F32 ? 32 : 64;   // columns of 128 bytes
     for (int c = 0; c < t.rows; c += COLS) {
         uint32_t w[32];
-        if (ZERO) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                w[i] = 0;
-        } else if (F32) {
+        if (F32) {
             ptx::tmem_ld32(src + c, w);
             ptx::tmem_ld_wait(w);
         } else {
@@ -392,20 +407,25 @@ __device__ __forceinline__ void store_weights(const Args &a, const CUtensorMap *
                 make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) {
-            if (F32 && a.accumulate)
-                asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                                 reinterpret_cast<uint64_t>(map)),
-                             "r"(ptx::smem_u32(buf)), "r"(t.r0 + c), "r"(n0), "r"(t.part * a.E + t.e)
-                             : "memory");
-            else
-                asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                                 reinterpret_cast<uint64_t>(map)),
-                             "r"(ptx::smem_u32(buf)), "r"(t.r0 + c), "r"(n0), "r"(t.part * a.E + t.e)
-                             : "memory");
-            ptx::bulk_commit();
-        }
+        if (lane == 0)
+            send_weights(a, map, t, buf, c, n0, F32 && a.accumulate);
     }
+}
+// Zeros for an empty group's rows: one buffer of them feeds all the stores.
+__device__ __forceinline__ void store_zeros(const Args &a, const CUtensorMap *map, const Tile &t, uint8_t *buf, int n0, int lane)
+{
+    if (lane == 0)
+        ptx::bulk_wait_read<0>();
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<uint4 *>(buf + (q * 32 + lane) * 16) = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    const int cols = a.out32 ? 32 : 64;
+    if (lane == 0)
+        for (int c = 0; c < t.rows; c += cols)
+            send_weights(a, map, t, buf, c, n0, false);
 }
 
 // The accumulating form in 16 bits: 32 columns of this lane's row n, added in fp32 and rounded
@@ -432,7 +452,7 @@ __device__ __forceinline__ void add_weights16(const Args &a, const Tile &t, cons
 }
 
 template <Kind KIND>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<KIND == WEIGHTS>, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ MapsB maps_b,
                    const __grid_constant__ CUtensorMap map_out, const Args a)
 {
@@ -652,7 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
     } else if (warp >= 4) {
         // -------------------------------------------------------------------- epilogue ----
-        const int quarter = warp - 4;
+        const int quarter = warp & 3, group = (warp >> 2) - 1;
         if (KIND != WEIGHTS && a.splits == 1) {
             // rows that belong to no expert: zero (before the first one only if offsets[0] > 0)
             uint32_t *out = static_cast<uint32_t *>(a.out);
@@ -660,7 +680,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const int lo = s.off[0], hi = s.off[a.E];
             for (int i = blockIdx.x; i < lo + a.M - hi; i += gridDim.x) {
                 const int row = i < lo ? i : hi + i - lo;
-                for (int w = threadIdx.x - 128; w < words; w += 128)
+                for (int w = threadIdx.x - 128; w < words; w += blockDim.x - 128)
                     out[(static_cast<size_t>(row) * a.ldo >> 1) + w] = 0;
             }
         }
@@ -669,21 +689,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         uint8_t *buf = ring + RING * STAGE + quarter * STAGE_OUT;   // WEIGHTS
-        int flip = 0;
         while (ok && list.next(t)) {
             const int f0 = t.f0 + static_cast<int>(rank) * 128 + quarter * 32;
             if (KIND == WEIGHTS && t.blocks == 0) {
-                if (!a.accumulate && f0 < a.F) {
-                    if (a.out32)
-                        store_weights<true, true>(a, &map_out, t, 0, buf, f0, lane);
-                    else
-                        store_weights<false, true>(a, &map_out, t, 0, buf, f0, lane);
-                }
+                if (!a.accumulate && f0 < a.F)
+                    store_zeros(a, &map_out, t, buf, f0, lane);
+                continue;
+            }
+            if (KIND != WEIGHTS && acc != group) {   // the other group's accumulator
+                acc ^= 1;
+                if (acc == 0)
+                    acc_phase ^= 1;
                 continue;
             }
             ok = __all_sync(0xFFFFFFFFu, wait_phase(&s.acc_full[acc], acc_phase));
             if (KIND != WEIGHTS)
-                ok = epilogue_all(ok);   // store_rows' barriers need all four warps
+                ok = epilogue_all(ok, 1 + group);   // store_rows' barriers need all four warps
             if (!ok)
                 break;
             ptx::tc_fence_after();
@@ -691,9 +712,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (KIND == WEIGHTS && (a.out32 || !a.accumulate)) {
                 if (f0 < a.F) {
                     if (a.out32)
-                        store_weights<true, false>(a, &map_out, t, src, buf, f0, lane);
+                        store_weights<true>(a, &map_out, t, src, buf, f0, lane);
                     else
-                        store_weights<false, false>(a, &map_out, t, src, buf, f0, lane);
+                        store_weights<false>(a, &map_out, t, src, buf, f0, lane);
+                }
+            } else if (KIND != WEIGHTS && a.splits > 1) {
+                // two chunks' registers: a load need not wait for the stores of the chunk before it
+                // (850 rows, 5 experts, 128 x 1480: 9.9 us, 13.7 with one)
+                uint32_t v[2][32];
+                ptx::tmem_ld32(src, v[0]);
+                for (int c = 0; c < t.rows; c += 64) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int at = c + 32 * h;
+                        if (at >= t.rows)
+                            break;
+                        ptx::tmem_ld_wait(v[h]);
+                        if (at + 32 < t.rows)
+                            ptx::tmem_ld32(src + at + 32, v[h ^ 1]);
+                        store_part(a, t, v[h], at, f0 + lane);
+                    }
                 }
             } else {
                 for (int c = 0; c < t.rows; c += 32) {
@@ -702,12 +740,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     ptx::tmem_ld_wait(v);
                     if (KIND == WEIGHTS)
                         add_weights16(a, t, v, c, f0 + lane);
-                    else if (a.splits > 1)
-                        store_part(a, t, v, c, f0 + lane);
-                    else {
-                        store_rows(a, t, v, c, f0 - quarter * 32, quarter, lane, ring + RING * STAGE + flip);
-                        flip ^= ROW_BUFFER;   // (goes on over the tiles: a warp may be one chunk ahead)
-                    }
+                    else
+                        store_rows(a, t, v, c, f0 - quarter * 32, quarter, lane, ring + RING * STAGE + group * ROW_BUFFER, 1 + group);
                 }
             }
             ptx::tc_fence_before();
@@ -869,7 +903,7 @@ int launch_grouped(const CUtensorMap &ma, const MapsB &mb, const CUtensorMap &mo
     constexpr int smem = KIND == WEIGHTS ? SMEM_WEIGHTS : SMEM;
     if (ensure_max_dynamic_smem(reinterpret_cast<const void *>(kern), smem) != cudaSuccess)
         return MOE_ERR_CUDA;
-    return launch_programmatic(kern, sms / 2 * 2, THREADS, smem, s, ma, mb, mo, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return launch_programmatic(kern, sms / 2 * 2, THREADS<KIND == WEIGHTS>, smem, s, ma, mb, mo, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 bool grouped_sizes_ok(int64_t M, int E, int N, int K, int dtype)
