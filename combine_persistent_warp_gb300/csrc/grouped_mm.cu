@@ -915,7 +915,7 @@ bool grouped_sizes_ok(int64_t M, int E, int N, int K, int dtype)
 // Parts of the contraction: as many as the idle pairs allow, with at least four stages each, and
 // only where the stages saved (0.3 us each) outweigh the second launch (3 us) and the traffic of the
 // parts (`out` elements of fp32 each, written and read at 4 TB/s).  Measured, split and not: 16
-// rows, one expert, 256 x 7168 10.5 and 25.3 us; 64 rows, 8 experts, 256 x 4096 8.9 and 16.3;
+// rows, one expert, 256 x 7168 9.9 and 25.3 us; 64 rows, 8 experts, 256 x 4096 8.9 and 16.3;
 // weights' gradient of 16384 rows, 4 experts, 512 x 512 17.6 and 24.1; 400 rows, 2 experts, 2048 x
 // 1024 (not split) 15.1 and 10.1.
 int split_count(long long tiles, long long blocks, double out, int sms)

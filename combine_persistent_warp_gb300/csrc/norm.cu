@@ -9,8 +9,8 @@
 // statistic and sum is held in fp32.
 //
 // Measured on a GB300, bf16: 16384 x 4096 forward 45 us, backward 72 us (HBM floors 40 and 60 us
-// at the measured copy bandwidth), FP8 form 54 us (floor 30: its group maxima and conversions
-// are bound by issue); 128 x 7168 FP8 form 2.9 us in a graph; 4099 x 1001 fp32 9 and 13 us; 8939 x 2895
+// at the measured copy bandwidth), FP8 form 48 us (floor 30: its group maxima and conversions
+// take issue slots); 128 x 7168 FP8 form 2.9 us in a graph; 4099 x 1001 fp32 9 and 13 us; 8939 x 2895
 // fp16, rows off 16-byte boundaries, 29 and 45 (2896: 20 and 39; floors 16 and 23).
 //
 // Long batches run in persistent blocks that keep the next rows on their way: every thread
