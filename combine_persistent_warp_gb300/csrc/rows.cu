@@ -134,7 +134,6 @@ struct PackBackward {
     __device__ __forceinline__ void zero(const RowArgs &a, int b, int blocks) const { zero_rest<T, V>(a, a.dy, b, blocks); }
 };
 
-
 // Vectors (or elements) of all tokens in a line; a thread takes `run` of them, a block's width apart.
 struct Line {
     int t, g;
