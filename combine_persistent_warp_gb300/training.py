@@ -30,7 +30,8 @@ class _LayerNorm(Function):
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         dx, dweight, dbias = ops.layer_norm_backward(_rows(dy), x, weight, mean, rstd)
-        return dx, dweight, dbias, None
+        _, weight_grad, bias_grad, _ = ctx.needs_input_grad   # (False for None, which may have no gradient)
+        return dx, dweight if weight_grad else None, dbias if bias_grad else None, None
 
 
 class _RouteTopk(Function):
@@ -73,7 +74,7 @@ class _CombineRows(Function):
     def backward(ctx, dout):
         y, rows, w, offsets = ctx.saved_tensors
         dy, dw = ops.combine_rows_backward(_rows(dout), y, rows, w, offsets)
-        return dy, None, dw, None
+        return dy, None, dw if ctx.needs_input_grad[2] else None, None
 
 
 class _GroupedMM(Function):

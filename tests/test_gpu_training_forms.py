@@ -1,0 +1,40 @@
+"""The autograd functions on the GPU in the forms that the operators document: parameters that are absent."""
+import pytest
+import torch
+
+from combine_persistent_warp_gb300 import ops, training
+
+pytestmark = pytest.mark.gpu
+
+
+def _order(T, k, E, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return ops.expert_order(torch.randint(-1, E, (T, k), generator=g, device="cuda"), E)
+
+
+@pytest.mark.parametrize("with_weight", [True, False])
+@pytest.mark.parametrize("with_bias", [True, False])
+def test_layer_norm_without_weight_or_bias(with_weight, with_bias):
+    # fp32 sums of 64 and 33 terms: a few dozen roundings of 2^-24 on values of up to about 30
+    torch.manual_seed(0)
+    x = torch.randn(33, 64, device="cuda", requires_grad=True)
+    g = torch.randn(64, device="cuda", requires_grad=True) if with_weight else None
+    b = torch.randn(64, device="cuda", requires_grad=True) if with_bias else None
+    dy = torch.randn(33, 64, device="cuda")
+    training.layer_norm(x, g, b).backward(dy)
+    want = [t.detach().double().requires_grad_() if t is not None else None for t in (x, g, b)]
+    torch.nn.functional.layer_norm(want[0], (64,), want[1], want[2]).backward(dy.double())
+    for got, ref in zip((x, g, b), want):
+        if got is not None:
+            assert (got.grad - ref.grad).abs().max() <= 1e-4
+
+
+def test_combine_without_gate_weights():
+    o = _order(20, 3, 4)
+    y = torch.randn(60, 24, device="cuda", requires_grad=True)
+    dout = torch.randn(20, 24, device="cuda")
+    training.combine_rows(y, o, None).backward(dout)
+    want = torch.zeros(60, 24, device="cuda")
+    named = o.rows >= 0
+    want[o.rows[named].long()] = dout[named.nonzero()[:, 0]]
+    assert torch.equal(y.grad, want)

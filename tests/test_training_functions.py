@@ -1,0 +1,76 @@
+"""The autograd functions of `training` around stand-ins of the operators on the CPU: which gradients they
+return, of which type, and what they hand to the operators."""
+import pytest
+import torch
+
+from combine_persistent_warp_gb300 import ops, training
+
+
+def _layer_norm(x, weight=None, bias=None, eps=1e-5):
+    f = x.float()
+    mean = f.mean(1)
+    rstd = (f.var(1, unbiased=False) + eps).rsqrt()
+    y = (f - mean[:, None]) * rstd[:, None]
+    y = y * weight.float() if weight is not None else y
+    return (y + bias.float() if bias is not None else y).to(x.dtype), mean, rstd
+
+
+def _layer_norm_backward(dy, x, weight, mean, rstd, *, param_dtype=None, **_):
+    xh = (x.float() - mean[:, None]) * rstd[:, None]
+    d = dy.float()
+    g = d * weight.float() if weight is not None else d
+    dx = (g - g.mean(1, keepdim=True) - xh * (g * xh).mean(1, keepdim=True)) * rstd[:, None]
+    to = weight.dtype if weight is not None else param_dtype or x.dtype
+    return dx.to(x.dtype), (d * xh).sum(0).to(to), d.sum(0).to(to)
+
+
+def _combine_rows(y, rows, w=None):
+    v = y[rows.clamp_min(0).long()].float() * (w if w is not None else torch.ones(rows.shape))[:, :, None]
+    return torch.where((rows < 0)[:, :, None], 0.0, v).sum(1).to(y.dtype)
+
+
+def _combine_rows_backward(dout, y, rows, w, offsets, **_):
+    named = rows >= 0
+    at = rows[named].long()
+    weights = w if w is not None else torch.ones(rows.shape)
+    dy = torch.zeros_like(y, dtype=torch.float32)
+    dy[at] = (weights[:, :, None] * dout.float()[:, None])[named]
+    dw = torch.zeros(rows.shape)
+    dw[named] = (y[at].float() * dout.float()[named.nonzero()[:, 0]]).sum(1)
+    return dy.to(y.dtype), dw
+
+
+@pytest.fixture(autouse=True)
+def stand_ins(monkeypatch):
+    for f in (_layer_norm, _layer_norm_backward, _combine_rows, _combine_rows_backward):
+        monkeypatch.setattr(ops, f.__name__[1:], f)
+
+
+ORDER = ops.ExpertOrder(torch.tensor([0, 2, 5], dtype=torch.int32), torch.tensor([[0, 2], [1, -1], [3, 4]], dtype=torch.int32),
+                        torch.zeros(1, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("with_weight", [True, False])
+@pytest.mark.parametrize("with_bias", [True, False])
+def test_layer_norm_without_weight_or_bias(with_weight, with_bias):
+    torch.manual_seed(0)
+    x = torch.randn(5, 16, requires_grad=True)
+    g = torch.randn(16, requires_grad=True) if with_weight else None
+    b = torch.randn(16, requires_grad=True) if with_bias else None
+    dy = torch.randn(5, 16)
+    training.layer_norm(x, g, b).backward(dy)
+    want = [t.detach().clone().requires_grad_() if t is not None else None for t in (x, g, b)]
+    torch.nn.functional.layer_norm(want[0], (16,), want[1], want[2]).backward(dy)
+    for got, ref in zip((x, g, b), want):
+        if got is not None:
+            assert (got.grad - ref.grad).abs().max() <= 1e-5
+
+
+def test_combine_without_gate_weights():
+    y = torch.randn(6, 8, requires_grad=True)
+    dout = torch.randn(3, 8)
+    training.combine_rows(y, ORDER, None).backward(dout)
+    want = torch.zeros(6, 8)
+    for t, j in ORDER.rows.ge(0).nonzero().tolist():
+        want[ORDER.rows[t, j]] = dout[t]
+    assert torch.equal(y.grad, want)
