@@ -23,13 +23,14 @@ class _LayerNorm(Function):
     def forward(ctx, x, weight, bias, eps):
         y, mean, rstd = ops.layer_norm(x, weight, bias, eps)
         ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.bias_dtype = bias.dtype if bias is not None else None
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
-        dx, dweight, dbias = ops.layer_norm_backward(_rows(dy), x, weight, mean, rstd)
+        dx, dweight, dbias = ops.layer_norm_backward(_rows(dy), x, weight, mean, rstd, param_dtype=ctx.bias_dtype)
         _, weight_grad, bias_grad, _ = ctx.needs_input_grad   # (False for None, which may have no gradient)
         return dx, dweight if weight_grad else None, dbias if bias_grad else None, None
 

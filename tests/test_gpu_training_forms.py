@@ -38,3 +38,14 @@ def test_combine_without_gate_weights():
     named = o.rows >= 0
     want[o.rows[named].long()] = dout[named.nonzero()[:, 0]]
     assert torch.equal(y.grad, want)
+
+
+def test_a_bias_in_fp32_without_a_weight():
+    torch.manual_seed(3)
+    x = torch.randn(40, 64, device="cuda").bfloat16()
+    b = torch.randn(64, device="cuda", requires_grad=True)
+    dy = torch.randn(40, 64, device="cuda").bfloat16()
+    training.layer_norm(x, None, b).backward(dy)
+    assert b.grad.dtype == torch.float32
+    # a 40-term sum in fp32, not a bf16 of it
+    assert ((b.grad - dy.double().sum(0)).abs() <= 40 * 2.0 ** -24 * dy.double().abs().sum(0)).all()

@@ -74,3 +74,12 @@ def test_combine_without_gate_weights():
     for t, j in ORDER.rows.ge(0).nonzero().tolist():
         want[ORDER.rows[t, j]] = dout[t]
     assert torch.equal(y.grad, want)
+
+
+def test_a_bias_in_fp32_without_a_weight_keeps_its_gradients_bits():
+    torch.manual_seed(3)
+    x = torch.randn(7, 16).bfloat16()
+    b = torch.zeros(16, requires_grad=True)
+    dy = torch.randn(7, 16).bfloat16()
+    training.layer_norm(x, None, b).backward(dy)
+    assert torch.equal(b.grad, dy.float().sum(0))       # not rounded to x's type on its way
