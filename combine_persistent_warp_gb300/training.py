@@ -95,10 +95,16 @@ class _GroupedMM(Function):
 
 
 def _rows(t):
-    """A gradient as the operators take matrices: rows that are contiguous, apart from each other and
-    on 16-byte boundaries (autograd hands over expanded or transposed ones, of a sum for instance)."""
-    ok = t.stride(1) == 1 and t.stride(0) >= t.shape[1] and (t.stride(0) * t.element_size()) % 16 == 0 and t.data_ptr() % 16 == 0
-    return t if ok else t.contiguous()
+    """A gradient as the operators take matrices: rows that are contiguous, apart from each other and,
+    where their width allows it, on 16-byte boundaries (autograd hands over expanded or transposed
+    ones, of a sum for instance, and pieces of others that start anywhere)."""
+    size = t.element_size()
+    if t.stride(1) == 1 and t.stride(0) >= t.shape[1] and (t.stride(0) * size) % 16 == 0 and t.data_ptr() % 16 == 0:
+        return t
+    if t.is_contiguous() and (t.shape[1] * size) % 16 != 0:
+        return t
+    # (contiguous() gives a contiguous tensor back as it is, wherever it starts)
+    return t.clone(memory_format=torch.contiguous_format)
 
 
 def layer_norm(x, weight, bias, eps: float = 1e-5):

@@ -49,3 +49,23 @@ def test_a_bias_in_fp32_without_a_weight():
     assert b.grad.dtype == torch.float32
     # a 40-term sum in fp32, not a bf16 of it
     assert ((b.grad - dy.double().sum(0)).abs() <= 40 * 2.0 ** -24 * dy.double().abs().sum(0)).all()
+
+
+@pytest.mark.parametrize("rows", [1, 5])
+def test_gradients_that_start_anywhere(rows):
+    """The gradient of y in torch.cat([s, y.view(-1)]) is contiguous and starts behind s."""
+    torch.manual_seed(4)
+    off = torch.tensor([0, rows // 2, rows], dtype=torch.int32, device="cuda")
+    x = torch.randn(rows, 64, device="cuda").bfloat16().requires_grad_()
+    w = torch.randn(2, 72, 64, device="cuda").bfloat16().requires_grad_()
+    y = training.grouped_mm(x, w, off)
+    d = torch.randn(rows * 72 + 3, device="cuda").bfloat16()
+    torch.cat([torch.zeros(3, device="cuda", dtype=torch.bfloat16), y.view(-1)]).backward(d)
+    dy = d[3:].clone().view(rows, 72)
+    assert torch.equal(x.grad, ops.grouped_mm_dx(dy, w.detach(), off))
+    assert torch.equal(w.grad, ops.grouped_mm_dw(dy, x.detach(), off))
+    # a part of a wider gradient
+    x.grad = None
+    wide = torch.randn(rows, 77, device="cuda").bfloat16()
+    training.grouped_mm(x, w, off).backward(wide[:, 5:])
+    assert torch.equal(x.grad, ops.grouped_mm_dx(wide[:, 5:].clone(), w.detach(), off))

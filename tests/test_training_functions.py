@@ -83,3 +83,30 @@ def test_a_bias_in_fp32_without_a_weight_keeps_its_gradients_bits():
     dy = torch.randn(7, 16).bfloat16()
     training.layer_norm(x, None, b).backward(dy)
     assert torch.equal(b.grad, dy.float().sum(0))       # not rounded to x's type on its way
+
+
+def _views():
+    flat = torch.arange(3 + 4 * 64, dtype=torch.float32).bfloat16()
+    wide = torch.randn(5, 67).bfloat16()
+    return {"contiguous off a 16-byte boundary": flat[3:].view(4, 64), "one row of an odd stride": wide[:1, :64],
+            "one row inside a row": wide[2:3, 3:67], "expanded": flat[:1].expand(4, 64), "transposed": torch.randn(64, 4).bfloat16().t(),
+            "odd stride": wide[:, :64]}
+
+
+@pytest.mark.parametrize("kind", _views())
+def test_gradients_reach_the_operators_on_16_byte_boundaries(kind):
+    t = _views()[kind]
+    r = training._rows(t)
+    assert torch.equal(r, t) or t.isnan().any()
+    assert r.data_ptr() % 16 == 0 and r.stride(1) == 1 and r.stride(0) >= r.shape[1] and r.stride(0) * r.element_size() % 16 == 0
+
+
+def test_gradients_that_fit_are_not_copied():
+    t = torch.randn(4, 64).bfloat16()
+    assert training._rows(t) is t
+
+
+def test_rows_of_an_odd_width_are_not_copied():
+    """No copy puts them on 16-byte boundaries, and what has such rows takes them as they are."""
+    for t in (torch.randn(4, 33).bfloat16(), torch.arange(3 + 4 * 33).bfloat16()[3:].view(4, 33)):
+        assert training._rows(t) is t
