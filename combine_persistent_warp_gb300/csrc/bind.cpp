@@ -120,7 +120,8 @@ Matrix matrix(const at::Tensor &t, const char *name, const First &f, int64_t row
         throw ValueErr(std::string(name) + ": the elements of a row must be contiguous");
     if (n > 1 && ld < w)
         throw ValueErr(std::string(name) + ": rows must not overlap");
-    return {n, w, n > 1 ? ld : std::max<int64_t>({ld, w, 1}), t.data_ptr()};
+    // (the stride of a single row is never used and may be anything)
+    return {n, w, n > 1 ? ld : std::max<int64_t>(w, 1), t.data_ptr()};
 }
 
 // A contiguous tensor of the given shape.

@@ -1,0 +1,25 @@
+"""What the operators' Python entry points take and refuse on the GPU."""
+import pytest
+import torch
+
+from combine_persistent_warp_gb300 import ops
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("rows", [0, 1])
+def test_the_stride_of_a_single_row_may_be_anything(rows):
+    torch.manual_seed(0)
+    base = torch.randn(3, 67 * 128 + 3, device="cuda").bfloat16()
+    x, dy = base[:rows, :256], base[1:1 + rows, 5:5 + 128].clone().as_strided((rows, 128), (131, 1))
+    assert rows == 0 or x.stride(0) % 8 and dy.stride(0) % 8
+    w = torch.randn(2, 128, 256, device="cuda").bfloat16()
+    off = torch.tensor([0, 0, rows], dtype=torch.int32, device="cuda")
+    plain = lambda t: t.clone(memory_format=torch.contiguous_format)
+    assert torch.equal(ops.grouped_mm(x, w, off), ops.grouped_mm(plain(x), w, off))
+    assert torch.equal(ops.grouped_mm_dx(dy, w, off), ops.grouped_mm_dx(plain(dy), w, off))
+    assert torch.equal(ops.grouped_mm_dw(dy, x, off), ops.grouped_mm_dw(plain(dy), plain(x), off))
+    out = torch.zeros(3, 131, device="cuda").bfloat16()[:rows, :128]
+    assert torch.equal(ops.grouped_mm(x, w, off, out=out), ops.grouped_mm(plain(x), w, off))
+    for a, b in zip(ops.layer_norm_fp8(x), ops.layer_norm_fp8(plain(x))):
+        assert torch.equal(a, b)
