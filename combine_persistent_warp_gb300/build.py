@@ -30,7 +30,7 @@ def _nvcc():
 
 
 def _deps():
-    return (glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
+    return (glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
             [os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "cpw_moe.h"), __file__])
 
 

@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "op_common.cuh"
+#include "rows_index.h"
 
 using namespace cpw;
 
@@ -93,8 +94,7 @@ template <typename T, int V>
 __device__ __forceinline__ void zero_rest(const RowArgs &a, void *out, int b, int blocks)
 {
     const int packs = a.H / V;
-    int first = *a.total;
-    first = first < 0 ? 0 : first;
+    const int first = rest_begin(*a.total, a.M);
     Pack<T, V> z;
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -219,26 +219,6 @@ __global__ void __launch_bounds__(BLOCK) combine_kernel(const RowArgs a, int vec
 // neighbours' first, so they come from L1).  Those may hold bytes of the neighbouring rows, which
 // are not used, but none outside the matrix: a vector whose sources might leave it is moved by
 // elements.  Nothing outside a row is written.
-// vectors that a row of H elements may touch
-template <typename T>
-int vectors_of(int H)
-{
-    return (H + VEC<T> - 1 + VEC<T> - 1) / VEC<T>;
-}
-// The aligned vectors of elements e .. e + V - 1 of a row lie inside the row, for every e that
-// vector g has whatever the row's lead.
-template <typename T>
-__device__ __forceinline__ bool inside(int g, int H)
-{
-    return g >= 2 && (g + 2) * VEC<T> <= H;
-}
-// Row r of `rows` has 2 * V elements of its matrix before and after it (rim: rows that hold them).
-__device__ __forceinline__ bool amid(int r, int rows, int rim) { return r >= rim && r < rows - rim; }
-template <typename T>
-int rim_of(int H)
-{
-    return (2 * VEC<T> + H - 1) / H;
-}
 
 // Elements e .. e + V - 1 of a row one by one, zeros outside it.
 template <typename T>
@@ -268,8 +248,7 @@ template <typename T>
 __device__ __forceinline__ void zero_rest_shifted(const RowArgs &a, void *out, int vectors, int b, int blocks)
 {
     constexpr int V = VEC<T>;
-    int first = *a.total;
-    first = first < 0 ? 0 : first;
+    const int first = rest_begin(*a.total, a.M);
     Pack<T, V> z;
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -293,7 +272,7 @@ __global__ void __launch_bounds__(BLOCK) gather_shifted_kernel(const RowArgs a, 
     if (l.t >= a.T)
         return;
     const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(l.t) * a.ldx;
-    const bool in = inside<T>(l.g, a.H) || amid(l.t, a.T, a.rim);
+    const bool in = inside(l.g, a.H, VEC<T>) || amid(l.t, a.T, a.rim);
     for (int j0 = 0; j0 < a.k; j0 += FEW_SLOTS) {
         int r[FEW_SLOTS];
         float w[FEW_SLOTS];
@@ -332,7 +311,7 @@ __global__ void __launch_bounds__(BLOCK) combine_shifted_kernel(const RowArgs a,
                 slot_of(a, l.t, j0 + i, r[i], w[i]);
                 in = in && (r[i] < 0 || amid(r[i], a.M, a.rim));
             }
-            if (in || inside<T>(l.g, a.H)) {
+            if (in || inside(l.g, a.H, VEC<T>)) {
                 Halves h[FEW_SLOTS];
 #pragma unroll
                 for (int i = 0; i < FEW_SLOTS; ++i)
@@ -385,7 +364,7 @@ struct ShiftedBackward {
             e[i] = g * V - lead_of(dy + static_cast<long long>(r[i]) * a.H);
             in = in && (r[i] < 0 || amid(r[i], a.M, a.rim));
         }
-        if (in || inside<T>(g, a.H)) {
+        if (in || inside(g, a.H, VEC<T>)) {
             uint4 lo[FEW_SLOTS], hi[SAME ? 1 : FEW_SLOTS];
 #pragma unroll
             for (int i = 0; i < FEW_SLOTS; ++i) {
@@ -609,8 +588,8 @@ int moe_gather_rows(int T, int topk, int H, int E, int64_t M, const void *x, int
             gather_kernel<Ty, 1><<<blocks + sms, BLOCK, 0, st>>>(a, H, blocks);
             return;
         }
-        a.rim = rim_of<Ty>(H);
-        const int vectors = vectors_of<Ty>(H), blocks = blocks_of(T, vectors, 1);
+        a.rim = rim_of(H, VEC<Ty>);
+        const int vectors = vectors_of(H, VEC<Ty>), blocks = blocks_of(T, vectors, 1);
         gather_shifted_kernel<Ty><<<blocks + sms, BLOCK, 0, st>>>(a, vectors, blocks);
     });
 }
@@ -637,8 +616,8 @@ int moe_combine_rows(int T, int topk, int H, int64_t M, const void *y, int dtype
             combine_kernel<Ty, SLOTS><<<blocks, BLOCK, 0, st>>>(a, vectors, run);
     }, [&](auto *t) {
         using Ty = std::remove_pointer_t<decltype(t)>;
-        a.rim = rim_of<Ty>(H);
-        const int vectors = vectors_of<Ty>(H), run = run_of(T, vectors, sms);
+        a.rim = rim_of(H, VEC<Ty>);
+        const int vectors = vectors_of(H, VEC<Ty>), run = run_of(T, vectors, sms);
         combine_shifted_kernel<Ty><<<blocks_of(T, vectors, run), BLOCK, 0, st>>>(a, vectors, run);
     });
 }
@@ -666,15 +645,15 @@ int moe_combine_rows_backward(int T, int topk, int H, int E, int64_t M, const vo
             launch_backward<Ty>(a, PackBackward<Ty, VEC<Ty>, SLOTS>{H / VEC<Ty>}, sms, st);
     }, [&](auto *t) {
         using Ty = std::remove_pointer_t<decltype(t)>;
-        a.rim = rim_of<Ty>(H);
+        a.rim = rim_of(H, VEC<Ty>);
         if (H <= NARROW_ELEMENTS && topk <= FEW_SLOTS)
             launch_warps<Ty>(a, PackBackward<Ty, 1, FEW_SLOTS>{H}, sms, st);
         else if (H <= NARROW_ELEMENTS)
             launch_warps<Ty>(a, PackBackward<Ty, 1, SLOTS>{H}, sms, st);
         else if (op_aligned(reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(dy)), 16))
-            launch_backward<Ty>(a, ShiftedBackward<Ty, true>{vectors_of<Ty>(H)}, sms, st);
+            launch_backward<Ty>(a, ShiftedBackward<Ty, true>{vectors_of(H, VEC<Ty>)}, sms, st);
         else
-            launch_backward<Ty>(a, ShiftedBackward<Ty, false>{vectors_of<Ty>(H)}, sms, st);
+            launch_backward<Ty>(a, ShiftedBackward<Ty, false>{vectors_of(H, VEC<Ty>)}, sms, st);
     });
 }
 

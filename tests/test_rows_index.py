@@ -1,0 +1,36 @@
+"""The row kernels' index arithmetic (csrc/rows_index.h), enumerated on the host."""
+import os
+import subprocess
+
+import pytest
+
+from combine_persistent_warp_gb300 import build
+
+PRELUDE = '#include <cstdio>\n#include "rows_index.h"\nusing namespace cpw;\n'
+
+
+def _run(tmp_path, body):
+    src, exe = tmp_path / "check.cpp", tmp_path / "check"
+    src.write_text(PRELUDE + "int main() {\n" + body + "\nreturn 0; }\n")
+    flags = ["-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover=undefined"]
+    subprocess.run(["g++", *flags, "-I" + build.CSRC, str(src), "-o", str(exe)], check=True, capture_output=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_rows_that_are_zeroed_stay_inside_whatever_the_offsets_hold(tmp_path):
+    """Block b of `blocks` walks the rows rest_begin() + b, + blocks, ... below M."""
+    _run(tmp_path, """
+    const int ends[] = {-2147483647 - 1, -7, 0, 1, 29, 30, 31, 1 << 30, 2147483400, 2147483647};
+    const int sizes[] = {0, 1, 30, 1 << 30};
+    for (int M : sizes)
+        for (int total : ends) {
+            const int first = rest_begin(total, M);
+            if (first < 0 || first > M) { printf("M %d, offsets[E] %d: from row %d on\\n", M, total, first); return 1; }
+            for (int blocks : {1, 152, 2048})
+                for (int b = 0; b < blocks; ++b)
+                    for (int r = first + b, n = 0; r < M && n < 3; r += blocks, ++n)
+                        if (r < 0) { printf("M %d, offsets[E] %d, block %d: row %d\\n", M, total, b, r); return 1; }
+            if (total >= 0 && total <= M && first != total) return 1;
+        }
+    """)
