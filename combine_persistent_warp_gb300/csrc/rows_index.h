@@ -22,8 +22,11 @@ CPW_HD int vectors_of(int H, int V) { return (H + V - 1 + V - 1) / V; }
 // The aligned vectors of elements e .. e + V - 1 of a row lie inside the row, for every e that
 // vector g has whatever the row's lead.
 CPW_HD bool inside(int g, int H, int V) { return g >= 2 && (g + 2) * V <= H; }
-// Row r of `rows` has 2 * V elements of its matrix before and after it (rim: rows that hold them).
+// Row r of `rows` has as many elements of its matrix before and after it as those vectors may reach past
+// its ends, whatever the leads (rim: rows that hold them).  A row's first vector starts at element -(V - 1)
+// at least, and the aligned ones up to V - 1 before that: 2 V - 2.  Its last one starts at H + V - 2 at most
+// (H past a multiple of V by 2, no lead) and takes two aligned ones from there: 3 V - 2 past the end.
 CPW_HD bool amid(int r, int rows, int rim) { return r >= rim && r < rows - rim; }
-CPW_HD int rim_of(int H, int V) { return (2 * V + H - 1) / H; }
+CPW_HD int rim_of(int H, int V) { return (3 * V - 2 + H - 1) / H; }
 
 }  // namespace cpw

@@ -32,3 +32,21 @@ def test_offsets_that_lie_are_kept_inside(H, dtype, end):
     assert (guarded[:1000] == 7).all() and (guarded[1000 + M:] == 7).all()
     if end >= M:
         assert torch.equal(out, ops.combine_rows_backward(x, y, order.rows, w, order.offsets)[0])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [1, 2, 3, 5, 6, 7, 10, 13, 18, 21, 22])
+def test_combine_of_short_rows_near_the_matrix_ends(H, dtype):
+    """Every row of y by itself, first to last, for rows shorter than the vectors that move them."""
+    M = 64
+    torch.manual_seed(H)
+    rows = torch.arange(M, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    buf = torch.full((M * H + 16,), float("nan"), dtype=dtype, device="cuda")
+    lib, s = native.load(), torch.cuda.current_stream().cuda_stream
+    for at in range(0, 8):
+        y = buf[at:at + M * H].view(M, H)
+        buf.fill_(float("nan"))
+        y.copy_(torch.randn(M, H, device="cuda"))
+        out = torch.zeros(M, H, dtype=dtype, device="cuda")
+        assert lib.moe_combine_rows(M, 1, H, M, y.data_ptr(), CODE[dtype], rows.data_ptr(), None, out.data_ptr(), s) == 0
+        assert torch.equal(out, y)

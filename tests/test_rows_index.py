@@ -30,3 +30,33 @@ def test_rows_that_are_zeroed_stay_inside_whatever_the_offsets_hold(tmp_path):
             if (total >= 0 && total <= M && first != total) return 1;
         }
     """)
+
+
+def test_shifted_vectors_are_read_from_inside_the_matrix(tmp_path):
+    """Whatever the leads of the written and of the read rows, the two aligned vectors that hold elements
+    e .. e + V - 1 lie inside the matrix wherever the kernels load them: where `inside` holds for the
+    vector, or the row is `amid` the matrix."""
+    _run(tmp_path, """
+    for (int V : {4, 8})
+        for (int H = 1; H <= 70; ++H) {
+            const int rim = rim_of(H, V), vectors = vectors_of(H, V);
+            for (int lead = 0; lead < V; ++lead)                      // of the written row
+                if (vectors * V - lead < H) { printf("H %d V %d: elements left over\\n", H, V); return 1; }
+            for (int rows : {1, 2, 2 * rim, 2 * rim + 1, 2 * rim + 3})
+                for (int r = 0; r < rows; ++r)
+                    for (int g = 0; g < vectors; ++g) {
+                        if (!inside(g, H, V) && !amid(r, rows, rim))
+                            continue;
+                        for (int lead = 0; lead < V; ++lead)
+                            for (int past = 0; past < V; ++past) {    // the read row's elements past a boundary
+                                const int e = g * V - lead, at = past + e, start = (at + 64 * V) / V * V - 64 * V;
+                                const long long lo = static_cast<long long>(r) * H + start - past, hi = lo + 2 * V;
+                                if (lo < 0 || hi > static_cast<long long>(rows) * H) {
+                                    printf("V %d H %d, row %d of %d, vector %d, leads %d and %d: elements %lld .. %lld of %lld\\n", V, H, r, rows, g,
+                                           lead, past, lo, hi, static_cast<long long>(rows) * H);
+                                    return 1;
+                                }
+                            }
+                    }
+        }
+    """)
