@@ -818,7 +818,11 @@ template <typename T, int V, int VPT>
 __global__ void __launch_bounds__(ROW_WARPS * 32) norm_backward_warp_kernel(const NormBwdArgs a)
 {
     constexpr int P = PAIRS<V, VPT>;
-    __shared__ float sums[2][ROW_WARPS][32 * V * VPT];
+    struct alignas(16) Sums {
+        float v[32 * V * VPT];
+    };
+    static_assert(alignof(Sums) >= alignof(Pack<float, V>), "put() stores whole packs into them");
+    __shared__ Sums sums[2][ROW_WARPS];
     const int packs = a.H / V, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float inv = 1.0f / static_cast<float>(a.H);
     const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
@@ -856,15 +860,15 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) norm_backward_warp_kernel(cons
         }
     }
     if (a.part) {
-        put<float, V, VPT>(sums[0][warp], dg, lane, 32, 32 * VPT);
-        put<float, V, VPT>(sums[1][warp], db, lane, 32, 32 * VPT);
+        put<float, V, VPT>(sums[0][warp].v, dg, lane, 32, 32 * VPT);
+        put<float, V, VPT>(sums[1][warp].v, db, lane, 32, 32 * VPT);
         __syncthreads();
         for (int i = threadIdx.x; i < 2 * a.H; i += ROW_WARPS * 32) {
             const int which = i >= a.H, c = i - which * a.H;
             float v = 0.0f;
 #pragma unroll
             for (int k = 0; k < ROW_WARPS; ++k)
-                v += sums[which][k][c];
+                v += sums[which][k].v[c];
             a.part[(static_cast<size_t>(which) * gridDim.x + blockIdx.x) * a.pitch + c] = v;
         }
     }
