@@ -283,7 +283,7 @@ PyObject *layer_norm_fp8(Args a)
     return tuple_of({q, sf});
 }
 
-// (dy, x, weight, mean, rstd, params fp32)
+// (dy, x, weight, mean, rstd, params fp32, dweight wanted, dbias wanted)
 PyObject *layer_norm_backward(Args a)
 {
     const at::Tensor &x = tensor(a[1], "x");
@@ -297,14 +297,19 @@ PyObject *layer_norm_backward(Args a)
     const void *mean = flat(tensor(a[3], "mean"), "mean", {m.rows}, at::kFloat, f.dev);
     const void *rstd = flat(tensor(a[4], "rstd"), "rstd", {m.rows}, at::kFloat, f.dev);
     const int T = count(m.rows, "x"), H = count(m.width, "x");
+    const bool want_w = truth(a[6]), want_b = truth(a[7]);
     uint64_t need = 0;
-    check(moe_layer_norm_backward_workspace(T, H, &need), "moe_layer_norm_backward_workspace");
+    if (want_w || want_b)
+        check(moe_layer_norm_backward_workspace(T, H, &need), "moe_layer_norm_backward_workspace");
     const Workspace ws(need);
-    at::Tensor dx = make({m.rows, m.width}, f.type, f.dev);
-    at::Tensor dweight = make({m.width}, w.type, f.dev), dbias = make({m.width}, w.type, f.dev);
+    at::Tensor dx = make({m.rows, m.width}, f.type, f.dev), dweight, dbias;   // (an undefined tensor is None)
+    if (want_w)
+        dweight = make({m.width}, w.type, f.dev);
+    if (want_b)
+        dbias = make({m.width}, w.type, f.dev);
     check(moe_layer_norm_backward(T, H, d.p, d.ld, m.p, m.ld, f.dtype, w.weight, w.dtype, static_cast<const float *>(mean),
-                                  static_cast<const float *>(rstd), dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(),
-                                  ws.get(), need, current_stream(f.dev)),
+                                  static_cast<const float *>(rstd), dx.data_ptr(),
+                                  want_w ? dweight.data_ptr() : nullptr, want_b ? dbias.data_ptr() : nullptr, ws.get(), need, current_stream(f.dev)),
           "moe_layer_norm_backward");
     return tuple_of({dx, dweight, dbias});
 }
@@ -429,7 +434,7 @@ PyObject *combine_rows(Args a)
     return THPVariable_Wrap(out);
 }
 
-// (dout, y, rows, w, offsets)
+// (dout, y, rows, w, offsets, dw wanted)
 PyObject *combine_rows_backward(Args a)
 {
     const at::Tensor &y = tensor(a[1], "y");
@@ -440,9 +445,12 @@ PyObject *combine_rows_backward(Args a)
     const Groups g = groups(a[4], f.dev);
     const Matrix d = matrix(tensor(a[0], "dout"), "dout", f, r.T, H);
     const void *pw = flat_or_null(a[3], "w", {r.T, r.k}, at::kFloat, f.dev);
-    at::Tensor dy = make({M, H}, f.type, f.dev), dw = make({r.T, r.k}, at::kFloat, f.dev);
+    at::Tensor dy = make({M, H}, f.type, f.dev), dw;   // (an undefined tensor is None)
+    if (truth(a[5]))
+        dw = make({r.T, r.k}, at::kFloat, f.dev);
     check(moe_combine_rows_backward(count(r.T, "rows"), count(r.k, "rows"), count(H, "y"), g.E, M, d.p, d.ld, py, f.dtype, r.p,
-                                    static_cast<const float *>(pw), g.p, dy.data_ptr(), dw.data_ptr<float>(), current_stream(f.dev)),
+                                    static_cast<const float *>(pw), g.p, dy.data_ptr(),
+                                    dw.defined() ? dw.data_ptr<float>() : nullptr, current_stream(f.dev)),
           "moe_combine_rows_backward");
     return tuple_of({dy, dw});
 }
@@ -539,13 +547,13 @@ PyObject *get_error(Args)
 #define CALL(name, n, fn) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(guarded<n, fn>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CALL("layer_norm", 4, layer_norm),
                          CALL("layer_norm_fp8", 5, layer_norm_fp8),
-                         CALL("layer_norm_backward", 6, layer_norm_backward),
+                         CALL("layer_norm_backward", 8, layer_norm_backward),
                          CALL("route_topk", 4, route_topk),
                          CALL("route_topk_backward", 5, route_topk_backward),
                          CALL("expert_order", 2, expert_order),
                          CALL("gather_rows", 3, gather_rows),
                          CALL("combine_rows", 3, combine_rows),
-                         CALL("combine_rows_backward", 5, combine_rows_backward),
+                         CALL("combine_rows_backward", 6, combine_rows_backward),
                          CALL("grouped_mm", 4, grouped<true>),
                          CALL("grouped_mm_dx", 4, grouped<false>),
                          CALL("grouped_mm_dw", 6, grouped_dw),

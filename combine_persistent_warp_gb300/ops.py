@@ -61,14 +61,17 @@ def layer_norm_fp8(x, weight=None, bias=None, eps: float = 1e-5, *, pow2_scales:
     return _call(stream, _ops.layer_norm_fp8, x, weight, bias, eps, pow2_scales)
 
 
-def layer_norm_backward(dy, x, weight, mean, rstd, *, param_dtype=None, stream=None):
+def layer_norm_backward(dy, x, weight, mean, rstd, *, param_dtype=None, weight_grad: bool = True, bias_grad: bool = True,
+                        stream=None):
     """Gradients (dx, dweight, dbias) of layer_norm.  dweight and dbias are of the weight's type
-    (without a weight: ``param_dtype``, float32 or by default x's type)."""
+    (without a weight: ``param_dtype``, float32 or by default x's type); one that is not asked for is
+    None, and without either their sums are not taken."""
     if param_dtype is not None and param_dtype != torch.float32 and param_dtype != x.dtype:
         raise TypeError(f"param_dtype: {param_dtype} is neither {x.dtype} nor float32")
+    args = dy, x, weight, mean, rstd, param_dtype == torch.float32, weight_grad, bias_grad
     if stream is None:
-        return _ops.layer_norm_backward(dy, x, weight, mean, rstd, param_dtype == torch.float32)
-    return _call(stream, _ops.layer_norm_backward, dy, x, weight, mean, rstd, param_dtype == torch.float32)
+        return _ops.layer_norm_backward(*args)
+    return _call(stream, _ops.layer_norm_backward, *args)
 
 
 # ------------------------------------------------------------------------------ router ----
@@ -109,11 +112,11 @@ def combine_rows(y, rows, w=None, *, stream=None):
     return _call(stream, _ops.combine_rows, y, rows, w)
 
 
-def combine_rows_backward(dout, y, rows, w, offsets, *, stream=None):
-    """Gradients (dy, dw) of combine_rows: dy like y, dw fp32 [T, topk]."""
+def combine_rows_backward(dout, y, rows, w, offsets, *, gate_grad: bool = True, stream=None):
+    """Gradients (dy, dw) of combine_rows: dy like y, dw fp32 [T, topk] (None without ``gate_grad``)."""
     if stream is None:
-        return _ops.combine_rows_backward(dout, y, rows, w, offsets)
-    return _call(stream, _ops.combine_rows_backward, dout, y, rows, w, offsets)
+        return _ops.combine_rows_backward(dout, y, rows, w, offsets, gate_grad)
+    return _call(stream, _ops.combine_rows_backward, dout, y, rows, w, offsets, gate_grad)
 
 
 # -------------------------------------------------------------------- grouped products ----

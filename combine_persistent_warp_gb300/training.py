@@ -30,9 +30,9 @@ class _LayerNorm(Function):
     @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
-        dx, dweight, dbias = ops.layer_norm_backward(_rows(dy), x, weight, mean, rstd, param_dtype=ctx.bias_dtype)
         _, weight_grad, bias_grad, _ = ctx.needs_input_grad   # (False for None, which may have no gradient)
-        return dx, dweight if weight_grad else None, dbias if bias_grad else None, None
+        return *ops.layer_norm_backward(_rows(dy), x, weight, mean, rstd, param_dtype=ctx.bias_dtype, weight_grad=weight_grad,
+                                        bias_grad=bias_grad), None
 
 
 class _RouteTopk(Function):
@@ -74,8 +74,8 @@ class _CombineRows(Function):
     @once_differentiable
     def backward(ctx, dout):
         y, rows, w, offsets = ctx.saved_tensors
-        dy, dw = ops.combine_rows_backward(_rows(dout), y, rows, w, offsets)
-        return dy, None, dw if ctx.needs_input_grad[2] else None, None
+        dy, dw = ops.combine_rows_backward(_rows(dout), y, rows, w, offsets, gate_grad=ctx.needs_input_grad[2])
+        return dy, None, dw, None
 
 
 class _GroupedMM(Function):

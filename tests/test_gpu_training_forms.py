@@ -69,3 +69,22 @@ def test_gradients_that_start_anywhere(rows):
     wide = torch.randn(rows, 77, device="cuda").bfloat16()
     training.grouped_mm(x, w, off).backward(wide[:, 5:])
     assert torch.equal(x.grad, ops.grouped_mm_dx(wide[:, 5:].clone(), w.detach(), off))
+
+
+@pytest.mark.parametrize("T,H", [(0, 64), (1, 64), (300, 512), (40, 1001), (3000, 2048), (3000, 2049), (5, 12000)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradients_that_are_not_asked_for(T, H, dtype):
+    torch.manual_seed(5)
+    x, dy = torch.randn(T, H, device="cuda").to(dtype), torch.randn(T, H, device="cuda").to(dtype)
+    g = torch.randn(H, device="cuda").to(dtype)
+    _, mean, rstd = ops.layer_norm(x, g)
+    full = ops.layer_norm_backward(dy, x, g, mean, rstd)
+    for weight_grad, bias_grad in ((False, False), (True, False), (False, True)):
+        part = ops.layer_norm_backward(dy, x, g, mean, rstd, weight_grad=weight_grad, bias_grad=bias_grad)
+        for a, b, asked in zip(part, full, (True, weight_grad, bias_grad)):
+            assert torch.equal(a, b) if asked else a is None
+    o = _order(T, 2, 4)
+    y, w = torch.randn(2 * T, H, device="cuda").to(dtype), torch.rand(T, 2, device="cuda")
+    dout = torch.randn(T, H, device="cuda").to(dtype)
+    dy, dw = ops.combine_rows_backward(dout, y, o.rows, w, o.offsets, gate_grad=False)
+    assert dw is None and torch.equal(dy, ops.combine_rows_backward(dout, y, o.rows, w, o.offsets)[0])

@@ -15,13 +15,13 @@ def _layer_norm(x, weight=None, bias=None, eps=1e-5):
     return (y + bias.float() if bias is not None else y).to(x.dtype), mean, rstd
 
 
-def _layer_norm_backward(dy, x, weight, mean, rstd, *, param_dtype=None, **_):
+def _layer_norm_backward(dy, x, weight, mean, rstd, *, param_dtype=None, weight_grad=True, bias_grad=True):
     xh = (x.float() - mean[:, None]) * rstd[:, None]
     d = dy.float()
     g = d * weight.float() if weight is not None else d
     dx = (g - g.mean(1, keepdim=True) - xh * (g * xh).mean(1, keepdim=True)) * rstd[:, None]
     to = weight.dtype if weight is not None else param_dtype or x.dtype
-    return dx.to(x.dtype), (d * xh).sum(0).to(to), d.sum(0).to(to)
+    return dx.to(x.dtype), (d * xh).sum(0).to(to) if weight_grad else None, d.sum(0).to(to) if bias_grad else None
 
 
 def _combine_rows(y, rows, w=None):
@@ -29,7 +29,7 @@ def _combine_rows(y, rows, w=None):
     return torch.where((rows < 0)[:, :, None], 0.0, v).sum(1).to(y.dtype)
 
 
-def _combine_rows_backward(dout, y, rows, w, offsets, **_):
+def _combine_rows_backward(dout, y, rows, w, offsets, *, gate_grad=True):
     named = rows >= 0
     at = rows[named].long()
     weights = w if w is not None else torch.ones(rows.shape)
@@ -37,7 +37,7 @@ def _combine_rows_backward(dout, y, rows, w, offsets, **_):
     dy[at] = (weights[:, :, None] * dout.float()[:, None])[named]
     dw = torch.zeros(rows.shape)
     dw[named] = (y[at].float() * dout.float()[named.nonzero()[:, 0]]).sum(1)
-    return dy.to(y.dtype), dw
+    return dy.to(y.dtype), dw if gate_grad else None
 
 
 @pytest.fixture(autouse=True)
@@ -110,3 +110,18 @@ def test_rows_of_an_odd_width_are_not_copied():
     """No copy puts them on 16-byte boundaries, and what has such rows takes them as they are."""
     for t in (torch.randn(4, 33).bfloat16(), torch.arange(3 + 4 * 33).bfloat16()[3:].view(4, 33)):
         assert training._rows(t) is t
+
+
+def test_gradients_of_frozen_parameters_are_not_asked_for(monkeypatch):
+    seen = []
+    for name in ("layer_norm_backward", "combine_rows_backward"):
+        f = getattr(ops, name)
+        monkeypatch.setattr(ops, name, lambda *a, _f=f, **k: (seen.append(k), _f(*a, **k))[1])
+    x, g, b = torch.randn(3, 16, requires_grad=True), torch.randn(16), torch.randn(16, requires_grad=True)
+    training.layer_norm(x, g, b).sum().backward()
+    assert g.grad is None and b.grad is not None and not seen[0]["weight_grad"] and seen[0]["bias_grad"]
+    y, w = torch.randn(6, 8, requires_grad=True), torch.rand(3, 2)
+    training.combine_rows(y, ORDER, w).sum().backward()
+    assert w.grad is None and not seen[1]["gate_grad"]
+    training.combine_rows(y, ORDER, w.requires_grad_()).sum().backward()
+    assert w.grad is not None and seen[2]["gate_grad"]
