@@ -124,6 +124,13 @@ Matrix matrix(const at::Tensor &t, const char *name, const First &f, int64_t row
     return {n, w, n > 1 ? ld : std::max<int64_t>(w, 1), t.data_ptr()};
 }
 
+// An output that the caller gave has been written: what autograd saved of it is no longer there.
+void written(const at::Tensor &t)
+{
+    if (!t.is_inference())   // (inference tensors have no version)
+        t.unsafeGetTensorImpl()->bump_version();
+}
+
 // A contiguous tensor of the given shape.
 void *flat(const at::Tensor &t, const char *name, at::IntArrayRef shape, at::ScalarType dtype, int dev)
 {
@@ -496,6 +503,7 @@ PyObject *grouped(Args a)
           TO_N ? "moe_grouped_mm" : "moe_grouped_mm_dx");
     if (none(a[3]))
         return THPVariable_Wrap(fresh);
+    written(tensor(a[3], "out"));
     Py_INCREF(a[3]);
     return a[3];
 }
@@ -532,6 +540,7 @@ PyObject *grouped_dw(Args a)
           "moe_grouped_mm_dw");
     if (none(a[3]))
         return THPVariable_Wrap(fresh);
+    written(tensor(a[3], "out"));
     Py_INCREF(a[3]);
     return a[3];
 }

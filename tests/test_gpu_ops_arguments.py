@@ -23,3 +23,28 @@ def test_the_stride_of_a_single_row_may_be_anything(rows):
     assert torch.equal(ops.grouped_mm(x, w, off, out=out), ops.grouped_mm(plain(x), w, off))
     for a, b in zip(ops.layer_norm_fp8(x), ops.layer_norm_fp8(plain(x))):
         assert torch.equal(a, b)
+
+
+def _products():
+    torch.manual_seed(1)
+    x, dy = torch.randn(6, 64, device="cuda").bfloat16(), torch.randn(6, 72, device="cuda").bfloat16()
+    w = torch.randn(2, 72, 64, device="cuda").bfloat16()
+    off = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    return [(lambda out: ops.grouped_mm(x, w, off, out=out), (6, 72)), (lambda out: ops.grouped_mm_dx(dy, w, off, out=out), (6, 64)),
+            (lambda out: ops.grouped_mm_dw(dy, x, off, out=out), (2, 72, 64)),
+            (lambda out: ops.grouped_mm_dw(dy, x, off, out=out, accumulate=True), (2, 72, 64))]
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_an_output_that_autograd_saved_and_a_call_overwrote_raises(which):
+    call, shape = _products()[which]
+    out = torch.ones(shape, device="cuda", dtype=torch.bfloat16)
+    p = torch.ones(shape, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    z = (p * out).sum()                      # saves out
+    v = out._version
+    assert call(out) is out and out._version == v + 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.backward()
+    with torch.inference_mode():
+        fresh = torch.ones(shape, device="cuda", dtype=torch.bfloat16)
+        assert call(fresh) is fresh
