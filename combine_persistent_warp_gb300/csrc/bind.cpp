@@ -12,6 +12,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <algorithm>
 #include <climits>
 #include <sstream>
 #include <stdexcept>
@@ -463,6 +464,48 @@ PyObject *combine_rows_backward(Args a)
 }
 
 // ------------------------------------------------------------------ grouped products ----
+// The bytes of a tensor: rows of `width` bytes, `pitch` apart (pitch >= width).
+struct Bytes {
+    const char *p;
+    int64_t rows, width, pitch;
+};
+Bytes bytes_of(const Matrix &m, size_t size)
+{
+    const int64_t b = static_cast<int64_t>(size);
+    return {static_cast<const char *>(m.p), m.rows, m.width * b, m.ld * b};
+}
+Bytes bytes_of(const void *p, int64_t elements, size_t size)
+{
+    const int64_t n = elements * static_cast<int64_t>(size);
+    return {static_cast<const char *>(p), 1, n, n};
+}
+bool overlap(Bytes a, Bytes b)
+{
+    if (a.rows == 0 || b.rows == 0 || a.width == 0 || b.width == 0)
+        return false;
+    if (a.p >= b.p + b.pitch * (b.rows - 1) + b.width || b.p >= a.p + a.pitch * (a.rows - 1) + a.width)
+        return false;
+    // the tensors lie among each other: parts of the rows of one buffer, perhaps
+    if (a.rows > b.rows)
+        std::swap(a, b);
+    for (int64_t r = 0; r < a.rows; ++r) {
+        const char *lo = a.p + r * a.pitch, *hi = lo + a.width;
+        if (hi <= b.p)
+            continue;
+        // the last row of b that starts before this row's end is the only one of those that may pass its start
+        const int64_t j = std::min((hi - 1 - b.p) / b.pitch, b.rows - 1);
+        if (b.p + j * b.pitch + b.width > lo)
+            return true;
+    }
+    return false;
+}
+// A product's blocks write its output while others still read the inputs.
+void apart(const Bytes &out, const Bytes &in, const char *name)
+{
+    if (overlap(out, in))
+        throw ValueErr(std::string("out overlaps ") + name);
+}
+
 struct Weights {
     int64_t E, N, K;
     const void *p;
@@ -493,6 +536,10 @@ PyObject *grouped(Args a)
         o = {m.rows, width, std::max<int64_t>(width, 1), fresh.data_ptr()};
     } else {
         o = matrix(tensor(a[3], "out"), "out", f, m.rows, width);
+        const Bytes to = bytes_of(o, 2);
+        apart(to, bytes_of(m, 2), name);
+        apart(to, bytes_of(w.p, w.E * w.N * w.K, 2), "w");
+        apart(to, bytes_of(g.p, w.E + 1, 4), "offsets");
     }
     const auto call = TO_N ? moe_grouped_mm : moe_grouped_mm_dx;
     uint64_t need = 0;
@@ -531,6 +578,10 @@ PyObject *grouped_dw(Args a)
         if (type != f.type && type != at::kFloat)
             throw TypeErr("out: dtype " + dtype_name(type) + " is neither " + dtype_name(f.type) + " nor Float");
         po = flat(out, "out", {g.E, N, K}, type, f.dev);
+        const Bytes to = bytes_of(po, g.E * N * K, type == at::kFloat ? 4 : 2);
+        apart(to, bytes_of(d, 2), "dy");
+        apart(to, bytes_of(m, 2), "x");
+        apart(to, bytes_of(g.p, g.E + 1, 4), "offsets");
     }
     uint64_t need = 0;
     check(moe_grouped_mm_dw_workspace(m.rows, g.E, count(N, "dy"), count(K, "x"), &need), "moe_grouped_mm_dw_workspace");

@@ -5,7 +5,8 @@ Entry points over the C ABI of include/cpw_moe.h; the module ``_ops`` (csrc/bind
 arguments.  Shapes, types and devices are checked there (``ValueError`` / ``TypeError``), sizes and
 alignment by the library (:class:`MoeError`).  Every call is asynchronous on ``stream`` (default: the
 current stream) and takes its outputs from PyTorch's pool of that stream; with another stream than
-the current one, inputs are marked as in use there, and the caller orders the streams.
+the current one, inputs are marked as in use there, and the caller orders the streams.  An ``out``
+shares no memory with an input.
 
     h = ops.layer_norm(x, g, b)[0]
     idx, w = ops.route_topk(logits, topk)

@@ -294,6 +294,7 @@ int moe_route_noalloc(int T, int E, int topk, int R, const int64_t *topk_idx, ui
  *
  * Pointers are device pointers aligned to their element type unless a call asks for more; a row
  * stride (ld...) counts elements and is at least the row's length; other tensors are contiguous.
+ * Results and workspaces share no memory with the inputs (an accumulating dw is its own).
  * T, M, T*topk and the rows' H are at most 2^30.
  * Calls with T == 0 (or M == 0) do nothing but write the results that an empty batch has (zero
  * gradients of weights, zero offsets). */

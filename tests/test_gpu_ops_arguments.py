@@ -48,3 +48,35 @@ def test_an_output_that_autograd_saved_and_a_call_overwrote_raises(which):
     with torch.inference_mode():
         fresh = torch.ones(shape, device="cuda", dtype=torch.bfloat16)
         assert call(fresh) is fresh
+
+
+def test_an_output_that_overlaps_an_input_is_refused():
+    torch.manual_seed(2)
+    bf = dict(device="cuda", dtype=torch.bfloat16)
+    w = torch.randn(2, 64, 64, **bf)
+    off = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    x = torch.randn(6, 64, **bf)
+    for f, name in ((ops.grouped_mm, "x"), (ops.grouped_mm_dx, "dy")):
+        for out, what in ((x, name), (w[0, :6], "w")):
+            with pytest.raises(ValueError, match=f"out overlaps {what}"):
+                f(x, w, off, out=out)
+    # rows of one buffer: apart, and one column in common
+    wide = torch.randn(6, 136, **bf)
+    part = wide[:, :64]
+    want = ops.grouped_mm(part.clone(), w, off)
+    assert torch.equal(ops.grouped_mm(part, w, off, out=wide[:, 72:]), want)
+    assert torch.equal(part, wide[:, :64])
+    with pytest.raises(ValueError, match="overlaps"):
+        ops.grouped_mm(part, w, off, out=wide[:, 56:120])
+    # of the same buffer at different strides: rows 0, 2, ... of it and rows 1, 3, ..., and all rows
+    rows = torch.randn(12, 64, **bf)
+    assert torch.equal(ops.grouped_mm(rows[::2], w, off, out=rows[1::2]), ops.grouped_mm(rows[::2].clone(), w, off))
+    with pytest.raises(ValueError, match="overlaps"):
+        ops.grouped_mm(rows[::2], w, off, out=rows[:6])
+    both = torch.randn(13, 64, **bf)
+    assert ops.grouped_mm(both[:6], w, off, out=both[6:12]) is not None
+    buf = torch.randn(64 * 64, **bf)
+    inside, apart, one = buf[:6 * 64].view(6, 64), torch.randn(6, 64, **bf), torch.tensor([0, 6], dtype=torch.int32, device="cuda")
+    for dy, x, what in ((inside, apart, "dy"), (apart, inside, "x")):
+        with pytest.raises(ValueError, match=f"out overlaps {what}"):
+            ops.grouped_mm_dw(dy, x, one, out=buf.view(1, 64, 64))
