@@ -600,7 +600,12 @@ PyObject *grouped_dw(Args a)
 PyObject *get_error(Args)
 {
     int st = 0;
-    check(moe_ops_get_error(&st, current_stream(c10::cuda::current_device())), "moe_ops_get_error");
+    void *const stream = current_stream(c10::cuda::current_device());
+    int rc;
+    Py_BEGIN_ALLOW_THREADS   // it waits for the stream, whose work may itself wait for a Python thread
+    rc = moe_ops_get_error(&st, stream);
+    Py_END_ALLOW_THREADS
+    check(rc, "moe_ops_get_error");
     return PyLong_FromLong(st);
 }
 

@@ -1,4 +1,7 @@
 """What the operators' Python entry points take and refuse on the GPU."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -80,3 +83,23 @@ def test_an_output_that_overlaps_an_input_is_refused():
     for dy, x, what in ((inside, apart, "dy"), (apart, inside, "x")):
         with pytest.raises(ValueError, match=f"out overlaps {what}"):
             ops.grouped_mm_dw(dy, x, one, out=buf.view(1, 64, 64))
+
+
+def test_other_threads_run_while_get_error_waits():
+    ticks, stop = [], threading.Event()
+
+    def tick():
+        while not stop.wait(0.005):
+            ticks.append(time.monotonic())
+
+    t = threading.Thread(target=tick)
+    t.start()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(1_000_000_000)         # about half a second of the stream
+    start = time.monotonic()
+    assert ops.get_error() == 0
+    end = time.monotonic()
+    stop.set()
+    t.join()
+    assert end - start > 0.2
+    assert sum(start < x < end for x in ticks) >= 5
