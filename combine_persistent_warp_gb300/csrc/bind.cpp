@@ -62,8 +62,8 @@ int code_of(at::ScalarType t)
 
 int count(int64_t n, const char *name)
 {
-    if (n > INT_MAX)
-        throw ValueErr(std::string(name) + ": a dimension passes 2^31 - 1");
+    if (n > INT_MAX || n < INT_MIN)
+        throw ValueErr(std::string(name) + ": " + std::to_string(n) + " passes 31 bits");
     return static_cast<int>(n);
 }
 

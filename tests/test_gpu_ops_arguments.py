@@ -103,3 +103,13 @@ def test_other_threads_run_while_get_error_waits():
     t.join()
     assert end - start > 0.2
     assert sum(start < x < end for x in ticks) >= 5
+
+
+def test_numbers_past_31_bits_are_refused():
+    logits = torch.zeros(4, 8, device="cuda")
+    idx = torch.zeros(4, 2, dtype=torch.int64, device="cuda")
+    for far in (1 << 32, -(1 << 32), -(1 << 40)):
+        with pytest.raises(ValueError, match="31 bits"):
+            ops.route_topk(logits, 2 + far)
+        with pytest.raises(ValueError, match="31 bits"):
+            ops.expert_order(idx, 8 + far)
