@@ -57,7 +57,12 @@ constexpr int RING = 6;
 template <bool DW>
 constexpr int THREADS = DW ? 256 : 384;   // four warps, and four of the epilogue; eight for rows (two tiles at a time)
 constexpr int MAX_E = 1024;
-constexpr uint64_t WAIT_NS = 2000000000ull;    // limit of every wait
+constexpr uint64_t WAIT_NS = 2000000000ull;    // limit of every wait but one:
+// An accumulator takes as long as its tile has stages, 0.23 us each, and a group of the weights' gradient
+// may hold every row there is (2^30 in one of 128 experts: 3.9 s).
+constexpr uint64_t STAGE_NS = 2000;
+__host__ __device__ constexpr uint64_t tile_wait_ns(int stages) { return WAIT_NS + STAGE_NS * static_cast<uint64_t>(stages); }
+static_assert(tile_wait_ns(MAX_ROWS / KB) > 4 * 230 * (MAX_ROWS / KB), "the longest group's products are waited for");
 constexpr int STAGE_OUT = 32 * 128;    // dW: an epilogue warp's 32 rows x 128 bytes on their way out
 constexpr int ROWS_OUT = 2 * 32 * (256 + 64);   // the other products: 32 rows of two tiles on their way out
 constexpr int SMEM = RING * STAGE + 1024 + ROWS_OUT;
@@ -702,7 +707,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<KIND == WEIG
                     acc_phase ^= 1;
                 continue;
             }
-            ok = __all_sync(0xFFFFFFFFu, wait_phase(&s.acc_full[acc], acc_phase));
+            ok = __all_sync(0xFFFFFFFFu, wait_phase(&s.acc_full[acc], acc_phase, tile_wait_ns(t.blocks)));
             if (KIND != WEIGHTS)
                 ok = epilogue_all(ok, 1 + group);   // store_rows' barriers need all four warps
             if (!ok)

@@ -392,7 +392,8 @@ int moe_grouped_mm_dw(int64_t M, int E, int N, int K, const void *dy, int64_t ld
 
 /* Waits for `stream`, then returns and clears the sticky status of the operators' device-side
  * waits on the current device: MOE_OK, or MOE_ERR_TIMEOUT if a wait of a grouped product ran
- * past its limit (2 s; its outputs are then undefined).  Not inside a stream capture. */
+ * past its limit (2 s, and 2 us for each 64 of the contraction; its outputs are then undefined).  The
+ * status is the device's, not a stream's or a thread's: who asks first has it, and clears it for all.  Not inside a stream capture. */
 int moe_ops_get_error(int *device_status, void *stream);
 
 /* Release every device buffer of the handle (after syncing its last stream): the teardown
