@@ -146,7 +146,9 @@ class MoEBlock(nn.Module):
         self.w_down = p(E, H, I)
 
     def forward(self, x, token_mask=None):
-        h = layer_norm(x, self.norm_weight, self.norm_bias, self.eps)
+        # (an unrouted token's gradients are zeros, but zero times what padding may hold is not always zero)
+        seen = x if token_mask is None else x.masked_fill(~token_mask[:, None], 0)
+        h = layer_norm(seen, self.norm_weight, self.norm_bias, self.eps)
         idx, w = route_topk(h @ self.router.t(), self.topk, token_mask)
         order = ops.expert_order(idx, self.E)
         gate, up = grouped_mm(gather_rows(h, order), self.w_gate_up, order.offsets).chunk(2, dim=1)

@@ -88,3 +88,22 @@ def test_gradients_that_are_not_asked_for(T, H, dtype):
     dout = torch.randn(T, H, device="cuda").to(dtype)
     dy, dw = ops.combine_rows_backward(dout, y, o.rows, w, o.offsets, gate_grad=False)
     assert dw is None and torch.equal(dy, ops.combine_rows_backward(dout, y, o.rows, w, o.offsets)[0])
+
+
+@pytest.mark.parametrize("held", [float("nan"), float("inf"), 1e30, 0.0])
+def test_what_unrouted_tokens_hold_reaches_no_gradient(held):
+    torch.manual_seed(6)
+    block = training.MoEBlock(4, 64, 64, 2, std=0.1).cuda()
+    x = torch.randn(50, 64, device="cuda").bfloat16()
+    mask = torch.arange(50, device="cuda") % 3 != 0
+    want = {}
+    for fill in (1.0, held):
+        v = torch.where(mask[:, None], x, fill).requires_grad_()
+        block.zero_grad()
+        out = block(v, mask)
+        out[mask].float().square().mean().backward()
+        got = dict({n: p.grad.clone() for n, p in block.named_parameters()}, x=v.grad, out=out[mask].detach())
+        assert all(t.isfinite().all() for t in got.values()) and not v.grad[~mask].any()
+        want = want or got
+    for n, t in want.items():
+        assert torch.equal(t, got[n]), n
