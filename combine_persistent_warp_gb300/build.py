@@ -3,7 +3,8 @@
 The translation units are compiled in parallel and linked into one shared library
 that exports the C ABI of include/cpw_moe.h.  The CUDA runtime is linked statically;
 the driver's tensor-map encoder is fetched at run time, so no libcuda link is needed.
-_ops.so (g++, PyTorch's headers) marshals the operators' arguments over that ABI.
+_ops.so (g++, PyTorch's headers) marshals the operators' arguments over that ABI; the layer itself
+does without it.
 """
 import concurrent.futures as cf
 import glob
@@ -29,16 +30,24 @@ def _nvcc():
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _deps():
-    return (glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
-            [os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "cpw_moe.h"), __file__])
+HEADER = os.path.join(ROOT, "include", "cpw_moe.h")
+
+
+def _newer_than(target, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
+
+
+def library_up_to_date() -> bool:
+    sources = [p for kind in ("*.cu", "*.cuh", "*.h") for p in glob.glob(os.path.join(CSRC, kind))]
+    return _newer_than(LIB, sources + [HEADER, __file__])
+
+
+def binding_up_to_date() -> bool:
+    return _newer_than(OPS, [os.path.join(CSRC, "bind.cpp"), HEADER, __file__])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(OPS):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(OPS))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return library_up_to_date() and binding_up_to_date()
 
 
 def _compile_binding() -> str:
@@ -72,8 +81,9 @@ def _link_binding(obj: str) -> None:
     os.replace(tmp, OPS)
 
 
-def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and up_to_date():
+def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
+    """libcpw_moe.so: needs nvcc and its host compiler alone."""
+    if not force and library_up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -87,8 +97,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
+    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
     if verbose_ptxas:
         for _, log in results:
@@ -99,7 +108,25 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding.result())
+    return LIB
+
+
+def build_binding(force: bool = False) -> str:
+    """_ops.so, over a built library: needs g++ and the headers of Python and PyTorch too."""
+    if force or not binding_up_to_date():
+        os.makedirs(BUILD, exist_ok=True)
+        _link_binding(_compile_binding())
+    return OPS
+
+
+def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    """Both, side by side; the library is there even where the module cannot be built."""
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(1) as ex:
+        binding = ex.submit(_compile_binding) if force or not binding_up_to_date() else None
+        build_library(force, verbose_ptxas)
+        if binding:
+            _link_binding(binding.result())
     return LIB
 
 

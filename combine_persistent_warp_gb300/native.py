@@ -66,7 +66,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         return _lib
     if build_if_missing:
         from . import build as _build
-        _build.build()
+        _build.build_library()
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"CUDA library {LIB_PATH} is not built (run __graft_entry__.build())")
     L = ctypes.CDLL(LIB_PATH)

@@ -23,11 +23,12 @@ from typing import NamedTuple
 
 import torch
 
-from . import native
+from . import build, native
 from .native import MoeError  # noqa: F401
 
 native.load()
-from . import _ops  # noqa: E402  (linked against the library that load() builds where it is missing)
+build.build_binding()
+from . import _ops  # noqa: E402  (linked against the library, and like it built where it is missing)
 
 
 class ExpertOrder(NamedTuple):
