@@ -42,8 +42,23 @@ def library_up_to_date() -> bool:
     return _newer_than(LIB, sources + [HEADER, __file__])
 
 
+def _built_against() -> str:
+    """What _ops.so depends on besides its sources: the interpreter and PyTorch's binary interface."""
+    import sysconfig
+
+    import torch
+
+    return f"torch {torch.__version__} cxx11 {int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
 def binding_up_to_date() -> bool:
-    return _newer_than(OPS, [os.path.join(CSRC, "bind.cpp"), HEADER, __file__])
+    if not _newer_than(OPS, [os.path.join(CSRC, "bind.cpp"), HEADER, __file__]):
+        return False
+    try:
+        with open(OPS + ".for", encoding="utf-8") as f:
+            return f.read() == _built_against()
+    except OSError:
+        return False
 
 
 def up_to_date() -> bool:
@@ -79,6 +94,9 @@ def _link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, OPS)
+    with open(tmp, "w", encoding="utf-8") as f:
+        f.write(_built_against())
+    os.replace(tmp, OPS + ".for")
 
 
 def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
