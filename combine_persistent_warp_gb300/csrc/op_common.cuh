@@ -45,9 +45,6 @@ __device__ __forceinline__ Pack<T, N> load_pack(const T *p)
         Pack<T, 1> r;
         r.v[0] = __ldg(p);
         return r;
-    } else if constexpr (sizeof(T) * N == 4) {
-        const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(p));
-        return *reinterpret_cast<const Pack<T, N> *>(&u);
     } else {
         static_assert(sizeof(T) * N % 16 == 0, "whole accesses");
         union {
@@ -66,9 +63,8 @@ __device__ __forceinline__ void store_pack(T *p, const Pack<T, N> &v)
 {
     if constexpr (N == 1) {
         *p = v.v[0];
-    } else if constexpr (sizeof(T) * N == 4) {
-        *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<const uint32_t *>(&v);
     } else {
+        static_assert(sizeof(T) * N % 16 == 0, "whole accesses");
         union {
             Pack<T, N> pack;
             uint4 q[sizeof(T) * N / 16];
