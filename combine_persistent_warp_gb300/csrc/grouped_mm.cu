@@ -26,10 +26,11 @@
 // With a short contraction the epilogue bounds: rows' gradient of 42000 x 3320 over 256 in 9 groups 86
 // us, 100 with four warps; without one 1% is lost (94 groups of 27 rows, 136 x 88: 9.0 us and 8.9).
 // Measured on a GB300, bf16 operands N(0,1) x N(0,0.02): 32 experts of about 1024 rows, N 4096,
-// K 7168: forward 1.22-1.25 ms back to back under the power cap (1.55 PFLOP/s; the library's batched
-// product on equal groups of 1024 rows 1.14 ms), 1.9 PFLOP/s in short bursts, the tensor pipe 86 to
+// K 7168: forward 1.23-1.31 ms back to back under the power cap (1.47 to 1.56 PFLOP/s; on equal groups
+// of 1024 rows 1.18 ms, the library's batched product 1.14 ms), 1.9 PFLOP/s in short bursts, the tensor pipe 86 to
 // 90% active; 32 rows an expert: 281 us, 6.8 TB/s of weights; weights' gradient of 128 experts,
-// 4096 x 1536, 131072 rows: 1.06 ms.  Loads of the shared operand multicast over clusters of four
+// 4096 x 1536, 131072 rows: 1.05-1.10 ms; on equal groups in bursts 0.90 ms, in fp32 1.00, added to an
+// fp32 dw 1.26 (its bytes' floor 1.19), added to a 16-bit one 2.28 (add_weights16: a row a lane).  Loads of the shared operand multicast over clusters of four
 // CTAs measured the same (144 of 152 SMs in such clusters) and are not used; L2 eviction hints on
 // the weights cost up to 6%.
 // Operand layouts, both 128-byte swizzled: "K-major" rows of 64 contracted elements, and

@@ -11,7 +11,10 @@
 // Measured on a GB300, bf16: 16384 x 4096 forward 45 us, backward 72 us (HBM floors 40 and 60 us
 // at the measured copy bandwidth), FP8 form 48 us (floor 30: its group maxima and conversions
 // take issue slots); 128 x 7168 FP8 form 2.9 us in a graph; 4099 x 1001 fp32 9 and 13 us; 8939 x 2895
-// fp16, rows off 16-byte boundaries, 29 and 45 (2896: 20 and 39; floors 16 and 23).
+// fp16, rows off 16-byte boundaries, 29 and 45 (2896: 20 and 39; floors 16 and 23).  fp32: 16384 x 4096
+// 90 and 153 us (floors 80 and 121).  Over 8192 columns the backward pass holds more than its registers
+// and spills 320 to 700 bytes a thread: 4096 x 12288 bf16 44 and 103 us (floors 30 and 45), off the
+// boundaries (12287) 92 and 352; 4096 x 16384 fp32 140 and 221 (80 and 121).
 //
 // Long batches run in persistent blocks that keep the next rows on their way: every thread
 // copies the packs of the rows ahead that it will itself use into its own slots of shared memory
@@ -428,7 +431,8 @@ __device__ __forceinline__ float fp8_scale(float m, int pow2)
 }
 // Scales of the groups that the half-warp's packs j make up, from the lanes' maxima m[j]: stored, and one
 // reciprocal r[j] a group, not a quotient an element: the product is within a few fp32 roundings of
-// the quotient, which e4m3's three bits of fraction hide.  Of four groups every lane reduces one (lane
+// the quotient, so a code whose quotient lies that near to the middle between two may be its neighbour
+// (with power-of-two scales the reciprocal is exact, and so is every code).  Of four groups every lane reduces one (lane
 // bits 3 and 2 name it): 9 shuffles and one division, where four apart take 16 and 4 (16384 x 4096 bf16 54
 // us so).
 template <int VPT>

@@ -15,7 +15,8 @@ shares no memory with an input.
     y = ops.grouped_mm(rows, weights, order.offsets)              # weights [E, N, H]
     out = ops.combine_rows(y, order.rows, w)                      # [T, N]
 
-``training`` has these as autograd functions.
+``training`` has these as autograd functions.  The calls here are opaque to PyTorch: they record no
+gradient, and cannot be traced, compiled or mapped.
 """
 from __future__ import annotations
 
@@ -101,7 +102,9 @@ def expert_order(idx, E: int, *, stream=None) -> ExpertOrder:
 # -------------------------------------------------------------------------------- rows ----
 def gather_rows(x, rows, offsets, *, stream=None):
     """Rows of x [T, H] in expert order: out [T*topk, H] with out[rows[t, j]] = x[t], and zeros in the
-    rows that no slot has.  Its gradient is ``combine_rows(dout, rows)``."""
+    rows from offsets[E] on.  rows and offsets are an ``expert_order``, in which every row before has its
+    slot: to skip a slot, put -1 into the order's idx, not into its rows.  Its gradient is
+    ``combine_rows(dout, rows)``."""
     if stream is None:
         return _ops.gather_rows(x, rows, offsets)
     return _call(stream, _ops.gather_rows, x, rows, offsets)
@@ -115,7 +118,8 @@ def combine_rows(y, rows, w=None, *, stream=None):
 
 
 def combine_rows_backward(dout, y, rows, w, offsets, *, gate_grad: bool = True, stream=None):
-    """Gradients (dy, dw) of combine_rows: dy like y, dw fp32 [T, topk] (None without ``gate_grad``)."""
+    """Gradients (dy, dw) of combine_rows: dy like y, dw fp32 [T, topk] (None without ``gate_grad``).
+    rows and offsets as in ``gather_rows``."""
     if stream is None:
         return _ops.combine_rows_backward(dout, y, rows, w, offsets, gate_grad)
     return _call(stream, _ops.combine_rows_backward, dout, y, rows, w, offsets, gate_grad)
@@ -152,7 +156,8 @@ def grouped_mm_dw(dy, x, offsets, *, out=None, accumulate: bool = False, dtype=N
 
 def get_error(stream=None) -> int:
     """Waits for ``stream`` (default: the current stream), then returns (and clears) the sticky status
-    of the grouped products' bounded waits: 0 or MOE_ERR_TIMEOUT."""
+    of the grouped products' bounded waits: 0 or MOE_ERR_TIMEOUT.  After the latter what they wrote is
+    undefined.  The status is the device's: one that another thread asked for is cleared."""
     if stream is None:
         return _ops.get_error()
     return _call(stream, _ops.get_error)

@@ -7,6 +7,10 @@
 Every product, norm, router and row movement of the block, forward and backward, is one of the
 framework's kernels; what is left to PyTorch is elementwise (SwiGLU, the residual sum) and the
 small dense product with the router's weight.
+
+The functions are differentiable once, and cannot be traced, compiled or mapped (``torch.func.vmap``).
+The waits inside the grouped products are bounded; one that ran out shows in ``ops.get_error()``,
+which a training program asks where it waits for the GPU anyway.
 """
 from __future__ import annotations
 

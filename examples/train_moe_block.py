@@ -11,6 +11,7 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
+from combine_persistent_warp_gb300 import ops  # noqa: E402
 from combine_persistent_warp_gb300.training import MoEBlock  # noqa: E402
 
 
@@ -37,6 +38,8 @@ def train(steps: int = 60, tokens: int = 2048, E: int = 8, H: int = 256, I: int 
                 p.copy_(m)
         losses.append(loss.detach())
     losses = torch.stack(losses).tolist()
+    if status := ops.get_error():
+        raise RuntimeError(f"device status {status}")
     return block, losses[0], losses[-1]
 
 
@@ -48,7 +51,7 @@ def serve(block, tokens: int = 512):
     layer = block.serving_layer(tokens)
     fp8 = block.serve(layer, x).float() - x.float()
     torch.cuda.synchronize()
-    status = layer.get_error()
+    status = layer.get_error() or ops.get_error()
     layer.close()
     if status:
         raise RuntimeError(f"device status {status}")

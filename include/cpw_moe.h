@@ -311,7 +311,8 @@ int moe_layer_norm(int T, int H, const void *x, int64_t ldx, int dtype, const vo
 
 /* Layer norm written as the FP8 rows and 1x128 scales that moe_forward reads: q [T][H] e4m3,
  * sf [T][H/128] = max(amax, 1e-4) / 448 of each group of 128, or with pow2_scales = 1 the
- * smallest power of two at or above it (what the block-scaled kernel needs).  H % 128 == 0;
+ * smallest power of two at or above it (what the block-scaled kernel needs).  Codes are y times the scale's reciprocal: beside scales that
+ * are no powers of two they may be one step off the quotient's.  H % 128 == 0;
  * x, weight, bias and q 16-byte aligned, rows of x too. */
 int moe_layer_norm_fp8(int T, int H, const void *x, int64_t ldx, int dtype, const void *weight, const void *bias,
                        int w_dtype, float eps, int pow2_scales, uint8_t *q, float *sf, void *stream);
@@ -350,7 +351,8 @@ int moe_expert_order(int T, int topk, int E, const int64_t *topk_idx, int32_t *o
                      int32_t *status, void *workspace, uint64_t workspace_bytes, void *stream);
 
 /* out[rows[t][j]] = x[t] for every slot with a row in [0, M); the rows of out [M][H] from
- * offsets[E] on are zeroed.  Its gradient is moe_combine_rows with w = NULL. */
+ * offsets[E] on are zeroed.  rows and offsets are an order as moe_expert_order gives it: every row
+ * before offsets[E] has its slot (one that had none would keep what out held), none from there on has.  Its gradient is moe_combine_rows with w = NULL. */
 int moe_gather_rows(int T, int topk, int H, int E, int64_t M, const void *x, int64_t ldx, int dtype,
                     const int32_t *rows, const int32_t *offsets, void *out, void *stream);
 
@@ -360,7 +362,7 @@ int moe_combine_rows(int T, int topk, int H, int64_t M, const void *y, int dtype
                      void *out, void *stream);
 
 /* Gradients of moe_combine_rows: dy[rows[t][j]] = w[t][j] * dout[t] (rows of dy [M][H] from offsets[E]
- * on are zeroed) and dw[t][j] = <dout[t], y[rows[t][j]]> (0 in a slot without a row; NULL: not
+ * on are zeroed; rows and offsets as in moe_gather_rows) and dw[t][j] = <dout[t], y[rows[t][j]]> (0 in a slot without a row; NULL: not
  * written).  No two slots may have the same row. */
 int moe_combine_rows_backward(int T, int topk, int H, int E, int64_t M, const void *dout, int64_t lddout, const void *y,
                               int dtype, const int32_t *rows, const float *w, const int32_t *offsets, void *dy,
@@ -379,7 +381,7 @@ int moe_combine_rows_backward(int T, int topk, int H, int E, int64_t M, const vo
  * moe_grouped_mm_dx need theirs (one size serves both) where a small batch is split along the
  * contraction; 0 bytes otherwise.  Results do not depend on anything but the arguments: equal
  * inputs give equal bits.  The tensor core adds products to a 32-bit sum
- * by truncation, so an fp32 dw is a few 1e-6 off over a thousand rows. */
+ * by truncation, so an fp32 dw is about 1e-6 off over a thousand rows and 2e-5 over 16000. */
 int moe_grouped_mm_workspace(int64_t M, int E, int N, int K, uint64_t *bytes);
 int moe_grouped_mm(int64_t M, int E, int N, int K, const void *x, int64_t ldx, const void *w, const int32_t *offsets,
                    void *out, int64_t ldo, int dtype, void *workspace, uint64_t workspace_bytes, void *stream);
