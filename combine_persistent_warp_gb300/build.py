@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcpw_moe.so")
 OPS = os.path.join(PKG, "_ops.so")
 SOURCES = ["api.cu", "routing.cu", "ffn.cu", "ffn_bs.cu", "noalloc.cu", "norm.cu", "router.cu",
-           "rows.cu", "grouped_mm.cu"]
+           "rows.cu", "grouped_mm.cu", "rms_norm.cu", "scores.cu", "swiglu.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                 "-I" + os.path.join(ROOT, "include")]

@@ -596,6 +596,229 @@ PyObject *grouped_dw(Args a)
     return a[3];
 }
 
+// ------------------------------------------------------------------ RMS norm -------------
+// A norm's weight [H] (or None): of x's type or fp32.
+Affine norm_weight(PyObject *weight, int64_t H, const First &f) { return affine(weight, Py_None, H, f); }
+
+struct Stream {
+    Matrix x, r;
+    bool has;
+    at::Tensor h;   // the sum's buffer (undefined without a residual)
+};
+Stream residual_stream(const at::Tensor &x, PyObject *residual, const First &f)
+{
+    Stream s{matrix(x, "x", f), {}, !none(residual), {}};
+    if (s.has)
+        s.r = matrix(tensor(residual, "residual"), "residual", f, s.x.rows, s.x.width);
+    return s;
+}
+
+// (x, weight, eps, residual)
+PyObject *rms_norm(Args a)
+{
+    const at::Tensor &x = tensor(a[0], "x");
+    const First f = first(x, "x");
+    Stream st = residual_stream(x, a[3], f);
+    const Matrix &m = st.x;
+    const Affine w = norm_weight(a[1], m.width, f);
+    const float eps = real(a[2]);
+    at::Tensor y = make({m.rows, m.width}, f.type, f.dev), rstd = make({m.rows}, at::kFloat, f.dev);
+    if (st.has)
+        st.h = make({m.rows, m.width}, f.type, f.dev);
+    check(moe_rms_norm(count(m.rows, "x"), count(m.width, "x"), m.p, m.ld, st.r.p, st.r.ld, f.dtype, w.weight, w.dtype, eps,
+                       st.has ? st.h.data_ptr() : nullptr, y.data_ptr(), rstd.data_ptr<float>(), current_stream(f.dev)),
+          "moe_rms_norm");
+    return tuple_of({y, rstd, st.has ? st.h : x});
+}
+
+// (x, weight, eps, residual, pow2_scales)
+PyObject *rms_norm_fp8(Args a)
+{
+    const at::Tensor &x = tensor(a[0], "x");
+    const First f = first(x, "x");
+    Stream st = residual_stream(x, a[3], f);
+    const Matrix &m = st.x;
+    const Affine w = norm_weight(a[1], m.width, f);
+    const float eps = real(a[2]);
+    const bool pow2 = truth(a[4]);
+    at::Tensor q = make({m.rows, m.width}, at::kByte, f.dev), sf = make({m.rows, m.width / 128}, at::kFloat, f.dev);
+    if (st.has)
+        st.h = make({m.rows, m.width}, f.type, f.dev);
+    check(moe_rms_norm_fp8(count(m.rows, "x"), count(m.width, "x"), m.p, m.ld, st.r.p, st.r.ld, f.dtype, w.weight, w.dtype, eps, pow2,
+                           st.has ? st.h.data_ptr() : nullptr, q.data_ptr<uint8_t>(), sf.data_ptr<float>(), current_stream(f.dev)),
+          "moe_rms_norm_fp8");
+    return tuple_of({q, sf, st.has ? st.h : x});
+}
+
+// (dy, h, weight, rstd, dh, params fp32, dweight wanted)
+PyObject *rms_norm_backward(Args a)
+{
+    const at::Tensor &h = tensor(a[1], "h");
+    const First f = first(h, "h");
+    const Matrix m = matrix(h, "h", f), d = matrix(tensor(a[0], "dy"), "dy", f, m.rows, m.width);
+    Affine w = norm_weight(a[2], m.width, f);
+    if (none(a[2]) && truth(a[5])) {
+        w.type = at::kFloat;
+        w.dtype = MOE_F32;
+    }
+    const void *rstd = flat(tensor(a[3], "rstd"), "rstd", {m.rows}, at::kFloat, f.dev);
+    Matrix dh{};
+    if (!none(a[4]))
+        dh = matrix(tensor(a[4], "dh"), "dh", f, m.rows, m.width);
+    const int T = count(m.rows, "h"), H = count(m.width, "h");
+    const bool want = truth(a[6]);
+    uint64_t need = 0;
+    if (want)
+        check(moe_rms_norm_backward_workspace(T, H, &need), "moe_rms_norm_backward_workspace");
+    const Workspace ws(need);
+    at::Tensor dx = make({m.rows, m.width}, f.type, f.dev), dweight;   // (an undefined tensor is None)
+    if (want)
+        dweight = make({m.width}, w.type, f.dev);
+    check(moe_rms_norm_backward(T, H, d.p, d.ld, m.p, m.ld, none(a[4]) ? nullptr : dh.p, dh.ld, f.dtype, w.weight, w.dtype,
+                                static_cast<const float *>(rstd), dx.data_ptr(), want ? dweight.data_ptr() : nullptr, ws.get(), need,
+                                current_stream(f.dev)),
+          "moe_rms_norm_backward");
+    return tuple_of({dx, dweight});
+}
+
+// ------------------------------------------------------------------ scores ---------------
+// (logits, topk, score, bias, groups, topk_groups, group_top, renormalize, scale, token_mask)
+PyObject *route_scores(Args a)
+{
+    const at::Tensor &l = tensor(a[0], "logits");
+    const First f = first(l, "logits");
+    const Matrix m = matrix(l, "logits", f);
+    const int k = small(a[1], "topk"), score = small(a[2], "score");
+    const void *bias = flat_or_null(a[3], "bias", {m.width}, at::kFloat, f.dev);
+    const int groups = small(a[4], "groups"), kept = small(a[5], "topk_groups"), top = small(a[6], "group_top");
+    const bool renorm = truth(a[7]);
+    const float scale = real(a[8]);
+    const void *mask = flat_or_null(a[9], "token_mask", {m.rows}, at::kBool, f.dev);
+    at::Tensor idx = make({m.rows, std::max(k, 0)}, at::kLong, f.dev), w = make({m.rows, std::max(k, 0)}, at::kFloat, f.dev);
+    check(moe_route_scores(count(m.rows, "logits"), count(m.width, "logits"), k, m.p, m.ld, f.dtype, score, static_cast<const float *>(bias),
+                           groups, kept, top, static_cast<const uint8_t *>(mask), renorm, scale, idx.data_ptr<int64_t>(),
+                           w.data_ptr<float>(), current_stream(f.dev)),
+          "moe_route_scores");
+    return tuple_of({idx, w});
+}
+
+// (dw, idx, w, logits, score, renormalize, scale)
+PyObject *route_scores_backward(Args a)
+{
+    const at::Tensor &l = tensor(a[3], "logits"), &idx = slots(a[1]);
+    const First f = first(l, "logits");
+    const Matrix m = matrix(l, "logits", f);
+    const int64_t k = idx.size(1);
+    const void *pi = flat(idx, "idx", {m.rows, k}, at::kLong, f.dev);
+    const void *pw = flat(tensor(a[2], "w"), "w", {m.rows, k}, at::kFloat, f.dev);
+    const void *pd = flat(tensor(a[0], "dw"), "dw", {m.rows, k}, at::kFloat, f.dev);
+    const int score = small(a[4], "score");
+    const bool renorm = truth(a[5]);
+    const float scale = real(a[6]);
+    at::Tensor d = make({m.rows, m.width}, f.type, f.dev);
+    check(moe_route_scores_backward(count(m.rows, "logits"), count(m.width, "logits"), count(k, "idx"), static_cast<const float *>(pd),
+                                    static_cast<const int64_t *>(pi), static_cast<const float *>(pw), m.p, m.ld, f.dtype, score, renorm,
+                                    scale, d.data_ptr(), current_stream(f.dev)),
+          "moe_route_scores_backward");
+    return THPVariable_Wrap(d);
+}
+
+// ------------------------------------------------------------------ activation, 8 bits ---
+int64_t scale_groups(int64_t width) { return (width + 31) / 32; }
+
+// The halves of rows of gate and up.
+int64_t half_of(int64_t width, const char *name)
+{
+    if (width < 2 || width % 2 != 0)
+        throw ValueErr(std::string(name) + ": width " + std::to_string(width) + " is not that of gate and up");
+    return width / 2;
+}
+
+// (gu, checkpoint wanted)
+PyObject *swiglu(Args a)
+{
+    const at::Tensor &gu = tensor(a[0], "gu");
+    const First f = first(gu, "gu");
+    const Matrix m = matrix(gu, "gu", f);
+    const int64_t I = half_of(m.width, "gu");
+    const bool keep = truth(a[1]);
+    at::Tensor act = make({m.rows, I}, f.type, f.dev), codes, scales;
+    if (keep) {
+        codes = make({m.rows, 2 * I}, at::kChar, f.dev);
+        scales = make({m.rows, 2 * scale_groups(I)}, at::kByte, f.dev);
+    }
+    check(moe_swiglu(m.rows, count(I, "gu"), m.p, m.ld, f.dtype, act.data_ptr(), keep ? codes.data_ptr<int8_t>() : nullptr,
+                     keep ? scales.data_ptr<uint8_t>() : nullptr, current_stream(f.dev)),
+          "moe_swiglu");
+    return keep ? tuple_of({act, codes, scales}) : THPVariable_Wrap(act);
+}
+
+// (dact, gu)
+PyObject *swiglu_backward(Args a)
+{
+    const at::Tensor &gu = tensor(a[1], "gu");
+    const First f = first(gu, "gu");
+    const Matrix m = matrix(gu, "gu", f);
+    const int64_t I = half_of(m.width, "gu");
+    const Matrix d = matrix(tensor(a[0], "dact"), "dact", f, m.rows, I);
+    at::Tensor dgu = make({m.rows, 2 * I}, f.type, f.dev);
+    check(moe_swiglu_backward(m.rows, count(I, "gu"), d.p, d.ld, m.p, m.ld, nullptr, nullptr, f.dtype, dgu.data_ptr(), nullptr,
+                              current_stream(f.dev)),
+          "moe_swiglu_backward");
+    return THPVariable_Wrap(dgu);
+}
+
+// (dact, codes, scales)
+PyObject *swiglu_checkpoint_backward(Args a)
+{
+    const at::Tensor &da = tensor(a[0], "dact");
+    const First f = first(da, "dact");
+    const Matrix d = matrix(da, "dact", f);
+    const int64_t I = d.width;
+    const void *codes = flat(tensor(a[1], "codes"), "codes", {d.rows, 2 * I}, at::kChar, f.dev);
+    const void *scales = flat(tensor(a[2], "scales"), "scales", {d.rows, 2 * scale_groups(I)}, at::kByte, f.dev);
+    at::Tensor dgu = make({d.rows, 2 * I}, f.type, f.dev), act = make({d.rows, I}, f.type, f.dev);
+    check(moe_swiglu_backward(d.rows, count(I, "dact"), d.p, d.ld, nullptr, 0, static_cast<const int8_t *>(codes),
+                              static_cast<const uint8_t *>(scales), f.dtype, dgu.data_ptr(), act.data_ptr(), current_stream(f.dev)),
+          "moe_swiglu_backward");
+    return tuple_of({dgu, act});
+}
+
+// (x)
+PyObject *checkpoint_rows(Args a)
+{
+    const at::Tensor &x = tensor(a[0], "x");
+    const First f = first(x, "x");
+    const Matrix m = matrix(x, "x", f);
+    at::Tensor codes = make({m.rows, m.width}, at::kChar, f.dev), scales = make({m.rows, scale_groups(m.width)}, at::kByte, f.dev);
+    check(moe_checkpoint_rows(m.rows, count(m.width, "x"), m.p, m.ld, f.dtype, codes.data_ptr<int8_t>(), scales.data_ptr<uint8_t>(),
+                              current_stream(f.dev)),
+          "moe_checkpoint_rows");
+    return tuple_of({codes, scales});
+}
+
+// (codes, scales, moe_dtype)
+PyObject *restore_rows(Args a)
+{
+    const at::Tensor &codes = tensor(a[0], "codes");
+    if (codes.dim() != 2)
+        throw ValueErr("codes: shape " + shape_of(codes) + " is not [rows, width]");
+    if (!codes.is_cuda())
+        throw ValueErr("codes must be a CUDA tensor");
+    const int dev = codes.device().index();
+    if (dev != c10::cuda::current_device())
+        throw ValueErr("codes is not on the current device");
+    const int64_t M = codes.size(0), H = codes.size(1);
+    const void *pc = flat(codes, "codes", {M, H}, at::kChar, dev);
+    const void *ps = flat(tensor(a[1], "scales"), "scales", {M, scale_groups(H)}, at::kByte, dev);
+    const int dtype = small(a[2], "dtype");
+    at::Tensor x = make({M, H}, dtype == MOE_F32 ? at::kFloat : dtype == MOE_BF16 ? at::kBFloat16 : at::kHalf, dev);
+    check(moe_restore_rows(M, count(H, "codes"), static_cast<const int8_t *>(pc), static_cast<const uint8_t *>(ps), dtype, x.data_ptr(),
+                           current_stream(dev)),
+          "moe_restore_rows");
+    return THPVariable_Wrap(x);
+}
+
 // ()
 PyObject *get_error(Args)
 {
@@ -622,6 +845,16 @@ PyMethodDef methods[] = {CALL("layer_norm", 4, layer_norm),
                          CALL("grouped_mm", 4, grouped<true>),
                          CALL("grouped_mm_dx", 4, grouped<false>),
                          CALL("grouped_mm_dw", 6, grouped_dw),
+                         CALL("rms_norm", 4, rms_norm),
+                         CALL("rms_norm_fp8", 5, rms_norm_fp8),
+                         CALL("rms_norm_backward", 7, rms_norm_backward),
+                         CALL("route_scores", 10, route_scores),
+                         CALL("route_scores_backward", 7, route_scores_backward),
+                         CALL("swiglu", 2, swiglu),
+                         CALL("swiglu_backward", 2, swiglu_backward),
+                         CALL("swiglu_checkpoint_backward", 3, swiglu_checkpoint_backward),
+                         CALL("checkpoint_rows", 1, checkpoint_rows),
+                         CALL("restore_rows", 3, restore_rows),
                          CALL("get_error", 0, get_error),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -18,28 +18,11 @@
 #include "op_common.cuh"
 #include "moe_internal.cuh"
 #include "ptx.cuh"
+#include "router_common.cuh"
 
 using namespace cpw;
 
 namespace {
-
-constexpr int WARPS = 4;   // tokens of a block
-
-// Order-preserving 32-bit key of a logit: 0 for -inf (never chosen), the largest for NaN, the
-// same for both zeros.
-__device__ __forceinline__ uint32_t order_key(float f)
-{
-    if (f != f)
-        return 0xFFFFFFFFu;
-    if (f == -INFINITY)
-        return 0u;
-    const uint32_t u = __float_as_uint(f + 0.0f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t k)
-{
-    return k == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
 
 struct RouteArgs {
     int T, E, k;
@@ -451,25 +434,6 @@ void order_shape(long long n, int E, int &blocks, int &chunk)
     blocks = static_cast<int>(n <= 0 ? 1 : (n + c - 1) / c);
 }
 
-template <template <typename, int> class Launch, typename A>
-void by_width(int dtype, int E, const A &a, cudaStream_t s)
-{
-    with_dtype(dtype, [&](auto *t) {
-        using T = std::remove_pointer_t<decltype(t)>;
-        const int ipl = (E + 31) / 32;
-        if (ipl <= 1)
-            Launch<T, 1>::go(a, s);
-        else if (ipl <= 2)
-            Launch<T, 2>::go(a, s);
-        else if (ipl <= 4)
-            Launch<T, 4>::go(a, s);
-        else if (ipl <= 8)
-            Launch<T, 8>::go(a, s);
-        else
-            Launch<T, 32>::go(a, s);
-    });
-}
-
 template <typename T, int IPL>
 struct RouteLaunch {
     static void go(const RouteArgs &a, cudaStream_t s)
@@ -484,11 +448,6 @@ struct RouteBwdLaunch {
         route_backward_kernel<T, IPL><<<(a.T + WARPS - 1) / WARPS, WARPS * 32, 0, s>>>(a);
     }
 };
-
-bool route_sizes_ok(int T, int E, int topk, int dtype)
-{
-    return T >= 0 && T <= MAX_ROWS && E >= 1 && E <= 1024 && topk >= 1 && topk <= 32 && topk <= E && dtype_ok(dtype);
-}
 
 }  // namespace
 

@@ -33,6 +33,7 @@ COMBINE_KERNEL, COMBINE_IN_FFN, COMBINE_AUTO = 0, 1, 2   # values of OPT_COMBINE
 SCALE_FP32, SCALE_POW2, SCALE_AUTO = 0, 1, 2   # values of OPT_SCALE_MODE (default SCALE_AUTO)
 WEIGHTS_FP8, WEIGHTS_MXFP4 = 0, 1              # values of MoeInfo.weight_format
 F32, BF16, F16 = 0, 1, 2                       # moe_dtype of the operators' tensors
+SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1            # moe_score of the router over scores
 
 
 class MoeError(RuntimeError):
@@ -110,6 +111,16 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "moe_grouped_mm_dx": [I64, I, I, I, P, I64, P, P, P, I64, I, P, U64, P],
         "moe_grouped_mm_dw_workspace": [I64, I, I, I, ctypes.POINTER(U64)],
         "moe_grouped_mm_dw": [I64, I, I, I, P, I64, P, I64, P, P, I, I, I, P, U64, P],
+        "moe_rms_norm": [I, I, P, I64, P, I64, I, P, I, F, P, P, P, P],
+        "moe_rms_norm_fp8": [I, I, P, I64, P, I64, I, P, I, F, I, P, P, P, P],
+        "moe_rms_norm_backward_workspace": [I, I, ctypes.POINTER(U64)],
+        "moe_rms_norm_backward": [I, I, P, I64, P, I64, P, I64, I, P, I, P, P, P, P, U64, P],
+        "moe_route_scores": [I, I, I, P, I64, I, I, P, I, I, I, P, I, F, P, P, P],
+        "moe_route_scores_backward": [I, I, I, P, P, P, P, I64, I, I, I, F, P, P],
+        "moe_swiglu": [I64, I, P, I64, I, P, P, P, P],
+        "moe_swiglu_backward": [I64, I, P, I64, P, I64, P, P, I, P, P, P],
+        "moe_checkpoint_rows": [I64, I, P, I64, I, P, P, P],
+        "moe_restore_rows": [I64, I, P, P, I, P, P],
         "moe_ops_get_error": [ctypes.POINTER(I), P],
     }
     for name, args in sig.items():

@@ -285,8 +285,8 @@ int moe_route_noalloc(int T, int E, int topk, int R, const int64_t *topk_idx, ui
 
 /* ---------------------------------------------------------------------------------------
  * Operators around the expert layer, for training a block and for feeding the layer above:
- * layer norm, the router with its gradient, rows into and out of expert order, and products
- * with one weight per expert over ragged groups of rows.  They need no handle; the caller owns
+ * layer and RMS norm, routers with their gradients, rows into and out of expert order, products
+ * with one weight per expert over ragged groups of rows, the experts' activation and 8-bit checkpoints.  They need no handle; the caller owns
  * every buffer, workspaces included (the *_workspace calls say how many bytes).  All are
  * asynchronous on `stream`, which belongs to the current device, an sm_103 GPU
  * (MOE_ERR_UNSUPPORTED_DEVICE otherwise), allocate nothing, and may be captured into a graph.
@@ -391,6 +391,68 @@ int moe_grouped_mm_dw_workspace(int64_t M, int E, int N, int K, uint64_t *bytes)
 int moe_grouped_mm_dw(int64_t M, int E, int N, int K, const void *dy, int64_t lddy, const void *x, int64_t ldx,
                       const int32_t *offsets, void *dw, int dtype, int dw_dtype, int accumulate, void *workspace,
                       uint64_t workspace_bytes, void *stream);
+
+/* RMS norm of each of T rows with the residual's addition: h = x + residual, rounded to their type (the
+ * residual stream, written to h [T][H]; without a residual, NULL, h is not written and stands for x),
+ * rstd = 1 / sqrt(sum(h^2)/H + eps) in fp32, y = h * rstd * weight [T][H] of x's type.  weight [H] is of
+ * w_dtype (x's type or MOE_F32) or NULL; rstd [T] fp32 (NULL: not written) is what the backward call reads.
+ * 1 <= H <= 16384. */
+int moe_rms_norm(int T, int H, const void *x, int64_t ldx, const void *residual, int64_t ldr, int dtype, const void *weight,
+                 int w_dtype, float eps, void *h, void *y, float *rstd, void *stream);
+
+/* The same written as the FP8 rows and 1x128 scales that moe_forward reads (see moe_layer_norm_fp8).
+ * H % 128 == 0; x, residual, weight, h and q 16-byte aligned, rows of x and residual too. */
+int moe_rms_norm_fp8(int T, int H, const void *x, int64_t ldx, const void *residual, int64_t ldr, int dtype, const void *weight,
+                     int w_dtype, float eps, int pow2_scales, void *h, uint8_t *q, float *sf, void *stream);
+
+/* Gradients of moe_rms_norm from h (x where there was no residual): dx [T][H] of its type, of x and of the
+ * residual alike, dh [T][H] (the gradient of h from elsewhere; NULL: none) added to it, and the sums
+ * over the rows dweight [H] of w_dtype (may be NULL).  Sums as in moe_layer_norm_backward; the workspace
+ * is needed when dweight is asked for (16-byte aligned). */
+int moe_rms_norm_backward_workspace(int T, int H, uint64_t *bytes);
+int moe_rms_norm_backward(int T, int H, const void *dy, int64_t lddy, const void *h, int64_t ldh, const void *dh, int64_t lddh,
+                          int dtype, const void *weight, int w_dtype, const float *rstd, void *dx, void *dweight, void *workspace,
+                          uint64_t workspace_bytes, void *stream);
+
+/* The router over scores s of the logits ([T][E], rows ld apart): sigmoid, or softmax over all experts.
+ * The choice goes by c = s + bias (fp32 [E], NULL: none).  With groups > 1, of E/groups neighbouring
+ * experts each, a group's score is the sum of its group_top (1 or 2) largest c, the topk_groups best
+ * groups stay, and the topk experts with the largest c are chosen from theirs, in descending order; ties go
+ * to the lowest group and expert.  c and its sums are compared as computed in 64 bits.  The gate weights are
+ * scale * s, or with renormalize = 1 scale * s / sum of s over the chosen ones.  -inf, NaN, fewer
+ * candidates than topk, and token_mask as in moe_route_topk (a bias of -inf excludes its expert).
+ * E <= 1024, topk <= 32, groups <= 32 and a divisor of E, topk <= topk_groups * E/groups, scale finite and
+ * not 0. */
+enum moe_score { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
+int moe_route_scores(int T, int E, int topk, const void *logits, int64_t ld, int dtype, int score, const float *bias, int groups,
+                     int topk_groups, int group_top, const uint8_t *token_mask, int renormalize, float scale, int64_t *topk_idx,
+                     float *topk_w, void *stream);
+
+/* Gradient of the logits ([T][E], of `dtype`) from that of the gate weights, dw [T][topk] fp32, with the
+ * indices and weights that the forward call gave, and its score, renormalize and scale.  The choice is
+ * constant.  logits is not read for renormalised softmax scores (may be NULL).  dw in a slot of
+ * index -1 is not read. */
+int moe_route_scores_backward(int T, int E, int topk, const float *dw, const int64_t *topk_idx, const float *topk_w,
+                              const void *logits, int64_t ld, int dtype, int score, int renormalize, float scale, void *dlogits,
+                              void *stream);
+
+/* The experts' activation over rows of gate and up, gu [M][2*I] (gate first): act = silu(gate) * up, [M][I],
+ * in fp32 and rounded once.  With codes and scales (both or neither) gate and up are also kept in 8 bits
+ * for the backward call: codes [M][2*I], scales [M][2*ceil(I/32)].  The format (of MX blocks with INT8
+ * elements): 32 neighbours of a row (of gate, of up; the last group may be shorter) have a byte b, and a code n
+ * stands for n * 2^(b - 133); b = 127 + floor(log2 of the largest magnitude), at least 7; n is the nearest in
+ * -127 .. 127, ties to even.  A NaN or an infinity makes its group NaN (b = 255). */
+int moe_swiglu(int64_t M, int I, const void *gu, int64_t ldg, int dtype, void *act, int8_t *codes, uint8_t *scales, void *stream);
+
+/* Gradient of moe_swiglu's gate and up, dgu [M][2*I] of `dtype`, from dact [M][I] and either gu or the codes
+ * and scales that stand for it (the other NULL); act [M][I] (NULL: not wanted) gets the activation again. */
+int moe_swiglu_backward(int64_t M, int I, const void *dact, int64_t ldd, const void *gu, int64_t ldg, const int8_t *codes,
+                        const uint8_t *scales, int dtype, void *dgu, void *act, void *stream);
+
+/* Rows x [M][H] in the 8-bit format of moe_swiglu, codes [M][H] and scales [M][ceil(H/32)], and back (any byte
+ * and code; rounded to `dtype`).  M <= 2^30, and H and I <= 2^20 here and in the calls above. */
+int moe_checkpoint_rows(int64_t M, int H, const void *x, int64_t ldx, int dtype, int8_t *codes, uint8_t *scales, void *stream);
+int moe_restore_rows(int64_t M, int H, const int8_t *codes, const uint8_t *scales, int dtype, void *x, void *stream);
 
 /* Waits for `stream`, then returns and clears the sticky status of the operators' device-side
  * waits on the current device: MOE_OK, or MOE_ERR_TIMEOUT if a wait of a grouped product ran
