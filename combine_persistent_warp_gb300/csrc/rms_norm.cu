@@ -27,18 +27,37 @@ struct RmsArgs {
 };
 
 // ------------------------------------------------------------------ forward -------------
+// x + r in x's type, as the stream keeps it.
+template <typename T, int P>
+__device__ __forceinline__ void add_residual(float2 (&f)[P], const float2 (&r)[P])
+{
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const float2 v = add2(f[i], r[i]);
+        if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+            const __nv_bfloat162 h = __float22bfloat162_rn(v);
+            f[i] = pair_of<T>(&h.x);
+        } else {
+            f[i] = make_float2(to_f<T>(from_f<T>(v.x)), to_f<T>(from_f<T>(v.y)));
+        }
+    }
+}
+
 // The row held in f (zeros past its end): its statistic and outputs; w: the thread's columns of the weight.
-template <typename T, int V, int VPT, bool FP8, bool WARP>
-__device__ __forceinline__ void rms_row(const RmsArgs &a, int row, float2 (&f)[PAIRS<V, VPT>], const float2 (&w)[PAIRS<V, VPT>], float *red)
+// `after_read` runs once every thread has its row in registers.
+template <typename T, int V, int VPT, bool FP8, bool WARP, bool LEAD, typename F>
+__device__ __forceinline__ void rms_row(const RmsArgs &a, int row, int lead, float2 (&f)[PAIRS<V, VPT>], const float2 (&w)[PAIRS<V, VPT>],
+                                        float *red, int slot, F after_read)
 {
     constexpr int P = PAIRS<V, VPT>;
-    const int packs = a.H / V, t = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
+    const int packs = packs_of<V, LEAD>(a.H, lead), t = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
     float2 acc = both(0.0f);
 #pragma unroll
     for (int i = 0; i < P; ++i)
         acc = fma2(f[i], f[i], acc);
     float s[1] = {acc.x + acc.y};
-    row_sum<WARP>(s, red, 0);
+    row_sum<WARP>(s, red, slot);
+    after_read();
     const float rstd = 1.0f / sqrtf(s[0] / static_cast<float>(a.H) + a.eps);
     if (t == 0 && a.rstd)
         a.rstd[row] = rstd;
@@ -48,24 +67,12 @@ __device__ __forceinline__ void rms_row(const RmsArgs &a, int row, float2 (&f)[P
     if constexpr (FP8)
         put_fp8<V, VPT>(a.q + static_cast<size_t>(row) * a.H, a.sf + static_cast<size_t>(row) * (a.H / 128), f, t, step, packs, a.pow2);
     else
-        put<T, V, VPT>(static_cast<T *>(a.y) + static_cast<size_t>(row) * a.H, f, t, step, packs);
+        put<T, V, VPT, LEAD>(static_cast<T *>(a.y) + static_cast<size_t>(row) * a.H, f, t, step, packs, lead, a.H);
 }
 
-// x + r in x's type, as the stream keeps it.
-template <typename T, int V, int VPT>
-__device__ __forceinline__ void add_residual(float2 (&f)[PAIRS<V, VPT>], const Pack<T, V> (&q)[VPT])
-{
-    float2 r[PAIRS<V, VPT>];
-    unpack<T, V, VPT>(r, q);
-#pragma unroll
-    for (int i = 0; i < PAIRS<V, VPT>; ++i) {
-        const float2 v = add2(f[i], r[i]);
-        f[i] = make_float2(to_f<T>(from_f<T>(v.x)), to_f<T>(from_f<T>(v.y)));
-    }
-}
-
-// One row a block; or (WARP, rows of at most 1024 elements) one row a warp.
-template <typename T, int V, int VPT, bool FP8, bool WARP>
+// One row a block; or (WARP, rows of at most 1024 elements) one row a warp at a time, the next one on its
+// way.  The weight is loaded beside the first row, ahead of its sum.
+template <typename T, int V, int VPT, bool FP8, bool WARP, bool RES>
 __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : V * VPT == 32 ? 512 : 1024) rms_kernel(const RmsArgs a)
 {
     constexpr int P = PAIRS<V, VPT>;
@@ -73,20 +80,76 @@ __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : V * VPT == 32 ? 512 : 
     const int packs = a.H / V, t = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
     if constexpr (!WARP)
         clear_sums<1>(red);
-    const int row = WARP ? blockIdx.x * ROW_WARPS + (threadIdx.x >> 5) : blockIdx.x;
+    const T *x = static_cast<const T *>(a.x), *r = static_cast<const T *>(a.r);
+    int row = WARP ? blockIdx.x * ROW_WARPS + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= a.T)
         return;
-    Pack<T, V> q[VPT];
+    Pack<T, V> q[VPT], qr[RES ? VPT : 1];
+    fetch<T, V, VPT>(q, x + static_cast<size_t>(row) * a.ldx, t, step, packs);
+    if constexpr (RES)
+        fetch<T, V, VPT>(qr, r + static_cast<size_t>(row) * a.ldr, t, step, packs);
     float2 f[P], w[P];
-    fetch<T, V, VPT>(q, static_cast<const T *>(a.x) + static_cast<size_t>(row) * a.ldx, t, step, packs);
-    unpack<T, V, VPT>(f, q);
-    if (a.r) {
-        fetch<T, V, VPT>(q, static_cast<const T *>(a.r) + static_cast<size_t>(row) * a.ldr, t, step, packs);
-        add_residual<T, V, VPT>(f, q);
-        put<T, V, VPT>(static_cast<T *>(a.h) + static_cast<size_t>(row) * a.H, f, t, step, packs);
-    }
     load_columns<T, V, VPT>(w, a.weight, a.w32, 1.0f, t, step, packs);
-    rms_row<T, V, VPT, FP8, WARP>(a, row, f, w, red);
+    for (;;) {
+        unpack<T, V, VPT>(f, q);
+        if constexpr (RES) {
+            float2 g[P];
+            unpack<T, V, VPT>(g, qr);
+            add_residual<T>(f, g);
+            put<T, V, VPT>(static_cast<T *>(a.h) + static_cast<size_t>(row) * a.H, f, t, step, packs);
+        }
+        const int next = WARP ? row + gridDim.x * ROW_WARPS : a.T;
+        if (WARP && next < a.T) {
+            fetch<T, V, VPT>(q, x + static_cast<size_t>(next) * a.ldx, t, step, packs);
+            if constexpr (RES)
+                fetch<T, V, VPT>(qr, r + static_cast<size_t>(next) * a.ldr, t, step, packs);
+        }
+        rms_row<T, V, VPT, FP8, WARP, false>(a, row, 0, f, w, red, 0, [] {});
+        if (next >= a.T)
+            return;
+        row = next;
+    }
+}
+
+// Persistent blocks: rows copied AHEAD rows before their use, the weight kept in registers.
+template <typename T, int VPT, bool FP8, int AHEAD, bool LEAD, bool RES>
+__global__ void __launch_bounds__(512) rms_ring_kernel(const RmsArgs a)
+{
+    constexpr int V = 8, P = PAIRS<V, VPT>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float red[64];
+    Pack<T, V> *ring_x = reinterpret_cast<Pack<T, V> *>(smem), *ring_r = ring_x + AHEAD * VPT * blockDim.x;
+    const int lead = LEAD ? lead_of(static_cast<const T *>(a.x) + static_cast<size_t>(blockIdx.x) * a.ldx) : 0;
+    const int packs = packs_of<V, LEAD>(a.H, lead);
+    const bool cut = LEAD && cut_packs<V, VPT>(threadIdx.x, blockDim.x, lead, a.H);
+    const auto ahead = [&](int g, int row) {
+        fetch_ahead<T, V, VPT, LEAD>(ring_x, g, a.x, a.ldx, row, a.T, a.H, packs, lead);
+        if constexpr (RES)
+            fetch_ahead<T, V, VPT, LEAD>(ring_r, g, a.r, a.ldr, row, a.T, a.H, packs, lead);
+        copies_commit();
+    };
+#pragma unroll
+    for (int g = 0; g < AHEAD; ++g)
+        ahead(g, blockIdx.x + g * gridDim.x);
+    clear_sums<1>(red);
+    float2 w[P];
+    load_columns<T, V, VPT, LEAD>(w, a.weight, a.w32, 1.0f, threadIdx.x, blockDim.x, packs, lead, a.H);
+    int g = 0, slot = 0;
+    for (int row = blockIdx.x; row < a.T; row += gridDim.x, slot ^= 1) {
+        copies_wait<AHEAD - 1>();
+        float2 f[P];
+        from_ring<T, V, VPT>(f, ring_x, g);
+        if constexpr (RES) {
+            float2 r[P];
+            from_ring<T, V, VPT>(r, ring_r, g);
+            add_residual<T>(f, r);
+        }
+        clip<V, VPT>(f, threadIdx.x, blockDim.x, packs, LEAD && cut, lead, a.H);
+        if constexpr (RES)
+            put<T, V, VPT, LEAD>(static_cast<T *>(a.h) + static_cast<size_t>(row) * a.H, f, threadIdx.x, blockDim.x, packs, lead, a.H);
+        rms_row<T, V, VPT, FP8, false, LEAD>(a, row, lead, f, w, red, slot, [&] { ahead(g, row + AHEAD * gridDim.x); });
+        g = g == AHEAD - 1 ? 0 : g + 1;
+    }
 }
 
 // ------------------------------------------------------------------ backward ------------
@@ -98,91 +161,333 @@ struct RmsBwdArgs {
     int w32;
     const float *rstd;
     void *dx;
-    float *part;   // [blocks][pitch] sums of dy*xh over each block's rows (null: not wanted)
+    float *part;   // [blocks][pitch] sums of dy*xh over each block's rows (null: not wanted; LEAD: from their lead on)
     int pitch;
 };
 
-// Rows b, b + blocks, ... of block b: a thread keeps its columns' sums in registers over all of them.
-template <typename T, int V, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 : 512) rms_backward_kernel(const RmsBwdArgs a)
+// xh and a = dy*g of one row, their sum, and the columns' sums so far.
+template <int P>
+__device__ __forceinline__ float backward_sum(float2 (&xh)[P], float2 (&d)[P], const float2 (&w)[P], float2 (&dg)[P], float rstd)
+{
+    float2 acc = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        xh[i] = mul2(xh[i], both(rstd));
+        dg[i] = fma2(d[i], xh[i], dg[i]);
+        d[i] = mul2(d[i], w[i]);
+        acc = fma2(d[i], xh[i], acc);
+    }
+    return acc.x + acc.y;
+}
+template <int P>
+__device__ __forceinline__ void backward_out(float2 (&d)[P], const float2 (&xh)[P], float mean, float rstd)
+{
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        d[i] = mul2(fma2(xh[i], both(-mean), d[i]), both(rstd));
+}
+template <int P>
+__device__ __forceinline__ void add_all(float2 (&d)[P], const float2 (&v)[P])
+{
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        d[i] = add2(d[i], v[i]);
+}
+
+// Rows b, b + blocks, ... of block b: a thread keeps its columns' sums in registers over all of them, so
+// every tensor is read once from HBM.  AHEAD > 0: rows copied that many rows before use, and h and dy read from
+// shared memory twice (for the sum, then for dx) instead of held in registers between.
+template <typename T, int V, int VPT, int AHEAD, bool LEAD, bool DH>
+__global__ void __launch_bounds__(512) rms_backward_kernel(const RmsBwdArgs a)
 {
     constexpr int P = PAIRS<V, VPT>;
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[64];
-    const int t = threadIdx.x, step = blockDim.x, packs = a.H / V;
+    const int t = threadIdx.x, step = blockDim.x;
+    const int lead = LEAD ? lead_of(static_cast<const T *>(a.h) + static_cast<size_t>(blockIdx.x) * a.ldh) : 0;
+    const int packs = packs_of<V, LEAD>(a.H, lead);
+    const bool cut = LEAD && cut_packs<V, VPT>(t, step, lead, a.H);
     const float inv = 1.0f / static_cast<float>(a.H);
+    Pack<T, V> *ring_h = reinterpret_cast<Pack<T, V> *>(smem), *ring_d = ring_h + AHEAD * VPT * step, *ring_u = ring_d + AHEAD * VPT * step;
+    const auto ahead = [&](int g, int row) {
+        if constexpr (AHEAD > 0) {
+            fetch_ahead<T, V, VPT, LEAD>(ring_h, g, a.h, a.ldh, row, a.T, a.H, packs, lead);
+            fetch_ahead<T, V, VPT, LEAD>(ring_d, g, a.dy, a.lddy, row, a.T, a.H, packs, lead);
+            if constexpr (DH)
+                fetch_ahead<T, V, VPT, LEAD>(ring_u, g, a.dh, a.lddh, row, a.T, a.H, packs, lead);
+            copies_commit();
+        }
+    };
+#pragma unroll
+    for (int g = 0; g < AHEAD; ++g)
+        ahead(g, blockIdx.x + g * gridDim.x);
     clear_sums<1>(red);
     float2 w[P], dg[P];
-    load_columns<T, V, VPT>(w, a.weight, a.w32, 1.0f, t, step, packs);
+    load_columns<T, V, VPT, LEAD>(w, a.weight, a.w32, 1.0f, t, step, packs, lead, a.H);
 #pragma unroll
     for (int i = 0; i < P; ++i)
         dg[i] = both(0.0f);
-    int slot = 0;
+    int slot = 0, stage = 0;
+    float rstd = a.rstd[blockIdx.x];   // (no more blocks than rows)
     for (int row = blockIdx.x; row < a.T; row += gridDim.x, slot ^= 1) {
-        const float rstd = a.rstd[row];
-        Pack<T, V> q[VPT];
+        const int next = row + gridDim.x;
+        const float rstd1 = next < a.T ? a.rstd[next] : 0.0f;
         float2 xh[P], d[P];
-        fetch<T, V, VPT>(q, static_cast<const T *>(a.h) + static_cast<size_t>(row) * a.ldh, t, step, packs);
-        unpack<T, V, VPT>(xh, q);
-        fetch<T, V, VPT>(q, static_cast<const T *>(a.dy) + static_cast<size_t>(row) * a.lddy, t, step, packs);
-        unpack<T, V, VPT>(d, q);
-        float2 acc = both(0.0f);
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            xh[i] = mul2(xh[i], both(rstd));
-            dg[i] = fma2(d[i], xh[i], dg[i]);
-            d[i] = mul2(d[i], w[i]);
-            acc = fma2(d[i], xh[i], acc);
-        }
-        float s[1] = {acc.x + acc.y};
-        row_sum<WARP>(s, red, slot);
-        const float2 m = both(-s[0] * inv);
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-            d[i] = mul2(fma2(xh[i], m, d[i]), both(rstd));
-        if (a.dh) {
-            fetch<T, V, VPT>(q, static_cast<const T *>(a.dh) + static_cast<size_t>(row) * a.lddh, t, step, packs);
+        Pack<T, V> q[VPT];
+        if constexpr (AHEAD > 0) {
+            copies_wait<AHEAD - 1>();
+            from_ring<T, V, VPT>(xh, ring_h, stage);
+            from_ring<T, V, VPT>(d, ring_d, stage);
+            // what lies outside the row is not there: no products with it
+            clip<V, VPT>(xh, t, step, packs, LEAD && cut, lead, a.H);
+            clip<V, VPT>(d, t, step, packs, LEAD && cut, lead, a.H);
+        } else {
+            fetch<T, V, VPT>(q, static_cast<const T *>(a.h) + static_cast<size_t>(row) * a.ldh, t, step, packs);
             unpack<T, V, VPT>(xh, q);
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-                d[i] = add2(d[i], xh[i]);
+            fetch<T, V, VPT>(q, static_cast<const T *>(a.dy) + static_cast<size_t>(row) * a.lddy, t, step, packs);
+            unpack<T, V, VPT>(d, q);
+            if constexpr (DH)
+                fetch<T, V, VPT>(q, static_cast<const T *>(a.dh) + static_cast<size_t>(row) * a.lddh, t, step, packs);
         }
-        put<T, V, VPT>(static_cast<T *>(a.dx) + static_cast<size_t>(row) * a.H, d, t, step, packs);
+        float s[1] = {backward_sum(xh, d, w, dg, rstd)};
+        block_sum(s, red, slot);
+        if constexpr (AHEAD > 0) {
+            from_ring<T, V, VPT>(xh, ring_h, stage);
+            from_ring<T, V, VPT>(d, ring_d, stage);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                xh[i] = mul2(xh[i], both(rstd));
+                d[i] = mul2(d[i], w[i]);
+            }
+        }
+        backward_out(d, xh, s[0] * inv, rstd);
+        if constexpr (DH) {
+            if constexpr (AHEAD > 0)
+                from_ring<T, V, VPT>(xh, ring_u, stage);
+            else
+                unpack<T, V, VPT>(xh, q);
+            add_all(d, xh);
+        }
+        put<T, V, VPT, LEAD>(static_cast<T *>(a.dx) + static_cast<size_t>(row) * a.H, d, t, step, packs, lead, a.H);
+        if constexpr (AHEAD > 0) {   // (every value read above has been used by now)
+            ahead(stage, row + AHEAD * gridDim.x);
+            stage = stage == AHEAD - 1 ? 0 : stage + 1;
+        }
+        rstd = rstd1;
     }
     if (a.part)
         put<float, V, VPT>(a.part + static_cast<size_t>(blockIdx.x) * a.pitch, dg, t, step, packs);
     ptx::launch_dependents();
 }
 
-// ------------------------------------------------------------------ host side ------------
-template <typename T, bool FP8>
-void launch_rms(const RmsArgs &a, Rows rows, cudaStream_t s)
+// Rows of at most 1024 elements: one row a warp at a time, the next one on its way; the block's warps add
+// their columns' sums at the end, in order.
+template <typename T, int V, int VPT, bool DH>
+__global__ void __launch_bounds__(ROW_WARPS * 32) rms_backward_warp_kernel(const RmsBwdArgs a)
 {
-    const int packs = a.H / 8, warps = (a.T + ROW_WARPS - 1) / ROW_WARPS;
+    constexpr int P = PAIRS<V, VPT>;
+    struct alignas(16) Sums {
+        float v[32 * V * VPT];
+    };
+    static_assert(alignof(Sums) >= alignof(Pack<float, V>), "put() stores whole packs into them");
+    __shared__ Sums sums[ROW_WARPS];
+    const int packs = a.H / V, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float inv = 1.0f / static_cast<float>(a.H);
+    const T *h = static_cast<const T *>(a.h), *dy = static_cast<const T *>(a.dy), *dh = static_cast<const T *>(a.dh);
+    float2 w[P], dg[P];
+    load_columns<T, V, VPT>(w, a.weight, a.w32, 1.0f, lane, 32, packs);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        dg[i] = both(0.0f);
+    int row = blockIdx.x * ROW_WARPS + warp;
+    if (row < a.T) {
+        Pack<T, V> qh[VPT], qd[VPT], qu[DH ? VPT : 1];
+        const auto load = [&](int r) {
+            fetch<T, V, VPT>(qh, h + static_cast<size_t>(r) * a.ldh, lane, 32, packs);
+            fetch<T, V, VPT>(qd, dy + static_cast<size_t>(r) * a.lddy, lane, 32, packs);
+            if constexpr (DH)
+                fetch<T, V, VPT>(qu, dh + static_cast<size_t>(r) * a.lddh, lane, 32, packs);
+        };
+        load(row);
+        float rstd = a.rstd[row];
+        for (;;) {
+            float2 xh[P], d[P], u[DH ? P : 1];
+            unpack<T, V, VPT>(xh, qh);
+            unpack<T, V, VPT>(d, qd);
+            if constexpr (DH)
+                unpack<T, V, VPT>(u, qu);
+            const int next = row + gridDim.x * ROW_WARPS;
+            const float rs = rstd;
+            if (next < a.T) {
+                load(next);
+                rstd = a.rstd[next];
+            }
+            const float s = warp_sum(backward_sum(xh, d, w, dg, rs));
+            backward_out(d, xh, s * inv, rs);
+            if constexpr (DH)
+                add_all(d, u);
+            put<T, V, VPT>(static_cast<T *>(a.dx) + static_cast<size_t>(row) * a.H, d, lane, 32, packs);
+            if (next >= a.T)
+                break;
+            row = next;
+        }
+    }
+    if (a.part) {
+        put<float, V, VPT>(sums[warp].v, dg, lane, 32, 32 * VPT);
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.H; c += ROW_WARPS * 32) {
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < ROW_WARPS; ++k)
+                v += sums[k].v[c];
+            a.part[static_cast<size_t>(blockIdx.x) * a.pitch + c] = v;
+        }
+    }
+    ptx::launch_dependents();
+}
+
+// ------------------------------------------------------------------ host side ------------
+// Rows off the boundaries in packs with a lead: where the persistent kernels run.
+template <typename T>
+bool phased(int H, Rows rows)
+{
+    return rows == PHASED && H > 1024 && most_packs<T>(H, rows) <= 1024;
+}
+
+template <typename T, bool FP8, int AHEAD, bool LEAD, bool RES>
+bool try_rms_ring(const RmsArgs &a, int packs, int num_sms, cudaStream_t s)
+{
+    const int threads = round32((packs + 3) / 4);
+    size_t smem;
+    const int per_sm = ring_blocks<T, 8, 4>(threads, AHEAD, RES ? 2 : 1, smem);
+    // long batches only: every block has rows to copy ahead of
+    if (per_sm < 1 || a.T < AHEAD * per_sm * num_sms)
+        return false;
+    const auto kern = rms_ring_kernel<T, 4, FP8, AHEAD, LEAD, RES>;
+    if (!allow_smem(kern, smem))
+        return false;
+    kern<<<ring_grid(per_sm, num_sms), threads, smem, s>>>(a);
+    return true;
+}
+
+template <typename T, int V, int VPT, bool FP8, bool RES>
+void launch_rms_warps(const RmsArgs &a, int num_sms, cudaStream_t s)
+{
+    rms_kernel<T, V, VPT, FP8, true, RES><<<warp_blocks(a.T, 8, num_sms), ROW_WARPS * 32, 0, s>>>(a);
+}
+
+template <typename T, bool FP8, bool RES>
+void launch_rms(const RmsArgs &a, Rows rows, int num_sms, cudaStream_t s)
+{
+    constexpr int AHEAD = RES ? 3 : 4;
+    const bool few = a.T <= 2 * num_sms;
     if (rows == PACKED) {
-        if (packs <= 128)
-            rms_kernel<T, 8, 4, FP8, true><<<warps, ROW_WARPS * 32, 0, s>>>(a);
-        else
-            rms_kernel<T, 8, 4, FP8, false><<<a.T, round32((packs + 3) / 4), 0, s>>>(a);
+        // few rows: as many threads a row as it has packs, for latency
+        const int packs = a.H / 8;
+        if (packs <= 32)
+            launch_rms_warps<T, 8, 1, FP8, RES>(a, num_sms, s);
+        else if (packs <= 128 && !few)
+            launch_rms_warps<T, 8, 4, FP8, RES>(a, num_sms, s);
+        else if (few && packs <= 1024)
+            rms_kernel<T, 8, 1, FP8, false, RES><<<a.T, round32(packs), 0, s>>>(a);
+        else if (!try_rms_ring<T, FP8, AHEAD, false, RES>(a, packs, num_sms, s))
+            rms_kernel<T, 8, 4, FP8, false, RES><<<a.T, round32((packs + 3) / 4), 0, s>>>(a);
         return;
     }
     if constexpr (!FP8) {
-        if (a.H <= 1024)
-            rms_kernel<T, 1, 32, false, true><<<warps, ROW_WARPS * 32, 0, s>>>(a);
+        if (phased<T>(a.H, rows) && try_rms_ring<T, false, AHEAD, true, RES>(a, most_packs<T>(a.H, rows), num_sms, s))
+            return;
+        if (a.H <= 256)
+            launch_rms_warps<T, 1, 8, false, RES>(a, num_sms, s);
+        else if (a.H <= 1024)
+            launch_rms_warps<T, 1, 32, false, RES>(a, num_sms, s);
         else
-            rms_kernel<T, 1, 32, false, false><<<a.T, round32((a.H + 31) / 32), 0, s>>>(a);
+            rms_kernel<T, 1, 32, false, false, RES><<<a.T, round32((a.H + 31) / 32), 0, s>>>(a);
     }
 }
 
-int backward_blocks(int T, int num_sms) { return T < 2 * num_sms ? T : 2 * num_sms; }
-
+// The backward pass: kernel, blocks (each keeps a row of partial sums) and how they are found.
+enum Plan { WARPS_1, WARPS_4, RING, DIRECT };
 template <typename T>
-void launch_rms_backward(const RmsBwdArgs &a, Rows rows, int blocks, cudaStream_t s)
+Plan backward_plan(int T_, int H, Rows rows, int num_sms, int &blocks)
 {
-    const int packs = a.H / 8;
-    if (rows == PACKED)
-        rms_backward_kernel<T, 8, 4, false><<<blocks, round32((packs + 3) / 4), 0, s>>>(a);
+    if (H <= 256 || (H <= 1024 && (rows != PACKED || T_ > 2 * num_sms))) {
+        blocks = warp_blocks(T_, 3, num_sms);
+        return H <= 256 ? WARPS_1 : WARPS_4;
+    }
+    if (rows == PACKED || phased<T>(H, rows)) {
+        size_t smem;
+        const int packs = most_packs<T>(H, rows);
+        const int per_sm = packs <= 1024 ? ring_blocks<T, 8, 2>(round32((packs + 1) / 2), packs <= 512 ? 4 : 2, 3, smem)
+                                         : ring_blocks<T, 8, 4>(round32((packs + 3) / 4), 2, 3, smem);
+        if (per_sm >= 1 && T_ >= 4 * per_sm * num_sms) {
+            blocks = ring_grid(per_sm, num_sms);
+            return RING;
+        }
+    }
+    blocks = 2 * num_sms;
+    blocks = T_ < blocks ? T_ : blocks;
+    return DIRECT;
+}
+// (the workspace covers every alignment)
+template <typename T>
+int most_backward_blocks(int T_, int H, int num_sms)
+{
+    int most = 0;
+    for (const Rows rows : {PACKED, PHASED, ANY}) {
+        int b;
+        backward_plan<T>(T_, H, rows, num_sms, b);
+        most = b > most ? b : most;
+    }
+    return most;
+}
+
+template <typename T, int VPT, int AHEAD, bool LEAD, bool DH>
+bool launch_backward_ring(const RmsBwdArgs &a, int packs, int blocks, cudaStream_t s)
+{
+    const int threads = round32((packs + VPT - 1) / VPT);
+    size_t smem;
+    ring_blocks<T, 8, VPT>(threads, AHEAD, DH ? 3 : 2, smem);
+    const auto kern = rms_backward_kernel<T, 8, VPT, AHEAD, LEAD, DH>;
+    if (!allow_smem(kern, smem))
+        return false;
+    kern<<<blocks, threads, smem, s>>>(a);
+    return true;
+}
+
+template <typename T, bool DH>
+bool launch_rms_backward(const RmsBwdArgs &a, Rows rows, int num_sms, PartRows &part, cudaStream_t s)
+{
+    int blocks;
+    const Plan plan = backward_plan<T>(a.T, a.H, rows, num_sms, blocks);
+    const bool packed = rows == PACKED;
+    const int packs = most_packs<T>(a.H, rows);
+    constexpr int boundary = VEC<T>;
+    part = {a.part, blocks, a.pitch, plan == RING && !packed ? a.H % boundary : 0, boundary};
+    if (plan == RING && !packed)
+        return packs <= 512 ? launch_backward_ring<T, 2, 4, true, DH>(a, packs, blocks, s)
+                            : launch_backward_ring<T, 2, 2, true, DH>(a, packs, blocks, s);
+    if (plan == RING)
+        return packs <= 512    ? launch_backward_ring<T, 2, 4, false, DH>(a, packs, blocks, s)
+               : packs <= 1024 ? launch_backward_ring<T, 2, 2, false, DH>(a, packs, blocks, s)
+                               : launch_backward_ring<T, 4, 2, false, DH>(a, packs, blocks, s);
+    if (plan == WARPS_1 && packed)
+        rms_backward_warp_kernel<T, 8, 1, DH><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
+    else if (plan == WARPS_4 && packed)
+        rms_backward_warp_kernel<T, 8, 4, DH><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
+    else if (plan == DIRECT && packed && packs <= 1024)
+        rms_backward_kernel<T, 8, 2, 0, false, DH><<<blocks, round32((packs + 1) / 2), 0, s>>>(a);
+    else if (plan == DIRECT && packed)
+        rms_backward_kernel<T, 8, 4, 0, false, DH><<<blocks, round32((packs + 3) / 4), 0, s>>>(a);
+    else if (plan == WARPS_1)
+        rms_backward_warp_kernel<T, 1, 8, DH><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
+    else if (plan == WARPS_4)
+        rms_backward_warp_kernel<T, 1, 32, DH><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
+    else if (a.H <= 8192)
+        rms_backward_kernel<T, 1, 16, 0, false, DH><<<blocks, round32((a.H + 15) / 16), 0, s>>>(a);
     else
-        rms_backward_kernel<T, 1, 32, false><<<blocks, round32((a.H + 31) / 32), 0, s>>>(a);
+        rms_backward_kernel<T, 1, 32, 0, false, DH><<<blocks, round32((a.H + 31) / 32), 0, s>>>(a);
+    return true;
 }
 
 bool sizes_ok(int T, int H, int dtype, int w_dtype, const void *weight)
@@ -217,7 +522,9 @@ int moe_rms_norm(int T, int H, const void *x, int64_t ldx, const void *residual,
                                   residual ? rows_of(H, dtype, h, H) : PACKED),
                             worst(rows_of(H, dtype, y, H), affine_of(weight)));
     with_dtype(dtype, [&](auto *t) {
-        launch_rms<std::remove_pointer_t<decltype(t)>, false>(a, rows, static_cast<cudaStream_t>(stream));
+        using E = std::remove_pointer_t<decltype(t)>;
+        residual ? launch_rms<E, false, true>(a, rows, sms, static_cast<cudaStream_t>(stream))
+                 : launch_rms<E, false, false>(a, rows, sms, static_cast<cudaStream_t>(stream));
     });
     return launched();
 }
@@ -236,7 +543,9 @@ int moe_rms_norm_fp8(int T, int H, const void *x, int64_t ldx, const void *resid
     OP_DEVICE(sms);
     const RmsArgs a{T, H, x, residual, ldx, ldr, weight, w_dtype == MOE_F32 && dtype != MOE_F32, eps, h, nullptr, nullptr, q, sf, pow2_scales};
     with_dtype(dtype, [&](auto *t) {
-        launch_rms<std::remove_pointer_t<decltype(t)>, true>(a, PACKED, static_cast<cudaStream_t>(stream));
+        using E = std::remove_pointer_t<decltype(t)>;
+        residual ? launch_rms<E, true, true>(a, PACKED, sms, static_cast<cudaStream_t>(stream))
+                 : launch_rms<E, true, false>(a, PACKED, sms, static_cast<cudaStream_t>(stream));
     });
     return launched();
 }
@@ -246,7 +555,9 @@ int moe_rms_norm_backward_workspace(int T, int H, uint64_t *bytes)
     if (T < 0 || T > MAX_ROWS || H < 1 || H > MAX_H || !bytes)
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
-    *bytes = static_cast<uint64_t>(backward_blocks(T, sms)) * static_cast<uint64_t>(part_pitch(H)) * sizeof(float);
+    // enough for every element type
+    const int a = most_backward_blocks<float>(T, H, sms), b = most_backward_blocks<__nv_bfloat16>(T, H, sms);
+    *bytes = static_cast<uint64_t>(a > b ? a : b) * static_cast<uint64_t>(part_pitch(H)) * sizeof(float);
     return MOE_OK;
 }
 
@@ -270,14 +581,15 @@ int moe_rms_norm_backward(int T, int H, const void *dy, int64_t lddy, const void
         return MOE_ERR_INVALID_ARG;
     PartRows part{};
     if (T > 0) {
-        const int blocks = backward_blocks(T, sms);
         const RmsBwdArgs a{T, H, dy, h, dh, lddy, ldh, lddh, weight, w_dtype == MOE_F32 && dtype != MOE_F32, rstd, dx,
                            dweight ? static_cast<float *>(workspace) : nullptr, part_pitch(H)};
-        part = {a.part, blocks, a.pitch, 0, 8};
         const Rows rows = worst(worst(worst(rows_of(H, dtype, h, ldh), rows_of(H, dtype, dy, lddy)), rows_or_absent(H, dtype, dh, lddh)),
                                 worst(rows_of(H, dtype, dx, H), affine_of(weight)));
-        with_dtype(dtype, [&](auto *t) { launch_rms_backward<std::remove_pointer_t<decltype(t)>>(a, rows, blocks, s); });
-        if (launched() != MOE_OK)
+        const bool ok = with_dtype(dtype, [&](auto *t) {
+            using E = std::remove_pointer_t<decltype(t)>;
+            return dh ? launch_rms_backward<E, true>(a, rows, sms, part, s) : launch_rms_backward<E, false>(a, rows, sms, part, s);
+        });
+        if (!ok || launched() != MOE_OK)
             return MOE_ERR_CUDA;
     }
     if (dweight) {
