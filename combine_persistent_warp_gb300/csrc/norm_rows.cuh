@@ -13,51 +13,11 @@ namespace cpw {
 constexpr int MAX_H = 16384;   // as moe_create: a row fits one block's registers
 constexpr int ROW_WARPS = 4;   // rows of a block in the kernels of one row a warp
 
-// ------------------------------------------------------------------ elements in pairs ----
-// Two fp32 values an instruction: these kernels would otherwise be bound by issue, not by HBM.
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(r)
-        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
-    return reinterpret_cast<float2 &>(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(r)
-        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
-    return reinterpret_cast<float2 &>(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(r)
-        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
-          "l"(reinterpret_cast<unsigned long long &>(c)));
-    return reinterpret_cast<float2 &>(r);
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
 // ------------------------------------------------------------------ a thread's part of a row ----
 // VPT packs of V elements (V = 8: 16-byte accesses; V = 1: any alignment), pack j at position
 // t + j * step of the row for thread t of the `step` threads that share it; held as pairs.
 template <int V, int VPT>
 constexpr int PAIRS = V * VPT / 2;
-
-template <typename T>
-__device__ __forceinline__ float2 pair_of(const T *q)
-{
-    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-        const uint32_t u = *reinterpret_cast<const uint32_t *>(q);
-        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
-    } else {
-        return make_float2(to_f<T>(q[0]), to_f<T>(q[1]));
-    }
-}
 
 template <typename T, int V, int VPT>
 __device__ __forceinline__ void unpack(float2 (&f)[PAIRS<V, VPT>], const Pack<T, V> (&q)[VPT])

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -73,6 +74,61 @@ __device__ __forceinline__ void store_pack(T *p, const Pack<T, N> &v)
 #pragma unroll
         for (int i = 0; i < static_cast<int>(sizeof(T) * N / 16); ++i)
             reinterpret_cast<uint4 *>(p)[i] = u.q[i];
+    }
+}
+
+// ------------------------------------------------------------------ elements in pairs ----
+// Two fp32 values an instruction: what these kernels do to an element would otherwise be bound by issue,
+// not by HBM.
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return reinterpret_cast<float2 &>(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return reinterpret_cast<float2 &>(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
+          "l"(reinterpret_cast<unsigned long long &>(c)));
+    return reinterpret_cast<float2 &>(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+template <typename T>
+__device__ __forceinline__ float2 pair_of(const T *q)
+{
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        const uint32_t u = *reinterpret_cast<const uint32_t *>(q);
+        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+    } else {
+        return make_float2(to_f<T>(q[0]), to_f<T>(q[1]));
+    }
+}
+
+// A pair rounded to T and back in memory order.
+template <typename T>
+__device__ __forceinline__ void put_pair(T *q, float2 u)
+{
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        *reinterpret_cast<__nv_bfloat162 *>(q) = __float22bfloat162_rn(u);
+    } else if constexpr (std::is_same_v<T, __half>) {
+        *reinterpret_cast<__half2 *>(q) = __float22half2_rn(u);
+    } else {
+        q[0] = u.x;
+        q[1] = u.y;
     }
 }
 

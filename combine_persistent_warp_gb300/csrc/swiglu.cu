@@ -10,6 +10,7 @@
 // four neighbouring lanes hold a group of 32; rows that are not whole packs on 16-byte boundaries go
 // element by element, a group a warp access.
 #include <climits>
+#include <initializer_list>
 #include <type_traits>
 
 #include "op_common.cuh"
@@ -38,15 +39,31 @@ __device__ __forceinline__ float logistic(float g)
         return s;
     }
 }
-struct Grads {
-    float dg, du, act;
-};
+// The same of a pair, and the gradients of a pair of gates and ups (in place; d becomes the activation).
 template <typename T>
-__device__ __forceinline__ Grads gradients(float da, float g, float u)
+__device__ __forceinline__ float2 logistic2(float2 g)
 {
-    const float s = logistic<T>(g), t = g * s, du = da * t;
-    // s + t (1 - s)
-    return {da * u * fmaf(t, 1.0f - s, s), du, t * u};
+    if constexpr (std::is_same_v<T, float>) {
+        return make_float2(logistic<T>(g.x), logistic<T>(g.y));
+    } else {
+        float2 e = mul2(g, both(-1.44269504f));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+        e = add2(e, both(1.0f));
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+        return e;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void gradients(float2 &d, float2 &g, float2 &u)
+{
+    const float2 s = logistic2<T>(g), t = mul2(g, s), part = mul2(d, u);
+    u = mul2(t, u);                                                          // the activation
+    const float2 du = mul2(d, t);
+    g = mul2(part, fma2(t, fma2(s, both(-1.0f), both(1.0f)), s));             // s + t (1 - s)
+    d = u;
+    u = du;
 }
 
 // ------------------------------------------------------------------ 8 bits --------------
@@ -63,90 +80,217 @@ __device__ __forceinline__ float steps_per_one(uint32_t byte) { return __uint_as
 // X/64 of any byte
 __device__ __forceinline__ float step_of(uint32_t byte)
 {
-    if (byte == 255u)
-        return __uint_as_float(0x7FC00000u);
-    return __uint_as_float(byte > 6u ? (byte - 6u) << 23 : 1u << (byte + 16u));
+    const float low = __uint_as_float(0x00010000u << min(byte, 6u));   // (not a normal number)
+    const float v = byte > 6u ? __uint_as_float((byte - 6u) << 23) : low;
+    return byte == 255u ? __uint_as_float(0x7FC00000u) : v;
 }
 // n in the low byte: adding 1.5 * 2^23 rounds to the nearest whole number, ties to even.
+constexpr float ROUND = 12582912.0f;
 __device__ __forceinline__ uint32_t code_of(float v, float per_one)
 {
-    constexpr float BIG = 12582912.0f;
-    return __float_as_uint(fmaxf(fminf(fmaf(v, per_one, BIG), BIG + 127.0f), BIG - 127.0f));
+    return __float_as_uint(fmaxf(fminf(fmaf(v, per_one, ROUND), ROUND + 127.0f), ROUND - 127.0f));
 }
-__device__ __forceinline__ uint32_t four_codes(const float *v, float per_one)
+__device__ __forceinline__ uint32_t four_codes(float2 a, float2 b)
 {
-    const uint32_t lo = __byte_perm(code_of(v[0], per_one), code_of(v[1], per_one), 0x0040);
-    const uint32_t hi = __byte_perm(code_of(v[2], per_one), code_of(v[3], per_one), 0x0040);
+    const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
     return __byte_perm(lo, hi, 0x5410);
 }
-// Code k of a word: its byte, offset by 128, in the last bits of 2^23.
+// Codes 2k and 2k + 1 of a word whose bytes are offset by 128: in the last bits of 2^23.
 template <int K>
-__device__ __forceinline__ float value_of(uint32_t offset, float step)
+__device__ __forceinline__ float2 two_values(uint32_t offset, float step)
 {
-    return (__uint_as_float(__byte_perm(offset, 0x4B000000u, 0x7540 | K)) - 8388736.0f) * step;
-}
-__device__ __forceinline__ void eight_values(float (&v)[8], uint2 codes, float step)
-{
-    const uint32_t lo = codes.x ^ 0x80808080u, hi = codes.y ^ 0x80808080u;
-    v[0] = value_of<0>(lo, step);
-    v[1] = value_of<1>(lo, step);
-    v[2] = value_of<2>(lo, step);
-    v[3] = value_of<3>(lo, step);
-    v[4] = value_of<0>(hi, step);
-    v[5] = value_of<1>(hi, step);
-    v[6] = value_of<2>(hi, step);
-    v[7] = value_of<3>(hi, step);
+    const float2 v = make_float2(__uint_as_float(__byte_perm(offset, 0x4B000000u, 0x7540 | (2 * K))),
+                                 __uint_as_float(__byte_perm(offset, 0x4B000000u, 0x7540 | (2 * K + 1))));
+    return mul2(add2(v, both(-8388736.0f)), both(step));
 }
 
-// A thread's eight elements, packed: the group's four lanes agree on its byte; its codes.
-__device__ __forceinline__ uint2 keep_pack(const float (&v)[8], uint32_t &byte)
+// ------------------------------------------------------------------ a thread's elements ----
+// E neighbours: a pack of 8 (16-byte accesses; 32 bits: two), or of 16-bit types 16 (32-byte accesses, for rows
+// that are on such boundaries).
+template <typename T, int E>
+struct Elements {
+    static constexpr int BYTES = static_cast<int>(sizeof(T)) * E, WORDS = BYTES / 4;
+    union {
+        T v[E];
+        uint32_t w[WORDS];
+    };
+    __device__ Elements() {}
+};
+template <typename T, int E>
+__device__ __forceinline__ void load(Elements<T, E> &q, const T *p)
 {
-    uint32_t m = 0;
+    if constexpr (sizeof(T) == 2 && E == 16) {
+        asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=r"(q.w[0]), "=r"(q.w[1]), "=r"(q.w[2]), "=r"(q.w[3]), "=r"(q.w[4]), "=r"(q.w[5]), "=r"(q.w[6]), "=r"(q.w[7])
+            : "l"(p));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        m = max(m, magnitude(v[i]));
-    m = max(m, __shfl_xor_sync(ALL, m, 1));
-    m = max(m, __shfl_xor_sync(ALL, m, 2));
-    byte = scale_byte(m);
-    const float per_one = steps_per_one(byte);
-    return make_uint2(four_codes(v, per_one), four_codes(v + 4, per_one));
+        for (int i = 0; i < Elements<T, E>::WORDS / 4; ++i)
+            *reinterpret_cast<uint4 *>(&q.w[4 * i]) = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    }
+}
+template <typename T, int E>
+__device__ __forceinline__ void store(T *p, const Elements<T, E> &q)
+{
+    if constexpr (sizeof(T) == 2 && E == 16) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(q.w[0]), "r"(q.w[1]), "r"(q.w[2]), "r"(q.w[3]),
+                     "r"(q.w[4]), "r"(q.w[5]), "r"(q.w[6]), "r"(q.w[7])
+                     : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < Elements<T, E>::WORDS / 4; ++i)
+            reinterpret_cast<uint4 *>(p)[i] = make_uint4(q.w[4 * i], q.w[4 * i + 1], q.w[4 * i + 2], q.w[4 * i + 3]);
+    }
+}
+template <typename T, int E>
+__device__ __forceinline__ void zero(Elements<T, E> &q)
+{
+#pragma unroll
+    for (int i = 0; i < Elements<T, E>::WORDS; ++i)
+        q.w[i] = 0u;
+}
+template <typename T, int E>
+__device__ __forceinline__ void to_pairs(float2 (&f)[E / 2], const Elements<T, E> &q)
+{
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i)
+        f[i] = pair_of<T>(&q.v[2 * i]);
+}
+template <typename T, int E>
+__device__ __forceinline__ void store_pairs(T *p, const float2 (&f)[E / 2])
+{
+    Elements<T, E> q;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i)
+        put_pair<T>(&q.v[2 * i], f[i]);
+    store<T, E>(p, q);
 }
 
-template <typename T>
-__device__ __forceinline__ void unpack8(float (&f)[8], const Pack<T, 8> &q)
+template <int E>
+struct Codes {
+    uint32_t w[E / 4];
+};
+template <int E>
+__device__ __forceinline__ void store(int8_t *p, const Codes<E> &c)
 {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        f[i] = to_f<T>(q.v[i]);
+    if constexpr (E == 16)
+        *reinterpret_cast<uint4 *>(p) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+    else
+        *reinterpret_cast<uint2 *>(p) = make_uint2(c.w[0], c.w[1]);
 }
-template <typename T>
-__device__ __forceinline__ void store8(T *p, const float (&f)[8])
+template <int E>
+__device__ __forceinline__ Codes<E> load_codes(const int8_t *p)
 {
-    Pack<T, 8> q;
+    Codes<E> c;
+    if constexpr (E == 16)
+        *reinterpret_cast<uint4 *>(c.w) = __ldg(reinterpret_cast<const uint4 *>(p));
+    else
+        *reinterpret_cast<uint2 *>(c.w) = __ldg(reinterpret_cast<const uint2 *>(p));
+    return c;
+}
+template <int E>
+__device__ __forceinline__ void values_of(float2 (&f)[E / 2], const Codes<E> &c, float step)
+{
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        q.v[i] = from_f<T>(f[i]);
-    store_pack<T, 8>(p, q);
+    for (int i = 0; i < E / 4; ++i) {
+        const uint32_t offset = c.w[i] ^ 0x80808080u;
+        f[2 * i] = two_values<0>(offset, step);
+        f[2 * i + 1] = two_values<1>(offset, step);
+    }
+}
+
+// Codes and scale byte of the thread's elements, the same byte in the lanes of a group.  16-bit elements stay
+// in pairs as far as they can: the magnitudes (whole numbers order them) and the cut at 127 steps, which
+// in units of X is 127/64, a number of either type (of an fp16 group of subnormal numbers no value comes near it).
+template <typename T, int E>
+__device__ __forceinline__ Codes<E> keep(Elements<T, E> q, uint32_t &byte)
+{
+    constexpr int LANES = GROUP / E;
+    Codes<E> c;
+    if constexpr (sizeof(T) == 2) {
+        uint32_t m = q.w[0] & 0x7FFF7FFFu;
+#pragma unroll
+        for (int i = 1; i < E / 2; ++i)
+            m = __vmaxu2(m, q.w[i] & 0x7FFF7FFFu);
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1)
+            m = __vmaxu2(m, __shfl_xor_sync(ALL, m, o));
+        const uint16_t top = static_cast<uint16_t>(max(m & 0xFFFFu, m >> 16));
+        byte = scale_byte(__float_as_uint(to_f<T>(*reinterpret_cast<const T *>(&top))));
+        const float per_one = steps_per_one(byte);
+        if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+            const __nv_bfloat162 most = __float2bfloat162_rn(__uint_as_float(byte << 23 | 0x7E0000u));
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                __nv_bfloat162 &v = *reinterpret_cast<__nv_bfloat162 *>(&q.w[i]);
+                v = __hmax2(__hmin2(v, most), __hneg2(most));
+            }
+        } else {
+            const __half2 most = __float2half2_rn(__uint_as_float(byte << 23 | 0x7E0000u));
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                __half2 &v = *reinterpret_cast<__half2 *>(&q.w[i]);
+                v = __hmax2(__hmin2(v, most), __hneg2(most));
+            }
+        }
+        float2 f[E / 2];
+        to_pairs(f, q);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i)
+            f[i] = fma2(f[i], both(per_one), both(ROUND));
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i)
+            c.w[i] = four_codes(f[2 * i], f[2 * i + 1]);
+    } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            m = max(m, q.w[i] & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1)
+            m = max(m, __shfl_xor_sync(ALL, m, o));
+        byte = scale_byte(m);
+        const float per_one = steps_per_one(byte);
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+            const auto n = [&](int k) { return __uint_as_float(code_of(q.v[4 * i + k], per_one)); };
+            c.w[i] = four_codes(make_float2(n(0), n(1)), make_float2(n(2), n(3)));
+        }
+    }
+    return c;
 }
 
 // ------------------------------------------------------------------ where a thread works ----
-// Units (packs, or warps' chunks) of the rows in a line, `per_row` of them a row: a row's index is a
-// product's upper half (magic = floor(2^64 / per_row) + 1, exact while units * per_row < 2^64).
+// Units (threads' elements, or warps' chunks) of the rows in a line, `per_row` of them a row.  A block's first
+// unit is divided by products' upper halves (exact while units * per_row < 2^64), and its others are at most
+// THREADS past it.
 struct Units {
     long long count;
-    uint64_t magic;
+    uint64_t magic;      // floor(2^64 / per_row) + 1 (0: one a row)
+    uint32_t magic32;    // floor(2^32 / per_row) + 1
     int per_row;
 };
 Units units(long long rows, int per_row)
 {
-    return {rows * per_row, per_row == 1 ? 0ull : ~0ull / static_cast<uint64_t>(per_row) + 1, per_row};
+    const uint64_t d = static_cast<uint64_t>(per_row);
+    return {rows * per_row, per_row == 1 ? 0ull : ~0ull / d + 1, static_cast<uint32_t>((1ull << 32) / d + (d > 1)), per_row};
 }
-__device__ __forceinline__ long long row_of(const Units &u, long long i, int &within)
+// Unit `nth` of the block's `of`: its row, and where in the row it is.
+__device__ __forceinline__ long long row_of(const Units &u, int nth, int of, int &within)
 {
-    const long long row = u.magic ? static_cast<long long>(__umul64hi(static_cast<uint64_t>(i), u.magic)) : i;
-    within = static_cast<int>(i - row * u.per_row);
-    return row;
+    const unsigned long long first = static_cast<unsigned long long>(blockIdx.x) * of;
+    const unsigned long long row = u.magic ? __umul64hi(first, u.magic) : first;
+    const int x = static_cast<int>(first - row * u.per_row) + nth;
+    int more;
+    if (u.per_row >= THREADS)
+        more = x >= u.per_row;
+    else
+        more = u.per_row == 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), u.magic32));
+    within = x - more * u.per_row;
+    return static_cast<long long>(row) + more;
 }
+__device__ __forceinline__ bool there(const Units &u, int nth, int of) { return static_cast<long long>(blockIdx.x) * of + nth < u.count; }
 
 struct ActArgs {
     Units u;
@@ -159,84 +303,84 @@ struct ActArgs {
 };
 
 // ------------------------------------------------------------------ packs ---------------
-template <typename T, bool KEEP>
+template <typename T, int E, bool KEEP>
 __global__ void __launch_bounds__(THREADS) swiglu_pack_kernel(const ActArgs a)
 {
-    const long long i = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x;
+    constexpr int LANES = GROUP / E;
     int p;
-    const long long row = row_of(a.u, i, p);
-    const int c = p * 8;
-    const bool in = i < a.u.count && c < a.I;
-    float g[8], u[8];
+    const long long row = row_of(a.u, threadIdx.x, THREADS, p);
+    const int c = p * E;
+    const bool in = there(a.u, threadIdx.x, THREADS) && c < a.I;
+    Elements<T, E> qg, qu;
     if (in) {
         const T *src = static_cast<const T *>(a.gu) + row * a.ldg + c;
-        const Pack<T, 8> qg = load_pack<T, 8>(src), qu = load_pack<T, 8>(src + a.I);
-        unpack8(g, qg);
-        unpack8(u, qu);
+        load(qg, src);
+        load(qu, src + a.I);
     } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            g[k] = u[k] = 0.0f;
+        zero(qg);
+        zero(qu);
     }
     if constexpr (KEEP) {
         uint32_t bg, bu;
-        const uint2 cg = keep_pack(g, bg), cu = keep_pack(u, bu);
+        const Codes<E> cg = keep(qg, bg), cu = keep(qu, bu);
         if (in) {
             int8_t *codes = a.codes + row * 2 * a.I + c;
-            *reinterpret_cast<uint2 *>(codes) = cg;
-            *reinterpret_cast<uint2 *>(codes + a.I) = cu;
-            if ((p & 3) == 0) {
-                uint8_t *scales = a.scales + row * 2 * a.groups + (p >> 2);
+            store(codes, cg);
+            store(codes + a.I, cu);
+            if (p % LANES == 0) {
+                uint8_t *scales = a.scales + row * 2 * a.groups + p / LANES;
                 scales[0] = static_cast<uint8_t>(bg);
                 scales[a.groups] = static_cast<uint8_t>(bu);
             }
         }
     }
     if (in) {
+        float2 g[E / 2], u[E / 2];
+        to_pairs(g, qg);
+        to_pairs(u, qu);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            g[k] = g[k] * logistic<T>(g[k]) * u[k];
-        store8(static_cast<T *>(a.act) + row * a.I + c, g);
+        for (int k = 0; k < E / 2; ++k)
+            g[k] = mul2(mul2(g[k], logistic2<T>(g[k])), u[k]);
+        store_pairs<T, E>(static_cast<T *>(a.act) + row * a.I + c, g);
     }
 }
 
-template <typename T, bool KEPT>
+template <typename T, int E, bool KEPT>
 __global__ void __launch_bounds__(THREADS) swiglu_backward_pack_kernel(const ActArgs a)
 {
-    const long long i = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x;
+    constexpr int LANES = GROUP / E;
     int p;
-    const long long row = row_of(a.u, i, p);
-    const int c = p * 8;
-    if (i >= a.u.count || c >= a.I)
+    const long long row = row_of(a.u, threadIdx.x, THREADS, p);
+    const int c = p * E;
+    if (!there(a.u, threadIdx.x, THREADS) || c >= a.I)
         return;
-    float g[8], u[8], d[8];
-    const Pack<T, 8> qd = load_pack<T, 8>(static_cast<const T *>(a.da) + row * a.ldd + c);
+    float2 g[E / 2], u[E / 2], d[E / 2];
+    Elements<T, E> qd;
+    load(qd, static_cast<const T *>(a.da) + row * a.ldd + c);
     if constexpr (KEPT) {
         const int8_t *codes = a.codes + row * 2 * a.I + c;
-        const uint8_t *scales = a.scales + row * 2 * a.groups + (p >> 2);
-        const uint2 cg = __ldg(reinterpret_cast<const uint2 *>(codes)), cu = __ldg(reinterpret_cast<const uint2 *>(codes + a.I));
+        const uint8_t *scales = a.scales + row * 2 * a.groups + p / LANES;
+        const Codes<E> cg = load_codes<E>(codes), cu = load_codes<E>(codes + a.I);
         const uint32_t bg = __ldg(scales), bu = __ldg(scales + a.groups);
-        eight_values(g, cg, step_of(bg));
-        eight_values(u, cu, step_of(bu));
+        values_of<E>(g, cg, step_of(bg));
+        values_of<E>(u, cu, step_of(bu));
     } else {
+        Elements<T, E> qg, qu;
         const T *src = static_cast<const T *>(a.gu) + row * a.ldg + c;
-        const Pack<T, 8> qg = load_pack<T, 8>(src), qu = load_pack<T, 8>(src + a.I);
-        unpack8(g, qg);
-        unpack8(u, qu);
+        load(qg, src);
+        load(qu, src + a.I);
+        to_pairs(g, qg);
+        to_pairs(u, qu);
     }
-    unpack8(d, qd);
+    to_pairs(d, qd);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const Grads r = gradients<T>(d[k], g[k], u[k]);
-        g[k] = r.dg;
-        u[k] = r.du;
-        d[k] = r.act;
-    }
+    for (int k = 0; k < E / 2; ++k)
+        gradients<T>(d[k], g[k], u[k]);
     T *out = static_cast<T *>(a.dgu) + row * 2 * a.I + c;
-    store8(out, g);
-    store8(out + a.I, u);
+    store_pairs<T, E>(out, g);
+    store_pairs<T, E>(out + a.I, u);
     if (a.act)
-        store8(static_cast<T *>(a.act) + row * a.I + c, d);
+        store_pairs<T, E>(static_cast<T *>(a.act) + row * a.I + c, d);
 }
 
 struct KeepArgs {
@@ -249,44 +393,41 @@ struct KeepArgs {
     void *out;         // [M][H]
 };
 
-template <typename T>
+template <typename T, int E>
 __global__ void __launch_bounds__(THREADS) checkpoint_pack_kernel(const KeepArgs a)
 {
-    const long long i = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x;
+    constexpr int LANES = GROUP / E;
     int p;
-    const long long row = row_of(a.u, i, p);
-    const int c = p * 8;
-    const bool in = i < a.u.count && c < a.H;
-    float v[8];
-    if (in) {
-        unpack8(v, load_pack<T, 8>(static_cast<const T *>(a.x) + row * a.ldx + c));
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] = 0.0f;
-    }
+    const long long row = row_of(a.u, threadIdx.x, THREADS, p);
+    const int c = p * E;
+    const bool in = there(a.u, threadIdx.x, THREADS) && c < a.H;
+    Elements<T, E> q;
+    if (in)
+        load(q, static_cast<const T *>(a.x) + row * a.ldx + c);
+    else
+        zero(q);
     uint32_t byte;
-    const uint2 codes = keep_pack(v, byte);
+    const Codes<E> codes = keep(q, byte);
     if (in) {
-        *reinterpret_cast<uint2 *>(a.codes + row * a.H + c) = codes;
-        if ((p & 3) == 0)
-            a.scales[row * a.groups + (p >> 2)] = static_cast<uint8_t>(byte);
+        store(a.codes + row * a.H + c, codes);
+        if (p % LANES == 0)
+            a.scales[row * a.groups + p / LANES] = static_cast<uint8_t>(byte);
     }
 }
 
-template <typename T>
+template <typename T, int E>
 __global__ void __launch_bounds__(THREADS) restore_pack_kernel(const KeepArgs a)
 {
-    const long long i = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x;
+    constexpr int LANES = GROUP / E;
     int p;
-    const long long row = row_of(a.u, i, p);
-    const int c = p * 8;
-    if (i >= a.u.count || c >= a.H)
+    const long long row = row_of(a.u, threadIdx.x, THREADS, p);
+    const int c = p * E;
+    if (!there(a.u, threadIdx.x, THREADS) || c >= a.H)
         return;
-    float v[8];
-    const uint2 codes = __ldg(reinterpret_cast<const uint2 *>(a.codes + row * a.H + c));
-    eight_values(v, codes, step_of(__ldg(a.scales + row * a.groups + (p >> 2))));
-    store8(static_cast<T *>(a.out) + row * a.H + c, v);
+    float2 v[E / 2];
+    const Codes<E> codes = load_codes<E>(a.codes + row * a.H + c);
+    values_of<E>(v, codes, step_of(__ldg(a.scales + row * a.groups + p / LANES)));
+    store_pairs<T, E>(static_cast<T *>(a.out) + row * a.H + c, v);
 }
 
 // ------------------------------------------------------------------ element by element ----
@@ -300,14 +441,15 @@ struct Chunk {
 };
 __device__ __forceinline__ Chunk chunk_of(const Units &u)
 {
-    const long long w = (static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x) >> 5;
+    constexpr int WARPS = THREADS / 32;
+    const int warp = threadIdx.x >> 5;
     Chunk k;
     int within;
-    k.row = row_of(u, w, within);
+    k.row = row_of(u, warp, WARPS, within);
     k.lane = threadIdx.x & 31;
     k.first = within * CHUNK;
     k.c = k.first + k.lane;
-    k.in = w < u.count;
+    k.in = there(u, warp, WARPS);
     return k;
 }
 template <typename T>
@@ -386,11 +528,12 @@ __global__ void __launch_bounds__(THREADS) swiglu_backward_kernel(const ActArgs 
         load_spread(u, src + a.I, k.c, a.I);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const Grads r = gradients<T>(d[j], g[j], u[j]);
-        g[j] = r.dg;
-        u[j] = r.du;
-        d[j] = r.act;
+    for (int j = 0; j < 8; j += 2) {
+        float2 d2 = make_float2(d[j], d[j + 1]), g2 = make_float2(g[j], g[j + 1]), u2 = make_float2(u[j], u[j + 1]);
+        gradients<T>(d2, g2, u2);
+        d[j] = d2.x, d[j + 1] = d2.y;
+        g[j] = g2.x, g[j + 1] = g2.y;
+        u[j] = u2.x, u[j + 1] = u2.y;
     }
     T *out = static_cast<T *>(a.dgu) + k.row * 2 * a.I;
     store_spread(out, g, k.c, a.I);
@@ -426,18 +569,53 @@ constexpr int MAX_WIDTH = 1 << 20;
 
 int groups_of(int width) { return (width + GROUP - 1) / GROUP; }
 bool sizes_ok(long long M, int width, int dtype) { return M >= 0 && M <= MAX_ROWS && width >= 1 && width <= MAX_WIDTH && dtype_ok(dtype); }
-// Rows of whole packs on 16-byte boundaries (null: not there).
-bool packed(const void *p, long long ld, int dtype) { return op_aligned(p, 16) && (p == nullptr || ld * dtype_bytes(dtype) % 16 == 0); }
-
-// Blocks of THREADS threads, or -1: more than a grid has (2^39 threads, which no memory holds).
-long long blocks_of(long long threads)
+// How rows move: element by element (0), or the elements of a thread, for which every tensor (null: not there)
+// starts, row by row, on their boundaries.
+struct Rows {
+    const void *p;
+    long long ld;   // elements
+    size_t size;    // of an element
+};
+int elements_of(int width, int dtype, std::initializer_list<Rows> tensors)
 {
-    const long long b = (threads + THREADS - 1) / THREADS;
+    const auto fits = [&](int e) {
+        if (width % e != 0)
+            return false;
+        for (const Rows &r : tensors) {
+            const size_t bytes = e * r.size <= 32 && !(e == 8 && r.size == 4) ? e * r.size : 16;
+            if (r.p && (!op_aligned(r.p, bytes) || r.ld * r.size % bytes != 0))
+                return false;
+        }
+        return true;
+    };
+    if (dtype != MOE_F32 && fits(16))
+        return 16;
+    return fits(8) ? 8 : 0;
+}
+// E: the elements of a thread, the last group's included where it is not whole; chunks of warps if 0.
+Units units_of(long long M, int width, int e)
+{
+    return e ? units(M, GROUP / e * groups_of(width)) : units(M, (width + CHUNK - 1) / CHUNK);
+}
+// Blocks of THREADS threads, or -1: more than a grid has (2^39 threads, which no memory holds).
+long long blocks_of(const Units &u, int e)
+{
+    const long long b = ((e ? u.count : 32 * u.count) + THREADS - 1) / THREADS;
     return b <= INT_MAX ? b : -1;
 }
-// Packs: four lanes a group, the last group's included where it is not whole.
-Units pack_units(long long M, int width) { return units(M, 4 * groups_of(width)); }
-Units chunk_units(long long M, int width) { return units(M, (width + CHUNK - 1) / CHUNK); }
+// Calls f with a null pointer of the element type and the elements of a thread.
+template <typename F>
+void with_elements(int dtype, int e, F f)
+{
+    with_dtype(dtype, [&](auto *t) {
+        using T = std::remove_pointer_t<decltype(t)>;
+        if constexpr (sizeof(T) == 2) {
+            if (e == 16)
+                return f(t, std::integral_constant<int, 16>());
+        }
+        e ? f(t, std::integral_constant<int, 8>()) : f(t, std::integral_constant<int, 0>());
+    });
+}
 
 }  // namespace
 
@@ -452,10 +630,10 @@ int moe_swiglu(int64_t M, int I, const void *gu, int64_t ldg, int dtype, void *a
     const size_t b = dtype_bytes(dtype);
     if (!gu || !act || !op_aligned(gu, b) || !op_aligned(act, b))
         return MOE_ERR_INVALID_ARG;
-    const bool packs = I % 8 == 0 && packed(gu, ldg, dtype) && packed(act, I, dtype) && op_aligned(codes, 8);
+    const int e = elements_of(I, dtype, {{gu, ldg, b}, {act, I, b}, {codes, 2ll * I, 1}});
     ActArgs a{};
-    a.u = packs ? pack_units(M, I) : chunk_units(M, I);
-    const long long blocks = blocks_of(packs ? a.u.count : 32 * a.u.count);
+    a.u = units_of(M, I, e);
+    const long long blocks = blocks_of(a.u, e);
     if (blocks < 0)
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
@@ -468,16 +646,13 @@ int moe_swiglu(int64_t M, int I, const void *gu, int64_t ldg, int dtype, void *a
     a.act = act;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const dim3 grid(static_cast<unsigned>(blocks));
-    with_dtype(dtype, [&](auto *t) {
+    with_elements(dtype, e, [&](auto *t, auto elements) {
         using T = std::remove_pointer_t<decltype(t)>;
-        if (packs && codes)
-            swiglu_pack_kernel<T, true><<<grid, THREADS, 0, s>>>(a);
-        else if (packs)
-            swiglu_pack_kernel<T, false><<<grid, THREADS, 0, s>>>(a);
-        else if (codes)
-            swiglu_kernel<T, true><<<grid, THREADS, 0, s>>>(a);
+        constexpr int E = decltype(elements)::value;
+        if constexpr (E > 0)
+            codes ? swiglu_pack_kernel<T, E, true><<<grid, THREADS, 0, s>>>(a) : swiglu_pack_kernel<T, E, false><<<grid, THREADS, 0, s>>>(a);
         else
-            swiglu_kernel<T, false><<<grid, THREADS, 0, s>>>(a);
+            codes ? swiglu_kernel<T, true><<<grid, THREADS, 0, s>>>(a) : swiglu_kernel<T, false><<<grid, THREADS, 0, s>>>(a);
     });
     return launched();
 }
@@ -492,11 +667,10 @@ int moe_swiglu_backward(int64_t M, int I, const void *dact, int64_t ldd, const v
     const size_t b = dtype_bytes(dtype);
     if (!dact || !dgu || !gu == !codes || !op_aligned(dact, b) || !op_aligned(gu, b) || !op_aligned(dgu, b) || !op_aligned(act, b))
         return MOE_ERR_INVALID_ARG;
-    const bool packs = I % 8 == 0 && packed(dact, ldd, dtype) && packed(gu, ldg, dtype) && packed(dgu, 2ll * I, dtype) &&
-                       packed(act, I, dtype) && op_aligned(codes, 8);
+    const int e = elements_of(I, dtype, {{dact, ldd, b}, {gu, ldg, b}, {dgu, 2ll * I, b}, {act, I, b}, {codes, 2ll * I, 1}});
     ActArgs a{};
-    a.u = packs ? pack_units(M, I) : chunk_units(M, I);
-    const long long blocks = blocks_of(packs ? a.u.count : 32 * a.u.count);
+    a.u = units_of(M, I, e);
+    const long long blocks = blocks_of(a.u, e);
     if (blocks < 0)
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
@@ -512,16 +686,14 @@ int moe_swiglu_backward(int64_t M, int I, const void *dact, int64_t ldd, const v
     a.dgu = dgu;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const dim3 grid(static_cast<unsigned>(blocks));
-    with_dtype(dtype, [&](auto *t) {
+    with_elements(dtype, e, [&](auto *t, auto elements) {
         using T = std::remove_pointer_t<decltype(t)>;
-        if (packs && codes)
-            swiglu_backward_pack_kernel<T, true><<<grid, THREADS, 0, s>>>(a);
-        else if (packs)
-            swiglu_backward_pack_kernel<T, false><<<grid, THREADS, 0, s>>>(a);
-        else if (codes)
-            swiglu_backward_kernel<T, true><<<grid, THREADS, 0, s>>>(a);
+        constexpr int E = decltype(elements)::value;
+        if constexpr (E > 0)
+            codes ? swiglu_backward_pack_kernel<T, E, true><<<grid, THREADS, 0, s>>>(a)
+                  : swiglu_backward_pack_kernel<T, E, false><<<grid, THREADS, 0, s>>>(a);
         else
-            swiglu_backward_kernel<T, false><<<grid, THREADS, 0, s>>>(a);
+            codes ? swiglu_backward_kernel<T, true><<<grid, THREADS, 0, s>>>(a) : swiglu_backward_kernel<T, false><<<grid, THREADS, 0, s>>>(a);
     });
     return launched();
 }
@@ -534,19 +706,20 @@ int moe_checkpoint_rows(int64_t M, int H, const void *x, int64_t ldx, int dtype,
         return MOE_OK;
     if (!x || !codes || !scales || !op_aligned(x, dtype_bytes(dtype)))
         return MOE_ERR_INVALID_ARG;
-    const bool packs = H % 8 == 0 && packed(x, ldx, dtype) && op_aligned(codes, 8);
-    const Units u = packs ? pack_units(M, H) : chunk_units(M, H);
-    const long long blocks = blocks_of(packs ? u.count : 32 * u.count);
+    const int e = elements_of(H, dtype, {{x, ldx, dtype_bytes(dtype)}, {codes, H, 1}});
+    const Units u = units_of(M, H, e);
+    const long long blocks = blocks_of(u, e);
     if (blocks < 0)
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
     const KeepArgs a{u, H, groups_of(H), x, ldx, codes, scales, nullptr};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const dim3 grid(static_cast<unsigned>(blocks));
-    with_dtype(dtype, [&](auto *t) {
+    with_elements(dtype, e, [&](auto *t, auto elements) {
         using T = std::remove_pointer_t<decltype(t)>;
-        if (packs)
-            checkpoint_pack_kernel<T><<<grid, THREADS, 0, s>>>(a);
+        constexpr int E = decltype(elements)::value;
+        if constexpr (E > 0)
+            checkpoint_pack_kernel<T, E><<<grid, THREADS, 0, s>>>(a);
         else
             checkpoint_kernel<T><<<grid, THREADS, 0, s>>>(a);
     });
@@ -561,19 +734,20 @@ int moe_restore_rows(int64_t M, int H, const int8_t *codes, const uint8_t *scale
         return MOE_OK;
     if (!x || !codes || !scales || !op_aligned(x, dtype_bytes(dtype)))
         return MOE_ERR_INVALID_ARG;
-    const bool packs = H % 8 == 0 && packed(x, H, dtype) && op_aligned(codes, 8);
-    const Units u = packs ? pack_units(M, H) : chunk_units(M, H);
-    const long long blocks = blocks_of(packs ? u.count : 32 * u.count);
+    const int e = elements_of(H, dtype, {{x, H, dtype_bytes(dtype)}, {codes, H, 1}});
+    const Units u = units_of(M, H, e);
+    const long long blocks = blocks_of(u, e);
     if (blocks < 0)
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
     const KeepArgs a{u, H, groups_of(H), nullptr, 0, const_cast<int8_t *>(codes), const_cast<uint8_t *>(scales), x};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const dim3 grid(static_cast<unsigned>(blocks));
-    with_dtype(dtype, [&](auto *t) {
+    with_elements(dtype, e, [&](auto *t, auto elements) {
         using T = std::remove_pointer_t<decltype(t)>;
-        if (packs)
-            restore_pack_kernel<T><<<grid, THREADS, 0, s>>>(a);
+        constexpr int E = decltype(elements)::value;
+        if constexpr (E > 0)
+            restore_pack_kernel<T, E><<<grid, THREADS, 0, s>>>(a);
         else
             restore_kernel<T><<<grid, THREADS, 0, s>>>(a);
     });
