@@ -23,6 +23,7 @@ constexpr int THREADS = 256;
 constexpr int GROUP = 32;       // values of a scale
 constexpr int CHUNK = 256;      // elements of a warp (8 a lane)
 constexpr uint32_t ALL = 0xFFFFFFFFu;
+__host__ __device__ __forceinline__ int groups_of(int width) { return (width + GROUP - 1) / GROUP; }
 
 // ------------------------------------------------------------------ the activation ------
 // 1/(1 + exp(-g)).  For 16-bit results two approximate instructions, together 2^-21 off at |g| <= 16 (the
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(THREADS) restore_pack_kernel(const KeepArgs a)
 
 // ------------------------------------------------------------------ element by element ----
 // A warp's chunk of a row: lane l has its elements l, 32 + l, ..., so every access of the warp is one group
-// of 32 neighbours, at any alignment.
+// of 32 neighbours, at any alignment.  WHOLE: the row has all of the chunk, and nothing is asked of the columns.
 struct Chunk {
     long long row;
     int c, first;    // this lane's first column, the chunk's
@@ -452,80 +453,106 @@ __device__ __forceinline__ Chunk chunk_of(const Units &u)
     k.in = there(u, warp, WARPS);
     return k;
 }
-template <typename T>
+// (columns past the end: the last one's value, so that no load waits behind a branch, then zeros)
+template <bool WHOLE, typename T>
 __device__ __forceinline__ void load_spread(float (&f)[8], const T *row, int c, int n)
 {
+    T v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        f[j] = c + 32 * j < n ? to_f<T>(__ldg(row + c + 32 * j)) : 0.0f;
+        v[j] = __ldg(row + (WHOLE ? c + 32 * j : min(c + 32 * j, n - 1)));
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        f[j] = WHOLE || c + 32 * j < n ? to_f<T>(v[j]) : 0.0f;
 }
-template <typename T>
+template <bool WHOLE, typename T>
 __device__ __forceinline__ void store_spread(T *row, const float (&f)[8], int c, int n)
 {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        if (c + 32 * j < n)
+        if (WHOLE || c + 32 * j < n)
             row[c + 32 * j] = from_f<T>(f[j]);
 }
+template <bool WHOLE>
 __device__ __forceinline__ void keep_spread(const float (&f)[8], int8_t *codes, uint8_t *scales, const Chunk &k, int n)
 {
+    uint32_t mine = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        if (k.first + 32 * j >= n)
-            break;
         const uint32_t byte = scale_byte(__reduce_max_sync(ALL, magnitude(f[j])));
-        if (k.c + 32 * j < n)
-            codes[k.c + 32 * j] = static_cast<int8_t>(code_of(f[j], steps_per_one(byte)) & 0xFFu);
-        if (k.lane == 0)
-            scales[(k.first >> 5) + j] = static_cast<uint8_t>(byte);
+        const uint32_t code = code_of(f[j], steps_per_one(byte));
+        if (WHOLE || k.c + 32 * j < n)
+            codes[k.c + 32 * j] = static_cast<int8_t>(code & 0xFFu);
+        mine = k.lane == j ? byte : mine;
     }
+    if (k.lane < 8 && (WHOLE || k.first + 32 * k.lane < n))
+        scales[(k.first >> 5) + k.lane] = static_cast<uint8_t>(mine);
 }
+template <bool WHOLE>
 __device__ __forceinline__ void restore_spread(float (&f)[8], const int8_t *codes, const uint8_t *scales, const Chunk &k, int n)
 {
+    // lane j has the step of group j
+    const int group = (k.first >> 5) + (k.lane & 7);
+    const uint8_t byte = __ldg(scales + (WHOLE ? group : min(group, groups_of(n) - 1)));
+    uint8_t v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        f[j] = k.c + 32 * j < n ? static_cast<float>(__ldg(codes + k.c + 32 * j)) * step_of(__ldg(scales + (k.first >> 5) + j)) : 0.0f;
+        v[j] = __ldg(reinterpret_cast<const uint8_t *>(codes) + (WHOLE ? k.c + 32 * j : min(k.c + 32 * j, n - 1)));
+    const float step = step_of(byte);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float value = (__uint_as_float(0x4B000000u | (v[j] ^ 0x80u)) - 8388736.0f) * __shfl_sync(ALL, step, j);
+        f[j] = WHOLE || k.c + 32 * j < n ? value : 0.0f;
+    }
 }
 
+template <bool WHOLE, typename T, bool KEEP>
+__device__ __forceinline__ void swiglu_chunk(const ActArgs &a, const Chunk &k)
+{
+    float g[8], u[8];
+    const T *src = static_cast<const T *>(a.gu) + k.row * a.ldg;
+    load_spread<WHOLE>(g, src, k.c, a.I);
+    load_spread<WHOLE>(u, src + a.I, k.c, a.I);
+    if constexpr (KEEP) {
+        int8_t *codes = a.codes + k.row * 2 * a.I;
+        uint8_t *scales = a.scales + k.row * 2 * a.groups;
+        keep_spread<WHOLE>(g, codes, scales, k, a.I);
+        keep_spread<WHOLE>(u, codes + a.I, scales + a.groups, k, a.I);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const float2 v = make_float2(g[j], g[j + 1]);
+        const float2 r = mul2(mul2(v, logistic2<T>(v)), make_float2(u[j], u[j + 1]));
+        g[j] = r.x, g[j + 1] = r.y;
+    }
+    store_spread<WHOLE>(static_cast<T *>(a.act) + k.row * a.I, g, k.c, a.I);
+}
 template <typename T, bool KEEP>
 __global__ void __launch_bounds__(THREADS) swiglu_kernel(const ActArgs a)
 {
     const Chunk k = chunk_of(a.u);
     if (!k.in)
         return;
-    float g[8], u[8];
-    const T *src = static_cast<const T *>(a.gu) + k.row * a.ldg;
-    load_spread(g, src, k.c, a.I);
-    load_spread(u, src + a.I, k.c, a.I);
-    if constexpr (KEEP) {
-        int8_t *codes = a.codes + k.row * 2 * a.I;
-        uint8_t *scales = a.scales + k.row * 2 * a.groups;
-        keep_spread(g, codes, scales, k, a.I);
-        keep_spread(u, codes + a.I, scales + a.groups, k, a.I);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        g[j] = g[j] * logistic<T>(g[j]) * u[j];
-    store_spread(static_cast<T *>(a.act) + k.row * a.I, g, k.c, a.I);
+    if (k.first + CHUNK <= a.I)
+        swiglu_chunk<true, T, KEEP>(a, k);
+    else
+        swiglu_chunk<false, T, KEEP>(a, k);
 }
 
-template <typename T, bool KEPT>
-__global__ void __launch_bounds__(THREADS) swiglu_backward_kernel(const ActArgs a)
+template <bool WHOLE, typename T, bool KEPT>
+__device__ __forceinline__ void swiglu_backward_chunk(const ActArgs &a, const Chunk &k)
 {
-    const Chunk k = chunk_of(a.u);
-    if (!k.in)
-        return;
     float g[8], u[8], d[8];
-    load_spread(d, static_cast<const T *>(a.da) + k.row * a.ldd, k.c, a.I);
+    load_spread<WHOLE>(d, static_cast<const T *>(a.da) + k.row * a.ldd, k.c, a.I);
     if constexpr (KEPT) {
         const int8_t *codes = a.codes + k.row * 2 * a.I;
         const uint8_t *scales = a.scales + k.row * 2 * a.groups;
-        restore_spread(g, codes, scales, k, a.I);
-        restore_spread(u, codes + a.I, scales + a.groups, k, a.I);
+        restore_spread<WHOLE>(g, codes, scales, k, a.I);
+        restore_spread<WHOLE>(u, codes + a.I, scales + a.groups, k, a.I);
     } else {
         const T *src = static_cast<const T *>(a.gu) + k.row * a.ldg;
-        load_spread(g, src, k.c, a.I);
-        load_spread(u, src + a.I, k.c, a.I);
+        load_spread<WHOLE>(g, src, k.c, a.I);
+        load_spread<WHOLE>(u, src + a.I, k.c, a.I);
     }
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
@@ -536,10 +563,21 @@ __global__ void __launch_bounds__(THREADS) swiglu_backward_kernel(const ActArgs 
         u[j] = u2.x, u[j + 1] = u2.y;
     }
     T *out = static_cast<T *>(a.dgu) + k.row * 2 * a.I;
-    store_spread(out, g, k.c, a.I);
-    store_spread(out + a.I, u, k.c, a.I);
+    store_spread<WHOLE>(out, g, k.c, a.I);
+    store_spread<WHOLE>(out + a.I, u, k.c, a.I);
     if (a.act)
-        store_spread(static_cast<T *>(a.act) + k.row * a.I, d, k.c, a.I);
+        store_spread<WHOLE>(static_cast<T *>(a.act) + k.row * a.I, d, k.c, a.I);
+}
+template <typename T, bool KEPT>
+__global__ void __launch_bounds__(THREADS) swiglu_backward_kernel(const ActArgs a)
+{
+    const Chunk k = chunk_of(a.u);
+    if (!k.in)
+        return;
+    if (k.first + CHUNK <= a.I)
+        swiglu_backward_chunk<true, T, KEPT>(a, k);
+    else
+        swiglu_backward_chunk<false, T, KEPT>(a, k);
 }
 
 template <typename T>
@@ -548,9 +586,15 @@ __global__ void __launch_bounds__(THREADS) checkpoint_kernel(const KeepArgs a)
     const Chunk k = chunk_of(a.u);
     if (!k.in)
         return;
-    float v[8];
-    load_spread(v, static_cast<const T *>(a.x) + k.row * a.ldx, k.c, a.H);
-    keep_spread(v, a.codes + k.row * a.H, a.scales + k.row * a.groups, k, a.H);
+    const auto go = [&](auto whole) {
+        float v[8];
+        load_spread<decltype(whole)::value>(v, static_cast<const T *>(a.x) + k.row * a.ldx, k.c, a.H);
+        keep_spread<decltype(whole)::value>(v, a.codes + k.row * a.H, a.scales + k.row * a.groups, k, a.H);
+    };
+    if (k.first + CHUNK <= a.H)
+        go(std::true_type());
+    else
+        go(std::false_type());
 }
 
 template <typename T>
@@ -559,15 +603,20 @@ __global__ void __launch_bounds__(THREADS) restore_kernel(const KeepArgs a)
     const Chunk k = chunk_of(a.u);
     if (!k.in)
         return;
-    float v[8];
-    restore_spread(v, a.codes + k.row * a.H, a.scales + k.row * a.groups, k, a.H);
-    store_spread(static_cast<T *>(a.out) + k.row * a.H, v, k.c, a.H);
+    const auto go = [&](auto whole) {
+        float v[8];
+        restore_spread<decltype(whole)::value>(v, a.codes + k.row * a.H, a.scales + k.row * a.groups, k, a.H);
+        store_spread<decltype(whole)::value>(static_cast<T *>(a.out) + k.row * a.H, v, k.c, a.H);
+    };
+    if (k.first + CHUNK <= a.H)
+        go(std::true_type());
+    else
+        go(std::false_type());
 }
 
 // ------------------------------------------------------------------ host side ------------
 constexpr int MAX_WIDTH = 1 << 20;
 
-int groups_of(int width) { return (width + GROUP - 1) / GROUP; }
 bool sizes_ok(long long M, int width, int dtype) { return M >= 0 && M <= MAX_ROWS && width >= 1 && width <= MAX_WIDTH && dtype_ok(dtype); }
 // How rows move: element by element (0), or the elements of a thread, for which every tensor (null: not there)
 // starts, row by row, on their boundaries.
