@@ -6,8 +6,8 @@
 //   7), and each is n X/64 with the nearest whole n in -127 .. 127, ties to even (an MX block of INT8
 //   elements).  X is a power of two, so v 64/X and n X/64 are exact and the rounding to n is the only one.
 //
-// All of it is elementwise and bound by HBM.  A thread takes a pack of 8 neighbours of gate and of up, so
-// four neighbouring lanes hold a group of 32; rows that are not whole packs on 16-byte boundaries go
+// All of it is elementwise and bound by HBM.  A thread takes E neighbours of gate and of up (32 bytes, or 16 or 8
+// where the rows' boundaries allow no more), so 32/E neighbouring lanes hold a group; rows off those boundaries go
 // element by element, a group a warp access.
 #include <climits>
 #include <initializer_list>
@@ -107,42 +107,39 @@ __device__ __forceinline__ float2 two_values(uint32_t offset, float step)
 }
 
 // ------------------------------------------------------------------ a thread's elements ----
-// E neighbours: a pack of 8 (16-byte accesses; 32 bits: two), or of 16-bit types 16 (32-byte accesses, for rows
-// that are on such boundaries).
+// E neighbours, one access of 32, 16 or 8 bytes, on whose boundaries the rows are.
 template <typename T, int E>
 struct Elements {
     static constexpr int BYTES = static_cast<int>(sizeof(T)) * E, WORDS = BYTES / 4;
     union {
         T v[E];
-        uint32_t w[WORDS];
+        alignas(BYTES < 16 ? BYTES : 16) uint32_t w[WORDS];
     };
     __device__ Elements() {}
 };
 template <typename T, int E>
 __device__ __forceinline__ void load(Elements<T, E> &q, const T *p)
 {
-    if constexpr (sizeof(T) == 2 && E == 16) {
+    if constexpr (Elements<T, E>::BYTES == 32)
         asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
             : "=r"(q.w[0]), "=r"(q.w[1]), "=r"(q.w[2]), "=r"(q.w[3]), "=r"(q.w[4]), "=r"(q.w[5]), "=r"(q.w[6]), "=r"(q.w[7])
             : "l"(p));
-    } else {
-#pragma unroll
-        for (int i = 0; i < Elements<T, E>::WORDS / 4; ++i)
-            *reinterpret_cast<uint4 *>(&q.w[4 * i]) = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-    }
+    else if constexpr (Elements<T, E>::BYTES == 16)
+        *reinterpret_cast<uint4 *>(q.w) = __ldg(reinterpret_cast<const uint4 *>(p));
+    else
+        *reinterpret_cast<uint2 *>(q.w) = __ldg(reinterpret_cast<const uint2 *>(p));
 }
 template <typename T, int E>
 __device__ __forceinline__ void store(T *p, const Elements<T, E> &q)
 {
-    if constexpr (sizeof(T) == 2 && E == 16) {
+    if constexpr (Elements<T, E>::BYTES == 32)
         asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(q.w[0]), "r"(q.w[1]), "r"(q.w[2]), "r"(q.w[3]),
                      "r"(q.w[4]), "r"(q.w[5]), "r"(q.w[6]), "r"(q.w[7])
                      : "memory");
-    } else {
-#pragma unroll
-        for (int i = 0; i < Elements<T, E>::WORDS / 4; ++i)
-            reinterpret_cast<uint4 *>(p)[i] = make_uint4(q.w[4 * i], q.w[4 * i + 1], q.w[4 * i + 2], q.w[4 * i + 3]);
-    }
+    else if constexpr (Elements<T, E>::BYTES == 16)
+        *reinterpret_cast<uint4 *>(p) = make_uint4(q.w[0], q.w[1], q.w[2], q.w[3]);
+    else
+        *reinterpret_cast<uint2 *>(p) = make_uint2(q.w[0], q.w[1]);
 }
 template <typename T, int E>
 __device__ __forceinline__ void zero(Elements<T, E> &q)
@@ -170,15 +167,17 @@ __device__ __forceinline__ void store_pairs(T *p, const float2 (&f)[E / 2])
 
 template <int E>
 struct Codes {
-    uint32_t w[E / 4];
+    alignas(E) uint32_t w[E / 4];
 };
 template <int E>
 __device__ __forceinline__ void store(int8_t *p, const Codes<E> &c)
 {
     if constexpr (E == 16)
         *reinterpret_cast<uint4 *>(p) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
-    else
+    else if constexpr (E == 8)
         *reinterpret_cast<uint2 *>(p) = make_uint2(c.w[0], c.w[1]);
+    else
+        *reinterpret_cast<uint32_t *>(p) = c.w[0];
 }
 template <int E>
 __device__ __forceinline__ Codes<E> load_codes(const int8_t *p)
@@ -186,8 +185,10 @@ __device__ __forceinline__ Codes<E> load_codes(const int8_t *p)
     Codes<E> c;
     if constexpr (E == 16)
         *reinterpret_cast<uint4 *>(c.w) = __ldg(reinterpret_cast<const uint4 *>(p));
-    else
+    else if constexpr (E == 8)
         *reinterpret_cast<uint2 *>(c.w) = __ldg(reinterpret_cast<const uint2 *>(p));
+    else
+        c.w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
     return c;
 }
 template <int E>
@@ -630,16 +631,14 @@ int elements_of(int width, int dtype, std::initializer_list<Rows> tensors)
     const auto fits = [&](int e) {
         if (width % e != 0)
             return false;
-        for (const Rows &r : tensors) {
-            const size_t bytes = e * r.size <= 32 && !(e == 8 && r.size == 4) ? e * r.size : 16;
-            if (r.p && (!op_aligned(r.p, bytes) || r.ld * r.size % bytes != 0))
+        for (const Rows &r : tensors)
+            if (r.p && (!op_aligned(r.p, e * r.size) || r.ld % e != 0))
                 return false;
-        }
         return true;
     };
     if (dtype != MOE_F32 && fits(16))
         return 16;
-    return fits(8) ? 8 : 0;
+    return fits(8) ? 8 : fits(4) ? 4 : 0;
 }
 // E: the elements of a thread, the last group's included where it is not whole; chunks of warps if 0.
 Units units_of(long long M, int width, int e)
@@ -662,7 +661,9 @@ void with_elements(int dtype, int e, F f)
             if (e == 16)
                 return f(t, std::integral_constant<int, 16>());
         }
-        e ? f(t, std::integral_constant<int, 8>()) : f(t, std::integral_constant<int, 0>());
+        if (e == 8)
+            return f(t, std::integral_constant<int, 8>());
+        e ? f(t, std::integral_constant<int, 4>()) : f(t, std::integral_constant<int, 0>());
     });
 }
 
