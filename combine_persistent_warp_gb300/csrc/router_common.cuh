@@ -57,19 +57,25 @@ __device__ __forceinline__ double warp_sum(double v)
     return v;
 }
 
+// Experts of a lane.
+inline int lane_experts(int E)
+{
+    const int n = (E + 31) / 32;
+    return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 8 ? 8 : 32;
+}
 template <template <typename, int> class Launch, typename A>
 void by_width(int dtype, int E, const A &a, cudaStream_t s)
 {
     with_dtype(dtype, [&](auto *t) {
         using T = std::remove_pointer_t<decltype(t)>;
-        const int ipl = (E + 31) / 32;
-        if (ipl <= 1)
+        const int ipl = lane_experts(E);
+        if (ipl == 1)
             Launch<T, 1>::go(a, s);
-        else if (ipl <= 2)
+        else if (ipl == 2)
             Launch<T, 2>::go(a, s);
-        else if (ipl <= 4)
+        else if (ipl == 4)
             Launch<T, 4>::go(a, s);
-        else if (ipl <= 8)
+        else if (ipl == 8)
             Launch<T, 8>::go(a, s);
         else
             Launch<T, 32>::go(a, s);

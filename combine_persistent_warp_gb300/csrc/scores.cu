@@ -11,7 +11,7 @@
 //
 // The choice is that of c in 64 bits.  Two values of c that 32 bits hold for equal or swap are rare, and
 // which expert a token goes to should not hang on a rounding: c is computed in 32 bits with a bound of
-// its error, and a token whose choice that bound leaves open is chosen again in 64.
+// its error, and the candidates that this bound leaves open are ranked again in 64.
 #include <climits>
 
 #include "router_common.cuh"
@@ -31,8 +31,10 @@ struct ScoreArgs {
     const uint8_t *mask;   // nonzero: the token is routed (null: every token)
     int softmax, renorm;
     int groups, kept, pair;   // pair: a group's score is the sum of two
-    int per, lanes, shift;    // experts of a group; lanes that look through one, 1 << shift
+    int group_shift;          // a group is 1 << group_shift lanes (-1: it is not)
+    int per, lanes, shift;    // otherwise: experts of a group; lanes that look through one, 1 << shift
     uint32_t per_magic;       // e / per = e * per_magic >> 20
+    int vec, bias_vec;        // rows of logits, the bias: in vectors (see load_lane)
     float scale;
     int64_t *idx;
     float *w;
@@ -46,98 +48,123 @@ __device__ __forceinline__ float warp_max_f(float v)
     return v;
 }
 // ------------------------------------------------------------------ the choice ----------
-// Where expert e's key lies for the lanes that look through the groups: 4 words further every 32, so that
-// the lanes of 8 groups of 16 or 32 read different banks.
-__device__ __forceinline__ int spot(int e) { return e + (e >> 5) * 4; }
+// Lane l holds experts l * IPL .. l * IPL + IPL - 1 (a group of experts is then a few neighbouring lanes, mostly).
+//
+// A word is what the choice goes by: the upper bits of c's order key and, below them, the expert (ties to
+// the lowest), so that one warp maximum a slot finds both.  The bits that the expert takes from the key make
+// more values look equal; what the words leave open is settled by the candidates' exact values.
 template <int IPL>
-constexpr int SPOTS = IPL * 36;
+constexpr int BITS = IPL == 1 ? 5 : IPL == 2 ? 6 : IPL == 4 ? 7 : IPL == 8 ? 8 : 10;
+template <int IPL>
+constexpr uint32_t ID = (1u << BITS<IPL>) - 1u;
+constexpr uint32_t NEVER = 0x007FFFFFu;   // the key of -inf, and words and keys that are not there
 
-// Drops the keys of the groups that do not stay.  `least` and `most`: the lowest score that stays and the
-// highest that does not (0: none).
-template <int IPL, typename K>
-__device__ __forceinline__ void keep_groups(const ScoreArgs &a, K (&key)[IPL], K *seen, int lane, K &least, K &most)
+// Order key of a sum or product (whose NaN is the positive one).
+__device__ __forceinline__ uint32_t plain_key(float f)
 {
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < IPL; ++i)
-        if (i * 32 + lane < a.E)
-            seen[spot(i * 32 + lane)] = key[i];
-    __syncwarp();
-    const int g = lane >> a.shift, part = lane & (a.lanes - 1);
-    K first = 0, second = 0;
-    if (g < a.groups)
-        for (int e = part; e < a.per; e += a.lanes) {
-            const K v = seen[spot(g * a.per + e)];
-            second = max(second, min(first, v));
-            first = max(first, v);
-        }
-    for (int o = 1; o < a.lanes; o <<= 1) {
-        const K f = __shfl_xor_sync(ALL, first, o), s = __shfl_xor_sync(ALL, second, o);
-        second = max(max(second, s), min(first, f));
-        first = max(first, f);
-    }
+    const uint32_t u = __float_as_uint(f);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+template <int IPL>
+__device__ __forceinline__ uint32_t word_of(uint32_t key, int lane, int i)
+{
+    return (key & ~ID<IPL>) | (ID<IPL> - static_cast<uint32_t>(lane * IPL + i));
+}
+template <int IPL>
+__device__ __forceinline__ int expert_of(uint32_t word) { return static_cast<int>(ID<IPL> - (word & ID<IPL>)); }
+// The least and the most that the c of a word can be.
+template <int IPL>
+__device__ __forceinline__ float least_of(uint32_t word) { return key_value(word & ~ID<IPL>); }
+template <int IPL>
+__device__ __forceinline__ float most_of(uint32_t word) { return key_value(word | ID<IPL>); }
+
+// Whether the lane's group of experts stays, from the group's two largest keys (0: none): `least` and `most` are
+// the lowest score that stays and the highest that does not (0: none).  Group g is that of the lanes
+// g << shift and after.
+template <typename K>
+__device__ __forceinline__ bool group_stays(const ScoreArgs &a, K first, K second, int lane, int shift, K &least, K &most)
+{
+    const int g = lane >> shift;
     K score = first;
     if (a.pair && second != 0)
         score = order_key(key_value(first) + key_value(second));
     int rank = 0;
+#pragma unroll 4
     for (int h = 0; h < a.groups; ++h) {
-        const K other = __shfl_sync(ALL, score, h << a.shift);
+        const K other = __shfl_sync(ALL, score, h << shift);
         rank += other > score || (other == score && h < g);
     }
     const bool there = g < a.groups && score != 0, stays = there && rank < a.kept;
-    const uint32_t stay = __ballot_sync(ALL, stays);
     // the lowest: the complement of the largest complement
     least = ~warp_max(stays ? static_cast<K>(~score) : static_cast<K>(0));
     most = warp_max(there && !stays ? score : static_cast<K>(0));
+    return stays;
+}
+template <typename K>
+__device__ __forceinline__ void insert(K v, K &first, K &second)
+{
+    second = max(second, min(first, v));
+    first = max(first, v);
+}
+template <typename K>
+__device__ __forceinline__ void merge_lanes(K &first, K &second, int lanes)
+{
+    for (int o = 1; o < lanes; o <<= 1) {
+        const K f = __shfl_xor_sync(ALL, first, o), s = __shfl_xor_sync(ALL, second, o);
+        second = max(max(second, s), min(first, f));
+        first = max(first, f);
+    }
+}
+// Where expert e's key lies for the lanes that look through groups that are not whole lanes.
+__device__ __forceinline__ int spot(int e) { return e + (e >> 5) * 4; }
+template <int IPL>
+constexpr int SPOTS = IPL * 36;
+
+// Zeroes the keys of the groups that do not stay.
+template <int IPL, typename K>
+__device__ __forceinline__ void keep_groups(const ScoreArgs &a, K (&key)[IPL], K *seen, int lane, K &least, K &most)
+{
+    K first = 0, second = 0;
+    if (a.group_shift >= 0) {   // a group is 1 << group_shift lanes
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+            insert(key[i], first, second);
+        merge_lanes(first, second, 1 << a.group_shift);
+        const bool stays = group_stays(a, first, second, lane, a.group_shift, least, most);
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+            key[i] = stays ? key[i] : 0;
+        return;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < IPL; ++i)
+        if (lane * IPL + i < a.E)
+            seen[spot(lane * IPL + i)] = key[i];
+    __syncwarp();
+    const int g = lane >> a.shift;
+    if (g < a.groups)
+        for (int e = lane & (a.lanes - 1); e < a.per; e += a.lanes)
+            insert(seen[spot(g * a.per + e)], first, second);
+    merge_lanes(first, second, a.lanes);
+    const uint32_t stay = __ballot_sync(ALL, group_stays(a, first, second, lane, a.shift, least, most));
 #pragma unroll
     for (int i = 0; i < IPL; ++i) {
-        const int e = i * 32 + lane, ge = static_cast<int>((static_cast<uint32_t>(e) * a.per_magic) >> 20);
+        const int e = lane * IPL + i, ge = static_cast<int>((static_cast<uint32_t>(e) * a.per_magic) >> 20);
         if (e < a.E && !(stay >> (ge << a.shift) & 1u))
             key[i] = 0;
     }
 }
 
-// The k largest keys: lane j gets slot j's expert and key; the one after them (e -1: there is none).
-// Returns how many there are.
-template <int IPL, typename K>
-__device__ __forceinline__ int choose_keys(int k, K (&key)[IPL], int lane, int &my_idx, K &mine, int &next_idx, K &next)
-{
-    mine = next = 0;
-    next_idx = -1;
-    for (int j = 0;; ++j) {
-        K best = key[0];
-#pragma unroll
-        for (int i = 1; i < IPL; ++i)
-            best = max(best, key[i]);
-        const K m = warp_max(best);
-        if (m == 0)
-            return j;   // only what is never chosen is left
-        int at = INT_MAX;
-#pragma unroll
-        for (int i = IPL - 1; i >= 0; --i)
-            at = key[i] == m ? i * 32 + lane : at;
-        const int e = __reduce_min_sync(ALL, at);
-        if (j == k) {
-            next_idx = e;
-            next = m;
-            return k;
-        }
-#pragma unroll
-        for (int i = 0; i < IPL; ++i)
-            key[i] = i * 32 + lane == e ? 0 : key[i];
-        my_idx = lane == j ? e : my_idx;
-        mine = lane == j ? m : mine;
-    }
-}
-
-// The choice in 64 bits.
+// The choice in 64 bits of all experts.
 template <typename T, int IPL>
 __device__ __noinline__ int choose_exactly(const ScoreArgs &a, const T *l, uint64_t *seen, int lane, int &my_idx)
 {
+    constexpr int UNROLL = IPL <= 8 ? IPL : 1;
     double c[IPL], top = 0.0, total = 1.0;
 #pragma unroll
     for (int i = 0; i < IPL; ++i)
-        c[i] = i * 32 + lane < a.E ? static_cast<double>(to_f<T>(l[i * 32 + lane])) : -INFINITY;
+        c[i] = lane * IPL + i < a.E ? static_cast<double>(to_f<T>(l[lane * IPL + i])) : -INFINITY;
     if (a.softmax) {
         float m = -INFINITY;   // (the logits have at most 32 bits)
 #pragma unroll
@@ -145,27 +172,114 @@ __device__ __noinline__ int choose_exactly(const ScoreArgs &a, const T *l, uint6
             m = fmaxf(m, static_cast<float>(c[i]));
         top = static_cast<double>(warp_max_f(m));
         total = 0.0;
-#pragma unroll 1
+#pragma unroll UNROLL
         for (int i = 0; i < IPL; ++i)
-            if (i * 32 + lane < a.E)
+            if (lane * IPL + i < a.E)
                 total += exp(c[i] - top);
         total = warp_sum(total);
     }
     uint64_t key[IPL];
-#pragma unroll 1
+#pragma unroll UNROLL
     for (int i = 0; i < IPL; ++i) {
         key[i] = 0;
-        if (i * 32 + lane < a.E && c[i] != -INFINITY) {
+        if (lane * IPL + i < a.E && c[i] != -INFINITY) {
             const double s = a.softmax ? exp(c[i] - top) / total : 1.0 / (1.0 + exp(-c[i]));
-            key[i] = order_key(a.bias ? s + static_cast<double>(a.bias[i * 32 + lane]) : s);
+            key[i] = order_key(a.bias ? s + static_cast<double>(a.bias[lane * IPL + i]) : s);
         }
     }
-    uint64_t u0, u1, mine;
-    int next_idx;
+    if (a.groups > 1) {
+        uint64_t least, most;
+        keep_groups<IPL>(a, key, seen, lane, least, most);
+    }
     my_idx = -1;
-    if (a.groups > 1)
-        keep_groups<IPL>(a, key, seen, lane, u0, u1);
-    return choose_keys<IPL>(a.k, key, lane, my_idx, mine, next_idx, u0);
+    for (int j = 0; j < a.k; ++j) {
+        uint64_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < IPL; ++i)
+            best = max(best, key[i]);
+        const uint64_t m = warp_max(best);
+        if (m == 0)
+            return j;   // only what is never chosen is left
+        int at = INT_MAX;
+#pragma unroll
+        for (int i = IPL - 1; i >= 0; --i)
+            at = key[i] == m ? lane * IPL + i : at;
+        const int e = __reduce_min_sync(ALL, at);
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+            key[i] = lane * IPL + i == e ? 0 : key[i];
+        my_idx = lane == j ? e : my_idx;
+    }
+    return a.k;
+}
+
+template <int IPL>
+__device__ __forceinline__ uint32_t take_largest(uint32_t (&word)[IPL])
+{
+    uint32_t best = word[0];
+#pragma unroll
+    for (int i = 1; i < IPL; ++i)
+        best = max(best, word[i]);
+    const uint32_t m = warp_max(best);
+#pragma unroll
+    for (int i = 0; i < IPL; ++i)
+        word[i] = word[i] == m ? 0u : word[i];
+    return m;
+}
+
+// The n candidates in lanes 0 .. n - 1 by their values in 64 bits: lane j gets the j-th.
+template <bool DIRECT>
+__device__ __noinline__ int rank_exactly(float logit, float bias, bool has_bias, int idx, int n, int lane)
+{
+    const double l = static_cast<double>(logit), s = DIRECT ? l : 1.0 / (1.0 + exp(-l));
+    const uint64_t key = order_key(has_bias ? s + static_cast<double>(bias) : s);
+    int rank = 0;
+    for (int r = 0; r < n; ++r) {
+        const uint64_t other = __shfl_sync(ALL, key, r);
+        const int its = __shfl_sync(ALL, idx, r);
+        rank += other > key || (other == key && its < idx);
+    }
+    int got = -1;
+    for (int r = 0; r < n; ++r) {
+        const int at = __shfl_sync(ALL, rank, r), its = __shfl_sync(ALL, idx, r);
+        got = at == lane ? its : got;
+    }
+    return got;
+}
+
+// A lane's IPL neighbouring logits or biases, in accesses of up to 16 bytes where `vec` (the rows allow it);
+// -inf past the last expert.
+template <typename T, int IPL>
+__device__ __forceinline__ void load_lane(float (&f)[IPL], const T *row, int lane, int E, bool vec)
+{
+    constexpr int BYTES = IPL * static_cast<int>(sizeof(T)), PIECE = BYTES < 16 ? BYTES : 16, N = PIECE / static_cast<int>(sizeof(T));
+    if (N > 1 && vec) {   // (whole lanes are in or out)
+        struct alignas(PIECE) Piece {
+            T v[N];
+        };
+        Piece q[IPL / N];
+        const bool in = lane * IPL < E;
+#pragma unroll
+        for (int i = 0; i < IPL / N; ++i)
+            if (in)
+                q[i] = reinterpret_cast<const Piece *>(row + lane * IPL)[i];
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+            f[i] = in ? to_f<T>(q[i / N].v[i % N]) : -INFINITY;
+    } else {
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+            f[i] = lane * IPL + i < E ? to_f<T>(row[lane * IPL + i]) : -INFINITY;
+    }
+}
+
+// 1/(1 + exp(-l)) by two approximate instructions.
+__device__ __forceinline__ float logistic(float l)
+{
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return s;
 }
 
 template <typename T, int IPL>
@@ -180,10 +294,10 @@ __global__ void __launch_bounds__(WARPS * 32) score_kernel(const ScoreArgs a)
     float my_w = 0.0f;
     if (!a.mask || a.mask[t]) {
         const T *l = static_cast<const T *>(a.logits) + static_cast<size_t>(t) * a.ld;
-        float f[IPL], top = 0.0f, total = 1.0f;
-#pragma unroll
-        for (int i = 0; i < IPL; ++i)
-            f[i] = i * 32 + lane < a.E ? to_f<T>(l[i * 32 + lane]) : -INFINITY;
+        float f[IPL], b[IPL], top = 0.0f, total = 1.0f;
+        load_lane<T, IPL>(f, l, lane, a.E, a.vec);
+        if (a.bias)
+            load_lane<float, IPL>(b, a.bias, lane, a.E, a.bias_vec);
         // without a bias scores are in the order of the logits, which are exact
         const bool direct = !a.bias && (a.groups == 1 || !a.pair);
         if (a.softmax && !(direct && a.renorm)) {
@@ -195,65 +309,106 @@ __global__ void __launch_bounds__(WARPS * 32) score_kernel(const ScoreArgs a)
             total = 0.0f;
 #pragma unroll
             for (int i = 0; i < IPL; ++i)
-                if (i * 32 + lane < a.E)
+                if (lane * IPL + i < a.E)
                     total += expf(f[i] - top);
             total = warp_sum(total);
         }
-        uint32_t key[IPL];
-        float open = 0.0f;   // two values this near (and 2^-22 of their size) are open
+        uint32_t word[IPL];
+        // Two values of c that are this near (and 2^-22 of their size) are open.  Errors in units of 2^-24: the sigmoid's
+        // exponential (1.3 |l| + 2.8) times s (1 - s), at most 1, its sum 1/2, the reciprocal 2; softmax (times 1/total, the
+        // largest probability) 8 of the two exponentials and quotients, ln E of the exponents' roundings and 1/2
+        // for each of the sum's IPL + 5 additions.  Twice that for two values.
+        float open = 0.0f;
         if (direct) {
 #pragma unroll
             for (int i = 0; i < IPL; ++i)
-                key[i] = order_key(f[i]);
+                word[i] = plain_key(f[i] + 0.0f);
         } else {
-            // Errors of c in units of 2^-24: sigmoid at most 4 of its exponential, times s (1 - s) <= 1/4, its sum
-            // 1/2 and the quotient 1/2; softmax (times 1/total, the largest probability) 8 of the two
-            // exponentials and quotients, ln E of the exponents' roundings and 1/2 for each of the sum's IPL + 5
-            // additions.  Twice that for two values, and twice again.
             open = a.softmax ? (2.0f * IPL + 72.0f) * 0x1p-24f / total : 0x1p-21f;
+            const float inv = 1.0f / total;
 #pragma unroll
             for (int i = 0; i < IPL; ++i) {
-                const int e = i * 32 + lane;
-                key[i] = 0u;
-                if (e < a.E && f[i] != -INFINITY) {
-                    const float s = a.softmax ? expf(f[i] - top) / total : 1.0f / (1.0f + expf(-f[i]));
-                    key[i] = order_key(a.bias ? s + __ldg(a.bias + e) : s);
-                }
+                const float s = a.softmax ? expf(f[i] - top) * inv : logistic(f[i]), c = a.bias ? s + b[i] : s;
+                word[i] = f[i] == -INFINITY ? 0u : plain_key(c + 0.0f);
             }
         }
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+            word[i] = word[i] <= NEVER ? 0u : word[i];
         bool sure = true;
         if (a.groups > 1) {
             uint32_t least, most;
-            keep_groups<IPL>(a, key, reinterpret_cast<uint32_t *>(seen[warp]), lane, least, most);
+            keep_groups<IPL>(a, word, reinterpret_cast<uint32_t *>(seen[warp]), lane, least, most);
             if (!direct && most != 0u) {
                 const float v = key_value(least);
                 sure = v - key_value(most) > 2.0f * open + fabsf(v) * 0x1p-21f;
             }
         }
-        uint32_t mine, next;
-        int next_idx;
-        int found = choose_keys<IPL>(a.k, key, lane, my_idx, mine, next_idx, next);
-        float logit = lane < found ? to_f<T>(l[my_idx]) : 0.0f;
-        if (!direct) {
-            // every slot is above the one after it, or equal to it in what it is computed from
-            const float b = a.bias && lane < found ? __ldg(a.bias + my_idx) : 0.0f;
-            uint32_t after = __shfl_down_sync(ALL, mine, 1);
-            float after_logit = __shfl_down_sync(ALL, logit, 1), after_b = __shfl_down_sync(ALL, b, 1);
-            if (lane == a.k - 1) {
-                after = next;
-                after_logit = next_idx >= 0 ? to_f<T>(l[next_idx]) : 0.0f;
-                after_b = next_idx >= 0 && a.bias ? __ldg(a.bias + next_idx) : 0.0f;
+        int found;
+        float logit;
+        if (sure) {
+#pragma unroll
+            for (int i = 0; i < IPL; ++i)
+                word[i] = word[i] ? word_of<IPL>(word[i], lane, i) : 0u;
+            // lanes 0 .. n - 1 get the k largest words and the one after them
+            uint32_t mine = 0u;
+            const int most = min(a.k + 1, 32);
+            int n = 0;
+            bool left = true;   // there are others
+            for (; n < most; ++n) {
+                const uint32_t m = take_largest<IPL>(word);
+                if (m == 0u) {
+                    left = false;   // only what is never chosen
+                    break;
+                }
+                mine = lane == n ? m : mine;
             }
-            bool ok = true;
-            if (lane < found && after != 0u) {
-                const float v = key_value(mine);
-                ok = v - key_value(after) > open + fabsf(v) * 0x1p-22f || (logit == after_logit && b == after_b);
+            my_idx = lane < n ? expert_of<IPL>(mine) : -1;
+            logit = lane < n ? to_f<T>(l[my_idx]) : 0.0f;
+            found = min(n, a.k);
+            if (!direct || sizeof(T) == 4) {
+                const bool more = n > a.k || left;   // (with k = 32 the one after them is not in a lane)
+                float bias = a.bias && lane < n ? __ldg(a.bias + my_idx) : 0.0f;
+                // what the words leave out is below the k-th, and every slot above the one after it, or equal to it in
+                // what it is computed from
+                float c = logit;
+                if (!direct)
+                    c = (a.softmax ? expf(logit - top) / total : 1.0f / (1.0f + expf(-logit))) + bias;
+                const float after = __shfl_down_sync(ALL, c, 1), after_logit = __shfl_down_sync(ALL, logit, 1);
+                const float after_bias = __shfl_down_sync(ALL, bias, 1);
+                const int after_idx = __shfl_down_sync(ALL, my_idx, 1);
+                bool ok = true;
+                if (lane + 1 < n)
+                    ok = c - after > open + fabsf(c) * (direct ? 0.0f : 0x1p-22f) ||
+                         (logit == after_logit && bias == after_bias && my_idx < after_idx);
+                const auto apart = [&](uint32_t last) {   // (all lanes: what is below `last` is below the k-th)
+                    const float v = least_of<IPL>(__shfl_sync(ALL, mine, a.k - 1));
+                    return v - most_of<IPL>(last) > open + fabsf(v) * (direct ? 0.0f : 0x1p-22f);
+                };
+                bool whole = !more || (n > a.k && apart(__shfl_sync(ALL, mine, a.k & 31)));
+                if (!whole || !__all_sync(ALL, ok)) {
+                    while (!whole && n < 32) {
+                        const uint32_t m = take_largest<IPL>(word);
+                        mine = lane == n ? m : mine;
+                        whole = m == 0u || apart(m);
+                        n += m != 0u;
+                    }
+                    if (!whole || (a.softmax && !direct)) {
+                        found = choose_exactly<T, IPL>(a, l, seen[warp], lane, my_idx);
+                    } else {
+                        my_idx = lane < n ? expert_of<IPL>(mine) : -1;
+                        logit = lane < n ? to_f<T>(l[my_idx]) : 0.0f;
+                        bias = a.bias && lane < n ? __ldg(a.bias + my_idx) : 0.0f;
+                        my_idx = direct ? rank_exactly<true>(logit, 0.0f, false, my_idx, n, lane)
+                                        : rank_exactly<false>(logit, bias, a.bias, my_idx, n, lane);
+                    }
+                    logit = lane < found ? to_f<T>(l[my_idx]) : 0.0f;
+                }
             }
-            sure = __all_sync(ALL, ok && sure);
-            if (!sure) {
-                found = choose_exactly<T, IPL>(a, l, seen[warp], lane, my_idx);
-                logit = lane < found ? to_f<T>(l[my_idx]) : 0.0f;
-            }
+            my_idx = lane < found ? my_idx : -1;
+        } else {
+            found = choose_exactly<T, IPL>(a, l, seen[warp], lane, my_idx);
+            logit = lane < found ? to_f<T>(l[my_idx]) : 0.0f;
         }
         float p = 0.0f;
         if (a.softmax) {
@@ -264,9 +419,11 @@ __global__ void __launch_bounds__(WARPS * 32) score_kernel(const ScoreArgs a)
                 total = warp_sum(p);
         } else {
             // s = exp(l - m) / (1 + exp(l)) * exp(m), m = min(0, largest): all scores may be tiny, their quotients are not
-            const float m = a.renorm ? fminf(0.0f, warp_max_f(lane < found ? logit : -INFINITY)) : 0.0f;
-            if (lane < found)
-                p = (logit >= 0.0f ? 1.0f : expf(logit - m)) / (1.0f + expf(-fabsf(logit)));
+            const float e = expf(-fabsf(logit));
+            float over = logit >= 0.0f ? 1.0f : e;
+            if (a.renorm && !__any_sync(ALL, lane < found && logit >= 0.0f))
+                over = expf(logit - warp_max_f(lane < found ? logit : -INFINITY));
+            p = lane < found ? over / (1.0f + e) : 0.0f;
             total = a.renorm ? warp_sum(p) : 1.0f;
         }
         if (lane < found)
@@ -396,16 +553,31 @@ int moe_route_scores(int T, int E, int topk, const void *logits, int64_t ld, int
         !op_aligned(topk_idx, 8) || !op_aligned(topk_w, 4))
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
-    ScoreArgs a{T, E, topk, logits, ld, bias, token_mask, score == MOE_SCORE_SOFTMAX, renormalize, groups, topk_groups, group_top == 2,
-                E / groups, 1, 0, 0, scale, topk_idx, topk_w};
-    if (topk_groups == groups)
-        a.groups = a.kept = 1;   // all of them stay: no groups
+    ScoreArgs a{};
+    a.T = T, a.E = E, a.k = topk;
+    a.logits = logits, a.ld = ld, a.bias = bias, a.mask = token_mask;
+    a.softmax = score == MOE_SCORE_SOFTMAX, a.renorm = renormalize, a.scale = scale;
+    a.idx = topk_idx, a.w = topk_w;
+    a.groups = topk_groups == groups ? 1 : groups;   // (if all of them stay there are none)
+    a.kept = topk_groups, a.pair = group_top == 2;
     a.per = E / a.groups;
+    a.lanes = 1;
     while ((a.lanes * 2) * a.groups <= 32) {
         a.lanes *= 2;
         ++a.shift;
     }
     a.per_magic = (1u << 20) / static_cast<uint32_t>(a.per) + 1;   // exact for e, per <= 1024
+    const int ipl = lane_experts(E);
+    a.group_shift = -1;
+    for (int s = 0; s <= 5; ++s)
+        if (a.per == ipl << s)
+            a.group_shift = s;
+    const auto vectors = [&](const void *p, size_t pitch, size_t size) {
+        const size_t piece = ipl * size < 16 ? ipl * size : 16;
+        return E % ipl == 0 && op_aligned(p, piece) && pitch * size % piece == 0;
+    };
+    a.vec = vectors(logits, static_cast<size_t>(ld), dtype_bytes(dtype));
+    a.bias_vec = vectors(bias, 0, 4);
     by_width<ScoreLaunch>(dtype, E, a, static_cast<cudaStream_t>(stream));
     return launched();
 }
