@@ -57,13 +57,18 @@ template <int IPL>
 constexpr int BITS = IPL == 1 ? 5 : IPL == 2 ? 6 : IPL == 4 ? 7 : IPL == 8 ? 8 : 10;
 template <int IPL>
 constexpr uint32_t ID = (1u << BITS<IPL>) - 1u;
-constexpr uint32_t NEVER = 0x007FFFFFu;   // the key of -inf, and words and keys that are not there
+template <typename K>   // the key of -inf; words and keys up to it are not there
+constexpr K NEVER = sizeof(K) == 4 ? static_cast<K>(0x007FFFFFu) : static_cast<K>(0x000FFFFFFFFFFFFFull);
 
 // Order key of a sum or product (whose NaN is the positive one).
 __device__ __forceinline__ uint32_t plain_key(float f)
 {
     const uint32_t u = __float_as_uint(f);
     return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float plain_value(uint32_t key)
+{
+    return __uint_as_float(key ^ (static_cast<uint32_t>(static_cast<int32_t>(~key) >> 31) | 0x80000000u));
 }
 template <int IPL>
 __device__ __forceinline__ uint32_t word_of(uint32_t key, int lane, int i)
@@ -74,30 +79,34 @@ template <int IPL>
 __device__ __forceinline__ int expert_of(uint32_t word) { return static_cast<int>(ID<IPL> - (word & ID<IPL>)); }
 // The least and the most that the c of a word can be.
 template <int IPL>
-__device__ __forceinline__ float least_of(uint32_t word) { return key_value(word & ~ID<IPL>); }
+__device__ __forceinline__ float least_of(uint32_t word) { return plain_value(word & ~ID<IPL>); }
 template <int IPL>
-__device__ __forceinline__ float most_of(uint32_t word) { return key_value(word | ID<IPL>); }
+__device__ __forceinline__ float most_of(uint32_t word) { return plain_value(word | ID<IPL>); }
 
-// Whether the lane's group of experts stays, from the group's two largest keys (0: none): `least` and `most` are
+// Whether the lane's group of experts stays, from the group's two largest keys: `least` and `most` are
 // the lowest score that stays and the highest that does not (0: none).  Group g is that of the lanes
 // g << shift and after.
+__device__ __forceinline__ uint32_t key_sum(uint32_t a, uint32_t b) { return plain_key(plain_value(a) + plain_value(b)); }
+__device__ __forceinline__ uint64_t key_sum(uint64_t a, uint64_t b) { return order_key(key_value(a) + key_value(b)); }
 template <typename K>
 __device__ __forceinline__ bool group_stays(const ScoreArgs &a, K first, K second, int lane, int shift, K &least, K &most)
 {
     const int g = lane >> shift;
-    K score = first;
-    if (a.pair && second != 0)
-        score = order_key(key_value(first) + key_value(second));
-    int rank = 0;
-#pragma unroll 4
-    for (int h = 0; h < a.groups; ++h) {
-        const K other = __shfl_sync(ALL, score, h << shift);
-        rank += other > score || (other == score && h < g);
+    K score = g < a.groups && first > NEVER<K> ? first : 0;
+    if (a.pair && second > NEVER<K>)
+        score = key_sum(first, second);
+    bool stays = false;
+    least = 0;
+    for (int j = 0; j < a.kept; ++j) {
+        const K m = warp_max(score);
+        if (m == 0)
+            break;
+        least = m;
+        const int best = (__ffs(static_cast<int>(__ballot_sync(ALL, score == m))) - 1) >> shift;   // ties: the lowest
+        stays = stays || g == best;
+        score = g == best ? 0 : score;
     }
-    const bool there = g < a.groups && score != 0, stays = there && rank < a.kept;
-    // the lowest: the complement of the largest complement
-    least = ~warp_max(stays ? static_cast<K>(~score) : static_cast<K>(0));
-    most = warp_max(there && !stays ? score : static_cast<K>(0));
+    most = warp_max(score);
     return stays;
 }
 template <typename K>
@@ -126,8 +135,9 @@ __device__ __forceinline__ void keep_groups(const ScoreArgs &a, K (&key)[IPL], K
 {
     K first = 0, second = 0;
     if (a.group_shift >= 0) {   // a group is 1 << group_shift lanes
+        first = key[0];
 #pragma unroll
-        for (int i = 0; i < IPL; ++i)
+        for (int i = 1; i < IPL; ++i)
             insert(key[i], first, second);
         merge_lanes(first, second, 1 << a.group_shift);
         const bool stays = group_stays(a, first, second, lane, a.group_shift, least, most);
@@ -213,18 +223,57 @@ __device__ __noinline__ int choose_exactly(const ScoreArgs &a, const T *l, uint6
     return a.k;
 }
 
+// A lane's words in descending order (a sorting network; words differ), so that a lane's largest is its first;
+// more than 8 stay as they are.
 template <int IPL>
-__device__ __forceinline__ uint32_t take_largest(uint32_t (&word)[IPL])
+constexpr bool SORTED = IPL <= 8;
+__device__ __forceinline__ void order_two(uint32_t &a, uint32_t &b)
 {
-    uint32_t best = word[0];
+    const uint32_t hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+template <int IPL>
+__device__ __forceinline__ void sort_lane(uint32_t (&w)[IPL])
+{
+    if constexpr (SORTED<IPL>) {
+        // odd-even merges (Batcher)
 #pragma unroll
-    for (int i = 1; i < IPL; ++i)
-        best = max(best, word[i]);
-    const uint32_t m = warp_max(best);
+        for (int p = 1; p < IPL; p *= 2)
 #pragma unroll
-    for (int i = 0; i < IPL; ++i)
-        word[i] = word[i] == m ? 0u : word[i];
-    return m;
+            for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+                for (int j = k % p; j + k < IPL; j += 2 * k)
+#pragma unroll
+                    for (int i = 0; i < k; ++i)
+                        if (i + j + k < IPL && (i + j) / (2 * p) == (i + j + k) / (2 * p))
+                            order_two(w[i + j], w[i + j + k]);
+    }
+}
+// The warp's largest word, taken out.
+template <int IPL>
+__device__ __forceinline__ uint32_t take_largest(uint32_t (&w)[IPL])
+{
+    if constexpr (SORTED<IPL>) {
+        const uint32_t m = warp_max(w[0]);
+        if (w[0] == m) {
+#pragma unroll
+            for (int i = 0; i + 1 < IPL; ++i)
+                w[i] = w[i + 1];
+            w[IPL - 1] = 0u;
+        }
+        return m;
+    } else {
+        uint32_t best = w[0];
+#pragma unroll
+        for (int i = 1; i < IPL; ++i)
+            best = max(best, w[i]);
+        const uint32_t m = warp_max(best);
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+            w[i] = w[i] == m ? 0u : w[i];
+        return m;
+    }
 }
 
 // The n candidates in lanes 0 .. n - 1 by their values in 64 bits: lane j gets the j-th.
@@ -322,76 +371,86 @@ __global__ void __launch_bounds__(WARPS * 32) score_kernel(const ScoreArgs a)
         if (direct) {
 #pragma unroll
             for (int i = 0; i < IPL; ++i)
-                word[i] = plain_key(f[i] + 0.0f);
+                word[i] = plain_key(f[i] + 0.0f);   // (-0 as +0)
         } else {
             open = a.softmax ? (2.0f * IPL + 72.0f) * 0x1p-24f / total : 0x1p-21f;
             const float inv = 1.0f / total;
 #pragma unroll
             for (int i = 0; i < IPL; ++i) {
-                const float s = a.softmax ? expf(f[i] - top) * inv : logistic(f[i]), c = a.bias ? s + b[i] : s;
-                word[i] = f[i] == -INFINITY ? 0u : plain_key(c + 0.0f);
+                const float s = a.softmax ? expf(f[i] - top) * inv : logistic(f[i]);
+                // (the sum is of no account but for a logit of -inf)
+                word[i] = plain_key(fminf(a.bias ? s + b[i] : s, f[i] + 3e38f));
             }
         }
-#pragma unroll
-        for (int i = 0; i < IPL; ++i)
-            word[i] = word[i] <= NEVER ? 0u : word[i];
         bool sure = true;
         if (a.groups > 1) {
             uint32_t least, most;
             keep_groups<IPL>(a, word, reinterpret_cast<uint32_t *>(seen[warp]), lane, least, most);
             if (!direct && most != 0u) {
-                const float v = key_value(least);
-                sure = v - key_value(most) > 2.0f * open + fabsf(v) * 0x1p-21f;
+                const float v = plain_value(least);
+                sure = v - plain_value(most) > 2.0f * open + fabsf(v) * 0x1p-21f;
             }
         }
         int found;
-        float logit;
+        float logit, e, s = 0.0f;   // of the lane's candidate: its logit, exp(-|logit|), its score
+        const auto look = [&](int idx, bool is) {
+            logit = is ? to_f<T>(l[idx]) : 0.0f;
+            e = expf(-fabsf(logit));
+            if (!a.softmax)
+                s = __fdividef(logit >= 0.0f ? 1.0f : e, 1.0f + e);
+            else if (!direct)
+                s = expf(logit - top) / total;
+        };
         if (sure) {
 #pragma unroll
             for (int i = 0; i < IPL; ++i)
-                word[i] = word[i] ? word_of<IPL>(word[i], lane, i) : 0u;
+                word[i] = word_of<IPL>(word[i], lane, i);
+            sort_lane<IPL>(word);
             // lanes 0 .. n - 1 get the k largest words and the one after them
             uint32_t mine = 0u;
-            const int most = min(a.k + 1, 32);
+            const int most = min(direct && sizeof(T) == 2 ? a.k : a.k + 1, 32);
             int n = 0;
             bool left = true;   // there are others
             for (; n < most; ++n) {
                 const uint32_t m = take_largest<IPL>(word);
-                if (m == 0u) {
+                if (m <= NEVER<uint32_t>) {
                     left = false;   // only what is never chosen
                     break;
                 }
                 mine = lane == n ? m : mine;
             }
             my_idx = lane < n ? expert_of<IPL>(mine) : -1;
-            logit = lane < n ? to_f<T>(l[my_idx]) : 0.0f;
+            look(my_idx, lane < n);
             found = min(n, a.k);
             if (!direct || sizeof(T) == 4) {
                 const bool more = n > a.k || left;   // (with k = 32 the one after them is not in a lane)
                 float bias = a.bias && lane < n ? __ldg(a.bias + my_idx) : 0.0f;
                 // what the words leave out is below the k-th, and every slot above the one after it, or equal to it in
                 // what it is computed from
-                float c = logit;
-                if (!direct)
-                    c = (a.softmax ? expf(logit - top) / total : 1.0f / (1.0f + expf(-logit))) + bias;
-                const float after = __shfl_down_sync(ALL, c, 1), after_logit = __shfl_down_sync(ALL, logit, 1);
-                const float after_bias = __shfl_down_sync(ALL, bias, 1);
-                const int after_idx = __shfl_down_sync(ALL, my_idx, 1);
-                bool ok = true;
-                if (lane + 1 < n)
-                    ok = c - after > open + fabsf(c) * (direct ? 0.0f : 0x1p-22f) ||
-                         (logit == after_logit && bias == after_bias && my_idx < after_idx);
-                const auto apart = [&](uint32_t last) {   // (all lanes: what is below `last` is below the k-th)
-                    const float v = least_of<IPL>(__shfl_sync(ALL, mine, a.k - 1));
-                    return v - most_of<IPL>(last) > open + fabsf(v) * (direct ? 0.0f : 0x1p-22f);
+                const float c = direct ? logit : s + bias;
+                const float after = __shfl_down_sync(ALL, c, 1);
+                const float near = direct ? 0.0f : 0x1p-22f;
+                bool ok = lane + 1 >= n || c - after > open + fabsf(c) * near;
+                if (!__all_sync(ALL, ok)) {
+                    const float after_logit = __shfl_down_sync(ALL, logit, 1), after_bias = __shfl_down_sync(ALL, bias, 1);
+                    const int after_idx = __shfl_down_sync(ALL, my_idx, 1);
+                    ok = __all_sync(ALL, ok || (logit == after_logit && bias == after_bias && my_idx < after_idx));
+                }
+                const uint32_t last = __shfl_sync(ALL, mine, a.k - 1);
+                const auto apart = [&](uint32_t word_after) {
+                    const float v = least_of<IPL>(last);
+                    return v - most_of<IPL>(word_after) > open + fabsf(v) * near;
                 };
                 bool whole = !more || (n > a.k && apart(__shfl_sync(ALL, mine, a.k & 31)));
-                if (!whole || !__all_sync(ALL, ok)) {
+                if (!whole || !ok) {
                     while (!whole && n < 32) {
                         const uint32_t m = take_largest<IPL>(word);
-                        mine = lane == n ? m : mine;
-                        whole = m == 0u || apart(m);
-                        n += m != 0u;
+                        whole = m <= NEVER<uint32_t>;
+                        if (!whole) {
+                            mine = lane == n ? m : mine;
+                            ++n;
+                            whole = apart(m);
+                        }
                     }
                     if (!whole || (a.softmax && !direct)) {
                         found = choose_exactly<T, IPL>(a, l, seen[warp], lane, my_idx);
@@ -402,31 +461,32 @@ __global__ void __launch_bounds__(WARPS * 32) score_kernel(const ScoreArgs a)
                         my_idx = direct ? rank_exactly<true>(logit, 0.0f, false, my_idx, n, lane)
                                         : rank_exactly<false>(logit, bias, a.bias, my_idx, n, lane);
                     }
-                    logit = lane < found ? to_f<T>(l[my_idx]) : 0.0f;
+                    look(my_idx, lane < found);
                 }
             }
             my_idx = lane < found ? my_idx : -1;
         } else {
             found = choose_exactly<T, IPL>(a, l, seen[warp], lane, my_idx);
-            logit = lane < found ? to_f<T>(l[my_idx]) : 0.0f;
+            look(my_idx, lane < found);
         }
+        const bool chosen = lane < found;
         float p = 0.0f;
         if (a.softmax) {
             if (a.renorm)
-                top = warp_max_f(lane < found ? logit : -INFINITY);
-            p = lane < found ? expf(logit - top) : 0.0f;
+                top = warp_max_f(chosen ? logit : -INFINITY);
+            p = chosen ? expf(logit - top) : 0.0f;
             if (a.renorm)
                 total = warp_sum(p);
         } else {
-            // s = exp(l - m) / (1 + exp(l)) * exp(m), m = min(0, largest): all scores may be tiny, their quotients are not
-            const float e = expf(-fabsf(logit));
-            float over = logit >= 0.0f ? 1.0f : e;
-            if (a.renorm && !__any_sync(ALL, lane < found && logit >= 0.0f))
-                over = expf(logit - warp_max_f(lane < found ? logit : -INFINITY));
-            p = lane < found ? over / (1.0f + e) : 0.0f;
+            p = chosen ? s : 0.0f;
+            // all scores may be tiny, their quotients are not: s = exp(l - m) / (1 + exp(l)) * exp(m) with m the largest
+            if (a.renorm && !__any_sync(ALL, chosen && logit >= 0.0f)) {
+                const float m = warp_max_f(chosen ? logit : -INFINITY);
+                p = chosen ? expf(logit - m) / (1.0f + e) : 0.0f;
+            }
             total = a.renorm ? warp_sum(p) : 1.0f;
         }
-        if (lane < found)
+        if (chosen)
             my_w = p / total * a.scale;
     }
     if (lane < a.k) {
@@ -475,8 +535,8 @@ __global__ void __launch_bounds__(WARPS * 32) score_backward_kernel(const ScoreB
     if (!a.softmax && e >= 0)
         d /= 1.0f + expf(to_f<T>(l[e]));
     // an expert that is in several slots gets their sum, in order
-    const uint32_t same = __match_any_sync(ALL, e >= 0 ? e : -1 - lane);
-    if (__any_sync(ALL, same & (same - 1u))) {
+    const uint32_t same = __match_any_sync(ALL, e);
+    if (__any_sync(ALL, e >= 0 && (same & (same - 1u)) != 0u)) {
         float sum = 0.0f;
         for (int j = 0; j < a.k; ++j) {
             const float v = __shfl_sync(ALL, d, j);
