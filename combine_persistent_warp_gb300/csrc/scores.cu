@@ -50,9 +50,11 @@ __device__ __forceinline__ float warp_max_f(float v)
 // ------------------------------------------------------------------ the choice ----------
 // Lane l holds experts l * IPL .. l * IPL + IPL - 1 (a group of experts is then a few neighbouring lanes, mostly).
 //
-// A word is what the choice goes by: the upper bits of c's order key and, below them, the expert (ties to
-// the lowest), so that one warp maximum a slot finds both.  The bits that the expert takes from the key make
-// more values look equal; what the words leave open is settled by the candidates' exact values.
+// A word is what the choice goes by: c in its upper bits and, below them, the expert (ties to the lowest), so that
+// one warp maximum a slot finds both.  The bits that the expert takes make a few more values look equal; what
+// the words leave open is settled by the candidates' exact values.  c is there as the upper bits of its order
+// key or, where it is a sigmoid with a bias between -0.999 and 0.999, as a whole number of 2^-21 (FIXED): near 1 the
+// key's 7 bits less would leave 2^-16.
 template <int IPL>
 constexpr int BITS = IPL == 1 ? 5 : IPL == 2 ? 6 : IPL == 4 ? 7 : IPL == 8 ? 8 : 10;
 template <int IPL>
@@ -70,18 +72,37 @@ __device__ __forceinline__ float plain_value(uint32_t key)
 {
     return __uint_as_float(key ^ (static_cast<uint32_t>(static_cast<int32_t>(~key) >> 31) | 0x80000000u));
 }
-template <int IPL>
-__device__ __forceinline__ uint32_t word_of(uint32_t key, int lane, int i)
+// FIXED: 3 * 2^22 + c * 2^21 as a float, whose bits are in order; a c of -1 stands for one that is not there.
+constexpr float FIXED_ZERO = 12582912.0f, FIXED_ONE = 2097152.0f;
+template <int IPL, bool FIXED>
+__device__ __forceinline__ uint32_t word_of(float c, int lane, int i)
 {
-    return (key & ~ID<IPL>) | (ID<IPL> - static_cast<uint32_t>(lane * IPL + i));
+    const uint32_t id = ID<IPL> - static_cast<uint32_t>(lane * IPL + i);
+    if constexpr (FIXED) {
+        float t;
+        asm("max.NaN.f32 %0, %1, 0fBF800000;" : "=f"(t) : "f"(c));   // (a NaN stays one: the largest)
+        t = fmaf(t, FIXED_ONE, FIXED_ZERO);
+        return (__float_as_uint(t) << BITS<IPL>) + id;
+    } else {
+        return (plain_key(c) & ~ID<IPL>) | id;
+    }
 }
+// Words up to this one are not there.
+template <int IPL, bool FIXED>
+constexpr uint32_t NO_WORD = FIXED ? ((0x4B400000u - 0x200000u) << BITS<IPL>) + ID<IPL> : 0x007FFFFFu;
 template <int IPL>
 __device__ __forceinline__ int expert_of(uint32_t word) { return static_cast<int>(ID<IPL> - (word & ID<IPL>)); }
-// The least and the most that the c of a word can be.
-template <int IPL>
-__device__ __forceinline__ float least_of(uint32_t word) { return plain_value(word & ~ID<IPL>); }
-template <int IPL>
-__device__ __forceinline__ float most_of(uint32_t word) { return plain_value(word | ID<IPL>); }
+// The least (most) that the c of a word can be.
+template <int IPL, bool FIXED, bool MOST>
+__device__ __forceinline__ float bound_of(uint32_t word)
+{
+    if constexpr (FIXED) {
+        const float t = __uint_as_float(0x4B000000u + (word >> BITS<IPL> & 0xFFFFFFu));
+        return (t - FIXED_ZERO) * (1.0f / FIXED_ONE) + (MOST ? 0x1p-22f : -0x1p-22f);
+    } else {
+        return plain_value(MOST ? word | ID<IPL> : word & ~ID<IPL>);
+    }
+}
 
 // Whether the lane's group of experts stays, from the group's two largest keys: `least` and `most` are
 // the lowest score that stays and the highest that does not (0: none).  Group g is that of the lanes
@@ -129,28 +150,28 @@ __device__ __forceinline__ int spot(int e) { return e + (e >> 5) * 4; }
 template <int IPL>
 constexpr int SPOTS = IPL * 36;
 
-// Zeroes the keys of the groups that do not stay.
-template <int IPL, typename K>
-__device__ __forceinline__ void keep_groups(const ScoreArgs &a, K (&key)[IPL], K *seen, int lane, K &least, K &most)
+// -inf in place of the c of the groups that do not stay.
+template <int IPL>
+__device__ __forceinline__ void keep_groups(const ScoreArgs &a, float (&c)[IPL], uint32_t *seen, int lane, uint32_t &least, uint32_t &most)
 {
-    K first = 0, second = 0;
+    uint32_t first = 0, second = 0;
     if (a.group_shift >= 0) {   // a group is 1 << group_shift lanes
-        first = key[0];
+        first = plain_key(c[0]);
 #pragma unroll
         for (int i = 1; i < IPL; ++i)
-            insert(key[i], first, second);
+            insert(plain_key(c[i]), first, second);
         merge_lanes(first, second, 1 << a.group_shift);
         const bool stays = group_stays(a, first, second, lane, a.group_shift, least, most);
 #pragma unroll
         for (int i = 0; i < IPL; ++i)
-            key[i] = stays ? key[i] : 0;
+            c[i] = stays ? c[i] : -INFINITY;
         return;
     }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < IPL; ++i)
         if (lane * IPL + i < a.E)
-            seen[spot(lane * IPL + i)] = key[i];
+            seen[spot(lane * IPL + i)] = plain_key(c[i]);
     __syncwarp();
     const int g = lane >> a.shift;
     if (g < a.groups)
@@ -162,62 +183,67 @@ __device__ __forceinline__ void keep_groups(const ScoreArgs &a, K (&key)[IPL], K
     for (int i = 0; i < IPL; ++i) {
         const int e = lane * IPL + i, ge = static_cast<int>((static_cast<uint32_t>(e) * a.per_magic) >> 20);
         if (e < a.E && !(stay >> (ge << a.shift) & 1u))
-            key[i] = 0;
+            c[i] = -INFINITY;
     }
 }
 
-// The choice in 64 bits of all experts.
+// The choice in 64 bits of all experts.  Seldom run, so that its code is seldom at hand: short, over keys in shared
+// memory.
 template <typename T, int IPL>
 __device__ __noinline__ int choose_exactly(const ScoreArgs &a, const T *l, uint64_t *seen, int lane, int &my_idx)
 {
-    constexpr int UNROLL = IPL <= 8 ? IPL : 1;
-    double c[IPL], top = 0.0, total = 1.0;
-#pragma unroll
-    for (int i = 0; i < IPL; ++i)
-        c[i] = lane * IPL + i < a.E ? static_cast<double>(to_f<T>(l[lane * IPL + i])) : -INFINITY;
+    double top = 0.0, total = 1.0;
     if (a.softmax) {
         float m = -INFINITY;   // (the logits have at most 32 bits)
-#pragma unroll
-        for (int i = 0; i < IPL; ++i)
-            m = fmaxf(m, static_cast<float>(c[i]));
+        for (int e = lane; e < a.E; e += 32)
+            m = fmaxf(m, to_f<T>(l[e]));
         top = static_cast<double>(warp_max_f(m));
-        total = 0.0;
-#pragma unroll UNROLL
-        for (int i = 0; i < IPL; ++i)
-            if (lane * IPL + i < a.E)
-                total += exp(c[i] - top);
-        total = warp_sum(total);
     }
-    uint64_t key[IPL];
-#pragma unroll UNROLL
-    for (int i = 0; i < IPL; ++i) {
-        key[i] = 0;
-        if (lane * IPL + i < a.E && c[i] != -INFINITY) {
-            const double s = a.softmax ? exp(c[i] - top) / total : 1.0 / (1.0 + exp(-c[i]));
-            key[i] = order_key(a.bias ? s + static_cast<double>(a.bias[lane * IPL + i]) : s);
+    // softmax: the sum first
+    for (int pass = a.softmax ? 0 : 1; pass < 2; ++pass) {
+        double sum = 0.0;
+#pragma unroll 2
+        for (int e = lane; e < a.E; e += 32) {
+            const float f = to_f<T>(l[e]);
+            const double x = exp(a.softmax ? static_cast<double>(f) - top : -static_cast<double>(f));
+            sum += x;
+            const double s = (a.softmax ? x : 1.0) / (a.softmax ? total : 1.0 + x);
+            seen[spot(e)] = f == -INFINITY ? 0ull : order_key(a.bias ? s + static_cast<double>(a.bias[e]) : s);
         }
+        if (pass == 0)
+            total = warp_sum(sum);
     }
+    __syncwarp();
     if (a.groups > 1) {
-        uint64_t least, most;
-        keep_groups<IPL>(a, key, seen, lane, least, most);
+        uint64_t first = 0, second = 0, least, most;
+        const int g = lane >> a.shift;
+        if (g < a.groups)
+#pragma unroll 2
+            for (int e = lane & (a.lanes - 1); e < a.per; e += a.lanes)
+                insert(seen[spot(g * a.per + e)], first, second);
+        merge_lanes(first, second, a.lanes);
+        const uint32_t stay = __ballot_sync(ALL, group_stays(a, first, second, lane, a.shift, least, most));
+        for (int e = lane; e < a.E; e += 32)
+            if (!(stay >> (static_cast<int>((static_cast<uint32_t>(e) * a.per_magic) >> 20) << a.shift) & 1u))
+                seen[spot(e)] = 0;
+        __syncwarp();
     }
     my_idx = -1;
     for (int j = 0; j < a.k; ++j) {
-        uint64_t best = key[0];
-#pragma unroll
-        for (int i = 1; i < IPL; ++i)
-            best = max(best, key[i]);
+        uint64_t best = 0;
+        int at = INT_MAX;
+#pragma unroll 4
+        for (int e = lane; e < a.E; e += 32) {
+            const uint64_t key = seen[spot(e)];
+            at = key > best ? e : at;
+            best = max(best, key);
+        }
         const uint64_t m = warp_max(best);
         if (m == 0)
             return j;   // only what is never chosen is left
-        int at = INT_MAX;
-#pragma unroll
-        for (int i = IPL - 1; i >= 0; --i)
-            at = key[i] == m ? lane * IPL + i : at;
-        const int e = __reduce_min_sync(ALL, at);
-#pragma unroll
-        for (int i = 0; i < IPL; ++i)
-            key[i] = lane * IPL + i == e ? 0 : key[i];
+        const int e = __reduce_min_sync(ALL, best == m ? at : INT_MAX);
+        if ((e & 31) == lane)
+            seen[spot(e)] = 0;
         my_idx = lane == j ? e : my_idx;
     }
     return a.k;
@@ -331,168 +357,264 @@ __device__ __forceinline__ float logistic(float l)
     return s;
 }
 
-template <typename T, int IPL>
+// What a token's softmax is taken with, and how near two values of c are open (beside 2^-22 of their size).
+struct Softmax {
+    float top, total, open;
+};
+
+// A token's c from its logits and the biases, without those of the groups that do not stay.  False: which groups
+// stay is open.
+template <int IPL>
+__device__ __forceinline__ bool make_c(const ScoreArgs &a, float (&f)[IPL], const float (&b)[IPL], bool direct, uint64_t *seen, int lane,
+                                       Softmax &sm)
+{
+    sm = {0.0f, 1.0f, 0.0f};
+    if (a.softmax && !(direct && a.renorm)) {
+        sm.top = f[0];
+#pragma unroll
+        for (int i = 1; i < IPL; ++i)
+            sm.top = fmaxf(sm.top, f[i]);
+        sm.top = warp_max_f(sm.top);
+        float total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+            if (lane * IPL + i < a.E)
+                total += expf(f[i] - sm.top);
+        sm.total = warp_sum(total);
+    }
+    if (direct) {
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+            f[i] += 0.0f;   // (-0 as +0)
+    } else {
+        // Errors of c in units of 2^-24: the sigmoid's exponential (1.3 |l| + 2.8) times s (1 - s), at most 1, its
+        // sum 1/2, the reciprocal 2; softmax (times 1/total, the largest probability) 8 of the two exponentials and
+        // quotients, ln E of the exponents' roundings and 1/2 for each of the sum's IPL + 5 additions.  Twice that
+        // for two values.
+        sm.open = a.softmax ? (2.0f * IPL + 72.0f) * 0x1p-24f / sm.total : 0x1p-21f;
+        const float inv = 1.0f / sm.total;
+#pragma unroll
+        for (int i = 0; i < IPL; ++i) {
+            const float s = a.softmax ? expf(f[i] - sm.top) * inv : logistic(f[i]);
+            // (the sum is of no account but for a logit of -inf)
+            f[i] = fminf(a.bias ? s + b[i] : s, f[i] + 3e38f);
+        }
+    }
+    if (a.groups > 1) {
+        uint32_t least, most;
+        keep_groups<IPL>(a, f, reinterpret_cast<uint32_t *>(seen), lane, least, most);
+        if (!direct && most != 0u) {
+            const float v = plain_value(least);
+            return v - plain_value(most) > 2.0f * sm.open + fabsf(v) * 0x1p-21f;
+        }
+    }
+    return true;
+}
+template <int IPL, bool FIXED>
+__device__ __forceinline__ void make_words(uint32_t (&word)[IPL], const float (&c)[IPL], int lane)
+{
+#pragma unroll
+    for (int i = 0; i < IPL; ++i)
+        word[i] = word_of<IPL, FIXED>(c[i], lane, i);
+    sort_lane<IPL>(word);
+}
+// Whether what has the word `after` or a lower one is below what has the word `last`.
+template <int IPL, bool FIXED>
+__device__ __forceinline__ bool apart(uint32_t last, uint32_t after, float open, bool direct)
+{
+    const float v = bound_of<IPL, FIXED, false>(last);
+    return v - bound_of<IPL, FIXED, true>(after) > open + (direct ? 0.0f : fabsf(v) * 0x1p-22f);
+}
+// Without a bias scores are in the order of the logits, which are exact.
+__device__ __forceinline__ bool directly(const ScoreArgs &a) { return !a.bias && (a.groups == 1 || !a.pair); }
+
+// The choice of a token whose words leave it open: as many candidates as the words cannot tell from the k-th,
+// by their values in 64 bits; failing that, all experts by theirs.  Lane j gets slot j's expert.
+template <typename T, int IPL, bool FIXED>
+__device__ __noinline__ int choose_again(const ScoreArgs &a, const T *l, uint64_t *seen, int lane, int &my_idx)
+{
+    const bool direct = directly(a);
+    if (!a.softmax || direct) {
+        float f[IPL], b[IPL];
+        load_lane<T, IPL>(f, l, lane, a.E, a.vec);
+        if (a.bias)
+            load_lane<float, IPL>(b, a.bias, lane, a.E, a.bias_vec);
+        uint32_t word[IPL], mine = 0u, last = 0u;
+        Softmax sm;
+        bool whole = false;
+        int n = 0;
+        if (make_c<IPL>(a, f, b, direct, seen, lane, sm)) {
+            make_words<IPL, FIXED>(word, f, lane);
+            while (!whole && n < 32) {
+                const uint32_t m = take_largest<IPL>(word);
+                whole = m <= NO_WORD<IPL, FIXED>;
+                if (!whole) {
+                    mine = lane == n ? m : mine;
+                    last = n == a.k - 1 ? m : last;
+                    ++n;
+                    whole = n > a.k && apart<IPL, FIXED>(last, m, sm.open, direct);
+                }
+            }
+        }
+        if (whole) {
+            my_idx = lane < n ? expert_of<IPL>(mine) : -1;
+            const float logit = lane < n ? to_f<T>(l[my_idx]) : 0.0f;
+            const float bias = a.bias && lane < n ? __ldg(a.bias + my_idx) : 0.0f;
+            my_idx = direct ? rank_exactly<true>(logit, 0.0f, false, my_idx, n, lane)
+                            : rank_exactly<false>(logit, bias, a.bias, my_idx, n, lane);
+            return min(n, a.k);
+        }
+    }
+    return choose_exactly<T, IPL>(a, l, seen, lane, my_idx);
+}
+
+// Over the SEG lanes of a token.
+template <int SEG>
+__device__ __forceinline__ float seg_sum(float v)
+{
+#pragma unroll
+    for (int o = SEG / 2; o > 0; o >>= 1)
+        v += __shfl_xor_sync(ALL, v, o);
+    return v;
+}
+template <int SEG>
+__device__ __forceinline__ float seg_max(float v)
+{
+#pragma unroll
+    for (int o = SEG / 2; o > 0; o >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(ALL, v, o));
+    return v;
+}
+
+// A warp takes Q tokens: it chooses for one after the other, with all lanes, and then has the slots of all
+// of them, a lane each (SEG = 32/Q >= k lanes a token), for the weights and what is to be checked.
+template <typename T, int IPL, int Q, bool FIXED>
+__device__ __forceinline__ void score_tokens(const ScoreArgs &a, const float (&b)[IPL], uint64_t *seen, int t0, int lane)
+{
+    constexpr int SEG = 32 / Q;
+    const int seg = lane / SEG, slot = lane % SEG, t = t0 + seg;
+    const bool direct = !FIXED && directly(a);
+    // token q's row, by all lanes; bit q * SEG: it is routed
+    const auto row = [&](int q) { return static_cast<const T *>(a.logits) + static_cast<size_t>(t0 + q) * a.ld; };
+    const uint32_t lanes = __ballot_sync(ALL, slot == 0 && t < a.T && (!a.mask || a.mask[t]));
+    float f[Q][IPL];
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+        if (lanes >> (q * SEG) & 1u)
+            load_lane<T, IPL>(f[q], row(q), lane, a.E, a.vec);
+    // this lane's token: how many are found, the words of the slot, of the last and of the one after it
+    int found = 0;
+    uint32_t mine = 0u, next = 0u, last = 0u;
+    Softmax sm{0.0f, 1.0f, 0.0f};
+    bool sure = true;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        if (!(lanes >> (q * SEG) & 1u))
+            continue;
+        uint32_t word[IPL], m = 0u, after = 0u;
+        Softmax its;
+        const bool its_sure = make_c<IPL>(a, f[q], b, direct, seen, lane, its);
+        make_words<IPL, FIXED>(word, f[q], lane);
+        int n = 0;
+        for (; n < a.k; ++n) {
+            const uint32_t largest = take_largest<IPL>(word);
+            if (largest <= NO_WORD<IPL, FIXED>)
+                break;   // only what is never chosen is left
+            m = largest;
+            mine = lane == q * SEG + n ? m : mine;
+        }
+        if (!(direct && sizeof(T) == 2) && n == a.k)
+            after = take_largest<IPL>(word);
+        if (seg == q) {
+            found = n;
+            last = m;
+            next = after;
+            sm = its;
+            sure = its_sure;
+        }
+    }
+    const T *l = static_cast<const T *>(a.logits) + static_cast<size_t>(t) * a.ld;
+    int my_idx = slot < found ? expert_of<IPL>(mine) : -1;
+    float logit, e, s;   // of the lane's slot: its logit, exp(-|logit|), its score
+    const auto look = [&] {
+        logit = slot < found ? to_f<T>(l[my_idx]) : 0.0f;
+        if (a.softmax) {
+            s = expf(logit - sm.top) / sm.total;
+        } else {
+            e = expf(-fabsf(logit));
+            s = __fdividef(logit >= 0.0f ? 1.0f : e, 1.0f + e);
+        }
+    };
+    look();
+    if (!direct || sizeof(T) == 4) {
+        // what the words leave out is below the last slot, and every slot above the one after it, or equal to it in what
+        // it is computed from
+        const float bias = a.bias && slot < found ? __ldg(a.bias + my_idx) : 0.0f;
+        const float c = direct ? logit : s + bias;
+        const float after = __shfl_down_sync(ALL, c, 1), after_logit = __shfl_down_sync(ALL, logit, 1);
+        const float after_bias = __shfl_down_sync(ALL, bias, 1);
+        const int after_idx = __shfl_down_sync(ALL, my_idx, 1);
+        bool ok = sure && (next <= NO_WORD<IPL, FIXED> || apart<IPL, FIXED>(last, next, sm.open, direct));
+        if (slot + 1 < found)
+            ok = ok && (c - after > sm.open + (direct ? 0.0f : fabsf(c) * 0x1p-22f) ||
+                        (logit == after_logit && bias == after_bias && my_idx < after_idx));
+        uint32_t open = __ballot_sync(ALL, !ok);
+        if (open) {
+            do {
+                const int q = (__ffs(static_cast<int>(open)) - 1) / SEG;
+                int idx;
+                const int n = choose_again<T, IPL, FIXED>(a, row(q), seen, lane, idx);
+                idx = __shfl_sync(ALL, idx, slot);
+                if (seg == q) {
+                    found = n;
+                    my_idx = slot < n ? idx : -1;
+                }
+                open &= ~((SEG == 32 ? ALL : (1u << (SEG & 31)) - 1u) << (q * SEG));
+            } while (open);
+            look();
+        }
+    }
+    const bool chosen = slot < found;
+    float p = chosen ? s : 0.0f, total = 1.0f;
+    if (a.renorm) {
+        // all scores may be tiny, their quotients are not: s = exp(l - m) / (1 + exp(l)) * exp(m) with m the largest
+        const float m = seg_max<SEG>(chosen ? logit : -INFINITY);
+        if (chosen && a.softmax)
+            p = expf(logit - m);
+        else if (chosen && m < 0.0f)
+            p = expf(logit - m) / (1.0f + e);
+        total = seg_sum<SEG>(p);
+    }
+    if (slot < a.k && t < a.T) {
+        const size_t at = static_cast<size_t>(t) * a.k + slot;
+        a.idx[at] = my_idx;
+        a.w[at] = chosen ? p / total * a.scale : 0.0f;
+    }
+}
+
+template <typename T, int IPL, int Q>
 __global__ void __launch_bounds__(WARPS * 32) score_kernel(const ScoreArgs a)
 {
     __shared__ uint64_t seen[WARPS][SPOTS<IPL>];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x * WARPS + warp;
-    if (t >= a.T)
+    const int t0 = (blockIdx.x * WARPS + warp) * Q;
+    if (t0 >= a.T)
         return;
-    int my_idx = -1;
-    float my_w = 0.0f;
-    if (!a.mask || a.mask[t]) {
-        const T *l = static_cast<const T *>(a.logits) + static_cast<size_t>(t) * a.ld;
-        float f[IPL], b[IPL], top = 0.0f, total = 1.0f;
-        load_lane<T, IPL>(f, l, lane, a.E, a.vec);
-        if (a.bias)
-            load_lane<float, IPL>(b, a.bias, lane, a.E, a.bias_vec);
-        // without a bias scores are in the order of the logits, which are exact
-        const bool direct = !a.bias && (a.groups == 1 || !a.pair);
-        if (a.softmax && !(direct && a.renorm)) {
-            top = f[0];
+    float b[IPL];
+    bool fixed = false;
+    if (a.bias) {
+        load_lane<float, IPL>(b, a.bias, lane, a.E, a.bias_vec);
+        bool small = true;
 #pragma unroll
-            for (int i = 1; i < IPL; ++i)
-                top = fmaxf(top, f[i]);
-            top = warp_max_f(top);
-            total = 0.0f;
-#pragma unroll
-            for (int i = 0; i < IPL; ++i)
-                if (lane * IPL + i < a.E)
-                    total += expf(f[i] - top);
-            total = warp_sum(total);
-        }
-        uint32_t word[IPL];
-        // Two values of c that are this near (and 2^-22 of their size) are open.  Errors in units of 2^-24: the sigmoid's
-        // exponential (1.3 |l| + 2.8) times s (1 - s), at most 1, its sum 1/2, the reciprocal 2; softmax (times 1/total, the
-        // largest probability) 8 of the two exponentials and quotients, ln E of the exponents' roundings and 1/2
-        // for each of the sum's IPL + 5 additions.  Twice that for two values.
-        float open = 0.0f;
-        if (direct) {
-#pragma unroll
-            for (int i = 0; i < IPL; ++i)
-                word[i] = plain_key(f[i] + 0.0f);   // (-0 as +0)
-        } else {
-            open = a.softmax ? (2.0f * IPL + 72.0f) * 0x1p-24f / total : 0x1p-21f;
-            const float inv = 1.0f / total;
-#pragma unroll
-            for (int i = 0; i < IPL; ++i) {
-                const float s = a.softmax ? expf(f[i] - top) * inv : logistic(f[i]);
-                // (the sum is of no account but for a logit of -inf)
-                word[i] = plain_key(fminf(a.bias ? s + b[i] : s, f[i] + 3e38f));
-            }
-        }
-        bool sure = true;
-        if (a.groups > 1) {
-            uint32_t least, most;
-            keep_groups<IPL>(a, word, reinterpret_cast<uint32_t *>(seen[warp]), lane, least, most);
-            if (!direct && most != 0u) {
-                const float v = plain_value(least);
-                sure = v - plain_value(most) > 2.0f * open + fabsf(v) * 0x1p-21f;
-            }
-        }
-        int found;
-        float logit, e, s = 0.0f;   // of the lane's candidate: its logit, exp(-|logit|), its score
-        const auto look = [&](int idx, bool is) {
-            logit = is ? to_f<T>(l[idx]) : 0.0f;
-            e = expf(-fabsf(logit));
-            if (!a.softmax)
-                s = __fdividef(logit >= 0.0f ? 1.0f : e, 1.0f + e);
-            else if (!direct)
-                s = expf(logit - top) / total;
-        };
-        if (sure) {
-#pragma unroll
-            for (int i = 0; i < IPL; ++i)
-                word[i] = word_of<IPL>(word[i], lane, i);
-            sort_lane<IPL>(word);
-            // lanes 0 .. n - 1 get the k largest words and the one after them
-            uint32_t mine = 0u;
-            const int most = min(direct && sizeof(T) == 2 ? a.k : a.k + 1, 32);
-            int n = 0;
-            bool left = true;   // there are others
-            for (; n < most; ++n) {
-                const uint32_t m = take_largest<IPL>(word);
-                if (m <= NEVER<uint32_t>) {
-                    left = false;   // only what is never chosen
-                    break;
-                }
-                mine = lane == n ? m : mine;
-            }
-            my_idx = lane < n ? expert_of<IPL>(mine) : -1;
-            look(my_idx, lane < n);
-            found = min(n, a.k);
-            if (!direct || sizeof(T) == 4) {
-                const bool more = n > a.k || left;   // (with k = 32 the one after them is not in a lane)
-                float bias = a.bias && lane < n ? __ldg(a.bias + my_idx) : 0.0f;
-                // what the words leave out is below the k-th, and every slot above the one after it, or equal to it in
-                // what it is computed from
-                const float c = direct ? logit : s + bias;
-                const float after = __shfl_down_sync(ALL, c, 1);
-                const float near = direct ? 0.0f : 0x1p-22f;
-                bool ok = lane + 1 >= n || c - after > open + fabsf(c) * near;
-                if (!__all_sync(ALL, ok)) {
-                    const float after_logit = __shfl_down_sync(ALL, logit, 1), after_bias = __shfl_down_sync(ALL, bias, 1);
-                    const int after_idx = __shfl_down_sync(ALL, my_idx, 1);
-                    ok = __all_sync(ALL, ok || (logit == after_logit && bias == after_bias && my_idx < after_idx));
-                }
-                const uint32_t last = __shfl_sync(ALL, mine, a.k - 1);
-                const auto apart = [&](uint32_t word_after) {
-                    const float v = least_of<IPL>(last);
-                    return v - most_of<IPL>(word_after) > open + fabsf(v) * near;
-                };
-                bool whole = !more || (n > a.k && apart(__shfl_sync(ALL, mine, a.k & 31)));
-                if (!whole || !ok) {
-                    while (!whole && n < 32) {
-                        const uint32_t m = take_largest<IPL>(word);
-                        whole = m <= NEVER<uint32_t>;
-                        if (!whole) {
-                            mine = lane == n ? m : mine;
-                            ++n;
-                            whole = apart(m);
-                        }
-                    }
-                    if (!whole || (a.softmax && !direct)) {
-                        found = choose_exactly<T, IPL>(a, l, seen[warp], lane, my_idx);
-                    } else {
-                        my_idx = lane < n ? expert_of<IPL>(mine) : -1;
-                        logit = lane < n ? to_f<T>(l[my_idx]) : 0.0f;
-                        bias = a.bias && lane < n ? __ldg(a.bias + my_idx) : 0.0f;
-                        my_idx = direct ? rank_exactly<true>(logit, 0.0f, false, my_idx, n, lane)
-                                        : rank_exactly<false>(logit, bias, a.bias, my_idx, n, lane);
-                    }
-                    look(my_idx, lane < found);
-                }
-            }
-            my_idx = lane < found ? my_idx : -1;
-        } else {
-            found = choose_exactly<T, IPL>(a, l, seen[warp], lane, my_idx);
-            look(my_idx, lane < found);
-        }
-        const bool chosen = lane < found;
-        float p = 0.0f;
-        if (a.softmax) {
-            if (a.renorm)
-                top = warp_max_f(chosen ? logit : -INFINITY);
-            p = chosen ? expf(logit - top) : 0.0f;
-            if (a.renorm)
-                total = warp_sum(p);
-        } else {
-            p = chosen ? s : 0.0f;
-            // all scores may be tiny, their quotients are not: s = exp(l - m) / (1 + exp(l)) * exp(m) with m the largest
-            if (a.renorm && !__any_sync(ALL, chosen && logit >= 0.0f)) {
-                const float m = warp_max_f(chosen ? logit : -INFINITY);
-                p = chosen ? expf(logit - m) / (1.0f + e) : 0.0f;
-            }
-            total = a.renorm ? warp_sum(p) : 1.0f;
-        }
-        if (chosen)
-            my_w = p / total * a.scale;
+        for (int i = 0; i < IPL; ++i)
+            small = small && (fabsf(b[i]) <= 0.999f || b[i] == -INFINITY);
+        fixed = IPL <= 8 && !a.softmax && __all_sync(ALL, small);
     }
-    if (lane < a.k) {
-        a.idx[static_cast<size_t>(t) * a.k + lane] = my_idx;
-        a.w[static_cast<size_t>(t) * a.k + lane] = my_w;
+    if constexpr (IPL <= 8) {
+        if (fixed)
+            return score_tokens<T, IPL, Q, true>(a, b, seen[warp], t0, lane);
     }
+    score_tokens<T, IPL, Q, false>(a, b, seen[warp], t0, lane);
 }
 
 // ------------------------------------------------------------------ gradient ------------
@@ -577,11 +699,22 @@ __global__ void __launch_bounds__(WARPS * 32) score_backward_kernel(const ScoreB
 }
 
 // ------------------------------------------------------------------ host side ------------
+template <typename T, int IPL, int Q>
+void launch_scores(const ScoreArgs &a, cudaStream_t s)
+{
+    score_kernel<T, IPL, Q><<<(a.T + WARPS * Q - 1) / (WARPS * Q), WARPS * 32, 0, s>>>(a);
+}
+// Four tokens a warp where that leaves every SM several warps.
+constexpr int MANY_TOKENS = 4096;
 template <typename T, int IPL>
 struct ScoreLaunch {
     static void go(const ScoreArgs &a, cudaStream_t s)
     {
-        score_kernel<T, IPL><<<(a.T + WARPS - 1) / WARPS, WARPS * 32, 0, s>>>(a);
+        if constexpr (IPL <= 8) {
+            if (a.k <= 8 && a.T >= MANY_TOKENS)
+                return launch_scores<T, IPL, 4>(a, s);
+        }
+        launch_scores<T, IPL, 1>(a, s);
     }
 };
 template <typename T, int IPL>
