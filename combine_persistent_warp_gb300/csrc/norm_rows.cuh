@@ -376,7 +376,7 @@ template <typename TW>
 __global__ void norm_reduce_kernel(const PartRows p, int H, TW *dweight, TW *dbias)
 {
     __shared__ float tile[32][33];
-    ptx::grid_dependency_wait();
+    ptx::follow();
     const float *src = p.part + static_cast<size_t>(blockIdx.y) * p.blocks * p.pitch;
     TW *dst = blockIdx.y == 0 ? dweight : dbias;
     if (!dst)
@@ -384,7 +384,7 @@ __global__ void norm_reduce_kernel(const PartRows p, int H, TW *dweight, TW *dbi
     const int col = blockIdx.x * 32 + threadIdx.x;
     float s = 0.0f;
     if (col < H) {
-#pragma unroll 4
+#pragma unroll 16
         for (int b = threadIdx.y; b < p.blocks; b += 32)
             s += src[static_cast<size_t>(b) * p.pitch + col + ((b * p.step) & (p.boundary - 1))];
     }

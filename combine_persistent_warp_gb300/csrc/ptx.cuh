@@ -102,6 +102,14 @@ __device__ __forceinline__ void launch_dependents()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// The start of a kernel launched ahead of the one before it, in all of its threads: the next such kernel may
+// be launched, and nothing is read or written before the one before is done.
+__device__ __forceinline__ void follow()
+{
+    launch_dependents();
+    grid_dependency_wait();
+}
+
 // Order this thread's generic-proxy global accesses with its async-proxy (TMA) ones.
 __device__ __forceinline__ void fence_proxy_async_global()
 {

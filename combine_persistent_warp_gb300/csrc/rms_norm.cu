@@ -75,6 +75,7 @@ __device__ __forceinline__ void rms_row(const RmsArgs &a, int row, int lead, flo
 template <typename T, int V, int VPT, bool FP8, bool WARP, bool RES>
 __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : V * VPT == 32 ? 512 : 1024) rms_kernel(const RmsArgs a)
 {
+    ptx::follow();
     constexpr int P = PAIRS<V, VPT>;
     __shared__ __align__(16) float red[WARP ? 4 : 64];
     const int packs = a.H / V, t = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : V * VPT == 32 ? 512 : 
 template <typename T, int VPT, bool FP8, int AHEAD, bool LEAD, bool RES>
 __global__ void __launch_bounds__(512) rms_ring_kernel(const RmsArgs a)
 {
+    ptx::follow();
     constexpr int V = 8, P = PAIRS<V, VPT>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[64];
@@ -200,6 +202,7 @@ __device__ __forceinline__ void add_all(float2 (&d)[P], const float2 (&v)[P])
 template <typename T, int V, int VPT, int AHEAD, bool LEAD, bool DH>
 __global__ void __launch_bounds__(512) rms_backward_kernel(const RmsBwdArgs a)
 {
+    ptx::follow();
     constexpr int P = PAIRS<V, VPT>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[64];
@@ -277,7 +280,6 @@ __global__ void __launch_bounds__(512) rms_backward_kernel(const RmsBwdArgs a)
     }
     if (a.part)
         put<float, V, VPT>(a.part + static_cast<size_t>(blockIdx.x) * a.pitch, dg, t, step, packs);
-    ptx::launch_dependents();
 }
 
 // Rows of at most 1024 elements: one row a warp at a time, the next one on its way; the block's warps add
@@ -285,6 +287,7 @@ __global__ void __launch_bounds__(512) rms_backward_kernel(const RmsBwdArgs a)
 template <typename T, int V, int VPT, bool DH>
 __global__ void __launch_bounds__(ROW_WARPS * 32) rms_backward_warp_kernel(const RmsBwdArgs a)
 {
+    ptx::follow();
     constexpr int P = PAIRS<V, VPT>;
     struct alignas(16) Sums {
         float v[32 * V * VPT];
@@ -343,7 +346,6 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) rms_backward_warp_kernel(const
             a.part[static_cast<size_t>(blockIdx.x) * a.pitch + c] = v;
         }
     }
-    ptx::launch_dependents();
 }
 
 // ------------------------------------------------------------------ host side ------------
@@ -366,14 +368,14 @@ bool try_rms_ring(const RmsArgs &a, int packs, int num_sms, cudaStream_t s)
     const auto kern = rms_ring_kernel<T, 4, FP8, AHEAD, LEAD, RES>;
     if (!allow_smem(kern, smem))
         return false;
-    kern<<<ring_grid(per_sm, num_sms), threads, smem, s>>>(a);
+    launch_programmatic(kern, ring_grid(per_sm, num_sms), threads, smem, s, a);
     return true;
 }
 
 template <typename T, int V, int VPT, bool FP8, bool RES>
 void launch_rms_warps(const RmsArgs &a, int num_sms, cudaStream_t s)
 {
-    rms_kernel<T, V, VPT, FP8, true, RES><<<warp_blocks(a.T, 8, num_sms), ROW_WARPS * 32, 0, s>>>(a);
+    launch_programmatic(rms_kernel<T, V, VPT, FP8, true, RES>, warp_blocks(a.T, 8, num_sms), ROW_WARPS * 32, 0, s, a);
 }
 
 template <typename T, bool FP8, bool RES>
@@ -389,9 +391,9 @@ void launch_rms(const RmsArgs &a, Rows rows, int num_sms, cudaStream_t s)
         else if (packs <= 128 && !few)
             launch_rms_warps<T, 8, 4, FP8, RES>(a, num_sms, s);
         else if (few && packs <= 1024)
-            rms_kernel<T, 8, 1, FP8, false, RES><<<a.T, round32(packs), 0, s>>>(a);
+            launch_programmatic(rms_kernel<T, 8, 1, FP8, false, RES>, a.T, round32(packs), 0, s, a);
         else if (!try_rms_ring<T, FP8, AHEAD, false, RES>(a, packs, num_sms, s))
-            rms_kernel<T, 8, 4, FP8, false, RES><<<a.T, round32((packs + 3) / 4), 0, s>>>(a);
+            launch_programmatic(rms_kernel<T, 8, 4, FP8, false, RES>, a.T, round32((packs + 3) / 4), 0, s, a);
         return;
     }
     if constexpr (!FP8) {
@@ -402,7 +404,7 @@ void launch_rms(const RmsArgs &a, Rows rows, int num_sms, cudaStream_t s)
         else if (a.H <= 1024)
             launch_rms_warps<T, 1, 32, false, RES>(a, num_sms, s);
         else
-            rms_kernel<T, 1, 32, false, false, RES><<<a.T, round32((a.H + 31) / 32), 0, s>>>(a);
+            launch_programmatic(rms_kernel<T, 1, 32, false, false, RES>, a.T, round32((a.H + 31) / 32), 0, s, a);
     }
 }
 
@@ -451,7 +453,7 @@ bool launch_backward_ring(const RmsBwdArgs &a, int packs, int blocks, cudaStream
     const auto kern = rms_backward_kernel<T, 8, VPT, AHEAD, LEAD, DH>;
     if (!allow_smem(kern, smem))
         return false;
-    kern<<<blocks, threads, smem, s>>>(a);
+    launch_programmatic(kern, blocks, threads, smem, s, a);
     return true;
 }
 
@@ -472,21 +474,21 @@ bool launch_rms_backward(const RmsBwdArgs &a, Rows rows, int num_sms, PartRows &
                : packs <= 1024 ? launch_backward_ring<T, 2, 2, false, DH>(a, packs, blocks, s)
                                : launch_backward_ring<T, 4, 2, false, DH>(a, packs, blocks, s);
     if (plan == WARPS_1 && packed)
-        rms_backward_warp_kernel<T, 8, 1, DH><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
+        launch_programmatic(rms_backward_warp_kernel<T, 8, 1, DH>, blocks, ROW_WARPS * 32, 0, s, a);
     else if (plan == WARPS_4 && packed)
-        rms_backward_warp_kernel<T, 8, 4, DH><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
+        launch_programmatic(rms_backward_warp_kernel<T, 8, 4, DH>, blocks, ROW_WARPS * 32, 0, s, a);
     else if (plan == DIRECT && packed && packs <= 1024)
-        rms_backward_kernel<T, 8, 2, 0, false, DH><<<blocks, round32((packs + 1) / 2), 0, s>>>(a);
+        launch_programmatic(rms_backward_kernel<T, 8, 2, 0, false, DH>, blocks, round32((packs + 1) / 2), 0, s, a);
     else if (plan == DIRECT && packed)
-        rms_backward_kernel<T, 8, 4, 0, false, DH><<<blocks, round32((packs + 3) / 4), 0, s>>>(a);
+        launch_programmatic(rms_backward_kernel<T, 8, 4, 0, false, DH>, blocks, round32((packs + 3) / 4), 0, s, a);
     else if (plan == WARPS_1)
-        rms_backward_warp_kernel<T, 1, 8, DH><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
+        launch_programmatic(rms_backward_warp_kernel<T, 1, 8, DH>, blocks, ROW_WARPS * 32, 0, s, a);
     else if (plan == WARPS_4)
-        rms_backward_warp_kernel<T, 1, 32, DH><<<blocks, ROW_WARPS * 32, 0, s>>>(a);
+        launch_programmatic(rms_backward_warp_kernel<T, 1, 32, DH>, blocks, ROW_WARPS * 32, 0, s, a);
     else if (a.H <= 8192)
-        rms_backward_kernel<T, 1, 16, 0, false, DH><<<blocks, round32((a.H + 15) / 16), 0, s>>>(a);
+        launch_programmatic(rms_backward_kernel<T, 1, 16, 0, false, DH>, blocks, round32((a.H + 15) / 16), 0, s, a);
     else
-        rms_backward_kernel<T, 1, 32, 0, false, DH><<<blocks, round32((a.H + 31) / 32), 0, s>>>(a);
+        launch_programmatic(rms_backward_kernel<T, 1, 32, 0, false, DH>, blocks, round32((a.H + 31) / 32), 0, s, a);
     return true;
 }
 

@@ -14,6 +14,8 @@
 // its error, and the candidates that this bound leaves open are ranked again in 64.
 #include <climits>
 
+#include "moe_internal.cuh"
+#include "ptx.cuh"
 #include "router_common.cuh"
 
 using namespace cpw;
@@ -595,6 +597,7 @@ __device__ __forceinline__ void score_tokens(const ScoreArgs &a, const float (&b
 template <typename T, int IPL, int Q>
 __global__ void __launch_bounds__(WARPS * 32) score_kernel(const ScoreArgs a)
 {
+    ptx::follow();
     __shared__ uint64_t seen[WARPS][SPOTS<IPL>];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = (blockIdx.x * WARPS + warp) * Q;
@@ -633,6 +636,7 @@ struct ScoreBwdArgs {
 template <typename T, int IPL>
 __global__ void __launch_bounds__(WARPS * 32) score_backward_kernel(const ScoreBwdArgs a)
 {
+    ptx::follow();
     const int t = blockIdx.x * WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (t >= a.T)
         return;
@@ -702,7 +706,7 @@ __global__ void __launch_bounds__(WARPS * 32) score_backward_kernel(const ScoreB
 template <typename T, int IPL, int Q>
 void launch_scores(const ScoreArgs &a, cudaStream_t s)
 {
-    score_kernel<T, IPL, Q><<<(a.T + WARPS * Q - 1) / (WARPS * Q), WARPS * 32, 0, s>>>(a);
+    launch_programmatic(score_kernel<T, IPL, Q>, (a.T + WARPS * Q - 1) / (WARPS * Q), WARPS * 32, 0, s, a);
 }
 // Four tokens a warp where that leaves every SM several warps.
 constexpr int MANY_TOKENS = 4096;
@@ -721,7 +725,7 @@ template <typename T, int IPL>
 struct ScoreBwdLaunch {
     static void go(const ScoreBwdArgs &a, cudaStream_t s)
     {
-        score_backward_kernel<T, IPL><<<(a.T + WARPS - 1) / WARPS, WARPS * 32, 0, s>>>(a);
+        launch_programmatic(score_backward_kernel<T, IPL>, (a.T + WARPS - 1) / WARPS, WARPS * 32, 0, s, a);
     }
 };
 

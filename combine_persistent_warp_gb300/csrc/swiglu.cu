@@ -13,7 +13,9 @@
 #include <initializer_list>
 #include <type_traits>
 
+#include "moe_internal.cuh"
 #include "op_common.cuh"
+#include "ptx.cuh"
 
 using namespace cpw;
 
@@ -308,6 +310,7 @@ struct ActArgs {
 template <typename T, int E, bool KEEP>
 __global__ void __launch_bounds__(THREADS) swiglu_pack_kernel(const ActArgs a)
 {
+    ptx::follow();
     constexpr int LANES = GROUP / E;
     int p;
     const long long row = row_of(a.u, threadIdx.x, THREADS, p);
@@ -350,6 +353,7 @@ __global__ void __launch_bounds__(THREADS) swiglu_pack_kernel(const ActArgs a)
 template <typename T, int E, bool KEPT>
 __global__ void __launch_bounds__(THREADS) swiglu_backward_pack_kernel(const ActArgs a)
 {
+    ptx::follow();
     constexpr int LANES = GROUP / E;
     int p;
     const long long row = row_of(a.u, threadIdx.x, THREADS, p);
@@ -398,6 +402,7 @@ struct KeepArgs {
 template <typename T, int E>
 __global__ void __launch_bounds__(THREADS) checkpoint_pack_kernel(const KeepArgs a)
 {
+    ptx::follow();
     constexpr int LANES = GROUP / E;
     int p;
     const long long row = row_of(a.u, threadIdx.x, THREADS, p);
@@ -420,6 +425,7 @@ __global__ void __launch_bounds__(THREADS) checkpoint_pack_kernel(const KeepArgs
 template <typename T, int E>
 __global__ void __launch_bounds__(THREADS) restore_pack_kernel(const KeepArgs a)
 {
+    ptx::follow();
     constexpr int LANES = GROUP / E;
     int p;
     const long long row = row_of(a.u, threadIdx.x, THREADS, p);
@@ -531,6 +537,7 @@ __device__ __forceinline__ void swiglu_chunk(const ActArgs &a, const Chunk &k)
 template <typename T, bool KEEP>
 __global__ void __launch_bounds__(THREADS) swiglu_kernel(const ActArgs a)
 {
+    ptx::follow();
     const Chunk k = chunk_of(a.u);
     if (!k.in)
         return;
@@ -572,6 +579,7 @@ __device__ __forceinline__ void swiglu_backward_chunk(const ActArgs &a, const Ch
 template <typename T, bool KEPT>
 __global__ void __launch_bounds__(THREADS) swiglu_backward_kernel(const ActArgs a)
 {
+    ptx::follow();
     const Chunk k = chunk_of(a.u);
     if (!k.in)
         return;
@@ -584,6 +592,7 @@ __global__ void __launch_bounds__(THREADS) swiglu_backward_kernel(const ActArgs 
 template <typename T>
 __global__ void __launch_bounds__(THREADS) checkpoint_kernel(const KeepArgs a)
 {
+    ptx::follow();
     const Chunk k = chunk_of(a.u);
     if (!k.in)
         return;
@@ -601,6 +610,7 @@ __global__ void __launch_bounds__(THREADS) checkpoint_kernel(const KeepArgs a)
 template <typename T>
 __global__ void __launch_bounds__(THREADS) restore_kernel(const KeepArgs a)
 {
+    ptx::follow();
     const Chunk k = chunk_of(a.u);
     if (!k.in)
         return;
@@ -695,14 +705,14 @@ int moe_swiglu(int64_t M, int I, const void *gu, int64_t ldg, int dtype, void *a
     a.scales = scales;
     a.act = act;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid(static_cast<unsigned>(blocks));
+    const int grid = static_cast<int>(blocks);
     with_elements(dtype, e, [&](auto *t, auto elements) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int E = decltype(elements)::value;
         if constexpr (E > 0)
-            codes ? swiglu_pack_kernel<T, E, true><<<grid, THREADS, 0, s>>>(a) : swiglu_pack_kernel<T, E, false><<<grid, THREADS, 0, s>>>(a);
+            codes ? launch_programmatic(swiglu_pack_kernel<T, E, true>, grid, THREADS, 0, s, a) : launch_programmatic(swiglu_pack_kernel<T, E, false>, grid, THREADS, 0, s, a);
         else
-            codes ? swiglu_kernel<T, true><<<grid, THREADS, 0, s>>>(a) : swiglu_kernel<T, false><<<grid, THREADS, 0, s>>>(a);
+            codes ? launch_programmatic(swiglu_kernel<T, true>, grid, THREADS, 0, s, a) : launch_programmatic(swiglu_kernel<T, false>, grid, THREADS, 0, s, a);
     });
     return launched();
 }
@@ -735,15 +745,15 @@ int moe_swiglu_backward(int64_t M, int I, const void *dact, int64_t ldd, const v
     a.act = act;
     a.dgu = dgu;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid(static_cast<unsigned>(blocks));
+    const int grid = static_cast<int>(blocks);
     with_elements(dtype, e, [&](auto *t, auto elements) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int E = decltype(elements)::value;
         if constexpr (E > 0)
-            codes ? swiglu_backward_pack_kernel<T, E, true><<<grid, THREADS, 0, s>>>(a)
-                  : swiglu_backward_pack_kernel<T, E, false><<<grid, THREADS, 0, s>>>(a);
+            codes ? launch_programmatic(swiglu_backward_pack_kernel<T, E, true>, grid, THREADS, 0, s, a)
+                  : launch_programmatic(swiglu_backward_pack_kernel<T, E, false>, grid, THREADS, 0, s, a);
         else
-            codes ? swiglu_backward_kernel<T, true><<<grid, THREADS, 0, s>>>(a) : swiglu_backward_kernel<T, false><<<grid, THREADS, 0, s>>>(a);
+            codes ? launch_programmatic(swiglu_backward_kernel<T, true>, grid, THREADS, 0, s, a) : launch_programmatic(swiglu_backward_kernel<T, false>, grid, THREADS, 0, s, a);
     });
     return launched();
 }
@@ -764,14 +774,14 @@ int moe_checkpoint_rows(int64_t M, int H, const void *x, int64_t ldx, int dtype,
     OP_DEVICE(sms);
     const KeepArgs a{u, H, groups_of(H), x, ldx, codes, scales, nullptr};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid(static_cast<unsigned>(blocks));
+    const int grid = static_cast<int>(blocks);
     with_elements(dtype, e, [&](auto *t, auto elements) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int E = decltype(elements)::value;
         if constexpr (E > 0)
-            checkpoint_pack_kernel<T, E><<<grid, THREADS, 0, s>>>(a);
+            launch_programmatic(checkpoint_pack_kernel<T, E>, grid, THREADS, 0, s, a);
         else
-            checkpoint_kernel<T><<<grid, THREADS, 0, s>>>(a);
+            launch_programmatic(checkpoint_kernel<T>, grid, THREADS, 0, s, a);
     });
     return launched();
 }
@@ -792,14 +802,14 @@ int moe_restore_rows(int64_t M, int H, const int8_t *codes, const uint8_t *scale
     OP_DEVICE(sms);
     const KeepArgs a{u, H, groups_of(H), nullptr, 0, const_cast<int8_t *>(codes), const_cast<uint8_t *>(scales), x};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid(static_cast<unsigned>(blocks));
+    const int grid = static_cast<int>(blocks);
     with_elements(dtype, e, [&](auto *t, auto elements) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int E = decltype(elements)::value;
         if constexpr (E > 0)
-            restore_pack_kernel<T, E><<<grid, THREADS, 0, s>>>(a);
+            launch_programmatic(restore_pack_kernel<T, E>, grid, THREADS, 0, s, a);
         else
-            restore_kernel<T><<<grid, THREADS, 0, s>>>(a);
+            launch_programmatic(restore_kernel<T>, grid, THREADS, 0, s, a);
     });
     return launched();
 }
