@@ -40,19 +40,20 @@ __device__ __forceinline__ int packs_of(int H, int lead)
     return LEAD ? (lead + H + V - 1) / V : H / V;
 }
 
-// Packs past the row's end are zeros.
-template <typename T, int V, int VPT>
-__device__ __forceinline__ void fetch(Pack<T, V> (&q)[VPT], const T *row, int t, int step, int packs)
+// What is past the row's ends is zeros.
+template <typename T, int V, int VPT, bool LEAD = false>
+__device__ __forceinline__ void fetch(Pack<T, V> (&q)[VPT], const T *row, int t, int step, int packs, int lead = 0, int H = 0)
 {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int p = t + j * step;
-        if (p < packs) {
-            q[j] = load_pack<T, V>(row + static_cast<size_t>(p) * V);
+        const long long e = static_cast<long long>(p) * V - lead;
+        if (p < packs && (!LEAD || (e >= 0 && e + V <= H))) {
+            q[j] = load_pack<T, V>(row + e);
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                q[j].v[i] = from_f<T>(0.0f);
+                q[j].v[i] = LEAD && p < packs && e + i >= 0 && e + i < H ? __ldg(row + e + i) : from_f<T>(0.0f);
         }
     }
 }
@@ -384,9 +385,18 @@ __global__ void norm_reduce_kernel(const PartRows p, int H, TW *dweight, TW *dbi
     const int col = blockIdx.x * 32 + threadIdx.x;
     float s = 0.0f;
     if (col < H) {
-#pragma unroll 16
-        for (int b = threadIdx.y; b < p.blocks; b += 32)
-            s += src[static_cast<size_t>(b) * p.pitch + col + ((b * p.step) & (p.boundary - 1))];
+        // eight loads at a time, whether there are as many rows or not
+        for (int b0 = threadIdx.y; b0 < p.blocks; b0 += 8 * 32) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int b = b0 + 32 * i;
+                v[i] = b < p.blocks ? src[static_cast<size_t>(b) * p.pitch + col + ((b * p.step) & (p.boundary - 1))] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s = b0 + 32 * i < p.blocks ? s + v[i] : s;
+        }
     }
     tile[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
@@ -404,7 +414,7 @@ cudaError_t launch_reduce(const PartRows &p, int H, TW *dweight, TW *dbias, cuda
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((H + 31) / 32, 2);
+    cfg.gridDim = dim3((H + 31) / 32, dbias ? 2 : 1);
     cfg.blockDim = dim3(32, 32);
     cfg.stream = s;
     cfg.attrs = attr;

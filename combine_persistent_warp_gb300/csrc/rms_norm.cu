@@ -72,40 +72,41 @@ __device__ __forceinline__ void rms_row(const RmsArgs &a, int row, int lead, flo
 
 // One row a block; or (WARP, rows of at most 1024 elements) one row a warp at a time, the next one on its
 // way.  The weight is loaded beside the first row, ahead of its sum.
-template <typename T, int V, int VPT, bool FP8, bool WARP, bool RES>
+template <typename T, int V, int VPT, bool FP8, bool WARP, bool LEAD, bool RES>
 __global__ void __launch_bounds__(WARP ? ROW_WARPS * 32 : V * VPT == 32 ? 512 : 1024) rms_kernel(const RmsArgs a)
 {
     ptx::follow();
     constexpr int P = PAIRS<V, VPT>;
     __shared__ __align__(16) float red[WARP ? 4 : 64];
-    const int packs = a.H / V, t = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
+    const int t = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
     if constexpr (!WARP)
         clear_sums<1>(red);
     const T *x = static_cast<const T *>(a.x), *r = static_cast<const T *>(a.r);
     int row = WARP ? blockIdx.x * ROW_WARPS + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= a.T)
         return;
+    const int lead = LEAD ? lead_of(x + static_cast<size_t>(row) * a.ldx) : 0, packs = packs_of<V, LEAD>(a.H, lead);
     Pack<T, V> q[VPT], qr[RES ? VPT : 1];
-    fetch<T, V, VPT>(q, x + static_cast<size_t>(row) * a.ldx, t, step, packs);
+    fetch<T, V, VPT, LEAD>(q, x + static_cast<size_t>(row) * a.ldx, t, step, packs, lead, a.H);
     if constexpr (RES)
-        fetch<T, V, VPT>(qr, r + static_cast<size_t>(row) * a.ldr, t, step, packs);
+        fetch<T, V, VPT, LEAD>(qr, r + static_cast<size_t>(row) * a.ldr, t, step, packs, lead, a.H);
     float2 f[P], w[P];
-    load_columns<T, V, VPT>(w, a.weight, a.w32, 1.0f, t, step, packs);
+    load_columns<T, V, VPT, LEAD>(w, a.weight, a.w32, 1.0f, t, step, packs, lead, a.H);
     for (;;) {
         unpack<T, V, VPT>(f, q);
         if constexpr (RES) {
             float2 g[P];
             unpack<T, V, VPT>(g, qr);
             add_residual<T>(f, g);
-            put<T, V, VPT>(static_cast<T *>(a.h) + static_cast<size_t>(row) * a.H, f, t, step, packs);
+            put<T, V, VPT, LEAD>(static_cast<T *>(a.h) + static_cast<size_t>(row) * a.H, f, t, step, packs, lead, a.H);
         }
         const int next = WARP ? row + gridDim.x * ROW_WARPS : a.T;
         if (WARP && next < a.T) {
-            fetch<T, V, VPT>(q, x + static_cast<size_t>(next) * a.ldx, t, step, packs);
+            fetch<T, V, VPT, LEAD>(q, x + static_cast<size_t>(next) * a.ldx, t, step, packs, lead, a.H);
             if constexpr (RES)
-                fetch<T, V, VPT>(qr, r + static_cast<size_t>(next) * a.ldr, t, step, packs);
+                fetch<T, V, VPT, LEAD>(qr, r + static_cast<size_t>(next) * a.ldr, t, step, packs, lead, a.H);
         }
-        rms_row<T, V, VPT, FP8, WARP, false>(a, row, 0, f, w, red, 0, [] {});
+        rms_row<T, V, VPT, FP8, WARP, LEAD>(a, row, lead, f, w, red, 0, [] {});
         if (next >= a.T)
             return;
         row = next;
@@ -202,7 +203,7 @@ __device__ __forceinline__ void add_all(float2 (&d)[P], const float2 (&v)[P])
 template <typename T, int V, int VPT, int AHEAD, bool LEAD, bool DH>
 __global__ void __launch_bounds__(512) rms_backward_kernel(const RmsBwdArgs a)
 {
-    ptx::follow();
+    ptx::grid_dependency_wait();
     constexpr int P = PAIRS<V, VPT>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[64];
@@ -245,12 +246,12 @@ __global__ void __launch_bounds__(512) rms_backward_kernel(const RmsBwdArgs a)
             clip<V, VPT>(xh, t, step, packs, LEAD && cut, lead, a.H);
             clip<V, VPT>(d, t, step, packs, LEAD && cut, lead, a.H);
         } else {
-            fetch<T, V, VPT>(q, static_cast<const T *>(a.h) + static_cast<size_t>(row) * a.ldh, t, step, packs);
+            fetch<T, V, VPT, LEAD>(q, static_cast<const T *>(a.h) + static_cast<size_t>(row) * a.ldh, t, step, packs, lead, a.H);
             unpack<T, V, VPT>(xh, q);
-            fetch<T, V, VPT>(q, static_cast<const T *>(a.dy) + static_cast<size_t>(row) * a.lddy, t, step, packs);
+            fetch<T, V, VPT, LEAD>(q, static_cast<const T *>(a.dy) + static_cast<size_t>(row) * a.lddy, t, step, packs, lead, a.H);
             unpack<T, V, VPT>(d, q);
             if constexpr (DH)
-                fetch<T, V, VPT>(q, static_cast<const T *>(a.dh) + static_cast<size_t>(row) * a.lddh, t, step, packs);
+                fetch<T, V, VPT, LEAD>(q, static_cast<const T *>(a.dh) + static_cast<size_t>(row) * a.lddh, t, step, packs, lead, a.H);
         }
         float s[1] = {backward_sum(xh, d, w, dg, rstd)};
         block_sum(s, red, slot);
@@ -280,6 +281,7 @@ __global__ void __launch_bounds__(512) rms_backward_kernel(const RmsBwdArgs a)
     }
     if (a.part)
         put<float, V, VPT>(a.part + static_cast<size_t>(blockIdx.x) * a.pitch, dg, t, step, packs);
+    ptx::launch_dependents();
 }
 
 // Rows of at most 1024 elements: one row a warp at a time, the next one on its way; the block's warps add
@@ -287,14 +289,15 @@ __global__ void __launch_bounds__(512) rms_backward_kernel(const RmsBwdArgs a)
 template <typename T, int V, int VPT, bool DH>
 __global__ void __launch_bounds__(ROW_WARPS * 32) rms_backward_warp_kernel(const RmsBwdArgs a)
 {
-    ptx::follow();
+    ptx::grid_dependency_wait();
     constexpr int P = PAIRS<V, VPT>;
     struct alignas(16) Sums {
         float v[32 * V * VPT];
     };
     static_assert(alignof(Sums) >= alignof(Pack<float, V>), "put() stores whole packs into them");
     __shared__ Sums sums[ROW_WARPS];
-    const int packs = a.H / V, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int packs = a.H / V;
     const float inv = 1.0f / static_cast<float>(a.H);
     const T *h = static_cast<const T *>(a.h), *dy = static_cast<const T *>(a.dy), *dh = static_cast<const T *>(a.dh);
     float2 w[P], dg[P];
@@ -346,14 +349,33 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) rms_backward_warp_kernel(const
             a.part[static_cast<size_t>(blockIdx.x) * a.pitch + c] = v;
         }
     }
+    ptx::launch_dependents();
 }
 
 // ------------------------------------------------------------------ host side ------------
-// Rows off the boundaries in packs with a lead: where the persistent kernels run.
+// Rows in packs, without a lead or with one; others go element by element.  Not rows of at most 1024 elements with
+// a lead, whose ends are much of what a warp does then (16384 x 1001 bf16, with the residual and its gradient, 53 and 74 us in
+// packs).
 template <typename T>
-bool phased(int H, Rows rows)
+bool in_packs(int H, Rows rows)
 {
-    return rows == PHASED && H > 1024 && most_packs<T>(H, rows) <= 1024;
+    return rows == PACKED || (rows == PHASED && H > 1024 && most_packs<T>(H, rows) <= 2048);
+}
+// A ring's blocks, `per_sm` to an SM.  Launched ahead of the kernel before they are placed as its blocks leave, and
+// where an SM has room for many more, they crowd on the SMs that are left first (16384 x 4096 bf16 backward, room for
+// three: 81 us, and 70 launched after it); else it saves the launch (6001 x 2003 fp16 forward and backward
+// 47 -> 44).
+template <typename A>
+bool launch_ring(void (*kern)(A), int blocks, int threads, size_t smem, int per_sm, cudaStream_t s, const A &a)
+{
+    if (!allow_smem(kern, smem))
+        return false;
+    const int room = static_cast<int>(228 * 1024 / (smem + 1024));
+    if (8 * room <= 9 * per_sm)
+        launch_programmatic(kern, blocks, threads, static_cast<int>(smem), s, a);
+    else
+        kern<<<blocks, threads, smem, s>>>(a);
+    return true;
 }
 
 template <typename T, bool FP8, int AHEAD, bool LEAD, bool RES>
@@ -365,71 +387,80 @@ bool try_rms_ring(const RmsArgs &a, int packs, int num_sms, cudaStream_t s)
     // long batches only: every block has rows to copy ahead of
     if (per_sm < 1 || a.T < AHEAD * per_sm * num_sms)
         return false;
-    const auto kern = rms_ring_kernel<T, 4, FP8, AHEAD, LEAD, RES>;
-    if (!allow_smem(kern, smem))
-        return false;
-    launch_programmatic(kern, ring_grid(per_sm, num_sms), threads, smem, s, a);
-    return true;
+    return launch_ring(rms_ring_kernel<T, 4, FP8, AHEAD, LEAD, RES>, ring_grid(per_sm, num_sms), threads, smem, per_sm, s, a);
 }
 
 template <typename T, int V, int VPT, bool FP8, bool RES>
 void launch_rms_warps(const RmsArgs &a, int num_sms, cudaStream_t s)
 {
-    launch_programmatic(rms_kernel<T, V, VPT, FP8, true, RES>, warp_blocks(a.T, 8, num_sms), ROW_WARPS * 32, 0, s, a);
+    launch_programmatic(rms_kernel<T, V, VPT, FP8, true, false, RES>, warp_blocks(a.T, 8, num_sms), ROW_WARPS * 32, 0, s, a);
+}
+
+template <typename T, bool FP8, bool LEAD, bool RES>
+void launch_rms_packs(const RmsArgs &a, int packs, int num_sms, cudaStream_t s)
+{
+    // few rows: as many threads a row as it has packs, for latency
+    const bool few = a.T <= 2 * num_sms;
+    if (packs <= 32 && !LEAD)
+        launch_rms_warps<T, 8, 1, FP8, RES>(a, num_sms, s);
+    else if (packs <= 128 && !few && !LEAD)
+        launch_rms_warps<T, 8, 4, FP8, RES>(a, num_sms, s);
+    else if (few && packs <= 1024)
+        launch_programmatic(rms_kernel<T, 8, 1, FP8, false, LEAD, RES>, a.T, round32(packs), 0, s, a);
+    else if (packs > 2048 || !try_rms_ring<T, FP8, RES ? 3 : 4, LEAD, RES>(a, packs, num_sms, s))
+        launch_programmatic(rms_kernel<T, 8, 4, FP8, false, LEAD, RES>, a.T, round32((packs + 3) / 4), 0, s, a);
 }
 
 template <typename T, bool FP8, bool RES>
 void launch_rms(const RmsArgs &a, Rows rows, int num_sms, cudaStream_t s)
 {
-    constexpr int AHEAD = RES ? 3 : 4;
-    const bool few = a.T <= 2 * num_sms;
-    if (rows == PACKED) {
-        // few rows: as many threads a row as it has packs, for latency
-        const int packs = a.H / 8;
-        if (packs <= 32)
-            launch_rms_warps<T, 8, 1, FP8, RES>(a, num_sms, s);
-        else if (packs <= 128 && !few)
-            launch_rms_warps<T, 8, 4, FP8, RES>(a, num_sms, s);
-        else if (few && packs <= 1024)
-            launch_programmatic(rms_kernel<T, 8, 1, FP8, false, RES>, a.T, round32(packs), 0, s, a);
-        else if (!try_rms_ring<T, FP8, AHEAD, false, RES>(a, packs, num_sms, s))
-            launch_programmatic(rms_kernel<T, 8, 4, FP8, false, RES>, a.T, round32((packs + 3) / 4), 0, s, a);
-        return;
-    }
+    const int packs = most_packs<T>(a.H, rows);
+    if (rows == PACKED)
+        return launch_rms_packs<T, FP8, false, RES>(a, packs, num_sms, s);
     if constexpr (!FP8) {
-        if (phased<T>(a.H, rows) && try_rms_ring<T, false, AHEAD, true, RES>(a, most_packs<T>(a.H, rows), num_sms, s))
-            return;
+        if (in_packs<T>(a.H, rows))
+            return launch_rms_packs<T, false, true, RES>(a, packs, num_sms, s);
         if (a.H <= 256)
             launch_rms_warps<T, 1, 8, false, RES>(a, num_sms, s);
-        else if (a.H <= 1024)
+        else if (a.H <= 576 && a.T > 2 * num_sms)
+            launch_rms_warps<T, 1, 18, false, RES>(a, num_sms, s);
+        else if (a.H <= 1024 && a.T > 2 * num_sms)
             launch_rms_warps<T, 1, 32, false, RES>(a, num_sms, s);
+        else if (a.H <= 8192)
+            launch_programmatic(rms_kernel<T, 1, 8, false, false, false, RES>, a.T, round32((a.H + 7) / 8), 0, s, a);
         else
-            launch_programmatic(rms_kernel<T, 1, 32, false, false, RES>, a.T, round32((a.H + 31) / 32), 0, s, a);
+            launch_programmatic(rms_kernel<T, 1, 16, false, false, false, RES>, a.T, round32((a.H + 15) / 16), 0, s, a);
     }
 }
 
 // The backward pass: kernel, blocks (each keeps a row of partial sums) and how they are found.
-enum Plan { WARPS_1, WARPS_4, RING, DIRECT };
+enum Plan { WARPS, RING, DIRECT, ELEMENT_WARPS, ELEMENTS };
 template <typename T>
 Plan backward_plan(int T_, int H, Rows rows, int num_sms, int &blocks)
 {
-    if (H <= 256 || (H <= 1024 && (rows != PACKED || T_ > 2 * num_sms))) {
-        blocks = warp_blocks(T_, 3, num_sms);
-        return H <= 256 ? WARPS_1 : WARPS_4;
-    }
-    if (rows == PACKED || phased<T>(H, rows)) {
+    const int packs = most_packs<T>(H, rows);
+    if (in_packs<T>(H, rows)) {
+        if (rows == PACKED && (packs <= 32 || (packs <= 128 && T_ > 2 * num_sms))) {
+            blocks = warp_blocks(T_, 3, num_sms);
+            return WARPS;
+        }
         size_t smem;
-        const int packs = most_packs<T>(H, rows);
         const int per_sm = packs <= 1024 ? ring_blocks<T, 8, 2>(round32((packs + 1) / 2), packs <= 512 ? 4 : 2, 3, smem)
                                          : ring_blocks<T, 8, 4>(round32((packs + 3) / 4), 2, 3, smem);
         if (per_sm >= 1 && T_ >= 4 * per_sm * num_sms) {
             blocks = ring_grid(per_sm, num_sms);
             return RING;
         }
+        const int most = ring_grid(2, num_sms);
+        blocks = T_ < most ? T_ : most;
+        return DIRECT;
     }
-    blocks = 2 * num_sms;
-    blocks = T_ < blocks ? T_ : blocks;
-    return DIRECT;
+    if (H <= 256 || (H <= 1024 && T_ > 2 * num_sms)) {
+        blocks = warp_blocks(T_, 3, num_sms);
+        return ELEMENT_WARPS;
+    }
+    blocks = T_ < 2 * num_sms ? T_ : 2 * num_sms;
+    return ELEMENTS;
 }
 // (the workspace covers every alignment)
 template <typename T>
@@ -445,16 +476,32 @@ int most_backward_blocks(int T_, int H, int num_sms)
 }
 
 template <typename T, int VPT, int AHEAD, bool LEAD, bool DH>
-bool launch_backward_ring(const RmsBwdArgs &a, int packs, int blocks, cudaStream_t s)
+bool launch_backward_ring(const RmsBwdArgs &a, int packs, int blocks, int num_sms, cudaStream_t s)
 {
     const int threads = round32((packs + VPT - 1) / VPT);
     size_t smem;
     ring_blocks<T, 8, VPT>(threads, AHEAD, DH ? 3 : 2, smem);
-    const auto kern = rms_backward_kernel<T, 8, VPT, AHEAD, LEAD, DH>;
-    if (!allow_smem(kern, smem))
-        return false;
-    launch_programmatic(kern, blocks, threads, smem, s, a);
+    return launch_ring(rms_backward_kernel<T, 8, VPT, AHEAD, LEAD, DH>, blocks, threads, smem, (blocks + num_sms - 1) / num_sms, s, a);
+}
+
+template <typename T, bool LEAD, bool DH>
+bool launch_backward_packs(const RmsBwdArgs &a, Plan plan, int packs, int blocks, int num_sms, cudaStream_t s)
+{
+    if (plan == RING)
+        return packs <= 512    ? launch_backward_ring<T, 2, 4, LEAD, DH>(a, packs, blocks, num_sms, s)
+               : packs <= 1024 ? launch_backward_ring<T, 2, 2, LEAD, DH>(a, packs, blocks, num_sms, s)
+                               : launch_backward_ring<T, 4, 2, LEAD, DH>(a, packs, blocks, num_sms, s);
+    if (packs <= 1024)
+        launch_programmatic(rms_backward_kernel<T, 8, 2, 0, LEAD, DH>, blocks, round32((packs + 1) / 2), 0, s, a);
+    else
+        launch_programmatic(rms_backward_kernel<T, 8, 4, 0, LEAD, DH>, blocks, round32((packs + 3) / 4), 0, s, a);
     return true;
+}
+
+template <typename T, int V, int VPT, bool DH>
+void launch_backward_warps(const RmsBwdArgs &a, int blocks, cudaStream_t s)
+{
+    launch_programmatic(rms_backward_warp_kernel<T, V, VPT, DH>, blocks, ROW_WARPS * 32, 0, s, a);
 }
 
 template <typename T, bool DH>
@@ -462,33 +509,23 @@ bool launch_rms_backward(const RmsBwdArgs &a, Rows rows, int num_sms, PartRows &
 {
     int blocks;
     const Plan plan = backward_plan<T>(a.T, a.H, rows, num_sms, blocks);
-    const bool packed = rows == PACKED;
     const int packs = most_packs<T>(a.H, rows);
     constexpr int boundary = VEC<T>;
-    part = {a.part, blocks, a.pitch, plan == RING && !packed ? a.H % boundary : 0, boundary};
-    if (plan == RING && !packed)
-        return packs <= 512 ? launch_backward_ring<T, 2, 4, true, DH>(a, packs, blocks, s)
-                            : launch_backward_ring<T, 2, 2, true, DH>(a, packs, blocks, s);
-    if (plan == RING)
-        return packs <= 512    ? launch_backward_ring<T, 2, 4, false, DH>(a, packs, blocks, s)
-               : packs <= 1024 ? launch_backward_ring<T, 2, 2, false, DH>(a, packs, blocks, s)
-                               : launch_backward_ring<T, 4, 2, false, DH>(a, packs, blocks, s);
-    if (plan == WARPS_1 && packed)
-        launch_programmatic(rms_backward_warp_kernel<T, 8, 1, DH>, blocks, ROW_WARPS * 32, 0, s, a);
-    else if (plan == WARPS_4 && packed)
-        launch_programmatic(rms_backward_warp_kernel<T, 8, 4, DH>, blocks, ROW_WARPS * 32, 0, s, a);
-    else if (plan == DIRECT && packed && packs <= 1024)
-        launch_programmatic(rms_backward_kernel<T, 8, 2, 0, false, DH>, blocks, round32((packs + 1) / 2), 0, s, a);
-    else if (plan == DIRECT && packed)
-        launch_programmatic(rms_backward_kernel<T, 8, 4, 0, false, DH>, blocks, round32((packs + 3) / 4), 0, s, a);
-    else if (plan == WARPS_1)
-        launch_programmatic(rms_backward_warp_kernel<T, 1, 8, DH>, blocks, ROW_WARPS * 32, 0, s, a);
-    else if (plan == WARPS_4)
-        launch_programmatic(rms_backward_warp_kernel<T, 1, 32, DH>, blocks, ROW_WARPS * 32, 0, s, a);
-    else if (a.H <= 8192)
+    // (a block's row of sums starts at its rows' lead)
+    part = {a.part, blocks, a.pitch, rows == PHASED && (plan == RING || plan == DIRECT) ? a.H % boundary : 0, boundary};
+    if (plan == WARPS)
+        packs <= 32 ? launch_backward_warps<T, 8, 1, DH>(a, blocks, s) : launch_backward_warps<T, 8, 4, DH>(a, blocks, s);
+    else if (plan == ELEMENT_WARPS)
+        a.H <= 256   ? launch_backward_warps<T, 1, 8, DH>(a, blocks, s)
+        : a.H <= 576 ? launch_backward_warps<T, 1, 18, DH>(a, blocks, s)
+                     : launch_backward_warps<T, 1, 32, DH>(a, blocks, s);
+    else if (plan == ELEMENTS && a.H <= 8192)
         launch_programmatic(rms_backward_kernel<T, 1, 16, 0, false, DH>, blocks, round32((a.H + 15) / 16), 0, s, a);
-    else
+    else if (plan == ELEMENTS)
         launch_programmatic(rms_backward_kernel<T, 1, 32, 0, false, DH>, blocks, round32((a.H + 31) / 32), 0, s, a);
+    else
+        return rows == PACKED ? launch_backward_packs<T, false, DH>(a, plan, packs, blocks, num_sms, s)
+                              : launch_backward_packs<T, true, DH>(a, plan, packs, blocks, num_sms, s);
     return true;
 }
 
