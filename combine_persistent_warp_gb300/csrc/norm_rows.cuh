@@ -377,7 +377,7 @@ template <typename TW>
 __global__ void norm_reduce_kernel(const PartRows p, int H, TW *dweight, TW *dbias)
 {
     __shared__ float tile[32][33];
-    ptx::follow();
+    ptx::grid_dependency_wait();
     const float *src = p.part + static_cast<size_t>(blockIdx.y) * p.blocks * p.pitch;
     TW *dst = blockIdx.y == 0 ? dweight : dbias;
     if (!dst)
@@ -385,18 +385,22 @@ __global__ void norm_reduce_kernel(const PartRows p, int H, TW *dweight, TW *dbi
     const int col = blockIdx.x * 32 + threadIdx.x;
     float s = 0.0f;
     if (col < H) {
-        // eight loads at a time, whether there are as many rows or not
-        for (int b0 = threadIdx.y; b0 < p.blocks; b0 += 8 * 32) {
-            float v[8];
+        int b = threadIdx.y;
+        const auto add = [&](auto count) {   // so many loads at a time
+            constexpr int N = decltype(count)::value;
+            for (; b + 32 * (N - 1) < p.blocks; b += 32 * N) {
+                float v[N];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int b = b0 + 32 * i;
-                v[i] = b < p.blocks ? src[static_cast<size_t>(b) * p.pitch + col + ((b * p.step) & (p.boundary - 1))] : 0.0f;
+                for (int i = 0; i < N; ++i)
+                    v[i] = src[static_cast<size_t>(b + 32 * i) * p.pitch + col + (((b + 32 * i) * p.step) & (p.boundary - 1))];
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    s += v[i];
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                s = b0 + 32 * i < p.blocks ? s + v[i] : s;
-        }
+        };
+        add(std::integral_constant<int, 8>());
+        add(std::integral_constant<int, 4>());
+        add(std::integral_constant<int, 1>());
     }
     tile[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
