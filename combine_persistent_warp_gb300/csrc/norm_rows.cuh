@@ -49,11 +49,11 @@ __device__ __forceinline__ void fetch(Pack<T, V> (&q)[VPT], const T *row, int t,
         const int p = t + j * step;
         const long long e = static_cast<long long>(p) * V - lead;
         if (p < packs && (!LEAD || (e >= 0 && e + V <= H))) {
-            q[j] = load_pack<T, V>(row + e);
+            q[j] = load_pack<T, V, false>(row + e);
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                q[j].v[i] = LEAD && p < packs && e + i >= 0 && e + i < H ? __ldg(row + e + i) : from_f<T>(0.0f);
+                q[j].v[i] = LEAD && p < packs && e + i >= 0 && e + i < H ? row[e + i] : from_f<T>(0.0f);
         }
     }
 }
@@ -144,7 +144,7 @@ __device__ __forceinline__ void fetch_columns(float2 (&f)[PAIRS<V, VPT>], const 
 #pragma unroll
         for (int j = 0; j < VPT * M; ++j) {
             const int c = (t + j / M * step) * V - lead + j % M * N;
-            h[j] = load_halves(p + c, c >= N - 1 && c + 2 * N <= H);
+            h[j] = load_halves<false>(p + c, c >= N - 1 && c + 2 * N <= H);
         }
 #pragma unroll
         for (int j = 0; j < VPT * M; ++j) {
@@ -153,7 +153,7 @@ __device__ __forceinline__ void fetch_columns(float2 (&f)[PAIRS<V, VPT>], const 
             if (!(c >= N - 1 && c + 2 * N <= H) && c + N > 0 && c < H) {
 #pragma unroll
                 for (int i = 0; i < N; ++i)
-                    u.v[i] = c + i >= 0 && c + i < H ? __ldg(p + c + i) : from_f<W>(0.0f);
+                    u.v[i] = c + i >= 0 && c + i < H ? p[c + i] : from_f<W>(0.0f);
             }
 #pragma unroll
             for (int i = 0; i < N; ++i)

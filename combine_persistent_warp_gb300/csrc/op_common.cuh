@@ -39,12 +39,14 @@ struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
     T v[N];
 };
 
-template <typename T, int N>
+// READ_ONLY: nothing writes it while the kernel is there, which does not hold of one that is launched ahead of the
+// kernel before.
+template <typename T, int N, bool READ_ONLY = true>
 __device__ __forceinline__ Pack<T, N> load_pack(const T *p)
 {
     if constexpr (N == 1) {
         Pack<T, 1> r;
-        r.v[0] = __ldg(p);
+        r.v[0] = READ_ONLY ? __ldg(p) : *p;
         return r;
     } else {
         static_assert(sizeof(T) * N % 16 == 0, "whole accesses");
@@ -54,7 +56,7 @@ __device__ __forceinline__ Pack<T, N> load_pack(const T *p)
         } u;
 #pragma unroll
         for (int i = 0; i < static_cast<int>(sizeof(T) * N / 16); ++i)
-            u.q[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            u.q[i] = READ_ONLY ? __ldg(reinterpret_cast<const uint4 *>(p) + i) : reinterpret_cast<const uint4 *>(p)[i];
         return u.pack;
     }
 }
@@ -144,31 +146,38 @@ __device__ __forceinline__ int lead_of(const T *row)
 }
 // The aligned vector that holds p (zeros where `is` is false).  Written out, so that the loads of
 // all slots are issued without a branch between them.
-template <typename T>
+template <bool READ_ONLY = true, typename T>
 __device__ __forceinline__ uint4 load_aligned(const T *p, bool is, int ahead = 0)
 {
     uint4 q;
-    asm volatile("{\n\t"
-                 ".reg .pred p;\n\t"
-                 "setp.ne.s32 p, %5, 0;\n\t"
-                 "mov.b32 %0, 0;\n\t"
-                 "mov.b32 %1, 0;\n\t"
-                 "mov.b32 %2, 0;\n\t"
-                 "mov.b32 %3, 0;\n\t"
-                 "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t"
-                 "}"
-                 : "=&r"(q.x), "=&r"(q.y), "=&r"(q.z), "=&r"(q.w)
-                 : "l"((reinterpret_cast<uint64_t>(p) & ~15ull) + 16 * ahead), "r"(static_cast<int>(is)));
+    const uint64_t from = (reinterpret_cast<uint64_t>(p) & ~15ull) + 16 * ahead;
+#define LOAD_ALIGNED(kind)                                        \
+    asm volatile("{\n\t"                                          \
+                 ".reg .pred p;\n\t"                              \
+                 "setp.ne.s32 p, %5, 0;\n\t"                      \
+                 "mov.b32 %0, 0;\n\t"                             \
+                 "mov.b32 %1, 0;\n\t"                             \
+                 "mov.b32 %2, 0;\n\t"                             \
+                 "mov.b32 %3, 0;\n\t"                             \
+                 "@p " kind ".v4.b32 {%0, %1, %2, %3}, [%4];\n\t" \
+                 "}"                                              \
+                 : "=&r"(q.x), "=&r"(q.y), "=&r"(q.z), "=&r"(q.w) \
+                 : "l"(from), "r"(static_cast<int>(is)))
+    if constexpr (READ_ONLY)
+        LOAD_ALIGNED("ld.global.nc");
+    else
+        LOAD_ALIGNED("ld.global");
+#undef LOAD_ALIGNED
     return q;
 }
 // 16 bytes at any element: the two aligned vectors that cover them, shifted.
 struct Halves {
     uint4 lo, hi;
 };
-template <typename T>
+template <bool READ_ONLY = true, typename T>
 __device__ __forceinline__ Halves load_halves(const T *p, bool is = true)
 {
-    return {load_aligned(p, is), load_aligned(p, is, 1)};
+    return {load_aligned<READ_ONLY>(p, is), load_aligned<READ_ONLY>(p, is, 1)};
 }
 // The 16 bytes from p on.
 template <typename T>

@@ -461,7 +461,7 @@ __device__ __noinline__ int choose_again(const ScoreArgs &a, const T *l, uint64_
         if (whole) {
             my_idx = lane < n ? expert_of<IPL>(mine) : -1;
             const float logit = lane < n ? to_f<T>(l[my_idx]) : 0.0f;
-            const float bias = a.bias && lane < n ? __ldg(a.bias + my_idx) : 0.0f;
+            const float bias = a.bias && lane < n ? a.bias[my_idx] : 0.0f;
             my_idx = direct ? rank_exactly<true>(logit, 0.0f, false, my_idx, n, lane)
                             : rank_exactly<false>(logit, bias, a.bias, my_idx, n, lane);
             return min(n, a.k);
@@ -551,7 +551,7 @@ __device__ __forceinline__ void score_tokens(const ScoreArgs &a, const float (&b
     if (!direct || sizeof(T) == 4) {
         // what the words leave out is below the last slot, and every slot above the one after it, or equal to it in what
         // it is computed from
-        const float bias = a.bias && slot < found ? __ldg(a.bias + my_idx) : 0.0f;
+        const float bias = a.bias && slot < found ? a.bias[my_idx] : 0.0f;
         const float c = direct ? logit : s + bias;
         const float after = __shfl_down_sync(ALL, c, 1), after_logit = __shfl_down_sync(ALL, logit, 1);
         const float after_bias = __shfl_down_sync(ALL, bias, 1);

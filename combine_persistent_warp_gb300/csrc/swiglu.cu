@@ -6,6 +6,7 @@
 //   7), and each is n X/64 with the nearest whole n in -127 .. 127, ties to even (an MX block of INT8
 //   elements).  X is a power of two, so v 64/X and n X/64 are exact and the rounding to n is the only one.
 //
+// (Loads are plain ones, not of the read-only kind: kernels start before the one that writes what they read is done.)
 // All of it is elementwise and bound by HBM.  A thread takes E neighbours of gate and of up (32 bytes, or 16 or 8
 // where the rows' boundaries allow no more), so 32/E neighbouring lanes hold a group; rows off those boundaries go
 // element by element, a group a warp access.
@@ -123,13 +124,14 @@ template <typename T, int E>
 __device__ __forceinline__ void load(Elements<T, E> &q, const T *p)
 {
     if constexpr (Elements<T, E>::BYTES == 32)
-        asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-            : "=r"(q.w[0]), "=r"(q.w[1]), "=r"(q.w[2]), "=r"(q.w[3]), "=r"(q.w[4]), "=r"(q.w[5]), "=r"(q.w[6]), "=r"(q.w[7])
-            : "l"(p));
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(q.w[0]), "=r"(q.w[1]), "=r"(q.w[2]), "=r"(q.w[3]), "=r"(q.w[4]), "=r"(q.w[5]), "=r"(q.w[6]), "=r"(q.w[7])
+                     : "l"(p)
+                     : "memory");
     else if constexpr (Elements<T, E>::BYTES == 16)
-        *reinterpret_cast<uint4 *>(q.w) = __ldg(reinterpret_cast<const uint4 *>(p));
+        *reinterpret_cast<uint4 *>(q.w) = *reinterpret_cast<const uint4 *>(p);
     else
-        *reinterpret_cast<uint2 *>(q.w) = __ldg(reinterpret_cast<const uint2 *>(p));
+        *reinterpret_cast<uint2 *>(q.w) = *reinterpret_cast<const uint2 *>(p);
 }
 template <typename T, int E>
 __device__ __forceinline__ void store(T *p, const Elements<T, E> &q)
@@ -186,11 +188,11 @@ __device__ __forceinline__ Codes<E> load_codes(const int8_t *p)
 {
     Codes<E> c;
     if constexpr (E == 16)
-        *reinterpret_cast<uint4 *>(c.w) = __ldg(reinterpret_cast<const uint4 *>(p));
+        *reinterpret_cast<uint4 *>(c.w) = *reinterpret_cast<const uint4 *>(p);
     else if constexpr (E == 8)
-        *reinterpret_cast<uint2 *>(c.w) = __ldg(reinterpret_cast<const uint2 *>(p));
+        *reinterpret_cast<uint2 *>(c.w) = *reinterpret_cast<const uint2 *>(p);
     else
-        c.w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+        c.w[0] = *reinterpret_cast<const uint32_t *>(p);
     return c;
 }
 template <int E>
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(THREADS) swiglu_backward_pack_kernel(const Act
         const int8_t *codes = a.codes + row * 2 * a.I + c;
         const uint8_t *scales = a.scales + row * 2 * a.groups + p / LANES;
         const Codes<E> cg = load_codes<E>(codes), cu = load_codes<E>(codes + a.I);
-        const uint32_t bg = __ldg(scales), bu = __ldg(scales + a.groups);
+        const uint32_t bg = scales[0], bu = scales[a.groups];
         values_of<E>(g, cg, step_of(bg));
         values_of<E>(u, cu, step_of(bu));
     } else {
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(THREADS) restore_pack_kernel(const KeepArgs a)
         return;
     float2 v[E / 2];
     const Codes<E> codes = load_codes<E>(a.codes + row * a.H + c);
-    values_of<E>(v, codes, step_of(__ldg(a.scales + row * a.groups + p / LANES)));
+    values_of<E>(v, codes, step_of(a.scales[row * a.groups + p / LANES]));
     store_pairs<T, E>(static_cast<T *>(a.out) + row * a.H + c, v);
 }
 
@@ -467,7 +469,7 @@ __device__ __forceinline__ void load_spread(float (&f)[8], const T *row, int c, 
     T v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        v[j] = __ldg(row + (WHOLE ? c + 32 * j : min(c + 32 * j, n - 1)));
+        v[j] = row[WHOLE ? c + 32 * j : min(c + 32 * j, n - 1)];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         f[j] = WHOLE || c + 32 * j < n ? to_f<T>(v[j]) : 0.0f;
@@ -500,11 +502,11 @@ __device__ __forceinline__ void restore_spread(float (&f)[8], const int8_t *code
 {
     // lane j has the step of group j
     const int group = (k.first >> 5) + (k.lane & 7);
-    const uint8_t byte = __ldg(scales + (WHOLE ? group : min(group, groups_of(n) - 1)));
+    const uint8_t byte = scales[WHOLE ? group : min(group, groups_of(n) - 1)];
     uint8_t v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        v[j] = __ldg(reinterpret_cast<const uint8_t *>(codes) + (WHOLE ? k.c + 32 * j : min(k.c + 32 * j, n - 1)));
+        v[j] = *(reinterpret_cast<const uint8_t *>(codes) + (WHOLE ? k.c + 32 * j : min(k.c + 32 * j, n - 1)));
     const float step = step_of(byte);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
