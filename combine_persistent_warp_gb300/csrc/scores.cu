@@ -106,18 +106,26 @@ __device__ __forceinline__ float bound_of(uint32_t word)
     }
 }
 
+// The sigmoid's c in 64 bits, as a key.  (One copy of this code: what is seldom run is seldom at hand.)
+__device__ __noinline__ uint64_t exact_key(float logit, float bias, bool has_bias)
+{
+    const double s = 1.0 / (1.0 + exp(-static_cast<double>(logit)));
+    return logit == -INFINITY ? 0ull : order_key(has_bias ? s + static_cast<double>(bias) : s);
+}
+
 // Whether the lane's group of experts stays, from the group's two largest keys: `least` and `most` are
 // the lowest score that stays and the highest that does not (0: none).  Group g is that of the lanes
-// g << shift and after.
+// g << shift and after; `own` its score.
 __device__ __forceinline__ uint32_t key_sum(uint32_t a, uint32_t b) { return plain_key(plain_value(a) + plain_value(b)); }
 __device__ __forceinline__ uint64_t key_sum(uint64_t a, uint64_t b) { return order_key(key_value(a) + key_value(b)); }
 template <typename K>
-__device__ __forceinline__ bool group_stays(const ScoreArgs &a, K first, K second, int lane, int shift, K &least, K &most)
+__device__ __forceinline__ bool group_stays(const ScoreArgs &a, K first, K second, int lane, int shift, K &least, K &most, K &own)
 {
     const int g = lane >> shift;
     K score = g < a.groups && first > NEVER<K> ? first : 0;
     if (a.pair && second > NEVER<K>)
         score = key_sum(first, second);
+    own = score;
     bool stays = false;
     least = 0;
     for (int j = 0; j < a.kept; ++j) {
@@ -152,41 +160,90 @@ __device__ __forceinline__ int spot(int e) { return e + (e >> 5) * 4; }
 template <int IPL>
 constexpr int SPOTS = IPL * 36;
 
-// -inf in place of the c of the groups that do not stay.
-template <int IPL>
-__device__ __forceinline__ void keep_groups(const ScoreArgs &a, float (&c)[IPL], uint32_t *seen, int lane, uint32_t &least, uint32_t &most)
+// The same where scores within `open` of each other are in doubt: groups that are so far above all that do not stay
+// are sure to, and those in doubt are ranked by their scores in 64 bits for the places that are left.
+template <typename T>
+__device__ __noinline__ bool group_stays_exactly(const ScoreArgs &a, const T *l, uint32_t own, bool stays, uint32_t least, uint32_t most, float open,
+                                                 uint64_t *seen, int lane, int shift)
 {
-    uint32_t first = 0, second = 0;
-    if (a.group_shift >= 0) {   // a group is 1 << group_shift lanes
+    const float v = plain_value(own);
+    const bool head = (lane & ((1 << shift) - 1)) == 0 && own != 0u;
+    const bool sure = stays && v - plain_value(most) > open;
+    const bool doubt = own != 0u && !sure && (stays || !(plain_value(least) - v > open));
+    const uint32_t in_doubt = __ballot_sync(ALL, head && doubt);   // by their first lanes
+    const int left = a.kept - __popc(__ballot_sync(ALL, head && sure)), n = __popc(in_doubt);
+    for (int i = lane; i < n * a.per; i += 32) {
+        const int nth = static_cast<int>((static_cast<uint32_t>(i) * a.per_magic) >> 20);
+        uint32_t after = in_doubt;
+        for (int k = 0; k < nth; ++k)
+            after &= after - 1u;
+        const int e = ((__ffs(static_cast<int>(after)) - 1) >> shift) * a.per + i - nth * a.per;
+        seen[i] = exact_key(to_f<T>(l[e]), a.bias ? a.bias[e] : 0.0f, a.bias);
+    }
+    __syncwarp();
+    uint64_t first = 0, second = 0;
+    if (lane < n) {
+#pragma unroll 4
+        for (int i = 0; i < a.per; ++i)
+            insert(seen[lane * a.per + i], first, second);
+    }
+    __syncwarp();
+    if (a.pair && second != 0)
+        first = key_sum(first, second);
+    int rank = 0;
+    for (int r = 0; r < n; ++r) {
+        const uint64_t other = __shfl_sync(ALL, first, r);
+        rank += other > first || (other == first && r < lane);
+    }
+    const uint32_t chosen = __ballot_sync(ALL, lane < n && rank < left);
+    return sure || (doubt && (chosen >> __popc(in_doubt & ((1u << (lane >> shift << shift)) - 1u)) & 1u));
+}
+
+// -inf in place of the c of the groups that do not stay; two c's within `open` (and 2^-22 of their size) of each
+// other may be in another order (negative: none).  False: softmax scores, and which groups stay is in doubt.
+template <typename T, int IPL>
+__device__ __forceinline__ bool keep_groups(const ScoreArgs &a, const T *l, float (&c)[IPL], uint64_t *seen, int lane, float open)
+{
+    uint32_t first = 0, second = 0, least, most, own;
+    const bool in_lanes = a.group_shift >= 0;   // a group is 1 << group_shift lanes
+    const int shift = in_lanes ? a.group_shift : a.shift;
+    if (in_lanes) {
         first = plain_key(c[0]);
 #pragma unroll
         for (int i = 1; i < IPL; ++i)
             insert(plain_key(c[i]), first, second);
-        merge_lanes(first, second, 1 << a.group_shift);
-        const bool stays = group_stays(a, first, second, lane, a.group_shift, least, most);
+    } else {
+        uint32_t *keys = reinterpret_cast<uint32_t *>(seen);
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < IPL; ++i)
-            c[i] = stays ? c[i] : -INFINITY;
-        return;
+            if (lane * IPL + i < a.E)
+                keys[spot(lane * IPL + i)] = plain_key(c[i]);
+        __syncwarp();
+        const int g = lane >> shift;
+        if (g < a.groups)
+            for (int e = lane & (a.lanes - 1); e < a.per; e += a.lanes)
+                insert(keys[spot(g * a.per + e)], first, second);
+        __syncwarp();
     }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < IPL; ++i)
-        if (lane * IPL + i < a.E)
-            seen[spot(lane * IPL + i)] = plain_key(c[i]);
-    __syncwarp();
-    const int g = lane >> a.shift;
-    if (g < a.groups)
-        for (int e = lane & (a.lanes - 1); e < a.per; e += a.lanes)
-            insert(seen[spot(g * a.per + e)], first, second);
-    merge_lanes(first, second, a.lanes);
-    const uint32_t stay = __ballot_sync(ALL, group_stays(a, first, second, lane, a.shift, least, most));
+    merge_lanes(first, second, 1 << shift);
+    bool stays = group_stays(a, first, second, lane, shift, least, most, own), sure = true;
+    if (open >= 0.0f && most != 0u) {
+        const float v = plain_value(least), both = 2.0f * open + fabsf(v) * 0x1p-21f;
+        if (!(v - plain_value(most) > both)) {
+            if (a.softmax)
+                sure = false;
+            else
+                stays = group_stays_exactly<T>(a, l, own, stays, least, most, both, seen, lane, shift);
+        }
+    }
+    const uint32_t stay = __ballot_sync(ALL, stays);
 #pragma unroll
     for (int i = 0; i < IPL; ++i) {
         const int e = lane * IPL + i, ge = static_cast<int>((static_cast<uint32_t>(e) * a.per_magic) >> 20);
-        if (e < a.E && !(stay >> (ge << a.shift) & 1u))
-            c[i] = -INFINITY;
+        c[i] = (in_lanes ? stays : (e < a.E && (stay >> (ge << shift) & 1u))) ? c[i] : -INFINITY;
     }
+    return sure;
 }
 
 // The choice in 64 bits of all experts.  Seldom run, so that its code is seldom at hand: short, over keys in shared
@@ -207,24 +264,27 @@ __device__ __noinline__ int choose_exactly(const ScoreArgs &a, const T *l, uint6
 #pragma unroll 2
         for (int e = lane; e < a.E; e += 32) {
             const float f = to_f<T>(l[e]);
-            const double x = exp(a.softmax ? static_cast<double>(f) - top : -static_cast<double>(f));
-            sum += x;
-            const double s = (a.softmax ? x : 1.0) / (a.softmax ? total : 1.0 + x);
-            seen[spot(e)] = f == -INFINITY ? 0ull : order_key(a.bias ? s + static_cast<double>(a.bias[e]) : s);
+            if (a.softmax) {
+                const double x = exp(static_cast<double>(f) - top);
+                sum += x;
+                seen[spot(e)] = f == -INFINITY ? 0ull : order_key(a.bias ? x / total + static_cast<double>(a.bias[e]) : x / total);
+            } else {
+                seen[spot(e)] = exact_key(f, a.bias ? a.bias[e] : 0.0f, a.bias);
+            }
         }
         if (pass == 0)
             total = warp_sum(sum);
     }
     __syncwarp();
     if (a.groups > 1) {
-        uint64_t first = 0, second = 0, least, most;
+        uint64_t first = 0, second = 0, least, most, own;
         const int g = lane >> a.shift;
         if (g < a.groups)
 #pragma unroll 2
             for (int e = lane & (a.lanes - 1); e < a.per; e += a.lanes)
                 insert(seen[spot(g * a.per + e)], first, second);
         merge_lanes(first, second, a.lanes);
-        const uint32_t stay = __ballot_sync(ALL, group_stays(a, first, second, lane, a.shift, least, most));
+        const uint32_t stay = __ballot_sync(ALL, group_stays(a, first, second, lane, a.shift, least, most, own));
         for (int e = lane; e < a.E; e += 32)
             if (!(stay >> (static_cast<int>((static_cast<uint32_t>(e) * a.per_magic) >> 20) << a.shift) & 1u))
                 seen[spot(e)] = 0;
@@ -308,8 +368,7 @@ __device__ __forceinline__ uint32_t take_largest(uint32_t (&w)[IPL])
 template <bool DIRECT>
 __device__ __noinline__ int rank_exactly(float logit, float bias, bool has_bias, int idx, int n, int lane)
 {
-    const double l = static_cast<double>(logit), s = DIRECT ? l : 1.0 / (1.0 + exp(-l));
-    const uint64_t key = order_key(has_bias ? s + static_cast<double>(bias) : s);
+    const uint64_t key = DIRECT ? order_key(static_cast<double>(logit)) : exact_key(logit, bias, has_bias);
     int rank = 0;
     for (int r = 0; r < n; ++r) {
         const uint64_t other = __shfl_sync(ALL, key, r);
@@ -364,11 +423,10 @@ struct Softmax {
     float top, total, open;
 };
 
-// A token's c from its logits and the biases, without those of the groups that do not stay.  False: which groups
-// stay is open.
-template <int IPL>
-__device__ __forceinline__ bool make_c(const ScoreArgs &a, float (&f)[IPL], const float (&b)[IPL], bool direct, uint64_t *seen, int lane,
-                                       Softmax &sm)
+// A token's c from its logits and the biases, without those of the groups that do not stay (false: see keep_groups).
+template <typename T, int IPL>
+__device__ __forceinline__ bool make_c(const ScoreArgs &a, const T *l, float (&f)[IPL], const float (&b)[IPL], bool direct, uint64_t *seen,
+                                       int lane, Softmax &sm)
 {
     sm = {0.0f, 1.0f, 0.0f};
     if (a.softmax && !(direct && a.renorm)) {
@@ -402,15 +460,7 @@ __device__ __forceinline__ bool make_c(const ScoreArgs &a, float (&f)[IPL], cons
             f[i] = fminf(a.bias ? s + b[i] : s, f[i] + 3e38f);
         }
     }
-    if (a.groups > 1) {
-        uint32_t least, most;
-        keep_groups<IPL>(a, f, reinterpret_cast<uint32_t *>(seen), lane, least, most);
-        if (!direct && most != 0u) {
-            const float v = plain_value(least);
-            return v - plain_value(most) > 2.0f * sm.open + fabsf(v) * 0x1p-21f;
-        }
-    }
-    return true;
+    return a.groups == 1 || keep_groups<T, IPL>(a, l, f, seen, lane, direct ? -1.0f : sm.open);
 }
 template <int IPL, bool FIXED>
 __device__ __forceinline__ void make_words(uint32_t (&word)[IPL], const float (&c)[IPL], int lane)
@@ -445,7 +495,7 @@ __device__ __noinline__ int choose_again(const ScoreArgs &a, const T *l, uint64_
         Softmax sm;
         bool whole = false;
         int n = 0;
-        if (make_c<IPL>(a, f, b, direct, seen, lane, sm)) {
+        if (make_c<T, IPL>(a, l, f, b, direct, seen, lane, sm)) {
             make_words<IPL, FIXED>(word, f, lane);
             while (!whole && n < 32) {
                 const uint32_t m = take_largest<IPL>(word);
@@ -515,7 +565,7 @@ __device__ __forceinline__ void score_tokens(const ScoreArgs &a, const float (&b
             continue;
         uint32_t word[IPL], m = 0u, after = 0u;
         Softmax its;
-        const bool its_sure = make_c<IPL>(a, f[q], b, direct, seen, lane, its);
+        const bool its_sure = make_c<T, IPL>(a, row(q), f[q], b, direct, seen, lane, its);
         make_words<IPL, FIXED>(word, f[q], lane);
         int n = 0;
         for (; n < a.k; ++n) {
