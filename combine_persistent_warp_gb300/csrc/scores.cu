@@ -758,15 +758,19 @@ void launch_scores(const ScoreArgs &a, cudaStream_t s)
 {
     launch_programmatic(score_kernel<T, IPL, Q>, (a.T + WARPS * Q - 1) / (WARPS * Q), WARPS * 32, 0, s, a);
 }
-// Four tokens a warp where that leaves every SM several warps.
-constexpr int MANY_TOKENS = 4096;
+// Tokens of a warp: the more there are, the less their slots cost, and the later the last is begun.  128 experts in 8
+// groups, bf16, with 1, 2 and 4 of them: 4096 tokens 8.4, 8.7 and 11.4 us (one group, unbiased, 4.2, 3.9, 4.8), 8192
+// 10.8, 10.3, 13.3 (6.7, 5.7, 7.4), 16384 15.6, 14.2, 13.8 (11.2, 9.4, 9.7), 65536 49, 42, 40 (38, 30, 26).
+constexpr int TWO_TOKENS = 6144, FOUR_TOKENS = 16384;
 template <typename T, int IPL>
 struct ScoreLaunch {
     static void go(const ScoreArgs &a, cudaStream_t s)
     {
         if constexpr (IPL <= 8) {
-            if (a.k <= 8 && a.T >= MANY_TOKENS)
+            if (a.k <= 8 && a.T >= FOUR_TOKENS)
                 return launch_scores<T, IPL, 4>(a, s);
+            if (a.k <= 16 && a.T >= TWO_TOKENS)
+                return launch_scores<T, IPL, 2>(a, s);
         }
         launch_scores<T, IPL, 1>(a, s);
     }

@@ -234,3 +234,18 @@ def test_gradient_against_differences():
                 d[2, e] = 1e-5
                 # the differences are 1e-9 off, the gradient some hundred roundings of terms of at most 4
                 assert abs((f(l.double() + d) - f(l.double() - d)) / 2e-5 - got[2, e].double()) <= 1e-4
+
+
+@pytest.mark.parametrize("T,k", [(6143, 8), (6145, 8), (6147, 16), (16384, 8), (16387, 7), (16385, 16), (16386, 20)])
+@pytest.mark.parametrize("score,bias,groups,kept", [("sigmoid", True, 8, 4), ("sigmoid", True, 1, 1), ("softmax", False, 1, 1), ("sigmoid", False, 8, 3)])
+def test_long_batches(T, k, score, bias, groups, kept):
+    """Several tokens a warp, the last warp's not all there, some of them masked; a bias past what the words hold in fixed point."""
+    for dtype in (torch.bfloat16, torch.float32):
+        l = _logits(T, 96, dtype, seed=T)
+        mask = torch.rand(T, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda") > 0.1
+        b = _bias(96) if bias else None
+        _check(l, k, score, b, groups, kept, mask=mask)
+        if bias:
+            b = 5 * b
+            b[3] = -float("inf")
+            _check(l, k, score, b, groups, kept, scale=0.5)
