@@ -435,25 +435,32 @@ void launch_rms(const RmsArgs &a, Rows rows, int num_sms, cudaStream_t s)
 
 // The backward pass: kernel, blocks (each keeps a row of partial sums) and how they are found.
 enum Plan { WARPS, RING, DIRECT, ELEMENT_WARPS, ELEMENTS };
+// Rows of a warp are held in registers, with dh many of them, so that with dh longer rows go through rings (bf16, 16384 x
+// 1024 30.6 us by warps and 28.7 in rings, without dh 22.5 and 21.4, but x 768 15.5 and 19.1; off the boundaries, x 1001
+// 63 and 32, x 701 47 and 30, and without dh 26 and 28, 19 and 28).
 template <typename T>
-Plan backward_plan(int T_, int H, Rows rows, int num_sms, int &blocks)
+Plan backward_plan(int T_, int H, Rows rows, bool dh, int num_sms, int &blocks)
 {
     const int packs = most_packs<T>(H, rows);
-    if (in_packs<T>(H, rows)) {
-        if (rows == PACKED && (packs <= 32 || (packs <= 128 && T_ > 2 * num_sms))) {
-            blocks = warp_blocks(T_, 3, num_sms);
-            return WARPS;
-        }
+    const bool in_rings = rows == PHASED && dh && H > 576 && H <= 1024;
+    if (in_packs<T>(H, rows) || in_rings) {
         size_t smem;
         const int per_sm = packs <= 1024 ? ring_blocks<T, 8, 2>(round32((packs + 1) / 2), packs <= 512 ? 4 : 2, 3, smem)
                                          : ring_blocks<T, 8, 4>(round32((packs + 3) / 4), 2, 3, smem);
-        if (per_sm >= 1 && T_ >= 4 * per_sm * num_sms) {
+        const bool ring = per_sm >= 1 && T_ >= 4 * per_sm * num_sms;
+        if (rows == PACKED && (packs <= 32 || (packs <= 128 && T_ > 2 * num_sms && !(ring && dh && packs > 64)))) {
+            blocks = warp_blocks(T_, 3, num_sms);
+            return WARPS;
+        }
+        if (ring) {
             blocks = ring_grid(per_sm, num_sms);
             return RING;
         }
-        const int most = ring_grid(2, num_sms);
-        blocks = T_ < most ? T_ : most;
-        return DIRECT;
+        if (!in_rings) {
+            const int most = ring_grid(2, num_sms);
+            blocks = T_ < most ? T_ : most;
+            return DIRECT;
+        }
     }
     if (H <= 256 || (H <= 1024 && T_ > 2 * num_sms)) {
         blocks = warp_blocks(T_, 3, num_sms);
@@ -467,11 +474,12 @@ template <typename T>
 int most_backward_blocks(int T_, int H, int num_sms)
 {
     int most = 0;
-    for (const Rows rows : {PACKED, PHASED, ANY}) {
-        int b;
-        backward_plan<T>(T_, H, rows, num_sms, b);
-        most = b > most ? b : most;
-    }
+    for (const Rows rows : {PACKED, PHASED, ANY})
+        for (const bool dh : {false, true}) {
+            int b;
+            backward_plan<T>(T_, H, rows, dh, num_sms, b);
+            most = b > most ? b : most;
+        }
     return most;
 }
 
@@ -508,7 +516,7 @@ template <typename T, bool DH>
 bool launch_rms_backward(const RmsBwdArgs &a, Rows rows, int num_sms, PartRows &part, cudaStream_t s)
 {
     int blocks;
-    const Plan plan = backward_plan<T>(a.T, a.H, rows, num_sms, blocks);
+    const Plan plan = backward_plan<T>(a.T, a.H, rows, DH, num_sms, blocks);
     const int packs = most_packs<T>(a.H, rows);
     constexpr int boundary = VEC<T>;
     // (a block's row of sums starts at its rows' lead)
