@@ -246,25 +246,31 @@ __device__ __forceinline__ bool keep_groups(const ScoreArgs &a, const T *l, floa
     return sure;
 }
 
+// Without a bias scores are in the order of the logits, which are exact.
+__device__ __forceinline__ bool directly(const ScoreArgs &a) { return !a.bias && (a.groups == 1 || !a.pair); }
+
 // The choice in 64 bits of all experts.  Seldom run, so that its code is seldom at hand: short, over keys in shared
 // memory.
 template <typename T, int IPL>
 __device__ __noinline__ int choose_exactly(const ScoreArgs &a, const T *l, uint64_t *seen, int lane, int &my_idx)
 {
+    const bool direct = directly(a), softmax = a.softmax && !direct;
     double top = 0.0, total = 1.0;
-    if (a.softmax) {
+    if (softmax) {
         float m = -INFINITY;   // (the logits have at most 32 bits)
         for (int e = lane; e < a.E; e += 32)
             m = fmaxf(m, to_f<T>(l[e]));
         top = static_cast<double>(warp_max_f(m));
     }
     // softmax: the sum first
-    for (int pass = a.softmax ? 0 : 1; pass < 2; ++pass) {
+    for (int pass = softmax ? 0 : 1; pass < 2; ++pass) {
         double sum = 0.0;
 #pragma unroll 2
         for (int e = lane; e < a.E; e += 32) {
             const float f = to_f<T>(l[e]);
-            if (a.softmax) {
+            if (direct) {
+                seen[spot(e)] = order_key(static_cast<double>(f));
+            } else if (a.softmax) {
                 const double x = exp(static_cast<double>(f) - top);
                 sum += x;
                 seen[spot(e)] = f == -INFINITY ? 0ull : order_key(a.bias ? x / total + static_cast<double>(a.bias[e]) : x / total);
@@ -477,9 +483,6 @@ __device__ __forceinline__ bool apart(uint32_t last, uint32_t after, float open,
     const float v = bound_of<IPL, FIXED, false>(last);
     return v - bound_of<IPL, FIXED, true>(after) > open + (direct ? 0.0f : fabsf(v) * 0x1p-22f);
 }
-// Without a bias scores are in the order of the logits, which are exact.
-__device__ __forceinline__ bool directly(const ScoreArgs &a) { return !a.bias && (a.groups == 1 || !a.pair); }
-
 // The choice of a token whose words leave it open: as many candidates as the words cannot tell from the k-th,
 // by their values in 64 bits; failing that, all experts by theirs.  Lane j gets slot j's expert.
 template <typename T, int IPL, bool FIXED>

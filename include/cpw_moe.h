@@ -418,7 +418,8 @@ int moe_rms_norm_backward(int T, int H, const void *dy, int64_t lddy, const void
  * The choice goes by c = s + bias (fp32 [E], NULL: none).  With groups > 1, of E/groups neighbouring
  * experts each, a group's score is the sum of its group_top (1 or 2) largest c, the topk_groups best
  * groups stay, and the topk experts with the largest c are chosen from theirs, in descending order; ties go
- * to the lowest group and expert.  c and its sums are compared as computed in 64 bits.  The gate weights are
+ * to the lowest group and expert.  c and its sums are compared as computed in 64 bits (without a bias, and
+ * with sums of one, as the logits are).  The gate weights are
  * scale * s, or with renormalize = 1 scale * s / sum of s over the chosen ones.  -inf, NaN, fewer
  * candidates than topk, and token_mask as in moe_route_topk (a bias of -inf excludes its expert).
  * E <= 1024, topk <= 32, groups <= 32 and a divisor of E, topk <= topk_groups * E/groups, scale finite and

@@ -249,3 +249,14 @@ def test_long_batches(T, k, score, bias, groups, kept):
             b = 5 * b
             b[3] = -float("inf")
             _check(l, k, score, b, groups, kept, scale=0.5)
+
+
+@pytest.mark.parametrize("k", [5, 31, 32])
+def test_large_logits_without_a_bias_are_in_their_own_order(k):
+    """Sigmoids that are 1 in 64 bits too: what the choice goes by without a bias are the logits."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    l = 40.0 + 100 * torch.rand(30, 70, generator=g, device="cuda")
+    for v in (l, l.bfloat16()):
+        idx, w = ops.route_scores(v, k)
+        assert torch.equal(idx, torch.sort(v, dim=1, descending=True, stable=True).indices[:, :k])
+        assert ((w - 1.0 / k).abs() <= 8 * E24).all()
