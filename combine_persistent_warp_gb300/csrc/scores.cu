@@ -113,32 +113,44 @@ __device__ __noinline__ uint64_t exact_key(float logit, float bias, bool has_bia
     return logit == -INFINITY ? 0ull : order_key(has_bias ? s + static_cast<double>(bias) : s);
 }
 
-// Whether the lane's group of experts stays, from the group's two largest keys: `least` and `most` are
-// the lowest score that stays and the highest that does not (0: none).  Group g is that of the lanes
-// g << shift and after; `own` its score.
+// Whether the lane's group of experts stays, from the group's two largest keys, of Q tokens side by side: `least`
+// and `most` are the lowest score that stays and the highest that does not (0: none).  Group g is that of the
+// lanes g << shift and after; `own` its score.
 __device__ __forceinline__ uint32_t key_sum(uint32_t a, uint32_t b) { return plain_key(plain_value(a) + plain_value(b)); }
 __device__ __forceinline__ uint64_t key_sum(uint64_t a, uint64_t b) { return order_key(key_value(a) + key_value(b)); }
-template <typename K>
-__device__ __forceinline__ bool group_stays(const ScoreArgs &a, K first, K second, int lane, int shift, K &least, K &most, K &own)
+template <typename K, int Q>
+struct Groups {
+    K first[Q], second[Q], own[Q], least[Q], most[Q];
+    bool stays[Q];
+};
+template <typename K, int Q>
+__device__ __forceinline__ void choose_groups(const ScoreArgs &a, Groups<K, Q> &v, int lane, int shift)
 {
     const int g = lane >> shift;
-    K score = g < a.groups && first > NEVER<K> ? first : 0;
-    if (a.pair && second > NEVER<K>)
-        score = key_sum(first, second);
-    own = score;
-    bool stays = false;
-    least = 0;
-    for (int j = 0; j < a.kept; ++j) {
-        const K m = warp_max(score);
-        if (m == 0)
-            break;
-        least = m;
-        const int best = (__ffs(static_cast<int>(__ballot_sync(ALL, score == m))) - 1) >> shift;   // ties: the lowest
-        stays = stays || g == best;
-        score = g == best ? 0 : score;
+    K score[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        score[q] = g < a.groups && v.first[q] > NEVER<K> ? v.first[q] : 0;
+        if (a.pair && v.second[q] > NEVER<K>)
+            score[q] = key_sum(v.first[q], v.second[q]);
+        v.own[q] = score[q];
+        v.least[q] = 0;
+        v.stays[q] = false;
     }
-    most = warp_max(score);
-    return stays;
+    for (int j = 0; j < a.kept; ++j) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const K m = warp_max(score[q]);
+            const int best = (__ffs(static_cast<int>(__ballot_sync(ALL, score[q] == m))) - 1) >> shift;   // ties: the lowest
+            const bool mine = g == best && m != 0;
+            v.least[q] = m != 0 ? m : v.least[q];
+            v.stays[q] = v.stays[q] || mine;
+            score[q] = mine ? 0 : score[q];
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+        v.most[q] = warp_max(score[q]);
 }
 template <typename K>
 __device__ __forceinline__ void insert(K v, K &first, K &second)
@@ -146,13 +158,16 @@ __device__ __forceinline__ void insert(K v, K &first, K &second)
     second = max(second, min(first, v));
     first = max(first, v);
 }
-template <typename K>
-__device__ __forceinline__ void merge_lanes(K &first, K &second, int lanes)
+template <typename K, int Q>
+__device__ __forceinline__ void merge_lanes(Groups<K, Q> &v, int lanes)
 {
     for (int o = 1; o < lanes; o <<= 1) {
-        const K f = __shfl_xor_sync(ALL, first, o), s = __shfl_xor_sync(ALL, second, o);
-        second = max(max(second, s), min(first, f));
-        first = max(first, f);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const K f = __shfl_xor_sync(ALL, v.first[q], o), s = __shfl_xor_sync(ALL, v.second[q], o);
+            v.second[q] = max(max(v.second[q], s), min(v.first[q], f));
+            v.first[q] = max(v.first[q], f);
+        }
     }
 }
 // Where expert e's key lies for the lanes that look through groups that are not whole lanes.
@@ -199,51 +214,63 @@ __device__ __noinline__ bool group_stays_exactly(const ScoreArgs &a, const T *l,
     return sure || (doubt && (chosen >> __popc(in_doubt & ((1u << (lane >> shift << shift)) - 1u)) & 1u));
 }
 
-// -inf in place of the c of the groups that do not stay; two c's within `open` (and 2^-22 of their size) of each
-// other may be in another order (negative: none).  False: softmax scores, and which groups stay is in doubt.
-template <typename T, int IPL>
-__device__ __forceinline__ bool keep_groups(const ScoreArgs &a, const T *l, float (&c)[IPL], uint64_t *seen, int lane, float open)
+// What a token's softmax is taken with, and how near two values of c are open (beside 2^-22 of their size).
+struct Softmax {
+    float top, total, open;
+};
+
+// -inf in place of the c of the groups that do not stay, of Q tokens from row l on.  sure[q] is false where scores
+// are softmax and which groups stay is in doubt.
+template <typename T, int IPL, int Q>
+__device__ __forceinline__ void keep_groups(const ScoreArgs &a, const T *l, float (&c)[Q][IPL], const Softmax (&sm)[Q], bool direct, uint64_t *seen,
+                                            int lane, bool (&sure)[Q])
 {
-    uint32_t first = 0, second = 0, least, most, own;
+    Groups<uint32_t, Q> v;
     const bool in_lanes = a.group_shift >= 0;   // a group is 1 << group_shift lanes
     const int shift = in_lanes ? a.group_shift : a.shift;
-    if (in_lanes) {
-        first = plain_key(c[0]);
 #pragma unroll
-        for (int i = 1; i < IPL; ++i)
-            insert(plain_key(c[i]), first, second);
-    } else {
-        uint32_t *keys = reinterpret_cast<uint32_t *>(seen);
-        __syncwarp();
+    for (int q = 0; q < Q; ++q) {
+        v.first[q] = v.second[q] = 0u;
+        if (in_lanes) {
+            v.first[q] = plain_key(c[q][0]);
 #pragma unroll
-        for (int i = 0; i < IPL; ++i)
-            if (lane * IPL + i < a.E)
-                keys[spot(lane * IPL + i)] = plain_key(c[i]);
-        __syncwarp();
-        const int g = lane >> shift;
-        if (g < a.groups)
-            for (int e = lane & (a.lanes - 1); e < a.per; e += a.lanes)
-                insert(keys[spot(g * a.per + e)], first, second);
-        __syncwarp();
-    }
-    merge_lanes(first, second, 1 << shift);
-    bool stays = group_stays(a, first, second, lane, shift, least, most, own), sure = true;
-    if (open >= 0.0f && most != 0u) {
-        const float v = plain_value(least), both = 2.0f * open + fabsf(v) * 0x1p-21f;
-        if (!(v - plain_value(most) > both)) {
-            if (a.softmax)
-                sure = false;
-            else
-                stays = group_stays_exactly<T>(a, l, own, stays, least, most, both, seen, lane, shift);
+            for (int i = 1; i < IPL; ++i)
+                insert(plain_key(c[q][i]), v.first[q], v.second[q]);
+        } else {
+            uint32_t *keys = reinterpret_cast<uint32_t *>(seen);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < IPL; ++i)
+                if (lane * IPL + i < a.E)
+                    keys[spot(lane * IPL + i)] = plain_key(c[q][i]);
+            __syncwarp();
+            const int g = lane >> shift;
+            if (g < a.groups)
+                for (int e = lane & (a.lanes - 1); e < a.per; e += a.lanes)
+                    insert(keys[spot(g * a.per + e)], v.first[q], v.second[q]);
+            __syncwarp();
         }
     }
-    const uint32_t stay = __ballot_sync(ALL, stays);
+    merge_lanes(v, 1 << shift);
+    choose_groups(a, v, lane, shift);
 #pragma unroll
-    for (int i = 0; i < IPL; ++i) {
-        const int e = lane * IPL + i, ge = static_cast<int>((static_cast<uint32_t>(e) * a.per_magic) >> 20);
-        c[i] = (in_lanes ? stays : (e < a.E && (stay >> (ge << shift) & 1u))) ? c[i] : -INFINITY;
+    for (int q = 0; q < Q; ++q) {
+        if (!direct && v.most[q] != 0u) {
+            const float least = plain_value(v.least[q]), open = 2.0f * sm[q].open + fabsf(least) * 0x1p-21f;
+            if (!(least - plain_value(v.most[q]) > open)) {
+                if (a.softmax)
+                    sure[q] = false;
+                else
+                    v.stays[q] = group_stays_exactly<T>(a, l + q * a.ld, v.own[q], v.stays[q], v.least[q], v.most[q], open, seen, lane, shift);
+            }
+        }
+        const uint32_t stay = __ballot_sync(ALL, v.stays[q]);
+#pragma unroll
+        for (int i = 0; i < IPL; ++i) {
+            const int e = lane * IPL + i, ge = static_cast<int>((static_cast<uint32_t>(e) * a.per_magic) >> 20);
+            c[q][i] = (in_lanes ? v.stays[q] : (e < a.E && (stay >> (ge << shift) & 1u))) ? c[q][i] : -INFINITY;
+        }
     }
-    return sure;
 }
 
 // Without a bias scores are in the order of the logits, which are exact.
@@ -283,14 +310,18 @@ __device__ __noinline__ int choose_exactly(const ScoreArgs &a, const T *l, uint6
     }
     __syncwarp();
     if (a.groups > 1) {
-        uint64_t first = 0, second = 0, least, most, own;
+        Groups<uint64_t, 1> v;
+        uint64_t first = 0, second = 0;
         const int g = lane >> a.shift;
         if (g < a.groups)
 #pragma unroll 2
             for (int e = lane & (a.lanes - 1); e < a.per; e += a.lanes)
                 insert(seen[spot(g * a.per + e)], first, second);
-        merge_lanes(first, second, a.lanes);
-        const uint32_t stay = __ballot_sync(ALL, group_stays(a, first, second, lane, a.shift, least, most, own));
+        v.first[0] = first;
+        v.second[0] = second;
+        merge_lanes(v, a.lanes);
+        choose_groups(a, v, lane, a.shift);
+        const uint32_t stay = __ballot_sync(ALL, v.stays[0]);
         for (int e = lane; e < a.E; e += 32)
             if (!(stay >> (static_cast<int>((static_cast<uint32_t>(e) * a.per_magic) >> 20) << a.shift) & 1u))
                 seen[spot(e)] = 0;
@@ -424,49 +455,49 @@ __device__ __forceinline__ float logistic(float l)
     return s;
 }
 
-// What a token's softmax is taken with, and how near two values of c are open (beside 2^-22 of their size).
-struct Softmax {
-    float top, total, open;
-};
-
-// A token's c from its logits and the biases, without those of the groups that do not stay (false: see keep_groups).
-template <typename T, int IPL>
-__device__ __forceinline__ bool make_c(const ScoreArgs &a, const T *l, float (&f)[IPL], const float (&b)[IPL], bool direct, uint64_t *seen,
-                                       int lane, Softmax &sm)
+// The c of Q tokens, from row l on, from their logits and the biases, without those of the groups that do not stay.
+template <typename T, int IPL, int Q>
+__device__ __forceinline__ void make_c(const ScoreArgs &a, const T *l, float (&f)[Q][IPL], const float (&b)[IPL], bool direct, uint64_t *seen,
+                                       int lane, Softmax (&sm)[Q], bool (&sure)[Q])
 {
-    sm = {0.0f, 1.0f, 0.0f};
-    if (a.softmax && !(direct && a.renorm)) {
-        sm.top = f[0];
 #pragma unroll
-        for (int i = 1; i < IPL; ++i)
-            sm.top = fmaxf(sm.top, f[i]);
-        sm.top = warp_max_f(sm.top);
-        float total = 0.0f;
+    for (int q = 0; q < Q; ++q) {
+        sm[q] = {0.0f, 1.0f, 0.0f};
+        sure[q] = true;
+        if (a.softmax && !(direct && a.renorm)) {
+            float top = f[q][0], total = 0.0f;
 #pragma unroll
-        for (int i = 0; i < IPL; ++i)
-            if (lane * IPL + i < a.E)
-                total += expf(f[i] - sm.top);
-        sm.total = warp_sum(total);
-    }
-    if (direct) {
+            for (int i = 1; i < IPL; ++i)
+                top = fmaxf(top, f[q][i]);
+            top = warp_max_f(top);
 #pragma unroll
-        for (int i = 0; i < IPL; ++i)
-            f[i] += 0.0f;   // (-0 as +0)
-    } else {
-        // Errors of c in units of 2^-24: the sigmoid's exponential (1.3 |l| + 2.8) times s (1 - s), at most 1, its
-        // sum 1/2, the reciprocal 2; softmax (times 1/total, the largest probability) 8 of the two exponentials and
-        // quotients, ln E of the exponents' roundings and 1/2 for each of the sum's IPL + 5 additions.  Twice that
-        // for two values.
-        sm.open = a.softmax ? (2.0f * IPL + 72.0f) * 0x1p-24f / sm.total : 0x1p-21f;
-        const float inv = 1.0f / sm.total;
+            for (int i = 0; i < IPL; ++i)
+                if (lane * IPL + i < a.E)
+                    total += expf(f[q][i] - top);
+            sm[q].top = top;
+            sm[q].total = warp_sum(total);
+        }
+        if (direct) {
 #pragma unroll
-        for (int i = 0; i < IPL; ++i) {
-            const float s = a.softmax ? expf(f[i] - sm.top) * inv : logistic(f[i]);
-            // (the sum is of no account but for a logit of -inf)
-            f[i] = fminf(a.bias ? s + b[i] : s, f[i] + 3e38f);
+            for (int i = 0; i < IPL; ++i)
+                f[q][i] += 0.0f;   // (-0 as +0)
+        } else {
+            // Errors of c in units of 2^-24: the sigmoid's exponential (1.3 |l| + 2.8) times s (1 - s), at most 1, its
+            // sum 1/2, the reciprocal 2; softmax (times 1/total, the largest probability) 8 of the two exponentials and
+            // quotients, ln E of the exponents' roundings and 1/2 for each of the sum's IPL + 5 additions.  Twice that
+            // for two values.
+            sm[q].open = a.softmax ? (2.0f * IPL + 72.0f) * 0x1p-24f / sm[q].total : 0x1p-21f;
+            const float inv = 1.0f / sm[q].total;
+#pragma unroll
+            for (int i = 0; i < IPL; ++i) {
+                const float s = a.softmax ? expf(f[q][i] - sm[q].top) * inv : logistic(f[q][i]);
+                // (the sum is of no account but for a logit of -inf)
+                f[q][i] = fminf(a.bias ? s + b[i] : s, f[q][i] + 3e38f);
+            }
         }
     }
-    return a.groups == 1 || keep_groups<T, IPL>(a, l, f, seen, lane, direct ? -1.0f : sm.open);
+    if (a.groups > 1)
+        keep_groups<T, IPL, Q>(a, l, f, sm, direct, seen, lane, sure);
 }
 template <int IPL, bool FIXED>
 __device__ __forceinline__ void make_words(uint32_t (&word)[IPL], const float (&c)[IPL], int lane)
@@ -490,16 +521,17 @@ __device__ __noinline__ int choose_again(const ScoreArgs &a, const T *l, uint64_
 {
     const bool direct = directly(a);
     if (!a.softmax || direct) {
-        float f[IPL], b[IPL];
-        load_lane<T, IPL>(f, l, lane, a.E, a.vec);
+        float f[1][IPL], b[IPL];
+        load_lane<T, IPL>(f[0], l, lane, a.E, a.vec);
         if (a.bias)
             load_lane<float, IPL>(b, a.bias, lane, a.E, a.bias_vec);
         uint32_t word[IPL], mine = 0u, last = 0u;
-        Softmax sm;
-        bool whole = false;
+        Softmax sm[1];
+        bool whole = false, sure[1];
         int n = 0;
-        if (make_c<T, IPL>(a, l, f, b, direct, seen, lane, sm)) {
-            make_words<IPL, FIXED>(word, f, lane);
+        make_c<T, IPL, 1>(a, l, f, b, direct, seen, lane, sm, sure);
+        if (sure[0]) {
+            make_words<IPL, FIXED>(word, f[0], lane);
             while (!whole && n < 32) {
                 const uint32_t m = take_largest<IPL>(word);
                 whole = m <= NO_WORD<IPL, FIXED>;
@@ -507,7 +539,7 @@ __device__ __noinline__ int choose_again(const ScoreArgs &a, const T *l, uint64_
                     mine = lane == n ? m : mine;
                     last = n == a.k - 1 ? m : last;
                     ++n;
-                    whole = n > a.k && apart<IPL, FIXED>(last, m, sm.open, direct);
+                    whole = n > a.k && apart<IPL, FIXED>(last, m, sm[0].open, direct);
                 }
             }
         }
@@ -541,8 +573,9 @@ __device__ __forceinline__ float seg_max(float v)
     return v;
 }
 
-// A warp takes Q tokens: it chooses for one after the other, with all lanes, and then has the slots of all
-// of them, a lane each (SEG = 32/Q >= k lanes a token), for the weights and what is to be checked.
+// A warp takes Q tokens: it chooses for each with all lanes, side by side (a token's warp maxima wait for one
+// another), and then has the slots of all of them, a lane each (SEG = 32/Q >= k lanes a token), for the
+// weights and what is to be checked.
 template <typename T, int IPL, int Q, bool FIXED>
 __device__ __forceinline__ void score_tokens(const ScoreArgs &a, const float (&b)[IPL], uint64_t *seen, int t0, int lane)
 {
@@ -554,40 +587,47 @@ __device__ __forceinline__ void score_tokens(const ScoreArgs &a, const float (&b
     const uint32_t lanes = __ballot_sync(ALL, slot == 0 && t < a.T && (!a.mask || a.mask[t]));
     float f[Q][IPL];
 #pragma unroll
-    for (int q = 0; q < Q; ++q)
+    for (int q = 0; q < Q; ++q) {
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+            f[q][i] = 0.0f;
         if (lanes >> (q * SEG) & 1u)
             load_lane<T, IPL>(f[q], row(q), lane, a.E, a.vec);
-    // this lane's token: how many are found, the words of the slot, of the last and of the one after it
-    int found = 0;
+    }
+    uint32_t word[Q][IPL], largest[Q];
+    Softmax its[Q];
+    bool its_sure[Q];
+    make_c<T, IPL, Q>(a, row(0), f, b, direct, seen, lane, its, its_sure);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        make_words<IPL, FIXED>(word[q], f[q], lane);
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)   // a token that is not routed has none
+            word[q][i] = lanes >> (q * SEG) & 1u ? word[q][i] : 0u;
+    }
+    // this lane's token: the words of the slot, of the last and of the one after it, how many are found
     uint32_t mine = 0u, next = 0u, last = 0u;
+    for (int n = 0; n < a.k; ++n) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            largest[q] = take_largest<IPL>(word[q]);
+            mine = lane == q * SEG + n ? largest[q] : mine;
+        }
+    }
     Softmax sm{0.0f, 1.0f, 0.0f};
     bool sure = true;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-        if (!(lanes >> (q * SEG) & 1u))
-            continue;
-        uint32_t word[IPL], m = 0u, after = 0u;
-        Softmax its;
-        const bool its_sure = make_c<T, IPL>(a, row(q), f[q], b, direct, seen, lane, its);
-        make_words<IPL, FIXED>(word, f[q], lane);
-        int n = 0;
-        for (; n < a.k; ++n) {
-            const uint32_t largest = take_largest<IPL>(word);
-            if (largest <= NO_WORD<IPL, FIXED>)
-                break;   // only what is never chosen is left
-            m = largest;
-            mine = lane == q * SEG + n ? m : mine;
-        }
-        if (!(direct && sizeof(T) == 2) && n == a.k)
-            after = take_largest<IPL>(word);
+        const uint32_t after = direct && sizeof(T) == 2 ? 0u : take_largest<IPL>(word[q]);
         if (seg == q) {
-            found = n;
-            last = m;
+            last = largest[q];
             next = after;
-            sm = its;
-            sure = its_sure;
+            sm = its[q];
+            sure = its_sure[q] || !(lanes >> (q * SEG) & 1u);
         }
     }
+    // (what is never chosen comes last)
+    int found = __popc(__ballot_sync(ALL, mine > NO_WORD<IPL, FIXED>) >> (seg * SEG) & (SEG == 32 ? ALL : (1u << (SEG & 31)) - 1u));
     const T *l = static_cast<const T *>(a.logits) + static_cast<size_t>(t) * a.ld;
     int my_idx = slot < found ? expert_of<IPL>(mine) : -1;
     float logit, e, s;   // of the lane's slot: its logit, exp(-|logit|), its score
