@@ -4,7 +4,14 @@
 //   h = x + r (rounded to their type: it is the residual stream), rstd = 1/sqrt(sum(h^2)/H + eps), y = h rstd g
 //   a = dy g, xh = h rstd:  dx = dh + rstd (a - xh mean(a xh))  (of x and of r alike),  dg = sum_t dy xh
 //
-// Bound by HBM: every row is read once into registers and its sum of squares held in fp32.
+// Bound by HBM: every row is read once into registers and its sum of squares held in fp32.  Long batches run in
+// persistent blocks that copy the rows ahead into shared memory, as the layer norm's do; short rows go one a warp,
+// and rows off 16-byte boundaries in aligned packs whose lead a block's rows share.
+//
+// Measured on a GB300 in graphs, floors by bytes at the measured copy bandwidth in brackets: bf16 16384 x 4096 with the
+// residual forward 88 us (80), backward with dh 84 (80), FP8 form 82 (70); without either 47 and 70 (40, 60); fp16 6001
+// x 2003 15.7 and 22 (14.4 and 14.4; x 2008 15.6 and 20.9), of which the columns' sums are 4; 128 x 7168 FP8 form 3.2; over
+// 8192 columns the backward pass spills (2000 x 8191 bf16 45, floor 20).
 #include "norm_rows.cuh"
 
 using namespace cpw;
