@@ -225,11 +225,11 @@ struct Softmax {
     float top, total, open;
 };
 
-// -inf in place of the c of the groups that do not stay, of Q tokens from row l on.  sure[q] is false where scores
-// are softmax and which groups stay is in doubt.
+// -inf in place of the c of the groups that do not stay, of Q tokens from row l on (there: routed[q]).  sure[q] is
+// false where scores are softmax and which groups stay is in doubt.
 template <typename T, int IPL, int Q>
-__device__ __forceinline__ void keep_groups(const ScoreArgs &a, const T *l, float (&c)[Q][IPL], const Softmax (&sm)[Q], bool direct, uint64_t *seen,
-                                            int lane, bool (&sure)[Q])
+__device__ __forceinline__ void keep_groups(const ScoreArgs &a, const T *l, const bool (&routed)[Q], float (&c)[Q][IPL], const Softmax (&sm)[Q],
+                                            bool direct, uint64_t *seen, int lane, bool (&sure)[Q])
 {
     Groups<uint32_t, Q> v;
     const bool in_lanes = a.group_shift >= 0;   // a group is 1 << group_shift lanes
@@ -261,7 +261,7 @@ __device__ __forceinline__ void keep_groups(const ScoreArgs &a, const T *l, floa
     choose_groups(a, v, lane, shift);
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-        if (!direct && v.most[q] != 0u) {
+        if (routed[q] && !direct && v.most[q] != 0u) {
             const float least = plain_value(v.least[q]), open = 2.0f * sm[q].open + fabsf(least) * 0x1p-21f;
             if (!(least - plain_value(v.most[q]) > open)) {
                 if (a.softmax)
@@ -462,9 +462,10 @@ __device__ __forceinline__ float logistic(float l)
 }
 
 // The c of Q tokens, from row l on, from their logits and the biases, without those of the groups that do not stay.
+// Of tokens that are not routed, or not there, nothing is read.
 template <typename T, int IPL, int Q>
-__device__ __forceinline__ void make_c(const ScoreArgs &a, const T *l, float (&f)[Q][IPL], const float (&b)[IPL], bool direct, uint64_t *seen,
-                                       int lane, Softmax (&sm)[Q], bool (&sure)[Q])
+__device__ __forceinline__ void make_c(const ScoreArgs &a, const T *l, const bool (&routed)[Q], float (&f)[Q][IPL], const float (&b)[IPL],
+                                       bool direct, uint64_t *seen, int lane, Softmax (&sm)[Q], bool (&sure)[Q])
 {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
@@ -503,7 +504,7 @@ __device__ __forceinline__ void make_c(const ScoreArgs &a, const T *l, float (&f
         }
     }
     if (a.groups > 1)
-        keep_groups<T, IPL, Q>(a, l, f, sm, direct, seen, lane, sure);
+        keep_groups<T, IPL, Q>(a, l, routed, f, sm, direct, seen, lane, sure);
 }
 template <int IPL, bool FIXED>
 __device__ __forceinline__ void make_words(uint32_t (&word)[IPL], const float (&c)[IPL], int lane)
@@ -534,8 +535,9 @@ __device__ __noinline__ int choose_again(const ScoreArgs &a, const T *l, uint64_
         uint32_t word[IPL], mine = 0u, last = 0u;
         Softmax sm[1];
         bool whole = false, sure[1];
+        const bool routed[1] = {true};
         int n = 0;
-        make_c<T, IPL, 1>(a, l, f, b, direct, seen, lane, sm, sure);
+        make_c<T, IPL, 1>(a, l, routed, f, b, direct, seen, lane, sm, sure);
         if (sure[0]) {
             make_words<IPL, FIXED>(word, f[0], lane);
             while (!whole && n < 32) {
@@ -588,28 +590,30 @@ __device__ __forceinline__ void score_tokens(const ScoreArgs &a, const float (&b
     constexpr int SEG = 32 / Q;
     const int seg = lane / SEG, slot = lane % SEG, t = t0 + seg;
     const bool direct = !FIXED && directly(a);
-    // token q's row, by all lanes; bit q * SEG: it is routed
+    // token q's row, by all lanes; whether it is there and routed
     const auto row = [&](int q) { return static_cast<const T *>(a.logits) + static_cast<size_t>(t0 + q) * a.ld; };
     const uint32_t lanes = __ballot_sync(ALL, slot == 0 && t < a.T && (!a.mask || a.mask[t]));
+    bool routed[Q];
     float f[Q][IPL];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
+        routed[q] = lanes >> (q * SEG) & 1u;
 #pragma unroll
         for (int i = 0; i < IPL; ++i)
             f[q][i] = 0.0f;
-        if (lanes >> (q * SEG) & 1u)
+        if (routed[q])
             load_lane<T, IPL>(f[q], row(q), lane, a.E, a.vec);
     }
     uint32_t word[Q][IPL], largest[Q];
     Softmax its[Q];
     bool its_sure[Q];
-    make_c<T, IPL, Q>(a, row(0), f, b, direct, seen, lane, its, its_sure);
+    make_c<T, IPL, Q>(a, row(0), routed, f, b, direct, seen, lane, its, its_sure);
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         make_words<IPL, FIXED>(word[q], f[q], lane);
 #pragma unroll
         for (int i = 0; i < IPL; ++i)   // a token that is not routed has none
-            word[q][i] = lanes >> (q * SEG) & 1u ? word[q][i] : 0u;
+            word[q][i] = routed[q] ? word[q][i] : 0u;
     }
     // this lane's token: the words of the slot, of the last and of the one after it, how many are found
     uint32_t mine = 0u, next = 0u, last = 0u;
@@ -629,7 +633,7 @@ __device__ __forceinline__ void score_tokens(const ScoreArgs &a, const float (&b
             last = largest[q];
             next = after;
             sm = its[q];
-            sure = its_sure[q] || !(lanes >> (q * SEG) & 1u);
+            sure = its_sure[q];
         }
     }
     // (what is never chosen comes last)

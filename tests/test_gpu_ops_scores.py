@@ -24,6 +24,11 @@ def _scores(l, score):
     return p / p.sum(1, keepdim=True)
 
 
+def _ordered(c):
+    """NaN as one value, the largest: a sort goes by its bits, the sign among them."""
+    return torch.sort(c.masked_fill(c.isnan(), float("nan")), dim=-1, descending=True, stable=True)
+
+
 def _choice(l, k, score, bias, groups, kept, top):
     T, E = l.shape
     c = _scores(l, score)
@@ -31,13 +36,13 @@ def _choice(l, k, score, bias, groups, kept, top):
         c = c + bias.double()
     c = torch.where(l == -float("inf"), -float("inf"), c)
     if kept < groups:
-        v = torch.sort(c.view(T, groups, -1), dim=2, descending=True).values[:, :, :top]
+        v = _ordered(c.view(T, groups, -1)).values[:, :, :top]
         # fewer than `top` candidates: the sum of those there are
         g = torch.where(v[:, :, :1].isneginf().squeeze(2), -float("inf"), v.masked_fill(v.isneginf(), 0.0).sum(2))
-        order = torch.sort(g, dim=1, descending=True, stable=True).indices[:, :kept]
+        order = _ordered(g).indices[:, :kept]
         stays = torch.zeros_like(g, dtype=torch.bool).scatter_(1, order, True) & ~g.isneginf()
         c = torch.where(stays[:, :, None], c.view(T, groups, -1), -float("inf")).view(T, E)
-    v, idx = torch.sort(c, dim=1, descending=True, stable=True)
+    v, idx = _ordered(c)
     return torch.where(v[:, :k].isneginf(), -1, idx[:, :k])
 
 
@@ -260,3 +265,32 @@ def test_large_logits_without_a_bias_are_in_their_own_order(k):
         idx, w = ops.route_scores(v, k)
         assert torch.equal(idx, torch.sort(v, dim=1, descending=True, stable=True).indices[:, :k])
         assert ((w - 1.0 / k).abs() <= 8 * E24).all()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,k,groups,kept", [(64, 1, 1, 1), (64, 6, 1, 1), (64, 6, 8, 3), (72, 9, 3, 1), (512, 32, 16, 5)])
+def test_biases_and_logits_that_are_no_ordinary_numbers(score, E, k, groups, kept):
+    """A NaN is the largest and an infinite or huge bias takes its place in the order, as in 64 bits; the tail of a batch whose
+    groups are all equal, and tokens that are masked, are left alone."""
+    inf, nan = float("inf"), float("nan")
+    l = _logits(6145, E, torch.float32)
+    l[1, 3] = nan
+    l[2, 40] = inf
+    l[3, 5:9] = -nan
+    l[4, ::2] = -inf
+    l[4, 1] = nan
+    l[5, 60], l[5, 61] = inf, nan
+    l[6] = nan
+    l[7] = inf
+    plain = _bias(E)
+    for at in ({}, {7: nan}, {9: inf}, {9: inf, 40: inf, 50: nan}, {9: 3.4e38, 10: 3.2e38, 30: inf, 63: 3.3e38}, {3: -inf, 5: nan, 40: -3.4e38}):
+        b = plain.clone()
+        for e, v in at.items():
+            b[e] = v
+        for rows in (l[:40], l):
+            idx, _ = ops.route_scores(rows, k, score=score, bias=b, groups=groups, topk_groups=kept)
+            assert torch.equal(idx, _choice(rows, k, score, b, groups, kept, 2))
+    mask = torch.arange(6145, device="cuda") % 3 != 0
+    same = torch.zeros(6145, E, device="cuda")
+    for b in (None, torch.zeros(E, device="cuda")):
+        _check(same, k, score, b, groups, kept, mask=mask)
