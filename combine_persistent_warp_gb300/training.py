@@ -266,8 +266,8 @@ class MoEBlock(nn.Module):
         super().__init__()
         if norm not in ("layer", "rms"):
             raise ValueError(f"norm: {norm!r} is not 'layer' or 'rms'")
-        if score is None and (groups != 1 or not renormalize or scale != 1.0 or balance):
-            raise ValueError("groups, renormalize, scale and balance need a score")
+        if score is None and (groups != 1 or topk_groups is not None or group_top != 2 or not renormalize or scale != 1.0 or balance):
+            raise ValueError("groups, topk_groups, group_top, renormalize, scale and balance need a score")
         self.E, self.H, self.I, self.topk, self.eps = E, H, I, topk, eps
         self.norm, self.checkpoint = norm, checkpoint
         self.routing = None if score is None else dict(score=score, groups=groups, topk_groups=topk_groups, group_top=group_top,
@@ -281,6 +281,14 @@ class MoEBlock(nn.Module):
         self.w_down = p(E, H, I)
         self.register_buffer("balance_bias", torch.zeros(E, dtype=torch.float32) if balance else None)
         self.register_buffer("load", torch.zeros(E, dtype=torch.int64) if balance else None, persistent=False)
+
+    def _apply(self, fn, recurse=True):
+        # the biases move by less than a step of 16-bit numbers: a change of the block's type leaves them in fp32
+        exact = self.balance_bias
+        super()._apply(fn, recurse)
+        if exact is not None and self.balance_bias.dtype != exact.dtype:
+            self.balance_bias = exact.to(self.balance_bias.device)
+        return self
 
     def _route(self, h, token_mask, choose, choose_scores):
         logits = h @ self.router.t()

@@ -148,3 +148,22 @@ def test_balance_moves_against_the_loads():
     block.load += torch.tensor([10, 0, 5, 5])
     block.update_balance(0.5)
     assert block.balance_bias.tolist() == [-0.5, 0.5, 0.0, 0.0] and not block.load.any()
+
+
+def test_a_change_of_type_leaves_the_biases_as_they_are():
+    block = training.MoEBlock(4, 32, 32, 2, score="sigmoid", balance=True)
+    block.balance_bias += torch.tensor([1.001, -0.002, 0.0, 1e-9])
+    kept = block.balance_bias.clone()
+    for change in (lambda: block.half(), lambda: block.to(torch.bfloat16), lambda: block.float().bfloat16(), lambda: block.to("cpu")):
+        change()
+        assert block.balance_bias.dtype == torch.float32 and torch.equal(block.balance_bias, kept)
+        assert block.load.dtype == torch.int64 and block.balance_bias is dict(block.named_buffers())["balance_bias"]
+    assert block.router.dtype == torch.bfloat16
+    assert torch.equal(block.state_dict()["balance_bias"], kept)
+    training.MoEBlock(4, 32, 32, 2).half()
+
+
+@pytest.mark.parametrize("options", [dict(topk_groups=1), dict(group_top=1), dict(groups=2), dict(renormalize=False), dict(scale=2.0), dict(balance=True)])
+def test_options_of_the_scores_need_them(options):
+    with pytest.raises(ValueError, match="need a score"):
+        training.MoEBlock(4, 32, 32, 2, **options)

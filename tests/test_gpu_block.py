@@ -9,6 +9,7 @@ the values'; gate, up and the down products' rows in quadrature 2%, inside the 1
 """
 import os
 import sys
+import threading
 
 import pytest
 import torch
@@ -211,3 +212,49 @@ def test_example_trains_and_serves():
     assert all(p.grad is not None and p.grad.isfinite().all() for p in block.parameters())
     assert block.balance_bias.any()
     assert ex.serve(block, tokens=256) < 0.15     # (FP8 operands, as above)
+
+
+def test_empty_batch():
+    block = training.MoEBlock(4, 64, 64, 2, std=0.1, **dict(FORMS["all"], groups=2, topk_groups=1)).cuda()
+    x, r = (torch.randn(0, 64, device="cuda", dtype=torch.bfloat16, requires_grad=True) for _ in range(2))
+    for mask in (None, torch.ones(0, dtype=torch.bool, device="cuda")):
+        out = block(x, mask, residual=r)
+        assert out.shape == (0, 64)
+        out.sum().backward()
+    assert x.grad.shape == r.grad.shape == (0, 64) and not block.load.any()
+    assert all(p.grad is not None and not p.grad.any() for p in block.parameters())
+
+
+def test_two_threads_on_their_own_streams():
+    """Steps of two blocks side by side give the bits that each gives alone."""
+    torch.manual_seed(10)
+    blocks = [training.MoEBlock(8, 256, 136, 2, std=0.1, **dict(FORMS["all"], topk_groups=2)).cuda() for _ in range(2)]
+    data = [(torch.randn(T, 256, device="cuda").bfloat16(), torch.randn(T, 256, device="cuda").bfloat16()) for T in (300, 1111)]
+
+    def step(i):
+        x, r = (t.clone().requires_grad_() for t in data[i])
+        blocks[i].zero_grad(set_to_none=True)
+        out = blocks[i](x, residual=r)
+        out.backward(data[i][1])
+        return [out.detach(), x.grad, *(p.grad for p in blocks[i].parameters())]
+
+    alone = [step(i) for i in range(2)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(10):
+                    got = step(i)
+                    torch.cuda.current_stream().synchronize()
+                    wrong.extend((i, n) for n, (a, b) in enumerate(zip(got, alone[i])) if not torch.equal(a, b))
+        except Exception as e:
+            wrong.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
