@@ -581,6 +581,66 @@ __device__ __forceinline__ float seg_max(float v)
     return v;
 }
 
+// The lanes of a token.
+template <int Q>
+constexpr uint32_t SLOTS = Q == 1 ? ALL : (1u << (32 / Q)) - 1u;
+
+// The tokens of the lanes `open`, whose order or last place is: if what the words leave out is below the last slot, or is
+// with the exception of the one after it, the slots (and that one) by their values in 64 bits.  Returns
+// the lanes of the tokens of which more is in doubt.
+template <typename T, int IPL, int Q, bool FIXED>
+__device__ __forceinline__ uint32_t rank_again(const ScoreArgs &a, const T *l, uint32_t (&word)[Q][IPL], uint32_t last, uint32_t next, bool sure,
+                                               bool edge, bool in_order, float gap, uint32_t open, int found, float logit, float bias,
+                                               int &my_idx, int lane)
+{
+    constexpr int SEG = 32 / Q;
+    const int seg = lane / SEG, slot = lane % SEG;
+    const bool direct = !FIXED && directly(a);
+    if (a.softmax && !direct)
+        return open;
+    uint32_t third = 0u;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const uint32_t m = take_largest<IPL>(word[q]);
+        third = seg == q ? m : third;
+    }
+    const bool more = !edge && (third <= NO_WORD<IPL, FIXED> || apart<IPL, FIXED>(last, third, gap, direct));
+    const bool mine = (open >> (seg * SEG) & SLOTS<Q>) && sure && (edge || more);
+    const uint32_t ranked = __ballot_sync(ALL, mine);
+    const int x = mine && more ? expert_of<IPL>(next) : -1;
+    const float x_logit = x >= 0 ? to_f<T>(l[x]) : 0.0f, x_bias = x >= 0 && a.bias ? a.bias[x] : 0.0f;
+    // the last slot and the one after it are often equal in what their values are computed from
+    const float last_logit = __shfl_sync(ALL, logit, a.k - 1, SEG), last_bias = __shfl_sync(ALL, bias, a.k - 1, SEG);
+    const int last_idx = __shfl_sync(ALL, my_idx, a.k - 1, SEG);
+    const bool equal = last_logit == x_logit && last_bias == x_bias && last_idx < x;
+    if (__any_sync(ALL, mine && !(in_order && (edge || equal)))) {
+        const bool there = mine && slot < found;
+        uint64_t key = 0, its_key = 0;
+        if (direct) {
+            key = order_key(static_cast<double>(logit));
+            its_key = order_key(static_cast<double>(x_logit));
+        } else {
+            key = exact_key(logit, bias, a.bias);
+            if (__any_sync(ALL, x >= 0))
+                its_key = exact_key(x_logit, x_bias, a.bias);
+        }
+        int rank = x >= 0 && (its_key > key || (its_key == key && x < my_idx)), its_rank = 0;
+        for (int r = 0; r < a.k; ++r) {
+            const uint64_t other = __shfl_sync(ALL, key, r, SEG);
+            const int its = __shfl_sync(ALL, my_idx, r, SEG);
+            rank += its >= 0 && (other > key || (other == key && its < my_idx));
+            its_rank += other > its_key || (other == its_key && its < x);
+        }
+        int got = x >= 0 && its_rank == slot ? x : -1;
+        for (int r = 0; r < a.k; ++r) {
+            const int at = __shfl_sync(ALL, rank, r, SEG), its = __shfl_sync(ALL, my_idx, r, SEG);
+            got = its >= 0 && at == slot ? its : got;
+        }
+        my_idx = there ? got : my_idx;
+    }
+    return open & ~ranked;
+}
+
 // A warp takes Q tokens: it chooses for each with all lanes, side by side (a token's warp maxima wait for one
 // another), and then has the slots of all of them, a lane each (SEG = 32/Q >= k lanes a token), for the
 // weights and what is to be checked.
@@ -637,7 +697,7 @@ __device__ __forceinline__ void score_tokens(const ScoreArgs &a, const float (&b
         }
     }
     // (what is never chosen comes last)
-    int found = __popc(__ballot_sync(ALL, mine > NO_WORD<IPL, FIXED>) >> (seg * SEG) & (SEG == 32 ? ALL : (1u << (SEG & 31)) - 1u));
+    int found = __popc(__ballot_sync(ALL, mine > NO_WORD<IPL, FIXED>) >> (seg * SEG) & SLOTS<Q>);
     const T *l = static_cast<const T *>(a.logits) + static_cast<size_t>(t) * a.ld;
     int my_idx = slot < found ? expert_of<IPL>(mine) : -1;
     float logit, e, s;   // of the lane's slot: its logit, exp(-|logit|), its score
@@ -659,13 +719,15 @@ __device__ __forceinline__ void score_tokens(const ScoreArgs &a, const float (&b
         const float after = __shfl_down_sync(ALL, c, 1), after_logit = __shfl_down_sync(ALL, logit, 1);
         const float after_bias = __shfl_down_sync(ALL, bias, 1);
         const int after_idx = __shfl_down_sync(ALL, my_idx, 1);
-        bool ok = sure && (next <= NO_WORD<IPL, FIXED> || apart<IPL, FIXED>(last, next, sm.open, direct));
+        const bool edge = next <= NO_WORD<IPL, FIXED> || apart<IPL, FIXED>(last, next, sm.open, direct);
+        bool ok = true;
         if (slot + 1 < found)
-            ok = ok && (c - after > sm.open + (direct ? 0.0f : fabsf(c) * 0x1p-22f) ||
-                        (logit == after_logit && bias == after_bias && my_idx < after_idx));
-        uint32_t open = __ballot_sync(ALL, !ok);
+            ok = c - after > sm.open + (direct ? 0.0f : fabsf(c) * 0x1p-22f) ||
+                 (logit == after_logit && bias == after_bias && my_idx < after_idx);
+        uint32_t open = __ballot_sync(ALL, !(ok && sure && edge));
         if (open) {
-            do {
+            open = rank_again<T, IPL, Q, FIXED>(a, l, word, last, next, sure, edge, ok, sm.open, open, found, logit, bias, my_idx, lane);
+            while (open) {
                 const int q = (__ffs(static_cast<int>(open)) - 1) / SEG;
                 int idx;
                 const int n = choose_again<T, IPL, FIXED>(a, row(q), seen, lane, idx);
@@ -674,8 +736,8 @@ __device__ __forceinline__ void score_tokens(const ScoreArgs &a, const float (&b
                     found = n;
                     my_idx = slot < n ? idx : -1;
                 }
-                open &= ~((SEG == 32 ? ALL : (1u << (SEG & 31)) - 1u) << (q * SEG));
-            } while (open);
+                open &= ~(SLOTS<Q> << (q * SEG));
+            }
             look();
         }
     }
