@@ -585,35 +585,47 @@ __device__ __forceinline__ float seg_max(float v)
 template <int Q>
 constexpr uint32_t SLOTS = Q == 1 ? ALL : (1u << (32 / Q)) - 1u;
 
-// The tokens of the lanes `open`, whose order or last place is: if what the words leave out is below the last slot, or is
-// with the exception of the one after it, the slots (and that one) by their values in 64 bits.  Returns
-// the lanes of the tokens of which more is in doubt.
+// The tokens of the lanes `open`, whose order or last place is in doubt.  What the words leave out, from the one after
+// the last slot on, is below the last slot, or is equal to it in what it is computed from and a later
+// expert (with all slots in order the last is the lowest: it stays out then), but for one at most: then the slots
+// and that one are ranked by their values in 64 bits.  Returns the lanes of the tokens of which more is in doubt.
 template <typename T, int IPL, int Q, bool FIXED>
 __device__ __forceinline__ uint32_t rank_again(const ScoreArgs &a, const T *l, uint32_t (&word)[Q][IPL], uint32_t last, uint32_t next, bool sure,
-                                               bool edge, bool in_order, float gap, uint32_t open, int found, float logit, float bias,
-                                               int &my_idx, int lane)
+                                               bool in_order, float gap, uint32_t open, int found, float logit, float bias, int &my_idx,
+                                               int lane)
 {
     constexpr int SEG = 32 / Q;
     const int seg = lane / SEG, slot = lane % SEG;
     const bool direct = !FIXED && directly(a);
     if (a.softmax && !direct)
         return open;
-    uint32_t third = 0u;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        const uint32_t m = take_largest<IPL>(word[q]);
-        third = seg == q ? m : third;
-    }
-    const bool more = !edge && (third <= NO_WORD<IPL, FIXED> || apart<IPL, FIXED>(last, third, gap, direct));
-    const bool mine = (open >> (seg * SEG) & SLOTS<Q>) && sure && (edge || more);
-    const uint32_t ranked = __ballot_sync(ALL, mine);
-    const int x = mine && more ? expert_of<IPL>(next) : -1;
-    const float x_logit = x >= 0 ? to_f<T>(l[x]) : 0.0f, x_bias = x >= 0 && a.bias ? a.bias[x] : 0.0f;
-    // the last slot and the one after it are often equal in what their values are computed from
+    const uint32_t unordered = __ballot_sync(ALL, !in_order) >> (seg * SEG) & SLOTS<Q>;
     const float last_logit = __shfl_sync(ALL, logit, a.k - 1, SEG), last_bias = __shfl_sync(ALL, bias, a.k - 1, SEG);
     const int last_idx = __shfl_sync(ALL, my_idx, a.k - 1, SEG);
-    const bool equal = last_logit == x_logit && last_bias == x_bias && last_idx < x;
-    if (__any_sync(ALL, mine && !(in_order && (edge || equal)))) {
+    bool mine = (open >> (seg * SEG) & SLOTS<Q>) && sure;
+    int x = -1;   // the one more
+    float x_logit = 0.0f, x_bias = 0.0f;
+    for (;;) {
+        const bool more = mine && next > NO_WORD<IPL, FIXED> && !apart<IPL, FIXED>(last, next, gap, direct);
+        if (more) {
+            const int e = expert_of<IPL>(next);
+            const float e_logit = to_f<T>(l[e]), e_bias = a.bias ? a.bias[e] : 0.0f;
+            if (unordered || e_logit != last_logit || e_bias != last_bias || e < last_idx) {
+                mine = x < 0;
+                x = e, x_logit = e_logit, x_bias = e_bias;
+            }
+        }
+        if (!__any_sync(ALL, more && mine))
+            break;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const uint32_t m = take_largest<IPL>(word[q]);
+            next = seg == q ? m : next;
+        }
+    }
+    x = mine ? x : -1;
+    const uint32_t ranked = __ballot_sync(ALL, mine);
+    if (__any_sync(ALL, mine && (unordered || x >= 0))) {
         const bool there = mine && slot < found;
         uint64_t key = 0, its_key = 0;
         if (direct) {
@@ -726,7 +738,7 @@ __device__ __forceinline__ void score_tokens(const ScoreArgs &a, const float (&b
                  (logit == after_logit && bias == after_bias && my_idx < after_idx);
         uint32_t open = __ballot_sync(ALL, !(ok && sure && edge));
         if (open) {
-            open = rank_again<T, IPL, Q, FIXED>(a, l, word, last, next, sure, edge, ok, sm.open, open, found, logit, bias, my_idx, lane);
+            open = rank_again<T, IPL, Q, FIXED>(a, l, word, last, next, sure, ok, sm.open, open, found, logit, bias, my_idx, lane);
             while (open) {
                 const int q = (__ffs(static_cast<int>(open)) - 1) / SEG;
                 int idx;

@@ -294,3 +294,19 @@ def test_biases_and_logits_that_are_no_ordinary_numbers(score, E, k, groups, kep
     same = torch.zeros(6145, E, device="cuda")
     for b in (None, torch.zeros(E, device="cuda")):
         _check(same, k, score, b, groups, kept, mask=mask)
+
+
+@pytest.mark.parametrize("T,k", [(40, 8), (40, 1), (40, 32), (6145, 8), (16385, 8), (16385, 1)])
+def test_chains_of_ties_and_of_near_values(T, k):
+    """Around the last slot: equal values with and without nearly equal ones among them, in and out of order."""
+    g = torch.Generator(device="cuda").manual_seed(T + k)
+    ints = lambda n, *size: torch.randint(0, n, size, generator=g, device="cuda").float()
+    zero = torch.zeros(64, device="cuda")
+    step = ints(3, 64) * 0.25
+    for l in (ints(2, T, 64), ints(12, T, 64) * 0.25, 1 + ints(3, T, 64) * 2.0 ** -23, ints(2, T, 64) + ints(2, T, 64) * 2.0 ** -22,
+              (ints(2, T, 64) + 16) * (1 + ints(2, T, 64) * 2.0 ** -23), torch.zeros(T, 64, device="cuda")):
+        for b in (zero, step, step + ints(2, 64) * 2.0 ** -24, 3 * step):
+            for groups, kept in ((1, 1), (4, 2)):
+                if k <= kept * 64 // groups:
+                    idx, _ = ops.route_scores(l, k, bias=b, groups=groups, topk_groups=kept)
+                    assert torch.equal(idx, _choice(l, k, "sigmoid", b, groups, kept, 2))
