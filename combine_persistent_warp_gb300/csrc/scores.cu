@@ -119,44 +119,49 @@ __device__ __noinline__ uint64_t exact_key(float logit, float bias, bool has_bia
     return logit == -INFINITY ? 0ull : order_key(has_bias ? s + static_cast<double>(bias) : s);
 }
 
-// Whether the lane's group of experts stays, from the group's two largest keys, of Q tokens side by side: `least`
-// and `most` are the lowest score that stays and the highest that does not (0: none).  Group g is that of the
-// lanes g << shift and after; `own` its score.
+// The lanes of a token, of Q side by side.
+template <int Q>
+constexpr uint32_t SLOTS = Q == 1 ? ALL : (1u << (32 / Q)) - 1u;
+
+// Which groups of experts stay, from the two largest keys of each, of Q tokens side by side: keys of group g are those
+// of the lanes g << shift and after.  Lane q * SEG + g gets the score `own` of group g of token q (0: nothing there),
+// whether it stays, and the token's lowest score that stays and highest that does not (0: none).
 __device__ __forceinline__ uint32_t key_sum(uint32_t a, uint32_t b) { return plain_key(plain_value(a) + plain_value(b)); }
 __device__ __forceinline__ uint64_t key_sum(uint64_t a, uint64_t b) { return order_key(key_value(a) + key_value(b)); }
 template <typename K, int Q>
 struct Groups {
-    K first[Q], second[Q], own[Q], least[Q], most[Q];
-    bool stays[Q];
+    K first[Q], second[Q], own, least, most;
+    bool stays;
 };
 template <typename K, int Q>
 __device__ __forceinline__ void choose_groups(const ScoreArgs &a, Groups<K, Q> &v, int lane, int shift)
 {
-    const int g = lane >> shift;
-    K score[Q];
+    constexpr int SEG = 32 / Q;
+    const int seg = lane / SEG, slot = lane % SEG;
+    K own = 0;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-        score[q] = g < a.groups && v.first[q] > NEVER<K> ? v.first[q] : 0;
+        K score = v.first[q] > NEVER<K> ? v.first[q] : 0;
         if (a.pair && v.second[q] > NEVER<K>)
-            score[q] = key_sum(v.first[q], v.second[q]);
-        v.own[q] = score[q];
-        v.least[q] = 0;
-        v.stays[q] = false;
+            score = key_sum(v.first[q], v.second[q]);
+        const K its = __shfl_sync(ALL, score, slot << shift & 31);
+        own = seg == q ? its : own;
     }
-    for (int j = 0; j < a.kept; ++j) {
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const K m = warp_max(score[q]);
-            const int best = (__ffs(static_cast<int>(__ballot_sync(ALL, score[q] == m))) - 1) >> shift;   // ties: the lowest
-            const bool mine = g == best && m != 0;
-            v.least[q] = m != 0 ? m : v.least[q];
-            v.stays[q] = v.stays[q] || mine;
-            score[q] = mine ? 0 : score[q];
-        }
+    own = slot < a.groups ? own : 0;
+    int rank = 0;   // ties: the lowest first
+#pragma unroll 4
+    for (int g = 0; g < a.groups; ++g) {
+        const K other = __shfl_sync(ALL, own, g, SEG);
+        rank += other > own || (other == own && g < slot);
     }
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-        v.most[q] = warp_max(score[q]);
+    const uint32_t last = __ballot_sync(ALL, own != 0 && rank == a.kept - 1) >> (seg * SEG) & SLOTS<Q>;
+    const uint32_t after = __ballot_sync(ALL, own != 0 && rank == a.kept) >> (seg * SEG) & SLOTS<Q>;
+    const K least = __shfl_sync(ALL, own, __ffs(static_cast<int>(last)) - 1, SEG);
+    const K most = __shfl_sync(ALL, own, __ffs(static_cast<int>(after)) - 1, SEG);
+    v.own = own;
+    v.least = last ? least : 0;
+    v.most = after ? most : 0;
+    v.stays = own != 0 && rank < a.kept;
 }
 template <typename K>
 __device__ __forceinline__ void insert(K v, K &first, K &second)
@@ -181,24 +186,24 @@ __device__ __forceinline__ int spot(int e) { return e + (e >> 5) * 4; }
 template <int IPL>
 constexpr int SPOTS = IPL * 36;
 
-// The same where scores within `open` of each other are in doubt: groups that are so far above all that do not stay
-// are sure to, and those in doubt are ranked by their scores in 64 bits for the places that are left.
+// The same of one token, whose scores within `open` of each other are in doubt (lane g: group g): groups that are so far above
+// all that do not stay are sure to, and those in doubt are ranked by their scores in 64 bits for the places
+// that are left.  Returns the groups that stay.
 template <typename T>
-__device__ __noinline__ bool group_stays_exactly(const ScoreArgs &a, const T *l, uint32_t own, bool stays, uint32_t least, uint32_t most, float open,
-                                                 uint64_t *seen, int lane, int shift)
+__device__ __noinline__ uint32_t groups_exactly(const ScoreArgs &a, const T *l, uint32_t own, bool stays, float least, float most, float open,
+                                                uint64_t *seen, int lane)
 {
     const float v = plain_value(own);
-    const bool head = (lane & ((1 << shift) - 1)) == 0 && own != 0u;
-    const bool sure = stays && v - plain_value(most) > open;
-    const bool doubt = own != 0u && !sure && (stays || !(plain_value(least) - v > open));
-    const uint32_t in_doubt = __ballot_sync(ALL, head && doubt);   // by their first lanes
-    const int left = a.kept - __popc(__ballot_sync(ALL, head && sure)), n = __popc(in_doubt);
+    const bool sure = stays && v - most > open;
+    const bool doubt = own != 0u && !sure && (stays || !(least - v > open));
+    const uint32_t in_doubt = __ballot_sync(ALL, doubt);
+    const int left = a.kept - __popc(__ballot_sync(ALL, sure)), n = __popc(in_doubt);
     for (int i = lane; i < n * a.per; i += 32) {
         const int nth = static_cast<int>((static_cast<uint32_t>(i) * a.per_magic) >> 20);
         uint32_t after = in_doubt;
         for (int k = 0; k < nth; ++k)
             after &= after - 1u;
-        const int e = ((__ffs(static_cast<int>(after)) - 1) >> shift) * a.per + i - nth * a.per;
+        const int e = (__ffs(static_cast<int>(after)) - 1) * a.per + i - nth * a.per;
         seen[i] = exact_key(to_f<T>(l[e]), a.bias ? a.bias[e] : 0.0f, a.bias);
     }
     __syncwarp();
@@ -217,7 +222,7 @@ __device__ __noinline__ bool group_stays_exactly(const ScoreArgs &a, const T *l,
         rank += other > first || (other == first && r < lane);
     }
     const uint32_t chosen = __ballot_sync(ALL, lane < n && rank < left);
-    return sure || (doubt && (chosen >> __popc(in_doubt & ((1u << (lane >> shift << shift)) - 1u)) & 1u));
+    return __ballot_sync(ALL, sure || (doubt && (chosen >> __popc(in_doubt & ((1u << lane) - 1u)) & 1u)));
 }
 
 // What a token's softmax is taken with, and how near two values of c are open (beside 2^-22 of their size).
@@ -259,22 +264,32 @@ __device__ __forceinline__ void keep_groups(const ScoreArgs &a, const T *l, cons
     }
     merge_lanes(v, 1 << shift);
     choose_groups(a, v, lane, shift);
+    constexpr int SEG = 32 / Q;
+    float open = sm[0].open;
+#pragma unroll
+    for (int q = 1; q < Q; ++q)
+        open = lane / SEG == q ? sm[q].open : open;
+    const float least = plain_value(v.least), most = plain_value(v.most);
+    open = 2.0f * open + fabsf(least) * 0x1p-21f;
+    const uint32_t stays = __ballot_sync(ALL, v.stays);
+    const uint32_t doubt = __ballot_sync(ALL, !direct && v.most != 0u && !(least - most > open));
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-        if (routed[q] && !direct && v.most[q] != 0u) {
-            const float least = plain_value(v.least[q]), open = 2.0f * sm[q].open + fabsf(least) * 0x1p-21f;
-            if (!(least - plain_value(v.most[q]) > open)) {
-                if (a.softmax)
-                    sure[q] = false;
-                else
-                    v.stays[q] = group_stays_exactly<T>(a, l + q * a.ld, v.own[q], v.stays[q], v.least[q], v.most[q], open, seen, lane, shift);
+        uint32_t stay = stays >> (q * SEG) & SLOTS<Q>;
+        if (routed[q] && (doubt >> (q * SEG) & 1u)) {
+            if (a.softmax) {
+                sure[q] = false;
+            } else {
+                const int from = q * SEG + lane % SEG;
+                const uint32_t own = __shfl_sync(ALL, v.own, from);
+                const float its_least = __shfl_sync(ALL, least, from), its_most = __shfl_sync(ALL, most, from), its_open = __shfl_sync(ALL, open, from);
+                stay = groups_exactly<T>(a, l + q * a.ld, lane < SEG ? own : 0u, lane < SEG && (stay >> lane & 1u), its_least, its_most, its_open, seen, lane);
             }
         }
-        const uint32_t stay = __ballot_sync(ALL, v.stays[q]);
 #pragma unroll
         for (int i = 0; i < IPL; ++i) {
-            const int e = lane * IPL + i, ge = static_cast<int>((static_cast<uint32_t>(e) * a.per_magic) >> 20);
-            c[q][i] = (in_lanes ? v.stays[q] : (e < a.E && (stay >> (ge << shift) & 1u))) ? c[q][i] : -INFINITY;
+            const int e = lane * IPL + i, g = in_lanes ? lane >> shift : static_cast<int>((static_cast<uint32_t>(e) * a.per_magic) >> 20);
+            c[q][i] = e < a.E && (stay >> (g & 31) & 1u) ? c[q][i] : -INFINITY;
         }
     }
 }
@@ -327,9 +342,9 @@ __device__ __noinline__ int choose_exactly(const ScoreArgs &a, const T *l, uint6
         v.second[0] = second;
         merge_lanes(v, a.lanes);
         choose_groups(a, v, lane, a.shift);
-        const uint32_t stay = __ballot_sync(ALL, v.stays[0]);
+        const uint32_t stay = __ballot_sync(ALL, v.stays);
         for (int e = lane; e < a.E; e += 32)
-            if (!(stay >> (static_cast<int>((static_cast<uint32_t>(e) * a.per_magic) >> 20) << a.shift) & 1u))
+            if (!(stay >> ((static_cast<uint32_t>(e) * a.per_magic) >> 20) & 1u))
                 seen[spot(e)] = 0;
         __syncwarp();
     }
@@ -580,10 +595,6 @@ __device__ __forceinline__ float seg_max(float v)
         v = fmaxf(v, __shfl_xor_sync(ALL, v, o));
     return v;
 }
-
-// The lanes of a token.
-template <int Q>
-constexpr uint32_t SLOTS = Q == 1 ? ALL : (1u << (32 / Q)) - 1u;
 
 // The tokens of the lanes `open`, whose order or last place is in doubt.  What the words leave out, from the one after
 // the last slot on, is below the last slot, or is equal to it in what it is computed from and a later
@@ -894,9 +905,9 @@ struct ScoreLaunch {
     static void go(const ScoreArgs &a, cudaStream_t s)
     {
         if constexpr (IPL <= 8) {
-            if (a.k <= 8 && a.T >= FOUR_TOKENS)
+            if (a.k <= 8 && a.groups <= 8 && a.T >= FOUR_TOKENS)
                 return launch_scores<T, IPL, 4>(a, s);
-            if (a.k <= 16 && a.T >= TWO_TOKENS)
+            if (a.k <= 16 && a.groups <= 16 && a.T >= TWO_TOKENS)
                 return launch_scores<T, IPL, 2>(a, s);
         }
         launch_scores<T, IPL, 1>(a, s);
