@@ -303,31 +303,33 @@ template <typename T, int IPL>
 __device__ __noinline__ int choose_exactly(const ScoreArgs &a, const T *l, uint64_t *seen, int lane, int &my_idx)
 {
     const bool direct = directly(a), softmax = a.softmax && !direct;
-    double top = 0.0, total = 1.0;
+    double total = 1.0;
     if (softmax) {
         float m = -INFINITY;   // (the logits have at most 32 bits)
         for (int e = lane; e < a.E; e += 32)
             m = fmaxf(m, to_f<T>(l[e]));
-        top = static_cast<double>(warp_max_f(m));
-    }
-    // softmax: the sum first
-    for (int pass = softmax ? 0 : 1; pass < 2; ++pass) {
+        const double top = static_cast<double>(warp_max_f(m));
         double sum = 0.0;
+        // (each lane's exponentials wait for the total in the places of its keys)
 #pragma unroll 2
         for (int e = lane; e < a.E; e += 32) {
-            const float f = to_f<T>(l[e]);
-            if (direct) {
-                seen[spot(e)] = order_key(static_cast<double>(f));
-            } else if (a.softmax) {
-                const double x = exp(static_cast<double>(f) - top);
-                sum += x;
-                seen[spot(e)] = f == -INFINITY ? 0ull : order_key(a.bias ? x / total + static_cast<double>(a.bias[e]) : x / total);
-            } else {
-                seen[spot(e)] = exact_key(f, a.bias ? a.bias[e] : 0.0f, a.bias);
-            }
+            const double x = exp(static_cast<double>(to_f<T>(l[e])) - top);
+            sum += x;
+            seen[spot(e)] = static_cast<uint64_t>(__double_as_longlong(x));
         }
-        if (pass == 0)
-            total = warp_sum(sum);
+        total = warp_sum(sum);
+    }
+#pragma unroll 2
+    for (int e = lane; e < a.E; e += 32) {
+        const float f = to_f<T>(l[e]);
+        if (direct) {
+            seen[spot(e)] = order_key(static_cast<double>(f));
+        } else if (a.softmax) {
+            const double p = __longlong_as_double(static_cast<long long>(seen[spot(e)])) / total;
+            seen[spot(e)] = f == -INFINITY ? 0ull : order_key(a.bias ? p + static_cast<double>(a.bias[e]) : p);
+        } else {
+            seen[spot(e)] = exact_key(f, a.bias ? a.bias[e] : 0.0f, a.bias);
+        }
     }
     __syncwarp();
     if (a.groups > 1) {
