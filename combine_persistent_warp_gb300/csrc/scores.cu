@@ -469,6 +469,44 @@ __device__ __forceinline__ void load_lane(float (&f)[IPL], const T *row, int lan
     }
 }
 
+// The same of Q rows from row l on, `there` of which there are, all on their way before the first is looked at.
+template <typename T, int IPL>
+struct Lane {
+    T v[IPL];
+};
+template <typename T, int IPL, int Q>
+__device__ __forceinline__ void load_lanes(Lane<T, IPL> (&f)[Q], const T *l, long long ld, int there, int lane, int E, bool vec)
+{
+    constexpr int BYTES = IPL * static_cast<int>(sizeof(T)), PIECE = BYTES < 16 ? BYTES : 16, N = PIECE / static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+            f[q].v[i] = from_f<T>(0.0f);
+    if (N > 1 && vec) {
+        struct alignas(PIECE) Piece {
+            T v[N];
+        };
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int i = 0; i < IPL / N; ++i)
+                if (q < there && lane * IPL < E) {
+                    const Piece p = reinterpret_cast<const Piece *>(l + q * ld + lane * IPL)[i];
+#pragma unroll
+                    for (int k = 0; k < N; ++k)
+                        f[q].v[i * N + k] = p.v[k];
+                }
+    } else {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int i = 0; i < IPL; ++i)
+                if (q < there && lane * IPL + i < E)
+                    f[q].v[i] = l[q * ld + lane * IPL + i];
+    }
+}
+
 // 1/(1 + exp(-l)) by two approximate instructions.
 __device__ __forceinline__ float logistic(float l)
 {
@@ -479,7 +517,7 @@ __device__ __forceinline__ float logistic(float l)
 }
 
 // The c of Q tokens, from row l on, from their logits and the biases, without those of the groups that do not stay.
-// Of tokens that are not routed, or not there, nothing is read.
+// Of tokens that are not routed, or not there, no logit is looked up.
 template <typename T, int IPL, int Q>
 __device__ __forceinline__ void make_c(const ScoreArgs &a, const T *l, const bool (&routed)[Q], float (&f)[Q][IPL], const float (&b)[IPL],
                                        bool direct, uint64_t *seen, int lane, Softmax (&sm)[Q], bool (&sure)[Q])
@@ -670,14 +708,15 @@ __device__ __forceinline__ uint32_t rank_again(const ScoreArgs &a, const T *l, u
 // another), and then has the slots of all of them, a lane each (SEG = 32/Q >= k lanes a token), for the
 // weights and what is to be checked.
 template <typename T, int IPL, int Q, bool FIXED>
-__device__ __forceinline__ void score_tokens(const ScoreArgs &a, const float (&b)[IPL], uint64_t *seen, int t0, int lane)
+__device__ __forceinline__ void score_tokens(const ScoreArgs &a, const Lane<T, IPL> (&its_logits)[Q], bool is_routed, const float (&b)[IPL],
+                                             uint64_t *seen, int t0, int lane)
 {
     constexpr int SEG = 32 / Q;
     const int seg = lane / SEG, slot = lane % SEG, t = t0 + seg;
     const bool direct = !FIXED && directly(a);
     // token q's row, by all lanes; whether it is there and routed
     const auto row = [&](int q) { return static_cast<const T *>(a.logits) + static_cast<size_t>(t0 + q) * a.ld; };
-    const uint32_t lanes = __ballot_sync(ALL, slot == 0 && t < a.T && (!a.mask || a.mask[t]));
+    const uint32_t lanes = __ballot_sync(ALL, is_routed);
     bool routed[Q];
     float f[Q][IPL];
 #pragma unroll
@@ -685,9 +724,7 @@ __device__ __forceinline__ void score_tokens(const ScoreArgs &a, const float (&b
         routed[q] = lanes >> (q * SEG) & 1u;
 #pragma unroll
         for (int i = 0; i < IPL; ++i)
-            f[q][i] = 0.0f;
-        if (routed[q])
-            load_lane<T, IPL>(f[q], row(q), lane, a.E, a.vec);
+            f[q][i] = lane * IPL + i < a.E ? to_f<T>(its_logits[q].v[i]) : -INFINITY;
     }
     uint32_t word[Q][IPL], largest[Q];
     Softmax its[Q];
@@ -793,6 +830,11 @@ __global__ void __launch_bounds__(WARPS * 32) score_kernel(const ScoreArgs a)
     const int t0 = (blockIdx.x * WARPS + warp) * Q;
     if (t0 >= a.T)
         return;
+    // (what is read is on its way at once: padding too, which is not looked at)
+    Lane<T, IPL> l[Q];
+    load_lanes<T, IPL, Q>(l, static_cast<const T *>(a.logits) + static_cast<size_t>(t0) * a.ld, a.ld, a.T - t0, lane, a.E, a.vec);
+    const int t = t0 + lane / (32 / Q);
+    const bool routed = t < a.T && (!a.mask || a.mask[t]);
     float b[IPL];
     bool fixed = false;
     if (a.bias) {
@@ -805,9 +847,9 @@ __global__ void __launch_bounds__(WARPS * 32) score_kernel(const ScoreArgs a)
     }
     if constexpr (IPL <= 8) {
         if (fixed)
-            return score_tokens<T, IPL, Q, true>(a, b, seen[warp], t0, lane);
+            return score_tokens<T, IPL, Q, true>(a, l, routed, b, seen[warp], t0, lane);
     }
-    score_tokens<T, IPL, Q, false>(a, b, seen[warp], t0, lane);
+    score_tokens<T, IPL, Q, false>(a, l, routed, b, seen[warp], t0, lane);
 }
 
 // ------------------------------------------------------------------ gradient ------------
