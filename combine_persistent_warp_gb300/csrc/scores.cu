@@ -13,11 +13,11 @@
 // which expert a token goes to should not hang on a rounding: c is computed in 32 bits with a bound of
 // its error, and the candidates that this bound leaves open are ranked again in 64.
 //
-// The data is small, so issue bounds (half of it is the integer pipe's: keys, maxima and selections), and for few
-// tokens latency.  Measured on a GB300 in graphs, bf16, top 8: 16384 x 128 in 8 groups of which 4 stay 12.7 to 14.4 us
-// (a token that is ranked again adds 2 us, one whose groups are in doubt 3 to 4), in one group 9.6, without a bias 7.5; its gradient 4.5; 128 x
-// 32 fp32 in 4 groups 2.4 and 1.8.  Tokens whose logits have no bias but sums of two (16384 x 128, coarse values whose
-// sums tie) 20 to 26; softmax scores with a bias, chosen again with all experts where they are open, 24.
+// The data is small: the instructions bound it, and how many warps an SM has to hide their latency; for few tokens
+// latency alone.  Measured on a GB300 in graphs, bf16, top 8: 16384 x 128 in 8 groups of which 4 stay 10.3 to 11.2 us (a token
+// that is ranked in 64 bits adds 1 us, one whose groups are in doubt 2), in one group 7.6 to 8.5, without a bias 6.7; its
+// gradient 4.5; 128 x 32 fp32 in 4 groups 2.1 and 1.8.  Tokens whose logits have no bias but sums of two (16384 x 128, coarse
+// values whose sums tie) 20; softmax scores with a bias, chosen again with all experts where they are open, 19.
 #include <climits>
 
 #include "moe_internal.cuh"
@@ -821,8 +821,10 @@ __device__ __forceinline__ void score_tokens(const ScoreArgs &a, const Lane<T, I
     }
 }
 
+// Seven blocks an SM (at most 72 registers): with the 80 that four tokens would take 6144 x 128 bf16 in 8 groups is 7.8 us
+// and not 6.8, 16384 unbiased 7.1 and not 6.6 (in 8 groups 10.4 and 11.1); eight are as slow.
 template <typename T, int IPL, int Q>
-__global__ void __launch_bounds__(WARPS * 32) score_kernel(const ScoreArgs a)
+__global__ void __launch_bounds__(WARPS * 32, IPL <= 4 ? 7 : 1) score_kernel(const ScoreArgs a)
 {
     ptx::follow();
     __shared__ uint64_t seen[WARPS][SPOTS<IPL>];
@@ -941,9 +943,10 @@ void launch_scores(const ScoreArgs &a, cudaStream_t s)
     launch_programmatic(score_kernel<T, IPL, Q>, (a.T + WARPS * Q - 1) / (WARPS * Q), WARPS * 32, 0, s, a);
 }
 // Tokens of a warp: the more there are, the less their slots cost, and the fewer warps there are.  128 experts in 8
-// groups, bf16, with 1, 2 and 4 of them: 4096 tokens 8.6, 8.9 and 9.6 us (unbiased, one group: 3.9, 4.0, 4.2), 8192
-// 11.0, 10.4, 10.7 (6.4, 5.2, 5.6), 16384 15.1, 13.5, 14.4 (10.5, 8.2, 7.5), 65536 47, 38, 37 (35, 25, 23).
-constexpr int TWO_TOKENS = 6144, FOUR_TOKENS = 16384;
+// groups, bf16, with 1, 2 and 4 of them: 2048 tokens 5.0, 5.2 and 5.4 us (unbiased, one group: 2.6, 2.8, 3.1), 4096
+// 5.2, 4.9, 4.8 (3.9, 3.6, 4.2), 6144 7.0, 6.9, 8.1 (5.7, 4.3, 5.7), 8192 8.6, 7.5, 7.3 (6.3, 5.0, 4.8), 16384 14.6, 12.0, 11.2
+// (11.2, 8.0, 6.7), 65536 50, 38, 31 (39, 25, 21).
+constexpr int TWO_TOKENS = 4096, FOUR_TOKENS = 8192;
 template <typename T, int IPL>
 struct ScoreLaunch {
     static void go(const ScoreArgs &a, cudaStream_t s)
