@@ -16,7 +16,7 @@
 // The data is small: the instructions bound it, and how many warps an SM has to hide their latency; for few tokens
 // latency alone.  Measured on a GB300 in graphs, bf16, top 8: 16384 x 128 in 8 groups of which 4 stay 10.3 to 11.2 us (a token
 // that is ranked in 64 bits adds 1 us, one whose groups are in doubt 2), in one group 7.6 to 8.5, without a bias 6.7; its
-// gradient 4.5; 128 x 32 fp32 in 4 groups 2.1 and 1.8.  Tokens whose logits have no bias but sums of two (16384 x 128, coarse
+// gradient 3.2; 128 x 32 fp32 in 4 groups 2.1 and 1.8.  Tokens whose logits have no bias but sums of two (16384 x 128, coarse
 // values whose sums tie) 20; softmax scores with a bias, chosen again with all experts where they are open, 19.
 #include <climits>
 
@@ -865,75 +865,116 @@ struct ScoreBwdArgs {
     int softmax, renorm;
     float scale;
     void *dlogits;        // [T][E]
+    int vec;              // the rows that a warp clears start on 16-byte boundaries
 };
 
-template <typename T, int IPL>
-__global__ void __launch_bounds__(WARPS * 32) score_backward_kernel(const ScoreBwdArgs a)
+// Blocks are placed at some 300 cycles each an SM: eight warps a block (65536 x 64 softmax scores as they are 16.9 us with four,
+// 12.4 with eight).
+constexpr int BWD_WARPS = 8;
+// A slot's expert (-1: none), weight and gradient.
+struct Slot {
+    int e;
+    float w, dw;
+};
+__device__ __forceinline__ Slot load_slot(const ScoreBwdArgs &a, int t, int slot)
 {
-    ptx::follow();
-    const int t = blockIdx.x * WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (t >= a.T)
-        return;
-    int e = -1;
-    float w = 0.0f, dw = 0.0f;
-    if (lane < a.k) {
-        const size_t at = static_cast<size_t>(t) * a.k + lane;
+    Slot s{-1, 0.0f, 0.0f};
+    if (slot < a.k && t < a.T) {
+        const size_t at = static_cast<size_t>(t) * a.k + slot;
         const int64_t id = a.idx[at];
-        e = id >= 0 && id < a.E ? static_cast<int>(id) : -1;
-        if (e >= 0) {
-            w = a.w[at];
-            dw = a.dw[at];
-        }
+        if (id >= 0 && id < a.E)
+            s = {static_cast<int>(id), a.w[at], a.dw[at]};
     }
-    const float dot = warp_sum(w * dw);
-    const bool any = __any_sync(ALL, e >= 0);
-    const T *l = static_cast<const T *>(a.logits) + static_cast<size_t>(t) * a.ld;
-    T *out = static_cast<T *>(a.dlogits) + static_cast<size_t>(t) * a.E;
-    const bool dense = a.softmax && !a.renorm && any;
-    // what the slot adds: to the expert's logit, or (dense) to what its probability is multiplied by
-    float d = dense ? a.scale * dw : a.renorm ? w * (dw - dot / a.scale) : w * dw;
-    if (!a.softmax && e >= 0)
-        d /= 1.0f + expf(to_f<T>(l[e]));
-    // an expert that is in several slots gets their sum, in order
-    const uint32_t same = __match_any_sync(ALL, e);
+    return s;
+}
+// An expert that is in several slots of its token gets their sum, in order.
+template <int Q>
+__device__ __forceinline__ float sum_of_slots(float d, int e, int k, int lane)
+{
+    constexpr int SEG = 32 / Q;
+    const uint32_t same = __match_any_sync(ALL, e < 0 ? -1 : e * Q + lane / SEG);
     if (__any_sync(ALL, e >= 0 && (same & (same - 1u)) != 0u)) {
         float sum = 0.0f;
-        for (int j = 0; j < a.k; ++j) {
-            const float v = __shfl_sync(ALL, d, j);
-            sum += same >> j & 1u ? v : 0.0f;
+        for (int j = 0; j < k; ++j) {
+            const float v = __shfl_sync(ALL, d, j, SEG);
+            sum += same >> (lane / SEG * SEG + j) & 1u ? v : 0.0f;
         }
         d = sum;
     }
-    float top = 0.0f, inv = 0.0f;
-    if (dense) {
-        float f[IPL], sum = 0.0f;
-        top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < IPL; ++i) {
-            f[i] = i * 32 + lane < a.E ? to_f<T>(l[i * 32 + lane]) : -INFINITY;
-            top = fmaxf(top, f[i]);
-        }
-        top = warp_max_f(top);
-#pragma unroll
-        for (int i = 0; i < IPL; ++i) {
-            f[i] = expf(f[i] - top);   // NaN logits and top = +inf make NaN, as in the forward pass
-            if (i * 32 + lane < a.E)
-                sum += f[i];
-        }
-        inv = 1.0f / warp_sum(sum);
-#pragma unroll
-        for (int i = 0; i < IPL; ++i)
-            if (i * 32 + lane < a.E)
-                out[i * 32 + lane] = from_f<T>(f[i] * inv * -dot);
-    } else {
+    return d;
+}
+
+// All but softmax scores as they are: a gradient has k values and zeros around them.  A warp takes Q tokens, whose
+// rows it clears in one piece, and has the slots of all of them, a lane each.
+template <typename T, int Q>
+__global__ void __launch_bounds__(BWD_WARPS * 32) score_backward_kernel(const ScoreBwdArgs a)
+{
+    ptx::follow();
+    constexpr int SEG = 32 / Q, N = 16 / static_cast<int>(sizeof(T));
+    const int lane = threadIdx.x & 31, t0 = (blockIdx.x * BWD_WARPS + (threadIdx.x >> 5)) * Q, t = t0 + lane / SEG;
+    if (t0 >= a.T)
+        return;
+    const Slot s = load_slot(a, t, lane % SEG);
+    T *out = static_cast<T *>(a.dlogits) + static_cast<size_t>(t0) * a.E;
+    const int n = min(Q, a.T - t0) * a.E, whole = a.vec ? n / N * N : 0;
+    for (int i = lane * N; i < whole; i += 32 * N)
+        *reinterpret_cast<uint4 *>(out + i) = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = whole + lane; i < n; i += 32)
+        out[i] = from_f<T>(0.0f);
+    float d = s.w * s.dw;
+    const float dot = seg_sum<SEG>(d);
+    if (a.renorm)
+        d = s.w * (s.dw - dot / a.scale);
+    if (!a.softmax && s.e >= 0)
+        d /= 1.0f + expf(to_f<T>(static_cast<const T *>(a.logits)[static_cast<size_t>(t) * a.ld + s.e]));
+    d = sum_of_slots<Q>(d, s.e, a.k, lane);
+    __syncwarp();   // the chosen ones over the zeros that other lanes have written
+    if (s.e >= 0)
+        out[lane / SEG * a.E + s.e] = from_f<T>(d);
+}
+
+// Softmax scores as they are: every logit has a gradient.
+template <typename T, int IPL>
+__global__ void __launch_bounds__(BWD_WARPS * 32) softmax_backward_kernel(const ScoreBwdArgs a)
+{
+    ptx::follow();
+    const int t = blockIdx.x * BWD_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (t >= a.T)
+        return;
+    const Slot s = load_slot(a, t, lane);
+    const float dot = warp_sum(s.w * s.dw);
+    const T *l = static_cast<const T *>(a.logits) + static_cast<size_t>(t) * a.ld;
+    T *out = static_cast<T *>(a.dlogits) + static_cast<size_t>(t) * a.E;
+    if (!__any_sync(ALL, s.e >= 0)) {
 #pragma unroll
         for (int i = 0; i < IPL; ++i)
             if (i * 32 + lane < a.E)
                 out[i * 32 + lane] = from_f<T>(0.0f);
+        return;
     }
+    // what the slots add to that which the expert's probability is multiplied by
+    const float d = sum_of_slots<1>(a.scale * s.dw, s.e, a.k, lane);
+    float f[IPL], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < IPL; ++i) {
+        f[i] = i * 32 + lane < a.E ? to_f<T>(l[i * 32 + lane]) : -INFINITY;
+        top = fmaxf(top, f[i]);
+    }
+    top = warp_max_f(top);
+#pragma unroll
+    for (int i = 0; i < IPL; ++i) {
+        f[i] = expf(f[i] - top);   // NaN logits and top = +inf make NaN, as in the forward pass
+        if (i * 32 + lane < a.E)
+            sum += f[i];
+    }
+    const float inv = 1.0f / warp_sum(sum);
+#pragma unroll
+    for (int i = 0; i < IPL; ++i)
+        if (i * 32 + lane < a.E)
+            out[i * 32 + lane] = from_f<T>(f[i] * inv * -dot);
     __syncwarp();   // the chosen ones over what the row's other lanes have written
-    if (e >= 0)
-        out[e] = from_f<T>(dense ? expf(to_f<T>(l[e]) - top) * inv * (d - dot) : d);
+    if (s.e >= 0)
+        out[s.e] = from_f<T>(expf(to_f<T>(l[s.e]) - top) * inv * (d - dot));
 }
 
 // ------------------------------------------------------------------ host side ------------
@@ -947,6 +988,9 @@ void launch_scores(const ScoreArgs &a, cudaStream_t s)
 // 5.2, 4.9, 4.8 (3.9, 3.6, 4.2), 6144 7.0, 6.9, 8.1 (5.7, 4.3, 5.7), 8192 8.6, 7.5, 7.3 (6.3, 5.0, 4.8), 16384 14.6, 12.0, 11.2
 // (11.2, 8.0, 6.7), 65536 50, 38, 31 (39, 25, 21).
 constexpr int TWO_TOKENS = 4096, FOUR_TOKENS = 8192;
+// Of the gradient, 128 experts, bf16: 1024 tokens 1.9, 1.9, 2.0 us, 4096 2.5, 2.3, 2.1, 16384 4.5, 3.5, 3.8, 65536 16.9, 8.7, 7.2 (in
+// blocks of four warps).
+constexpr int BWD_TWO = 2048, BWD_FOUR = 32768;
 template <typename T, int IPL>
 struct ScoreLaunch {
     static void go(const ScoreArgs &a, cudaStream_t s)
@@ -960,11 +1004,24 @@ struct ScoreLaunch {
         launch_scores<T, IPL, 1>(a, s);
     }
 };
+template <typename T, int Q>
+void launch_score_backward(ScoreBwdArgs a, cudaStream_t s)
+{
+    a.vec = op_aligned(a.dlogits, 16) && Q * a.E * static_cast<int>(sizeof(T)) % 16 == 0;
+    launch_programmatic(score_backward_kernel<T, Q>, (a.T + BWD_WARPS * Q - 1) / (BWD_WARPS * Q), BWD_WARPS * 32, 0, s, a);
+}
+template <typename T>
+void launch_score_backward(const ScoreBwdArgs &a, cudaStream_t s)
+{
+    a.k <= 8 && a.T >= BWD_FOUR    ? launch_score_backward<T, 4>(a, s)
+    : a.k <= 16 && a.T >= BWD_TWO ? launch_score_backward<T, 2>(a, s)
+                                   : launch_score_backward<T, 1>(a, s);
+}
 template <typename T, int IPL>
-struct ScoreBwdLaunch {
+struct SoftmaxBwdLaunch {
     static void go(const ScoreBwdArgs &a, cudaStream_t s)
     {
-        launch_programmatic(score_backward_kernel<T, IPL>, (a.T + WARPS - 1) / WARPS, WARPS * 32, 0, s, a);
+        launch_programmatic(softmax_backward_kernel<T, IPL>, (a.T + BWD_WARPS - 1) / BWD_WARPS, BWD_WARPS * 32, 0, s, a);
     }
 };
 
@@ -1032,9 +1089,12 @@ int moe_route_scores_backward(int T, int E, int topk, const float *dw, const int
         !op_aligned(topk_w, 4) || !op_aligned(logits, dtype_bytes(dtype)) || !op_aligned(dlogits, dtype_bytes(dtype)))
         return MOE_ERR_INVALID_ARG;
     OP_DEVICE(sms);
-    by_width<ScoreBwdLaunch>(dtype, E,
-                             ScoreBwdArgs{T, E, topk, dw, topk_idx, topk_w, logits, ld, score == MOE_SCORE_SOFTMAX, renormalize, scale, dlogits},
-                             static_cast<cudaStream_t>(stream));
+    const ScoreBwdArgs a{T, E, topk, dw, topk_idx, topk_w, logits, ld, score == MOE_SCORE_SOFTMAX, renormalize, scale, dlogits, 0};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a.softmax && !renormalize)
+        by_width<SoftmaxBwdLaunch>(dtype, E, a, s);
+    else
+        with_dtype(dtype, [&](auto *t) { launch_score_backward<std::remove_pointer_t<decltype(t)>>(a, s); });
     return launched();
 }
 
