@@ -310,3 +310,23 @@ def test_chains_of_ties_and_of_near_values(T, k):
                 if k <= kept * 64 // groups:
                     idx, _ = ops.route_scores(l, k, bias=b, groups=groups, topk_groups=kept)
                     assert torch.equal(idx, _choice(l, k, "sigmoid", b, groups, kept, 2))
+
+
+@pytest.mark.parametrize("T,k", [(2051, 5), (2050, 16), (32771, 8)])
+@pytest.mark.parametrize("E", [40, 37])
+def test_gradient_of_several_tokens_a_warp(T, k, E):
+    """Experts in several slots, empty slots, and a last warp whose tokens are not all there."""
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    l = _logits(T, E, torch.float32)
+    idx = torch.randint(-1, 6, (T, k), generator=g, device="cuda")
+    w, dw = torch.rand(T, k, generator=g, device="cuda"), torch.randn(T, k, generator=g, device="cuda").clamp(-4, 4)
+    got = ops.route_scores_backward(dw, idx, w, l, renormalize=False)
+    at = idx.clamp_min(0)
+    part = (w * dw).double() * (1 - _scores(l, "sigmoid").gather(1, at))
+    want = torch.zeros(T, E, dtype=torch.float64, device="cuda").scatter_add_(1, at, part.masked_fill(idx < 0, 0.0))
+    # at most 16 terms of at most 4, 32 roundings of each
+    assert ((got.double() - want).abs() <= k * 4 * 32 * E24).all()
+    half = ops.route_scores_backward(dw, idx, w, l.bfloat16(), renormalize=False)
+    part = (w * dw).double() * (1 - _scores(l.bfloat16(), "sigmoid").gather(1, at))
+    want = torch.zeros_like(want).scatter_add_(1, at, part.masked_fill(idx < 0, 0.0))
+    assert ((half.double() - want).abs() <= k * 4 * 32 * E24 + U[torch.bfloat16] * want.abs() + 2.0 ** -126).all()
