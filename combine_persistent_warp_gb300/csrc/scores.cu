@@ -553,8 +553,8 @@ __device__ __forceinline__ void make_c(const ScoreArgs &a, const T *l, const boo
 #pragma unroll
             for (int i = 0; i < IPL; ++i) {
                 const float s = a.softmax ? expf(f[q][i] - sm[q].top) * inv : logistic(f[q][i]);
-                // (the sum is of no account but for a logit of -inf)
-                f[q][i] = fminf(a.bias ? s + b[i] : s, f[q][i] + 3e38f);
+                // (-inf alone is never chosen: the lowest finite logit has a score of zero like others far below)
+                f[q][i] = f[q][i] == -INFINITY ? -INFINITY : a.bias ? s + b[i] : s;
             }
         }
     }
