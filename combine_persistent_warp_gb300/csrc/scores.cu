@@ -125,29 +125,42 @@ constexpr uint32_t SLOTS = Q == 1 ? ALL : (1u << (32 / Q)) - 1u;
 
 // Which groups of experts stay, from the two largest keys of each, of Q tokens side by side: keys of group g are those
 // of the lanes g << shift and after.  Lane q * SEG + g gets the score `own` of group g of token q (0: nothing there),
-// whether it stays, and the token's lowest score that stays and highest that does not (0: none).
+// whether it stays, and the token's lowest score that stays and highest that does not (0: none); with SIZES also half the
+// size of what the score is the sum of (half: it is finite).
 __device__ __forceinline__ uint32_t key_sum(uint32_t a, uint32_t b) { return plain_key(plain_value(a) + plain_value(b)); }
 __device__ __forceinline__ uint64_t key_sum(uint64_t a, uint64_t b) { return order_key(key_value(a) + key_value(b)); }
 template <typename K, int Q>
 struct Groups {
     K first[Q], second[Q], own, least, most;
+    float size;
     bool stays;
 };
-template <typename K, int Q>
+template <bool SIZES, typename K, int Q>
 __device__ __forceinline__ void choose_groups(const ScoreArgs &a, Groups<K, Q> &v, int lane, int shift)
 {
     constexpr int SEG = 32 / Q;
     const int seg = lane / SEG, slot = lane % SEG;
     K own = 0;
+    float size = 0.0f;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         K score = v.first[q] > NEVER<K> ? v.first[q] : 0;
-        if (a.pair && v.second[q] > NEVER<K>)
+        const bool two = a.pair && v.second[q] > NEVER<K>;
+        if (two)
             score = key_sum(v.first[q], v.second[q]);
         const K its = __shfl_sync(ALL, score, slot << shift & 31);
         own = seg == q ? its : own;
+        if constexpr (SIZES) {
+            if (a.pair && a.bias) {
+                const float first = 0.5f * fabsf(plain_value(v.first[q])), second = two ? 0.5f * fabsf(plain_value(v.second[q])) : 0.0f;
+                const float its_size = __shfl_sync(ALL, first + second, slot << shift & 31);
+                size = seg == q ? its_size : size;
+            }
+        }
     }
     own = slot < a.groups ? own : 0;
+    if constexpr (SIZES)
+        v.size = a.pair && a.bias ? size : 0.5f * fabsf(plain_value(own));
     int rank = 0;   // ties: the lowest first
 #pragma unroll 4
     for (int g = 0; g < a.groups; ++g) {
@@ -186,16 +199,19 @@ __device__ __forceinline__ int spot(int e) { return e + (e >> 5) * 4; }
 template <int IPL>
 constexpr int SPOTS = IPL * 36;
 
-// The same of one token, whose scores within `open` of each other are in doubt (lane g: group g): groups that are so far above
-// all that do not stay are sure to, and those in doubt are ranked by their scores in 64 bits for the places
-// that are left.  Returns the groups that stay.
+// The same of one token, whose scores may be `off` away (lane g: group g): groups that are so far above all that do not stay
+// are sure to, and those in doubt are ranked by their scores in 64 bits for the places that are left.  Returns the
+// groups that stay.
 template <typename T>
-__device__ __noinline__ uint32_t groups_exactly(const ScoreArgs &a, const T *l, uint32_t own, bool stays, float least, float most, float open,
-                                                uint64_t *seen, int lane)
+__device__ __noinline__ uint32_t groups_exactly(const ScoreArgs &a, const T *l, uint32_t own, bool stays, float off, uint64_t *seen, int lane)
 {
     const float v = plain_value(own);
-    const bool sure = stays && v - most > open;
-    const bool doubt = own != 0u && !sure && (stays || !(least - v > open));
+    float low = v - off, high = v + off;   // (a NaN or an infinity: anywhere)
+    low = low == low ? low : -INFINITY;
+    high = high == high ? high : INFINITY;
+    const float least = -warp_max_f(own != 0u && stays ? -low : -INFINITY), most = warp_max_f(own != 0u && !stays ? high : -INFINITY);
+    const bool sure = stays && low > most;
+    const bool doubt = own != 0u && !sure && (stays || !(high < least));
     const uint32_t in_doubt = __ballot_sync(ALL, doubt);
     const int left = a.kept - __popc(__ballot_sync(ALL, sure)), n = __popc(in_doubt);
     for (int i = lane; i < n * a.per; i += 32) {
@@ -232,7 +248,7 @@ struct Softmax {
 
 // -inf in place of the c of the groups that do not stay, of Q tokens from row l on (there: routed[q]).  sure[q] is
 // false where scores are softmax and which groups stay is in doubt.
-template <typename T, int IPL, int Q>
+template <typename T, int IPL, int Q, bool FIXED>
 __device__ __forceinline__ void keep_groups(const ScoreArgs &a, const T *l, const bool (&routed)[Q], float (&c)[Q][IPL], const Softmax (&sm)[Q],
                                             bool direct, uint64_t *seen, int lane, bool (&sure)[Q])
 {
@@ -263,27 +279,31 @@ __device__ __forceinline__ void keep_groups(const ScoreArgs &a, const T *l, cons
         }
     }
     merge_lanes(v, 1 << shift);
-    choose_groups(a, v, lane, shift);
+    choose_groups<!FIXED>(a, v, lane, shift);
     constexpr int SEG = 32 / Q;
     float open = sm[0].open;
 #pragma unroll
     for (int q = 1; q < Q; ++q)
         open = lane / SEG == q ? sm[q].open : open;
-    const float least = plain_value(v.least), most = plain_value(v.most);
-    open = 2.0f * open + fabsf(least) * 0x1p-21f;
+    // A score is `off` away at most: its two values as far as two values of c are, 2^-24 of each for their sums with the bias and of
+    // their sum's own size, and as much again for the comparison's roundings.  The values' sizes are more than their sum's where
+    // their signs differ: by less than 2 with small biases (FIXED, no value below -1), by nothing without one.  Scores that are
+    // all on their side of the border by that much are in order.
+    const float own = plain_value(v.own), border = 0.5f * plain_value(v.least) + 0.5f * plain_value(v.most);
+    const float off = FIXED ? open + 0x1p-23f + fabsf(own) * 0x1p-22f : open + v.size * 0x1p-21f;
     const uint32_t stays = __ballot_sync(ALL, v.stays);
-    const uint32_t doubt = __ballot_sync(ALL, !direct && v.most != 0u && !(least - most > open));
+    const uint32_t doubt = __ballot_sync(ALL, !direct && v.most != 0u && v.own != 0u && !(v.stays ? own - off > border : own + off < border));
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         uint32_t stay = stays >> (q * SEG) & SLOTS<Q>;
-        if (routed[q] && (doubt >> (q * SEG) & 1u)) {
+        if (routed[q] && (doubt >> (q * SEG) & SLOTS<Q>)) {
             if (a.softmax) {
                 sure[q] = false;
             } else {
                 const int from = q * SEG + lane % SEG;
-                const uint32_t own = __shfl_sync(ALL, v.own, from);
-                const float its_least = __shfl_sync(ALL, least, from), its_most = __shfl_sync(ALL, most, from), its_open = __shfl_sync(ALL, open, from);
-                stay = groups_exactly<T>(a, l + q * a.ld, lane < SEG ? own : 0u, lane < SEG && (stay >> lane & 1u), its_least, its_most, its_open, seen, lane);
+                const uint32_t its_own = __shfl_sync(ALL, v.own, from);
+                const float its_off = __shfl_sync(ALL, off, from);
+                stay = groups_exactly<T>(a, l + q * a.ld, lane < SEG ? its_own : 0u, lane < SEG && (stay >> lane & 1u), its_off, seen, lane);
             }
         }
 #pragma unroll
@@ -343,7 +363,7 @@ __device__ __noinline__ int choose_exactly(const ScoreArgs &a, const T *l, uint6
         v.first[0] = first;
         v.second[0] = second;
         merge_lanes(v, a.lanes);
-        choose_groups(a, v, lane, a.shift);
+        choose_groups<false>(a, v, lane, a.shift);
         const uint32_t stay = __ballot_sync(ALL, v.stays);
         for (int e = lane; e < a.E; e += 32)
             if (!(stay >> ((static_cast<uint32_t>(e) * a.per_magic) >> 20) & 1u))
@@ -518,7 +538,7 @@ __device__ __forceinline__ float logistic(float l)
 
 // The c of Q tokens, from row l on, from their logits and the biases, without those of the groups that do not stay.
 // Of tokens that are not routed, or not there, no logit is looked up.
-template <typename T, int IPL, int Q>
+template <typename T, int IPL, int Q, bool FIXED>
 __device__ __forceinline__ void make_c(const ScoreArgs &a, const T *l, const bool (&routed)[Q], float (&f)[Q][IPL], const float (&b)[IPL],
                                        bool direct, uint64_t *seen, int lane, Softmax (&sm)[Q], bool (&sure)[Q])
 {
@@ -559,7 +579,7 @@ __device__ __forceinline__ void make_c(const ScoreArgs &a, const T *l, const boo
         }
     }
     if (a.groups > 1)
-        keep_groups<T, IPL, Q>(a, l, routed, f, sm, direct, seen, lane, sure);
+        keep_groups<T, IPL, Q, FIXED>(a, l, routed, f, sm, direct, seen, lane, sure);
 }
 template <int IPL, bool FIXED>
 __device__ __forceinline__ void make_words(uint32_t (&word)[IPL], const float (&c)[IPL], int lane)
@@ -592,7 +612,7 @@ __device__ __noinline__ int choose_again(const ScoreArgs &a, const T *l, uint64_
         bool whole = false, sure[1];
         const bool routed[1] = {true};
         int n = 0;
-        make_c<T, IPL, 1>(a, l, routed, f, b, direct, seen, lane, sm, sure);
+        make_c<T, IPL, 1, FIXED>(a, l, routed, f, b, direct, seen, lane, sm, sure);
         if (sure[0]) {
             make_words<IPL, FIXED>(word, f[0], lane);
             while (!whole && n < 32) {
@@ -729,7 +749,7 @@ __device__ __forceinline__ void score_tokens(const ScoreArgs &a, const Lane<T, I
     uint32_t word[Q][IPL], largest[Q];
     Softmax its[Q];
     bool its_sure[Q];
-    make_c<T, IPL, Q>(a, row(0), routed, f, b, direct, seen, lane, its, its_sure);
+    make_c<T, IPL, Q, FIXED>(a, row(0), routed, f, b, direct, seen, lane, its, its_sure);
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         make_words<IPL, FIXED>(word[q], f[q], lane);
