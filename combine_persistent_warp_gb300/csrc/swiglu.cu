@@ -14,8 +14,8 @@
 // Measured on a GB300 in graphs, floors by bytes at the measured copy bandwidth in brackets (a copy's writes are half of its
 // bytes; these kernels' are less): bf16 65536 x 2048 113 us (120), gradient 188 (200), with the checkpoint 153 (162), gradient from it 190
 // (202); rows of 32768 x 7168 kept 99 and restored 101 (106); 16-byte accesses and single fp32 operations took 181 for
-// the checkpoint and 149 + 122 for the rows.  Rows off the boundaries are bound by issue: 65536 x 1403 99, 167, 176
-// and 216 (82, 137, 111, 138), 20000 x 3001 kept 52 and restored 45 (27).
+// the checkpoint and 149 + 122 for the rows.  Rows off the boundaries are bound by issue: 65536 x 1403 104, 169, 177
+// and 217 (82, 137, 111, 138), 20000 x 3001 kept 52 and restored 45 (27).
 #include <climits>
 #include <initializer_list>
 #include <type_traits>
@@ -35,36 +35,27 @@ constexpr uint32_t ALL = 0xFFFFFFFFu;
 __host__ __device__ __forceinline__ int groups_of(int width) { return (width + GROUP - 1) / GROUP; }
 
 // ------------------------------------------------------------------ the activation ------
-// 1/(1 + exp(-g)).  For 16-bit results two approximate instructions, together 2^-21 off at |g| <= 16 (the
-// exponent's rounding grows with |g|), below 2^-126 zero; for fp32 the exact functions.
-template <typename T>
-__device__ __forceinline__ float logistic(float g)
-{
-    if constexpr (std::is_same_v<T, float>) {
-        return 1.0f / (1.0f + expf(-g));
-    } else {
-        float e, s;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
-        return s;
-    }
-}
-// The same of a pair, and the gradients of a pair of gates and ups (in place; d becomes the activation).
+// 1/(1 + exp(-g)) of a pair.  For 16-bit results two approximate instructions, together 2^-21 off at |g| <= 16 (the
+// exponent's rounding grows with |g|); for fp32 the exact functions.  Zero for gates below -88.7, where exp(-g) is past the
+// largest number.  The reciprocal flushes what is no normal number, which a bf16 `up` may bring back to an ordinary size (an
+// fp16 one does not): there it is taken of a quarter of the sum (65536 x 1403 104 us, 99 without).
 template <typename T>
 __device__ __forceinline__ float2 logistic2(float2 g)
 {
     if constexpr (std::is_same_v<T, float>) {
-        return make_float2(logistic<T>(g.x), logistic<T>(g.y));
+        return make_float2(1.0f / (1.0f + expf(-g.x)), 1.0f / (1.0f + expf(-g.y)));
     } else {
+        constexpr float PART = std::is_same_v<T, __nv_bfloat16> ? 0.25f : 1.0f;
         float2 e = mul2(g, both(-1.44269504f));
         asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
         asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-        e = add2(e, both(1.0f));
+        e = PART == 1.0f ? add2(e, both(1.0f)) : fma2(e, both(PART), both(PART));
         asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
         asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-        return e;
+        return PART == 1.0f ? e : mul2(e, both(PART));
     }
 }
+// The gradients of a pair of gates and ups (in place; d becomes the activation).
 template <typename T>
 __device__ __forceinline__ void gradients(float2 &d, float2 &g, float2 &u)
 {
