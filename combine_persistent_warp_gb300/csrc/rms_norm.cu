@@ -10,8 +10,11 @@
 //
 // Measured on a GB300 in graphs, floors by bytes at the measured copy bandwidth in brackets: bf16 16384 x 4096 with the
 // residual forward 88 us (80), backward with dh 84 (80), FP8 form 82 (70); without either 47 and 70 (40, 60); fp16 6001
-// x 2003 15.7 and 22 (14.4 and 14.4; x 2008 15.6 and 20.9), of which the columns' sums are 4; 128 x 7168 FP8 form 3.2; over
-// 8192 columns the backward pass spills (2000 x 8191 bf16 45, floor 20).
+// x 2003 15.7 and 22 (14.4 and 14.4; x 2008 15.6 and 20.9), of which the columns' sums are 4; 128 x 7168 FP8 form 3.2.  From 1025
+// packs on (H over 8192, off the boundaries over 8185) a ring's block has 288 threads and more, and an SM one of them, where 1024 packs
+// have two of 256 forward and one of 512 backward: 2000 x 8192 bf16 10 and 19 us without and with the residual, backward 22 and
+// 28 without and with dh (floors 10, 20, 15, 20), x 8200 17, 25, 33 and 40, x 8191 18, 30, 35 and 43.  Of short batches there (300 x 12288 14 and 17,
+// floors 3.3 and 4.4) the blocks without a ring spill up to 800 bytes a thread.
 #include "norm_rows.cuh"
 
 using namespace cpw;

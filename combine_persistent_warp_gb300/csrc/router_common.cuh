@@ -1,5 +1,6 @@
-// router_common.cuh -- what the routers (router.cu, scores.cu) share: a warp takes a token and holds its
-// logits in registers, lane l those of experts l, l + 32, ...
+// router_common.cuh -- what the routers (router.cu, scores.cu) share: the order of values as keys, and kernels by
+// how many experts a lane of the warp that takes a token holds.  Which they are is each file's: l, l + 32, ... in lane l in
+// router.cu and in the gradient of softmax scores as they are, neighbours in the choice by scores.
 #pragma once
 
 #include <type_traits>
@@ -8,7 +9,7 @@
 
 namespace cpw {
 
-constexpr int WARPS = 4;   // tokens of a block
+constexpr int WARPS = 4;   // of a block (a token each, or in scores.cu up to four)
 
 // Order-preserving 32-bit key of a logit: 0 for -inf (never chosen), the largest for NaN, the
 // same for both zeros.

@@ -2,8 +2,9 @@
 // scaled gate weights, and the gradient of the logits.
 //
 //   s_e = 1/(1 + exp(-l_e)) or exp(l_e)/sum exp(l);  c_e = s_e + b_e (the choice alone sees the bias)
-//   a group's score is the sum of its one or two largest c; the best groups stay, and of their experts the k
-//   with the largest c are chosen; ties go to the lowest group or expert; -inf is never chosen, NaN counts as the largest
+//   a group's score is the sum of its one or two largest c (of one where no more can be chosen); the best groups stay, and
+//   of their experts the k with the largest c are chosen; ties go to the lowest group or expert; -inf is never chosen, NaN
+//   counts as the largest
 //   w_j = scale * s_j, or scale * s_j / sum_i s_i over the chosen ones (renormalised)
 //   gradient, with dot = sum_i w_i dw_i:
 //     sigmoid  renormalised w_j (dw_j - dot/scale)(1 - s_j), otherwise w_j dw_j (1 - s_j)
@@ -14,10 +15,12 @@
 // its error, and the candidates that this bound leaves open are ranked again in 64.
 //
 // The data is small: the instructions bound it, and how many warps an SM has to hide their latency; for few tokens
-// latency alone.  Measured on a GB300 in graphs, bf16, top 8: 16384 x 128 in 8 groups of which 4 stay 10.3 to 11.2 us (a token
-// that is ranked in 64 bits adds 1 us, one whose groups are in doubt 2), in one group 7.6 to 8.5, without a bias 6.7; its
-// gradient 3.2; 128 x 32 fp32 in 4 groups 2.1 and 1.8.  Tokens whose logits have no bias but sums of two (16384 x 128, coarse
-// values whose sums tie) 20; softmax scores with a bias, chosen again with all experts where they are open, 19.
+// latency alone.  Measured on a GB300 in graphs, bf16, top 8: 16384 x 128 in 8 groups of which 4 stay 11.0 us (a token
+// that is ranked in 64 bits adds 1 us, one whose groups are in doubt 2), in one group 8.5, without a bias 6.7; its
+// gradient 3.3; x 256 14.6, 9.0, 8.2 and 3.7; 128 x 32 fp32 in 4 groups 2.2 and 1.8.  Slower: tokens whose logits have no
+// bias but sums of two (16384 x 128, coarse values whose sums tie) 21; softmax scores with a bias, chosen again with all
+// experts where they are open, 19 (in 8 groups 23; x 256 41 and 34); over 256 experts, as lanes hold 32 each, of which 384
+// fill 12 lanes and 512 16, unsorted and with ten bits of the word for the expert (x 384 58 in one group, x 512 77 in 8).
 #include <climits>
 
 #include "moe_internal.cuh"
@@ -1004,12 +1007,13 @@ void launch_scores(const ScoreArgs &a, cudaStream_t s)
     launch_programmatic(score_kernel<T, IPL, Q>, (a.T + WARPS * Q - 1) / (WARPS * Q), WARPS * 32, 0, s, a);
 }
 // Tokens of a warp: the more there are, the less their slots cost, and the fewer warps there are.  128 experts in 8
-// groups, bf16, with 1, 2 and 4 of them: 2048 tokens 5.0, 5.2 and 5.4 us (unbiased, one group: 2.6, 2.8, 3.1), 4096
-// 5.2, 4.9, 4.8 (3.9, 3.6, 4.2), 6144 7.0, 6.9, 8.1 (5.7, 4.3, 5.7), 8192 8.6, 7.5, 7.3 (6.3, 5.0, 4.8), 16384 14.6, 12.0, 11.2
-// (11.2, 8.0, 6.7), 65536 50, 38, 31 (39, 25, 21).
+// groups, bf16, with 1, 2 and 4 of them: 2048 tokens 5.1, 5.2 and 5.5 us (unbiased, one group: 2.6, 2.8, 3.2), 4096
+// 6.5, 6.0, 6.3 (4.0, 3.6, 4.1), 6144 7.8, 7.0, 8.8 (5.6, 4.3, 5.8), 8192 8.3, 6.7, 6.6 (6.4, 4.9, 4.8), 16384 15.6, 12.7, 10.9
+// (11.2, 8.1, 6.7), 65536 50, 38, 31 (39, 25, 21).  256 experts: 4096 6.6, 5.5, 5.4 (4.9, 3.7, 3.8), 8192 10.7, 9.9, 10.0 (7.5, 6.1, 5.0),
+// 65536 64, 55, 45 (44, 35, 27); 128 in fp32: 4096 6.2, 5.7, 5.6 (4.1, 3.9, 4.3), 8192 8.1, 7.7, 7.4 (7.2, 5.7, 5.8), 65536 48, 37, 31 (39, 26, 21).
 constexpr int TWO_TOKENS = 4096, FOUR_TOKENS = 8192;
-// Of the gradient, 128 experts, bf16: 1024 tokens 1.9, 1.9, 2.0 us, 4096 2.5, 2.3, 2.1, 16384 4.5, 3.5, 3.8, 65536 16.9, 8.7, 7.2 (in
-// blocks of four warps).
+// Of the gradient, 128 experts, bf16: 1024 tokens 1.8, 2.0, 2.0 us, 2048 2.2, 2.0, 2.1, 4096 2.6, 2.4, 2.2, 16384 4.2, 3.2, 4.0, 32768
+// 6.8, 4.8, 4.6, 65536 12.1, 8.1, 7.1; 256 experts: 2048 2.3, 2.1, 2.2, 16384 4.3, 3.7, 4.9, 32768 7.0, 5.7, 5.7, 65536 12.5, 9.6, 9.3.
 constexpr int BWD_TWO = 2048, BWD_FOUR = 32768;
 template <typename T, int IPL>
 struct ScoreLaunch {

@@ -143,9 +143,10 @@ def route_scores(logits, topk: int, *, score: str = "sigmoid", bias=None, groups
     gate weights, FusedMoE.forward's (topk_idx int64, topk_w fp32) [T, topk].
 
     The choice goes by score + bias (fp32 [E]).  With ``groups`` of E/groups neighbouring experts, the
-    ``topk_groups`` (default: all) groups with the largest sums of their ``group_top`` (1 or 2) best stay.  The
-    weights are the chosen scores without the bias, divided by their sum (``renormalize``), times ``scale``.
-    Values are compared as in 64 bits; ties, -inf logits and ``token_mask`` as in ``route_topk``."""
+    ``topk_groups`` (default: all) groups with the largest sums of their ``group_top`` (1 or 2) best stay (a group
+    with one expert that can be chosen is scored by that one).  The weights are the chosen scores without the
+    bias, divided by their sum (``renormalize``), times ``scale``.  Values are compared as in 64 bits; ties, -inf
+    logits and ``token_mask`` as in ``route_topk``."""
     args = (logits, topk, _score(score), bias, groups, groups if topk_groups is None else topk_groups, group_top, renormalize, scale,
             token_mask)
     if stream is None:

@@ -6,8 +6,8 @@
 
 Every product, norm, router and row movement of the block, forward and backward, is one of the
 framework's kernels; what is left to PyTorch is elementwise (SwiGLU, the residual sum) and the
-small dense product with the router's weight.  With an RMS norm, a router over scores and 8-bit
-checkpoints, the SwiGLU and the norm's residual are kernels too:
+small dense product with the router's weight.  With an RMS norm the residual that it adds is a
+kernel's too, and with 8-bit checkpoints the SwiGLU:
 
     block = MoEBlock(E, H, I, topk, norm="rms", score="sigmoid", groups=8, topk_groups=4, balance=True, checkpoint=True)
     y = block(x, residual=stream)      # s + MoE(RMSNorm(s)), s = x + stream
@@ -258,7 +258,8 @@ class MoEBlock(nn.Module):
     ``norm="rms"``: an RMS norm, and :meth:`forward` takes a ``residual`` that it adds on the way.
     ``score``: the router of ops.route_scores with ``groups``, ``topk_groups``, ``group_top``, ``renormalize`` and
     ``scale``; with ``balance`` it has a bias for each expert, which :meth:`update_balance` moves against the
-    loads of the batches since.  ``checkpoint``: the experts' activations are kept in 8 bits (``experts``)."""
+    loads of the batches since.  ``checkpoint``: the experts' activations are kept in 8 bits (``experts``),
+    and the SwiGLU is rounded once (without, PyTorch's rounds silu(gate) too, so that the last bits differ)."""
 
     def __init__(self, E: int, H: int, I: int, topk: int, *, eps: float = 1e-5, dtype=torch.bfloat16, std: float = 0.02,
                  norm: str = "layer", score: str | None = None, groups: int = 1, topk_groups: int | None = None, group_top: int = 2,

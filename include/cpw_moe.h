@@ -416,11 +416,11 @@ int moe_rms_norm_backward(int T, int H, const void *dy, int64_t lddy, const void
 
 /* The router over scores s of the logits ([T][E], rows ld apart): sigmoid, or softmax over all experts.
  * The choice goes by c = s + bias (fp32 [E], NULL: none).  With groups > 1, of E/groups neighbouring
- * experts each, a group's score is the sum of its group_top (1 or 2) largest c, the topk_groups best
- * groups stay, and the topk experts with the largest c are chosen from theirs, in descending order; ties go
- * to the lowest group and expert.  c and its sums are compared as computed in 64 bits (without a bias, and
- * with sums of one, as the logits are).  The gate weights are
- * scale * s, or with renormalize = 1 scale * s / sum of s over the chosen ones.  -inf, NaN, fewer
+ * experts each, a group's score is the sum of its group_top (1 or 2) largest c (of the one, where but one
+ * of its experts can be chosen; a group with none is left out), the topk_groups best groups stay, and the
+ * topk experts with the largest c are chosen from theirs, in descending order; ties go to the lowest group
+ * and expert.  c and its sums are compared as computed in 64 bits (without a bias, unless sums of two choose
+ * among the groups, as the logits are): the lowest finite logit has a score of 0.  The gate weights are scale * s, or with renormalize = 1 scale * s / sum of s over the chosen ones.  -inf, NaN, fewer
  * candidates than topk, and token_mask as in moe_route_topk (a bias of -inf excludes its expert).
  * E <= 1024, topk <= 32, groups <= 32 and a divisor of E, topk <= topk_groups * E/groups, scale finite and
  * not 0. */
@@ -438,7 +438,7 @@ int moe_route_scores_backward(int T, int E, int topk, const float *dw, const int
                               void *stream);
 
 /* The experts' activation over rows of gate and up, gu [M][2*I] (gate first): act = silu(gate) * up, [M][I],
- * in fp32 and rounded once.  With codes and scales (both or neither) gate and up are also kept in 8 bits
+ * in fp32 and rounded once (0 for gates below -88.7, where exp(-gate) is past fp32).  With codes and scales (both or neither) gate and up are also kept in 8 bits
  * for the backward call: codes [M][2*I], scales [M][2*ceil(I/32)].  The format (of MX blocks with INT8
  * elements): 32 neighbours of a row (of gate, of up; the last group may be shorter) have a byte b, and a code n
  * stands for n * 2^(b - 133); b = 127 + floor(log2 of the largest magnitude), at least 7; n is the nearest in
